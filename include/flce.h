@@ -294,6 +294,44 @@ FLCE_API int flce_fwd_noalloc(const void* X, const void* W, const int64_t* targe
                               float* loss_dev, float* lse_out, int64_t* n_valid_dev,
                               int32_t* status_dev, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the head: what feeds X, what takes dX back, and what turns
+ * a matrix's gradient into an update.  They use these fields of flce_opts
+ * (NULL = defaults) and ignore the rest: dtype, sync, stream, workspace,
+ * workspace_bytes, workspace_used, status_dev, target_is_int32 (for token
+ * ids).  Conventions on status, scratch, streams and graph capture are those
+ * at the top of this file.  A call with opts->sync == 0 and a NULL status_dev
+ * reports no kernel-side error; the outputs it names for such a case stand.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Embedding lookup: Y[i] = scale * W[ids[i]], scaled in fp32 and rounded once
+ * to opts->dtype.
+ *   W [V, H] and Y [N, H] of type opts->dtype, row-major, contiguous, 16-byte
+ *   aligned, H * sizeof(element) a multiple of 16, H <= 2^20; ids [N] int64
+ *   (int32 with opts->target_is_int32).
+ * A token whose id is ignore_index gets a row of zeros.  So does a token whose
+ * id is outside [0, V), which also reports FLCE_ERR_TARGET.
+ */
+FLCE_API int flce_embed_fwd(const void* W, const void* ids, int64_t N, int64_t H, int64_t V,
+                            float scale, int64_t ignore_index, void* Y, const flce_opts* opts);
+
+/*
+ * Its gradient: dW[v] = scale * sum of dY[i] over the tokens i with ids[i] == v,
+ * or dW[v] += that sum when accumulate is not 0 (a weight tied to the head's:
+ * dW then holds what flce_fwd_bwd() left there; rows that no token has are not
+ * touched).  Equal ids are added in ascending token order in fp32, so the
+ * result does not change from run to run.
+ *   dY [N, H] of type opts->dtype; dW [V, H] fp32; alignment as above.
+ * Ignored and out-of-range ids take no part (the latter report
+ * FLCE_ERR_TARGET).  N == 0 clears dW, or leaves it when accumulate is set.
+ * Scratch: 16 bytes per token, two fp32 rows per 4 to 64 tokens, and V / 8
+ * bytes without accumulate; opts->workspace_used reports it.
+ */
+FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_t V,
+                            float scale, int64_t ignore_index, float* dW, int32_t accumulate,
+                            const flce_opts* opts);
+
 #ifdef __cplusplus
 }
 #endif

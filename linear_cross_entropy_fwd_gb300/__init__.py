@@ -37,7 +37,8 @@ TRACE_KINDS = {1: "logits_lse", 2: "combine", 3: "logits_grad", 4: "dw", 5: "dx"
 EXPORTED = ["flce_opts_init", "flce_fwd_bwd", "flce_fwd_bwd_ex", "flce_fwd",
             "flce_fwd_bwd_host", "flce_workspace_bytes", "flce_status_str",
             "flce_last_error", "flce_version", "flce_opts_sizeof", "flce_fwd_noalloc",
-            "flce_ce_fwd_bwd", "flce_selftest_wait_expiry", "flce_scale_convert"]
+            "flce_ce_fwd_bwd", "flce_selftest_wait_expiry", "flce_scale_convert",
+            "flce_embed_fwd", "flce_embed_bwd"]
 
 
 class FlceOpts(ctypes.Structure):
@@ -119,6 +120,11 @@ def load_library(path: str | None = None):
         lib.flce_selftest_wait_expiry.restype = i32
         lib.flce_scale_convert.argtypes = [vp, i32, vp, i32, i64, vp, vp]
         lib.flce_scale_convert.restype = i32
+        f32 = ctypes.c_float
+        lib.flce_embed_fwd.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, po]
+        lib.flce_embed_fwd.restype = i32
+        lib.flce_embed_bwd.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, ctypes.c_int32, po]
+        lib.flce_embed_bwd.restype = i32
         if lib.flce_opts_sizeof() != ctypes.sizeof(FlceOpts):
             raise RuntimeError("flce_opts layout mismatch between libflce and the binding")
         _lib = lib
@@ -562,3 +568,6 @@ class LinearCrossEntropyLoss(torch.nn.Module):
 
     def forward(self, weight, inp, target):
         return _FLCEFunction.apply(weight, inp, target, self.ignore_index)
+
+
+from .step import Embedding, flce_embed_bwd, flce_embed_fwd  # noqa: E402,F401

@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libflce.so")
-SOURCES = ["gemm_bf16.cu", "gemm_fp32.cu", "small_kernels.cu", "flce_api.cu"]
+SOURCES = ["gemm_bf16.cu", "gemm_fp32.cu", "small_kernels.cu", "flce_api.cu",
+           "step_common.cu", "embed.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

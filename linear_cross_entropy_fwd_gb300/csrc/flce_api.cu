@@ -22,6 +22,7 @@
 #include <mutex>
 
 #include "../../include/flce.h"
+#include "host_util.h"
 #include "launch.h"
 
 namespace flce {
@@ -612,6 +613,10 @@ int status_from_bits(int32_t bits) {
     set_error("a target is outside [0, V) and is not the ignore index");
     return FLCE_ERR_TARGET;
   }
+  if (bits & FLCE_DEV_SEQLENS) {
+    set_error("the sequence offsets are out of order or outside [0, T]");
+    return FLCE_ERR_ARG;
+  }
   return FLCE_OK;
 }
 
@@ -814,6 +819,58 @@ int ce_entry(const void* logits, const int64_t* target, int64_t N, int64_t V,
 }
 
 }  // namespace
+}  // namespace flce
+
+// --------------------------------- services for the other entry points' files
+namespace flce {
+
+void host_clear_error() { g_last_error[0] = 0; }
+
+int host_error(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+int host_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+int host_device(int* sms) {
+  DeviceInfo D;
+  const int rc = device_info(FLCE_BF16, &D);
+  if (rc == FLCE_OK) *sms = D.sms;
+  return rc;
+}
+
+int host_pool_alloc(void** p, size_t bytes, cudaStream_t s) { return pool_alloc(p, bytes, s); }
+
+int host_status(int32_t bits) { return status_from_bits(bits); }
+
+int host_tensor_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank,
+                    const uint64_t* dims, const uint64_t* pitch, const uint32_t* box,
+                    const char* what) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn)
+    return host_error(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[5], st[5];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i > 0) st[i - 1] = pitch[i - 1];
+  }
+  const CUresult r =
+      fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return host_error(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what,
+                      static_cast<int>(r));
+  return FLCE_OK;
+}
+
 }  // namespace flce
 
 // ------------------------------------------------ allocation-free loss entry
