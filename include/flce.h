@@ -332,6 +332,60 @@ FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t 
                             float scale, int64_t ignore_index, float* dW, int32_t accumulate,
                             const flce_opts* opts);
 
+/*
+ * Causal attention over packed sequences with grouped heads.  Sequence b is
+ * tokens cu_seqlens[b] .. cu_seqlens[b+1]-1 of the T tokens; a token sees the
+ * tokens of its own sequence up to itself.  For query head h and kv head
+ * h / (heads_q / heads_kv):
+ *   S = scale Q K^T,  lse_i = ln sum_{j <= i} exp S_ij,  P = exp(S - lse),  O = P V
+ * and for the gradients, with delta_i = sum_d dO_id O_id:
+ *   dS = P o (dO V^T - delta),  dQ = scale dS K,
+ *   dK = scale dS^T Q and dV = P^T dO, summed over the query heads of the group.
+ * Products are bf16 with fp32 sums; P and dS are rounded to bf16 for theirs.
+ *
+ * Every tensor is bf16 [T, heads, head_dim] with a contiguous last axis and
+ * its own token and head strides in elements (multiples of 8, not 0, so q, k
+ * and v may be slices of one projection's output), 16-byte aligned; lse is
+ * fp32 [heads_q, T], contiguous.  cu_seqlens: int32 [batch + 1] on the device,
+ * 0 <= cu_seqlens[0] <= ... <= cu_seqlens[batch] <= T; offsets that break this
+ * are reported as FLCE_ERR_ARG and count as no sequence at all.  A sequence
+ * may be empty.  Tokens outside every sequence get zeros in o, dq, dk and dv
+ * and -inf in lse; what their inputs hold is not used.
+ * A NaN or infinity in a token's k or v reaches only its own sequence; there
+ * it may also reach tokens before it in the same block of 128 tokens.
+ */
+typedef struct flce_attn {
+  int64_t T;                 /* tokens, < 2^31 - 256 */
+  int64_t batch;             /* sequences, >= 0 */
+  const int32_t* cu_seqlens;
+  int32_t heads_q, heads_kv; /* heads_kv divides heads_q */
+  int32_t head_dim;          /* a multiple of 8, 8 .. 128 */
+  float scale;               /* > 0, finite */
+  const void* q;             /* each followed by its token and head strides */
+  int64_t q_token, q_head;
+  const void* k;
+  int64_t k_token, k_head;
+  const void* v;
+  int64_t v_token, v_head;
+  void* o;                   /* written by flce_attn_fwd, read by flce_attn_bwd */
+  int64_t o_token, o_head;
+  float* lse;                /* likewise */
+  const void* dO;            /* the rest: flce_attn_bwd only */
+  int64_t dO_token, dO_head;
+  void* dq;
+  int64_t dq_token, dq_head;
+  void* dk;
+  int64_t dk_token, dk_head;
+  void* dv;
+  int64_t dv_token, dv_head;
+} flce_attn;
+
+FLCE_API int flce_attn_fwd(const flce_attn* a, const flce_opts* opts);
+FLCE_API int flce_attn_bwd(const flce_attn* a, const flce_opts* opts);
+
+/* sizeof(flce_attn) as compiled into the library. */
+FLCE_API size_t flce_attn_sizeof(void);
+
 #ifdef __cplusplus
 }
 #endif

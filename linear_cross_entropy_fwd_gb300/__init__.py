@@ -38,7 +38,8 @@ EXPORTED = ["flce_opts_init", "flce_fwd_bwd", "flce_fwd_bwd_ex", "flce_fwd",
             "flce_fwd_bwd_host", "flce_workspace_bytes", "flce_status_str",
             "flce_last_error", "flce_version", "flce_opts_sizeof", "flce_fwd_noalloc",
             "flce_ce_fwd_bwd", "flce_selftest_wait_expiry", "flce_scale_convert",
-            "flce_embed_fwd", "flce_embed_bwd"]
+            "flce_embed_fwd", "flce_embed_bwd", "flce_attn_fwd", "flce_attn_bwd",
+            "flce_attn_sizeof"]
 
 
 class FlceOpts(ctypes.Structure):
@@ -66,6 +67,24 @@ class FlceOpts(ctypes.Structure):
         ("trace_capacity", ctypes.c_int32),
         ("trace_count", ctypes.POINTER(ctypes.c_int32)),
     ]
+
+
+class FlceAttn(ctypes.Structure):
+    """Mirror of ``struct flce_attn`` (include/flce.h)."""
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("batch", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("heads_q", ctypes.c_int32),
+        ("heads_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ] + [f for name in ("q", "k", "v", "o") for f in (
+        (name, ctypes.c_void_p), (name + "_token", ctypes.c_int64),
+        (name + "_head", ctypes.c_int64))] + [("lse", ctypes.c_void_p)] + [
+        f for name in ("dO", "dq", "dk", "dv") for f in (
+            (name, ctypes.c_void_p), (name + "_token", ctypes.c_int64),
+            (name + "_head", ctypes.c_int64))]
 
 
 class FlceError(RuntimeError):
@@ -125,6 +144,14 @@ def load_library(path: str | None = None):
         lib.flce_embed_fwd.restype = i32
         lib.flce_embed_bwd.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, ctypes.c_int32, po]
         lib.flce_embed_bwd.restype = i32
+        pa = ctypes.POINTER(FlceAttn)
+        for fn in (lib.flce_attn_fwd, lib.flce_attn_bwd):
+            fn.argtypes = [pa, po]
+            fn.restype = i32
+        lib.flce_attn_sizeof.argtypes = []
+        lib.flce_attn_sizeof.restype = ctypes.c_size_t
+        if lib.flce_attn_sizeof() != ctypes.sizeof(FlceAttn):
+            raise RuntimeError("flce_attn layout mismatch between libflce and the binding")
         if lib.flce_opts_sizeof() != ctypes.sizeof(FlceOpts):
             raise RuntimeError("flce_opts layout mismatch between libflce and the binding")
         _lib = lib
@@ -570,4 +597,5 @@ class LinearCrossEntropyLoss(torch.nn.Module):
         return _FLCEFunction.apply(weight, inp, target, self.ignore_index)
 
 
-from .step import Embedding, flce_embed_bwd, flce_embed_fwd  # noqa: E402,F401
+from .step import (Embedding, PackedAttention, flce_attn_bwd, flce_attn_fwd,  # noqa: E402,F401
+                   flce_embed_bwd, flce_embed_fwd)

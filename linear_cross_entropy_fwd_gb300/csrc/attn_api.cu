@@ -1,0 +1,146 @@
+// attn_api.cu -- host side of packed causal attention: argument checks,
+// tensor maps, scratch and the launch sequence.
+#include <cmath>
+
+#include "attn.h"
+#include "host_util.h"
+
+namespace flce {
+namespace {
+
+// A [T, heads, D] operand: address and strides, with the stride of an axis of
+// one element (which may be anything) replaced by a valid one.
+struct Operand {
+  const void* p;
+  int64_t token, head;
+};
+
+int operand(Operand* out, const char* name, const void* p, int64_t token, int64_t head, int64_t T,
+            int heads, int D) {
+  if (!p) return host_error(FLCE_ERR_ARG, "%s is null", name);
+  if (heads == 1) head = D;
+  if (T == 1) token = head * heads;
+  if (token <= 0 || head <= 0)
+    return host_error(FLCE_ERR_ARG, "%s: strides must be positive", name);
+  if (token % 8 != 0 || head % 8 != 0 || !aligned16(p))
+    return host_error(FLCE_ERR_ALIGN,
+                      "%s must be 16-byte aligned with strides that are multiples of 8", name);
+  if (token >= (int64_t{1} << 38) || head >= (int64_t{1} << 38))
+    return host_error(FLCE_ERR_ARG, "%s: stride too large", name);
+  *out = Operand{p, token, head};
+  return FLCE_OK;
+}
+
+int tensor_map(CUtensorMap* m, const Operand& t, int64_t T, int heads, int D, const char* name) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(heads),
+                            static_cast<uint64_t>(T)};
+  const uint64_t pitch[2] = {static_cast<uint64_t>(t.head) * 2, static_cast<uint64_t>(t.token) * 2};
+  const uint32_t box[3] = {64, 1, kTile};
+  return host_tensor_map(m, t.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, pitch, box, name);
+}
+
+int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
+  host_clear_error();
+  const flce_opts o = opts_or_default(opts);
+  if (!a) return host_error(FLCE_ERR_ARG, "null flce_attn");
+  if (o.dtype != FLCE_BF16)
+    return host_error(FLCE_ERR_ARG, "attention takes bf16 inputs (dtype %d)", o.dtype);
+  if (a->T < 0 || a->T >= (int64_t{1} << 31) - 256 || a->batch < 0 ||
+      a->batch >= (int64_t{1} << 30))
+    return host_error(FLCE_ERR_ARG, "sizes must satisfy 0 <= T < 2^31 - 256, 0 <= batch < 2^30");
+  if (a->heads_kv < 1 || a->heads_q < 1 || a->heads_q % a->heads_kv != 0)
+    return host_error(FLCE_ERR_ARG, "heads_kv must be positive and divide heads_q");
+  const int D = a->head_dim;
+  if (D < 8 || D > 128 || D % 8 != 0)
+    return host_error(FLCE_ERR_ARG, "head_dim must be a multiple of 8 in 8 .. 128 (got %d)", D);
+  if (!(a->scale > 0.f) || std::isinf(a->scale))
+    return host_error(FLCE_ERR_ARG, "scale must be positive and finite");
+  if (!a->cu_seqlens) return host_error(FLCE_ERR_ARG, "cu_seqlens is null");
+  const int64_t T = a->T;
+  const int64_t max_tiles = T / kTile + a->batch;
+  if (max_tiles * a->heads_q >= (int64_t{1} << 31))
+    return host_error(FLCE_ERR_ARG, "(T / 128 + batch) * heads_q must be below 2^31");
+  int rc = FLCE_OK;
+  Operand q, k, v, oo, dO{}, dq{}, dk{}, dv{};
+  if (T > 0) {
+    if ((rc = operand(&q, "q", a->q, a->q_token, a->q_head, T, a->heads_q, D))) return rc;
+    if ((rc = operand(&k, "k", a->k, a->k_token, a->k_head, T, a->heads_kv, D))) return rc;
+    if ((rc = operand(&v, "v", a->v, a->v_token, a->v_head, T, a->heads_kv, D))) return rc;
+    if ((rc = operand(&oo, "o", a->o, a->o_token, a->o_head, T, a->heads_q, D))) return rc;
+    if (!a->lse) return host_error(FLCE_ERR_ARG, "lse is null");
+    if (backward) {
+      if ((rc = operand(&dO, "dO", a->dO, a->dO_token, a->dO_head, T, a->heads_q, D))) return rc;
+      if ((rc = operand(&dq, "dq", a->dq, a->dq_token, a->dq_head, T, a->heads_q, D))) return rc;
+      if ((rc = operand(&dk, "dk", a->dk, a->dk_token, a->dk_head, T, a->heads_kv, D))) return rc;
+      if ((rc = operand(&dv, "dv", a->dv, a->dv_token, a->dv_head, T, a->heads_kv, D))) return rc;
+    }
+  }
+  int sms = 0;
+  if ((rc = host_device(&sms))) return rc;
+  CUtensorMap mq, mk, mv, mO;
+  if (T > 0) {
+    if ((rc = tensor_map(&mq, q, T, a->heads_q, D, "q"))) return rc;
+    if ((rc = tensor_map(&mk, k, T, a->heads_kv, D, "k"))) return rc;
+    if ((rc = tensor_map(&mv, v, T, a->heads_kv, D, "v"))) return rc;
+    if (backward && (rc = tensor_map(&mO, dO, T, a->heads_q, D, "dO"))) return rc;
+  }
+  AttnParams p{};
+  p.cu = a->cu_seqlens;
+  p.B = static_cast<int32_t>(a->batch);
+  p.T = static_cast<int32_t>(T);
+  p.Hq = a->heads_q;
+  p.Hkv = a->heads_kv;
+  p.D = D;
+  p.scale = a->scale;
+  p.max_tiles = static_cast<int32_t>(max_tiles);
+  p.max_depth = static_cast<int32_t>((T + kTile - 1) / kTile);
+  const size_t b_tiles = round256(static_cast<size_t>(max_tiles) * sizeof(AttnTile));
+  const size_t b_bucket = round256((static_cast<size_t>(p.max_depth) + 2) * 4);
+  const size_t b_delta =
+      backward ? round256(static_cast<size_t>(a->heads_q) * static_cast<size_t>(T) * 4) : 0;
+  StepCall call;
+  if ((rc = call.begin(o, T > 0 ? 256 + b_tiles + b_bucket + b_delta : 0,
+                       T > 0 ? StepCall::kKernelClears : StepCall::kIfAsked)))
+    return rc;
+  if (T == 0) return call.end(FLCE_OK);
+  uint8_t* w = call.scratch;
+  p.n_tiles = reinterpret_cast<int32_t*>(w);
+  p.tiles = reinterpret_cast<AttnTile*>(w + 256);
+  p.bucket = reinterpret_cast<int32_t*>(w + 256 + b_tiles);
+  p.delta = backward ? reinterpret_cast<float*>(w + 256 + b_tiles + b_bucket) : nullptr;
+  p.lse = a->lse;
+  p.status = call.status;
+  p.o = AttnOut{a->o, oo.token, oo.head};
+  p.dO = AttnOut{const_cast<void*>(a->dO), dO.token, dO.head};
+  p.dq = AttnOut{a->dq, dq.token, dq.head};
+  p.dk = AttnOut{a->dk, dk.token, dk.head};
+  p.dv = AttnOut{a->dv, dv.token, dv.head};
+  cudaError_t e = launch_attn_plan(p, backward, sms, call.stream);
+  if (max_tiles > 0) {
+    if (backward) {
+      if (e == cudaSuccess) e = launch_attn_dkdv(mq, mk, mv, mO, p, call.stream);
+      if (e == cudaSuccess) e = launch_attn_dq(mq, mk, mv, mO, p, call.stream);
+    } else if (e == cudaSuccess) {
+      e = launch_attn_fwd(mq, mk, mv, p, call.stream);
+    }
+  }
+  if (e != cudaSuccess) rc = host_cuda_error(e, backward ? "flce_attn_bwd" : "flce_attn_fwd");
+  return call.end(rc);
+}
+
+}  // namespace
+}  // namespace flce
+
+extern "C" {
+
+int flce_attn_fwd(const flce_attn* a, const flce_opts* opts) {
+  return flce::attention(a, opts, false);
+}
+
+int flce_attn_bwd(const flce_attn* a, const flce_opts* opts) {
+  return flce::attention(a, opts, true);
+}
+
+size_t flce_attn_sizeof(void) { return sizeof(flce_attn); }
+
+}  // extern "C"

@@ -1,0 +1,591 @@
+// attn_bwd.cu -- gradients of packed causal attention, in two kernels that
+// each own their outputs: no atomics, the same bits on every run.
+//
+//   dkdv  one CTA per (key tile of 128 rows, kv head); for every query head of
+//         the group and every query tile i that sees the key tile:
+//           S^T = K Q_i^T, dP^T = V dO_i^T
+//           P^T = 2^(c S^T - lse2_i), dS^T = P^T o (dP^T - delta_i)
+//           dV += P^T dO_i, dK += dS^T Q_i     accumulated in TMEM
+//   dq    one CTA per (query tile, query head); for every key tile j:
+//           S = Q K_j^T, dP = dO V_j^T, dS = P o (dP - delta), dQ += dS K_j
+//
+// Seven products where one kernel for all three would do with five, adding dQ
+// to memory from every CTA; that would make dQ depend on the order of the
+// additions (or need one more pass over fp32 partial sums).
+//
+// P and dS are rounded to bf16, the type of the MMA operands; sums are fp32.
+// Only tiles on the diagonal and at a sequence's end are masked, by selection,
+// and rows past the end of the sequence are cleared in shared memory where
+// they are summed over (they belong to another sequence and may hold anything).
+//
+// Roles (320 threads): warps 0-7 elementwise (warp w: TMEM lanes 32 (w % 4) ..,
+// columns 64 (w / 4) .. of a tile), warp 8 TMA, warp 9 MMA.
+#include "attn.h"
+#include "host_util.h"
+#include "sm103_attn.cuh"
+
+namespace flce {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 320;
+constexpr int kEwThreads = 256;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kBoxBytes = kTile * 128;  // 128 rows x 64 bf16
+
+template <int DP>
+struct BwdShape {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
+  static constexpr uint32_t kPBytes = 2 * kBoxBytes;  // 128 x 128 bf16
+  // dkdv: K, V, two Q and two dO tiles, P^T, lse2 and delta twice, barriers
+  static constexpr uint32_t kSmemDkDv = 6 * kTileBytes + kPBytes + 2048 + 256;
+  // dq: Q, dO, three K and two V tiles, barriers
+  static constexpr uint32_t kSmemDq = 7 * kTileBytes + 256;
+};
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <int BOXES>
+__device__ __forceinline__ void load_tile(const CUtensorMap* m, uint64_t* bar, uint8_t* dst,
+                                          int head, int token) {
+#pragma unroll
+  for (int b = 0; b < BOXES; ++b)
+    tma_load_3d(m, bar, dst + b * kBoxBytes, 64 * b, head, token);
+}
+
+// D = A B^T over the head dimension, both tiles K-major in shared memory.
+__device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint32_t a, uint32_t b, int k_steps) {
+  constexpr uint32_t kIdesc = make_idesc(1, false, false, kTile, kTile);
+  for (int k = 0; k < k_steps; ++k) {
+    const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
+    mma_f16(d_tmem, smem_desc_sw128(a + off, 0, 1024), smem_desc_sw128(b + off, 0, 1024), kIdesc,
+            k > 0);
+  }
+}
+
+// D (+)= A B over 128 rows of B, B a [128 rows, DP] tile in shared memory;
+// A in TMEM.
+template <int DP>
+__device__ __forceinline__ void mma_over_rows_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
+                                                 bool add) {
+  constexpr uint32_t kIdesc = make_idesc(1, false, true, kTile, DP);
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    mma_f16_ts(d_tmem, a_tmem + 8 * k, smem_desc_sw128(b + k * 2048, kBoxBytes, 1024), kIdesc,
+               (add || k > 0) ? 1u : 0u);
+}
+
+// The same with A a K-major [128, 128] tile in shared memory.
+template <int DP>
+__device__ __forceinline__ void mma_over_rows_ss(uint32_t d_tmem, uint32_t a, uint32_t b,
+                                                 bool add) {
+  constexpr uint32_t kIdesc = make_idesc(1, false, true, kTile, DP);
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    mma_f16(d_tmem, smem_desc_sw128(a + (k >> 2) * kBoxBytes + (k & 3) * 32, 0, 1024),
+            smem_desc_sw128(b + k * 2048, kBoxBytes, 1024), kIdesc, (add || k > 0) ? 1u : 0u);
+}
+
+// Rows [valid, 128) of a tile become zeros (the elementwise threads).
+template <int BOXES>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int valid) {
+  const int per = (kTile - valid) * 8;  // 16-byte pieces per box
+  for (int i = threadIdx.x; i < per * BOXES; i += kEwThreads)
+    st_shared_v4(smem_addr(tile) + (i / per) * kBoxBytes + valid * 128 + (i % per) * 16, 0, 0, 0,
+                 0);
+  fence_proxy_async_smem();
+}
+
+// Accumulator columns [c0, c0 + 32) of this thread's row, times f, to bf16.
+__device__ __forceinline__ void store_cols(uint32_t taddr, float f, uint16_t* row, int c0, int D,
+                                           bool in) {
+  uint32_t o[32];
+  tmem_ld_32x32b_x32(taddr, o);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f,
+                         __uint_as_float(o[8 * i + 2 * k + 1]) * f);
+    const int d = c0 + 8 * i;
+    if (in && d < D) *reinterpret_cast<uint4*>(row + d) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ===================================================================== dkdv
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmO, const AttnParams p) {
+  using S = BwdShape<DP>;
+  constexpr uint32_t TB = S::kTileBytes;
+  const int kvh = static_cast<int>(blockIdx.x % p.Hkv);
+  const int idx = static_cast<int>(blockIdx.x / p.Hkv);
+  grid_dependency_wait();  // the tile list and delta
+  if (idx >= *p.n_tiles) return;
+  const AttnTile t = p.tiles[idx];
+  const int n_q = t.tile + 1;                           // query tiles that see this key tile
+  const int kt = (t.len + kTile - 1) / kTile - n_q;     // this key tile
+  const int group = p.Hq / p.Hkv;
+  const int total = n_q * group;                        // (head, query tile) pairs
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* smK = smem;
+  uint8_t* smV = smK + TB;
+  uint8_t* smQ = smV + TB;       // [2]
+  uint8_t* smO = smQ + 2 * TB;   // [2] dO
+  uint8_t* smP = smO + 2 * TB;
+  float* rows = reinterpret_cast<float*>(smP + S::kPBytes);  // [2][lse2 128, delta 128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 512);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;    // [2]
+  uint64_t* q_empty = bars + 3;   // [2]
+  uint64_t* o_full = bars + 5;    // [2]
+  uint64_t* o_empty = bars + 7;   // [2]
+  uint64_t* s_full = bars + 9;
+  uint64_t* dp_full = bars + 10;
+  uint64_t* p_full = bars + 11;
+  uint64_t* p_empty = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* acc_full = bars + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 15; ++i) mbar_init(&bars[i], (i == 11 || i == 13) ? 8 : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tS = *tmem_slot, tDP = tS + kTile, tDV = tDP + kTile, tDK = tDV + DP;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * TB);
+      load_tile<S::kBoxes>(&tmK, kv_full, smK, kvh, t.start + kt * kTile);
+      load_tile<S::kBoxes>(&tmV, kv_full, smV, kvh, t.start + kt * kTile);
+      int n = 0;  // loads issued per ring: n of Q, n or n - 1 of dO
+      int n_o = 0;
+      for (int it = 0; it < total; ++it) {
+        const int s = it & 1;
+        const uint32_t par = ((it >> 1) & 1) ^ 1;
+        const int head = kvh * group + it / n_q;
+        const int tok = t.start + (kt + it % n_q) * kTile;
+        if (!mbar_wait(&q_empty[s], par, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(&q_full[s], TB);
+        load_tile<S::kBoxes>(&tmQ, &q_full[s], smQ + s * TB, head, tok);
+        ++n;
+        if (!mbar_wait(&o_empty[s], par, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(&o_full[s], TB);
+        load_tile<S::kBoxes>(&tmO, &o_full[s], smO + s * TB, head, tok);
+        ++n_o;
+      }
+      // every load has landed before this CTA's shared memory goes away
+      mbar_wait_drain(kv_full, 0);
+      for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait_drain(&q_full[i & 1], (i >> 1) & 1);
+      for (int i = n_o > 2 ? n_o - 2 : 0; i < n_o; ++i)
+        mbar_wait_drain(&o_full[i & 1], (i >> 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      const uint32_t aK = smem_addr(smK), aV = smem_addr(smV), aQ = smem_addr(smQ),
+                     aO = smem_addr(smO), aP = smem_addr(smP);
+      const int k_steps = (p.D + 15) / 16;  // columns past D are zeros
+      bool ok = mbar_wait(kv_full, 0, abort_flag, p.status) &&
+                mbar_wait(&q_full[0], 0, abort_flag, p.status);
+      if (ok) {
+        tc_fence_after();
+        mma_over_d(tS, aK, aQ, k_steps);
+        mma_commit(s_full);
+        ok = mbar_wait(&o_full[0], 0, abort_flag, p.status);
+      }
+      if (ok) {
+        tc_fence_after();
+        mma_over_d(tDP, aV, aO, k_steps);
+        mma_commit(dp_full);
+      }
+      for (int it = 0; ok && it < total; ++it) {
+        const int s = it & 1, s1 = s ^ 1;
+        const uint32_t par1 = ((it + 1) >> 1) & 1;
+        const bool more = it + 1 < total;
+        // P^T is in shared memory, and S^T has been read
+        if (!mbar_wait(p_full, it & 1, abort_flag, p.status)) break;
+        if (more) {
+          if (!mbar_wait(&q_full[s1], par1, abort_flag, p.status)) break;
+          tc_fence_after();
+          mma_over_d(tS, aK, aQ + s1 * TB, k_steps);
+          mma_commit(s_full);
+        }
+        tc_fence_after();
+        mma_over_rows_ss<DP>(tDV, aP, aO + s * TB, it > 0);
+        mma_commit(&o_empty[s]);
+        mma_commit(p_empty);
+        // dS^T is in TMEM, and dP^T has been read
+        if (!mbar_wait(ds_full, it & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        mma_over_rows_ts<DP>(tDK, tDP, aQ + s * TB, it > 0);
+        mma_commit(&q_empty[s]);
+        if (more) {
+          if (!mbar_wait(&o_full[s1], par1, abort_flag, p.status)) break;
+          tc_fence_after();
+          mma_over_d(tDP, aV, aO + s1 * TB, k_steps);
+          mma_commit(dp_full);
+        }
+      }
+      mma_commit(acc_full);  // all MMAs issued by this thread are done
+      mbar_wait_drain(acc_full, 0);
+    }
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const int row = 32 * quarter + lane;  // key row
+    const int tid = threadIdx.x;
+    const float c = p.scale * kLog2e;
+    // thread t stages lse2 (t < 128) or delta of one query row per tile
+    auto fetch = [&](int it) {
+      const int q = (kt + it % n_q) * kTile + (tid & 127);
+      if (it >= total || q >= t.len) return 0.f;
+      const int64_t at = static_cast<int64_t>(kvh * group + it / n_q) * p.T + t.start + q;
+      return tid < kTile ? p.lse[at] * kLog2e : p.delta[at];
+    };
+    float next = fetch(0);
+    // After a wait has expired the loop goes on without results, so that every
+    // warp still meets the others at the named barriers; later waits then
+    // return at once.
+    bool ok = true;
+    for (int it = 0; it < total; ++it) {
+      const int s = it & 1;
+      const int qt = kt + it % n_q;
+      const int valid = t.len - qt * kTile < kTile ? t.len - qt * kTile : kTile;
+      const bool masked = qt == kt || valid < kTile;
+      float* lse2 = rows + s * 256;
+      lse2[tid] = next;
+      named_barrier(1, kEwThreads);
+      next = fetch(it + 1);
+      const float* dl = lse2 + kTile + 64 * half;
+      const float* ls = lse2 + 64 * half;
+
+      ok = warp_wait(s_full, it & 1, abort_flag, p.status) && ok;
+      tc_fence_after();
+      float P[64];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        tmem_ld_32x32b_x32(tS + lanes + 64 * half + 32 * q,
+                           reinterpret_cast<uint32_t(&)[32]>(P[32 * q]));
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        const float4 L = *reinterpret_cast<const float4*>(ls + i);
+        P[i] = fast_exp2(fmaf(P[i], c, -L.x));
+        P[i + 1] = fast_exp2(fmaf(P[i + 1], c, -L.y));
+        P[i + 2] = fast_exp2(fmaf(P[i + 2], c, -L.z));
+        P[i + 3] = fast_exp2(fmaf(P[i + 3], c, -L.w));
+      }
+      // columns [lo, hi) of this thread's half are queries that see this key
+      const int lo = (qt == kt ? row : 0) - 64 * half, hi = valid - 64 * half;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) P[i] = (i >= lo && i < hi) ? P[i] : 0.f;
+      }
+      ok = warp_wait(p_empty, (it & 1) ^ 1, abort_flag, p.status) && ok;
+      const uint32_t prow = smem_addr(smP) + half * kBoxBytes + row * 128;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        st_shared_v4(prow + ((i ^ (row & 7)) << 4), pack_bf16x2(P[8 * i], P[8 * i + 1]),
+                     pack_bf16x2(P[8 * i + 2], P[8 * i + 3]),
+                     pack_bf16x2(P[8 * i + 4], P[8 * i + 5]),
+                     pack_bf16x2(P[8 * i + 6], P[8 * i + 7]));
+      if (valid < kTile) {
+        // S^T of this tile is complete, so Q is only read again by dK
+        ok = warp_wait(&o_full[s], (it >> 1) & 1, abort_flag, p.status) && ok;
+        clear_rows<S::kBoxes>(smO + s * TB, valid);
+        clear_rows<S::kBoxes>(smQ + s * TB, valid);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+
+      ok = warp_wait(dp_full, it & 1, abort_flag, p.status) && ok;
+      tc_fence_after();
+      float d[64];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        tmem_ld_32x32b_x32(tDP + lanes + 64 * half + 32 * q,
+                           reinterpret_cast<uint32_t(&)[32]>(d[32 * q]));
+      tmem_ld_wait();
+      // dS^T goes over columns that the other half's warp reads
+      tc_fence_before();
+      named_barrier(2 + quarter, 64);
+      tc_fence_after();
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        const float4 L = *reinterpret_cast<const float4*>(dl + i);
+        d[i] = P[i] * (d[i] - L.x);
+        d[i + 1] = P[i + 1] * (d[i + 1] - L.y);
+        d[i + 2] = P[i + 2] * (d[i + 2] - L.z);
+        d[i + 3] = P[i + 3] * (d[i + 3] - L.w);
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) d[i] = (i >= lo && i < hi) ? d[i] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+      tmem_st_32x32b_x32(tDP + lanes + 32 * half, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (warp_wait(acc_full, 0, abort_flag, p.status) && ok) {
+      tc_fence_after();
+      const int key = kt * kTile + row;
+      const int64_t tok = static_cast<int64_t>(t.start) + key;
+      const bool in = key < t.len;
+      uint16_t* dv = static_cast<uint16_t*>(p.dv.p) + tok * p.dv.token + kvh * p.dv.head;
+      uint16_t* dk = static_cast<uint16_t*>(p.dk.p) + tok * p.dk.token + kvh * p.dk.head;
+#pragma unroll 1
+      for (int q = half * (DP / 64); q < (half + 1) * (DP / 64); ++q) {
+        store_cols(tDV + lanes + 32 * q, 1.f, dv, 32 * q, p.D, in);
+        store_cols(tDK + lanes + 32 * q, p.scale, dk, 32 * q, p.D, in);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tS, kTmemCols);
+  }
+}
+
+// ======================================================================= dq
+// S has two buffers, so S of the next tile is complete before the elementwise
+// work of this one is; dS takes the place of its own S, which frees dP as soon
+// as it has been read.
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ CUtensorMap tmO, const AttnParams p) {
+  using S = BwdShape<DP>;
+  constexpr uint32_t TB = S::kTileBytes;
+  const int h = static_cast<int>(blockIdx.x % p.Hq);
+  const int idx = static_cast<int>(blockIdx.x / p.Hq);
+  if (idx >= *p.n_tiles) return;
+  const AttnTile t = p.tiles[idx];
+  const int n_kv = t.tile + 1;
+  const int kvh = h / (p.Hq / p.Hkv);
+  const int q0 = t.tile * kTile;
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* smQ = smem;
+  uint8_t* smO = smQ + TB;
+  uint8_t* smK = smO + TB;       // [3]
+  uint8_t* smV = smK + 3 * TB;   // [2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smV + 2 * TB);
+  uint64_t* qo_full = bars;
+  uint64_t* k_full = bars + 1;    // [3]
+  uint64_t* k_empty = bars + 4;   // [3]
+  uint64_t* v_full = bars + 7;    // [2]
+  uint64_t* v_empty = bars + 9;   // [2]
+  uint64_t* sdp_full = bars + 11;
+  uint64_t* dp_read = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* acc_full = bars + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 15; ++i) mbar_init(&bars[i], (i == 12 || i == 13) ? 8 : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tS = *tmem_slot, tDP = tS + 2 * kTile, tDQ = tDP + kTile;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(qo_full, 2 * TB);
+      load_tile<S::kBoxes>(&tmQ, qo_full, smQ, h, t.start + q0);
+      load_tile<S::kBoxes>(&tmO, qo_full, smO, h, t.start + q0);
+      int n_k = 0, n_v = 0;
+      for (int j = 0; j < n_kv; ++j) {
+        const int sk = j % 3, sv = j & 1;
+        const int tok = t.start + j * kTile;
+        if (!mbar_wait(&k_empty[sk], ((j / 3) & 1) ^ 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(&k_full[sk], TB);
+        load_tile<S::kBoxes>(&tmK, &k_full[sk], smK + sk * TB, kvh, tok);
+        ++n_k;
+        if (!mbar_wait(&v_empty[sv], ((j >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(&v_full[sv], TB);
+        load_tile<S::kBoxes>(&tmV, &v_full[sv], smV + sv * TB, kvh, tok);
+        ++n_v;
+      }
+      mbar_wait_drain(qo_full, 0);
+      for (int i = n_k > 3 ? n_k - 3 : 0; i < n_k; ++i)
+        mbar_wait_drain(&k_full[i % 3], (i / 3) & 1);
+      for (int i = n_v > 2 ? n_v - 2 : 0; i < n_v; ++i)
+        mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      const uint32_t aQ = smem_addr(smQ), aO = smem_addr(smO), aK = smem_addr(smK),
+                     aV = smem_addr(smV);
+      const int k_steps = (p.D + 15) / 16;
+      auto issue_s = [&](int j) {
+        if (!mbar_wait(&k_full[j % 3], (j / 3) & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        mma_over_d(tS + (j & 1) * kTile, aQ, aK + (j % 3) * TB, k_steps);
+        return true;
+      };
+      auto issue_dp = [&](int j) {
+        if (!mbar_wait(&v_full[j & 1], (j >> 1) & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        mma_over_d(tDP, aO, aV + (j & 1) * TB, k_steps);
+        mma_commit(&v_empty[j & 1]);
+        mma_commit(sdp_full);  // S of this tile was issued earlier
+        return true;
+      };
+      bool ok = mbar_wait(qo_full, 0, abort_flag, p.status) && issue_s(0) && issue_dp(0) &&
+                (n_kv < 2 || issue_s(1));
+      for (int j = 0; ok && j < n_kv; ++j) {
+        if (!mbar_wait(dp_read, j & 1, abort_flag, p.status)) break;
+        if (j + 1 < n_kv && !issue_dp(j + 1)) break;
+        if (!mbar_wait(ds_full, j & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        mma_over_rows_ts<DP>(tDQ, tS + (j & 1) * kTile, aK + (j % 3) * TB, j > 0);
+        mma_commit(&k_empty[j % 3]);
+        if (j + 2 < n_kv && !issue_s(j + 2)) break;
+      }
+      mma_commit(acc_full);
+      mbar_wait_drain(acc_full, 0);
+    }
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const int row = 32 * quarter + lane;
+    const bool in = q0 + row < t.len;
+    const int64_t tok = static_cast<int64_t>(t.start) + q0 + row;
+    const float c = p.scale * kLog2e;
+    const int64_t at = static_cast<int64_t>(h) * p.T + tok;
+    const float lse2 = in ? p.lse[at] * kLog2e : 0.f;
+    const float delta = in ? p.delta[at] : 0.f;
+    bool ok = true;
+    for (int j = 0; j < n_kv; ++j) {
+      const bool diag = j == n_kv - 1;
+      ok = warp_wait(sdp_full, j & 1, abort_flag, p.status) && ok;
+      tc_fence_after();
+      const uint32_t tSj = tS + (j & 1) * kTile;
+      float P[64], d[64];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        tmem_ld_32x32b_x32(tSj + lanes + 64 * half + 32 * q,
+                           reinterpret_cast<uint32_t(&)[32]>(P[32 * q]));
+        tmem_ld_32x32b_x32(tDP + lanes + 64 * half + 32 * q,
+                           reinterpret_cast<uint32_t(&)[32]>(d[32 * q]));
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dp_read);
+      named_barrier(2 + quarter, 64);  // the other half has read S too
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) d[i] = fast_exp2(fmaf(P[i], c, -lse2)) * (d[i] - delta);
+      if (diag) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) d[i] = i + 64 * half > row ? 0.f : d[i];
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+      tmem_st_32x32b_x32(tSj + lanes + 32 * half, w);
+      tmem_st_wait();
+      // S of this tile is complete, so K is only read again by dQ
+      if (diag && t.len - q0 < kTile) clear_rows<S::kBoxes>(smK + (j % 3) * TB, t.len - q0);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (warp_wait(acc_full, 0, abort_flag, p.status) && ok) {
+      tc_fence_after();
+      uint16_t* dq = static_cast<uint16_t*>(p.dq.p) + tok * p.dq.token + h * p.dq.head;
+#pragma unroll 1
+      for (int q = half * (DP / 64); q < (half + 1) * (DP / 64); ++q)
+        store_cols(tDQ + lanes + 32 * q, p.scale, dq, 32 * q, p.D, in);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tS, kTmemCols);
+  }
+}
+
+template <class KernelT>
+cudaError_t launch(KernelT kernel, uint32_t smem, unsigned blocks, bool overlap,
+                   const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, q, k, v, dO, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                             const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hkv);
+  return p.D <= 64 ? launch(attn_dkdv_kernel<64>, BwdShape<64>::kSmemDkDv, blocks, true, q, k, v,
+                            dO, p, s)
+                   : launch(attn_dkdv_kernel<128>, BwdShape<128>::kSmemDkDv, blocks, true, q, k,
+                            v, dO, p, s);
+}
+
+cudaError_t launch_attn_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                           const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hq);
+  return p.D <= 64 ? launch(attn_dq_kernel<64>, BwdShape<64>::kSmemDq, blocks, false, q, k, v, dO,
+                            p, s)
+                   : launch(attn_dq_kernel<128>, BwdShape<128>::kSmemDq, blocks, false, q, k, v,
+                            dO, p, s);
+}
+
+}  // namespace flce

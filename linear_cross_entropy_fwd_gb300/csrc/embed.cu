@@ -572,7 +572,7 @@ int flce_embed_fwd(const void* W, const void* ids, int64_t N, int64_t H, int64_t
   int sms = 0;
   if ((rc = host_device(&sms))) return rc;
   StepCall call;
-  if ((rc = call.begin(o, 0, false))) return rc;
+  if ((rc = call.begin(o, 0, StepCall::kIfAsked))) return rc;
   if (N > 0) {
     const int elt = o.dtype == FLCE_FP32 ? 4 : 2;
     const uint32_t nv = static_cast<uint32_t>(H * elt / 16);
@@ -609,7 +609,7 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   const int elt = o.dtype == FLCE_FP32 ? 4 : 2;
   const BwdPlan b = plan_bwd(N, H, V, elt, accumulate == 0);
   StepCall call;
-  if ((rc = call.begin(o, N > 0 ? b.total : 0, false))) return rc;
+  if ((rc = call.begin(o, N > 0 ? b.total : 0, StepCall::kIfAsked))) return rc;
   if (N == 0) {
     if (!accumulate) {
       const cudaError_t e =

@@ -839,8 +839,15 @@ int host_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what)
 int host_device(int* sms) {
   DeviceInfo D;
   const int rc = device_info(FLCE_BF16, &D);
-  if (rc == FLCE_OK) *sms = D.sms;
-  return rc;
+  if (rc != FLCE_OK) return rc;
+  *sms = D.sms;
+  // Encoding a tensor map needs a context on the calling thread, and a thread
+  // that has only launched through the runtime (a backward pass's worker) may
+  // have none yet.
+  int dev = 0;
+  FLCE_CUDA(cudaGetDevice(&dev));
+  FLCE_CUDA(cudaSetDevice(dev));
+  return FLCE_OK;
 }
 
 int host_pool_alloc(void** p, size_t bytes, cudaStream_t s) { return pool_alloc(p, bytes, s); }

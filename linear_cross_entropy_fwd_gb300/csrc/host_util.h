@@ -42,8 +42,11 @@ inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 struct StepCall {
   cudaStream_t stream = nullptr;
   uint8_t* scratch = nullptr;   // `bytes` bytes after the status word
-  int32_t* status = nullptr;    // device status word, cleared; nullptr when nothing needs it
-  int begin(const flce_opts& o, size_t bytes, bool status_needed);
+  int32_t* status = nullptr;    // device status word; nullptr when nothing needs it
+  // kIfAsked: a status word only if the caller looks at it; kCleared: always;
+  // kKernelClears: always, and the call's first kernel writes it.
+  enum Status { kIfAsked, kCleared, kKernelClears };
+  int begin(const flce_opts& o, size_t bytes, Status mode);
   int end(int rc);              // rc: what the launches returned
 
  private:

@@ -17,10 +17,10 @@ constexpr size_t kStatusBytes = 256;
 
 }  // namespace
 
-int StepCall::begin(const flce_opts& o, size_t bytes, bool status_needed) {
+int StepCall::begin(const flce_opts& o, size_t bytes, Status mode) {
   o_ = &o;
   stream = static_cast<cudaStream_t>(o.stream);
-  const bool want = status_needed || o.status_dev || o.sync;
+  const bool want = mode != kIfAsked || o.status_dev || o.sync;
   const size_t total = (want ? kStatusBytes : 0) + bytes;
   if (o.workspace_used) *o.workspace_used = kStatusBytes + bytes;
   if (total == 0) return FLCE_OK;
@@ -42,7 +42,9 @@ int StepCall::begin(const flce_opts& o, size_t bytes, bool status_needed) {
   scratch = base_ + (want ? kStatusBytes : 0);
   if (want) {
     status = reinterpret_cast<int32_t*>(base_);
-    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int32_t), stream);
+    const cudaError_t e = mode == kKernelClears
+                              ? cudaSuccess
+                              : cudaMemsetAsync(status, 0, sizeof(int32_t), stream);
     if (e != cudaSuccess) return end(host_cuda_error(e, "cudaMemsetAsync(status)"));
   }
   return FLCE_OK;

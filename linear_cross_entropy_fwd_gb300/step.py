@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from . import (_check, _check_out, _dtype_code, _is32, load_library, make_opts,
+from . import (FlceAttn, _check, _check_out, _dtype_code, _is32, load_library, make_opts,
                scale_convert)
 
 
@@ -128,3 +128,125 @@ class Embedding(torch.nn.Module):
 
     def forward(self, weight, ids):
         return _EmbedFunction.apply(weight, ids, self.scale, self.ignore_index)
+
+
+def _heads_tensor(name, t, shape, device):
+    """A bf16 [T, heads, D] tensor with a contiguous last axis on ``device``."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bf16, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have a contiguous last axis")
+
+
+def _attn_args(q, k, v, cu_seqlens, scale, o, lse):
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q [T, heads_q, D], k and v [T, heads_kv, D]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dev = q.device
+    _heads_tensor("q", q, (T, Hq, D), dev)
+    _heads_tensor("k", k, (T, Hkv, D), dev)
+    _heads_tensor("v", v, (T, Hkv, D), dev)
+    _heads_tensor("o", o, (T, Hq, D), dev)
+    _check_out(lse, (Hq, T), torch.float32, dev, "lse")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold one offset more than there are sequences")
+    _check_out(cu_seqlens, tuple(cu_seqlens.shape), torch.int32, dev, "cu_seqlens")
+    a = FlceAttn()
+    a.T, a.batch, a.cu_seqlens = T, cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    a.heads_q, a.heads_kv, a.head_dim = Hq, Hkv, D
+    a.scale = D ** -0.5 if scale is None else float(scale)
+    _put(a, q=q, k=k, v=v, o=o)
+    a.lse = lse.data_ptr()
+    return a
+
+
+def _put(a, **tensors):
+    for name, t in tensors.items():
+        setattr(a, name, t.data_ptr())
+        setattr(a, name + "_token", t.stride(0))
+        setattr(a, name + "_head", t.stride(1))
+
+
+def flce_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                  scale: float | None = None, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, sync: bool = False,
+                  workspace: torch.Tensor | None = None, info: dict | None = None):
+    """Causal attention over packed sequences; returns (o, lse).
+
+    q [T, heads_q, D], k and v [T, heads_kv, D] in bf16 with a contiguous last
+    axis (slices of one projection's output will do); ``cu_seqlens`` int32
+    [sequences + 1] on the device.  ``scale`` defaults to D ** -0.5.  o is
+    [T, heads_q, D], lse fp32 [heads_q, T]."""
+    lib = load_library()
+    if q.dim() != 3:
+        raise ValueError("q [T, heads_q, D], k and v [T, heads_kv, D]")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    a = _attn_args(q, k, v, cu_seqlens, scale, out, lse)
+    _call(lib.flce_attn_fwd, q.device, q.dtype, (ctypes.byref(a),), sync=sync,
+          workspace=workspace, info=info)
+    return out, lse
+
+
+def flce_attn_bwd(dO: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                  o: torch.Tensor, lse: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                  scale: float | None = None, dq: torch.Tensor | None = None,
+                  dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                  sync: bool = False, workspace: torch.Tensor | None = None,
+                  info: dict | None = None):
+    """Gradients of ``flce_attn_fwd`` at its inputs and outputs; returns
+    (dq, dk, dv) in bf16, dk and dv summed over the query heads they serve."""
+    lib = load_library()
+    a = _attn_args(q, k, v, cu_seqlens, scale, o, lse)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+    for name, t, like in (("dO", dO, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _heads_tensor(name, t, like.shape, q.device)
+    _put(a, dO=dO, dq=dq, dk=dk, dv=dv)
+    _call(lib.flce_attn_bwd, q.device, q.dtype, (ctypes.byref(a),), sync=sync,
+          workspace=workspace, info=info)
+    return dq, dk, dv
+
+
+def _strided(t):
+    """t itself if the library takes its strides, else a contiguous copy (a
+    broadcast axis has stride 0)."""
+    ok = (t.stride(2) == 1 and all(s > 0 and s % 8 == 0 for s in t.stride()[:2])
+          and t.data_ptr() % 16 == 0)
+    return t if ok else t.contiguous()
+
+
+class _AttnFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale):
+        q, k, v = _strided(q), _strided(k), _strided(v)
+        o, lse = flce_attn_fwd(q, k, v, cu_seqlens, scale=scale)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        dq, dk, dv = flce_attn_bwd(_strided(grad_out), q, k, v, o, lse, cu_seqlens,
+                                   scale=ctx.scale)
+        return dq, dk, dv, None, None
+
+
+class PackedAttention(torch.nn.Module):
+    """``attn(q, k, v, cu_seqlens)`` -> o, differentiable in q, k and v."""
+
+    def __init__(self, scale: float | None = None):
+        super().__init__()
+        self.scale = scale
+
+    def forward(self, q, k, v, cu_seqlens):
+        return _AttnFunction.apply(q, k, v, cu_seqlens, self.scale)

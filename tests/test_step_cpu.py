@@ -52,3 +52,64 @@ def test_embed_binding_refusals():
         flce.flce_embed_fwd(W, ids)
     with pytest.raises(ValueError):
         flce.flce_embed_bwd(torch.zeros(3, 8), ids, 5)
+
+
+def _attn(**kw):
+    """A flce_attn that no check refuses, with some fields replaced."""
+    a = flce.FlceAttn()
+    f = dict(T=300, batch=2, cu_seqlens=A, heads_q=4, heads_kv=2, head_dim=64, scale=0.125, lse=A)
+    for n, h in (("q", 4), ("k", 2), ("v", 2), ("o", 4), ("dO", 4), ("dq", 4), ("dk", 2),
+                 ("dv", 2)):
+        f.update({n: A, n + "_token": 64 * h, n + "_head": 64})
+    f.update(kw)
+    for n, x in f.items():
+        setattr(a, n, x)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), flce.FLCE_ERR_ARG),
+    (dict(T=(1 << 31) - 256), flce.FLCE_ERR_ARG),
+    (dict(batch=-1), flce.FLCE_ERR_ARG),
+    (dict(batch=1 << 29), flce.FLCE_ERR_ARG),        # too many CTAs
+    (dict(cu_seqlens=None), flce.FLCE_ERR_ARG),
+    (dict(heads_q=3), flce.FLCE_ERR_ARG),
+    (dict(heads_kv=0), flce.FLCE_ERR_ARG),
+    (dict(head_dim=0), flce.FLCE_ERR_ARG),
+    (dict(head_dim=68), flce.FLCE_ERR_ARG),
+    (dict(head_dim=136), flce.FLCE_ERR_ARG),
+    (dict(scale=0.0), flce.FLCE_ERR_ARG),
+    (dict(scale=float("inf")), flce.FLCE_ERR_ARG),
+    (dict(scale=float("nan")), flce.FLCE_ERR_ARG),
+    (dict(q=None), flce.FLCE_ERR_ARG),
+    (dict(o=None), flce.FLCE_ERR_ARG),
+    (dict(lse=None), flce.FLCE_ERR_ARG),
+    (dict(k_token=0), flce.FLCE_ERR_ARG),
+    (dict(k_head=0), flce.FLCE_ERR_ARG),
+    (dict(v_head=-64), flce.FLCE_ERR_ARG),
+    (dict(v_token=132), flce.FLCE_ERR_ALIGN),
+    (dict(k=A + 8), flce.FLCE_ERR_ALIGN),
+])
+def test_attention_refusals(lib, kw, status):
+    o = flce.make_opts(sync=0)
+    for fn in (lib.flce_attn_fwd, lib.flce_attn_bwd):
+        assert fn(ctypes.byref(_attn(**kw)), ctypes.byref(o)) == status
+        assert lib.flce_last_error()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dO=None), flce.FLCE_ERR_ARG),
+    (dict(dq=None), flce.FLCE_ERR_ARG),
+    (dict(dk_head=0), flce.FLCE_ERR_ARG),
+    (dict(dv=A + 4), flce.FLCE_ERR_ALIGN),
+])
+def test_attention_gradient_refusals(lib, kw, status):
+    o = flce.make_opts(sync=0)
+    assert lib.flce_attn_bwd(ctypes.byref(_attn(**kw)), ctypes.byref(o)) == status
+
+
+def test_attention_refuses_other_types(lib):
+    o = flce.make_opts(sync=0)
+    o.dtype = flce.FLCE_FP32
+    assert lib.flce_attn_fwd(ctypes.byref(_attn()), ctypes.byref(o)) == flce.FLCE_ERR_ARG
+    assert lib.flce_attn_fwd(None, None) == flce.FLCE_ERR_ARG
