@@ -386,6 +386,26 @@ FLCE_API int flce_attn_bwd(const flce_attn* a, const flce_opts* opts);
 /* sizeof(flce_attn) as compiled into the library. */
 FLCE_API size_t flce_attn_sizeof(void);
 
+/*
+ * Orthogonalises matrices by Newton-Schulz products (the update of a
+ * projection whose singular values are to become about 1):
+ *   X = G / (|G|_F + eps);  `steps` times:  A = X X^T,  X = a X + (b A + c A^2) X
+ * (with X^T X on the other side when rows > cols, which gives the same X).
+ *   G [batch, rows, cols] of type opts->dtype, contiguous; out bf16, same shape,
+ *   may not overlap G.  rows, cols <= 2^20; empty matrices are allowed.
+ *   coeffs: {a, b, c} on the host, or NULL for {3.4445, -4.7750, 2.0315}.  A
+ *   polynomial s (a + b s^2 + c s^4) that takes singular values of [0, 1] out
+ *   of the range of the products (|s| < 3.8, |b s^2 + c s^4| < 15) within
+ *   `steps` steps (1 .. 64) is refused with FLCE_ERR_ARG.
+ *   eps >= 0; a matrix of zeros gives zeros when eps > 0.
+ * Products take fp16 operands with fp32 sums, beside an fp32 X; the result is
+ * rounded to bf16 once.  |G|_F is summed in fp32 (finite for |G_ij| < 1e19).
+ * Scratch: about 8 bytes per element of G and 4 per element of A.
+ */
+FLCE_API int flce_orthogonalize(const void* G, int64_t batch, int64_t rows, int64_t cols,
+                                int32_t steps, const float* coeffs, float eps, void* out,
+                                const flce_opts* opts);
+
 #ifdef __cplusplus
 }
 #endif

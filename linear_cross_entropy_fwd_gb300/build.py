@@ -23,7 +23,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libflce.so")
 SOURCES = ["gemm_bf16.cu", "gemm_fp32.cu", "small_kernels.cu", "flce_api.cu",
            "step_common.cu", "embed.cu", "attn_plan.cu", "attn_fwd.cu", "attn_bwd.cu",
-           "attn_api.cu"]
+           "attn_api.cu", "ortho.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

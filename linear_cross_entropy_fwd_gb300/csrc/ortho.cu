@@ -1,0 +1,779 @@
+// ortho.cu -- orthogonalising an update by Newton-Schulz products.
+//
+//   X = G / (|G|_F + eps);  repeat: A = X X^T, B = b A + c A^2, X = a X + B X
+//
+// on [rows, cols] matrices, a batch at a time.  A matrix with more rows than
+// columns is transposed on the way in and out (X^T X takes the place of X X^T,
+// and the same polynomial results), so here X is k x n with k <= n.
+//
+// Numbers.  The products run on the tensor cores in fp16 with fp32 sums, X, A
+// and B stored as 4096 times their values: the entries of all three are below
+// 16 (their singular values are, see check_polynomial), and fp16 then holds
+// them to 2^-11 down to 2^-26.  X itself is kept in fp32 beside its fp16 copy,
+// and only B X goes through the rounded copies.  Without that, the rounding
+// errors of X in directions where X has (almost) nothing grow by a = 3.4 per
+// step with X: a nearly low-rank 512 x 512 matrix came out 3e-2 off, against
+// 2e-3 with it (bf16 operands: 2e-1 and 3e-3; the result's own rounding to
+// bf16 is 1.7e-3).
+//
+// A and A^2 are symmetric: tiles below the diagonal are computed, and written
+// twice.  That makes the flops of a step k^2 n + k^3 + 2 k^2 n.
+//
+// Launches: norm, split (fp32 and fp16 X), then three GEMMs per step.  Two
+// GEMM shapes, both with 32 KB stages of A and B, six deep: CTA pairs on
+// 256 x 256 tiles, and single CTAs on 128 x 128 tiles for small matrices.
+#include <cmath>
+
+#include "host_util.h"
+#include "sm103_attn.cuh"
+
+#include <cuda_fp16.h>
+
+namespace flce {
+namespace {
+
+constexpr float kHold = 4096.f;              // stored value / value
+constexpr float kUnhold = 1.f / 4096.f;
+constexpr int kStages = 6;
+constexpr uint32_t kHalfStage = 128 * 128;   // 128 rows x 64 fp16 (or two 64 x 64 boxes)
+constexpr uint32_t kStageBytes = 2 * kHalfStage;
+constexpr int kStagingBytes = 4096;          // one 32 x 32 fp32 block per epilogue warp
+constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + EPI_WARPS * kStagingBytes + 256;
+constexpr int kThreads = NUM_THREADS;        // TMA, MMA and four epilogue warps
+
+enum Mode { kGram, kPoly, kUpdate };
+
+struct OrthoParams {
+  int32_t m_blk, n_blk, k_blk;    // tiles of one matrix; K blocks of 64
+  int32_t tiles;                  // of one matrix (symmetric: on and below the diagonal)
+  int32_t batch;
+  int32_t symmetric;
+  int32_t rows, cols;             // of the output (k x k or k x n)
+  int64_t ld;                     // of the fp16 output, in elements
+  int64_t stride;                 // between matrices of the fp16 output
+  __half* out;                    // A, B or the next X, times 4096
+  const __half* gram;             // kPoly: A (same layout as out)
+  float* x;                       // kUpdate: X in fp32, [rows, ldx]
+  int64_t ldx, x_stride;
+  uint16_t* result;               // last kUpdate: bf16 result (out unused)
+  int32_t transposed;             // result is [cols, rows]
+  int32_t result_vec;             // result rows are whole 16-byte vectors
+  float a, b, c;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cluster,
+                                                 void* dst, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Tile t of one matrix.
+__device__ __forceinline__ void tile_of(const OrthoParams& p, int t, int& mi, int& ni) {
+  if (p.symmetric) {
+    int i = static_cast<int>((sqrtf(8.f * static_cast<float>(t) + 1.f) - 1.f) * 0.5f);
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    while (i * (i + 1) / 2 > t) --i;
+    mi = i;
+    ni = t - i * (i + 1) / 2;
+  } else {
+    mi = t % p.m_blk;  // a column of blocks together: they share a slab of X
+    ni = t / p.m_blk;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 rows (one per lane) x 32 columns to memory through shared memory, so
+// that each row goes out in whole 16-byte pieces next to one another.
+__device__ __forceinline__ void store_f32(uint8_t* buf, const float (&v)[32], float* dst,
+                                          int64_t ld, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_addr(buf);
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st_shared_v4(base + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+                 __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                 __float_as_uint(v[4 * c + 3]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3), c = lane & 7;
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    if (r < rows && 4 * c < cols) *reinterpret_cast<uint4*>(dst + r * ld + 4 * c) = w;
+  }
+  __syncwarp();
+}
+
+// The same for 16-bit values, already packed in pairs.
+__device__ __forceinline__ void store_16(uint8_t* buf, const uint32_t (&v)[16], uint16_t* dst,
+                                         int64_t ld, int rows, int cols, bool vec) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_addr(buf);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    st_shared_v4(base + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v[4 * c], v[4 * c + 1],
+                 v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), c = lane & 3;
+      const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      if (r < rows && 8 * c < cols) *reinterpret_cast<uint4*>(dst + r * ld + 8 * c) = w;
+    }
+  } else {
+    for (int r = 0; r < rows && r < 32; ++r) {
+      const int c = lane >> 3;
+      const uint16_t w = *reinterpret_cast<const uint16_t*>(
+          buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+      if (lane < cols) dst[r * ld + lane] = w;
+    }
+  }
+  __syncwarp();
+}
+
+// Column j of the block becomes row j of dst (32 lanes: 64 contiguous bytes).
+__device__ __forceinline__ void store_16_transposed(const uint32_t (&v)[16], uint16_t* dst,
+                                                    int64_t ld, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < cols && lane < rows)
+      dst[j * ld + lane] = static_cast<uint16_t>(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
+}
+
+// Epilogue of one accumulator: 128 rows of this CTA, columns [col0, col0 + width).
+template <int MODE>
+__device__ __forceinline__ void epilogue(const OrthoParams& p, uint32_t taddr, int bi, int row0,
+                                         int col0, int width, bool mirror, uint8_t* buf) {
+  const int lane = threadIdx.x & 31;
+  const int rows = p.rows - row0;  // of this warp's 32
+  if (rows <= 0) return;
+  const bool in = lane < rows;
+#pragma unroll 1
+  for (int u = 0; u < width; u += 32) {
+    const int c0 = col0 + u, cols = p.cols - c0;
+    if (cols <= 0) break;
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + u, r);
+    const int64_t at = bi * p.stride + (row0 + lane) * p.ld + c0;  // kGram, kPoly, X's copy
+    float v[32];
+    if (MODE == kUpdate) {
+      const float* x = p.x + bi * p.x_stride + (row0 + lane) * p.ldx + c0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in && 4 * i < cols) o = *reinterpret_cast<const float4*>(x + 4 * i);
+        v[4 * i] = o.x;
+        v[4 * i + 1] = o.y;
+        v[4 * i + 2] = o.z;
+        v[4 * i + 3] = o.w;
+      }
+    } else if (MODE == kPoly) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (in && 8 * i < cols) o = *reinterpret_cast<const uint4*>(p.gram + at + 8 * i);
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          v[8 * i + 2 * k] = f.x;
+          v[8 * i + 2 * k + 1] = f.y;
+        }
+      }
+    }
+    tmem_ld_wait();
+    // the accumulator holds 4096^2 times the product
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float acc = __uint_as_float(r[i]);
+      if (MODE == kGram)
+        v[i] = acc * kUnhold;
+      else if (MODE == kPoly)
+        v[i] = fmaf(p.c * kUnhold, acc, p.b * v[i]);
+      else
+        v[i] = fmaf(acc, kUnhold * kUnhold, p.a * v[i]);
+    }
+    uint32_t w[16];
+    if (MODE == kUpdate && p.result) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      uint16_t* res = p.result + static_cast<int64_t>(bi) * p.rows * p.cols;
+      if (p.transposed)
+        store_16_transposed(w, res + static_cast<int64_t>(c0) * p.rows + row0, p.rows, rows, cols);
+      else
+        store_16(buf, w, res + static_cast<int64_t>(row0) * p.cols + c0, p.cols, rows, cols,
+                 p.result_vec != 0);
+      continue;
+    }
+    if (MODE == kUpdate) {
+      store_f32(buf, v, p.x + bi * p.x_stride + row0 * p.ldx + c0, p.ldx, rows, cols);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= kHold;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + bi * p.stride;
+    store_16(buf, w, o + row0 * p.ld + c0, p.ld, rows, cols, true);
+    if (mirror) store_16_transposed(w, o + c0 * p.ld + row0, p.ld, rows, cols);
+  }
+}
+
+// D = A B^T (B K-major) or A B (B_MN: B stored [K, N]), one tile per
+// accumulator; persistent, the epilogue of a tile runs beside the MMAs of the
+// next.  PAIR: a cluster of two CTAs per 256 x 256 tile, else one CTA per
+// 128 x 128 tile.  Both operands come from the previous launch.
+template <int MODE, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    ortho_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const OrthoParams p) {
+  constexpr bool B_MN = MODE == kUpdate;
+  constexpr int kCtas = PAIR ? 2 : 1;
+  constexpr int kN = PAIR ? 256 : 128;
+  constexpr uint32_t kCols = 2 * kN;  // two accumulators
+  constexpr uint32_t kIdesc = make_idesc(0, false, B_MN, 128 * kCtas, kN);
+  constexpr uint32_t kBox = 64 * 128;  // one MN-major box: 64 K rows x 64 columns
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* staging = smem + kStages * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI_WARPS * kStagingBytes);
+  uint64_t* full = bars;                  // [kStages] (the even CTA's are the ones used)
+  uint64_t* empty = bars + kStages;       // [kStages]
+  uint64_t* acc_full = empty + kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2] (the even CTA's are the ones used)
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int unit = static_cast<int>(blockIdx.x) / kCtas;
+  const int units = static_cast<int>(gridDim.x) / kCtas;
+  const int total = p.tiles * p.batch;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], EPI_WARPS * kCtas);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, kCols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();  // the peer's barriers exist before any remote signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t gk = 0;
+      bool ok = true;
+      grid_dependency_wait();
+      for (int t = unit; ok && t < total; t += units) {
+        const int bi = t / p.tiles;
+        int mi, ni;
+        tile_of(p, t - bi * p.tiles, mi, ni);
+        const int a_row = (mi * kCtas + static_cast<int>(rank)) * 128;
+        const int b_row = ni * kN + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < p.k_blk; ++kb, ++gk) {
+          const uint32_t s = gk % kStages, r = gk / kStages;
+          if (!mbar_wait(&empty[s], (r & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], kCtas * kStageBytes);
+          uint8_t* a_dst = smem + s * kStageBytes;
+          uint8_t* b_dst = a_dst + kHalfStage;
+          const uint32_t fb = PAIR ? mapa_shared(smem_addr(&full[s]), 0) : smem_addr(&full[s]);
+          if (PAIR) {
+            tma_load_3d_pair(&tmA, fb, a_dst, 64 * kb, a_row, bi);
+            if (B_MN) {
+              tma_load_3d_pair(&tmB, fb, b_dst, b_row, 64 * kb, bi);
+              tma_load_3d_pair(&tmB, fb, b_dst + kBox, b_row + 64, 64 * kb, bi);
+            } else {
+              tma_load_3d_pair(&tmB, fb, b_dst, 64 * kb, b_row, bi);
+            }
+          } else {
+            tma_load_3d(&tmA, &full[s], a_dst, 64 * kb, a_row, bi);
+            if (B_MN) {
+              tma_load_3d(&tmB, &full[s], b_dst, b_row, 64 * kb, bi);
+              tma_load_3d(&tmB, &full[s], b_dst + kBox, b_row + 64, 64 * kb, bi);
+            } else {
+              tma_load_3d(&tmB, &full[s], b_dst, 64 * kb, b_row, bi);
+            }
+          }
+        }
+      }
+      // every stage this thread loaded has landed (the odd CTA's loads land on
+      // the even CTA's barrier: it waits until the MMAs released them)
+      const uint32_t n_drain = gk < kStages ? gk : kStages;
+      for (uint32_t i = 0; i < n_drain; ++i) {
+        const uint32_t q = gk - 1 - i;
+        mbar_wait_drain(rank == 0 ? &full[q % kStages] : &empty[q % kStages], (q / kStages) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0 && rank == 0) {
+      uint32_t gk = 0, it = 0;
+      bool ok = true;
+      const uint32_t base = smem_addr(smem);
+      for (int t = unit; ok && t < total; t += units, ++it) {
+        const uint32_t buf = it & 1, use = it >> 1;
+        if (!mbar_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * kN;
+        for (int kb = 0; kb < p.k_blk; ++kb, ++gk) {
+          const uint32_t s = gk % kStages, r = gk / kStages;
+          if (!mbar_wait(&full[s], r & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = base + s * kStageBytes, b = a + kHalfStage;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ad = smem_desc_sw128(a + 32 * k, 0, 1024);
+            const uint64_t bd = B_MN ? smem_desc_sw128(b + 2048 * k, kBox, 1024)
+                                     : smem_desc_sw128(b + 32 * k, 0, 1024);
+            const uint32_t add = (kb > 0 || k > 0) ? 1u : 0u;
+            if (PAIR)
+              mma_f16_pair(d, ad, bd, kIdesc, add);
+            else
+              mma_f16(d, ad, bd, kIdesc, add);
+          }
+          if (PAIR)
+            mma_commit_pair_mc(&empty[s], 0x3);
+          else
+            mma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        if (PAIR)
+          mma_commit_pair_mc(&acc_full[buf], 0x3);
+        else
+          mma_commit(&acc_full[buf]);
+      }
+      if (PAIR)
+        mma_commit_pair(drain);
+      else
+        mma_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    grid_dependency_wait();
+    if (warp == 2 && lane == 0) grid_launch_dependents();
+    const int q = warp & 3;
+    uint8_t* buf_s = staging + (warp - 2) * kStagingBytes;
+    uint32_t it = 0;
+    for (int t = unit; t < total; t += units, ++it) {
+      const uint32_t buf = it & 1, use = it >> 1;
+      if (!warp_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      const int bi = t / p.tiles;
+      int mi, ni;
+      tile_of(p, t - bi * p.tiles, mi, ni);
+      epilogue<MODE>(p, tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN, bi,
+                     (mi * kCtas + static_cast<int>(rank)) * 128 + 32 * q, ni * kN, kN,
+                     p.symmetric && mi != ni, buf_s);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_cluster(mapa_shared(smem_addr(&acc_empty[buf]), 0));
+        else
+          mbar_arrive(&acc_empty[buf]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();  // neither CTA leaves while the pair still uses it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, kCols);
+    else
+      tmem_dealloc(tmem_base, kCols);
+  }
+}
+
+// ------------------------------------------------------------- norm and split
+constexpr int kNormThreads = 256;
+constexpr int kMaxParts = 256;  // partial sums of one matrix
+
+template <int ELT>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  return ELT == 4 ? static_cast<const float*>(p)[i]
+                  : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i])
+                                    << 16);
+}
+
+// Sum over the CTA in a fixed order, in every thread.
+__device__ float cta_sum(float s) {
+  __shared__ float part[kNormThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  float all = 0.f;
+#pragma unroll
+  for (int w = 0; w < kNormThreads / 32; ++w) all += part[w];
+  __syncthreads();
+  return all;
+}
+
+// parts[b][x] = sum of squares of the x-th share of matrix b.
+template <int ELT>
+__global__ void __launch_bounds__(kNormThreads)
+    ortho_norm(const void* g, int64_t elems, int vec, float* parts) {
+  const int64_t base = static_cast<int64_t>(blockIdx.y) * elems;
+  float s = 0.f;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kNormThreads;
+  if (vec) {
+    constexpr int kPer = 16 / ELT;
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + base * ELT);
+    const int64_t n = elems / kPer;
+#pragma unroll 4
+    for (int64_t i = me; i < n; i += step) {
+      const uint4 q = __ldg(v + i);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (ELT == 4) {
+          const float f = __uint_as_float(w[k]);
+          s = fmaf(f, f, s);
+        } else {
+          const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+          s = fmaf(lo, lo, s);
+          s = fmaf(hi, hi, s);
+        }
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int64_t i = me; i < elems; i += step) {
+      const float f = load1<ELT>(g, base + i);
+      s = fmaf(f, f, s);
+    }
+  }
+  s = cta_sum(s);
+  if (threadIdx.x == 0) parts[static_cast<int64_t>(blockIdx.y) * kMaxParts + blockIdx.x] = s;
+}
+
+struct SplitParams {
+  const void* g;
+  int64_t rows, cols;      // of G
+  const float* parts;
+  int32_t n_parts;
+  float eps;
+  float* x;                // [k][ldx]
+  __half* xh;              // [k][ldh]
+  int64_t ldx, ldh, x_stride, h_stride;
+};
+
+// X = G / (|G| + eps) in fp32 and, times 4096, in fp16; 64 x 64 blocks, which
+// TRANSPOSED turns around in shared memory.
+template <int ELT, bool TRANSPOSED>
+__global__ void __launch_bounds__(kNormThreads) ortho_split(const SplitParams p) {
+  __shared__ float tile[TRANSPOSED ? 64 : 1][65];
+  const int b = static_cast<int>(blockIdx.z);
+  float part = threadIdx.x < p.n_parts ? p.parts[static_cast<int64_t>(b) * kMaxParts + threadIdx.x]
+                                       : 0.f;
+  const float inv = 1.f / (sqrtf(cta_sum(part)) + p.eps);
+  const int64_t base = static_cast<int64_t>(b) * p.rows * p.cols;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
+  float* x = p.x + b * p.x_stride;
+  __half* xh = p.xh + b * p.h_stride;
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;  // 64 x 4
+  if (TRANSPOSED) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) {
+      const int64_t r = r0 + ty + i, c = c0 + tx;
+      tile[ty + i][tx] = (r < p.rows && c < p.cols) ? load1<ELT>(p.g, base + r * p.cols + c) : 0.f;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 64; i += 4) {
+    // row and column of X (k x n)
+    const int64_t r = (TRANSPOSED ? c0 : r0) + ty + i, c = (TRANSPOSED ? r0 : c0) + tx;
+    const int64_t k = TRANSPOSED ? p.cols : p.rows, n = TRANSPOSED ? p.rows : p.cols;
+    if (r >= k) continue;
+    float v = 0.f;
+    if (c < n) v = (TRANSPOSED ? tile[tx][ty + i] : load1<ELT>(p.g, base + r * p.cols + c)) * inv;
+    if (c < p.ldx) x[r * p.ldx + c] = v;
+    if (c < p.ldh) xh[r * p.ldh + c] = __float2half_rn(v * kHold);
+  }
+}
+
+// --------------------------------------------------------------------- host
+// The singular values of X start in [0, 1] and each step takes s to
+// p(s) = s (a + b s^2 + c s^4).  Bounds |s| over the steps by p's values at the
+// ends of the interval and at its turning points; false if |s|, or an
+// eigenvalue b s^2 + c s^4 of B, or s^2 leaves the range fp16 holds here.
+bool check_polynomial(double a, double b, double c, int steps) {
+  if (!(std::isfinite(a) && std::isfinite(b) && std::isfinite(c))) return false;
+  double top = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    const double t = top * top;  // s^2 in [0, t]
+    double eig = std::fabs(b * t + c * t * t);
+    if (c != 0.0) {
+      const double v = -b / (2 * c);
+      if (v > 0 && v < t) eig = std::fmax(eig, std::fabs(b * v + c * v * v));
+    }
+    if (!(eig < 15.0) || !(t < 15.0)) return false;
+    auto value = [&](double s2) { return std::fabs(std::sqrt(s2) * (a + b * s2 + c * s2 * s2)); };
+    double next = value(t);
+    // p'(s) = a + 3 b s^2 + 5 c s^4 = 0
+    if (c != 0.0) {
+      const double disc = 9 * b * b - 20 * a * c;
+      if (disc >= 0) {
+        for (int sign = -1; sign <= 1; sign += 2) {
+          const double r = (-3 * b + sign * std::sqrt(disc)) / (10 * c);
+          if (r > 0 && r < t) next = std::fmax(next, value(r));
+        }
+      }
+    } else if (b != 0.0) {
+      const double r = -a / (3 * b);
+      if (r > 0 && r < t) next = std::fmax(next, value(r));
+    }
+    top = next * 1.001;  // rounding of the operands
+    if (!(top < 3.8)) return false;
+  }
+  return true;
+}
+
+struct Layout {
+  int64_t k, n, ldx, ldh, lda;
+  int32_t parts;
+  size_t off_parts, off_x, off_h[2], off_a, off_b, total;
+};
+
+Layout layout(int64_t batch, int64_t rows, int64_t cols) {
+  Layout l{};
+  l.k = rows < cols ? rows : cols;
+  l.n = rows < cols ? cols : rows;
+  l.ldx = (l.n + 63) / 64 * 64;
+  l.ldh = l.ldx;
+  l.lda = (l.k + 63) / 64 * 64;
+  const int64_t elems = rows * cols;
+  int64_t parts = (elems + 8191) / 8192;
+  l.parts = static_cast<int32_t>(parts < 1 ? 1 : parts > kMaxParts ? kMaxParts : parts);
+  size_t o = 0;
+  const size_t B = static_cast<size_t>(batch);
+  l.off_parts = o;
+  o += round256(B * kMaxParts * 4);
+  l.off_x = o;
+  o += round256(B * static_cast<size_t>(l.k * l.ldx) * 4);
+  for (int i = 0; i < 2; ++i) {
+    l.off_h[i] = o;
+    o += round256(B * static_cast<size_t>(l.k * l.ldh) * 2);
+  }
+  l.off_a = o;
+  o += round256(B * static_cast<size_t>(l.k * l.lda) * 2);
+  l.off_b = o;
+  o += round256(B * static_cast<size_t>(l.k * l.lda) * 2);
+  l.total = o;
+  return l;
+}
+
+// An fp16 [batch][rows][cols] operand; box of 64 columns by `box_rows`.
+int half_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
+             int64_t batch, uint32_t box_rows, const char* what) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows),
+                            static_cast<uint64_t>(batch)};
+  const uint64_t pitch[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[3] = {64, box_rows, 1};
+  return host_tensor_map(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, pitch, box, what);
+}
+
+template <int MODE, bool PAIR>
+cudaError_t launch_shape(const CUtensorMap& A, const CUtensorMap& B, OrthoParams p, int64_t k,
+                         int sms, cudaStream_t s) {
+  const int tile = PAIR ? 256 : 128;
+  p.m_blk = (p.rows + tile - 1) / tile;
+  p.n_blk = (p.cols + tile - 1) / tile;
+  p.k_blk = static_cast<int32_t>((k + 63) / 64);
+  p.symmetric = MODE != kUpdate;
+  p.tiles = p.symmetric ? p.m_blk * (p.m_blk + 1) / 2 : p.m_blk * p.n_blk;
+  const auto kernel = ortho_gemm<MODE, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t total = static_cast<int64_t>(p.tiles) * p.batch;
+  const int64_t cap = PAIR ? sms / 2 : sms;
+  const int units = static_cast<int>(total < cap ? total : cap);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(static_cast<unsigned>(units * (PAIR ? 2 : 1)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // the prologue overlaps the previous launch's tail; loads and stores wait
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, A, B, p);
+}
+
+// Pairs where their 256 x 256 tiles fill at least half of the GPU's CTA pairs.
+template <int MODE>
+cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoParams& p, int64_t k,
+                        int sms, cudaStream_t s) {
+  const int64_t mb = (p.rows + 255) / 256, nb = (p.cols + 255) / 256;
+  const int64_t pair_tiles = (MODE != kUpdate ? mb * (mb + 1) / 2 : mb * nb) * p.batch;
+  return pair_tiles * 2 >= sms / 2 ? launch_shape<MODE, true>(A, B, p, k, sms, s)
+                                   : launch_shape<MODE, false>(A, B, p, k, sms, s);
+}
+
+int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps,
+        const float* coeffs, float eps, void* out, const Layout& l, uint8_t* w, int32_t* status,
+        int sms, cudaStream_t s) {
+  float* parts = reinterpret_cast<float*>(w + l.off_parts);
+  float* x = reinterpret_cast<float*>(w + l.off_x);
+  __half* h[2] = {reinterpret_cast<__half*>(w + l.off_h[0]),
+                  reinterpret_cast<__half*>(w + l.off_h[1])};
+  __half* A = reinterpret_cast<__half*>(w + l.off_a);
+  __half* Bm = reinterpret_cast<__half*>(w + l.off_b);
+  const int64_t elems = rows * cols;
+  const int elt = dtype == FLCE_FP32 ? 4 : 2;
+  const int vec = aligned16(g) && (elems * elt) % 16 == 0;
+  const unsigned nb = static_cast<unsigned>(batch);
+  const dim3 ngrid(static_cast<unsigned>(l.parts), nb);
+  if (elt == 4)
+    ortho_norm<4><<<ngrid, kNormThreads, 0, s>>>(g, elems, vec, parts);
+  else
+    ortho_norm<2><<<ngrid, kNormThreads, 0, s>>>(g, elems, vec, parts);
+  FLCE_TRY(cudaGetLastError());
+  const SplitParams sp{g,   rows, cols,  parts, l.parts,      eps,
+                       x,   h[0], l.ldx, l.ldh, l.k * l.ldx,  l.k * l.ldh};
+  const dim3 sgrid(static_cast<unsigned>((cols + 63) / 64), static_cast<unsigned>((rows + 63) / 64),
+                   nb);
+  const bool tr = rows > cols;
+  if (elt == 4)
+    tr ? ortho_split<4, true><<<sgrid, kNormThreads, 0, s>>>(sp)
+       : ortho_split<4, false><<<sgrid, kNormThreads, 0, s>>>(sp);
+  else
+    tr ? ortho_split<2, true><<<sgrid, kNormThreads, 0, s>>>(sp)
+       : ortho_split<2, false><<<sgrid, kNormThreads, 0, s>>>(sp);
+  FLCE_TRY(cudaGetLastError());
+  int rc;
+  CUtensorMap mx[2], mxn[2], ma, mb;
+  for (int i = 0; i < 2; ++i) {
+    if ((rc = half_map(&mx[i], h[i], l.k, l.n, l.ldh, l.k * l.ldh, batch, 128, "X"))) return rc;
+    if ((rc = half_map(&mxn[i], h[i], l.k, l.n, l.ldh, l.k * l.ldh, batch, 64, "X^T"))) return rc;
+  }
+  if ((rc = half_map(&ma, A, l.k, l.k, l.lda, l.k * l.lda, batch, 128, "A"))) return rc;
+  if ((rc = half_map(&mb, Bm, l.k, l.k, l.lda, l.k * l.lda, batch, 128, "B"))) return rc;
+  OrthoParams p{};
+  p.batch = static_cast<int32_t>(batch);
+  p.rows = static_cast<int32_t>(l.k);
+  p.x = x;
+  p.ldx = l.ldx;
+  p.x_stride = l.k * l.ldx;
+  p.a = coeffs[0];
+  p.b = coeffs[1];
+  p.c = coeffs[2];
+  p.status = status;
+  for (int i = 0; i < steps; ++i) {
+    p.cols = static_cast<int32_t>(l.k);
+    p.ld = l.lda;
+    p.stride = l.k * l.lda;
+    p.out = A;
+    FLCE_TRY(launch_gemm<kGram>(mx[i & 1], mx[i & 1], p, l.n, sms, s));
+    p.out = Bm;
+    p.gram = A;
+    FLCE_TRY(launch_gemm<kPoly>(ma, ma, p, l.k, sms, s));
+    p.cols = static_cast<int32_t>(l.n);
+    p.ld = l.ldh;
+    p.stride = l.k * l.ldh;
+    p.out = h[(i + 1) & 1];
+    if (i == steps - 1) {
+      p.result = static_cast<uint16_t*>(out);
+      p.transposed = tr;
+      p.result_vec = aligned16(out) && cols % 8 == 0;
+    }
+    FLCE_TRY(launch_gemm<kUpdate>(mb, mxn[i & 1], p, l.k, sms, s));
+  }
+  return FLCE_OK;
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" int flce_orthogonalize(const void* G, int64_t batch, int64_t rows, int64_t cols,
+                                  int32_t steps, const float* coeffs, float eps, void* out,
+                                  const flce_opts* opts) {
+  host_clear_error();
+  const flce_opts o = opts_or_default(opts);
+  if (o.dtype != FLCE_BF16 && o.dtype != FLCE_FP32)
+    return host_error(FLCE_ERR_ARG, "flce_orthogonalize: unknown dtype %d", o.dtype);
+  if (batch < 0 || rows < 0 || cols < 0 || batch > 65535 || rows > (1 << 20) || cols > (1 << 20))
+    return host_error(FLCE_ERR_ARG,
+                      "flce_orthogonalize: 0 <= batch <= 65535 and 0 <= rows, cols <= 2^20");
+  if (steps < 1 || steps > 64)
+    return host_error(FLCE_ERR_ARG, "flce_orthogonalize: steps must be in 1 .. 64");
+  if (!(eps >= 0.f) || std::isinf(eps))
+    return host_error(FLCE_ERR_ARG, "flce_orthogonalize: eps must be finite and not negative");
+  const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
+  const float* c = coeffs ? coeffs : standard;
+  if (!check_polynomial(c[0], c[1], c[2], steps))
+    return host_error(FLCE_ERR_ARG,
+                      "flce_orthogonalize: the polynomial takes singular values of [0, 1] out of "
+                      "the range of the fp16 products");
+  const bool empty = batch == 0 || rows == 0 || cols == 0;
+  if (!empty && (!G || !out)) return host_error(FLCE_ERR_ARG, "flce_orthogonalize: null pointer");
+  const uintptr_t el = o.dtype == FLCE_FP32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(G) & el) || (reinterpret_cast<uintptr_t>(out) & 1))
+    return host_error(FLCE_ERR_ALIGN, "flce_orthogonalize: misaligned pointer");
+  int sms = 0;
+  int rc = host_device(&sms);
+  if (rc) return rc;
+  const Layout l = layout(batch, rows, cols);
+  const int64_t blocks = (l.k + 127) / 128 * ((l.n + 127) / 128) * batch;
+  if (blocks >= (int64_t{1} << 31) || (rows + 63) / 64 > 65535)
+    return host_error(FLCE_ERR_ARG, "flce_orthogonalize: too many tiles");
+  StepCall call;
+  if ((rc = call.begin(o, empty ? 0 : l.total, empty ? StepCall::kIfAsked : StepCall::kCleared)))
+    return rc;
+  if (!empty)
+    rc = run(G, o.dtype, batch, rows, cols, steps, c, eps, out, l, call.scratch, call.status, sms,
+             call.stream);
+  return call.end(rc);
+}

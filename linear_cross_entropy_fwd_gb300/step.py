@@ -250,3 +250,31 @@ class PackedAttention(torch.nn.Module):
 
     def forward(self, q, k, v, cu_seqlens):
         return _AttnFunction.apply(q, k, v, cu_seqlens, self.scale)
+
+
+def flce_orthogonalize(G: torch.Tensor, *, steps: int = 5,
+                       coeffs: tuple[float, float, float] = (3.4445, -4.7750, 2.0315),
+                       eps: float = 1e-7, out: torch.Tensor | None = None, sync: bool = False,
+                       workspace: torch.Tensor | None = None, info: dict | None = None):
+    """Newton-Schulz orthogonalisation of each matrix of G [..., rows, cols]
+    (bf16 or fp32): ``X = G / (|G|_F + eps)``, then ``steps`` times
+    ``X = a X + (b A + c A A) X`` with ``A = X X^T``.  Returns X in bf16."""
+    lib = load_library()
+    if G.dim() < 2 or not G.is_cuda or not G.is_contiguous():
+        raise ValueError("G must be a contiguous CUDA tensor [..., rows, cols]")
+    _dtype_code(G)
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be (a, b, c)")
+    rows, cols = G.shape[-2:]
+    batch = 1
+    for n in G.shape[:-2]:
+        batch *= n
+    if out is None:
+        out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+    else:
+        _check_out(out, G.shape, torch.bfloat16, G.device, "out")
+    abc = (ctypes.c_float * 3)(*coeffs)
+    _call(lib.flce_orthogonalize, G.device, G.dtype,
+          (G.data_ptr(), batch, rows, cols, int(steps), ctypes.cast(abc, ctypes.c_void_p),
+           float(eps), out.data_ptr()), sync=sync, workspace=workspace, info=info)
+    return out

@@ -113,3 +113,36 @@ def test_attention_refuses_other_types(lib):
     o.dtype = flce.FLCE_FP32
     assert lib.flce_attn_fwd(ctypes.byref(_attn()), ctypes.byref(o)) == flce.FLCE_ERR_ARG
     assert lib.flce_attn_fwd(None, None) == flce.FLCE_ERR_ARG
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(G=None), flce.FLCE_ERR_ARG),
+    (dict(out=None), flce.FLCE_ERR_ARG),
+    (dict(batch=-1), flce.FLCE_ERR_ARG),
+    (dict(batch=65536), flce.FLCE_ERR_ARG),
+    (dict(rows=-1), flce.FLCE_ERR_ARG),
+    (dict(cols=(1 << 20) + 1), flce.FLCE_ERR_ARG),
+    (dict(steps=0), flce.FLCE_ERR_ARG),
+    (dict(steps=65), flce.FLCE_ERR_ARG),
+    (dict(eps=-1e-3), flce.FLCE_ERR_ARG),
+    (dict(eps=float("nan")), flce.FLCE_ERR_ARG),
+    (dict(dtype=9), flce.FLCE_ERR_ARG),
+    (dict(G=A + 1), flce.FLCE_ERR_ALIGN),
+    (dict(out=A + 1), flce.FLCE_ERR_ALIGN),
+    (dict(coeffs=(float("nan"), 0, 0)), flce.FLCE_ERR_ARG),
+    (dict(coeffs=(4.0, 0.0, 0.0)), flce.FLCE_ERR_ARG),      # s -> 4 s
+    (dict(coeffs=(3.0, 0.0, 0.0), steps=2), flce.FLCE_ERR_ARG),
+    (dict(coeffs=(1.0, -16.0, 0.0)), flce.FLCE_ERR_ARG),    # B out of range
+    (dict(coeffs=(1.0, 0.0, 3.0), steps=2), flce.FLCE_ERR_ARG),
+    (dict(coeffs=(3.4445, -4.7750, 2.6)), flce.FLCE_ERR_ARG),  # the standard one, grown
+])
+def test_orthogonalize_refusals(lib, kw, status):
+    a = dict(G=A, batch=1, rows=8, cols=16, steps=5, coeffs=None, eps=1e-7, out=A,
+             dtype=flce.FLCE_BF16)
+    a.update(kw)
+    o = flce.make_opts(sync=0)
+    o.dtype = a["dtype"]
+    c = None if a["coeffs"] is None else (ctypes.c_float * 3)(*a["coeffs"])
+    assert lib.flce_orthogonalize(a["G"], a["batch"], a["rows"], a["cols"], a["steps"], c,
+                                  a["eps"], a["out"], ctypes.byref(o)) == status
+    assert lib.flce_last_error()
