@@ -8,16 +8,21 @@
 //
 // The gradient sums equal ids in ascending token order, in fp32, and gives
 // the same bits on every run: no floating-point atomics.  Three launches:
-//   1  sort     tokens by id, stable (one 8-CTA cluster, radix digits of at
-//               most 9 bits).  One launch, because its phases need only a
-//               cluster barrier between them.
-//   2  sum      CTA c walks entries [c*C, (c+1)*C) of the sorted order and
-//               adds up runs of one id.  A run inside the chunk goes straight
-//               to dW; a run that crosses a chunk's border leaves an fp32
-//               partial row.  When dW is overwritten, further CTAs of the same
-//               launch write zeros to the rows no token has (a bitmap made by
-//               the sort says which), so each row is written once.
-//   3  join     adds the partial rows of each crossing run, in order.
+//   1  sort     tokens by id, stable (radix digits of at most 9 bits), in one
+//               launch: one CTA with everything in shared memory for up to
+//               2048 tokens (7 to 13 us; at 4096 21 us against the cluster's
+//               13), else one 8-CTA cluster, whose phases need only a cluster
+//               barrier between them (14 us at 8192 tokens, 46 at 65536).  When
+//               64 MB or more are cleared meanwhile, one CTA up to 4096 tokens:
+//               the clearing takes as long, and runs on all other SMs (128 MB
+//               in 19 us, against 23 beside a cluster).  When dW is overwritten, the
+//               other CTAs of the launch clear it meanwhile.
+//   2  sum      a run of one id is cut into pieces of at most L entries; CTA c
+//               adds up the pieces that begin in entries [c*C, (c+1)*C) of the
+//               sorted order.  A run of one piece goes straight to dW; the
+//               pieces of a longer one leave fp32 partial rows, and the run
+//               goes on a list.
+//   3  join     adds the partial rows of each run on the list, in order.
 #include "host_util.h"
 #include "sm103.cuh"
 
@@ -88,22 +93,30 @@ __global__ void __launch_bounds__(kFwdThreads)
 }
 
 // --------------------------------------------------------------------- sort
-constexpr int kSortCtas = 8;
+constexpr int kSortCtas = 8;           // of the cluster, for more tokens than one CTA holds
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
-constexpr int kSortSmem = (kSortWarps * kMaxDigits + 2 * kMaxDigits + 32) * 4;
+constexpr int kOneCtaTokens = 4096;  // that fit
+constexpr int kOneCtaFaster = 2048;
+constexpr int64_t kClearHides = int64_t{64} << 20;
+constexpr int kHistBytes = (kSortWarps * kMaxDigits + 2 * kMaxDigits + 32) * 4;
+
+// Shared memory of the sort: one CTA keeps the (key, token) pairs twice.
+constexpr int sort_smem(int ctas) { return kHistBytes + (ctas == 1 ? kOneCtaTokens * 16 : 0); }
 
 struct SortParams {
   Ids ids;
   int64_t N;               // < 2^31
   int64_t V;
   int64_t ignore_index;
-  uint32_t* key[2];        // [N] each; the last pass writes key[passes & 1]
-  uint32_t* pos[2];
-  uint32_t* bitmap;        // ceil(V / 32) words: rows that have a token (or NULL)
-  uint32_t* n_sorted;      // tokens that take part
+  uint2* pair[2];          // [N] (key, token): scratch of the cluster's passes
+  uint32_t* key;           // [N] sorted
+  uint32_t* pos;           // [N] the tokens in that order
+  uint32_t* counts;        // [0] tokens that take part, [1] runs to join
+  float4* clear;           // dW, to be cleared (or NULL)
+  int64_t clear_vecs;
   int32_t passes, digit_bits;
   int32_t* status;
 };
@@ -120,19 +133,17 @@ __device__ uint32_t cta_exclusive_sum(uint32_t x, uint32_t* warp_sums) {
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    uint32_t w = lane < kSortWarps ? warp_sums[lane] : 0u;
+    const uint32_t w = warp_sums[lane];
     uint32_t winc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, winc, o);
       if (lane >= o) winc += y;
     }
-    if (lane < kSortWarps) warp_sums[lane] = winc - w;
+    warp_sums[lane] = winc - w;
   }
   __syncthreads();
-  const uint32_t r = warp_sums[warp] + inc - x;
-  __syncthreads();
-  return r;
+  return warp_sums[warp] + inc - x;
 }
 
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr) {
@@ -141,63 +152,79 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr)
   return v;
 }
 
-// Least-significant-digit radix sort.  Token i belongs to the warp whose
-// contiguous range holds it, and warps are ordered by (CTA rank, warp), so
-// placing each warp's tokens in order after all earlier warps' tokens of the
-// same digit keeps equal digits in input order (stable).  Ignored and bad ids
-// get the key V, which sorts behind every row.
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1)
-    embed_sort_kernel(const SortParams p) {
+// The lanes whose digit (of `bits` bits) is this lane's; `in`: whether the lane
+// has one.  One ballot per bit.
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, int bits, bool in) {
+  uint32_t peers = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+  for (int b = 0; b < kMaxDigitBits; ++b) {
+    if (b < bits) {
+      const uint32_t m = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+      peers &= (d >> b) & 1u ? m : ~m;
+    }
+  }
+  return peers;
+}
+
+// Least-significant-digit radix sort.  A warp owns a contiguous range of the
+// entries, and warps are ordered by (CTA rank, warp), so placing each warp's
+// entries in order after all earlier warps' entries of the same digit keeps
+// equal digits in input order (stable).  Ignored and bad ids get the key V,
+// which sorts behind every row.
+template <int CTAS>
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortParams p) {
+  grid_launch_dependents();
+  if (blockIdx.x >= CTAS) {  // not the sorting CTAs
+    const int64_t step = static_cast<int64_t>(gridDim.x - CTAS) * kSortThreads;
+#pragma unroll 4
+    for (int64_t i = static_cast<int64_t>(blockIdx.x - CTAS) * kSortThreads + threadIdx.x;
+         i < p.clear_vecs; i += step)
+      __stcs(p.clear + i, make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
   extern __shared__ uint32_t sm[];
   uint32_t* hist = sm;                                // [warp][digit]
   uint32_t* total = sm + kSortWarps * kMaxDigits;     // [digit] this CTA's count
   uint32_t* base = total + kMaxDigits;                // [digit] first place of this CTA
   uint32_t* warp_sums = base + kMaxDigits;
+  uint2* own = reinterpret_cast<uint2*>(warp_sums + 32);  // CTAS == 1: two lists of pairs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = CTAS > 1 ? cluster_ctarank() : 0u;
   const uint32_t gwarp = rank * kSortWarps + warp;
-  const int64_t per_warp = (p.N + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps);
+  const int64_t per_warp = (p.N + CTAS * kSortWarps - 1) / (CTAS * kSortWarps);
   const int64_t lo = gwarp * per_warp < p.N ? gwarp * per_warp : p.N;
   const int64_t hi = lo + per_warp < p.N ? lo + per_warp : p.N;
   const uint32_t digits = 1u << p.digit_bits;
-
-  if (p.bitmap) {
-    const int64_t words = (p.V + 31) / 32;
-    for (int64_t w = rank * kSortThreads + tid; w < words; w += kSortCtas * kSortThreads)
-      p.bitmap[w] = 0u;
-  }
-  if (rank == 0 && tid == 0) *p.n_sorted = 0u;
+  uint32_t taking_part = 0u;  // of this warp's tokens
+  if (rank == 0 && tid < 2) p.counts[tid] = 0u;
 
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.digit_bits;
-    const uint32_t* key_in = p.key[pass & 1];
-    const uint32_t* pos_in = p.pos[pass & 1];
-    uint32_t* key_out = p.key[(pass + 1) & 1];
-    uint32_t* pos_out = p.pos[(pass + 1) & 1];
-    auto load = [&](int64_t i, uint32_t& k, uint32_t& q) {
-      if (pass == 0) {
-        const int64_t id = p.ids[i];
-        const bool in = id >= 0 && id < p.V && id != p.ignore_index;
-        k = in ? static_cast<uint32_t>(id) : static_cast<uint32_t>(p.V);
-        q = static_cast<uint32_t>(i);
-        return in || id == p.ignore_index;
-      }
-      k = __ldcg(key_in + i);
-      q = __ldcg(pos_in + i);
-      return true;
-    };
+    const bool odd = pass & 1;
+    uint2* in = CTAS > 1 ? (odd ? p.pair[1] : p.pair[0]) : own + odd * kOneCtaTokens;
+    uint2* out = CTAS > 1 ? (odd ? p.pair[0] : p.pair[1]) : own + !odd * kOneCtaTokens;
     for (uint32_t d = lane; d < digits; d += 32) hist[warp * kMaxDigits + d] = 0u;
     __syncwarp();
     // count (each warp owns its row of the histogram)
     for (int64_t i0 = lo; i0 < hi; i0 += 32) {
       const int64_t i = i0 + lane;
       uint32_t d = 0xffffffffu;
+      bool part = false;
       if (i < hi) {
-        uint32_t k, q;
-        if (!load(i, k, q) && p.status) atomicOr(p.status, FLCE_DEV_TARGET);
+        uint32_t k;
+        if (pass == 0) {
+          const int64_t id = p.ids[i];
+          part = id >= 0 && id < p.V && id != p.ignore_index;
+          if (!part && id != p.ignore_index && p.status) atomicOr(p.status, FLCE_DEV_TARGET);
+          k = part ? static_cast<uint32_t>(id) : static_cast<uint32_t>(p.V);
+          in[i] = make_uint2(k, static_cast<uint32_t>(i));
+        } else {
+          k = CTAS > 1 ? __ldcg(&in[i].x) : in[i].x;
+        }
         d = (k >> shift) & (digits - 1);
       }
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      if (pass == 0) taking_part += __popc(__ballot_sync(0xffffffffu, part));
+      const uint32_t peers = same_digit(d, p.digit_bits, i < hi);
       if (i < hi && lane == __ffs(peers) - 1) hist[warp * kMaxDigits + d] += __popc(peers);
       __syncwarp();
     }
@@ -205,75 +232,85 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     // per digit: offsets of the warps within the CTA, and the CTA's count
     uint32_t mine = 0u;
     if (tid < static_cast<int>(digits)) {
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = hist[w * kMaxDigits + tid];
         hist[w * kMaxDigits + tid] = mine;
         mine += c;
       }
-      total[tid] = mine;
+      if (CTAS > 1) total[tid] = mine;
     }
-    cluster_sync();
-    uint32_t all = 0u, before = 0u;
-    if (tid < static_cast<int>(digits)) {
-      const uint32_t a = smem_addr(&total[tid]);
+    uint32_t all = mine, before = 0u;
+    if (CTAS > 1) {
+      cluster_sync();
+      if (tid < static_cast<int>(digits)) {
+        const uint32_t a = smem_addr(&total[tid]);
+        all = 0u;
 #pragma unroll
-      for (uint32_t r = 0; r < kSortCtas; ++r) {
-        const uint32_t c = ld_shared_cluster_u32(mapa_shared(a, r));
-        if (r < rank) before += c;
-        all += c;
+        for (int r = 0; r < CTAS; ++r) {
+          const uint32_t c = ld_shared_cluster_u32(mapa_shared(a, static_cast<uint32_t>(r)));
+          if (r < static_cast<int>(rank)) before += c;
+          all += c;
+        }
       }
     }
     const uint32_t first = cta_exclusive_sum(all, warp_sums);
     if (tid < static_cast<int>(digits)) base[tid] = first + before;
     __syncthreads();
+    // counts[0] was cleared before the barriers just passed
+    if (pass == 0 && lane == 0 && taking_part) atomicAdd(p.counts, taking_part);
     // place
+    const bool last = pass == p.passes - 1;
     for (int64_t i0 = lo; i0 < hi; i0 += 32) {
       const int64_t i = i0 + lane;
-      uint32_t d = 0xffffffffu, k = 0u, q = 0u;
+      uint32_t d = 0xffffffffu;
+      uint2 e = make_uint2(0u, 0u);
       if (i < hi) {
-        load(i, k, q);
-        d = (k >> shift) & (digits - 1);
+        e = CTAS > 1 ? __ldcg(in + i) : in[i];
+        d = (e.x >> shift) & (digits - 1);
       }
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      const uint32_t peers = same_digit(d, p.digit_bits, i < hi);
       if (i < hi) {
-        const uint32_t before_me = __popc(peers & ((1u << lane) - 1u));
-        const uint32_t at = base[d] + hist[warp * kMaxDigits + d] + before_me;
-        key_out[at] = k;
-        pos_out[at] = q;
+        const uint32_t at = base[d] + hist[warp * kMaxDigits + d] +
+                            __popc(peers & ((1u << lane) - 1u));
+        if (last) {
+          p.key[at] = e.x;
+          p.pos[at] = e.y;
+        } else {
+          out[at] = e;
+        }
       }
       __syncwarp();
       if (i < hi && lane == __ffs(peers) - 1) hist[warp * kMaxDigits + d] += __popc(peers);
       __syncwarp();
     }
-    cluster_sync();  // this pass's keys are in place; every `total` has been read
-  }
-  // the rows that have a token, and where the ignored tokens begin
-  const uint32_t* key = p.key[p.passes & 1];
-  for (int64_t i = rank * kSortThreads + tid; i < p.N; i += kSortCtas * kSortThreads) {
-    const uint32_t k = __ldcg(key + i);
-    if (k >= p.V) continue;
-    const uint32_t next = i + 1 < p.N ? __ldcg(key + i + 1) : static_cast<uint32_t>(p.V);
-    if (next != k && p.bitmap) atomicOr(p.bitmap + (k >> 5), 1u << (k & 31));
-    if (next >= p.V) *p.n_sorted = static_cast<uint32_t>(i + 1);
+    // this pass's entries are in place, and every `total` has been read
+    if (CTAS > 1)
+      cluster_sync();
+    else
+      __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------- sum
-constexpr int kSumThreads = 256;
-constexpr int kSumVecs = 2;  // 16-byte vectors of a row per thread
+constexpr int kSumThreads = 256;  // at most: one per 16-byte vector of a row
+constexpr int kAhead = 8;         // rows in flight
 constexpr int kMaxChunk = 64;
+constexpr int kMinPiece = 32;
+constexpr int kMaxPiece = kMaxChunk;  // pieces are at least as long as chunks
 
 struct SumParams {
   const void* dY;
   const uint32_t* key;       // sorted
   const uint32_t* pos;
-  const uint32_t* n_sorted;
-  const uint32_t* bitmap;    // with dW overwritten
+  uint32_t* counts;          // see SortParams
+  uint32_t* runs;            // [chunks] where the runs to join begin
   float* dW;
-  float* partial;            // [chunks][2][H]: a run that came in, a run that goes on
+  float* partial;            // [chunks][2][H]: the last piece of a run; any other piece
   int64_t H, V;
   uint32_t nv;               // 16-byte vectors of dY per row
-  int32_t chunk;             // sorted entries per CTA
+  int32_t chunk;             // C: entries per CTA
+  int32_t piece;             // L >= C
   int32_t chunks;
   int32_t accumulate;
   float scale;
@@ -306,167 +343,164 @@ struct Acc {  // the elements of one 16-byte vector in fp32
   }
 };
 
-// dW row piece: (dW +) scale * sum
+// dW row piece: (dW +) scale * sum.  The addition is done at L2, so that no
+// thread waits for the old value; every element gets one addend.
 __device__ __forceinline__ void finish4(float* dst, float4 v, float scale, bool accumulate) {
-  float4* d = reinterpret_cast<float4*>(dst);
   v.x *= scale;
   v.y *= scale;
   v.z *= scale;
   v.w *= scale;
-  if (accumulate) {
-    const float4 o = *d;
-    v.x += o.x;
-    v.y += o.y;
-    v.z += o.z;
-    v.w += o.w;
-  }
-  *d = v;
+  if (accumulate)
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+  else
+    *reinterpret_cast<float4*>(dst) = v;
 }
 
-// Rows that no token has, one warp per row.
-__device__ void write_zero_rows(const SumParams& p, int64_t block, int64_t blocks) {
-  const int lane = threadIdx.x & 31;
-  const int64_t h4 = p.H / 4;
-  for (int64_t r = block * (kSumThreads / 32) + (threadIdx.x >> 5); r < p.V;
-       r += blocks * (kSumThreads / 32)) {
-    if ((__ldg(p.bitmap + (r >> 5)) >> (r & 31)) & 1u) continue;
-    float4* row = reinterpret_cast<float4*>(p.dW + r * p.H);
-    for (int64_t c = lane; c < h4; c += 32) __stcs(row + c, make_float4(0.f, 0.f, 0.f, 0.f));
-  }
-}
-
-// Grid: x = chunks (then CTAs that write zero rows), y = slices of the row.
+// Grid: x = chunks, y = slices of the row.  Since L >= C, at most one piece
+// that does not end its run begins in a chunk, and at most one that ends a run
+// begun earlier: two partial rows per chunk hold whatever a chunk leaves.
 template <int ELT>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams p) {
-  if (static_cast<int>(blockIdx.x) >= p.chunks) {
-    write_zero_rows(p, (blockIdx.x - p.chunks) * gridDim.y + blockIdx.y,
-                    static_cast<int64_t>(gridDim.x - p.chunks) * gridDim.y);
-    return;
-  }
-  __shared__ uint32_t s_key[kMaxChunk + 2];  // with the neighbours on both sides
-  __shared__ uint32_t s_pos[kMaxChunk];
-  const int64_t n = *p.n_sorted;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __shared__ uint32_t s_key[kMaxChunk + kMaxPiece + 2];  // entry i0 - 1 + t at t
+  __shared__ uint32_t s_pos[kMaxChunk + kMaxPiece];
+  const int64_t n = p.counts[0];
+  const int C = p.chunk, L = p.piece, threads = static_cast<int>(blockDim.x);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * C;
   if (i0 >= n) return;
-  const int cnt = static_cast<int>(n - i0 < p.chunk ? n - i0 : p.chunk);
+  const int cnt = static_cast<int>(n - i0 < C + L ? n - i0 : C + L);  // entries in reach
   constexpr uint32_t kNone = 0xffffffffu;  // no row has this id (ids < 2^31)
-  for (int t = threadIdx.x; t < cnt + 2; t += kSumThreads) {
+  for (int t = threadIdx.x; t < cnt + 2; t += threads) {
     const int64_t i = i0 + t - 1;
-    s_key[t] = (i >= 0 && i < n) ? __ldg(p.key + i) : kNone;
-    if (t >= 1 && t <= cnt) s_pos[t - 1] = __ldg(p.pos + i);
+    s_key[t] = (i >= 0 && i < n) ? __ldcg(p.key + i) : kNone;
+    if (t >= 1 && t <= cnt) s_pos[t - 1] = __ldcg(p.pos + i);
   }
   __syncthreads();
+  const uint32_t* key = s_key + 1;
+  int j = 0;            // first entry of the next piece
+  bool first = true;    // it begins its run
+  if (key[-1] == key[0]) {
+    // the run began earlier: how much earlier decides where its pieces begin.
+    // Its first entry is in [b0, b1]; every round probes one place per thread between.
+    int64_t b0 = 0, b1 = i0 - 1;
+    while (b0 < b1) {
+      const int64_t step = (b1 - b0 + threads - 1) / threads;
+      const int64_t i = b0 + threadIdx.x * step;
+      const int less = __syncthreads_count(i < b1 && __ldcg(p.key + i) < key[0]);
+      const int64_t top = b0 + less * step;  // the first probe that is not less, or past them
+      if (top < b1) b1 = top;
+      if (less > 0) b0 = b0 + (less - 1) * step + 1;
+    }
+    const int64_t back = i0 - b1;
+    const uint32_t k0 = key[0];
+    const int next = static_cast<int>((L - back % L) % L);
+    while (j < next && j < cnt && key[j] == k0) ++j;
+    first = !(j < cnt && key[j] == k0);
+  }
   const uint4* dY = static_cast<const uint4*>(p.dY);
-  const uint32_t c0 = blockIdx.y * (kSumThreads * kSumVecs) + threadIdx.x;
-  Acc<ELT> acc[kSumVecs];
-#pragma unroll
-  for (int u = 0; u < kSumVecs; ++u) acc[u].zero();
-  bool came_in = s_key[0] == s_key[1];
-  constexpr int kAhead = 4;  // rows in flight
-  for (int j0 = 0; j0 < cnt; j0 += kAhead) {
-    uint4 v[kAhead][kSumVecs];
+  const uint32_t c = blockIdx.y * threads + threadIdx.x;  // vector of the row
+  if (c >= p.nv) return;
+  constexpr int kN = Acc<ELT>::kN;
+  Acc<ELT> acc;
+  acc.zero();
+  int from = j;  // first entry of the current piece
+  bool done = j >= C || j >= cnt;
+  while (!done) {
+    uint4 v[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) {
-        const uint32_t c = c0 + u * kSumThreads;
-        if (j0 + a < cnt && c < p.nv)
-          v[a][u] = __ldcs(dY + static_cast<int64_t>(s_pos[j0 + a]) * p.nv + c);
-      }
+      if (j + a < cnt) v[a] = __ldcs(dY + static_cast<int64_t>(s_pos[j + a]) * p.nv + c);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int j = j0 + a;
-      if (j >= cnt) break;
+      if (done) break;
+      acc.add(v[a]);
+      const uint32_t k = key[j];
+      ++j;
+      const bool goes_on = key[j] == k;  // key[cnt] is in place too
+      if (goes_on && j - from < L) continue;
+      if (goes_on && first && c == 0)
+        p.runs[atomicAdd(p.counts + 1, 1u)] =  // in any order: the runs are disjoint
+            static_cast<uint32_t>(i0 + from);
+      if (!first || goes_on) {
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (goes_on ? 1 : 0);
+        acc.put(p.partial + slot * p.H + static_cast<int64_t>(c) * kN);
+      } else {
+        float* dst = p.dW + static_cast<int64_t>(k) * p.H + static_cast<int64_t>(c) * kN;
 #pragma unroll
-      for (int u = 0; u < kSumVecs; ++u)
-        if (c0 + u * kSumThreads < p.nv) acc[u].add(v[a][u]);
-      if (s_key[j + 2] == s_key[j + 1] && j + 1 < cnt) continue;  // the run goes on here
-      const bool goes_on = s_key[j + 2] == s_key[j + 1];
-      constexpr int kN = Acc<ELT>::kN;
-#pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) {
-        const uint32_t c = c0 + u * kSumThreads;
-        if (c < p.nv) {
-          if (came_in || goes_on) {
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (came_in ? 0 : 1);
-            acc[u].put(p.partial + slot * p.H + static_cast<int64_t>(c) * kN);
-          } else {
-            float* dst = p.dW + static_cast<int64_t>(s_key[j + 1]) * p.H +
-                         static_cast<int64_t>(c) * kN;
-#pragma unroll
-            for (int k = 0; k < kN; k += 4)
-              finish4(dst + k,
-                      make_float4(acc[u].a[k], acc[u].a[k + 1], acc[u].a[k + 2], acc[u].a[k + 3]),
-                      p.scale, p.accumulate != 0);
-          }
-        }
-        acc[u].zero();
+        for (int e = 0; e < kN; e += 4)
+          finish4(dst + e, make_float4(acc.a[e], acc.a[e + 1], acc.a[e + 2], acc.a[e + 3]),
+                   p.scale, p.accumulate != 0);
       }
-      came_in = false;
+      acc.zero();
+      first = !goes_on;
+      from = j;
+      done = j >= C || j >= cnt;
     }
   }
 }
 
 // --------------------------------------------------------------------- join
-// CTA (c, y): if a run begins in chunk c and goes on into chunk c + 1, adds
-// its partial rows: chunk c's second slot, then the first slot of each chunk
-// up to the one where the run ends.  Eight groups of threads take contiguous
-// shares of those chunks; their sums are added in order.
-constexpr int kJoinCols = 32;    // float4 columns per CTA
+// One work item per (run on the list, slice of the row).  The pieces of a run
+// that begins at entry r begin at r, r + L, r + 2 L, ...; each left its sum with
+// the chunk it begins in.  Eight groups of threads take contiguous shares of
+// the pieces; their sums are added in order.
+constexpr int kJoinCols = 32;    // float4 columns per item
 constexpr int kJoinGroups = 8;
 constexpr int kJoinThreads = kJoinCols * kJoinGroups;
 
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParams p) {
-  const int64_t n = *p.n_sorted;
-  const int64_t C = p.chunk;
-  const int64_t c = blockIdx.x;
-  const int64_t after = (c + 1) * C;  // first entry of the next chunk
-  if (after >= n) return;
-  const uint32_t k = __ldg(p.key + after);
-  if (__ldg(p.key + after - 1) != k) return;                        // no run goes on
-  if (c > 0 && __ldg(p.key + c * C) == k && __ldg(p.key + c * C - 1) == k) return;  // began earlier
-  // chunks c+1 .. last begin with the run's id
-  int64_t last = c;
-  for (;;) {
-    const int64_t e = (last + 1 + threadIdx.x) * C;
-    const int hit = __syncthreads_count(e < n && __ldg(p.key + e) == k);
-    last += hit;
-    if (hit < kJoinThreads) break;
-  }
-  const int group = threadIdx.x / kJoinCols, col = threadIdx.x % kJoinCols;
-  const int64_t h4 = p.H / 4;
-  const int64_t x = static_cast<int64_t>(blockIdx.y) * kJoinCols + col;
-  const int64_t parts = last - c;  // of the first-slot partials
-  const int64_t share = (parts + kJoinGroups - 1) / kJoinGroups;
-  const int64_t lo = c + 1 + group * share;
-  const int64_t hi = lo + share < last + 1 ? lo + share : last + 1;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* part = reinterpret_cast<const float4*>(p.partial);
-  if (x < h4) {
-    if (group == 0) s = __ldcs(part + (2 * c + 1) * h4 + x);
-#pragma unroll 8
-    for (int64_t q = lo; q < hi; ++q) {
-      const float4 v = __ldcs(part + 2 * q * h4 + x);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-  }
+  grid_dependency_wait();
   __shared__ float4 s_part[kJoinGroups][kJoinCols];
-  s_part[group][col] = s;
-  __syncthreads();
-  if (group == 0 && x < h4) {
-#pragma unroll
-    for (int g = 1; g < kJoinGroups; ++g) {
-      const float4 v = s_part[g][col];
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+  const int64_t n = p.counts[0];
+  const int64_t C = p.chunk, L = p.piece;
+  const int64_t h4 = p.H / 4;
+  const int64_t slices = (h4 + kJoinCols - 1) / kJoinCols;
+  const int64_t items = p.counts[1] * slices;
+  const float4* part = reinterpret_cast<const float4*>(p.partial);
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t r = __ldcg(p.runs + item / slices);
+    const uint32_t k = __ldcg(p.key + r);
+    int64_t pieces = 0;
+    for (;;) {
+      const int64_t e = r + (pieces + threadIdx.x) * L;
+      const int hit = __syncthreads_count(e < n && __ldcg(p.key + e) == k);
+      pieces += hit;
+      if (hit < kJoinThreads) break;
     }
-    finish4(p.dW + static_cast<int64_t>(k) * p.H + 4 * x, s, p.scale, p.accumulate != 0);
-  }
+    const int group = threadIdx.x / kJoinCols, col = threadIdx.x % kJoinCols;
+    const int64_t x = item % slices * kJoinCols + col;
+    const int64_t share = (pieces + kJoinGroups - 1) / kJoinGroups;
+    const int64_t lo = group * share;
+    const int64_t hi = lo + share < pieces ? lo + share : pieces;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (x < h4) {
+#pragma unroll 8
+      for (int64_t q = lo; q < hi; ++q) {
+        const int64_t slot = 2 * ((r + q * L) / C) + (q + 1 < pieces ? 1 : 0);
+        const float4 v = __ldcs(part + slot * h4 + x);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+    }
+    s_part[group][col] = s;
+    __syncthreads();
+    if (group == 0 && x < h4) {
+#pragma unroll
+      for (int g = 1; g < kJoinGroups; ++g) {
+        const float4 v = s_part[g][col];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      finish4(p.dW + static_cast<int64_t>(k) * p.H + 4 * x, s, p.scale, p.accumulate != 0);
+    }
+  }  // the next item's barrier comes before s_part is written again
 }
 
 // --------------------------------------------------------------------- host
@@ -490,69 +524,102 @@ int check_embed(const char* who, const void* table, const void* rows, const void
   return FLCE_OK;
 }
 
+bool one_cta_sorts(int64_t N, int64_t clear_bytes) {
+  return N <= kOneCtaFaster || (N <= kOneCtaTokens && clear_bytes >= kClearHides);
+}
+
 struct BwdPlan {
-  int32_t passes, digit_bits, chunk, chunks;
-  size_t key[2], pos[2], bitmap, n_sorted, partial, total;
+  int32_t passes, digit_bits, chunk, piece, chunks;
+  size_t key, pos, pair[2], counts, runs, partial, total;
 };
 
-// Entries per CTA of the sum: enough CTAs for eight on each of 152 SMs, so
-// short inputs spread over the GPU; at most kMaxChunk.
-BwdPlan plan_bwd(int64_t N, int64_t H, int64_t V, int elt, bool dense) {
+// Entries per CTA of the sum: enough CTAs for twelve on each of 152 SMs,
+// within 4 .. kMaxChunk.
+BwdPlan plan_bwd(int64_t N, int64_t H, int64_t V, int elt) {
   BwdPlan b{};
   int bits = 1;
   while ((int64_t{1} << bits) <= V) ++bits;  // keys 0 .. V
   b.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   b.digit_bits = (bits + b.passes - 1) / b.passes;
-  const int64_t slices = (H * elt / 16 + kSumThreads * kSumVecs - 1) / (kSumThreads * kSumVecs);
-  int64_t c = (N * slices + 152 * 8 - 1) / (152 * 8);
+  const int64_t slices = (H * elt / 16 + kSumThreads - 1) / kSumThreads;
+  int64_t c = (N * slices + 152 * 12 - 1) / (152 * 12);
   if (c < 4) c = 4;
   if (c > kMaxChunk) c = kMaxChunk;
   b.chunk = static_cast<int32_t>(c);
+  b.piece = b.chunk > kMinPiece ? b.chunk : kMinPiece;
   b.chunks = static_cast<int32_t>((N + c - 1) / c);
   size_t o = 0;
   const size_t list = round256(static_cast<size_t>(N) * 4);
+  b.key = o;
+  o += list;
+  b.pos = o;
+  o += list;
   for (int i = 0; i < 2; ++i) {
-    b.key[i] = o;
-    o += list;
-    b.pos[i] = o;
-    o += list;
+    b.pair[i] = o;
+    if (N > kOneCtaFaster) o += round256(static_cast<size_t>(N) * 8);
   }
-  b.bitmap = o;
-  if (dense) o += round256(static_cast<size_t>((V + 31) / 32) * 4);
-  b.n_sorted = o;
+  b.counts = o;
   o += 256;
+  b.runs = o;
+  o += round256(static_cast<size_t>(b.chunks) * 4);
   b.partial = o;
   o += round256(static_cast<size_t>(b.chunks) * 2 * static_cast<size_t>(H) * 4);
   b.total = o;
   return b;
 }
 
-int run_bwd(const void* dY, const SortParams& sort, const SumParams& sum_in, int elt, int sms,
-            cudaStream_t s) {
-  SumParams sum = sum_in;
-  FLCE_TRY(cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSortSmem));
-  embed_sort_kernel<<<kSortCtas, kSortThreads, kSortSmem, s>>>(sort);
-  FLCE_TRY(cudaGetLastError());
-  const unsigned slices =
-      static_cast<unsigned>((sum.nv + kSumThreads * kSumVecs - 1) / (kSumThreads * kSumVecs));
-  unsigned x = static_cast<unsigned>(sum.chunks);
-  if (!sum.accumulate) {
-    const int64_t want = (sum.V + kSumThreads / 32 - 1) / (kSumThreads / 32);
-    const int64_t cap = static_cast<int64_t>(sms) * 8;
-    x += static_cast<unsigned>(want < cap ? want : cap);
-  }
-  if (elt == 2)
-    embed_sum_kernel<2><<<dim3(x, slices), kSumThreads, 0, s>>>(sum);
-  else
-    embed_sum_kernel<4><<<dim3(x, slices), kSumThreads, 0, s>>>(sum);
-  FLCE_TRY(cudaGetLastError());
-  if (sum.chunks > 1) {
-    const unsigned cols = static_cast<unsigned>((sum.H / 4 + kJoinCols - 1) / kJoinCols);
-    embed_join_kernel<<<dim3(static_cast<unsigned>(sum.chunks - 1), cols), kJoinThreads, 0, s>>>(
-        sum);
-    FLCE_TRY(cudaGetLastError());
-  }
+// A launch whose CTAs may start while the previous launch finishes; the kernel
+// waits for it before it reads.
+template <class KernelT, class P>
+cudaError_t launch_after(KernelT kernel, dim3 grid, int threads, const P& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int CTAS>
+cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(embed_sort_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           sort_smem(CTAS));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  // the sorting CTAs, and others that clear: one on each of the other SMs, or
+  // 14 clusters, which find room beside the sorting one
+  const int clear = p.clear ? (CTAS == 1 ? sms - 1 : 14 * CTAS) : 0;
+  cfg.gridDim = dim3(static_cast<unsigned>(CTAS + clear));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = sort_smem(CTAS);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, embed_sort_kernel<CTAS>, p);
+}
+
+int run_bwd(const SortParams& sort, const SumParams& sum, int elt, int sms, cudaStream_t s) {
+  FLCE_TRY(one_cta_sorts(sort.N, sort.clear ? sort.clear_vecs * 16 : 0)
+               ? launch_sort<1>(sort, sms, s)
+               : launch_sort<kSortCtas>(sort, sms, s));
+  const unsigned slices = (sum.nv + kSumThreads - 1) / kSumThreads;
+  const int threads = static_cast<int>(((sum.nv + slices - 1) / slices + 31) / 32 * 32);
+  const dim3 g(static_cast<unsigned>(sum.chunks), slices);
+  FLCE_TRY(elt == 2 ? launch_after(embed_sum_kernel<2>, g, threads, sum, s)
+                    : launch_after(embed_sum_kernel<4>, g, threads, sum, s));
+  if (sort.N > sum.piece)  // else no run is longer than a piece
+    FLCE_TRY(launch_after(embed_join_kernel, dim3(static_cast<unsigned>(sms) * 4), kJoinThreads,
+                          sum, s));
   return FLCE_OK;
 }
 
@@ -607,7 +674,7 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   int sms = 0;
   if ((rc = host_device(&sms))) return rc;
   const int elt = o.dtype == FLCE_FP32 ? 4 : 2;
-  const BwdPlan b = plan_bwd(N, H, V, elt, accumulate == 0);
+  const BwdPlan b = plan_bwd(N, H, V, elt);
   StepCall call;
   if ((rc = call.begin(o, N > 0 ? b.total : 0, StepCall::kIfAsked))) return rc;
   if (N == 0) {
@@ -624,31 +691,32 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   sp.N = N;
   sp.V = V;
   sp.ignore_index = ignore_index;
-  for (int i = 0; i < 2; ++i) {
-    sp.key[i] = reinterpret_cast<uint32_t*>(w + b.key[i]);
-    sp.pos[i] = reinterpret_cast<uint32_t*>(w + b.pos[i]);
-  }
-  sp.bitmap = accumulate ? nullptr : reinterpret_cast<uint32_t*>(w + b.bitmap);
-  sp.n_sorted = reinterpret_cast<uint32_t*>(w + b.n_sorted);
+  sp.key = reinterpret_cast<uint32_t*>(w + b.key);
+  sp.pos = reinterpret_cast<uint32_t*>(w + b.pos);
+  for (int i = 0; i < 2; ++i) sp.pair[i] = reinterpret_cast<uint2*>(w + b.pair[i]);
+  sp.counts = reinterpret_cast<uint32_t*>(w + b.counts);
+  sp.clear = accumulate ? nullptr : reinterpret_cast<float4*>(dW);
+  sp.clear_vecs = V * H / 4;
   sp.passes = b.passes;
   sp.digit_bits = b.digit_bits;
   sp.status = call.status;
   SumParams sm{};
   sm.dY = dY;
-  sm.key = sp.key[b.passes & 1];
-  sm.pos = sp.pos[b.passes & 1];
-  sm.n_sorted = sp.n_sorted;
-  sm.bitmap = sp.bitmap;
+  sm.key = sp.key;
+  sm.pos = sp.pos;
+  sm.counts = sp.counts;
+  sm.runs = reinterpret_cast<uint32_t*>(w + b.runs);
   sm.dW = dW;
   sm.partial = reinterpret_cast<float*>(w + b.partial);
   sm.H = H;
   sm.V = V;
   sm.nv = static_cast<uint32_t>(H * elt / 16);
   sm.chunk = b.chunk;
+  sm.piece = b.piece;
   sm.chunks = b.chunks;
   sm.accumulate = accumulate != 0 ? 1 : 0;
   sm.scale = scale;
-  return call.end(run_bwd(dY, sp, sm, elt, sms, call.stream));
+  return call.end(run_bwd(sp, sm, elt, sms, call.stream));
 }
 
 }  // extern "C"

@@ -38,8 +38,9 @@ constexpr int kStages = 6;
 constexpr uint32_t kHalfStage = 128 * 128;   // 128 rows x 64 fp16 (or two 64 x 64 boxes)
 constexpr uint32_t kStageBytes = 2 * kHalfStage;
 constexpr int kStagingBytes = 4096;          // one 32 x 32 fp32 block per epilogue warp
-constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + EPI_WARPS * kStagingBytes + 256;
-constexpr int kThreads = NUM_THREADS;        // TMA, MMA and four epilogue warps
+constexpr int kEpiWarps = 8;                 // two per quarter of the TMEM lanes
+constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStagingBytes + 256;
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // TMA, MMA, epilogue
 
 enum Mode { kGram, kPoly, kUpdate };
 
@@ -149,58 +150,64 @@ __device__ __forceinline__ void store_16_transposed(const uint32_t (&v)[16], uin
       dst[j * ld + lane] = static_cast<uint16_t>(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
 }
 
-// Epilogue of one accumulator: 128 rows of this CTA, columns [col0, col0 + width).
+// What the epilogue adds the product to: 32 columns of this lane's row of X
+// (fp32) or of A (fp16), and the rows of its matrix that this warp has.
 template <int MODE>
-__device__ __forceinline__ void epilogue(const OrthoParams& p, uint32_t taddr, int bi, int row0,
-                                         int col0, int width, bool mirror, uint8_t* buf) {
+struct Addend {
+  uint4 v[MODE == kUpdate ? 8 : 4];
+  __device__ __forceinline__ void load(const OrthoParams& p, int bi, int row, int c0) {
+    if (MODE == kGram) return;
+    constexpr int kPer = MODE == kUpdate ? 4 : 8;  // elements per vector
+    const uint4* src =
+        MODE == kUpdate
+            ? reinterpret_cast<const uint4*>(p.x + bi * p.x_stride + row * p.ldx + c0)
+            : reinterpret_cast<const uint4*>(p.gram + bi * p.stride + row * p.ld + c0);
+    const int n = row < p.rows ? p.cols - c0 : 0;
+#pragma unroll
+    for (int i = 0; i < 32 / kPer; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (kPer * i < n) v[i] = __ldcg(src + i);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if (MODE == kGram) return 0.f;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+    if (MODE == kUpdate) return __uint_as_float(w[i]);
+    const __half2 h = *reinterpret_cast<const __half2*>(w + (i >> 1));
+    return i & 1 ? __high2float(h) : __low2float(h);
+  }
+};
+
+// Epilogue of 32 rows of an accumulator, columns [col0, col0 + width); `add`
+// holds the first 32 columns' addend, fetched before the accumulator was
+// complete, and each later one is fetched while the one before it is stored.
+template <int MODE>
+__device__ __forceinline__ void epilogue(const OrthoParams& p, Addend<MODE>& add, uint32_t taddr,
+                                         int bi, int row0, int col0, int width, bool mirror,
+                                         uint8_t* buf) {
   const int lane = threadIdx.x & 31;
   const int rows = p.rows - row0;  // of this warp's 32
   if (rows <= 0) return;
-  const bool in = lane < rows;
 #pragma unroll 1
   for (int u = 0; u < width; u += 32) {
     const int c0 = col0 + u, cols = p.cols - c0;
     if (cols <= 0) break;
     uint32_t r[32];
     tmem_ld_32x32b_x32(taddr + u, r);
-    const int64_t at = bi * p.stride + (row0 + lane) * p.ld + c0;  // kGram, kPoly, X's copy
-    float v[32];
-    if (MODE == kUpdate) {
-      const float* x = p.x + bi * p.x_stride + (row0 + lane) * p.ldx + c0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in && 4 * i < cols) o = *reinterpret_cast<const float4*>(x + 4 * i);
-        v[4 * i] = o.x;
-        v[4 * i + 1] = o.y;
-        v[4 * i + 2] = o.z;
-        v[4 * i + 3] = o.w;
-      }
-    } else if (MODE == kPoly) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (in && 8 * i < cols) o = *reinterpret_cast<const uint4*>(p.gram + at + 8 * i);
-        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-          v[8 * i + 2 * k] = f.x;
-          v[8 * i + 2 * k + 1] = f.y;
-        }
-      }
-    }
+    const Addend<MODE> cur = add;
+    if (u + 32 < width) add.load(p, bi, row0 + lane, c0 + 32);
     tmem_ld_wait();
     // the accumulator holds 4096^2 times the product
+    float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float acc = __uint_as_float(r[i]);
       if (MODE == kGram)
         v[i] = acc * kUnhold;
       else if (MODE == kPoly)
-        v[i] = fmaf(p.c * kUnhold, acc, p.b * v[i]);
+        v[i] = fmaf(p.c * kUnhold, acc, p.b * cur.at(i));
       else
-        v[i] = fmaf(acc, kUnhold * kUnhold, p.a * v[i]);
+        v[i] = fmaf(acc, kUnhold * kUnhold, p.a * cur.at(i));
     }
     uint32_t w[16];
     if (MODE == kUpdate && p.result) {
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + kStages * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI_WARPS * kStagingBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStagingBytes);
   uint64_t* full = bars;                  // [kStages] (the even CTA's are the ones used)
   uint64_t* empty = bars + kStages;       // [kStages]
   uint64_t* acc_full = empty + kStages;   // [2]
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], EPI_WARPS * kCtas);
+      mbar_init(&acc_empty[b], kEpiWarps * kCtas);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -390,18 +397,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_wait();
     if (warp == 2 && lane == 0) grid_launch_dependents();
     const int q = warp & 3;
+    const int half = (warp - 2) >> 2;  // of the tile's columns
     uint8_t* buf_s = staging + (warp - 2) * kStagingBytes;
     uint32_t it = 0;
     for (int t = unit; t < total; t += units, ++it) {
       const uint32_t buf = it & 1, use = it >> 1;
-      if (!warp_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
-      tc_fence_after();
       const int bi = t / p.tiles;
       int mi, ni;
       tile_of(p, t - bi * p.tiles, mi, ni);
-      epilogue<MODE>(p, tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN, bi,
-                     (mi * kCtas + static_cast<int>(rank)) * 128 + 32 * q, ni * kN, kN,
-                     p.symmetric && mi != ni, buf_s);
+      const int row0 = (mi * kCtas + static_cast<int>(rank)) * 128 + 32 * q;
+      const int col0 = ni * kN + half * (kN / 2);
+      Addend<MODE> add;
+      add.load(p, bi, row0 + lane, col0);
+      if (!warp_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      epilogue<MODE>(p, add,
+                     tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + half * (kN / 2),
+                     bi, row0, col0, kN / 2, p.symmetric && mi != ni, buf_s);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------- norm and split
 constexpr int kNormThreads = 256;
-constexpr int kMaxParts = 256;  // partial sums of one matrix
+constexpr int kMaxParts = 256;  // partial sums of one matrix (kNormThreads at most)
 
 template <int ELT>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -500,15 +512,63 @@ struct SplitParams {
   int64_t ldx, ldh, x_stride, h_stride;
 };
 
-// X = G / (|G| + eps) in fp32 and, times 4096, in fp16; 64 x 64 blocks, which
-// TRANSPOSED turns around in shared memory.
+// 1 / (|G_b| + eps), from the partial sums.
+__device__ float inverse_norm(const SplitParams& p, int b) {
+  const float part =
+      threadIdx.x < p.n_parts ? p.parts[static_cast<int64_t>(b) * kMaxParts + threadIdx.x] : 0.f;
+  return 1.f / (sqrtf(cta_sum(part)) + p.eps);
+}
+
+// X = G / (|G| + eps) in fp32 and, times 4096, in fp16, for G with rows of
+// whole 16-byte vectors and rows <= cols: eight elements per thread at a time.
+template <int ELT>
+__global__ void __launch_bounds__(kNormThreads) ortho_split_rows(const SplitParams p) {
+  const int b = static_cast<int>(blockIdx.y);
+  const float inv = inverse_norm(p, b);
+  const uint8_t* g = static_cast<const uint8_t*>(p.g) + static_cast<int64_t>(b) * p.rows * p.cols * ELT;
+  const int64_t per_row = p.ldx / 8, n = p.rows * per_row;
+#pragma unroll 2
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kNormThreads) {
+    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+    float v[8] = {};
+    if (c < p.cols) {
+      const uint4* src = reinterpret_cast<const uint4*>(g + (r * p.cols + c) * ELT);
+      if (ELT == 4) {
+        const uint4 lo = __ldcs(src), hi = __ldcs(src + 1);
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+      } else {
+        const uint4 q = __ldcs(src);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] = __uint_as_float(w[k] << 16);
+          v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= inv;
+    float4* x = reinterpret_cast<float4*>(p.x + b * p.x_stride + r * p.ldx + c);
+    x[0] = make_float4(v[0], v[1], v[2], v[3]);
+    x[1] = make_float4(v[4], v[5], v[6], v[7]);
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = pack_half2(v[2 * k] * kHold, v[2 * k + 1] * kHold);
+    *reinterpret_cast<uint4*>(p.xh + b * p.h_stride + r * p.ldh + c) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+// The same for any G, in 64 x 64 blocks, which TRANSPOSED turns around in
+// shared memory.
 template <int ELT, bool TRANSPOSED>
 __global__ void __launch_bounds__(kNormThreads) ortho_split(const SplitParams p) {
   __shared__ float tile[TRANSPOSED ? 64 : 1][65];
   const int b = static_cast<int>(blockIdx.z);
-  float part = threadIdx.x < p.n_parts ? p.parts[static_cast<int64_t>(b) * kMaxParts + threadIdx.x]
-                                       : 0.f;
-  const float inv = 1.f / (sqrtf(cta_sum(part)) + p.eps);
+  const float inv = inverse_norm(p, b);
   const int64_t base = static_cast<int64_t>(b) * p.rows * p.cols;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
   float* x = p.x + b * p.x_stride;
@@ -681,15 +741,24 @@ int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
   FLCE_TRY(cudaGetLastError());
   const SplitParams sp{g,   rows, cols,  parts, l.parts,      eps,
                        x,   h[0], l.ldx, l.ldh, l.k * l.ldx,  l.k * l.ldh};
-  const dim3 sgrid(static_cast<unsigned>((cols + 63) / 64), static_cast<unsigned>((rows + 63) / 64),
-                   nb);
   const bool tr = rows > cols;
-  if (elt == 4)
-    tr ? ortho_split<4, true><<<sgrid, kNormThreads, 0, s>>>(sp)
-       : ortho_split<4, false><<<sgrid, kNormThreads, 0, s>>>(sp);
-  else
-    tr ? ortho_split<2, true><<<sgrid, kNormThreads, 0, s>>>(sp)
-       : ortho_split<2, false><<<sgrid, kNormThreads, 0, s>>>(sp);
+  if (!tr && aligned16(g) && cols % 8 == 0) {
+    const int64_t want = (l.k * (l.ldx / 8) + kNormThreads - 1) / kNormThreads, cap = 8 * sms;
+    const dim3 sgrid(static_cast<unsigned>(want < cap ? want : cap), nb);
+    if (elt == 4)
+      ortho_split_rows<4><<<sgrid, kNormThreads, 0, s>>>(sp);
+    else
+      ortho_split_rows<2><<<sgrid, kNormThreads, 0, s>>>(sp);
+  } else {
+    const dim3 sgrid(static_cast<unsigned>((cols + 63) / 64),
+                     static_cast<unsigned>((rows + 63) / 64), nb);
+    if (elt == 4)
+      tr ? ortho_split<4, true><<<sgrid, kNormThreads, 0, s>>>(sp)
+         : ortho_split<4, false><<<sgrid, kNormThreads, 0, s>>>(sp);
+    else
+      tr ? ortho_split<2, true><<<sgrid, kNormThreads, 0, s>>>(sp)
+         : ortho_split<2, false><<<sgrid, kNormThreads, 0, s>>>(sp);
+  }
   FLCE_TRY(cudaGetLastError());
   int rc;
   CUtensorMap mx[2], mxn[2], ma, mb;

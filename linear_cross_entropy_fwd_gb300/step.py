@@ -13,14 +13,26 @@ import ctypes
 
 import torch
 
-from . import (FlceAttn, _check, _check_out, _dtype_code, _is32, load_library, make_opts,
-               scale_convert)
+from . import (FLCE_FP32, FlceAttn, FlceOpts, _check, _check_out, _dtype_code, _is32,
+               load_library, make_opts, scale_convert)
+
+
+_defaults = None  # a flce_opts as flce_opts_init leaves it, with sync off
 
 
 def _call(fn, dev, dtype, args, *, sync, workspace, info, ids32=0):
     """Run C entry ``fn(*args, opts)`` on ``dev``'s current stream."""
-    o = make_opts(dtype, torch.cuda.current_stream(dev).cuda_stream, sync=1 if sync else 0,
-                  target_is_int32=ids32)
+    global _defaults
+    if _defaults is None:
+        _defaults = bytes(make_opts(sync=0))
+    o = FlceOpts.from_buffer_copy(_defaults)
+    if dtype is torch.float32:
+        o.dtype = FLCE_FP32
+    o.stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if sync:
+        o.sync = 1
+    if ids32:
+        o.target_is_int32 = 1
     if workspace is not None:
         _check_out(workspace, (workspace.numel(),), workspace.dtype, dev, "workspace")
         o.workspace = workspace.data_ptr()
@@ -35,7 +47,8 @@ def _call(fn, dev, dtype, args, *, sync, workspace, info, ids32=0):
     else:
         with torch.cuda.device(dev):
             st = fn(*args, ctypes.byref(o))
-    _check(st)
+    if st:
+        _check(st)
     if info is not None:
         info.update(status=status, workspace_bytes=used.value)
 
