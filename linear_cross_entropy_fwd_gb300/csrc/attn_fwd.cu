@@ -185,10 +185,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
         for (int i = 0; i < kTile; ++i) s[i] = i > row ? -INFINITY : s[i];
       }
-      float mx = s[0];
+      // independent chains: two warps per scheduler leave latency to hide
+      float mxs[8];
 #pragma unroll
-      for (int i = 1; i < kTile; ++i) mx = fmaxf(mx, s[i]);
-      mx *= c;
+      for (int i = 0; i < 8; ++i) mxs[i] = s[i];
+#pragma unroll
+      for (int i = 8; i < kTile; ++i) mxs[i & 7] = fmaxf(mxs[i & 7], s[i]);
+      const float mx = c * fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
+                                 fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
       if (j == 0) {
         m = mx;
       } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
@@ -207,20 +211,23 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           tmem_st_32x32b_x32(tO + lanes + 32 * q, o);
         }
       }
-      float sum = 0.f;
+      float2 sums[4] = {};
+      const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float a = fast_exp2(fmaf(s[32 * q + 2 * i], c, -m));
-          const float b = fast_exp2(fmaf(s[32 * q + 2 * i + 1], c, -m));
-          sum += a + b;
-          pk[i] = pack_bf16x2(a, b);
+          float2 e = fma2(make_float2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), c2, m2);
+          e.x = fast_exp2(e.x);
+          e.y = fast_exp2(e.y);
+          sums[i & 3] = add2(sums[i & 3], e);
+          pk[i] = pack_bf16x2(e.x, e.y);
         }
         tmem_st_32x32b_x16(tS + lanes + 16 * q, pk);
       }
-      l += sum;
+      const float2 sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+      l += sum.x + sum.y;
       tmem_st_wait();
       if (diag && valid < kTile) {
         const int gv = 2 * j + 1, sv = gv % kSlots;
