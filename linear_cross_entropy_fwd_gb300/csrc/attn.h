@@ -19,11 +19,11 @@ namespace flce {
 
 constexpr int kTile = 128;  // rows of a query tile and of a key tile
 
-// One tile of a sequence.
+// One unit of work of a sequence: `unit` consecutive tiles (AttnParams).
 struct AttnTile {
   int32_t start;  // first token of the sequence
   int32_t len;    // its length
-  int32_t tile;   // tokens [128 tile, 128 tile + 128) of the sequence
+  int32_t tile;   // index of the unit within the sequence
   int32_t pad;
 };
 
@@ -37,11 +37,12 @@ struct AttnParams {
   const int32_t* cu;    // [B + 1]
   int32_t B, T, Hq, Hkv, D;
   float scale;          // > 0
-  AttnTile* tiles;      // [max_tiles], most key tiles first
+  int32_t unit;         // tiles per unit: 2 forward, 1 backward
+  AttnTile* tiles;      // [max_tiles] units, highest index first
   int32_t* n_tiles;
   int32_t* bucket;      // [max_depth + 2] scratch of the plan
   int32_t max_tiles;    // an upper bound from B and T alone
-  int32_t max_depth;    // tiles of the longest possible sequence
+  int32_t max_depth;    // units of the longest possible sequence
   float* lse;           // [Hq][T]
   float* delta;         // [Hq][T]
   AttnOut o, dO, dq, dk, dv;
@@ -51,7 +52,7 @@ struct AttnParams {
 // Launchers.  Tensor maps: box 64 x 1 x 128 of [T, heads, D], 128-byte swizzle.
 cudaError_t launch_attn_plan(const AttnParams& p, bool backward, int sms, cudaStream_t s);
 cudaError_t launch_attn_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const AttnParams& p, cudaStream_t s);
+                            const AttnParams& p, int sms, cudaStream_t s);
 cudaError_t launch_attn_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                              const CUtensorMap& dO, const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,

@@ -57,8 +57,9 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
     return host_error(FLCE_ERR_ARG, "scale must be positive and finite");
   if (!a->cu_seqlens) return host_error(FLCE_ERR_ARG, "cu_seqlens is null");
   const int64_t T = a->T;
-  const int64_t max_tiles = T / kTile + a->batch;
-  if (max_tiles * a->heads_q >= (int64_t{1} << 31))
+  const int unit = backward ? 1 : 2;
+  const int64_t max_tiles = T / (kTile * unit) + a->batch;
+  if ((T / kTile + a->batch) * a->heads_q >= (int64_t{1} << 31))
     return host_error(FLCE_ERR_ARG, "(T / 128 + batch) * heads_q must be below 2^31");
   int rc = FLCE_OK;
   Operand q, k, v, oo, dO{}, dq{}, dk{}, dv{};
@@ -93,7 +94,8 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   p.D = D;
   p.scale = a->scale;
   p.max_tiles = static_cast<int32_t>(max_tiles);
-  p.max_depth = static_cast<int32_t>((T + kTile - 1) / kTile);
+  p.unit = unit;
+  p.max_depth = static_cast<int32_t>((T + kTile * unit - 1) / (kTile * unit));
   const size_t b_tiles = round256(static_cast<size_t>(max_tiles) * sizeof(AttnTile));
   const size_t b_bucket = round256((static_cast<size_t>(p.max_depth) + 2) * 4);
   const size_t b_delta =
@@ -121,7 +123,7 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
       if (e == cudaSuccess) e = launch_attn_dkdv(mq, mk, mv, mO, p, call.stream);
       if (e == cudaSuccess) e = launch_attn_dq(mq, mk, mv, mO, p, call.stream);
     } else if (e == cudaSuccess) {
-      e = launch_attn_fwd(mq, mk, mv, p, call.stream);
+      e = launch_attn_fwd(mq, mk, mv, p, sms, call.stream);
     }
   }
   if (e != cudaSuccess) rc = host_cuda_error(e, backward ? "flce_attn_bwd" : "flce_attn_fwd");

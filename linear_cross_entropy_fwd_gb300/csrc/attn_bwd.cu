@@ -54,40 +54,41 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* m, uint64_t* bar, u
                                           int head, int token) {
 #pragma unroll
   for (int b = 0; b < BOXES; ++b)
-    tma_load_3d(m, bar, dst + b * kBoxBytes, 64 * b, head, token);
+    tma_load_3d_elected(m, bar, smem_addr(dst) + b * kBoxBytes, 64 * b, head, token);
 }
 
 // D = A B^T over the head dimension, both tiles K-major in shared memory.
-__device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint32_t a, uint32_t b, int k_steps) {
+template <int DP>
+__device__ __forceinline__ void mma_over_d(uint32_t d_tmem, const Operand16& a, const Operand16& b,
+                                           int k_steps) {
   constexpr uint32_t kIdesc = make_idesc(1, false, false, kTile, kTile);
-  for (int k = 0; k < k_steps; ++k) {
+#pragma unroll
+  for (int k = 0; k < DP / 16; ++k) {
     const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
-    mma_f16(d_tmem, smem_desc_sw128(a + off, 0, 1024), smem_desc_sw128(b + off, 0, 1024), kIdesc,
-            k > 0);
+    if (k < k_steps) mma_f16_at(d_tmem, a, off, b, off, kIdesc, k > 0);
   }
 }
 
-// D (+)= A B over 128 rows of B, B a [128 rows, DP] tile in shared memory;
-// A in TMEM.
+// D (+)= A B over 128 rows of B, B a [128 rows, DP] tile in shared memory
+// (MN-major); A in TMEM.
 template <int DP>
-__device__ __forceinline__ void mma_over_rows_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
-                                                 bool add) {
+__device__ __forceinline__ void mma_over_rows_ts(uint32_t d_tmem, uint32_t a_tmem,
+                                                 const Operand16& b, bool add) {
   constexpr uint32_t kIdesc = make_idesc(1, false, true, kTile, DP);
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
-    mma_f16_ts(d_tmem, a_tmem + 8 * k, smem_desc_sw128(b + k * 2048, kBoxBytes, 1024), kIdesc,
-               (add || k > 0) ? 1u : 0u);
+    mma_f16_ts_at(d_tmem, a_tmem + 8 * k, b, k * 2048, kIdesc, (add || k > 0) ? 1u : 0u);
 }
 
 // The same with A a K-major [128, 128] tile in shared memory.
 template <int DP>
-__device__ __forceinline__ void mma_over_rows_ss(uint32_t d_tmem, uint32_t a, uint32_t b,
-                                                 bool add) {
+__device__ __forceinline__ void mma_over_rows_ss(uint32_t d_tmem, const Operand16& a,
+                                                 const Operand16& b, bool add) {
   constexpr uint32_t kIdesc = make_idesc(1, false, true, kTile, DP);
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
-    mma_f16(d_tmem, smem_desc_sw128(a + (k >> 2) * kBoxBytes + (k & 3) * 32, 0, 1024),
-            smem_desc_sw128(b + k * 2048, kBoxBytes, 1024), kIdesc, (add || k > 0) ? 1u : 0u);
+    mma_f16_at(d_tmem, a, (k >> 2) * kBoxBytes + (k & 3) * 32, b, k * 2048, kIdesc,
+               (add || k > 0) ? 1u : 0u);
 }
 
 // Rows [valid, 128) of a tile become zeros (the elementwise threads).
@@ -131,8 +132,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int idx = static_cast<int>(blockIdx.x / p.Hkv);
   grid_dependency_wait();  // the tile list and delta
   if (idx >= *p.n_tiles) return;
-  const AttnTile t = p.tiles[idx];
-  const int n_q = t.tile + 1;                           // query tiles that see this key tile
+  AttnTile t = p.tiles[idx];
+  t.start = uniform(t.start);
+  t.len = uniform(t.len);
+  const int n_q = uniform(t.tile) + 1;                           // query tiles that see this key tile
   const int kt = (t.len + kTile - 1) / kTile - n_q;     // this key tile
   const int group = p.Hq / p.Hkv;
   const int total = n_q * group;                        // (head, query tile) pairs
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 15; ++i) mbar_init(&bars[i], (i == 11 || i == 13) ? 8 : 1);
     *abort_flag = 0;
@@ -172,84 +175,84 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = *tmem_slot, tDP = tS + kTile, tDV = tDP + kTile, tDK = tDV + DP;
+  const uint32_t tS = uniform(*tmem_slot), tDP = tS + kTile, tDV = tDP + kTile, tDK = tDV + DP;
 
   if (warp == kTmaWarp) {
+    expect_tx_elected(kv_full, 2 * TB);
+    load_tile<S::kBoxes>(&tmK, kv_full, smK, kvh, t.start + kt * kTile);
+    load_tile<S::kBoxes>(&tmV, kv_full, smV, kvh, t.start + kt * kTile);
+    int n = 0;  // loads issued per ring: n of Q, n or n - 1 of dO
+    int n_o = 0;
+    for (int it = 0; it < total; ++it) {
+      const int s = it & 1;
+      const uint32_t par = ((it >> 1) & 1) ^ 1;
+      const int head = kvh * group + it / n_q;
+      const int tok = t.start + (kt + it % n_q) * kTile;
+      if (!uniform_wait(&q_empty[s], par, abort_flag, p.status)) break;
+      expect_tx_elected(&q_full[s], TB);
+      load_tile<S::kBoxes>(&tmQ, &q_full[s], smQ + s * TB, head, tok);
+      ++n;
+      if (!uniform_wait(&o_empty[s], par, abort_flag, p.status)) break;
+      expect_tx_elected(&o_full[s], TB);
+      load_tile<S::kBoxes>(&tmO, &o_full[s], smO + s * TB, head, tok);
+      ++n_o;
+    }
+    // every load has landed before this CTA's shared memory goes away
     if (lane == 0) {
-      mbar_arrive_expect_tx(kv_full, 2 * TB);
-      load_tile<S::kBoxes>(&tmK, kv_full, smK, kvh, t.start + kt * kTile);
-      load_tile<S::kBoxes>(&tmV, kv_full, smV, kvh, t.start + kt * kTile);
-      int n = 0;  // loads issued per ring: n of Q, n or n - 1 of dO
-      int n_o = 0;
-      for (int it = 0; it < total; ++it) {
-        const int s = it & 1;
-        const uint32_t par = ((it >> 1) & 1) ^ 1;
-        const int head = kvh * group + it / n_q;
-        const int tok = t.start + (kt + it % n_q) * kTile;
-        if (!mbar_wait(&q_empty[s], par, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(&q_full[s], TB);
-        load_tile<S::kBoxes>(&tmQ, &q_full[s], smQ + s * TB, head, tok);
-        ++n;
-        if (!mbar_wait(&o_empty[s], par, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(&o_full[s], TB);
-        load_tile<S::kBoxes>(&tmO, &o_full[s], smO + s * TB, head, tok);
-        ++n_o;
-      }
-      // every load has landed before this CTA's shared memory goes away
       mbar_wait_drain(kv_full, 0);
       for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait_drain(&q_full[i & 1], (i >> 1) & 1);
       for (int i = n_o > 2 ? n_o - 2 : 0; i < n_o; ++i)
         mbar_wait_drain(&o_full[i & 1], (i >> 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t aK = smem_addr(smK), aV = smem_addr(smV), aQ = smem_addr(smQ),
-                     aO = smem_addr(smO), aP = smem_addr(smP);
-      const int k_steps = (p.D + 15) / 16;  // columns past D are zeros
-      bool ok = mbar_wait(kv_full, 0, abort_flag, p.status) &&
-                mbar_wait(&q_full[0], 0, abort_flag, p.status);
-      if (ok) {
-        tc_fence_after();
-        mma_over_d(tS, aK, aQ, k_steps);
-        mma_commit(s_full);
-        ok = mbar_wait(&o_full[0], 0, abort_flag, p.status);
-      }
-      if (ok) {
-        tc_fence_after();
-        mma_over_d(tDP, aV, aO, k_steps);
-        mma_commit(dp_full);
-      }
-      for (int it = 0; ok && it < total; ++it) {
-        const int s = it & 1, s1 = s ^ 1;
-        const uint32_t par1 = ((it + 1) >> 1) & 1;
-        const bool more = it + 1 < total;
-        // P^T is in shared memory, and S^T has been read
-        if (!mbar_wait(p_full, it & 1, abort_flag, p.status)) break;
-        if (more) {
-          if (!mbar_wait(&q_full[s1], par1, abort_flag, p.status)) break;
-          tc_fence_after();
-          mma_over_d(tS, aK, aQ + s1 * TB, k_steps);
-          mma_commit(s_full);
-        }
-        tc_fence_after();
-        mma_over_rows_ss<DP>(tDV, aP, aO + s * TB, it > 0);
-        mma_commit(&o_empty[s]);
-        mma_commit(p_empty);
-        // dS^T is in TMEM, and dP^T has been read
-        if (!mbar_wait(ds_full, it & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        mma_over_rows_ts<DP>(tDK, tDP, aQ + s * TB, it > 0);
-        mma_commit(&q_empty[s]);
-        if (more) {
-          if (!mbar_wait(&o_full[s1], par1, abort_flag, p.status)) break;
-          tc_fence_after();
-          mma_over_d(tDP, aV, aO + s1 * TB, k_steps);
-          mma_commit(dp_full);
-        }
-      }
-      mma_commit(acc_full);  // all MMAs issued by this thread are done
-      mbar_wait_drain(acc_full, 0);
+    // operands over the head dimension, and (r..) over rows
+    const Operand16 aK(smem_addr(smK), 0), aV(smem_addr(smV), 0), aQ(smem_addr(smQ), 0),
+        aO(smem_addr(smO), 0), aP(smem_addr(smP), 0);
+    const Operand16 rQ(smem_addr(smQ), kBoxBytes), rO(smem_addr(smO), kBoxBytes);
+    const int k_steps = (p.D + 15) / 16;  // columns past D are zeros
+    bool ok = uniform_wait(kv_full, 0, abort_flag, p.status) &&
+              uniform_wait(&q_full[0], 0, abort_flag, p.status);
+    if (ok) {
+      tc_fence_after();
+      mma_over_d<DP>(tS, aK, aQ, k_steps);
+      commit_elected(s_full);
+      ok = uniform_wait(&o_full[0], 0, abort_flag, p.status);
     }
+    if (ok) {
+      tc_fence_after();
+      mma_over_d<DP>(tDP, aV, aO, k_steps);
+      commit_elected(dp_full);
+    }
+    for (int it = 0; ok && it < total; ++it) {
+      const int s = it & 1, s1 = s ^ 1;
+      const uint32_t par1 = ((it + 1) >> 1) & 1;
+      const bool more = it + 1 < total;
+      // P^T is in shared memory, and S^T has been read
+      if (!uniform_wait(p_full, it & 1, abort_flag, p.status)) break;
+      if (more) {
+        if (!uniform_wait(&q_full[s1], par1, abort_flag, p.status)) break;
+        tc_fence_after();
+        mma_over_d<DP>(tS, aK, moved(aQ, s1 * TB), k_steps);
+        commit_elected(s_full);
+      }
+      tc_fence_after();
+      mma_over_rows_ss<DP>(tDV, aP, moved(rO, s * TB), it > 0);
+      commit_elected(&o_empty[s]);
+      commit_elected(p_empty);
+      // dS^T is in TMEM, and dP^T has been read
+      if (!uniform_wait(ds_full, it & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      mma_over_rows_ts<DP>(tDK, tDP, moved(rQ, s * TB), it > 0);
+      commit_elected(&q_empty[s]);
+      if (more) {
+        if (!uniform_wait(&o_full[s1], par1, abort_flag, p.status)) break;
+        tc_fence_after();
+        mma_over_d<DP>(tDP, aV, moved(aO, s1 * TB), k_steps);
+        commit_elected(dp_full);
+      }
+    }
+    commit_elected(acc_full);  // all MMAs issued by this thread are done
+    if (lane == 0) mbar_wait_drain(acc_full, 0);
   } else {
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
@@ -390,7 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int h = static_cast<int>(blockIdx.x % p.Hq);
   const int idx = static_cast<int>(blockIdx.x / p.Hq);
   if (idx >= *p.n_tiles) return;
-  const AttnTile t = p.tiles[idx];
+  AttnTile t = p.tiles[idx];
+  t.start = uniform(t.start);
+  t.tile = uniform(t.tile);
   const int n_kv = t.tile + 1;
   const int kvh = h / (p.Hq / p.Hkv);
   const int q0 = t.tile * kTile;
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 15; ++i) mbar_init(&bars[i], (i == 12 || i == 13) ? 8 : 1);
     *abort_flag = 0;
@@ -426,26 +431,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = *tmem_slot, tDP = tS + 2 * kTile, tDQ = tDP + kTile;
+  const uint32_t tS = uniform(*tmem_slot), tDP = tS + 2 * kTile, tDQ = tDP + kTile;
 
   if (warp == kTmaWarp) {
+    expect_tx_elected(qo_full, 2 * TB);
+    load_tile<S::kBoxes>(&tmQ, qo_full, smQ, h, t.start + q0);
+    load_tile<S::kBoxes>(&tmO, qo_full, smO, h, t.start + q0);
+    int n_k = 0, n_v = 0;
+    for (int j = 0; j < n_kv; ++j) {
+      const int sk = j % 3, sv = j & 1;
+      const int tok = t.start + j * kTile;
+      if (!uniform_wait(&k_empty[sk], ((j / 3) & 1) ^ 1, abort_flag, p.status)) break;
+      expect_tx_elected(&k_full[sk], TB);
+      load_tile<S::kBoxes>(&tmK, &k_full[sk], smK + sk * TB, kvh, tok);
+      ++n_k;
+      if (!uniform_wait(&v_empty[sv], ((j >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+      expect_tx_elected(&v_full[sv], TB);
+      load_tile<S::kBoxes>(&tmV, &v_full[sv], smV + sv * TB, kvh, tok);
+      ++n_v;
+    }
     if (lane == 0) {
-      mbar_arrive_expect_tx(qo_full, 2 * TB);
-      load_tile<S::kBoxes>(&tmQ, qo_full, smQ, h, t.start + q0);
-      load_tile<S::kBoxes>(&tmO, qo_full, smO, h, t.start + q0);
-      int n_k = 0, n_v = 0;
-      for (int j = 0; j < n_kv; ++j) {
-        const int sk = j % 3, sv = j & 1;
-        const int tok = t.start + j * kTile;
-        if (!mbar_wait(&k_empty[sk], ((j / 3) & 1) ^ 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(&k_full[sk], TB);
-        load_tile<S::kBoxes>(&tmK, &k_full[sk], smK + sk * TB, kvh, tok);
-        ++n_k;
-        if (!mbar_wait(&v_empty[sv], ((j >> 1) & 1) ^ 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(&v_full[sv], TB);
-        load_tile<S::kBoxes>(&tmV, &v_full[sv], smV + sv * TB, kvh, tok);
-        ++n_v;
-      }
       mbar_wait_drain(qo_full, 0);
       for (int i = n_k > 3 ? n_k - 3 : 0; i < n_k; ++i)
         mbar_wait_drain(&k_full[i % 3], (i / 3) & 1);
@@ -453,38 +458,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t aQ = smem_addr(smQ), aO = smem_addr(smO), aK = smem_addr(smK),
-                     aV = smem_addr(smV);
-      const int k_steps = (p.D + 15) / 16;
-      auto issue_s = [&](int j) {
-        if (!mbar_wait(&k_full[j % 3], (j / 3) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        mma_over_d(tS + (j & 1) * kTile, aQ, aK + (j % 3) * TB, k_steps);
-        return true;
-      };
-      auto issue_dp = [&](int j) {
-        if (!mbar_wait(&v_full[j & 1], (j >> 1) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        mma_over_d(tDP, aO, aV + (j & 1) * TB, k_steps);
-        mma_commit(&v_empty[j & 1]);
-        mma_commit(sdp_full);  // S of this tile was issued earlier
-        return true;
-      };
-      bool ok = mbar_wait(qo_full, 0, abort_flag, p.status) && issue_s(0) && issue_dp(0) &&
-                (n_kv < 2 || issue_s(1));
-      for (int j = 0; ok && j < n_kv; ++j) {
-        if (!mbar_wait(dp_read, j & 1, abort_flag, p.status)) break;
-        if (j + 1 < n_kv && !issue_dp(j + 1)) break;
-        if (!mbar_wait(ds_full, j & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        mma_over_rows_ts<DP>(tDQ, tS + (j & 1) * kTile, aK + (j % 3) * TB, j > 0);
-        mma_commit(&k_empty[j % 3]);
-        if (j + 2 < n_kv && !issue_s(j + 2)) break;
-      }
-      mma_commit(acc_full);
-      mbar_wait_drain(acc_full, 0);
+    const Operand16 aQ(smem_addr(smQ), 0), aO(smem_addr(smO), 0), aK(smem_addr(smK), 0),
+        aV(smem_addr(smV), 0);
+    const Operand16 rK(smem_addr(smK), kBoxBytes);  // over rows
+    const int k_steps = (p.D + 15) / 16;
+    auto issue_s = [&](int j) {
+      if (!uniform_wait(&k_full[j % 3], (j / 3) & 1, abort_flag, p.status)) return false;
+      tc_fence_after();
+      mma_over_d<DP>(tS + (j & 1) * kTile, aQ, moved(aK, (j % 3) * TB), k_steps);
+      return true;
+    };
+    auto issue_dp = [&](int j) {
+      if (!uniform_wait(&v_full[j & 1], (j >> 1) & 1, abort_flag, p.status)) return false;
+      tc_fence_after();
+      mma_over_d<DP>(tDP, aO, moved(aV, (j & 1) * TB), k_steps);
+      commit_elected(&v_empty[j & 1]);
+      commit_elected(sdp_full);  // S of this tile was issued earlier
+      return true;
+    };
+    bool ok = uniform_wait(qo_full, 0, abort_flag, p.status) && issue_s(0) && issue_dp(0) &&
+              (n_kv < 2 || issue_s(1));
+    for (int j = 0; ok && j < n_kv; ++j) {
+      if (!uniform_wait(dp_read, j & 1, abort_flag, p.status)) break;
+      if (j + 1 < n_kv && !issue_dp(j + 1)) break;
+      if (!uniform_wait(ds_full, j & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      mma_over_rows_ts<DP>(tDQ, tS + (j & 1) * kTile, moved(rK, (j % 3) * TB), j > 0);
+      commit_elected(&k_empty[j % 3]);
+      if (j + 2 < n_kv && !issue_s(j + 2)) break;
     }
+    commit_elected(acc_full);
+    if (lane == 0) mbar_wait_drain(acc_full, 0);
   } else {
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;

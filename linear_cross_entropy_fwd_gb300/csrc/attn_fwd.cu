@@ -1,13 +1,21 @@
 // attn_fwd.cu -- forward pass of packed causal attention.
 //
-// One CTA per (query tile of 128 rows, query head); two CTAs per SM, so that
-// one CTA's MMAs run while the other's exponentials do.  For each key tile j:
+// A unit of work is 256 query rows (two tiles, A and B) of one query head.
+// For each key tile j and each of the two query tiles:
 //   MMA      S = Q K_j^T            into TMEM (128 fp32 columns)
-//   softmax  one thread per row: running maximum m and sum l, P = 2^(cS - m)
-//            as bf16 over S's own columns
+//   softmax  two threads per row, 64 columns each: running maximum m and sum
+//            l, P = 2^(cS - m) as bf16 over S's own columns
 //   MMA      O += P V_j             P from TMEM, V_j as it lies in memory
 // with c = scale log2(e).  Only the tile on the diagonal is masked, and it is
-// the last one.
+// a query tile's last one.
+//
+// One CTA per SM walks the units, deepest first.  The tensor cores work on one
+// tile while the other's exponentials are taken, and both tiles share one load
+// of K_j and V_j: the operands' way through shared memory (TMA in, MMA out) is
+// 256 KB per two tile products at 128 bytes a clock, just what the MMAs take.
+// Each tile has an MMA thread of its own (PV, next S, PV, ...): issuing an MMA
+// of 64 clocks takes about 75 beside the other warps, a commit or a wait 100 to
+// 200, so that one thread for both keeps the tensor cores half idle.
 //
 // The maximum that P and O are relative to follows the true one only when it
 // has grown by more than 2^8: until then O needs no rescaling, and P <= 2^8,
@@ -19,7 +27,11 @@
 // masked in S; the rows of V there (another sequence's, of any value) are
 // cleared in shared memory, since 0 * NaN would reach O.
 //
-// Roles (192 threads): warps 0-3 softmax and output, warp 4 TMA, warp 5 MMA.
+// Roles (640 threads): warps 0-7 softmax and output of tile A, 8-15 of tile B
+// (warp w: TMEM lanes 32 (w % 4) .., columns 64 ((w / 4) % 2) ..), warp 16 TMA,
+// warp 17 MMA.  The launch gives each thread 96 registers (640 x 96 = 61440);
+// the four softmax warpgroups go up to 104 and the last one down to 64
+// (512 x 104 + 128 x 64 = 61440).
 #include "attn.h"
 #include "host_util.h"
 #include "sm103_attn.cuh"
@@ -29,266 +41,383 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kFwdThreads = 192;
-constexpr float kRescale = 8.f;  // log2 of the growth that triggers a rescaling
+constexpr int kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kFwdThreads = 20 * 32;  // whole warpgroups
+constexpr int kGroupThreads = 256;  // softmax threads of one tile
+constexpr float kRescale = 8.f;     // log2 of the growth that triggers a rescaling
+constexpr uint32_t kTmemCols = 512;
 
 template <int DP>
 struct FwdShape {
   static constexpr int kBoxes = DP / 64;
   static constexpr uint32_t kBoxBytes = kTile * 128;             // 128 rows x 64 elements
   static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
-  // K and V tiles in flight; with the query tile this leaves room for two
-  // CTAs on an SM and no more (TMEM holds two)
-  static constexpr int kSlots = DP == 128 ? 2 : 4;
-  static constexpr uint32_t kSmem = 1024 + (1 + kSlots) * kTileBytes + 256;
+  static constexpr int kSlots = DP == 128 ? 4 : 8;               // K and V tiles in flight
+  static constexpr uint32_t kExchange = 4096;                    // row maxima and sums
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + kExchange + 256;
 };
 
-constexpr uint32_t kTmemCols = 256;  // S (128) and O (DP <= 128)
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The units of a CTA: rounds go through the list forwards and backwards in
+// turn, so that no CTA always gets the deeper one.
+struct Unit {
+  AttnTile t;
+  int head;
+  int n[2];  // key tiles of the two query tiles (n[1] = 0: one tile only)
+  __device__ __forceinline__ bool get(const AttnParams& p, int round, int total) {
+    const int g = static_cast<int>(gridDim.x);
+    const int b = static_cast<int>(blockIdx.x);
+    const int64_t u = static_cast<int64_t>(round) * g + (round & 1 ? g - 1 - b : b);
+    if (u >= total) return false;
+    const int i = static_cast<int>(u / p.Hq);
+    t = p.tiles[i];
+    head = static_cast<int>(u - static_cast<int64_t>(i) * p.Hq);
+    const int nt = (t.len + kTile - 1) / kTile;
+    n[0] = 2 * t.tile + 1;
+    n[1] = n[0] < nt ? n[0] + 1 : 0;
+    return true;
+  }
+  __device__ __forceinline__ bool get_uniform(const AttnParams& p, int round, int total) {
+    if (!get(p, round, total)) return false;
+    t.start = uniform(t.start);
+    t.tile = uniform(t.tile);
+    n[0] = uniform(n[0]);
+    n[1] = uniform(n[1]);
+    return true;
+  }
+  __device__ __forceinline__ int depth() const { return n[1] ? n[1] : n[0]; }
+};
 
 template <int DP>
-__global__ void __launch_bounds__(kFwdThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using S = FwdShape<DP>;
   constexpr int kSlots = S::kSlots;
-  const int h = static_cast<int>(blockIdx.x % p.Hq);
-  const int idx = static_cast<int>(blockIdx.x / p.Hq);
-  grid_dependency_wait();  // the tile list
-  if (idx >= *p.n_tiles) return;
-  const AttnTile t = p.tiles[idx];
-  const int n_kv = t.tile + 1;
-  const int kvh = h / (p.Hq / p.Hkv);
+  constexpr uint32_t TB = S::kTileBytes;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* smQ = smem;
-  uint8_t* smKV = smem + S::kTileBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smKV + kSlots * S::kTileBytes);
-  uint64_t* q_full = bars;
-  uint64_t* kv_full = bars + 1;               // [kSlots]
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* smQ = smem;                        // [2]
+  uint8_t* smKV = smem + 2 * TB;              // [kSlots]
+  float* exchange = reinterpret_cast<float*>(smKV + kSlots * TB);  // [tile][turn][half][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smKV + kSlots * TB + S::kExchange);
+  uint64_t* kv_full = bars;                   // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;      // [kSlots]
-  uint64_t* s_full = kv_empty + kSlots;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* o_full = p_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  uint64_t* q_full = kv_empty + kSlots;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;             // [2] per tile, from here on
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* o_empty = o_full + 2;
+  uint64_t* drain = o_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);  // both query tiles are done with it
     }
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
-    mbar_init(o_full, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 8);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&o_empty[x], 8);
+      mbar_init(&drain[x], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = *tmem_slot, tO = tS + kTile;
-  const int q0 = t.tile * kTile;
+  const uint32_t tmem = uniform(*tmem_slot);  // S_A, S_B, O_A, O_B
+  grid_dependency_wait();            // the tile list
+  const int total = uniform(*p.n_tiles) * p.Hq;
+  Unit w;
 
-  if (warp == 4) {
-    // ------------------------------------------------------------- TMA
-    if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, S::kTileBytes);
-#pragma unroll
-      for (int b = 0; b < S::kBoxes; ++b)
-        tma_load_3d(&tmQ, q_full, smQ + b * S::kBoxBytes, 64 * b, h, t.start + q0);
-      int g = 0;
+  if (warp >= kTmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------------- TMA
+      int g = 0, n_q = 0;
       bool ok = true;
-      for (int j = 0; ok && j < n_kv; ++j) {
-        for (int w = 0; w < 2; ++w, ++g) {  // K_j, then V_j
-          const int s = g % kSlots;
-          if (!mbar_wait(&kv_empty[s], ((g / kSlots) & 1) ^ 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&kv_full[s], S::kTileBytes);
+      const uint32_t q_dst = smem_addr(smQ), kv_dst = smem_addr(smKV);
+      for (int round = 0; ok && w.get_uniform(p, round, total); ++round) {
+        const int kvh = uniform(w.head / (p.Hq / p.Hkv));
+        if (!uniform_wait(q_empty, (round & 1) ^ 1, abort_flag, p.status)) break;
+        const int tiles = w.n[1] ? 2 : 1;
+        expect_tx_elected(q_full, tiles * TB);
+        for (int x = 0; x < tiles; ++x)
 #pragma unroll
           for (int b = 0; b < S::kBoxes; ++b)
-            tma_load_3d(w ? &tmV : &tmK, &kv_full[s], smKV + s * S::kTileBytes + b * S::kBoxBytes,
-                        64 * b, kvh, t.start + j * kTile);
+            tma_load_3d_elected(&tmQ, q_full, q_dst + x * TB + b * S::kBoxBytes, 64 * b, w.head,
+                                w.t.start + (2 * w.t.tile + x) * kTile);
+        ++n_q;
+        const int depth = w.depth();
+        for (int j = 0; ok && j < depth; ++j) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {  // K_j, then V_j
+            const int s = g % kSlots;
+            ok = ok && uniform_wait(&kv_empty[s], ((g / kSlots) & 1) ^ 1, abort_flag, p.status);
+            if (ok) {
+              expect_tx_elected(&kv_full[s], TB);
+#pragma unroll
+              for (int b = 0; b < S::kBoxes; ++b)
+                tma_load_3d_elected(v ? &tmV : &tmK, &kv_full[s],
+                                    kv_dst + s * TB + b * S::kBoxBytes, 64 * b, kvh,
+                                    w.t.start + j * kTile);
+              ++g;
+            }
+          }
         }
       }
       // every load has landed before this CTA's shared memory goes away
-      mbar_wait_drain(q_full, 0);
-      for (int i = g > kSlots ? g - kSlots : 0; i < g; ++i)
-        mbar_wait_drain(&kv_full[i % kSlots], (i / kSlots) & 1);
+      if (lane == 0) {
+        if (n_q > 0) mbar_wait_drain(q_full, (n_q - 1) & 1);
+        for (int i = g > kSlots ? g - kSlots : 0; i < g; ++i)
+          mbar_wait_drain(&kv_full[i % kSlots], (i / kSlots) & 1);
+      }
     }
-  } else if (warp == 5) {
-    // ------------------------------------------------------------- MMA
-    if (lane == 0) {
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ------------------------------------------------------------- MMA
+      const int x = warp - kMmaWarp;  // query tile
       constexpr uint32_t kIdescS = make_idesc(1, false, false, kTile, kTile);
       constexpr uint32_t kIdescO = make_idesc(1, false, true, kTile, DP);
-      const uint32_t q_addr = smem_addr(smQ), kv_addr = smem_addr(smKV);
+      const Operand16 q_op(smem_addr(smQ + x * TB), 0), k_op(smem_addr(smKV), 0),
+          v_op(smem_addr(smKV), S::kBoxBytes);
+      const uint32_t tS = tmem + x * kTile, tO = tmem + 2 * kTile + x * DP;
       const int k_steps = (p.D + 15) / 16;  // columns past D are zeros
-      bool ok = mbar_wait(q_full, 0, abort_flag, p.status);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int gk = 2 * j, gv = gk + 1;
-        const int sk = gk % kSlots, sv = gv % kSlots;
-        if (!mbar_wait(&kv_full[sk], (gk / kSlots) & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t k_addr = kv_addr + sk * S::kTileBytes;
-        for (int k = 0; k < k_steps; ++k) {
-          const uint32_t off = (k >> 2) * S::kBoxBytes + (k & 3) * 32;
-          mma_f16(tS, smem_desc_sw128(q_addr + off, 0, 1024),
-                  smem_desc_sw128(k_addr + off, 0, 1024), kIdescS, k > 0);
+      int g = 0;                            // K and V tiles so far
+      int n_p = 0, n_u = 0;                 // products P V, and units, of this tile so far
+      auto wait_kv = [&](int i) {
+        return uniform_wait(&kv_full[i % kSlots], (i / kSlots) & 1, abort_flag, p.status);
+      };
+      // K tile i -> S; or nothing, if this query tile does not see it.  Either
+      // way the slot is released, and after the unit's last S the query tile.
+      auto scores = [&](int i, bool use, bool last) {
+        if (!wait_kv(i)) return false;
+        const int slot = i % kSlots;
+        if (!use) {
+          arrive_elected(&kv_empty[slot]);
+          return true;
         }
-        mma_commit(&kv_empty[sk]);
-        mma_commit(s_full);
-        if (!mbar_wait(&kv_full[sv], (gv / kSlots) & 1, abort_flag, p.status)) break;
-        if (!mbar_wait(p_full, j & 1, abort_flag, p.status)) break;
         tc_fence_after();
-        const uint32_t v_addr = kv_addr + sv * S::kTileBytes;
+        const Operand16 k = moved(k_op, slot * TB);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_f16_ts(tO, tS + 8 * k, smem_desc_sw128(v_addr + k * 2048, S::kBoxBytes, 1024),
-                     kIdescO, (j > 0 || k > 0) ? 1u : 0u);
-        mma_commit(&kv_empty[sv]);
+        for (int e = 0; e < DP / 16; ++e) {
+          const uint32_t off = (e >> 2) * S::kBoxBytes + (e & 3) * 32;
+          if (e < k_steps) mma_f16_at(tS, q_op, off, k, off, kIdescS, e > 0);
+        }
+        commit_elected(&s_full[x]);
+        commit_elected(&kv_empty[slot]);
+        if (last) commit_elected(q_empty);
+        return true;
+      };
+      bool ok = true;
+      for (int round = 0; ok && w.get_uniform(p, round, total); ++round) {
+        const int n = w.n[x], depth = w.depth();
+        ok = uniform_wait(q_full, round & 1, abort_flag, p.status);
+        if (ok && n == 0) arrive_elected(q_empty);
+        ok = ok && scores(g, n > 0, n == 1);
+        for (int j = 0; ok && j < depth; ++j) {
+          const int i = g + 2 * j + 1, slot = i % kSlots;
+          if (!(ok = wait_kv(i))) break;
+          if (j < n) {
+            ok = (j > 0 || uniform_wait(&o_empty[x], (n_u & 1) ^ 1, abort_flag, p.status)) &&
+                 uniform_wait(&p_full[x], n_p & 1, abort_flag, p.status);
+            if (!ok) break;
+            ++n_p;
+            tc_fence_after();
+            const Operand16 v = moved(v_op, slot * TB);
+#pragma unroll
+            for (int e = 0; e < kTile / 16; ++e)
+              mma_f16_ts_at(tO, tS + 8 * e, v, e * 2048, kIdescO, (j > 0 || e > 0) ? 1u : 0u);
+            commit_elected(&kv_empty[slot]);
+            if (j == n - 1) commit_elected(&o_full[x]);
+          } else {
+            arrive_elected(&kv_empty[slot]);
+          }
+          if (j + 1 < depth) ok = scores(i + 1, j + 1 < n, j + 2 == n);
+        }
+        g += 2 * depth;
+        if (n > 0) ++n_u;
       }
-      mma_commit(o_full);  // all MMAs issued by this thread are done
-      mbar_wait_drain(o_full, 0);
+      commit_elected(&drain[x]);  // all MMAs issued by this thread are done
+      if (lane == 0) mbar_wait_drain(&drain[x], 0);
     }
   } else {
-    // --------------------------------------------------- softmax, output
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-    const int row = 32 * warp + lane;
-    const int valid = t.len - q0 < kTile ? t.len - q0 : kTile;  // rows of the query tile
+    // ----------------------------------------------------- softmax, output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int x = warp >> 3;                                  // query tile
+    const int quarter = warp & 3, half = (warp >> 2) & 1;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t tS = tmem + x * kTile + lanes, tO = tmem + 2 * kTile + x * DP + lanes;
+    const int row = 32 * quarter + lane;
     const float c = p.scale * kLog2e;
-    float m = -INFINITY, l = 0.f;
+    float* ex = exchange + x * 512;
+    // After a wait has expired the loops go on without results, so that the two
+    // warps of a row still meet at their barrier; later waits then return at once.
     bool ok = true;
-    for (int j = 0; j < n_kv; ++j) {
-      if (!warp_wait(s_full, j & 1, abort_flag, p.status)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const bool diag = j == n_kv - 1;
-      float s[kTile];
+    int n_s = 0;  // score tiles so far
+    int n_x = 0;  // exchanges between the halves so far
+    int J = 0;    // key tiles before this unit
+    int n_u = 0;  // units of this tile so far
+    for (int round = 0; w.get(p, round, total); J += w.depth(), ++round) {
+      const int n = w.n[x];
+      if (n == 0) continue;
+      const int q0 = (2 * w.t.tile + x) * kTile;
+      const int valid = w.t.len - q0 < kTile ? w.t.len - q0 : kTile;  // rows of this tile
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++n_s, ++n_x) {
+        ok = warp_wait(&s_full[x], n_s & 1, abort_flag, p.status) && ok;
+        tc_fence_after();
+        const bool diag = j == n - 1;
+        float s[64];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        tmem_ld_32x32b_x32(tS + lanes + 32 * q,
-                           reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
-      tmem_ld_wait();
-      if (diag) {
+        for (int q = 0; q < 2; ++q)
+          tmem_ld_32x32b_x32(tS + 64 * half + 32 * q,
+                             reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
+        tmem_ld_wait();
+        if (diag) {
+          const int lim = row - 64 * half;
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) s[i] = i > row ? -INFINITY : s[i];
-      }
-      // independent chains: two warps per scheduler leave latency to hide
-      float mxs[8];
+          for (int i = 0; i < 64; ++i) s[i] = i > lim ? -INFINITY : s[i];
+        }
+        // independent chains: few warps per scheduler leave latency to hide
+        float mxs[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mxs[i] = s[i];
+        for (int i = 0; i < 8; ++i) mxs[i] = s[i];
 #pragma unroll
-      for (int i = 8; i < kTile; ++i) mxs[i & 7] = fmaxf(mxs[i & 7], s[i]);
-      const float mx = c * fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
-                                 fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
-      if (j == 0) {
-        m = mx;
-      } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
-        // S_j complete means every MMA issued before it is: O is at rest
-        const float mn = fmaxf(m, mx);
-        const float f = fast_exp2(m - mn);
-        m = mn;
-        l *= f;
+        for (int i = 8; i < 64; ++i) mxs[i & 7] = fmaxf(mxs[i & 7], s[i]);
+        float mx = fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
+                         fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
+        // the other half's maximum; P goes over columns of S that it has read
+        float* turn = ex + (n_x & 1) * 256;
+        turn[half * kTile + row] = mx;
+        tc_fence_before();
+        named_barrier(1 + 4 * x + quarter, 64);
+        tc_fence_after();
+        mx = c * fmaxf(mx, turn[(half ^ 1) * kTile + row]);
+        if (j == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
+          // S_j complete means every MMA issued before it is: O is at rest
+          const float mn = fmaxf(m, mx);
+          const float f = fast_exp2(m - mn);
+          m = mn;
+          l *= f;
 #pragma unroll 1
-        for (int q = 0; q < DP / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tO + lanes + 32 * q, o);
-          tmem_ld_wait();
+          for (int q = 0; q < DP / 64; ++q) {
+            uint32_t o[32];
+            const uint32_t at = tO + half * (DP / 2) + 32 * q;
+            tmem_ld_32x32b_x32(at, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st_32x32b_x32(tO + lanes + 32 * q, o);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_32x32b_x32(at, o);
+          }
         }
-      }
-      float2 sums[4] = {};
-      const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+        float2 sums[4] = {};
+        const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t pk[16];
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 e = fma2(make_float2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), c2, m2);
-          e.x = fast_exp2(e.x);
-          e.y = fast_exp2(e.y);
-          sums[i & 3] = add2(sums[i & 3], e);
-          pk[i] = pack_bf16x2(e.x, e.y);
+          for (int i = 0; i < 16; ++i) {
+            float2 e = fma2(make_float2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), c2, m2);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sums[i & 3] = add2(sums[i & 3], e);
+            pk[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st_32x32b_x16(tS + 32 * half + 16 * q, pk);
         }
-        tmem_st_32x32b_x16(tS + lanes + 16 * q, pk);
+        const float2 sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+        l += sum.x + sum.y;
+        if (diag && valid < kTile) {
+          const int g = 2 * (J + j) + 1, sv = g % kSlots;
+          ok = warp_wait(&kv_full[sv], (g / kSlots) & 1, abort_flag, p.status) && ok;
+          const int per = (kTile - valid) * 8;
+          for (int i = threadIdx.x & (kGroupThreads - 1); i < per * S::kBoxes; i += kGroupThreads)
+            st_shared_v4(smem_addr(smKV) + sv * TB + (i / per) * S::kBoxBytes + valid * 128 +
+                             (i % per) * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      const float2 sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
-      l += sum.x + sum.y;
-      tmem_st_wait();
-      if (diag && valid < kTile) {
-        const int gv = 2 * j + 1, sv = gv % kSlots;
-        if (!warp_wait(&kv_full[sv], (gv / kSlots) & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        uint8_t* v = smKV + sv * S::kTileBytes;
-        for (int i = threadIdx.x; i < (kTile - valid) * 8 * S::kBoxes; i += kTile) {
-          const int b = i / ((kTile - valid) * 8), r = i % ((kTile - valid) * 8);
-          st_shared_v4(smem_addr(v) + b * S::kBoxBytes + valid * 128 + r * 16, 0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-    }
-    if (ok && warp_wait(o_full, 0, abort_flag, p.status)) {
+      // both halves' sums; this turn's slots were last read a tile ago
+      float* turn = ex + (n_x & 1) * 256;
+      turn[half * kTile + row] = l;
+      named_barrier(1 + 4 * x + quarter, 64);
+      l += turn[(half ^ 1) * kTile + row];
+      ++n_x;
+      ok = warp_wait(&o_full[x], n_u & 1, abort_flag, p.status) && ok;
+      ++n_u;
       tc_fence_after();
       const float inv = 1.f / l;
-      const int64_t tok = static_cast<int64_t>(t.start) + q0 + row;
-      uint16_t* out = static_cast<uint16_t*>(p.o.p) + tok * p.o.token + h * p.o.head;
+      const int64_t tok = static_cast<int64_t>(w.t.start) + q0 + row;
+      uint16_t* out = static_cast<uint16_t*>(p.o.p) + tok * p.o.token + w.head * p.o.head;
+      const bool in = ok && row < valid;
 #pragma unroll
-      for (int q = 0; q < DP / 32; ++q) {
+      for (int q = 0; q < DP / 64; ++q) {
         uint32_t o[32];
-        tmem_ld_32x32b_x32(tO + lanes + 32 * q, o);
+        tmem_ld_32x32b_x32(tO + half * (DP / 2) + 32 * q, o);
         tmem_ld_wait();
+        if (q == DP / 64 - 1) {  // O may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_empty[x]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t w[4];
+          uint32_t v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
+            v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
                                __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-          const int d = 32 * q + 8 * i;
-          if (row < valid && d < p.D)
-            *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          const int d = half * (DP / 2) + 32 * q + 8 * i;
+          if (in && d < p.D)
+            *reinterpret_cast<uint4*>(out + d) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
-      if (row < valid) p.lse[static_cast<int64_t>(h) * p.T + tok] = (m + fast_log2(l)) * kLn2;
+      if (in && half == 0)
+        p.lse[static_cast<int64_t>(w.head) * p.T + tok] = (m + fast_log2(l)) * kLn2;
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tS, kTmemCols);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
 template <int DP>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                     const AttnParams& p, cudaStream_t s) {
+                     const AttnParams& p, int sms, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(FwdShape<DP>::kSmem));
   if (e != cudaSuccess) return e;
+  const int64_t most = static_cast<int64_t>(p.max_tiles) * p.Hq;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hq));
+  cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
   cfg.blockDim = dim3(kFwdThreads);
   cfg.dynamicSmemBytes = FwdShape<DP>::kSmem;
   cfg.stream = s;
@@ -302,8 +431,8 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
 }  // namespace
 
 cudaError_t launch_attn_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const AttnParams& p, cudaStream_t s) {
-  return p.D <= 64 ? launch_t<64>(q, k, v, p, s) : launch_t<128>(q, k, v, p, s);
+                            const AttnParams& p, int sms, cudaStream_t s) {
+  return p.D <= 64 ? launch_t<64>(q, k, v, p, sms, s) : launch_t<128>(q, k, v, p, sms, s);
 }
 
 }  // namespace flce

@@ -23,9 +23,9 @@ __device__ bool offsets_ok(const AttnParams& p) {
   return __syncthreads_or(bad) == 0;
 }
 
-// A sequence of nt tiles has one tile of each depth 1 .. nt (the number of
-// tiles it meets); entry.tile is depth - 1.  Counting sort, deepest first;
-// tiles of one depth come in any order.
+// The units of a sequence meet the more tiles the higher their index (a key
+// tile's, counted from the sequence's end).  Counting sort by that index, the
+// highest first; units of one index come in any order.
 __device__ void make_tiles(const AttnParams& p, bool ok) {
   __shared__ int32_t s_bucket[kSharedDepth];
   __shared__ int32_t s_warp[kThreads / 32];
@@ -35,15 +35,16 @@ __device__ void make_tiles(const AttnParams& p, bool ok) {
     if (threadIdx.x == 0) *p.n_tiles = 0;
     return;
   }
+  const int unit = kTile * p.unit;  // tokens
   int32_t* bucket = p.max_depth < kSharedDepth ? s_bucket : p.bucket;
   for (int k = threadIdx.x; k <= p.max_depth; k += kThreads) bucket[k] = 0;
   __syncthreads();
   for (int b = warp; b < p.B; b += kThreads / 32) {
-    const int nt = (p.cu[b + 1] - p.cu[b] + kTile - 1) / kTile;
+    const int nt = (p.cu[b + 1] - p.cu[b] + unit - 1) / unit;
     for (int i = lane; i < nt; i += 32) atomicAdd(&bucket[i], 1);
   }
   __syncthreads();
-  // bucket[k] = number of tiles deeper than k + 1
+  // bucket[k] = number of units of a higher index
   int32_t above = 0;
   for (int top = p.max_depth; top >= 0; top -= kThreads) {
     const int k = top - static_cast<int>(threadIdx.x);
@@ -67,7 +68,7 @@ __device__ void make_tiles(const AttnParams& p, bool ok) {
   }
   for (int b = warp; b < p.B; b += kThreads / 32) {
     const int c0 = p.cu[b], len = p.cu[b + 1] - c0;
-    const int nt = (len + kTile - 1) / kTile;
+    const int nt = (len + unit - 1) / unit;
     for (int i = lane; i < nt; i += 32) {
       const int at = atomicAdd(&bucket[i], 1);
       p.tiles[at] = AttnTile{c0, len, i, 0};

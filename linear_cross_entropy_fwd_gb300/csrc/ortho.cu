@@ -63,15 +63,6 @@ struct OrthoParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cluster,
-                                                 void* dst, int32_t x, int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
-      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // Tile t of one matrix.
 __device__ __forceinline__ void tile_of(const OrthoParams& p, int t, int& mi, int& ni) {
   if (p.symmetric) {
@@ -262,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? uniform(cluster_ctarank()) : 0u;
   const int unit = static_cast<int>(blockIdx.x) / kCtas;
   const int units = static_cast<int>(gridDim.x) / kCtas;
   const int total = p.tiles * p.batch;
@@ -294,103 +285,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (PAIR) cluster_sync();  // the peer's barriers exist before any remote signal
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = uniform(*tmem_slot);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      uint32_t gk = 0;
-      bool ok = true;
-      grid_dependency_wait();
-      for (int t = unit; ok && t < total; t += units) {
-        const int bi = t / p.tiles;
-        int mi, ni;
-        tile_of(p, t - bi * p.tiles, mi, ni);
-        const int a_row = (mi * kCtas + static_cast<int>(rank)) * 128;
-        const int b_row = ni * kN + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < p.k_blk; ++kb, ++gk) {
-          const uint32_t s = gk % kStages, r = gk / kStages;
-          if (!mbar_wait(&empty[s], (r & 1) ^ 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], kCtas * kStageBytes);
-          uint8_t* a_dst = smem + s * kStageBytes;
-          uint8_t* b_dst = a_dst + kHalfStage;
-          const uint32_t fb = PAIR ? mapa_shared(smem_addr(&full[s]), 0) : smem_addr(&full[s]);
-          if (PAIR) {
-            tma_load_3d_pair(&tmA, fb, a_dst, 64 * kb, a_row, bi);
-            if (B_MN) {
-              tma_load_3d_pair(&tmB, fb, b_dst, b_row, 64 * kb, bi);
-              tma_load_3d_pair(&tmB, fb, b_dst + kBox, b_row + 64, 64 * kb, bi);
-            } else {
-              tma_load_3d_pair(&tmB, fb, b_dst, 64 * kb, b_row, bi);
-            }
+    uint32_t stage = 0, phase = 1;  // parity of `empty` that a first use finds complete
+    uint32_t loads = 0;
+    bool ok = true;
+    const uint32_t base = smem_addr(smem);
+    // the even CTA's barrier, as a cluster address
+    const uint32_t full0 = PAIR ? uniform(mapa_shared(smem_addr(full), 0)) : 0u;
+    grid_dependency_wait();
+    for (int t = unit; ok && t < total; t += units) {
+      const int bi = t / p.tiles;
+      int mi, ni;
+      tile_of(p, t - bi * p.tiles, mi, ni);
+      const int a_row = uniform((mi * kCtas + static_cast<int>(rank)) * 128);
+      const int b_row = uniform(ni * kN + static_cast<int>(rank) * 128);
+      for (int kb = 0; kb < p.k_blk; ++kb) {
+        if (!(ok = uniform_wait(&empty[stage], phase, abort_flag, p.status))) break;
+        if (rank == 0) expect_tx_elected(&full[stage], kCtas * kStageBytes);
+        const uint32_t a_dst = base + stage * kStageBytes, b_dst = a_dst + kHalfStage;
+        const int k = 64 * kb;
+        if (PAIR) {
+          const uint32_t fb = full0 + stage * 8;
+          tma_load_3d_pair_elected(&tmA, fb, a_dst, k, a_row, bi);
+          if (B_MN) {
+            tma_load_3d_pair_elected(&tmB, fb, b_dst, b_row, k, bi);
+            tma_load_3d_pair_elected(&tmB, fb, b_dst + kBox, b_row + 64, k, bi);
           } else {
-            tma_load_3d(&tmA, &full[s], a_dst, 64 * kb, a_row, bi);
-            if (B_MN) {
-              tma_load_3d(&tmB, &full[s], b_dst, b_row, 64 * kb, bi);
-              tma_load_3d(&tmB, &full[s], b_dst + kBox, b_row + 64, 64 * kb, bi);
-            } else {
-              tma_load_3d(&tmB, &full[s], b_dst, 64 * kb, b_row, bi);
-            }
+            tma_load_3d_pair_elected(&tmB, fb, b_dst, k, b_row, bi);
+          }
+        } else {
+          tma_load_3d_elected(&tmA, &full[stage], a_dst, k, a_row, bi);
+          if (B_MN) {
+            tma_load_3d_elected(&tmB, &full[stage], b_dst, b_row, k, bi);
+            tma_load_3d_elected(&tmB, &full[stage], b_dst + kBox, b_row + 64, k, bi);
+          } else {
+            tma_load_3d_elected(&tmB, &full[stage], b_dst, k, b_row, bi);
           }
         }
+        ++loads;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      // every stage this thread loaded has landed (the odd CTA's loads land on
-      // the even CTA's barrier: it waits until the MMAs released them)
-      const uint32_t n_drain = gk < kStages ? gk : kStages;
+    }
+    // every stage this warp loaded has landed (the odd CTA's loads land on the
+    // even CTA's barrier: it waits until the MMAs released them)
+    if (lane == 0) {
+      const uint32_t n_drain = loads < kStages ? loads : kStages;
       for (uint32_t i = 0; i < n_drain; ++i) {
-        const uint32_t q = gk - 1 - i;
+        const uint32_t q = loads - 1 - i;
         mbar_wait_drain(rank == 0 ? &full[q % kStages] : &empty[q % kStages], (q / kStages) & 1);
       }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0 && rank == 0) {
-      uint32_t gk = 0, it = 0;
+    if (rank == 0) {
+      uint32_t stage = 0, phase = 0, it = 0;
       bool ok = true;
-      const uint32_t base = smem_addr(smem);
+      const Operand16 a_op(smem_addr(smem), 0), b_op(smem_addr(smem) + kHalfStage, B_MN ? kBox : 0);
       for (int t = unit; ok && t < total; t += units, ++it) {
         const uint32_t buf = it & 1, use = it >> 1;
-        if (!mbar_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.status)) break;
+        if (!uniform_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.status)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kN;
-        for (int kb = 0; kb < p.k_blk; ++kb, ++gk) {
-          const uint32_t s = gk % kStages, r = gk / kStages;
-          if (!mbar_wait(&full[s], r & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = base + s * kStageBytes, b = a + kHalfStage;
+        for (int kb = 0; kb < p.k_blk; ++kb) {
+          if (!(ok = uniform_wait(&full[stage], phase, abort_flag, p.status))) break;
+          const Operand16 a = moved(a_op, stage * kStageBytes), b = moved(b_op, stage * kStageBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint64_t ad = smem_desc_sw128(a + 32 * k, 0, 1024);
-            const uint64_t bd = B_MN ? smem_desc_sw128(b + 2048 * k, kBox, 1024)
-                                     : smem_desc_sw128(b + 32 * k, 0, 1024);
             const uint32_t add = (kb > 0 || k > 0) ? 1u : 0u;
+            const uint32_t b_off = B_MN ? 2048 * k : 32 * k;
             if (PAIR)
-              mma_f16_pair(d, ad, bd, kIdesc, add);
+              mma_f16_pair_at(d, a, 32 * k, b, b_off, kIdesc, add);
             else
-              mma_f16(d, ad, bd, kIdesc, add);
+              mma_f16_at(d, a, 32 * k, b, b_off, kIdesc, add);
           }
           if (PAIR)
-            mma_commit_pair_mc(&empty[s], 0x3);
+            commit_pair_elected(&empty[stage], 0x3);
           else
-            mma_commit(&empty[s]);
+            commit_elected(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
         if (!ok) break;
         if (PAIR)
-          mma_commit_pair_mc(&acc_full[buf], 0x3);
+          commit_pair_elected(&acc_full[buf], 0x3);
         else
-          mma_commit(&acc_full[buf]);
+          commit_elected(&acc_full[buf]);
       }
       if (PAIR)
-        mma_commit_pair(drain);
+        commit_pair_elected(drain, 0x1);
       else
-        mma_commit(drain);
-      mbar_wait_drain(drain, 0);
+        commit_elected(drain);
+      if (lane == 0) mbar_wait_drain(drain, 0);
     }
   } else {
     // ------------------------------------------------------------ epilogue

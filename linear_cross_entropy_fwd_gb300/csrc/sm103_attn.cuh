@@ -6,25 +6,151 @@
 
 namespace flce {
 
-// 3D tiled load global -> shared; completion counted in bytes on `bar`.
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
-                                            int32_t x, int32_t y, int32_t z) {
+// ------------------------------------------- issue by a converged warp
+// The MMA and TMA warps run their loops with all 32 lanes and let one elected
+// lane issue: what they compute then stays in uniform registers, where these
+// instructions take their operands from.  Issued from a branch that one lane
+// takes, four 64-clock MMAs with their wait and commit took 565 clocks, by a
+// converged warp 367 (eight: 774 and 592).
+
+// The same value in every lane, known to be so.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// mbar_wait by a converged warp; the same answer in every lane.
+__device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity,
+                                             volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+}
+
+// An operand tile in shared memory, 128-byte swizzle (see smem_desc_sw128);
+// offsets within the tile are constants added to the descriptor's lower half.
+struct Operand16 {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Operand16(uint32_t addr, uint32_t lbo_bytes) {
+    const uint64_t d = smem_desc_sw128(addr, lbo_bytes, 1024);
+    lo = static_cast<uint32_t>(d);
+    hi = static_cast<uint32_t>(d >> 32);
+  }
+};
+
+// An operand moved on by `bytes` (a multiple of 16).
+__device__ __forceinline__ Operand16 moved(Operand16 o, uint32_t bytes) {
+  o.lo += bytes >> 4;
+  return o;
+}
+
+// D[tmem] (+)= A * B^T with operands `a_off` and `b_off` bytes into their tiles.
+__device__ __forceinline__ void mma_f16_at(uint32_t d_tmem, const Operand16& a, uint32_t a_off,
+                                           const Operand16& b, uint32_t b_off, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+
+// The same over a CTA pair (issued by the even CTA; see mma_f16_pair).
+__device__ __forceinline__ void mma_f16_pair_at(uint32_t d_tmem, const Operand16& a,
+                                                uint32_t a_off, const Operand16& b,
+                                                uint32_t b_off, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc),
+      "r"(accumulate)
       : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit inputs, fp32 accumulate.  Lane i of
 // A holds row i, two K elements per 32-bit column (the lower half first).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts_at(uint32_t d_tmem, uint32_t a_tmem, const Operand16& b,
+                                              uint32_t b_off, uint32_t idesc,
+                                              uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on `bar` when every tcgen05 op that the elected lane issued is done.
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
+// The same for the MMAs of a CTA pair, on the barrier at this offset in every
+// CTA of `cta_mask`.
+__device__ __forceinline__ void commit_pair_elected(uint64_t* bar, uint16_t cta_mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+      ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+      "h"(cta_mask)
+      : "memory");
+}
+
+__device__ __forceinline__ void arrive_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_tx_elected(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(bytes)
+      : "memory");
+}
+
+// 3D tiled load global -> shared; completion counted in bytes on `bar`.
+__device__ __forceinline__ void tma_load_3d_elected(const CUtensorMap* map, uint64_t* bar,
+                                                    uint32_t dst, int32_t x, int32_t y,
+                                                    int32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// The same within a CTA pair: the byte count completes on the barrier at a
+// cluster address (of either CTA).
+__device__ __forceinline__ void tma_load_3d_pair_elected(const CUtensorMap* map,
+                                                         uint32_t bar_cluster, uint32_t dst,
+                                                         int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -83,10 +209,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return reinterpret_cast<const float2&>(d);
 }
 
-// mbar_wait by a whole warp: the same answer in every lane.
+// mbar_wait by a whole warp, the same answer in every lane.  One lane polls:
+// waiting warps share the shared-memory port with the operands of the MMAs.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, status);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 }  // namespace flce

@@ -318,3 +318,16 @@ def test_attention_broadcast_heads_gradient(cuda_lib):
     _, dk, _ = cuda_lib.flce_attn_bwd(C, q, k2, v, o2, lse, cu)
     assert torch.equal(o, o2)
     assert torch.equal(k1.grad, dk.sum(1, keepdim=True))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [
+    ([900, 257, 0, 130, 4, 1100], 40, 8, 128),   # several units per CTA, with and without a second tile
+    ([128] * 30 + [129] * 11, 16, 16, 64),
+])
+def test_attention_many_units(cuda_lib, lens, Hq, Hkv, D):
+    """More units of work than the GPU has SMs."""
+    q, k, v, dO, cu = _inputs(lens, Hq, Hkv, D, D, pad=3)
+    got = _run(cuda_lib, q, k, v, dO, cu)
+    val, tol = _reference(q, k, v, dO, lens, D ** -0.5)
+    for n in val:
+        _close(n, got[n], val[n], tol[n])
