@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* dl = lse2 + kTile + 64 * half;
       const float* ls = lse2 + 64 * half;
 
-      ok = warp_wait(s_full, it & 1, abort_flag, p.status) && ok;
+      ok = uniform_wait(s_full, it & 1, abort_flag, p.status) && ok;
       tc_fence_after();
       float P[64];
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) P[i] = (i >= lo && i < hi) ? P[i] : 0.f;
       }
-      ok = warp_wait(p_empty, (it & 1) ^ 1, abort_flag, p.status) && ok;
+      ok = uniform_wait(p_empty, (it & 1) ^ 1, abort_flag, p.status) && ok;
       const uint32_t prow = smem_addr(smP) + half * kBoxBytes + row * 128;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      pack_bf16x2(P[8 * i + 6], P[8 * i + 7]));
       if (valid < kTile) {
         // S^T of this tile is complete, so Q is only read again by dK
-        ok = warp_wait(&o_full[s], (it >> 1) & 1, abort_flag, p.status) && ok;
+        ok = uniform_wait(&o_full[s], (it >> 1) & 1, abort_flag, p.status) && ok;
         clear_rows<S::kBoxes>(smO + s * TB, valid);
         clear_rows<S::kBoxes>(smQ + s * TB, valid);
       }
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
 
-      ok = warp_wait(dp_full, it & 1, abort_flag, p.status) && ok;
+      ok = uniform_wait(dp_full, it & 1, abort_flag, p.status) && ok;
       tc_fence_after();
       float d[64];
 #pragma unroll
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
-    if (warp_wait(acc_full, 0, abort_flag, p.status) && ok) {
+    if (uniform_wait(acc_full, 0, abort_flag, p.status) && ok) {
       tc_fence_after();
       const int key = kt * kTile + row;
       const int64_t tok = static_cast<int64_t>(t.start) + key;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = 0; j < n_kv; ++j) {
       const bool diag = j == n_kv - 1;
-      ok = warp_wait(sdp_full, j & 1, abort_flag, p.status) && ok;
+      ok = uniform_wait(sdp_full, j & 1, abort_flag, p.status) && ok;
       tc_fence_after();
       const uint32_t tSj = tS + (j & 1) * kTile;
       float P[64], d[64];
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
-    if (warp_wait(acc_full, 0, abort_flag, p.status) && ok) {
+    if (uniform_wait(acc_full, 0, abort_flag, p.status) && ok) {
       tc_fence_after();
       uint16_t* dq = static_cast<uint16_t*>(p.dq.p) + tok * p.dq.token + h * p.dq.head;
 #pragma unroll 1

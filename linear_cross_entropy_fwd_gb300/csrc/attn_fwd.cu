@@ -3,19 +3,19 @@
 // A unit of work is 256 query rows (two tiles, A and B) of one query head.
 // For each key tile j and each of the two query tiles:
 //   MMA      S = Q K_j^T            into TMEM (128 fp32 columns)
-//   softmax  two threads per row, 64 columns each: running maximum m and sum
-//            l, P = 2^(cS - m) as bf16 over S's own columns
+//   softmax  one thread per row: running maximum m and sum l,
+//            P = 2^(cS - m) as bf16 over S's own columns
 //   MMA      O += P V_j             P from TMEM, V_j as it lies in memory
 // with c = scale log2(e).  Only the tile on the diagonal is masked, and it is
 // a query tile's last one.
 //
-// One CTA per SM walks the units, deepest first.  The tensor cores work on one
-// tile while the other's exponentials are taken, and both tiles share one load
-// of K_j and V_j: the operands' way through shared memory (TMA in, MMA out) is
-// 256 KB per two tile products at 128 bytes a clock, just what the MMAs take.
-// Each tile has an MMA thread of its own (PV, next S, PV, ...): issuing an MMA
-// of 64 clocks takes about 75 beside the other warps, a commit or a wait 100 to
-// 200, so that one thread for both keeps the tensor cores half idle.
+// One CTA per SM walks the units, deepest first.  Its MMA warp alternates
+// between the tiles (PV_A, next S_A, PV_B, next S_B), so the tensor cores work
+// on one tile while the other's exponentials are taken, and both tiles share
+// one load of K_j and V_j: the operands' way through shared memory (TMA in, MMA
+// out) is 256 KB per two tile products at 128 bytes a clock, just what the MMAs
+// take.  Measured at 8192 tokens, 32 heads of 128: two CTAs per SM with a tile
+// each 210 us, an MMA warp per tile 196 us, this 171 us.
 //
 // The maximum that P and O are relative to follows the true one only when it
 // has grown by more than 2^8: until then O needs no rescaling, and P <= 2^8,
@@ -27,11 +27,8 @@
 // masked in S; the rows of V there (another sequence's, of any value) are
 // cleared in shared memory, since 0 * NaN would reach O.
 //
-// Roles (640 threads): warps 0-7 softmax and output of tile A, 8-15 of tile B
-// (warp w: TMEM lanes 32 (w % 4) .., columns 64 ((w / 4) % 2) ..), warp 16 TMA,
-// warp 17 MMA.  The launch gives each thread 96 registers (640 x 96 = 61440);
-// the four softmax warpgroups go up to 104 and the last one down to 64
-// (512 x 104 + 128 x 64 = 61440).
+// Roles (320 threads): warps 0-3 softmax and output of tile A, 4-7 of tile B
+// (warp w: TMEM lanes 32 (w % 4) ..), warp 8 TMA, warp 9 MMA.
 #include "attn.h"
 #include "host_util.h"
 #include "sm103_attn.cuh"
@@ -41,9 +38,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kTmaWarp = 16, kMmaWarp = 17;
-constexpr int kFwdThreads = 20 * 32;  // whole warpgroups
-constexpr int kGroupThreads = 256;  // softmax threads of one tile
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kFwdThreads = 10 * 32;
 constexpr float kRescale = 8.f;     // log2 of the growth that triggers a rescaling
 constexpr uint32_t kTmemCols = 512;
 
@@ -53,13 +49,10 @@ struct FwdShape {
   static constexpr uint32_t kBoxBytes = kTile * 128;             // 128 rows x 64 elements
   static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kSlots = DP == 128 ? 4 : 8;               // K and V tiles in flight
-  static constexpr uint32_t kExchange = 4096;                    // row maxima and sums
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + kExchange + 256;
+  static constexpr int kBarriers = 2 * kSlots + 13;              // and a word each of TMEM, abort
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + 8 * (kBarriers + 1);
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
-
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 // The units of a CTA: rounds go through the list forwards and backwards in
 // turn, so that no CTA always gets the deeper one.
@@ -103,35 +96,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* smQ = smem;                        // [2]
   uint8_t* smKV = smem + 2 * TB;              // [kSlots]
-  float* exchange = reinterpret_cast<float*>(smKV + kSlots * TB);  // [tile][turn][half][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smKV + kSlots * TB + S::kExchange);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smKV + kSlots * TB);
   uint64_t* kv_full = bars;                   // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;      // [kSlots]
   uint64_t* q_full = kv_empty + kSlots;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;             // [2] per tile, from here on
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
+  uint64_t* p_full = s_full + 2;              // [2][2]
+  uint64_t* o_full = p_full + 4;
   uint64_t* o_empty = o_full + 2;
   uint64_t* drain = o_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::kBarriers);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 2);  // both query tiles are done with it
+      mbar_init(&kv_empty[i], 1);  // both query tiles are done with it
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);
+    mbar_init(q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 8);
+      mbar_init(&p_full[2 * x], 4);
+      mbar_init(&p_full[2 * x + 1], 4);
       mbar_init(&o_full[x], 1);
-      mbar_init(&o_empty[x], 8);
-      mbar_init(&drain[x], 1);
+      mbar_init(&o_empty[x], 4);
     }
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -148,7 +141,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   Unit w;
 
   if (warp >= kTmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kTmaWarp) {
       // ------------------------------------------------------------- TMA
       int g = 0, n_q = 0;
@@ -190,126 +182,126 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           mbar_wait_drain(&kv_full[i % kSlots], (i / kSlots) & 1);
       }
     }
-    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    if (warp == kMmaWarp) {
       // ------------------------------------------------------------- MMA
-      const int x = warp - kMmaWarp;  // query tile
       constexpr uint32_t kIdescS = make_idesc(1, false, false, kTile, kTile);
       constexpr uint32_t kIdescO = make_idesc(1, false, true, kTile, DP);
-      const Operand16 q_op(smem_addr(smQ + x * TB), 0), k_op(smem_addr(smKV), 0),
+      const Operand16 q_op(smem_addr(smQ), 0), k_op(smem_addr(smKV), 0),
           v_op(smem_addr(smKV), S::kBoxBytes);
-      const uint32_t tS = tmem + x * kTile, tO = tmem + 2 * kTile + x * DP;
       const int k_steps = (p.D + 15) / 16;  // columns past D are zeros
       int g = 0;                            // K and V tiles so far
-      int n_p = 0, n_u = 0;                 // products P V, and units, of this tile so far
+      int n_p[2] = {0, 0}, n_u[2] = {0, 0}; // products P V, and units, per query tile so far
       auto wait_kv = [&](int i) {
         return uniform_wait(&kv_full[i % kSlots], (i / kSlots) & 1, abort_flag, p.status);
       };
-      // K tile i -> S; or nothing, if this query tile does not see it.  Either
-      // way the slot is released, and after the unit's last S the query tile.
-      auto scores = [&](int i, bool use, bool last) {
-        if (!wait_kv(i)) return false;
-        const int slot = i % kSlots;
-        if (!use) {
-          arrive_elected(&kv_empty[slot]);
-          return true;
-        }
-        tc_fence_after();
-        const Operand16 k = moved(k_op, slot * TB);
+      auto scores = [&](int x, int i) {
+        const Operand16 q = moved(q_op, x * TB), k = moved(k_op, (i % kSlots) * TB);
 #pragma unroll
         for (int e = 0; e < DP / 16; ++e) {
           const uint32_t off = (e >> 2) * S::kBoxBytes + (e & 3) * 32;
-          if (e < k_steps) mma_f16_at(tS, q_op, off, k, off, kIdescS, e > 0);
+          if (e < k_steps) mma_f16_at(tmem + x * kTile, q, off, k, off, kIdescS, e > 0);
         }
         commit_elected(&s_full[x]);
-        commit_elected(&kv_empty[slot]);
-        if (last) commit_elected(q_empty);
-        return true;
       };
       bool ok = true;
       for (int round = 0; ok && w.get_uniform(p, round, total); ++round) {
-        const int n = w.n[x], depth = w.depth();
-        ok = uniform_wait(q_full, round & 1, abort_flag, p.status);
-        if (ok && n == 0) arrive_elected(q_empty);
-        ok = ok && scores(g, n > 0, n == 1);
+        const int depth = w.depth();
+        const int last = w.n[1] ? 1 : 0;  // the query tile that uses each key tile last
+        ok = uniform_wait(q_full, round & 1, abort_flag, p.status) && wait_kv(g);
+        if (!ok) break;
+        scores(0, g);
+        if (last) scores(1, g);
+        commit_elected(&kv_empty[g % kSlots]);
+        if (depth == 1) commit_elected(q_empty);
         for (int j = 0; ok && j < depth; ++j) {
-          const int i = g + 2 * j + 1, slot = i % kSlots;
-          if (!(ok = wait_kv(i))) break;
-          if (j < n) {
-            ok = (j > 0 || uniform_wait(&o_empty[x], (n_u & 1) ^ 1, abort_flag, p.status)) &&
-                 uniform_wait(&p_full[x], n_p & 1, abort_flag, p.status);
-            if (!ok) break;
-            ++n_p;
-            tc_fence_after();
-            const Operand16 v = moved(v_op, slot * TB);
+          const int iv = g + 2 * j + 1, ik = iv + 1;
+          bool have_k = false;
+          ok = wait_kv(iv);
 #pragma unroll
-            for (int e = 0; e < kTile / 16; ++e)
-              mma_f16_ts_at(tO, tS + 8 * e, v, e * 2048, kIdescO, (j > 0 || e > 0) ? 1u : 0u);
-            commit_elected(&kv_empty[slot]);
-            if (j == n - 1) commit_elected(&o_full[x]);
-          } else {
-            arrive_elected(&kv_empty[slot]);
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || x > last) break;
+            if (j < w.n[x]) {
+              ok = (j > 0 || uniform_wait(&o_empty[x], (n_u[x] & 1) ^ 1, abort_flag, p.status)) &&
+                   uniform_wait(&p_full[2 * x], n_p[x] & 1, abort_flag, p.status);
+              if (!ok) break;
+              const Operand16 v = moved(v_op, (iv % kSlots) * TB);
+              auto add_pv = [&](int from) {
+                tc_fence_after();
+#pragma unroll
+                for (int e = from; e < from + kTile / 32; ++e)
+                  mma_f16_ts_at(tmem + 2 * kTile + x * DP, tmem + x * kTile + 8 * e, v, e * 2048,
+                                kIdescO, (j > 0 || e > 0) ? 1u : 0u);
+              };
+              add_pv(0);
+              if (!(ok = uniform_wait(&p_full[2 * x + 1], n_p[x] & 1, abort_flag, p.status))) break;
+              add_pv(kTile / 32);
+              ++n_p[x];
+              if (j == 0) ++n_u[x];
+              if (j == w.n[x] - 1) commit_elected(&o_full[x]);
+            }
+            if (x == last) commit_elected(&kv_empty[iv % kSlots]);
+            if (j + 1 < w.n[x]) {
+              if (!have_k) ok = wait_kv(ik);
+              if (!ok) break;
+              have_k = true;
+              scores(x, ik);
+            }
+            if (x == last && j + 1 < depth) {
+              commit_elected(&kv_empty[ik % kSlots]);
+              if (j + 2 == depth) commit_elected(q_empty);
+            }
           }
-          if (j + 1 < depth) ok = scores(i + 1, j + 1 < n, j + 2 == n);
         }
         g += 2 * depth;
-        if (n > 0) ++n_u;
       }
-      commit_elected(&drain[x]);  // all MMAs issued by this thread are done
-      if (lane == 0) mbar_wait_drain(&drain[x], 0);
+      commit_elected(drain);  // all MMAs issued by this warp are done
+      if (lane == 0) mbar_wait_drain(drain, 0);
     }
   } else {
     // ----------------------------------------------------- softmax, output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    const int x = warp >> 3;                                  // query tile
-    const int quarter = warp & 3, half = (warp >> 2) & 1;
-    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const int x = warp >> 2;                                  // query tile
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + x * kTile + lanes, tO = tmem + 2 * kTile + x * DP + lanes;
-    const int row = 32 * quarter + lane;
+    const int row = threadIdx.x & (kTile - 1);
     const float c = p.scale * kLog2e;
-    float* ex = exchange + x * 512;
-    // After a wait has expired the loops go on without results, so that the two
-    // warps of a row still meet at their barrier; later waits then return at once.
     bool ok = true;
     int n_s = 0;  // score tiles so far
-    int n_x = 0;  // exchanges between the halves so far
     int J = 0;    // key tiles before this unit
     int n_u = 0;  // units of this tile so far
-    for (int round = 0; w.get(p, round, total); J += w.depth(), ++round) {
+    for (int round = 0; ok && w.get(p, round, total); J += w.depth(), ++round) {
       const int n = w.n[x];
       if (n == 0) continue;
       const int q0 = (2 * w.t.tile + x) * kTile;
       const int valid = w.t.len - q0 < kTile ? w.t.len - q0 : kTile;  // rows of this tile
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++n_s, ++n_x) {
-        ok = warp_wait(&s_full[x], n_s & 1, abort_flag, p.status) && ok;
+      float m = 0.f, l = 0.f;
+      for (int j = 0; j < n; ++j, ++n_s) {
+        if (!uniform_wait(&s_full[x], n_s & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const bool diag = j == n - 1;
-        float s[64];
+        float s[kTile];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          tmem_ld_32x32b_x32(tS + 64 * half + 32 * q,
-                             reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
+        for (int q = 0; q < 4; ++q)
+          tmem_ld_32x32b_x32(tS + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
         tmem_ld_wait();
         if (diag) {
-          const int lim = row - 64 * half;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = i > lim ? -INFINITY : s[i];
+          for (int i = 0; i < kTile; ++i) s[i] = i > row ? -INFINITY : s[i];
         }
         // independent chains: few warps per scheduler leave latency to hide
         float mxs[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mxs[i] = s[i];
+        for (int k = 0; k < 8; ++k) mxs[k] = max3(s[k], s[k + 8], s[k + 16]);
 #pragma unroll
-        for (int i = 8; i < 64; ++i) mxs[i & 7] = fmaxf(mxs[i & 7], s[i]);
-        float mx = fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
-                         fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
-        // the other half's maximum; P goes over columns of S that it has read
-        float* turn = ex + (n_x & 1) * 256;
-        turn[half * kTile + row] = mx;
-        tc_fence_before();
-        named_barrier(1 + 4 * x + quarter, 64);
-        tc_fence_after();
-        mx = c * fmaxf(mx, turn[(half ^ 1) * kTile + row]);
+        for (int i = 24; i < 120; i += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mxs[k] = max3(mxs[k], s[i + k], s[i + k + 8]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mxs[k] = fmaxf(mxs[k], s[120 + k]);
+        const float mx = c * fmaxf(max3(mxs[0], mxs[1], mxs[2]),
+                                   max3(max3(mxs[3], mxs[4], mxs[5]), mxs[6], mxs[7]));
         if (j == 0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
@@ -319,66 +311,64 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           m = mn;
           l *= f;
 #pragma unroll 1
-          for (int q = 0; q < DP / 64; ++q) {
-            uint32_t o[32];
-            const uint32_t at = tO + half * (DP / 2) + 32 * q;
-            tmem_ld_32x32b_x32(at, o);
+          for (int q = 0; q < DP / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tO + 16 * q, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st_32x32b_x32(at, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_32x32b_x16(tO + 16 * q, o);
           }
         }
-        float2 sums[4] = {};
-        const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 e = fma2(make_float2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), c2, m2);
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            sums[i & 3] = add2(sums[i & 3], e);
-            pk[i] = pack_bf16x2(e.x, e.y);
-          }
-          tmem_st_32x32b_x16(tS + 32 * half + 16 * q, pk);
-        }
-        const float2 sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
-        l += sum.x + sum.y;
         if (diag && valid < kTile) {
           const int g = 2 * (J + j) + 1, sv = g % kSlots;
-          ok = warp_wait(&kv_full[sv], (g / kSlots) & 1, abort_flag, p.status) && ok;
+          if (!uniform_wait(&kv_full[sv], (g / kSlots) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
           const int per = (kTile - valid) * 8;
-          for (int i = threadIdx.x & (kGroupThreads - 1); i < per * S::kBoxes; i += kGroupThreads)
+          for (int i = row; i < per * S::kBoxes; i += kTile)
             st_shared_v4(smem_addr(smKV) + sv * TB + (i / per) * S::kBoxBytes + valid * 128 +
                              (i % per) * 16, 0, 0, 0, 0);
           fence_proxy_async_smem();
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        // P in two halves: the product with the first runs while the second's
+        // exponentials are taken
+        const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+        float2 sums[2] = {};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float2 e = fma2(make_float2(s[64 * q + 2 * i], s[64 * q + 2 * i + 1]), c2, m2);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sums[i & 1] = add2(sums[i & 1], e);
+            pk[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st_32x32b_x32(tS + 32 * q, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + q]);
+        }
+        const float2 sum = add2(sums[0], sums[1]);
+        l += sum.x + sum.y;
       }
-      // both halves' sums; this turn's slots were last read a tile ago
-      float* turn = ex + (n_x & 1) * 256;
-      turn[half * kTile + row] = l;
-      named_barrier(1 + 4 * x + quarter, 64);
-      l += turn[(half ^ 1) * kTile + row];
-      ++n_x;
-      ok = warp_wait(&o_full[x], n_u & 1, abort_flag, p.status) && ok;
+      if (!ok || !uniform_wait(&o_full[x], n_u & 1, abort_flag, p.status)) break;
       ++n_u;
       tc_fence_after();
       const float inv = 1.f / l;
       const int64_t tok = static_cast<int64_t>(w.t.start) + q0 + row;
       uint16_t* out = static_cast<uint16_t*>(p.o.p) + tok * p.o.token + w.head * p.o.head;
-      const bool in = ok && row < valid;
+      const bool in = row < valid;
 #pragma unroll
-      for (int q = 0; q < DP / 64; ++q) {
+      for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
-        tmem_ld_32x32b_x32(tO + half * (DP / 2) + 32 * q, o);
+        tmem_ld_32x32b_x32(tO + 32 * q, o);
         tmem_ld_wait();
-        if (q == DP / 64 - 1) {  // O may be overwritten
+        if (q == DP / 32 - 1) {  // O may be overwritten
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_empty[x]);
@@ -390,13 +380,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int k = 0; k < 4; ++k)
             v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
                                __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-          const int d = half * (DP / 2) + 32 * q + 8 * i;
+          const int d = 32 * q + 8 * i;
           if (in && d < p.D)
             *reinterpret_cast<uint4*>(out + d) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
-      if (in && half == 0)
-        p.lse[static_cast<int64_t>(w.head) * p.T + tok] = (m + fast_log2(l)) * kLn2;
+      if (in) p.lse[static_cast<int64_t>(w.head) * p.T + tok] = (m + fast_log2(l)) * kLn2;
     }
     tc_fence_before();
   }

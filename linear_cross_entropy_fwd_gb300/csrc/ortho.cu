@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col0 = ni * kN + half * (kN / 2);
       Addend<MODE> add;
       add.load(p, bi, row0 + lane, col0);
-      if (!warp_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
+      if (!uniform_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
       tc_fence_after();
       epilogue<MODE>(p, add,
                      tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + half * (kN / 2),

@@ -16,10 +16,32 @@ namespace flce {
 // The same value in every lane, known to be so.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// mbar_wait by a converged warp; the same answer in every lane.
+// mbar_wait that looks at the clock and the abort flag only now and then: most
+// waits here end within a few hundred clocks, and reading the clock takes
+// about as long.
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int* status) {
+  const uint32_t a = smem_addr(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(a, parity)) return true;
+    if ((it & 255) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > FLCE_WAIT_LIMIT_NS) {
+        *abort_flag = 1;
+        atomicOr(status, FLCE_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// mbar_spin by a converged warp; the same answer in every lane.
 __device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity,
                                              volatile int* abort_flag, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+  return __all_sync(0xffffffffu, mbar_spin(bar, parity, abort_flag, status)) != 0;
 }
 
 // An operand tile in shared memory, 128-byte swizzle (see smem_desc_sw128);
@@ -154,6 +176,18 @@ __device__ __forceinline__ void tma_load_3d_pair_elected(const CUtensorMap* map,
       : "memory");
 }
 
+// 32 lanes x 16 consecutive 32-bit columns, TMEM -> registers.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns, registers -> TMEM.
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -209,13 +243,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return reinterpret_cast<const float2&>(d);
 }
 
-// mbar_wait by a whole warp, the same answer in every lane.  One lane polls:
-// waiting warps share the shared-memory port with the operands of the MMAs.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int* status) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, status);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 }  // namespace flce
