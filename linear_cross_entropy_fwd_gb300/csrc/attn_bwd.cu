@@ -101,22 +101,21 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int valid) {
   fence_proxy_async_smem();
 }
 
-// Accumulator columns [c0, c0 + 32) of this thread's row, times f, to bf16.
-__device__ __forceinline__ void store_cols(uint32_t taddr, float f, uint16_t* row, int c0, int D,
-                                           bool in) {
-  uint32_t o[32];
-  tmem_ld_32x32b_x32(taddr, o);
-  tmem_ld_wait();
+// Accumulator columns [c0, c0 + 64) of this warp's rows, times f, to bf16.
+__device__ __forceinline__ void store_cols(uint32_t taddr, float f, uint8_t* buf, uint16_t* dst,
+                                           int64_t pitch, int rows, int cols) {
+  uint32_t v[32];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w[4];
+  for (int q = 0; q < 2; ++q) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + 32 * q, r);
+    tmem_ld_wait();
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f,
-                         __uint_as_float(o[8 * i + 2 * k + 1]) * f);
-    const int d = c0 + 8 * i;
-    if (in && d < D) *reinterpret_cast<uint4*>(row + d) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 16; ++i)
+      v[16 * q + i] =
+          pack_bf16x2(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
   }
+  store_rows_bf16(buf, v, dst, pitch, rows, cols);
 }
 
 // ===================================================================== dkdv
@@ -359,15 +358,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (uniform_wait(acc_full, 0, abort_flag, p.status) && ok) {
       tc_fence_after();
-      const int key = kt * kTile + row;
-      const int64_t tok = static_cast<int64_t>(t.start) + key;
-      const bool in = key < t.len;
+      // every MMA is done: the query tiles' buffers stage the stores.  The two
+      // warps of a row take the 64-column blocks of dV and dK in turn.
+      uint8_t* buf = smQ + warp * 4096;
+      const int key0 = kt * kTile + 32 * quarter;
+      const int64_t tok = static_cast<int64_t>(t.start) + key0;
       uint16_t* dv = static_cast<uint16_t*>(p.dv.p) + tok * p.dv.token + kvh * p.dv.head;
       uint16_t* dk = static_cast<uint16_t*>(p.dk.p) + tok * p.dk.token + kvh * p.dk.head;
 #pragma unroll 1
-      for (int q = half * (DP / 64); q < (half + 1) * (DP / 64); ++q) {
-        store_cols(tDV + lanes + 32 * q, 1.f, dv, 32 * q, p.D, in);
-        store_cols(tDK + lanes + 32 * q, p.scale, dk, 32 * q, p.D, in);
+      for (int b = half; b < DP / 32; b += 2) {
+        const int c0 = 64 * (b % (DP / 64));
+        if (b < DP / 64)
+          store_cols(tDV + lanes + c0, 1.f, buf, dv + c0, p.dv.token, t.len - key0, p.D - c0);
+        else
+          store_cols(tDK + lanes + c0, p.scale, buf, dk + c0, p.dk.token, t.len - key0, p.D - c0);
       }
     }
     tc_fence_before();
@@ -538,10 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (uniform_wait(acc_full, 0, abort_flag, p.status) && ok) {
       tc_fence_after();
-      uint16_t* dq = static_cast<uint16_t*>(p.dq.p) + tok * p.dq.token + h * p.dq.head;
-#pragma unroll 1
-      for (int q = half * (DP / 64); q < (half + 1) * (DP / 64); ++q)
-        store_cols(tDQ + lanes + 32 * q, p.scale, dq, 32 * q, p.D, in);
+      // every MMA is done: the key tiles' buffers stage the stores
+      const int r0 = 32 * quarter;
+      uint16_t* dq = static_cast<uint16_t*>(p.dq.p) + (tok - lane) * p.dq.token + h * p.dq.head;
+      if (half < DP / 64)
+        store_cols(tDQ + lanes + 64 * half, p.scale, smK + warp * 4096, dq + 64 * half, p.dq.token,
+                   t.len - q0 - r0, p.D - 64 * half);
     }
     tc_fence_before();
   }

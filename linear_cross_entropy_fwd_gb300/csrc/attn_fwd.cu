@@ -50,7 +50,8 @@ struct FwdShape {
   static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kSlots = DP == 128 ? 4 : 8;               // K and V tiles in flight
   static constexpr int kBarriers = 2 * kSlots + 13;              // and a word each of TMEM, abort
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + 8 * (kBarriers + 1);
+  static constexpr uint32_t kStaging = 8 * 4096;                 // one block per softmax warp
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + kStaging + 8 * (kBarriers + 1);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -96,7 +97,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* smQ = smem;                        // [2]
   uint8_t* smKV = smem + 2 * TB;              // [kSlots]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smKV + kSlots * TB);
+  uint8_t* staging = smKV + kSlots * TB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + S::kStaging);
   uint64_t* kv_full = bars;                   // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;      // [kSlots]
   uint64_t* q_full = kv_empty + kSlots;
@@ -157,6 +159,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tma_load_3d_elected(&tmQ, q_full, q_dst + x * TB + b * S::kBoxBytes, 64 * b, w.head,
                                 w.t.start + (2 * w.t.tile + x) * kTile);
         ++n_q;
+        // the next unit's queries on their way into L2: they are loaded only
+        // when this unit's last scores are complete
+        Unit next;
+        if (next.get_uniform(p, round + 1, total))
+          for (int x = 0; x < (next.n[1] ? 2 : 1); ++x)
+#pragma unroll
+            for (int b = 0; b < S::kBoxes; ++b)
+              tma_prefetch_3d_elected(&tmQ, 64 * b, next.head,
+                                      next.t.start + (2 * next.t.tile + x) * kTile);
         const int depth = w.depth();
         for (int j = 0; ok && j < depth; ++j) {
 #pragma unroll
@@ -360,31 +371,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       ++n_u;
       tc_fence_after();
       const float inv = 1.f / l;
-      const int64_t tok = static_cast<int64_t>(w.t.start) + q0 + row;
-      uint16_t* out = static_cast<uint16_t*>(p.o.p) + tok * p.o.token + w.head * p.o.head;
-      const bool in = row < valid;
+      uint32_t o[DP / 2];
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tO + 32 * q, o);
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tO + 32 * q, r);
         tmem_ld_wait();
-        if (q == DP / 32 - 1) {  // O may be overwritten
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&o_empty[x]);
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                               __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-          const int d = 32 * q + 8 * i;
-          if (in && d < p.D)
-            *reinterpret_cast<uint4*>(out + d) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        for (int i = 0; i < 16; ++i)
+          o[16 * q + i] = pack_bf16x2(__uint_as_float(r[2 * i]) * inv,
+                                      __uint_as_float(r[2 * i + 1]) * inv);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[x]);  // O may be overwritten
+      const int64_t tok = static_cast<int64_t>(w.t.start) + q0 + row;
+      const bool in = row < valid;
+      uint16_t* out = static_cast<uint16_t*>(p.o.p) + (tok - lane) * p.o.token + w.head * p.o.head;
+#pragma unroll
+      for (int b = 0; b < DP / 64; ++b)
+        store_rows_bf16(staging + warp * 4096, reinterpret_cast<uint32_t(&)[32]>(o[32 * b]),
+                        out + 64 * b, p.o.token, valid - (row - lane), p.D - 64 * b);
       if (in) p.lse[static_cast<int64_t>(w.head) * p.T + tok] = (m + fast_log2(l)) * kLn2;
     }
     tc_fence_before();

@@ -249,4 +249,39 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Fetch a 3D box into L2 ahead of its load.
+__device__ __forceinline__ void tma_prefetch_3d_elected(const CUtensorMap* map, int32_t x,
+                                                        int32_t y, int32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n\t}" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// 32 rows (one per lane) x 64 bf16 columns, packed in pairs, to rows `pitch`
+// elements apart.  They go through 4 KB of shared memory, so that a store
+// instruction writes whole 128-byte lines (four rows): stored by the lanes that
+// hold the rows, 128 x 128 values took 3200 clocks.  Rows from `rows` on and
+// columns from `cols` on (a multiple of 8) are left out.
+__device__ __forceinline__ void store_rows_bf16(uint8_t* buf, const uint32_t (&v)[32],
+                                                uint16_t* dst, int64_t pitch, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_addr(buf);
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st_shared_v4(base + lane * 128 + ((c ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1],
+                 v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3), c = lane & 7;
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    if (r < rows && 8 * c < cols) *reinterpret_cast<uint4*>(dst + r * pitch + 8 * c) = w;
+  }
+  __syncwarp();
+}
+
 }  // namespace flce
