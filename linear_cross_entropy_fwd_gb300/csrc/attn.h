@@ -54,7 +54,7 @@ cudaError_t launch_attn_plan(const AttnParams& p, bool backward, int sms, cudaSt
 cudaError_t launch_attn_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                             const AttnParams& p, int sms, cudaStream_t s);
 cudaError_t launch_attn_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                             const CUtensorMap& dO, const AttnParams& p, cudaStream_t s);
+                             const CUtensorMap& dO, const AttnParams& p, int sms, cudaStream_t s);
 cudaError_t launch_attn_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& dO, const AttnParams& p, cudaStream_t s);
 

@@ -120,7 +120,7 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   cudaError_t e = launch_attn_plan(p, backward, sms, call.stream);
   if (max_tiles > 0) {
     if (backward) {
-      if (e == cudaSuccess) e = launch_attn_dkdv(mq, mk, mv, mO, p, call.stream);
+      if (e == cudaSuccess) e = launch_attn_dkdv(mq, mk, mv, mO, p, sms, call.stream);
       if (e == cudaSuccess) e = launch_attn_dq(mq, mk, mv, mO, p, call.stream);
     } else if (e == cudaSuccess) {
       e = launch_attn_fwd(mq, mk, mv, p, sms, call.stream);

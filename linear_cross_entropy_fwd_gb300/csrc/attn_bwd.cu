@@ -13,6 +13,11 @@
 // to memory from every CTA; that would make dQ depend on the order of the
 // additions (or need one more pass over fp32 partial sums).
 //
+// Where the key tiles alone leave SMs idle, the query heads of a group are shared
+// out over a cluster of up to eight CTAs; their fp32 sums are added in head
+// order through distributed shared memory (2048 tokens in eight sequences, 16
+// heads of 64 on 4: 44 -> 29 us).
+//
 // P and dS are rounded to bf16, the type of the MMA operands; sums are fp32.
 // Only tiles on the diagonal and at a sequence's end are masked, by selection,
 // and rows past the end of the sequence are cleared in shared memory where
@@ -118,17 +123,81 @@ __device__ __forceinline__ void store_cols(uint32_t taddr, float f, uint8_t* buf
   store_rows_bf16(buf, v, dst, pitch, rows, cols);
 }
 
+// Accumulator columns [c0, c0 + 64) of this thread's row, in fp32, to a
+// [128, DP] matrix in shared memory whose 16-byte pieces are swizzled by row.
+template <int DP>
+__device__ __forceinline__ void put_partial(uint32_t taddr, uint8_t* mat, int row, int c0) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + 32 * q, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int piece = (c0 + 32 * q) / 4 + i;
+      st_shared_v4(smem_addr(mat) + row * (DP * 4) + ((piece ^ (row & 7)) << 4), r[4 * i],
+                   r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    }
+  }
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// This CTA's share of dV and dK: the sums of the cluster's partial matrices in
+// rank order, eight columns at a time.
+template <int DP>
+__device__ __forceinline__ void add_partials(const AttnParams& p, const uint8_t* mats, int token0,
+                                             int rows, int kvh, int share, int split) {
+  constexpr int kItems = 2 * kTile * (DP / 8);
+  const int per = (kItems + split - 1) / split;
+  const int end = (share + 1) * per < kItems ? (share + 1) * per : kItems;
+  for (int i = share * per + static_cast<int>(threadIdx.x); i < end; i += kThreads) {
+    const int is_k = i / (kTile * (DP / 8));
+    const int row = i / (DP / 8) % kTile, c8 = i % (DP / 8);
+    if (row >= rows || 8 * c8 >= p.D) continue;
+    const uint32_t at = smem_addr(mats) + is_k * (kTile * DP * 4) + row * (DP * 4);
+    float v[8] = {};
+    for (int r = 0; r < split; ++r) {
+      const uint32_t remote = mapa_shared(at, static_cast<uint32_t>(r));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 f = ld_shared_cluster_f4(remote + (((2 * c8 + h) ^ (row & 7)) << 4));
+        v[4 * h] += f.x;
+        v[4 * h + 1] += f.y;
+        v[4 * h + 2] += f.z;
+        v[4 * h + 3] += f.w;
+      }
+    }
+    const float f = is_k ? p.scale : 1.f;
+    const AttnOut& o = is_k ? p.dk : p.dv;
+    uint16_t* dst = static_cast<uint16_t*>(o.p) + (static_cast<int64_t>(token0) + row) * o.token +
+                    kvh * o.head + 8 * c8;
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
+                   pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
+  }
+}
+
 // ===================================================================== dkdv
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ CUtensorMap tmO, const AttnParams p) {
+                     const __grid_constant__ CUtensorMap tmO, const AttnParams p,
+                     const int split) {
   using S = BwdShape<DP>;
   constexpr uint32_t TB = S::kTileBytes;
-  const int kvh = static_cast<int>(blockIdx.x % p.Hkv);
-  const int idx = static_cast<int>(blockIdx.x / p.Hkv);
+  const int share = static_cast<int>(blockIdx.x) % split;  // this CTA's rank in its cluster
+  const int kvh = static_cast<int>(blockIdx.x) / split % p.Hkv;
+  const int idx = static_cast<int>(blockIdx.x) / split / p.Hkv;
   grid_dependency_wait();  // the tile list and delta
   if (idx >= *p.n_tiles) return;
   AttnTile t = p.tiles[idx];
@@ -137,7 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_q = uniform(t.tile) + 1;                           // query tiles that see this key tile
   const int kt = (t.len + kTile - 1) / kTile - n_q;     // this key tile
   const int group = p.Hq / p.Hkv;
-  const int total = n_q * group;                        // (head, query tile) pairs
+  const int heads = group / split;                      // of this CTA
+  const int head0 = kvh * group + share * heads;
+  const int total = n_q * heads;                        // (head, query tile) pairs
 
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* smK = smem;
@@ -185,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < total; ++it) {
       const int s = it & 1;
       const uint32_t par = ((it >> 1) & 1) ^ 1;
-      const int head = kvh * group + it / n_q;
+      const int head = head0 + it / n_q;
       const int tok = t.start + (kt + it % n_q) * kTile;
       if (!uniform_wait(&q_empty[s], par, abort_flag, p.status)) break;
       expect_tx_elected(&q_full[s], TB);
@@ -262,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch = [&](int it) {
       const int q = (kt + it % n_q) * kTile + (tid & 127);
       if (it >= total || q >= t.len) return 0.f;
-      const int64_t at = static_cast<int64_t>(kvh * group + it / n_q) * p.T + t.start + q;
+      const int64_t at = static_cast<int64_t>(head0 + it / n_q) * p.T + t.start + q;
       return tid < kTile ? p.lse[at] * kLog2e : p.delta[at];
     };
     float next = fetch(0);
@@ -358,23 +429,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (uniform_wait(acc_full, 0, abort_flag, p.status) && ok) {
       tc_fence_after();
-      // every MMA is done: the query tiles' buffers stage the stores.  The two
-      // warps of a row take the 64-column blocks of dV and dK in turn.
-      uint8_t* buf = smQ + warp * 4096;
+      // Every MMA is done, and the tiles in shared memory are not needed any
+      // more.  The two warps of a row take the 64-column blocks of dV and dK in
+      // turn.
       const int key0 = kt * kTile + 32 * quarter;
       const int64_t tok = static_cast<int64_t>(t.start) + key0;
       uint16_t* dv = static_cast<uint16_t*>(p.dv.p) + tok * p.dv.token + kvh * p.dv.head;
       uint16_t* dk = static_cast<uint16_t*>(p.dk.p) + tok * p.dk.token + kvh * p.dk.head;
 #pragma unroll 1
       for (int b = half; b < DP / 32; b += 2) {
+        const bool is_k = b >= DP / 64;
         const int c0 = 64 * (b % (DP / 64));
-        if (b < DP / 64)
-          store_cols(tDV + lanes + c0, 1.f, buf, dv + c0, p.dv.token, t.len - key0, p.D - c0);
+        const uint32_t acc = (is_k ? tDK : tDV) + lanes + c0;
+        if (split > 1)
+          put_partial<DP>(acc, smem + is_k * (kTile * DP * 4), row, c0);
         else
-          store_cols(tDK + lanes + c0, p.scale, buf, dk + c0, p.dk.token, t.len - key0, p.D - c0);
+          store_cols(acc, is_k ? p.scale : 1.f, smQ + warp * 4096, (is_k ? dk : dv) + c0,
+                     is_k ? p.dk.token : p.dv.token, t.len - key0, p.D - c0);
       }
     }
     tc_fence_before();
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync();  // every CTA's partial sums are in its shared memory
+    add_partials<DP>(p, smem, t.start + kt * kTile, t.len - kt * kTile, kvh, share, split);
+    cluster_sync();  // no CTA leaves while others read it
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -558,44 +638,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <class KernelT>
-cudaError_t launch(KernelT kernel, uint32_t smem, unsigned blocks, bool overlap,
-                   const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
+template <class KernelT, class... Extra>
+cudaError_t launch(KernelT kernel, uint32_t smem, unsigned blocks, unsigned cluster, bool overlap,
+                   cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k,
+                   const CUtensorMap& v, const CUtensorMap& dO, const AttnParams& p,
+                   Extra... extra) {
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, q, k, v, dO, p);
+  cfg.numAttrs = overlap ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, q, k, v, dO, p, extra...);
+}
+
+// CTAs per key tile and kv head: the fewest that give every SM one, among the
+// divisors of the group up to eight (the cluster size that always fits).  The
+// 2048 tokens above: one 44 us, two or four 29.
+int split_heads(const AttnParams& p, int sms) {
+  const int group = p.Hq / p.Hkv;
+  const int64_t ctas = static_cast<int64_t>(p.max_tiles) * p.Hkv;
+  int best = 1;
+  for (int n = 1; n <= 8 && n <= group; ++n) {
+    if (group % n != 0) continue;
+    best = n;
+    if (ctas * n >= sms) break;
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_attn_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                             const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hkv);
-  return p.D <= 64 ? launch(attn_dkdv_kernel<64>, BwdShape<64>::kSmemDkDv, blocks, true, q, k, v,
-                            dO, p, s)
-                   : launch(attn_dkdv_kernel<128>, BwdShape<128>::kSmemDkDv, blocks, true, q, k,
-                            v, dO, p, s);
+                             const CUtensorMap& dO, const AttnParams& p, int sms, cudaStream_t s) {
+  const int split = split_heads(p, sms);
+  const unsigned c = static_cast<unsigned>(split);
+  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hkv) * c;
+  return p.D <= 64 ? launch(attn_dkdv_kernel<64>, BwdShape<64>::kSmemDkDv, blocks, c, true, s, q,
+                            k, v, dO, p, split)
+                   : launch(attn_dkdv_kernel<128>, BwdShape<128>::kSmemDkDv, blocks, c, true, s, q,
+                            k, v, dO, p, split);
 }
 
 cudaError_t launch_attn_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
   const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hq);
-  return p.D <= 64 ? launch(attn_dq_kernel<64>, BwdShape<64>::kSmemDq, blocks, false, q, k, v, dO,
-                            p, s)
-                   : launch(attn_dq_kernel<128>, BwdShape<128>::kSmemDq, blocks, false, q, k, v,
-                            dO, p, s);
+  return p.D <= 64 ? launch(attn_dq_kernel<64>, BwdShape<64>::kSmemDq, blocks, 1, false, s, q, k,
+                            v, dO, p)
+                   : launch(attn_dq_kernel<128>, BwdShape<128>::kSmemDq, blocks, 1, false, s, q, k,
+                            v, dO, p);
 }
 
 }  // namespace flce
