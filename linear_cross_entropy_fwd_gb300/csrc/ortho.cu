@@ -141,31 +141,63 @@ __device__ __forceinline__ void store_16_transposed(const uint32_t (&v)[16], uin
       dst[j * ld + lane] = static_cast<uint16_t>(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
 }
 
-// What the epilogue adds the product to: 32 columns of this lane's row of X
-// (fp32) or of A (fp16), and the rows of its matrix that this warp has.
+// What the epilogue adds the product to: a block of 32 x 32 values of X (fp32)
+// or of A (fp16).  Fetched in whole lines (a load instruction covers 4 or 8
+// rows) and turned around in shared memory into one row per lane; fetched by
+// the lanes that need the rows, a 256 x 256 tile's took 11 us.
 template <int MODE>
 struct Addend {
-  uint4 v[MODE == kUpdate ? 8 : 4];
-  __device__ __forceinline__ void load(const OrthoParams& p, int bi, int row, int c0) {
+  static constexpr int kVecs = MODE == kUpdate ? 8 : 4;  // 16-byte pieces of a row
+  static constexpr int kPer = 32 / kVecs;                // elements of a piece
+  static constexpr int kRows = 32 / kVecs;               // rows per load instruction
+  uint4 v[kVecs];
+
+  __device__ __forceinline__ void fetch(const OrthoParams& p, int bi, int row0, int c0) {
     if (MODE == kGram) return;
-    constexpr int kPer = MODE == kUpdate ? 4 : 8;  // elements per vector
+    const int lane = threadIdx.x & 31, c = lane % kVecs;
+    const int64_t ld = MODE == kUpdate ? p.ldx : p.ld;
     const uint4* src =
         MODE == kUpdate
-            ? reinterpret_cast<const uint4*>(p.x + bi * p.x_stride + row * p.ldx + c0)
-            : reinterpret_cast<const uint4*>(p.gram + bi * p.stride + row * p.ld + c0);
-    const int n = row < p.rows ? p.cols - c0 : 0;
+            ? reinterpret_cast<const uint4*>(p.x + bi * p.x_stride + row0 * ld + c0) + c
+            : reinterpret_cast<const uint4*>(p.gram + bi * p.stride + row0 * ld + c0) + c;
+    const bool in = kPer * c < p.cols - c0;
 #pragma unroll
-    for (int i = 0; i < 32 / kPer; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
+      const int r = kRows * i + lane / kVecs;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (kPer * i < n) v[i] = __ldcg(src + i);
+      if (in && row0 + r < p.rows) v[i] = __ldcg(src + r * ld / kPer);
     }
   }
-  __device__ __forceinline__ float at(int i) const {
-    if (MODE == kGram) return 0.f;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-    if (MODE == kUpdate) return __uint_as_float(w[i]);
-    const __half2 h = *reinterpret_cast<const __half2*>(w + (i >> 1));
-    return i & 1 ? __high2float(h) : __low2float(h);
+  // `buf`: 4 KB of this warp's
+  __device__ __forceinline__ void to_rows(uint8_t* buf, float (&out)[32]) const {
+    if (MODE == kGram) return;
+    const int lane = threadIdx.x & 31, c = lane % kVecs;
+    constexpr int kRowBytes = 16 * kVecs;
+    const uint32_t base = smem_addr(buf);
+    auto swizzle = [](int r) { return MODE == kUpdate ? r & 7 : (r >> 1) & 3; };
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int r = kRows * i + lane / kVecs;
+      st_shared_v4(base + r * kRowBytes + ((c ^ swizzle(r)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint4 q = *reinterpret_cast<const uint4*>(buf + lane * kRowBytes +
+                                                      ((i ^ swizzle(lane)) << 4));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (MODE == kUpdate) {
+          out[4 * i + k] = __uint_as_float(w[k]);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          out[8 * i + 2 * k] = f.x;
+          out[8 * i + 2 * k + 1] = f.y;
+        }
+      }
+    }
+    __syncwarp();
   }
 };
 
@@ -185,20 +217,20 @@ __device__ __forceinline__ void epilogue(const OrthoParams& p, Addend<MODE>& add
     if (cols <= 0) break;
     uint32_t r[32];
     tmem_ld_32x32b_x32(taddr + u, r);
-    const Addend<MODE> cur = add;
-    if (u + 32 < width) add.load(p, bi, row0 + lane, c0 + 32);
+    float v[32];
+    add.to_rows(buf, v);
+    if (u + 32 < width) add.fetch(p, bi, row0, c0 + 32);
     tmem_ld_wait();
     // the accumulator holds 4096^2 times the product
-    float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float acc = __uint_as_float(r[i]);
       if (MODE == kGram)
         v[i] = acc * kUnhold;
       else if (MODE == kPoly)
-        v[i] = fmaf(p.c * kUnhold, acc, p.b * cur.at(i));
+        v[i] = fmaf(p.c * kUnhold, acc, p.b * v[i]);
       else
-        v[i] = fmaf(acc, kUnhold * kUnhold, p.a * cur.at(i));
+        v[i] = fmaf(acc, kUnhold * kUnhold, p.a * v[i]);
     }
     uint32_t w[16];
     if (MODE == kUpdate && p.result) {
@@ -401,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = (mi * kCtas + static_cast<int>(rank)) * 128 + 32 * q;
       const int col0 = ni * kN + half * (kN / 2);
       Addend<MODE> add;
-      add.load(p, bi, row0 + lane, col0);
+      add.fetch(p, bi, row0, col0);
       if (!uniform_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
       tc_fence_after();
       epilogue<MODE>(p, add,
