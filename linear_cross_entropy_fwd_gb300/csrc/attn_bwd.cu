@@ -639,12 +639,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <class KernelT, class... Extra>
-cudaError_t launch(KernelT kernel, uint32_t smem, unsigned blocks, unsigned cluster, bool overlap,
-                   cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k,
-                   const CUtensorMap& v, const CUtensorMap& dO, const AttnParams& p,
-                   Extra... extra) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t launch(KernelT kernel, SmemLimit& limit, uint32_t smem, unsigned blocks,
+                   unsigned cluster, bool overlap, cudaStream_t s, const CUtensorMap& q,
+                   const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
+                   const AttnParams& p, Extra... extra) {
+  const cudaError_t e = limit.raise(kernel, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -661,6 +660,25 @@ cudaError_t launch(KernelT kernel, uint32_t smem, unsigned blocks, unsigned clus
   cfg.attrs = attr;
   cfg.numAttrs = overlap ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, q, k, v, dO, p, extra...);
+}
+
+template <int DP>
+cudaError_t launch_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                        const CUtensorMap& dO, const AttnParams& p, int split, cudaStream_t s) {
+  static SmemLimit limit;
+  const unsigned c = static_cast<unsigned>(split);
+  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hkv) * c;
+  return launch(attn_dkdv_kernel<DP>, limit, BwdShape<DP>::kSmemDkDv, blocks, c, true, s, q, k, v,
+                dO, p, split);
+}
+
+template <int DP>
+cudaError_t launch_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                      const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
+  static SmemLimit limit;
+  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hq);
+  return launch(attn_dq_kernel<DP>, limit, BwdShape<DP>::kSmemDq, blocks, 1, false, s, q, k, v, dO,
+                p);
 }
 
 // CTAs per key tile and kv head: the fewest that give every SM one, among the
@@ -683,21 +701,13 @@ int split_heads(const AttnParams& p, int sms) {
 cudaError_t launch_attn_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                              const CUtensorMap& dO, const AttnParams& p, int sms, cudaStream_t s) {
   const int split = split_heads(p, sms);
-  const unsigned c = static_cast<unsigned>(split);
-  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hkv) * c;
-  return p.D <= 64 ? launch(attn_dkdv_kernel<64>, BwdShape<64>::kSmemDkDv, blocks, c, true, s, q,
-                            k, v, dO, p, split)
-                   : launch(attn_dkdv_kernel<128>, BwdShape<128>::kSmemDkDv, blocks, c, true, s, q,
-                            k, v, dO, p, split);
+  return p.D <= 64 ? launch_dkdv<64>(q, k, v, dO, p, split, s)
+                   : launch_dkdv<128>(q, k, v, dO, p, split, s);
 }
 
 cudaError_t launch_attn_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hq);
-  return p.D <= 64 ? launch(attn_dq_kernel<64>, BwdShape<64>::kSmemDq, blocks, 1, false, s, q, k,
-                            v, dO, p)
-                   : launch(attn_dq_kernel<128>, BwdShape<128>::kSmemDq, blocks, 1, false, s, q, k,
-                            v, dO, p);
+  return p.D <= 64 ? launch_dq<64>(q, k, v, dO, p, s) : launch_dq<128>(q, k, v, dO, p, s);
 }
 
 }  // namespace flce

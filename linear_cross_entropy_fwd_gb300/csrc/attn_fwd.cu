@@ -406,9 +406,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <int DP>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                      const AttnParams& p, int sms, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(FwdShape<DP>::kSmem));
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(attn_fwd_kernel<DP>, FwdShape<DP>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(p.max_tiles) * p.Hq;
   cudaLaunchConfig_t cfg = {};

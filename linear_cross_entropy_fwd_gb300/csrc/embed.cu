@@ -586,9 +586,8 @@ cudaError_t launch_after(KernelT kernel, dim3 grid, int threads, const P& p, cud
 
 template <int CTAS>
 cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(embed_sort_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           sort_smem(CTAS));
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(embed_sort_kernel<CTAS>, sort_smem(CTAS));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/flce.h"
 #include "flce_internal.h"
 
@@ -33,6 +35,27 @@ int host_tensor_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, in
     const cudaError_t e_ = (call);                                     \
     if (e_ != cudaSuccess) return ::flce::host_cuda_error(e_, #call);  \
   } while (0)
+
+// A kernel's dynamic shared-memory limit, raised once per device (that costs
+// about as much as a launch).
+class SmemLimit {
+ public:
+  template <class KernelT>
+  cudaError_t raise(KernelT kernel, size_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};  // devices 0 .. 63 (host_device refuses others)
+};
 
 inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 

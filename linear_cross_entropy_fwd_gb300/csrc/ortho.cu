@@ -711,8 +711,8 @@ cudaError_t launch_shape(const CUtensorMap& A, const CUtensorMap& B, OrthoParams
   p.symmetric = MODE != kUpdate;
   p.tiles = p.symmetric ? p.m_blk * (p.m_blk + 1) / 2 : p.m_blk * p.n_blk;
   const auto kernel = ortho_gemm<MODE, PAIR>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(kernel, kSmem);
   if (e != cudaSuccess) return e;
   const int64_t total = static_cast<int64_t>(p.tiles) * p.batch;
   const int64_t cap = PAIR ? sms / 2 : sms;
