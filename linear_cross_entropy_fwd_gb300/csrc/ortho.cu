@@ -19,9 +19,13 @@
 // A and A^2 are symmetric: tiles below the diagonal are computed, and written
 // twice.  That makes the flops of a step k^2 n + k^3 + 2 k^2 n.
 //
-// Launches: norm, split (fp32 and fp16 X), then three GEMMs per step.  Two
-// GEMM shapes, both with 32 KB stages of A and B, six deep: CTA pairs on
-// 256 x 256 tiles, and single CTAs on 128 x 128 tiles for small matrices.
+// Launches: norm, split (fp32 and fp16 X), then three GEMMs per step, in three
+// shapes with 32 KB stages of A and B, six deep: CTA pairs on 256 x 256 tiles,
+// and for small matrices 128 x 128 tiles by single CTAs or by clusters of four
+// that share out K.  (All steps in one cooperative launch with a barrier over
+// the grid was built and took longer: 154 against 112 us for eight 256 x 1024
+// matrices.  Between two products the barrier, the fences before it and the first
+// loads after it took 4 to 5 us, and the next launch no more.)
 #include <cmath>
 
 #include "host_util.h"
@@ -131,14 +135,29 @@ __device__ __forceinline__ void store_16(uint8_t* buf, const uint32_t (&v)[16], 
   __syncwarp();
 }
 
-// Column j of the block becomes row j of dst (32 lanes: 64 contiguous bytes).
-__device__ __forceinline__ void store_16_transposed(const uint32_t (&v)[16], uint16_t* dst,
-                                                    int64_t ld, int rows, int cols) {
+// Column j of the block becomes row j of dst, 16 bytes at a time if `vec` (with
+// the last piece of a row written whole: rows are padded), else by element.
+__device__ __forceinline__ void store_16_transposed(uint8_t* buf, const uint32_t (&v)[16],
+                                                    uint16_t* dst, int64_t ld, int rows, int cols,
+                                                    bool vec) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (j < cols && lane < rows)
-      dst[j * ld + lane] = static_cast<uint16_t>(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
+    reinterpret_cast<uint16_t*>(buf)[j * 32 + lane] =
+        static_cast<uint16_t>(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
+  __syncwarp();
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 8 * i + (lane >> 2), c = lane & 3;
+      const uint4 w = *reinterpret_cast<const uint4*>(buf + j * 64 + c * 16);
+      if (j < cols && 8 * c < rows) *reinterpret_cast<uint4*>(dst + j * ld + 8 * c) = w;
+    }
+  } else {
+    for (int j = 0; j < cols && j < 32; ++j)
+      if (lane < rows) dst[j * ld + lane] = reinterpret_cast<const uint16_t*>(buf)[j * 32 + lane];
+  }
+  __syncwarp();
 }
 
 // What the epilogue adds the product to: a block of 32 x 32 values of X (fp32)
@@ -201,72 +220,131 @@ struct Addend {
   }
 };
 
-// Epilogue of 32 rows of an accumulator, columns [col0, col0 + width); `add`
-// holds the first 32 columns' addend, fetched before the accumulator was
+// A 32 x 32 block of an accumulator (row row0 + lane, columns c0 ..), turned into
+// the launch's result and stored.  `acc` holds 4096^2 times the product.
+template <int MODE>
+__device__ __forceinline__ void finish_block(const OrthoParams& p, const Addend<MODE>& add,
+                                             const float (&acc)[32], int bi, int row0, int c0,
+                                             bool mirror, uint8_t* buf) {
+  const int rows = p.rows - row0, cols = p.cols - c0;
+  float v[32];
+  add.to_rows(buf, v);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (MODE == kGram)
+      v[i] = acc[i] * kUnhold;
+    else if (MODE == kPoly)
+      v[i] = fmaf(p.c * kUnhold, acc[i], p.b * v[i]);
+    else
+      v[i] = fmaf(acc[i], kUnhold * kUnhold, p.a * v[i]);
+  }
+  uint32_t w[16];
+  if (MODE == kUpdate && p.result) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    uint16_t* res = p.result + static_cast<int64_t>(bi) * p.rows * p.cols;
+    if (p.transposed)
+      store_16_transposed(buf, w, res + static_cast<int64_t>(c0) * p.rows + row0, p.rows, rows,
+                          cols, p.result_vec != 0);
+    else
+      store_16(buf, w, res + static_cast<int64_t>(row0) * p.cols + c0, p.cols, rows, cols,
+               p.result_vec != 0);
+    return;
+  }
+  if (MODE == kUpdate) {
+    store_f32(buf, v, p.x + bi * p.x_stride + row0 * p.ldx + c0, p.ldx, rows, cols);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= kHold;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+  uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + bi * p.stride;
+  store_16(buf, w, o + row0 * p.ld + c0, p.ld, rows, cols, true);
+  if (mirror) store_16_transposed(buf, w, o + c0 * p.ld + row0, p.ld, rows, cols, true);
+}
+
+// 32 rows of an accumulator, columns [col0, col0 + width), block by block;
+// `add` holds the first block's addend, fetched before the accumulator was
 // complete, and each later one is fetched while the one before it is stored.
 template <int MODE>
 __device__ __forceinline__ void epilogue(const OrthoParams& p, Addend<MODE>& add, uint32_t taddr,
                                          int bi, int row0, int col0, int width, bool mirror,
                                          uint8_t* buf) {
-  const int lane = threadIdx.x & 31;
-  const int rows = p.rows - row0;  // of this warp's 32
-  if (rows <= 0) return;
+  if (row0 >= p.rows) return;
 #pragma unroll 1
   for (int u = 0; u < width; u += 32) {
-    const int c0 = col0 + u, cols = p.cols - c0;
-    if (cols <= 0) break;
+    const int c0 = col0 + u;
+    if (c0 >= p.cols) break;
     uint32_t r[32];
     tmem_ld_32x32b_x32(taddr + u, r);
-    float v[32];
-    add.to_rows(buf, v);
+    const Addend<MODE> cur = add;
     if (u + 32 < width) add.fetch(p, bi, row0, c0 + 32);
     tmem_ld_wait();
-    // the accumulator holds 4096^2 times the product
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float acc = __uint_as_float(r[i]);
-      if (MODE == kGram)
-        v[i] = acc * kUnhold;
-      else if (MODE == kPoly)
-        v[i] = fmaf(p.c * kUnhold, acc, p.b * v[i]);
-      else
-        v[i] = fmaf(acc, kUnhold * kUnhold, p.a * v[i]);
-    }
-    uint32_t w[16];
-    if (MODE == kUpdate && p.result) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      uint16_t* res = p.result + static_cast<int64_t>(bi) * p.rows * p.cols;
-      if (p.transposed)
-        store_16_transposed(w, res + static_cast<int64_t>(c0) * p.rows + row0, p.rows, rows, cols);
-      else
-        store_16(buf, w, res + static_cast<int64_t>(row0) * p.cols + c0, p.cols, rows, cols,
-                 p.result_vec != 0);
-      continue;
-    }
-    if (MODE == kUpdate) {
-      store_f32(buf, v, p.x + bi * p.x_stride + row0 * p.ldx + c0, p.ldx, rows, cols);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= kHold;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + bi * p.stride;
-    store_16(buf, w, o + row0 * p.ld + c0, p.ld, rows, cols, true);
-    if (mirror) store_16_transposed(w, o + c0 * p.ld + row0, p.ld, rows, cols);
+    finish_block<MODE>(p, cur, reinterpret_cast<const float(&)[32]>(r), bi, row0, c0, mirror, buf);
   }
 }
 
+// How a launch covers its tiles.
+enum Shape {
+  kPair,   // a cluster of two CTAs per 256 x 256 tile, persistent
+  kSingle, // one CTA per 128 x 128 tile, persistent
+  kSplit   // a cluster of four CTAs per 128 x 128 tile, each a quarter of K
+};
+constexpr int kSplitCtas = 4;
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b,
+                                              uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// This warp's 32 rows and 64 columns of a partial sum, to the CTAs that finish
+// them: CTA b of the cluster gets columns [32 b, 32 b + 32) of the tile from each
+// CTA's `from`, as a [128, 32] matrix whose 16-byte pieces are swizzled by row.
+__device__ __forceinline__ void send_partial(uint32_t taddr, uint8_t* ring, uint32_t from, int row,
+                                             int half) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + 32 * u, r);
+    tmem_ld_wait();
+    const uint32_t at = mapa_shared(smem_addr(ring) + from * 16384 + row * 128,
+                                    static_cast<uint32_t>(2 * half + u));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      st_cluster_v4(at + ((i ^ (row & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2],
+                    r[4 * i + 3]);
+  }
+}
+
+// The sum of the four partial sums that have arrived, in rank order.
+__device__ __forceinline__ void sum_partials(const uint8_t* ring, int row, float (&acc)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll
+  for (int from = 0; from < kSplitCtas; ++from)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(ring + from * 16384 + row * 128 +
+                                                        ((i ^ (row & 7)) << 4));
+      acc[4 * i] += f.x;
+      acc[4 * i + 1] += f.y;
+      acc[4 * i + 2] += f.z;
+      acc[4 * i + 3] += f.w;
+    }
+}
+
 // D = A B^T (B K-major) or A B (B_MN: B stored [K, N]), one tile per
-// accumulator; persistent, the epilogue of a tile runs beside the MMAs of the
-// next.  PAIR: a cluster of two CTAs per 256 x 256 tile, else one CTA per
-// 128 x 128 tile.  Both operands come from the previous launch.
-template <int MODE, bool PAIR>
+// accumulator; the epilogue of a tile runs beside the MMAs of the next.  Both
+// operands come from the previous launch.
+template <int MODE, Shape SHAPE>
 __global__ void __launch_bounds__(kThreads, 1)
     ortho_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const OrthoParams p) {
+  constexpr bool PAIR = SHAPE == kPair, SPLIT = SHAPE == kSplit;
   constexpr bool B_MN = MODE == kUpdate;
-  constexpr int kCtas = PAIR ? 2 : 1;
+  constexpr int kCtas = PAIR ? 2 : 1;  // that share a tile's rows
   constexpr int kN = PAIR ? 256 : 128;
   constexpr uint32_t kCols = 2 * kN;  // two accumulators
   constexpr uint32_t kIdesc = make_idesc(0, false, B_MN, 128 * kCtas, kN);
@@ -287,9 +365,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? uniform(cluster_ctarank()) : 0u;
-  const int unit = static_cast<int>(blockIdx.x) / kCtas;
-  const int units = static_cast<int>(gridDim.x) / kCtas;
+  constexpr int kUnit = SPLIT ? kSplitCtas : kCtas;  // CTAs per tile
+  const int unit = static_cast<int>(blockIdx.x) / kUnit;
+  const int units = static_cast<int>(gridDim.x) / kUnit;
   const int total = p.tiles * p.batch;
+  // this CTA's K blocks
+  const int quarter_k = SPLIT ? uniform(cluster_ctarank()) : 0;
+  const int kb0 = SPLIT ? p.k_blk * quarter_k / kSplitCtas : 0;
+  const int kb1 = SPLIT ? p.k_blk * (quarter_k + 1) / kSplitCtas : p.k_blk;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -334,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_of(p, t - bi * p.tiles, mi, ni);
       const int a_row = uniform((mi * kCtas + static_cast<int>(rank)) * 128);
       const int b_row = uniform(ni * kN + static_cast<int>(rank) * 128);
-      for (int kb = 0; kb < p.k_blk; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = uniform_wait(&empty[stage], phase, abort_flag, p.status))) break;
         if (rank == 0) expect_tx_elected(&full[stage], kCtas * kStageBytes);
         const uint32_t a_dst = base + stage * kStageBytes, b_dst = a_dst + kHalfStage;
@@ -384,12 +467,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!uniform_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.status)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kN;
-        for (int kb = 0; kb < p.k_blk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = uniform_wait(&full[stage], phase, abort_flag, p.status))) break;
           const Operand16 a = moved(a_op, stage * kStageBytes), b = moved(b_op, stage * kStageBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t add = (kb > 0 || k > 0) ? 1u : 0u;
+            const uint32_t add = (kb > kb0 || k > 0) ? 1u : 0u;
             const uint32_t b_off = B_MN ? 2048 * k : 32 * k;
             if (PAIR)
               mma_f16_pair_at(d, a, 32 * k, b, b_off, kIdesc, add);
@@ -425,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;  // of the tile's columns
     uint8_t* buf_s = staging + (warp - 2) * kStagingBytes;
     uint32_t it = 0;
+    bool ok = false;  // SPLIT: the partial sum is complete
     for (int t = unit; t < total; t += units, ++it) {
       const uint32_t buf = it & 1, use = it >> 1;
       const int bi = t / p.tiles;
@@ -433,9 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = (mi * kCtas + static_cast<int>(rank)) * 128 + 32 * q;
       const int col0 = ni * kN + half * (kN / 2);
       Addend<MODE> add;
-      add.fetch(p, bi, row0, col0);
+      if (!SPLIT) add.fetch(p, bi, row0, col0);
       if (!uniform_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
       tc_fence_after();
+      if (SPLIT) {  // one tile per cluster: the rest comes after the loop
+        ok = true;
+        break;
+      }
       epilogue<MODE>(p, add,
                      tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + half * (kN / 2),
                      bi, row0, col0, kN / 2, p.symmetric && mi != ni, buf_s);
@@ -448,6 +536,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&acc_empty[buf]);
       }
     }
+    if (SPLIT) {
+      // Every CTA's loads and MMAs are done (the other warps come here when they
+      // are): its ring takes the partial sums for the 32 columns it finishes.
+      const int row = 32 * q + lane;
+      __syncwarp();
+      cluster_sync();
+      if (ok)
+        send_partial(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + half * 64, smem,
+                     static_cast<uint32_t>(quarter_k), row, half);
+      const int bi = unit / p.tiles;
+      int mi, ni;
+      tile_of(p, unit - bi * p.tiles, mi, ni);
+      const int row0 = mi * 128 + 32 * q, col0 = ni * 128 + 32 * quarter_k;
+      const bool mine = ok && half == 0 && row0 < p.rows && col0 < p.cols;
+      Addend<MODE> add;
+      if (mine) add.fetch(p, bi, row0, col0);
+      __syncwarp();
+      cluster_sync();
+      if (mine) {
+        float acc[32];
+        sum_partials(smem, row, acc);
+        finish_block<MODE>(p, add, acc, bi, row0, col0, p.symmetric && mi != ni, buf_s);
+      }
+    }
+  }
+  if (SPLIT && warp < 2) {  // the two barriers of the epilogue
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
   tc_fence_before();
   __syncthreads();
@@ -701,30 +818,31 @@ int half_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t 
   return host_tensor_map(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, pitch, box, what);
 }
 
-template <int MODE, bool PAIR>
+template <int MODE, Shape SHAPE>
 cudaError_t launch_shape(const CUtensorMap& A, const CUtensorMap& B, OrthoParams p, int64_t k,
                          int sms, cudaStream_t s) {
-  const int tile = PAIR ? 256 : 128;
-  p.m_blk = (p.rows + tile - 1) / tile;
-  p.n_blk = (p.cols + tile - 1) / tile;
+  constexpr int kTileRows = SHAPE == kPair ? 256 : 128;
+  constexpr int kCluster = SHAPE == kPair ? 2 : SHAPE == kSplit ? kSplitCtas : 1;
+  p.m_blk = (p.rows + kTileRows - 1) / kTileRows;
+  p.n_blk = (p.cols + kTileRows - 1) / kTileRows;
   p.k_blk = static_cast<int32_t>((k + 63) / 64);
   p.symmetric = MODE != kUpdate;
   p.tiles = p.symmetric ? p.m_blk * (p.m_blk + 1) / 2 : p.m_blk * p.n_blk;
-  const auto kernel = ortho_gemm<MODE, PAIR>;
+  const auto kernel = ortho_gemm<MODE, SHAPE>;
   static SmemLimit limit;
   const cudaError_t e = limit.raise(kernel, kSmem);
   if (e != cudaSuccess) return e;
   const int64_t total = static_cast<int64_t>(p.tiles) * p.batch;
-  const int64_t cap = PAIR ? sms / 2 : sms;
-  const int units = static_cast<int>(total < cap ? total : cap);
+  const int64_t cap = SHAPE == kSplit ? total : sms / kCluster;  // split: one tile each
+  const int64_t units = total < cap ? total : cap;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(static_cast<unsigned>(units * (PAIR ? 2 : 1)));
+  cfg.gridDim = dim3(static_cast<unsigned>(units * kCluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   // the prologue overlaps the previous launch's tail; loads and stores wait
@@ -735,14 +853,25 @@ cudaError_t launch_shape(const CUtensorMap& A, const CUtensorMap& B, OrthoParams
   return cudaLaunchKernelEx(&cfg, kernel, A, B, p);
 }
 
-// Pairs where their 256 x 256 tiles fill at least half of the GPU's CTA pairs.
+// CTA pairs where their 256 x 256 tiles fill at least half of the GPU's pairs.
+// Else 128 x 128 tiles; those of X X^T by four CTAs each, where the GPU has that
+// many and K is at least 2048 (300 x 8000 all told 159 us against 226, 1000 x
+// 3584 187 against 199, 512 x 2048 123 against 128; but 1024 x 1024 157 against
+// 130: the exchange of the partial sums takes about 2 us).  The other products
+// have such a K only where they have more tiles.
 template <int MODE>
 cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoParams& p, int64_t k,
                         int sms, cudaStream_t s) {
-  const int64_t mb = (p.rows + 255) / 256, nb = (p.cols + 255) / 256;
-  const int64_t pair_tiles = (MODE != kUpdate ? mb * (mb + 1) / 2 : mb * nb) * p.batch;
-  return pair_tiles * 2 >= sms / 2 ? launch_shape<MODE, true>(A, B, p, k, sms, s)
-                                   : launch_shape<MODE, false>(A, B, p, k, sms, s);
+  auto tiles = [&](int64_t edge) {
+    const int64_t mb = (p.rows + edge - 1) / edge, nb = (p.cols + edge - 1) / edge;
+    return (MODE != kUpdate ? mb * (mb + 1) / 2 : mb * nb) * p.batch;
+  };
+  if (tiles(256) * 2 >= sms / 2) return launch_shape<MODE, kPair>(A, B, p, k, sms, s);
+  if constexpr (MODE == kGram) {
+    if (tiles(128) * kSplitCtas <= sms && k >= 2048)
+      return launch_shape<MODE, kSplit>(A, B, p, k, sms, s);
+  }
+  return launch_shape<MODE, kSingle>(A, B, p, k, sms, s);
 }
 
 int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps,

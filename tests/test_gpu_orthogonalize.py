@@ -148,3 +148,16 @@ def test_orthogonalize_refusals(cuda_lib):
         cuda_lib.flce_orthogonalize(G, out=torch.empty(8, 16, device=DEV))
     with pytest.raises(cuda_lib.FlceError):
         cuda_lib.flce_orthogonalize(G, coeffs=(5.0, 0.0, 0.0))
+
+
+@pytest.mark.parametrize("shape,dtype", [
+    ((260, 2300), "fp32"),        # X X^T with its long K shared out over four CTAs
+    ((2500, 129), "bf16"),
+    ((2, 100, 2049), "fp32"),
+    ((900, 2100), "bf16"),        # as many tiles as that shape takes
+])
+def test_orthogonalize_long_products(cuda_lib, shape, dtype):
+    G = _matrix("signal", shape, sum(shape), dtype)
+    got = cuda_lib.flce_orthogonalize(G, sync=True)
+    _check(got, _reference(G))
+    assert torch.equal(got, cuda_lib.flce_orthogonalize(G))
