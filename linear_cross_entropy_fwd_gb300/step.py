@@ -17,7 +17,15 @@ from . import (FLCE_FP32, FlceAttn, FlceOpts, _check, _check_out, _dtype_code, _
                load_library, make_opts, scale_convert)
 
 
+_lib = None
 _defaults = None  # a flce_opts as flce_opts_init leaves it, with sync off
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        _lib = load_library()
+    return _lib
 
 
 def _call(fn, dev, dtype, args, *, sync, workspace, info, ids32=0):
@@ -28,7 +36,8 @@ def _call(fn, dev, dtype, args, *, sync, workspace, info, ids32=0):
     o = FlceOpts.from_buffer_copy(_defaults)
     if dtype is torch.float32:
         o.dtype = FLCE_FP32
-    o.stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    index = dev.index
+    o.stream = torch._C._cuda_getCurrentRawStream(index)
     if sync:
         o.sync = 1
     if ids32:
@@ -42,7 +51,7 @@ def _call(fn, dev, dtype, args, *, sync, workspace, info, ids32=0):
         used = ctypes.c_size_t(0)
         o.status_dev = status.data_ptr()
         o.workspace_used = ctypes.pointer(used)
-    if dev.index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         st = fn(*args, ctypes.byref(o))
     else:
         with torch.cuda.device(dev):
@@ -67,7 +76,7 @@ def flce_embed_fwd(W: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
                    sync: bool = False, info: dict | None = None) -> torch.Tensor:
     """``out[i] = scale * W[ids[i]]`` in W's dtype (bf16 or fp32); rows of zeros
     where ``ids[i]`` is ``ignore_index``.  W [V, H], ids [N]; returns [N, H]."""
-    lib = load_library()
+    lib = _library()
     if W.dim() != 2 or not W.is_cuda or not W.is_contiguous():
         raise ValueError("W must be a contiguous CUDA tensor [V, H]")
     _dtype_code(W)
@@ -93,7 +102,7 @@ def flce_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, V: int | None = None, *,
     times the sum of ``dY[i]`` over the tokens with ``ids[i] == v``, added in
     ascending i.  ``accumulate=True`` adds it to ``dW`` (a weight tied to the
     head's) and touches no other row; otherwise dW is overwritten."""
-    lib = load_library()
+    lib = _library()
     if dY.dim() != 2 or not dY.is_cuda or not dY.is_contiguous():
         raise ValueError("dY must be a contiguous CUDA tensor [N, H]")
     _dtype_code(dY)
@@ -143,46 +152,39 @@ class Embedding(torch.nn.Module):
         return _EmbedFunction.apply(weight, ids, self.scale, self.ignore_index)
 
 
-def _heads_tensor(name, t, shape, device):
-    """A bf16 [T, heads, D] tensor with a contiguous last axis on ``device``."""
-    if t.dtype != torch.bfloat16:
+def _heads_tensor(name, t, T, heads, D, device):
+    """A bf16 [T, heads, D] tensor with a contiguous last axis on ``device``;
+    returns its address and its token and head strides."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bf16, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(t.shape)}")
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    token, head, last = t.stride()
+    if last != 1 and D > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
+    return t.data_ptr(), token, head
 
 
 def _attn_args(q, k, v, cu_seqlens, scale, o, lse):
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+    if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q [T, heads_q, D], k and v [T, heads_kv, D]")
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     dev = q.device
-    _heads_tensor("q", q, (T, Hq, D), dev)
-    _heads_tensor("k", k, (T, Hkv, D), dev)
-    _heads_tensor("v", v, (T, Hkv, D), dev)
-    _heads_tensor("o", o, (T, Hq, D), dev)
-    _check_out(lse, (Hq, T), torch.float32, dev, "lse")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must hold one offset more than there are sequences")
-    _check_out(cu_seqlens, tuple(cu_seqlens.shape), torch.int32, dev, "cu_seqlens")
-    a = FlceAttn()
-    a.T, a.batch, a.cu_seqlens = T, cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
-    a.heads_q, a.heads_kv, a.head_dim = Hq, Hkv, D
-    a.scale = D ** -0.5 if scale is None else float(scale)
-    _put(a, q=q, k=k, v=v, o=o)
-    a.lse = lse.data_ptr()
-    return a
-
-
-def _put(a, **tensors):
-    for name, t in tensors.items():
-        setattr(a, name, t.data_ptr())
-        setattr(a, name + "_token", t.stride(0))
-        setattr(a, name + "_head", t.stride(1))
+    for name, t, shape, dtype in (("lse", lse, (Hq, T), torch.float32),
+                                  ("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32)):
+        if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+            _check_out(t, shape, dtype, dev, name)
+    # in the order of the structure's fields
+    return FlceAttn(T, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr(), Hq, Hkv, D,
+                    D ** -0.5 if scale is None else float(scale),
+                    *_heads_tensor("q", q, T, Hq, D, dev), *_heads_tensor("k", k, T, Hkv, D, dev),
+                    *_heads_tensor("v", v, T, Hkv, D, dev), *_heads_tensor("o", o, T, Hq, D, dev),
+                    lse.data_ptr())
 
 
 def flce_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
@@ -195,15 +197,17 @@ def flce_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     axis (slices of one projection's output will do); ``cu_seqlens`` int32
     [sequences + 1] on the device.  ``scale`` defaults to D ** -0.5.  o is
     [T, heads_q, D], lse fp32 [heads_q, T]."""
-    lib = load_library()
+    lib = _library()
     if q.dim() != 3:
         raise ValueError("q [T, heads_q, D], k and v [T, heads_kv, D]")
+    T, Hq, D = q.shape
+    dev = q.device
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
     a = _attn_args(q, k, v, cu_seqlens, scale, out, lse)
-    _call(lib.flce_attn_fwd, q.device, q.dtype, (ctypes.byref(a),), sync=sync,
+    _call(lib.flce_attn_fwd, dev, q.dtype, (ctypes.byref(a),), sync=sync,
           workspace=workspace, info=info)
     return out, lse
 
@@ -216,14 +220,16 @@ def flce_attn_bwd(dO: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
                   info: dict | None = None):
     """Gradients of ``flce_attn_fwd`` at its inputs and outputs; returns
     (dq, dk, dv) in bf16, dk and dv summed over the query heads they serve."""
-    lib = load_library()
+    lib = _library()
     a = _attn_args(q, k, v, cu_seqlens, scale, o, lse)
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
     dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
     dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
     for name, t, like in (("dO", dO, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _heads_tensor(name, t, like.shape, q.device)
-    _put(a, dO=dO, dq=dq, dk=dk, dv=dv)
+        at, token, head = _heads_tensor(name, t, *like.shape, q.device)
+        setattr(a, name, at)
+        setattr(a, name + "_token", token)
+        setattr(a, name + "_head", head)
     _call(lib.flce_attn_bwd, q.device, q.dtype, (ctypes.byref(a),), sync=sync,
           workspace=workspace, info=info)
     return dq, dk, dv
@@ -272,7 +278,7 @@ def flce_orthogonalize(G: torch.Tensor, *, steps: int = 5,
     """Newton-Schulz orthogonalisation of each matrix of G [..., rows, cols]
     (bf16 or fp32): ``X = G / (|G|_F + eps)``, then ``steps`` times
     ``X = a X + (b A + c A A) X`` with ``A = X X^T``.  Returns X in bf16."""
-    lib = load_library()
+    lib = _library()
     if G.dim() < 2 or not G.is_cuda or not G.is_contiguous():
         raise ValueError("G must be a contiguous CUDA tensor [..., rows, cols]")
     _dtype_code(G)
