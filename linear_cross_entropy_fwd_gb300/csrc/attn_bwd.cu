@@ -199,6 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kvh = static_cast<int>(blockIdx.x) / split % p.Hkv;
   const int idx = static_cast<int>(blockIdx.x) / split / p.Hkv;
   grid_dependency_wait();  // the tile list and delta
+  // dq needs nothing of this launch: its CTAs may take the SMs that this one's
+  // last CTAs leave idle
+  grid_launch_dependents();
   if (idx >= *p.n_tiles) return;
   AttnTile t = p.tiles[idx];
   t.start = uniform(t.start);
@@ -476,7 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t TB = S::kTileBytes;
   const int h = static_cast<int>(blockIdx.x % p.Hq);
   const int idx = static_cast<int>(blockIdx.x / p.Hq);
-  if (idx >= *p.n_tiles) return;
+  // The launch before (dkdv) started when the tile list and delta were complete,
+  // so they are; that launch itself need only be complete when this one is.
+  if (idx >= *p.n_tiles) {
+    grid_dependency_wait();
+    return;
+  }
   AttnTile t = p.tiles[idx];
   t.start = uniform(t.start);
   t.tile = uniform(t.tile);
@@ -636,13 +644,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tS, kTmemCols);
   }
+  grid_dependency_wait();
 }
 
 template <class KernelT, class... Extra>
 cudaError_t launch(KernelT kernel, SmemLimit& limit, uint32_t smem, unsigned blocks,
-                   unsigned cluster, bool overlap, cudaStream_t s, const CUtensorMap& q,
-                   const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
-                   const AttnParams& p, Extra... extra) {
+                   unsigned cluster, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k,
+                   const CUtensorMap& v, const CUtensorMap& dO, const AttnParams& p,
+                   Extra... extra) {
   const cudaError_t e = limit.raise(kernel, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -658,7 +667,7 @@ cudaError_t launch(KernelT kernel, SmemLimit& limit, uint32_t smem, unsigned blo
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, q, k, v, dO, p, extra...);
 }
 
@@ -668,8 +677,8 @@ cudaError_t launch_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtens
   static SmemLimit limit;
   const unsigned c = static_cast<unsigned>(split);
   const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hkv) * c;
-  return launch(attn_dkdv_kernel<DP>, limit, BwdShape<DP>::kSmemDkDv, blocks, c, true, s, q, k, v,
-                dO, p, split);
+  return launch(attn_dkdv_kernel<DP>, limit, BwdShape<DP>::kSmemDkDv, blocks, c, s, q, k, v, dO, p,
+                split);
 }
 
 template <int DP>
@@ -677,8 +686,7 @@ cudaError_t launch_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensor
                       const CUtensorMap& dO, const AttnParams& p, cudaStream_t s) {
   static SmemLimit limit;
   const unsigned blocks = static_cast<unsigned>(p.max_tiles) * static_cast<unsigned>(p.Hq);
-  return launch(attn_dq_kernel<DP>, limit, BwdShape<DP>::kSmemDq, blocks, 1, false, s, q, k, v, dO,
-                p);
+  return launch(attn_dq_kernel<DP>, limit, BwdShape<DP>::kSmemDq, blocks, 1, s, q, k, v, dO, p);
 }
 
 // CTAs per key tile and kv head: the fewest that give every SM one, among the

@@ -118,6 +118,7 @@ __device__ void make_delta(const AttnParams& p, int64_t me, int64_t threads) {
 
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const AttnParams p) {
+  grid_launch_dependents();  // the next launch's setup may overlap this one
   const bool ok = offsets_ok(p);
   if (blockIdx.x == 0) {
     make_tiles(p, ok);
