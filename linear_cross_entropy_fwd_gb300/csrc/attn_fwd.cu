@@ -15,7 +15,10 @@
 // one load of K_j and V_j: the operands' way through shared memory (TMA in, MMA
 // out) is 256 KB per two tile products at 128 bytes a clock, just what the MMAs
 // take.  Measured at 8192 tokens, 32 heads of 128: two CTAs per SM with a tile
-// each 210 us, an MMA warp per tile 196 us, this 171 us.
+// each 210 us; an MMA warp per tile 196 us and this order 171 us, before the
+// softmax took its present form (150 us); the MMA warp serving whichever tile is
+// ready, so that one may run ahead into the next unit, 172 us (it polls three
+// barriers per product).
 //
 // The maximum that P and O are relative to follows the true one only when it
 // has grown by more than 2^8: until then O needs no rescaling, and P <= 2^8,
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);  // both query tiles are done with it
+      mbar_init(&kv_empty[i], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
