@@ -20,11 +20,11 @@
 // twice.  That makes the flops of a step k^2 n + k^3 + 2 k^2 n.
 //
 // Launches: norm, split (fp32 and fp16 X), then three GEMMs per step, in three
-// shapes with 32 KB stages of A and B, six deep: CTA pairs on 256 x 256 tiles,
+// shapes with 32 KB stages of A and B: CTA pairs on 256 x 256 tiles,
 // and for small matrices 128 x 128 tiles by single CTAs or by clusters of four
 // that share out K.  (All steps in one cooperative launch with a barrier over
 // the grid was built and took longer: 154 against 112 us for eight 256 x 1024
-// matrices.  Between two products the barrier, the fences before it and the first
+// matrices (106 now).  Between two products the barrier, the fences before it and the first
 // loads after it took 4 to 5 us, and the next launch no more.)
 #include <cmath>
 
@@ -36,15 +36,37 @@
 namespace flce {
 namespace {
 
-constexpr float kHold = 4096.f;              // stored value / value
+constexpr float kHold = 4096.f;       // stored value / value
 constexpr float kUnhold = 1.f / 4096.f;
-constexpr int kStages = 6;
-constexpr uint32_t kHalfStage = 128 * 128;   // 128 rows x 64 fp16 (or two 64 x 64 boxes)
-constexpr uint32_t kStageBytes = 2 * kHalfStage;
-constexpr int kStagingBytes = 4096;          // one 32 x 32 fp32 block per epilogue warp
-constexpr int kEpiWarps = 8;                 // two per quarter of the TMEM lanes
-constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStagingBytes + 256;
-constexpr int kThreads = 64 + 32 * kEpiWarps;  // TMA, MMA, epilogue
+constexpr uint32_t kBox = 64 * 128;   // 64 rows x 64 fp16
+constexpr int kStagingBytes = 4096;   // one 32 x 32 fp32 block per epilogue warp
+
+// How a launch covers its tiles.
+enum Shape {
+  kPair,    // a cluster of two CTAs per 256 x 256 tile, persistent
+  kSingle,  // one CTA per 128 x 128 tile, persistent
+  kSplit    // a cluster of four CTAs per 128 x 128 tile, each a quarter of K
+};
+constexpr int kSplitCtas = 4;
+
+template <Shape SHAPE>
+struct Config {
+  static constexpr int kCtas = SHAPE == kPair ? 2 : 1;  // that share a tile's rows
+  static constexpr int kCluster = SHAPE == kSplit ? kSplitCtas : kCtas;
+  static constexpr int kM = 128 * kCtas, kN = SHAPE == kPair ? 256 : 128;  // tile
+  // 16 where a tile's time is its latency (256 x 1024 all told 98.9 -> 96.3 us, 768 x
+  // 768 115.8 -> 111.7); with the larger tiles the fifth and sixth stage of the ring are
+  // worth more (2048 x 2048 221 us, 237 with 16 warps and five stages)
+  static constexpr int kEpiWarps = SHAPE == kSingle ? 16 : 8;
+  static constexpr int kParts = kEpiWarps / 4;  // warps that share a row of the tile
+  static constexpr int kStages = SHAPE == kSingle ? 5 : 6;
+  static constexpr uint32_t kABytes = 128 * 128;  // 128 rows x 64 fp16
+  static constexpr uint32_t kStageBytes = 2 * kABytes;  // A and B
+  static constexpr uint32_t kSmem =
+      1024 + kStages * kStageBytes + kEpiWarps * kStagingBytes + 256;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;  // TMA, MMA, epilogue
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
 
 enum Mode { kGram, kPoly, kUpdate };
 
@@ -86,28 +108,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 rows (one per lane) x 32 columns to memory through shared memory, so
-// that each row goes out in whole 16-byte pieces next to one another.
-__device__ __forceinline__ void store_f32(uint8_t* buf, const float (&v)[32], float* dst,
-                                          int64_t ld, int rows, int cols) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t base = smem_addr(buf);
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    st_shared_v4(base + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
-                 __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-                 __float_as_uint(v[4 * c + 3]));
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3), c = lane & 7;
-    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
-    if (r < rows && 4 * c < cols) *reinterpret_cast<uint4*>(dst + r * ld + 4 * c) = w;
-  }
-  __syncwarp();
-}
-
-// The same for 16-bit values, already packed in pairs.
+// 32 rows (one per lane) x 32 columns of 16-bit values, packed in pairs, to
+// memory through shared memory, so that each row goes out in whole 16-byte pieces
+// next to one another.
 __device__ __forceinline__ void store_16(uint8_t* buf, const uint32_t (&v)[16], uint16_t* dst,
                                          int64_t ld, int rows, int cols, bool vec) {
   const int lane = threadIdx.x & 31;
@@ -220,6 +223,56 @@ struct Addend {
   }
 };
 
+// The update's block, X and its fp16 copy (or the bf16 result, in whole vectors):
+// the product goes through shared memory into the layout that the addend was
+// fetched in (lane l: columns 4 (l % 8) .., rows l / 8 + 4 i), which is also the one
+// to store in.  Turning the addend into rows and both results back took 2.5 times
+// the shared memory accesses, and an update of 2048 x 2048 20.7 us instead of 19.0.
+// What is left is bound by L2: 40 MB in and out in the 6.5 us of the epilogue.
+__device__ __forceinline__ void finish_in_pieces(const OrthoParams& p, const Addend<kUpdate>& add,
+                                                 const float (&acc)[32], int bi, int row0, int c0,
+                                                 uint8_t* buf) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  const uint32_t base = smem_addr(buf);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    st_shared_v4(base + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(acc[4 * k]),
+                 __float_as_uint(acc[4 * k + 1]), __float_as_uint(acc[4 * k + 2]),
+                 __float_as_uint(acc[4 * k + 3]));
+  __syncwarp();
+  const bool in = c0 + 4 * c < p.cols;
+  const int64_t r0 = row0 + (lane >> 3), at = c0 + 4 * c;
+  float* x = p.x + bi * p.x_stride + r0 * p.ldx + at;
+  uint16_t* h = p.result ? p.result + static_cast<int64_t>(bi) * p.rows * p.cols + r0 * p.cols + at
+                         : reinterpret_cast<uint16_t*>(p.out) + bi * p.stride + r0 * p.ld + at;
+  const int64_t h_ld = p.result ? p.cols : p.ld;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    const float4 s = *reinterpret_cast<const float4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    constexpr float kU = kUnhold * kUnhold;
+    float4 v;
+    v.x = fmaf(s.x, kU, p.a * __uint_as_float(add.v[i].x));
+    v.y = fmaf(s.y, kU, p.a * __uint_as_float(add.v[i].y));
+    v.z = fmaf(s.z, kU, p.a * __uint_as_float(add.v[i].z));
+    v.w = fmaf(s.w, kU, p.a * __uint_as_float(add.v[i].w));
+    if (!in || row0 + r >= p.rows) continue;
+    uint2 w;
+    if (p.result) {
+      w = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    } else {
+      *reinterpret_cast<float4*>(x + 4 * i * p.ldx) = v;
+      w = make_uint2(pack_half2(v.x * kHold, v.y * kHold), pack_half2(v.z * kHold, v.w * kHold));
+    }
+    *reinterpret_cast<uint2*>(h + 4 * i * h_ld) = w;
+  }
+  __syncwarp();
+}
+
+template <int MODE>
+__device__ __forceinline__ void finish_in_pieces(const OrthoParams&, const Addend<MODE>&,
+                                                 const float (&)[32], int, int, int, uint8_t*) {}
+
 // A 32 x 32 block of an accumulator (row row0 + lane, columns c0 ..), turned into
 // the launch's result and stored.  `acc` holds 4096^2 times the product.
 template <int MODE>
@@ -227,6 +280,10 @@ __device__ __forceinline__ void finish_block(const OrthoParams& p, const Addend<
                                              const float (&acc)[32], int bi, int row0, int c0,
                                              bool mirror, uint8_t* buf) {
   const int rows = p.rows - row0, cols = p.cols - c0;
+  if (MODE == kUpdate && !(p.result && (p.transposed || !p.result_vec))) {
+    finish_in_pieces(p, add, acc, bi, row0, c0, buf);
+    return;
+  }
   float v[32];
   add.to_rows(buf, v);
 #pragma unroll
@@ -239,7 +296,7 @@ __device__ __forceinline__ void finish_block(const OrthoParams& p, const Addend<
       v[i] = fmaf(acc[i], kUnhold * kUnhold, p.a * v[i]);
   }
   uint32_t w[16];
-  if (MODE == kUpdate && p.result) {
+  if (MODE == kUpdate) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     uint16_t* res = p.result + static_cast<int64_t>(bi) * p.rows * p.cols;
@@ -247,14 +304,8 @@ __device__ __forceinline__ void finish_block(const OrthoParams& p, const Addend<
       store_16_transposed(buf, w, res + static_cast<int64_t>(c0) * p.rows + row0, p.rows, rows,
                           cols, p.result_vec != 0);
     else
-      store_16(buf, w, res + static_cast<int64_t>(row0) * p.cols + c0, p.cols, rows, cols,
-               p.result_vec != 0);
+      store_16(buf, w, res + static_cast<int64_t>(row0) * p.cols + c0, p.cols, rows, cols, false);
     return;
-  }
-  if (MODE == kUpdate) {
-    store_f32(buf, v, p.x + bi * p.x_stride + row0 * p.ldx + c0, p.ldx, rows, cols);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= kHold;
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
@@ -283,14 +334,6 @@ __device__ __forceinline__ void epilogue(const OrthoParams& p, Addend<MODE>& add
     finish_block<MODE>(p, cur, reinterpret_cast<const float(&)[32]>(r), bi, row0, c0, mirror, buf);
   }
 }
-
-// How a launch covers its tiles.
-enum Shape {
-  kPair,   // a cluster of two CTAs per 256 x 256 tile, persistent
-  kSingle, // one CTA per 128 x 128 tile, persistent
-  kSplit   // a cluster of four CTAs per 128 x 128 tile, each a quarter of K
-};
-constexpr int kSplitCtas = 4;
 
 __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b,
                                               uint32_t c, uint32_t d) {
@@ -339,22 +382,22 @@ __device__ __forceinline__ void sum_partials(const uint8_t* ring, int row, float
 // accumulator; the epilogue of a tile runs beside the MMAs of the next.  Both
 // operands come from the previous launch.
 template <int MODE, Shape SHAPE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Config<SHAPE>::kThreads, 1)
     ortho_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const OrthoParams p) {
-  constexpr bool PAIR = SHAPE == kPair, SPLIT = SHAPE == kSplit;
+  using C = Config<SHAPE>;
+  constexpr bool PAIR = C::kCtas == 2, SPLIT = SHAPE == kSplit;
   constexpr bool B_MN = MODE == kUpdate;
-  constexpr int kCtas = PAIR ? 2 : 1;  // that share a tile's rows
-  constexpr int kN = PAIR ? 256 : 128;
+  constexpr int kCtas = C::kCtas, kN = C::kN, kStages = C::kStages, kParts = C::kParts;
+  constexpr uint32_t kStageBytes = C::kStageBytes;
   constexpr uint32_t kCols = 2 * kN;  // two accumulators
-  constexpr uint32_t kIdesc = make_idesc(0, false, B_MN, 128 * kCtas, kN);
-  constexpr uint32_t kBox = 64 * 128;  // one MN-major box: 64 K rows x 64 columns
+  constexpr uint32_t kIdesc = make_idesc(0, false, B_MN, C::kM, kN);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + kStages * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStagingBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::kEpiWarps * kStagingBytes);
   uint64_t* full = bars;                  // [kStages] (the even CTA's are the ones used)
   uint64_t* empty = bars + kStages;       // [kStages]
   uint64_t* acc_full = empty + kStages;   // [2]
@@ -365,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? uniform(cluster_ctarank()) : 0u;
-  constexpr int kUnit = SPLIT ? kSplitCtas : kCtas;  // CTAs per tile
+  constexpr int kUnit = C::kCluster;  // CTAs per tile
   const int unit = static_cast<int>(blockIdx.x) / kUnit;
   const int units = static_cast<int>(gridDim.x) / kUnit;
   const int total = p.tiles * p.batch;
@@ -381,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kEpiWarps * kCtas);
+      mbar_init(&acc_empty[b], C::kEpiWarps * kCtas);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -420,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = uniform_wait(&empty[stage], phase, abort_flag, p.status))) break;
         if (rank == 0) expect_tx_elected(&full[stage], kCtas * kStageBytes);
-        const uint32_t a_dst = base + stage * kStageBytes, b_dst = a_dst + kHalfStage;
+        const uint32_t a_dst = base + stage * kStageBytes, b_dst = a_dst + C::kABytes;
         const int k = 64 * kb;
         if (PAIR) {
           const uint32_t fb = full0 + stage * 8;
@@ -461,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, it = 0;
       bool ok = true;
-      const Operand16 a_op(smem_addr(smem), 0), b_op(smem_addr(smem) + kHalfStage, B_MN ? kBox : 0);
+      const Operand16 a_op(smem_addr(smem), 0), b_op(smem_addr(smem) + C::kABytes, B_MN ? kBox : 0);
       for (int t = unit; ok && t < total; t += units, ++it) {
         const uint32_t buf = it & 1, use = it >> 1;
         if (!uniform_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.status)) break;
@@ -505,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_wait();
     if (warp == 2 && lane == 0) grid_launch_dependents();
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;  // of the tile's columns
+    const int part = (warp - 2) >> 2;  // of the tile's columns
     uint8_t* buf_s = staging + (warp - 2) * kStagingBytes;
     uint32_t it = 0;
     bool ok = false;  // SPLIT: the partial sum is complete
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mi, ni;
       tile_of(p, t - bi * p.tiles, mi, ni);
       const int row0 = (mi * kCtas + static_cast<int>(rank)) * 128 + 32 * q;
-      const int col0 = ni * kN + half * (kN / 2);
+      const int col0 = ni * kN + part * (kN / kParts);
       Addend<MODE> add;
       if (!SPLIT) add.fetch(p, bi, row0, col0);
       if (!uniform_wait(&acc_full[buf], use & 1, abort_flag, p.status)) break;
@@ -525,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       epilogue<MODE>(p, add,
-                     tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + half * (kN / 2),
-                     bi, row0, col0, kN / 2, p.symmetric && mi != ni, buf_s);
+                     tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + part * (kN / kParts),
+                     bi, row0, col0, kN / kParts, p.symmetric && mi != ni, buf_s);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -543,13 +586,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       cluster_sync();
       if (ok)
-        send_partial(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + half * 64, smem,
-                     static_cast<uint32_t>(quarter_k), row, half);
+        send_partial(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + part * 64, smem,
+                     static_cast<uint32_t>(quarter_k), row, part);
       const int bi = unit / p.tiles;
       int mi, ni;
       tile_of(p, unit - bi * p.tiles, mi, ni);
       const int row0 = mi * 128 + 32 * q, col0 = ni * 128 + 32 * quarter_k;
-      const bool mine = ok && half == 0 && row0 < p.rows && col0 < p.cols;
+      const bool mine = ok && part == 0 && row0 < p.rows && col0 < p.cols;
       Addend<MODE> add;
       if (mine) add.fetch(p, bi, row0, col0);
       __syncwarp();
@@ -821,28 +864,27 @@ int half_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t 
 template <int MODE, Shape SHAPE>
 cudaError_t launch_shape(const CUtensorMap& A, const CUtensorMap& B, OrthoParams p, int64_t k,
                          int sms, cudaStream_t s) {
-  constexpr int kTileRows = SHAPE == kPair ? 256 : 128;
-  constexpr int kCluster = SHAPE == kPair ? 2 : SHAPE == kSplit ? kSplitCtas : 1;
-  p.m_blk = (p.rows + kTileRows - 1) / kTileRows;
-  p.n_blk = (p.cols + kTileRows - 1) / kTileRows;
+  using C = Config<SHAPE>;
+  p.m_blk = (p.rows + C::kM - 1) / C::kM;
+  p.n_blk = (p.cols + C::kN - 1) / C::kN;
   p.k_blk = static_cast<int32_t>((k + 63) / 64);
   p.symmetric = MODE != kUpdate;
   p.tiles = p.symmetric ? p.m_blk * (p.m_blk + 1) / 2 : p.m_blk * p.n_blk;
   const auto kernel = ortho_gemm<MODE, SHAPE>;
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(kernel, kSmem);
+  const cudaError_t e = limit.raise(kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t total = static_cast<int64_t>(p.tiles) * p.batch;
-  const int64_t cap = SHAPE == kSplit ? total : sms / kCluster;  // split: one tile each
+  const int64_t cap = SHAPE == kSplit ? total : sms / C::kCluster;  // split: one tile each
   const int64_t units = total < cap ? total : cap;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(static_cast<unsigned>(units * kCluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.gridDim = dim3(static_cast<unsigned>(units * C::kCluster));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = C::kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   // the prologue overlaps the previous launch's tail; loads and stores wait
