@@ -16,15 +16,16 @@
 //               64 MB or more are cleared meanwhile, one CTA up to 4096 tokens:
 //               the clearing takes as long, and runs on all other SMs (128 MB
 //               in 19 us, against 23 beside a cluster).  The other CTAs of the
-//               launch clear dW meanwhile when it is overwritten; when it is
-//               added to, they fetch the tokens' rows of it into L2 (8192
-//               tokens of 4096 bf16 on a tied weight: 60 -> 56 us; fetching dY
-//               instead changes nothing).
+//               launch clear dW meanwhile when it is overwritten (a large one
+//               in part: see kClearSplit); when it is added to, they fetch the
+//               tokens' rows of it into L2 (8192 tokens of 4096 bf16 on a tied
+//               weight: 60 -> 56 us; fetching dY instead changes nothing).
 //   2  sum      a run of one id is cut into pieces of at most L entries; CTA c
 //               adds up the pieces that begin in entries [c*C, (c+1)*C) of the
 //               sorted order.  A run of one piece goes straight to dW; the
 //               pieces of a longer one leave fp32 partial rows, and the run
-//               goes on a list.
+//               goes on a list.  Further CTAs clear what the sort had no time
+//               for, except the rows that have tokens.
 //   3  join     adds the partial rows of each run on the list, in order.
 #include "host_util.h"
 #include "sm103.cuh"
@@ -121,6 +122,13 @@ constexpr int kMaxDigits = 1 << kMaxDigitBits;
 constexpr int kOneCtaTokens = 4096;  // that fit
 constexpr int kOneCtaFaster = 2048;
 constexpr int64_t kClearHides = int64_t{64} << 20;
+// A dW of this many bytes and more is cleared in two parts: what the sort has time
+// for beside it (5.5 MB per us), the rest beside the sums, there without the rows that
+// have tokens.  8192 tokens, 262 MB: 68 -> 60 us; 2.1 GB: 342 -> 310 (8 tokens: 332 ->
+// 284); but 3001 tokens, 128 MB: 35.5 -> 38.4, the sums of which it slows down.
+constexpr int64_t kClearSplit = int64_t{192} << 20;
+constexpr int64_t kClearBase = int64_t{40} << 20;
+constexpr int64_t kClearPerToken = 3 << 10;
 constexpr int64_t kFetchMost = int64_t{128} << 20;  // bytes of rows, with repetitions
 constexpr int64_t kFetchPiece = 1024;
 constexpr int kHistBytes = (kSortWarps * kMaxDigits + 2 * kMaxDigits + 32) * 4;
@@ -338,6 +346,8 @@ constexpr int kAhead = 8;         // rows in flight
 constexpr int kMaxChunk = 64;
 constexpr int kMinPiece = 32;
 constexpr int kMaxPiece = kMaxChunk;  // pieces are at least as long as chunks
+constexpr int64_t kClearUnit = int64_t{256} << 10;  // bytes that a CTA clears, at least one row
+constexpr int kMaxClearRows = 1024;
 
 struct SumParams {
   const void* dY;
@@ -354,7 +364,52 @@ struct SumParams {
   int32_t chunks;
   int32_t accumulate;
   float scale;
+  int64_t clear_from;        // rows [clear_from, V) that no token has are cleared here,
+  int32_t clear_rows;        // so many rows per CTA
 };
+
+// The first of the sorted entries [lo, hi) whose key is not less than k, or hi
+// (the whole CTA): every round probes one place per thread.
+__device__ __forceinline__ int64_t first_not_less(const uint32_t* key, int64_t lo, int64_t hi,
+                                                  uint32_t k) {
+  const int threads = static_cast<int>(blockDim.x);
+  while (lo < hi) {
+    const int64_t step = (hi - lo + threads - 1) / threads;
+    const int64_t i = lo + threadIdx.x * step;
+    const int less = __syncthreads_count(i < hi && __ldcg(key + i) < k);
+    const int64_t top = lo + less * step;  // the first probe that is not less, or past them
+    if (top < hi) hi = top;
+    if (less > 0) lo = lo + (less - 1) * step + 1;
+  }
+  return hi;
+}
+
+// Clears those of a unit's rows that no token has.
+__device__ void clear_unit(const SumParams& p, int64_t unit) {
+  __shared__ uint32_t s_has[kMaxClearRows / 32];  // rows with tokens
+  const int threads = static_cast<int>(blockDim.x);
+  const int64_t n = p.counts[0];
+  const int64_t a = p.clear_from + unit * p.clear_rows;
+  if (a >= p.V) return;
+  const int64_t b = a + p.clear_rows < p.V ? a + p.clear_rows : p.V;
+  for (int i = threadIdx.x; i < kMaxClearRows / 32; i += threads) s_has[i] = 0u;
+  int64_t i = first_not_less(p.key, 0, n, static_cast<uint32_t>(a)) + threadIdx.x;
+  __syncthreads();
+  for (;; i += threads) {
+    const uint32_t k = i < n ? __ldcg(p.key + i) : 0xffffffffu;
+    const bool in = k < static_cast<uint32_t>(b);  // b <= V < 2^31
+    if (in) atomicOr(&s_has[(k - a) >> 5], 1u << ((k - a) & 31));
+    if (!__syncthreads_or(in)) break;
+  }
+  const uint32_t h4 = static_cast<uint32_t>(p.H / 4);
+  const uint32_t vecs = static_cast<uint32_t>(b - a) * h4;  // kClearUnit / 16, or one row
+  float4* dst = reinterpret_cast<float4*>(p.dW + a * p.H);
+#pragma unroll 4
+  for (uint32_t v = threadIdx.x; v < vecs; v += threads) {
+    const uint32_t r = v / h4;
+    if (!((s_has[r >> 5] >> (r & 31)) & 1u)) __stcs(dst + v, make_float4(0.f, 0.f, 0.f, 0.f));
+  }
+}
 
 template <int ELT>
 struct Acc {  // the elements of one 16-byte vector in fp32
@@ -405,11 +460,16 @@ template <int ELT>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
+  const int64_t chunk = blockIdx.x;
+  if (chunk >= p.chunks) {
+    clear_unit(p, (chunk - p.chunks) * gridDim.y + blockIdx.y);
+    return;
+  }
   __shared__ uint32_t s_key[kMaxChunk + kMaxPiece + 2];  // entry i0 - 1 + t at t
   __shared__ uint32_t s_pos[kMaxChunk + kMaxPiece];
   const int64_t n = p.counts[0];
   const int C = p.chunk, L = p.piece, threads = static_cast<int>(blockDim.x);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * C;
+  const int64_t i0 = chunk * C;
   if (i0 >= n) return;
   const int cnt = static_cast<int>(n - i0 < C + L ? n - i0 : C + L);  // entries in reach
   constexpr uint32_t kNone = 0xffffffffu;  // no row has this id (ids < 2^31)
@@ -423,19 +483,9 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams 
   int j = 0;            // first entry of the next piece
   bool first = true;    // it begins its run
   if (key[-1] == key[0]) {
-    // the run began earlier: how much earlier decides where its pieces begin.
-    // Its first entry is in [b0, b1]; every round probes one place per thread between.
-    int64_t b0 = 0, b1 = i0 - 1;
-    while (b0 < b1) {
-      const int64_t step = (b1 - b0 + threads - 1) / threads;
-      const int64_t i = b0 + threadIdx.x * step;
-      const int less = __syncthreads_count(i < b1 && __ldcg(p.key + i) < key[0]);
-      const int64_t top = b0 + less * step;  // the first probe that is not less, or past them
-      if (top < b1) b1 = top;
-      if (less > 0) b0 = b0 + (less - 1) * step + 1;
-    }
-    const int64_t back = i0 - b1;
+    // the run began earlier: how much earlier decides where its pieces begin
     const uint32_t k0 = key[0];
+    const int64_t back = i0 - first_not_less(p.key, 0, i0 - 1, k0);
     const int next = static_cast<int>((L - back % L) % L);
     while (j < next && j < cnt && key[j] == k0) ++j;
     first = !(j < cnt && key[j] == k0);
@@ -465,7 +515,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumParams 
         p.runs[atomicAdd(p.counts + 1, 1u)] =  // in any order: the runs are disjoint
             make_uint2(static_cast<uint32_t>(i0 + from), k);
       if (!first || goes_on) {
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (goes_on ? 1 : 0);
+        const int64_t slot = 2 * chunk + (goes_on ? 1 : 0);
         acc.put(p.partial + slot * p.H + static_cast<int64_t>(c) * kN);
       } else {
         float* dst = p.dW + static_cast<int64_t>(k) * p.H + static_cast<int64_t>(c) * kN;
@@ -648,12 +698,16 @@ cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
 }
 
 int run_bwd(const SortParams& sort, const SumParams& sum, int elt, int sms, cudaStream_t s) {
-  FLCE_TRY(one_cta_sorts(sort.N, sort.clear ? sort.clear_vecs * 16 : 0)
-               ? launch_sort<1>(sort, sms, s)
-               : launch_sort<kSortCtas>(sort, sms, s));
+  FLCE_TRY(one_cta_sorts(sort.N, sort.clear_vecs * 16) ? launch_sort<1>(sort, sms, s)
+                                                       : launch_sort<kSortCtas>(sort, sms, s));
   const unsigned slices = (sum.nv + kSumThreads - 1) / kSumThreads;
   const int threads = static_cast<int>(((sum.nv + slices - 1) / slices + 31) / 32 * 32);
-  const dim3 g(static_cast<unsigned>(sum.chunks), slices);
+  int64_t x = sum.chunks;
+  if (sum.clear_from < sum.V) {
+    const int64_t units = (sum.V - sum.clear_from + sum.clear_rows - 1) / sum.clear_rows;
+    x += (units + slices - 1) / slices;
+  }
+  const dim3 g(static_cast<unsigned>(x), slices);
   FLCE_TRY(elt == 2 ? launch_after(embed_sum_kernel<2>, g, threads, sum, s)
                     : launch_after(embed_sum_kernel<4>, g, threads, sum, s));
   if (sort.N > sum.piece)  // else no run is longer than a piece
@@ -731,7 +785,10 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   for (int i = 0; i < 2; ++i) sp.pair[i] = reinterpret_cast<uint2*>(w + b.pair[i]);
   sp.counts = reinterpret_cast<uint32_t*>(w + b.counts);
   sp.clear = accumulate ? nullptr : reinterpret_cast<float4*>(dW);
-  sp.clear_vecs = accumulate ? 0 : V * H / 4;
+  const int64_t beside_sort = (kClearBase + N * kClearPerToken) / (H * 4);
+  const int64_t clear_first =
+      accumulate ? 0 : V * H * 4 < kClearSplit || V < beside_sort ? V : beside_sort;
+  sp.clear_vecs = clear_first * H / 4;
   sp.fetch = reinterpret_cast<const uint8_t*>(dW);
   sp.fetch_row = H * 4;
   const int64_t fetch = kFetchMost / sp.fetch_row;
@@ -755,6 +812,9 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   sm.chunks = b.chunks;
   sm.accumulate = accumulate != 0 ? 1 : 0;
   sm.scale = scale;
+  sm.clear_from = accumulate ? V : clear_first;
+  const int64_t rows = kClearUnit / (H * 4);
+  sm.clear_rows = static_cast<int32_t>(rows < 1 ? 1 : rows > kMaxClearRows ? kMaxClearRows : rows);
   return call.end(run_bwd(sp, sm, elt, sms, call.stream));
 }
 

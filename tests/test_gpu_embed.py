@@ -204,3 +204,32 @@ def test_tied_weight_accumulates_on_the_head(cuda_lib):
     head = dW.clone()
     cuda_lib.flce_embed_bwd(dX, t, dW=dW, accumulate=True)
     _check_bwd(dW, dX, t, 500, 1.0, head)
+
+
+@pytest.mark.parametrize("N,H,V,dtype,kind", [
+    (1, 1024, 50003, "bf16", "two"),
+    (9, 1024, 50003, "bf16", "none"),
+    (700, 1000, 50521, "fp32", "skewed"),
+    (3001, 1024, 50003, "bf16", "uniform"),
+    (9001, 1024, 50003, "bf16", "skewed"),
+    (2500, 8, 6300001, "bf16", "uniform"),      # many rows per clearing CTA
+    (33, 65544, 801, "fp32", "uniform"),        # less than one
+])
+def test_embed_bwd_large_tables(cuda_lib, N, H, V, dtype, kind):
+    """dW of more than 192 MiB, cleared in two parts: it holds NaN before, and each
+    row without a token is exactly zero after."""
+    ids = _ids(kind, N, V, N).to(DEV)
+    dY = torch.randn(N, H, generator=torch.Generator().manual_seed(N + 1)).to(DT[dtype]).to(DEV)
+    dW = torch.full((V, H), float("nan"), device=DEV)
+    assert dW.numel() * 4 > 192 << 20
+    cuda_lib.flce_embed_bwd(dY, ids, V, dW=dW, scale=0.5)
+    keep = ids != IGN
+    rows, where, n = torch.unique(ids[keep], return_inverse=True, return_counts=True)
+    ref = torch.zeros(rows.numel(), H, dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(ref)
+    ref.index_add_(0, where, dY[keep].double())
+    mag.index_add_(0, where, dY[keep].double().abs())
+    err = (dW[rows].double() - 0.5 * ref).abs()
+    assert bool((err <= (n[:, None] + 2) * 2.0 ** -24 * 0.5 * mag).all())
+    dW[rows] = 0.0
+    assert bool((dW == 0).all())
