@@ -651,6 +651,7 @@ __device__ float cta_sum(float s) {
 template <int ELT>
 __global__ void __launch_bounds__(kNormThreads)
     ortho_norm(const void* g, int64_t elems, int vec, float* parts) {
+  grid_launch_dependents();
   const int64_t base = static_cast<int64_t>(blockIdx.y) * elems;
   float s = 0.f;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
@@ -697,8 +698,10 @@ struct SplitParams {
   int64_t ldx, ldh, x_stride, h_stride;
 };
 
-// 1 / (|G_b| + eps), from the partial sums.
+// 1 / (|G_b| + eps), from the partial sums of the launch before.
 __device__ float inverse_norm(const SplitParams& p, int b) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const float part =
       threadIdx.x < p.n_parts ? p.parts[static_cast<int64_t>(b) * kMaxParts + threadIdx.x] : 0.f;
   return 1.f / (sqrtf(cta_sum(part)) + p.eps);
@@ -916,6 +919,21 @@ cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoP
   return launch_shape<MODE, kSingle>(A, B, p, k, sms, s);
 }
 
+// Starts while the norms are taken, for which the kernel waits.
+cudaError_t launch_split(void (*kernel)(SplitParams), dim3 grid, const SplitParams& p,
+                         cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kNormThreads);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps,
         const float* coeffs, float eps, void* out, const Layout& l, uint8_t* w, int32_t* status,
         int sms, cudaStream_t s) {
@@ -941,21 +959,14 @@ int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
   if (!tr && aligned16(g) && cols % 8 == 0) {
     const int64_t want = (l.k * (l.ldx / 8) + kNormThreads - 1) / kNormThreads, cap = 8 * sms;
     const dim3 sgrid(static_cast<unsigned>(want < cap ? want : cap), nb);
-    if (elt == 4)
-      ortho_split_rows<4><<<sgrid, kNormThreads, 0, s>>>(sp);
-    else
-      ortho_split_rows<2><<<sgrid, kNormThreads, 0, s>>>(sp);
+    FLCE_TRY(launch_split(elt == 4 ? ortho_split_rows<4> : ortho_split_rows<2>, sgrid, sp, s));
   } else {
     const dim3 sgrid(static_cast<unsigned>((cols + 63) / 64),
                      static_cast<unsigned>((rows + 63) / 64), nb);
-    if (elt == 4)
-      tr ? ortho_split<4, true><<<sgrid, kNormThreads, 0, s>>>(sp)
-         : ortho_split<4, false><<<sgrid, kNormThreads, 0, s>>>(sp);
-    else
-      tr ? ortho_split<2, true><<<sgrid, kNormThreads, 0, s>>>(sp)
-         : ortho_split<2, false><<<sgrid, kNormThreads, 0, s>>>(sp);
+    FLCE_TRY(launch_split(elt == 4 ? (tr ? ortho_split<4, true> : ortho_split<4, false>)
+                                   : (tr ? ortho_split<2, true> : ortho_split<2, false>),
+                          sgrid, sp, s));
   }
-  FLCE_TRY(cudaGetLastError());
   int rc;
   CUtensorMap mx[2], mxn[2], ma, mb;
   for (int i = 0; i < 2; ++i) {
