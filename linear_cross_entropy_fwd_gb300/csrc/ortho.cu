@@ -20,12 +20,15 @@
 // twice.  That makes the flops of a step k^2 n + k^3 + 2 k^2 n.
 //
 // Launches: norm, split (fp32 and fp16 X), then three GEMMs per step, in three
-// shapes with 32 KB stages of A and B: CTA pairs on 256 x 256 tiles,
-// and for small matrices 128 x 128 tiles by single CTAs or by clusters of four
-// that share out K.  (All steps in one cooperative launch with a barrier over
-// the grid was built and took longer: 154 against 112 us for eight 256 x 1024
-// matrices (106 now).  Between two products the barrier, the fences before it and the first
-// loads after it took 4 to 5 us, and the next launch no more.)
+// shapes with 32 KB stages of A and B: CTA pairs on 256 x 256 tiles, and for small
+// matrices 128 x 128 tiles by single CTAs or by clusters of four that share out K.
+// For k <= 256 the second and third product are one launch.  (All steps in one
+// cooperative launch with a barrier over the grid was built and took longer: 154 us
+// for eight 256 x 1024 matrices, when three launches per step took 112.  Between two
+// products the barrier, the fences before it and the first loads after it took 4 to
+// 5 us, and the next launch no more.)  What a launch takes beside its products: 1 us
+// until the one before counts as complete, 1 us for the first operands, 1 to 3 us
+// of epilogue.
 #include <cmath>
 
 #include "host_util.h"
@@ -296,7 +299,7 @@ __device__ __forceinline__ void finish_block(const OrthoParams& p, const Addend<
       v[i] = fmaf(acc[i], kUnhold * kUnhold, p.a * v[i]);
   }
   uint32_t w[16];
-  if (MODE == kUpdate) {
+  if constexpr (MODE == kUpdate) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     uint16_t* res = p.result + static_cast<int64_t>(bi) * p.rows * p.cols;
@@ -305,13 +308,13 @@ __device__ __forceinline__ void finish_block(const OrthoParams& p, const Addend<
                           cols, p.result_vec != 0);
     else
       store_16(buf, w, res + static_cast<int64_t>(row0) * p.cols + c0, p.cols, rows, cols, false);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-  uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + bi * p.stride;
-  store_16(buf, w, o + row0 * p.ld + c0, p.ld, rows, cols, true);
-  if (mirror) store_16_transposed(buf, w, o + c0 * p.ld + row0, p.ld, rows, cols, true);
+    for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + bi * p.stride;
+    store_16(buf, w, o + row0 * p.ld + c0, p.ld, rows, cols, true);
+    if (mirror) store_16_transposed(buf, w, o + c0 * p.ld + row0, p.ld, rows, cols, true);
+  }
 }
 
 // 32 rows of an accumulator, columns [col0, col0 + width), block by block;
@@ -622,6 +625,159 @@ __global__ void __launch_bounds__(Config<SHAPE>::kThreads, 1)
   }
 }
 
+// ------------------------------------------------- A^2 and the update at once
+// For k <= 256, where A fits into shared memory: a CTA computes the 128 rows of
+// B = b A + c A^2 that its 128 x 128 tile of X takes (again in every CTA of those
+// rows: 1 us of products), puts them in the place of A's rows, and goes on with B X.
+// That saves a launch, and X is fetched while the launch before still runs: eight
+// 256 x 1024 104 -> 85 us, one 256 x 256 83 -> 65, 64 x 64 61 -> 51.
+constexpr int kSmallK = 256;
+constexpr int kSmallWarps = 16;  // as in Config<kSingle>
+constexpr int kSmallThreads = 64 + 32 * kSmallWarps;
+constexpr uint32_t kABox = 128 * 128;   // 128 rows x 64 fp16
+constexpr uint32_t kXBlock = 2 * kBox;  // 64 rows x 128 fp16, as two boxes
+constexpr uint32_t kSmallSmem = 1024 + 8 * kABox + 4 * kXBlock + 256;
+static_assert(kSmallWarps * kStagingBytes <= 4 * kXBlock, "the last stage uses X's place");
+
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    ortho_small_update(const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmX, const OrthoParams p) {
+  constexpr uint32_t kIdescSquare = make_idesc(0, false, false, 128, 128);
+  constexpr uint32_t kIdescUpdate = make_idesc(0, false, true, 128, 128);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* smA = smem;               // [K block][row half] boxes
+  uint8_t* smX = smem + 8 * kABox;   // [K block]
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(smX + 4 * kXBlock);
+  uint64_t* x_full = a_full + 1;
+  uint64_t* square_full = a_full + 2;
+  uint64_t* b_full = a_full + 3;
+  uint64_t* acc_full = a_full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_full + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int bi = static_cast<int>(blockIdx.x) / p.tiles, t = static_cast<int>(blockIdx.x) % p.tiles;
+  const int mi = t % p.m_blk, ni = t / p.m_blk;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 5; ++i) mbar_init(&a_full[i], i == 3 ? kSmallWarps : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t square = uniform(*tmem_slot), acc = square + kSmallK;  // 256 and 128 columns
+
+  // The launch before (A = X X^T) let this one start when it had waited for the
+  // launch that made X: X is complete.  A is, once this launch has waited.
+  if (warp == 0) {
+    expect_tx_elected(x_full, p.k_blk * kXBlock);
+    for (int kb = 0; kb < p.k_blk; ++kb)
+      for (int c = 0; c < 2; ++c)
+        tma_load_3d_elected(&tmX, x_full, smem_addr(smX) + kb * kXBlock + c * kBox,
+                            128 * ni + 64 * c, 64 * kb, bi);
+    grid_dependency_wait();
+    expect_tx_elected(a_full, p.k_blk * p.m_blk * kABox);
+    for (int kb = 0; kb < p.k_blk; ++kb)
+      for (int r = 0; r < p.m_blk; ++r)
+        tma_load_3d_elected(&tmA, a_full, smem_addr(smA) + (2 * kb + r) * kABox, 64 * kb, 128 * r,
+                            bi);
+    if (lane == 0) {  // every load has landed before this CTA's shared memory goes away
+      mbar_wait_drain(x_full, 0);
+      mbar_wait_drain(a_full, 0);
+    }
+  } else if (warp == 1) {
+    const Operand16 a_op(smem_addr(smA), 0), x_op(smem_addr(smX), kBox);
+    if (uniform_wait(a_full, 0, abort_flag, p.status)) {
+      tc_fence_after();
+      for (int r = 0; r < p.m_blk; ++r)
+        for (int kb = 0; kb < p.k_blk; ++kb) {
+          const Operand16 a = moved(a_op, (2 * kb + mi) * kABox), b = moved(a_op, (2 * kb + r) * kABox);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_at(square + 128 * r, a, 32 * k, b, 32 * k, kIdescSquare,
+                       (kb > 0 || k > 0) ? 1u : 0u);
+        }
+      commit_elected(square_full);
+    }
+    if (uniform_wait(x_full, 0, abort_flag, p.status) &&
+        uniform_wait(b_full, 0, abort_flag, p.status)) {
+      tc_fence_after();
+      for (int kb = 0; kb < p.k_blk; ++kb) {
+        const Operand16 b = moved(a_op, (2 * kb + mi) * kABox), x = moved(x_op, kb * kXBlock);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16_at(acc, b, 32 * k, x, 2048 * k, kIdescUpdate, (kb > 0 || k > 0) ? 1u : 0u);
+      }
+    }
+    commit_elected(acc_full);  // all MMAs issued by this thread are done
+    if (lane == 0) mbar_wait_drain(acc_full, 0);
+  } else {
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const int row0 = mi * 128 + 32 * q, col0 = ni * 128 + 32 * part;
+    Addend<kUpdate> add;
+    add.fetch(p, bi, row0, col0);
+    grid_dependency_wait();  // nothing is stored before the launch before is complete
+    if (warp == 2 && lane == 0) grid_launch_dependents();
+    bool ok = uniform_wait(square_full, 0, abort_flag, p.status);
+    if (ok && part < p.k_blk) {
+      // K block `part` of B's rows, in the place of A's
+      tc_fence_after();
+      const int row = 32 * q + lane;
+      const uint8_t* mine = smA + (2 * part + mi) * kABox + row * 128;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(square + lanes + 64 * part + 32 * u, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = ((4 * u + i) ^ (row & 7)) << 4;
+          const uint4 a = *reinterpret_cast<const uint4*>(mine + at);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+            o[k] = pack_half2(
+                fmaf(p.c * kUnhold, __uint_as_float(r[8 * i + 2 * k]), p.b * f.x),
+                fmaf(p.c * kUnhold, __uint_as_float(r[8 * i + 2 * k + 1]), p.b * f.y));
+          }
+          st_shared_v4(smem_addr(mine) + at, o[0], o[1], o[2], o[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_full);
+    ok = uniform_wait(acc_full, 0, abort_flag, p.status) && ok;
+    if (ok && row0 < p.rows && col0 < p.cols) {
+      tc_fence_after();
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(acc + lanes + 32 * part, r);
+      tmem_ld_wait();
+      // X's place stages the stores: every MMA is done
+      finish_block<kUpdate>(p, add, reinterpret_cast<const float(&)[32]>(r), bi, row0, col0, false,
+                            smX + (warp - 2) * kStagingBytes);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(square, 512);
+  }
+}
+
 // ------------------------------------------------------------- norm and split
 constexpr int kNormThreads = 256;
 constexpr int kMaxParts = 256;  // partial sums of one matrix (kNormThreads at most)
@@ -919,19 +1075,41 @@ cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoP
   return launch_shape<MODE, kSingle>(A, B, p, k, sms, s);
 }
 
-// Starts while the norms are taken, for which the kernel waits.
-cudaError_t launch_split(void (*kernel)(SplitParams), dim3 grid, const SplitParams& p,
-                         cudaStream_t s) {
+// A launch that may start while the one before finishes; the kernel waits for it.
+template <class... ARGS>
+cudaError_t launch_after(void (*kernel)(ARGS...), dim3 grid, int threads, uint32_t smem,
+                         cudaStream_t s, const ARGS&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kNormThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Up to two rounds of CTAs (300 of 64 x 64 170 -> 92 us, 256 x 16000 182 -> 179; but
+// 256 x 65536 545 -> 611: there the tiles' loads, products and stores should overlap).
+bool small_update(const OrthoParams& p, int sms) {
+  const int64_t tiles = static_cast<int64_t>((p.rows + 127) / 128) * ((p.cols + 127) / 128);
+  return p.rows <= kSmallK && tiles * p.batch <= 2 * sms;
+}
+
+cudaError_t launch_small_update(const CUtensorMap& A, const CUtensorMap& X, OrthoParams p,
+                                cudaStream_t s) {
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(ortho_small_update, kSmallSmem);
+  if (e != cudaSuccess) return e;
+  p.m_blk = (p.rows + 127) / 128;
+  p.n_blk = (p.cols + 127) / 128;
+  p.k_blk = (p.rows + 63) / 64;
+  p.tiles = p.m_blk * p.n_blk;
+  return launch_after(ortho_small_update, dim3(static_cast<unsigned>(p.tiles * p.batch)),
+                      kSmallThreads, kSmallSmem, s, A, X, p);
 }
 
 int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps,
@@ -959,13 +1137,14 @@ int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
   if (!tr && aligned16(g) && cols % 8 == 0) {
     const int64_t want = (l.k * (l.ldx / 8) + kNormThreads - 1) / kNormThreads, cap = 8 * sms;
     const dim3 sgrid(static_cast<unsigned>(want < cap ? want : cap), nb);
-    FLCE_TRY(launch_split(elt == 4 ? ortho_split_rows<4> : ortho_split_rows<2>, sgrid, sp, s));
+    FLCE_TRY(launch_after(elt == 4 ? ortho_split_rows<4> : ortho_split_rows<2>, sgrid,
+                          kNormThreads, 0, s, sp));
   } else {
     const dim3 sgrid(static_cast<unsigned>((cols + 63) / 64),
                      static_cast<unsigned>((rows + 63) / 64), nb);
-    FLCE_TRY(launch_split(elt == 4 ? (tr ? ortho_split<4, true> : ortho_split<4, false>)
+    FLCE_TRY(launch_after(elt == 4 ? (tr ? ortho_split<4, true> : ortho_split<4, false>)
                                    : (tr ? ortho_split<2, true> : ortho_split<2, false>),
-                          sgrid, sp, s));
+                          sgrid, kNormThreads, 0, s, sp));
   }
   int rc;
   CUtensorMap mx[2], mxn[2], ma, mb;
@@ -991,9 +1170,9 @@ int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
     p.stride = l.k * l.lda;
     p.out = A;
     FLCE_TRY(launch_gemm<kGram>(mx[i & 1], mx[i & 1], p, l.n, sms, s));
-    p.out = Bm;
-    p.gram = A;
-    FLCE_TRY(launch_gemm<kPoly>(ma, ma, p, l.k, sms, s));
+    OrthoParams poly = p;
+    poly.out = Bm;
+    poly.gram = A;
     p.cols = static_cast<int32_t>(l.n);
     p.ld = l.ldh;
     p.stride = l.k * l.ldh;
@@ -1003,6 +1182,11 @@ int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
       p.transposed = tr;
       p.result_vec = aligned16(out) && cols % 8 == 0;
     }
+    if (small_update(p, sms)) {
+      FLCE_TRY(launch_small_update(ma, mxn[i & 1], p, s));
+      continue;
+    }
+    FLCE_TRY(launch_gemm<kPoly>(ma, ma, poly, l.k, sms, s));
     FLCE_TRY(launch_gemm<kUpdate>(mb, mxn[i & 1], p, l.k, sms, s));
   }
   return FLCE_OK;

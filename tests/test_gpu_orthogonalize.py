@@ -161,3 +161,22 @@ def test_orthogonalize_long_products(cuda_lib, shape, dtype):
     got = cuda_lib.flce_orthogonalize(G, sync=True)
     _check(got, _reference(G))
     assert torch.equal(got, cuda_lib.flce_orthogonalize(G))
+
+
+@pytest.mark.parametrize("shape,dtype", [
+    ((256, 256), "fp32"),
+    ((255, 1000), "bf16"),
+    ((192, 193), "fp32"),         # three K blocks, a second half of 64 rows
+    ((700, 65), "bf16"),          # tall
+    ((1, 5000), "fp32"),
+    ((300, 40, 24), "bf16"),      # two rounds of CTAs
+    ((9000, 250), "fp32"),
+    ((5, 256, 7001), "bf16"),     # more: products of their own
+    ((257, 300), "fp32"),         # just past it
+])
+def test_orthogonalize_small_side(cuda_lib, shape, dtype):
+    """The second and third product in one launch."""
+    G = _matrix("signal", shape, sum(shape) + 1, dtype)
+    got = cuda_lib.flce_orthogonalize(G, sync=True)
+    _check(got, _reference(G))
+    assert torch.equal(got, cuda_lib.flce_orthogonalize(G))
