@@ -1054,12 +1054,22 @@ cudaError_t launch_shape(const CUtensorMap& A, const CUtensorMap& B, OrthoParams
   return cudaLaunchKernelEx(&cfg, kernel, A, B, p);
 }
 
-// CTA pairs where their 256 x 256 tiles fill at least half of the GPU's pairs.
-// Else 128 x 128 tiles; those of X X^T by four CTAs each, where the GPU has that
-// many and K is at least 2048 (300 x 8000 all told 159 us against 226, 1000 x
-// 3584 187 against 199, 512 x 2048 123 against 128; but 1024 x 1024 157 against
-// 130: the exchange of the partial sums takes about 2 us).  The other products
-// have such a K only where they have more tiles.
+// Rounds of tiles, whose epilogues run beside the next round's products, and one
+// epilogue at the end.  Times in units of 0.03 us: a K block of 64 takes 7 on a 128 x
+// 128 tile (L2 feeds all SMs at 21 TB/s) and 10 on a pair's 256 x 256; an epilogue 2.5
+// us and 4.5, a pair's update 6.5.
+int64_t round_time(int64_t tiles, int64_t at_once, int64_t products, int64_t epilogue) {
+  return (tiles + at_once - 1) / at_once * (products > epilogue ? products : epilogue) + epilogue;
+}
+
+// X X^T by four CTAs per 128 x 128 tile, where the GPU has that many and K is at least
+// 2048 (300 x 8000 all told 159 us against 226, 1000 x 3584 187 against 199, 512 x 2048
+// 123 against 128; but 1024 x 1024 157 against 130: the exchange of the partial sums
+// takes about 5 us).  The other products have such a K only where they have more tiles.
+// Else the shape that the estimate above favours.  All told, single CTAs against pairs:
+// 3000 x 3000 479 us against 576 (78 pairs of tiles on 76 pairs of SMs), 1024 x 16000
+// 414 against 435, 1500 x 4000 260 against 281, 16 of 384 x 2000 261 against 309; but
+// 2304 x 2304 363 against 348, 4096 x 4096 1154 against 1034.
 template <int MODE>
 cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoParams& p, int64_t k,
                         int sms, cudaStream_t s) {
@@ -1067,12 +1077,15 @@ cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoP
     const int64_t mb = (p.rows + edge - 1) / edge, nb = (p.cols + edge - 1) / edge;
     return (MODE != kUpdate ? mb * (mb + 1) / 2 : mb * nb) * p.batch;
   };
-  if (tiles(256) * 2 >= sms / 2) return launch_shape<MODE, kPair>(A, B, p, k, sms, s);
   if constexpr (MODE == kGram) {
     if (tiles(128) * kSplitCtas <= sms && k >= 2048)
       return launch_shape<MODE, kSplit>(A, B, p, k, sms, s);
   }
-  return launch_shape<MODE, kSingle>(A, B, p, k, sms, s);
+  const int64_t k_blk = (k + 63) / 64;
+  if (round_time(tiles(128), sms, 7 * k_blk, 83) <=
+      round_time(tiles(256), sms / 2, 10 * k_blk, MODE == kUpdate ? 217 : 150))
+    return launch_shape<MODE, kSingle>(A, B, p, k, sms, s);
+  return launch_shape<MODE, kPair>(A, B, p, k, sms, s);
 }
 
 // A launch that may start while the one before finishes; the kernel waits for it.
