@@ -100,16 +100,21 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   const size_t b_bucket = round256((static_cast<size_t>(p.max_depth) + 2) * 4);
   const size_t b_delta =
       backward ? round256(static_cast<size_t>(a->heads_q) * static_cast<size_t>(T) * 4) : 0;
+  const bool direct = !backward && a->batch >= 1 && a->batch <= kDirectSeqs &&
+                      max_tiles * a->heads_q <= sms;
+  const bool planned = T > 0 && !direct;
   StepCall call;
-  if ((rc = call.begin(o, T > 0 ? 256 + b_tiles + b_bucket + b_delta : 0,
-                       T > 0 ? StepCall::kKernelClears : StepCall::kIfAsked)))
+  if ((rc = call.begin(o, planned ? 256 + b_tiles + b_bucket + b_delta : 0,
+                       planned ? StepCall::kKernelClears : StepCall::kIfAsked)))
     return rc;
   if (T == 0) return call.end(FLCE_OK);
-  uint8_t* w = call.scratch;
-  p.n_tiles = reinterpret_cast<int32_t*>(w);
-  p.tiles = reinterpret_cast<AttnTile*>(w + 256);
-  p.bucket = reinterpret_cast<int32_t*>(w + 256 + b_tiles);
-  p.delta = backward ? reinterpret_cast<float*>(w + 256 + b_tiles + b_bucket) : nullptr;
+  if (planned) {
+    uint8_t* w = call.scratch;
+    p.n_tiles = reinterpret_cast<int32_t*>(w);
+    p.tiles = reinterpret_cast<AttnTile*>(w + 256);
+    p.bucket = reinterpret_cast<int32_t*>(w + 256 + b_tiles);
+    p.delta = backward ? reinterpret_cast<float*>(w + 256 + b_tiles + b_bucket) : nullptr;
+  }
   p.lse = a->lse;
   p.status = call.status;
   p.o = AttnOut{a->o, oo.token, oo.head};
@@ -117,7 +122,7 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   p.dq = AttnOut{a->dq, dq.token, dq.head};
   p.dk = AttnOut{a->dk, dk.token, dk.head};
   p.dv = AttnOut{a->dv, dv.token, dv.head};
-  cudaError_t e = launch_attn_plan(p, backward, sms, call.stream);
+  cudaError_t e = planned ? launch_attn_plan(p, backward, sms, call.stream) : cudaSuccess;
   if (max_tiles > 0) {
     if (backward) {
       if (e == cudaSuccess) e = launch_attn_dkdv(mq, mk, mv, mO, p, sms, call.stream);

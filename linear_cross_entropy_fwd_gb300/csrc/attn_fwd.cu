@@ -54,7 +54,8 @@ struct FwdShape {
   static constexpr int kSlots = DP == 128 ? 4 : 8;               // K and V tiles in flight
   static constexpr int kBarriers = 2 * kSlots + 13;              // and a word each of TMEM, abort
   static constexpr uint32_t kStaging = 8 * 4096;                 // one block per softmax warp
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + kStaging + 8 * (kBarriers + 1);
+  static constexpr uint32_t kSmem =
+      (2 + kSlots) * kTileBytes + kStaging + 8 * (kBarriers + 1) + sizeof(AttnTile);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -64,21 +65,23 @@ struct Unit {
   AttnTile t;
   int head;
   int n[2];  // key tiles of the two query tiles (n[1] = 0: one tile only)
-  __device__ __forceinline__ bool get(const AttnParams& p, int round, int total) {
+  __device__ __forceinline__ bool get(const AttnParams& p, const AttnTile* own, int round,
+                                      int total) {
     const int g = static_cast<int>(gridDim.x);
     const int b = static_cast<int>(blockIdx.x);
     const int64_t u = static_cast<int64_t>(round) * g + (round & 1 ? g - 1 - b : b);
     if (u >= total) return false;
     const int i = static_cast<int>(u / p.Hq);
-    t = p.tiles[i];
+    t = p.tiles ? p.tiles[i] : *own;  // without a plan: round 0 only
     head = static_cast<int>(u - static_cast<int64_t>(i) * p.Hq);
     const int nt = (t.len + kTile - 1) / kTile;
     n[0] = 2 * t.tile + 1;
     n[1] = n[0] < nt ? n[0] + 1 : 0;
     return true;
   }
-  __device__ __forceinline__ bool get_uniform(const AttnParams& p, int round, int total) {
-    if (!get(p, round, total)) return false;
+  __device__ __forceinline__ bool get_uniform(const AttnParams& p, const AttnTile* own, int round,
+                                              int total) {
+    if (!get(p, own, round, total)) return false;
     t.start = uniform(t.start);
     t.tile = uniform(t.tile);
     n[0] = uniform(n[0]);
@@ -87,6 +90,37 @@ struct Unit {
   }
   __device__ __forceinline__ int depth() const { return n[1] ? n[1] : n[0]; }
 };
+
+// Without a plan: this CTA's unit, found from the offsets by a prefix sum over the
+// sequences, and its share of the tokens outside them.  Returns the number of
+// units of one head.  `sums`: a word per warp.
+__device__ int own_unit(const AttnParams& p, AttnTile* own, int32_t* sums) {
+  const int b = threadIdx.x, lane = b & 31, warp = b >> 5;
+  const int c0 = b < p.B ? p.cu[b] : 0, c1 = b < p.B ? p.cu[b + 1] : 0;
+  const bool ok = __syncthreads_or(c0 < 0 || c1 < c0 || c1 > p.T) == 0;
+  if (!ok && b == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, FLCE_DEV_SEQLENS);
+  const int unit = kTile * p.unit;
+  const int n = ok ? (c1 - c0 + unit - 1) / unit : 0;
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kFwdThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  const int at = static_cast<int>(blockIdx.x) / p.Hq - (before + inc - n);
+  if (at >= 0 && at < n) *own = AttnTile{c0, c1 - c0, at, 0};
+  blank_outside<false>(p, ok, static_cast<int64_t>(blockIdx.x) * kFwdThreads + b,
+                       static_cast<int64_t>(gridDim.x) * kFwdThreads);
+  __syncthreads();
+  return all;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -113,6 +147,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* drain = o_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::kBarriers);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  AttnTile* own = reinterpret_cast<AttnTile*>(tmem_slot + 2);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -141,8 +176,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);  // S_A, S_B, O_A, O_B
-  grid_dependency_wait();            // the tile list
-  const int total = uniform(*p.n_tiles) * p.Hq;
+  int units;
+  if (p.tiles) {
+    grid_dependency_wait();          // the tile list
+    units = *p.n_tiles;
+  } else {
+    units = own_unit(p, own, reinterpret_cast<int32_t*>(staging));
+  }
+  const int total = uniform(units) * p.Hq;
   Unit w;
 
   if (warp >= kTmaWarp) {
@@ -151,7 +192,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       int g = 0, n_q = 0;
       bool ok = true;
       const uint32_t q_dst = smem_addr(smQ), kv_dst = smem_addr(smKV);
-      for (int round = 0; ok && w.get_uniform(p, round, total); ++round) {
+      for (int round = 0; ok && w.get_uniform(p, own, round, total); ++round) {
         const int kvh = uniform(w.head / (p.Hq / p.Hkv));
         if (!uniform_wait(q_empty, (round & 1) ^ 1, abort_flag, p.status)) break;
         const int tiles = w.n[1] ? 2 : 1;
@@ -165,7 +206,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // the next unit's queries on their way into L2: they are loaded only
         // when this unit's last scores are complete
         Unit next;
-        if (next.get_uniform(p, round + 1, total))
+        if (next.get_uniform(p, own, round + 1, total))
           for (int x = 0; x < (next.n[1] ? 2 : 1); ++x)
 #pragma unroll
             for (int b = 0; b < S::kBoxes; ++b)
@@ -218,7 +259,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         commit_elected(&s_full[x]);
       };
       bool ok = true;
-      for (int round = 0; ok && w.get_uniform(p, round, total); ++round) {
+      for (int round = 0; ok && w.get_uniform(p, own, round, total); ++round) {
         const int depth = w.depth();
         const int last = w.n[1] ? 1 : 0;  // the query tile that uses each key tile last
         ok = uniform_wait(q_full, round & 1, abort_flag, p.status) && wait_kv(g);
@@ -282,7 +323,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     int n_s = 0;  // score tiles so far
     int J = 0;    // key tiles before this unit
     int n_u = 0;  // units of this tile so far
-    for (int round = 0; ok && w.get(p, round, total); J += w.depth(), ++round) {
+    for (int round = 0; ok && w.get(p, own, round, total); J += w.depth(), ++round) {
       const int n = w.n[x];
       if (n == 0) continue;
       const int q0 = (2 * w.t.tile + x) * kTile;
@@ -422,7 +463,7 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.tiles ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<DP>, q, k, v, p);
 }
 

@@ -1,4 +1,5 @@
-// attn_plan.cu -- the first launch of an attention call.  Block 0 turns the
+// attn_plan.cu -- the first launch of an attention call (a small forward pass has
+// none: see kDirectSeqs).  Block 0 turns the
 // sequence offsets into the list of tiles, longest work first, so that the
 // last CTAs to start are the short ones.  The other blocks write what no
 // tile covers (tokens outside every sequence) and, for the backward pass,
@@ -77,20 +78,6 @@ __device__ void make_tiles(const AttnParams& p, bool ok) {
   if (threadIdx.x == 0) *p.n_tiles = above;
 }
 
-// Zeros in the rows [t0, t1) of a [T, heads, D] output, 16 bytes at a time.
-__device__ void zero_rows(const AttnOut& o, int heads, int D, int t0, int t1, int64_t me,
-                          int64_t threads) {
-  const int vecs = D / 8;
-  const int64_t per = static_cast<int64_t>(heads) * vecs, n = (t1 - t0) * per;
-  for (int64_t i = me; i < n; i += threads) {
-    const int64_t t = t0 + i / per;
-    const int r = static_cast<int>(i % per);
-    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.p) + t * o.token +
-                                        (r / vecs) * o.head + (r % vecs) * 8);
-    *d = make_uint4(0u, 0u, 0u, 0u);
-  }
-}
-
 // delta of every token: 16 lanes per (head, token), eight products each.
 __device__ void make_delta(const AttnParams& p, int64_t me, int64_t threads) {
   const int part = static_cast<int>(me & 15);
@@ -126,24 +113,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const AttnParams p)
   }
   const int64_t me = static_cast<int64_t>(blockIdx.x - 1) * kThreads + threadIdx.x;
   const int64_t threads = static_cast<int64_t>(gridDim.x - 1) * kThreads;
-  // tokens before the first sequence and after the last (all of them if the
-  // offsets are bad)
-  const int lo = ok ? p.cu[0] : p.T, hi = ok ? p.cu[p.B] : p.T;
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const int t0 = side ? hi : 0, t1 = side ? p.T : lo;
-    if (t0 >= t1) continue;
-    if (BACKWARD) {
-      zero_rows(p.dq, p.Hq, p.D, t0, t1, me, threads);
-      zero_rows(p.dk, p.Hkv, p.D, t0, t1, me, threads);
-      zero_rows(p.dv, p.Hkv, p.D, t0, t1, me, threads);
-    } else {
-      zero_rows(p.o, p.Hq, p.D, t0, t1, me, threads);
-      const int64_t n = static_cast<int64_t>(p.Hq) * (t1 - t0);
-      for (int64_t i = me; i < n; i += threads)
-        p.lse[i / (t1 - t0) * p.T + t0 + i % (t1 - t0)] = -INFINITY;
-    }
-  }
+  blank_outside<BACKWARD>(p, ok, me, threads);
   if (BACKWARD) make_delta(p, me, threads);
 }
 

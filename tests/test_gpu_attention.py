@@ -331,3 +331,32 @@ def test_attention_many_units(cuda_lib, lens, Hq, Hkv, D):
     val, tol = _reference(q, k, v, dO, lens, D ** -0.5)
     for n in val:
         _close(n, got[n], val[n], tol[n])
+
+
+@pytest.mark.parametrize("lens,first,pad", [
+    ([7], 0, 0),
+    ([0, 40, 1, 0, 300, 0], 9, 3),      # tokens before the first sequence and after the last
+    ([1] * 70, 1, 0),                   # more sequences than two warps have threads
+    ([0, 0], 0, 50),                    # nothing but tokens outside
+])
+@pytest.mark.parametrize("status", [False, True])
+def test_attention_few_units(cuda_lib, lens, first, pad, status):
+    """A batch small enough to run without a plan gives what the same sequences give
+    as the first ones of a batch that is not, bit for bit."""
+    Hq, Hkv, D = 2, 1, 64
+    q, k, v, _, cu = _inputs([first] + lens, Hq, Hkv, D, sum(lens), pad)
+    cu = cu[1:].contiguous()
+    T, B = q.shape[0], len(lens)
+    o = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((Hq, T), 7.0, device=DEV)
+    info = {} if status else None
+    cuda_lib.flce_attn_fwd(q, k, v, cu, out=o, lse=lse, info=info)
+    if status:
+        assert int(info["status"].item()) == 0
+    more = torch.cat([cu, cu[-1:].expand(400)])  # empty sequences: too many units for one round
+    o2, lse2 = cuda_lib.flce_attn_fwd(q, k, v, more.contiguous())
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    outside = torch.ones(T, dtype=torch.bool, device=DEV)
+    outside[int(cu[0]):int(cu[-1])] = False
+    assert not o[outside].any() and bool((lse[:, outside] == -math.inf).all())
+    assert bool(torch.isfinite(lse[:, ~outside]).all())
