@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (FLCE_FP32, FlceAttn, FlceOpts, _check, _check_out, _dtype_code, _is32,
                load_library, make_opts, scale_convert)
@@ -130,6 +131,7 @@ class _EmbedFunction(torch.autograd.Function):
         return flce_embed_fwd(weight.contiguous(), ids, scale=scale, ignore_index=ignore_index)
 
     @staticmethod
+    @once_differentiable  # the kernels' results carry no graph of their own
     def backward(ctx, grad_out):
         (ids,) = ctx.saved_tensors
         V, dtype, scale, ignore_index = ctx.args
@@ -253,6 +255,7 @@ class _AttnFunction(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable  # the kernels' results carry no graph of their own
     def backward(ctx, grad_out):
         q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
         dq, dk, dv = flce_attn_bwd(_strided(grad_out), q, k, v, o, lse, cu_seqlens,

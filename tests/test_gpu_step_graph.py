@@ -1,5 +1,6 @@
 """A training step through the modules, captured into a CUDA graph: embedding,
-attention, their gradients, and the orthogonalised update."""
+attention, their gradients, and the orthogonalised update.  And second
+derivatives, which they refuse."""
 import pytest
 import torch
 
@@ -51,3 +52,16 @@ def test_captured_training_step(cuda_lib):
         for a, b in zip(got, _step(flce, E, Wqkv, ids, cu, C, heads, D)):
             assert torch.equal(a, b)
             assert torch.isfinite(a.float()).all() and a.float().abs().sum() > 0
+
+
+def test_second_derivatives_are_refused(cuda_lib):
+    import linear_cross_entropy_fwd_gb300 as flce
+    E = torch.randn(20, 64, device="cuda").bfloat16().requires_grad_()
+    ids = torch.arange(10, device="cuda")
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    for f in (lambda: flce.Embedding()(E, ids),
+              lambda: flce.PackedAttention()(*(E[:10].view(10, 1, 64),) * 3, cu)):
+        y = f().float().pow(2).sum()
+        g, = torch.autograd.grad(y, E, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.float().pow(2).sum().backward()
