@@ -61,6 +61,7 @@ struct FwdShape {
 
 // The units of a CTA: rounds go through the list forwards and backwards in
 // turn, so that no CTA always gets the deeper one.
+template <bool PLAN>
 struct Unit {
   AttnTile t;
   int head;
@@ -72,7 +73,7 @@ struct Unit {
     const int64_t u = static_cast<int64_t>(round) * g + (round & 1 ? g - 1 - b : b);
     if (u >= total) return false;
     const int i = static_cast<int>(u / p.Hq);
-    t = p.tiles ? p.tiles[i] : *own;  // without a plan: round 0 only
+    t = PLAN ? p.tiles[i] : *own;  // without a plan: round 0 only
     head = static_cast<int>(u - static_cast<int64_t>(i) * p.Hq);
     const int nt = (t.len + kTile - 1) / kTile;
     n[0] = 2 * t.tile + 1;
@@ -122,7 +123,12 @@ __device__ int own_unit(const AttnParams& p, AttnTile* own, int32_t* sums) {
   return all;
 }
 
-template <int DP>
+// Where the outcome of a wait goes that no caller asked for (a test for NULL in every
+// wait cost the passes with a plan 1.5%).
+__device__ int32_t g_unasked;
+
+// PLAN: units come from the plan's list.
+template <int DP, bool PLAN>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -176,15 +182,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);  // S_A, S_B, O_A, O_B
+  int32_t* const status = PLAN || p.status ? p.status : &g_unasked;
   int units;
-  if (p.tiles) {
+  if (PLAN) {
     grid_dependency_wait();          // the tile list
     units = *p.n_tiles;
   } else {
     units = own_unit(p, own, reinterpret_cast<int32_t*>(staging));
   }
   const int total = uniform(units) * p.Hq;
-  Unit w;
+  Unit<PLAN> w;
 
   if (warp >= kTmaWarp) {
     if (warp == kTmaWarp) {
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t q_dst = smem_addr(smQ), kv_dst = smem_addr(smKV);
       for (int round = 0; ok && w.get_uniform(p, own, round, total); ++round) {
         const int kvh = uniform(w.head / (p.Hq / p.Hkv));
-        if (!uniform_wait(q_empty, (round & 1) ^ 1, abort_flag, p.status)) break;
+        if (!uniform_wait(q_empty, (round & 1) ^ 1, abort_flag, status)) break;
         const int tiles = w.n[1] ? 2 : 1;
         expect_tx_elected(q_full, tiles * TB);
         for (int x = 0; x < tiles; ++x)
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ++n_q;
         // the next unit's queries on their way into L2: they are loaded only
         // when this unit's last scores are complete
-        Unit next;
+        Unit<PLAN> next;
         if (next.get_uniform(p, own, round + 1, total))
           for (int x = 0; x < (next.n[1] ? 2 : 1); ++x)
 #pragma unroll
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {  // K_j, then V_j
             const int s = g % kSlots;
-            ok = ok && uniform_wait(&kv_empty[s], ((g / kSlots) & 1) ^ 1, abort_flag, p.status);
+            ok = ok && uniform_wait(&kv_empty[s], ((g / kSlots) & 1) ^ 1, abort_flag, status);
             if (ok) {
               expect_tx_elected(&kv_full[s], TB);
 #pragma unroll
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       int g = 0;                            // K and V tiles so far
       int n_p[2] = {0, 0}, n_u[2] = {0, 0}; // products P V, and units, per query tile so far
       auto wait_kv = [&](int i) {
-        return uniform_wait(&kv_full[i % kSlots], (i / kSlots) & 1, abort_flag, p.status);
+        return uniform_wait(&kv_full[i % kSlots], (i / kSlots) & 1, abort_flag, status);
       };
       auto scores = [&](int x, int i) {
         const Operand16 q = moved(q_op, x * TB), k = moved(k_op, (i % kSlots) * TB);
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int round = 0; ok && w.get_uniform(p, own, round, total); ++round) {
         const int depth = w.depth();
         const int last = w.n[1] ? 1 : 0;  // the query tile that uses each key tile last
-        ok = uniform_wait(q_full, round & 1, abort_flag, p.status) && wait_kv(g);
+        ok = uniform_wait(q_full, round & 1, abort_flag, status) && wait_kv(g);
         if (!ok) break;
         scores(0, g);
         if (last) scores(1, g);
@@ -276,8 +283,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int x = 0; x < 2; ++x) {
             if (!ok || x > last) break;
             if (j < w.n[x]) {
-              ok = (j > 0 || uniform_wait(&o_empty[x], (n_u[x] & 1) ^ 1, abort_flag, p.status)) &&
-                   uniform_wait(&p_full[2 * x], n_p[x] & 1, abort_flag, p.status);
+              ok = (j > 0 || uniform_wait(&o_empty[x], (n_u[x] & 1) ^ 1, abort_flag, status)) &&
+                   uniform_wait(&p_full[2 * x], n_p[x] & 1, abort_flag, status);
               if (!ok) break;
               const Operand16 v = moved(v_op, (iv % kSlots) * TB);
               auto add_pv = [&](int from) {
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                 kIdescO, (j > 0 || e > 0) ? 1u : 0u);
               };
               add_pv(0);
-              if (!(ok = uniform_wait(&p_full[2 * x + 1], n_p[x] & 1, abort_flag, p.status))) break;
+              if (!(ok = uniform_wait(&p_full[2 * x + 1], n_p[x] & 1, abort_flag, status))) break;
               add_pv(kTile / 32);
               ++n_p[x];
               if (j == 0) ++n_u[x];
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int valid = w.t.len - q0 < kTile ? w.t.len - q0 : kTile;  // rows of this tile
       float m = 0.f, l = 0.f;
       for (int j = 0; j < n; ++j, ++n_s) {
-        if (!uniform_wait(&s_full[x], n_s & 1, abort_flag, p.status)) {
+        if (!uniform_wait(&s_full[x], n_s & 1, abort_flag, status)) {
           ok = false;
           break;
         }
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         if (diag && valid < kTile) {
           const int g = 2 * (J + j) + 1, sv = g % kSlots;
-          if (!uniform_wait(&kv_full[sv], (g / kSlots) & 1, abort_flag, p.status)) {
+          if (!uniform_wait(&kv_full[sv], (g / kSlots) & 1, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float2 sum = add2(sums[0], sums[1]);
         l += sum.x + sum.y;
       }
-      if (!ok || !uniform_wait(&o_full[x], n_u & 1, abort_flag, p.status)) break;
+      if (!ok || !uniform_wait(&o_full[x], n_u & 1, abort_flag, status)) break;
       ++n_u;
       tc_fence_after();
       const float inv = 1.f / l;
@@ -447,11 +454,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-template <int DP>
+template <int DP, bool PLAN>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                      const AttnParams& p, int sms, cudaStream_t s) {
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(attn_fwd_kernel<DP>, FwdShape<DP>::kSmem);
+  const cudaError_t e = limit.raise(attn_fwd_kernel<DP, PLAN>, FwdShape<DP>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(p.max_tiles) * p.Hq;
   cudaLaunchConfig_t cfg = {};
@@ -463,15 +470,19 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.tiles ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<DP>, q, k, v, p);
+  cfg.numAttrs = PLAN ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<DP, PLAN>, q, k, v, p);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                             const AttnParams& p, int sms, cudaStream_t s) {
-  return p.D <= 64 ? launch_t<64>(q, k, v, p, sms, s) : launch_t<128>(q, k, v, p, sms, s);
+  if (p.tiles)
+    return p.D <= 64 ? launch_t<64, true>(q, k, v, p, sms, s)
+                     : launch_t<128, true>(q, k, v, p, sms, s);
+  return p.D <= 64 ? launch_t<64, false>(q, k, v, p, sms, s)
+                   : launch_t<128, false>(q, k, v, p, sms, s);
 }
 
 }  // namespace flce

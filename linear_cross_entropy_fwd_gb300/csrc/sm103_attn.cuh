@@ -31,7 +31,7 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volati
       if (t0 == 0) t0 = t;
       if (t - t0 > FLCE_WAIT_LIMIT_NS) {
         *abort_flag = 1;
-        if (status) atomicOr(status, FLCE_DEV_TIMEOUT);
+        atomicOr(status, FLCE_DEV_TIMEOUT);
         return false;
       }
     }
