@@ -367,8 +367,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (j == 0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
-          // S_j complete means every MMA issued before it is: O is at rest
-          const float mn = fmaxf(m, mx);
+          // S_j complete means every MMA issued before it is: O is at rest.  Rows that
+          // need no rescaling keep m (f = 1), so that no row's bits depend on the
+          // others of its warp, which may be another sequence's.
+          const float mn = mx > m + kRescale ? mx : m;
           const float f = fast_exp2(m - mn);
           m = mn;
           l *= f;

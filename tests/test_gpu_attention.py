@@ -360,3 +360,28 @@ def test_attention_few_units(cuda_lib, lens, first, pad, status):
     outside[int(cu[0]):int(cu[-1])] = False
     assert not o[outside].any() and bool((lse[:, outside] == -math.inf).all())
     assert bool(torch.isfinite(lse[:, ~outside]).all())
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [
+    ([300, 90], 2, 1, 64),              # no plan
+    ([300, 90], 4, 2, 128),
+    ([290] + [40] * 60, 8, 2, 128),     # with one
+])
+def test_attention_bits_do_not_depend_on_what_follows(cuda_lib, lens, Hq, Hkv, D):
+    """Queries of another sequence, of padding, or later in the same sequence share a
+    block of rows with a token, and change no bit of its results."""
+    q, k, v, dO, cu = _inputs(lens, Hq, Hkv, D, 21, pad=7)
+    n = lens[0]
+    ref = _run(cuda_lib, q, k, v, dO, cu)
+    q2 = q.clone()
+    q2[n:] *= 64.0      # finite, and enough to raise the maximum at every key tile
+    got = _run(cuda_lib, q2, k, v, dO, cu)
+    for name in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[name][:n], ref[name][:n]), name
+    assert torch.equal(got["lse"][:, :n], ref["lse"][:, :n])
+    q3 = q.clone()
+    q3[n - 5:n] *= 64.0
+    got = _run(cuda_lib, q3, k, v, dO, cu)
+    for name in ("o", "dq"):
+        assert torch.equal(got[name][:n - 5], ref[name][:n - 5]), name
+    assert torch.equal(got["lse"][:, :n - 5], ref["lse"][:, :n - 5])
