@@ -351,8 +351,10 @@ FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t 
  * are reported as FLCE_ERR_ARG and count as no sequence at all.  A sequence
  * may be empty.  Tokens outside every sequence get zeros in o, dq, dk and dv
  * and -inf in lse; what their inputs hold is not used.
- * A NaN or infinity in a token's k or v reaches only its own sequence; there
- * it may also reach tokens before it in the same block of 128 tokens.
+ * A NaN or infinity reaches what the formulas take it to: nothing of another
+ * sequence, and in o and lse no token before it.  In the gradients one in k may also
+ * reach dq of tokens before it, and one in q or dO dk and dv of tokens after it, in the
+ * same block of 128 tokens.
  */
 typedef struct flce_attn {
   int64_t T;                 /* tokens, < 2^31 - 256 */

@@ -30,6 +30,14 @@
 // masked in S; the rows of V there (another sequence's, of any value) are
 // cleared in shared memory, since 0 * NaN would reach O.
 //
+// For the same reason NaN or an infinity in V would reach the rows of its tile that
+// do not see it.  A CTA whose outputs are not all finite goes over its units once
+// more, carefully: it clears what is not finite in the V tiles on the diagonal and adds
+// it, from memory, to the rows that see it (add_nonfinite).  Looking at every such
+// tile beforehand took 161 us in place of 149 at the 8192 tokens above (shared memory
+// is what the products wait for).  The careful form is a second instance of the same
+// code: as a switch at run time it took 152 us, as a function of its own 153.
+//
 // Roles (320 threads): warps 0-3 softmax and output of tile A, 4-7 of tile B
 // (warp w: TMEM lanes 32 (w % 4) ..), warp 8 TMA, warp 9 MMA.
 #include "attn.h"
@@ -55,7 +63,7 @@ struct FwdShape {
   static constexpr int kBarriers = 2 * kSlots + 13;              // and a word each of TMEM, abort
   static constexpr uint32_t kStaging = 8 * 4096;                 // one block per softmax warp
   static constexpr uint32_t kSmem =
-      (2 + kSlots) * kTileBytes + kStaging + 8 * (kBarriers + 1) + sizeof(AttnTile);
+      (2 + kSlots) * kTileBytes + kStaging + 8 * (kBarriers + 2) + sizeof(AttnTile);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -123,41 +131,64 @@ __device__ int own_unit(const AttnParams& p, AttnTile* own, int32_t* sums) {
   return all;
 }
 
+// Clears rows [valid, 128) of a V tile, and what is not finite in the rows before;
+// whether this thread cleared any of the latter.  128 threads, `i` of this one.
+template <int BOXES>
+__device__ __forceinline__ bool clear_masked_v(uint8_t* tile, int i, int valid) {
+  bool found = false;
+#pragma unroll 1
+  for (int k = 0; k < 8 * BOXES; ++k) {
+    const int piece = i + k * kTile, row = (piece >> 3) & (kTile - 1);
+    if (row < valid)
+      found |= clear_nonfinite_piece(tile + piece * 16);
+    else
+      st_shared_v4(smem_addr(tile) + piece * 16, 0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  return found;
+}
+
 // Where the outcome of a wait goes that no caller asked for (a test for NULL in every
 // wait cost the passes with a plan 1.5%).
 __device__ int32_t g_unasked;
 
-// PLAN: units come from the plan's list.
-template <int DP, bool PLAN>
-__global__ void __launch_bounds__(kFwdThreads, 1)
-    attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
-                    const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+// The shared memory of a CTA, and its barriers.
+template <int DP>
+struct FwdShared {
   using S = FwdShape<DP>;
-  constexpr int kSlots = S::kSlots;
-  constexpr uint32_t TB = S::kTileBytes;
+  uint8_t *q, *kv, *staging;   // [2], [kSlots], a block per softmax warp
+  uint64_t *kv_full, *kv_empty;         // [kSlots]
+  uint64_t *q_full, *q_empty, *drain;
+  uint64_t *s_full, *o_full, *o_empty;  // [2], per query tile
+  uint64_t* p_full;                     // [2][2]
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  AttnTile* own;
+  volatile int* again;  // an output is not finite
+  int* nonfinite_v;     // one more than the last round in which V was not, on the diagonal
 
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* smQ = smem;                        // [2]
-  uint8_t* smKV = smem + 2 * TB;              // [kSlots]
-  uint8_t* staging = smKV + kSlots * TB;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + S::kStaging);
-  uint64_t* kv_full = bars;                   // [kSlots]
-  uint64_t* kv_empty = kv_full + kSlots;      // [kSlots]
-  uint64_t* q_full = kv_empty + kSlots;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;             // [2] per tile, from here on
-  uint64_t* p_full = s_full + 2;              // [2][2]
-  uint64_t* o_full = p_full + 4;
-  uint64_t* o_empty = o_full + 2;
-  uint64_t* drain = o_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::kBarriers);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  AttnTile* own = reinterpret_cast<AttnTile*>(tmem_slot + 2);
+  __device__ __forceinline__ explicit FwdShared(uint8_t* smem) {
+    q = smem;
+    kv = q + 2 * S::kTileBytes;
+    staging = kv + S::kSlots * S::kTileBytes;
+    kv_full = reinterpret_cast<uint64_t*>(staging + S::kStaging);
+    kv_empty = kv_full + S::kSlots;
+    q_full = kv_empty + S::kSlots;
+    q_empty = q_full + 1;
+    s_full = q_empty + 1;
+    p_full = s_full + 2;
+    o_full = p_full + 4;
+    o_empty = o_full + 2;
+    drain = o_empty + 2;
+    tmem_slot = reinterpret_cast<uint32_t*>(kv_full + S::kBarriers);
+    abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    own = reinterpret_cast<AttnTile*>(tmem_slot + 2);
+    again = reinterpret_cast<volatile int*>(own + 1);
+    nonfinite_v = reinterpret_cast<int*>(own + 1) + 1;
+  }
 
-  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+  __device__ void init_barriers() const {  // one thread
+    for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
@@ -171,26 +202,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&o_empty[x], 4);
     }
     mbar_init(drain, 1);
-    *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = uniform(*tmem_slot);  // S_A, S_B, O_A, O_B
-  int32_t* const status = PLAN || p.status ? p.status : &g_unasked;
-  int units;
-  if (PLAN) {
-    grid_dependency_wait();          // the tile list
-    units = *p.n_tiles;
-  } else {
-    units = own_unit(p, own, reinterpret_cast<int32_t*>(staging));
-  }
-  const int total = uniform(units) * p.Hq;
+};
+
+// All units of this CTA.  PLAN: units come from the plan's list.  CAREFUL: with V's
+// values that are not finite taken out of the products (see the top).
+template <int DP, bool PLAN, bool CAREFUL>
+__device__ __forceinline__ void run_units(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                          const CUtensorMap& tmV, const AttnParams& p,
+                                          const FwdShared<DP>& sh, uint32_t tmem, int total,
+                                          int32_t* status) {
+  using S = FwdShape<DP>;
+  constexpr int kSlots = S::kSlots;
+  constexpr uint32_t TB = S::kTileBytes;
+  uint8_t *const smQ = sh.q, *const smKV = sh.kv, *const staging = sh.staging;
+  uint64_t *const kv_full = sh.kv_full, *const kv_empty = sh.kv_empty, *const q_full = sh.q_full,
+                  *const q_empty = sh.q_empty, *const s_full = sh.s_full,
+                  *const p_full = sh.p_full, *const o_full = sh.o_full,
+                  *const o_empty = sh.o_empty, *const drain = sh.drain;
+  volatile int* const abort_flag = sh.abort_flag;
+  const AttnTile* const own = sh.own;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   Unit<PLAN> w;
 
   if (warp >= kTmaWarp) {
@@ -266,7 +299,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         commit_elected(&s_full[x]);
       };
       bool ok = true;
-      for (int round = 0; ok && w.get_uniform(p, own, round, total); ++round) {
+      int round = 0;
+      for (; ok && w.get_uniform(p, own, round, total); ++round) {
         const int depth = w.depth();
         const int last = w.n[1] ? 1 : 0;  // the query tile that uses each key tile last
         ok = uniform_wait(q_full, round & 1, abort_flag, status) && wait_kv(g);
@@ -317,7 +351,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         g += 2 * depth;
       }
       commit_elected(drain);  // all MMAs issued by this warp are done
-      if (lane == 0) mbar_wait_drain(drain, 0);
+      if (lane == 0) {
+        mbar_wait_drain(drain, 0);
+        if (!CAREFUL && ok && round > 0) {  // and have arrived everywhere
+          for (int i = g > kSlots ? g - kSlots : 0; i < g; ++i)
+            mbar_wait_drain(&kv_empty[i % kSlots], (i / kSlots) & 1);
+          mbar_wait_drain(q_empty, (round - 1) & 1);
+        }
+      }
     }
   } else {
     // ----------------------------------------------------- softmax, output
@@ -337,12 +378,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int valid = w.t.len - q0 < kTile ? w.t.len - q0 : kTile;  // rows of this tile
       float m = 0.f, l = 0.f;
       for (int j = 0; j < n; ++j, ++n_s) {
+        const bool diag = j == n - 1;
+        if (CAREFUL && diag) {
+          // The other tile's product with this V, if there is one, comes after this
+          // tile's, and so after what is cleared here.
+          const int iv = 2 * (J + j) + 1, sv = iv % kSlots;
+          if (!uniform_wait(&kv_full[sv], (iv / kSlots) & 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          if (clear_masked_v<S::kBoxes>(smKV + sv * TB, row, valid))
+            atomicMax(sh.nonfinite_v, round + 1);
+        }
         if (!uniform_wait(&s_full[x], n_s & 1, abort_flag, status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const bool diag = j == n - 1;
         float s[kTile];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -384,9 +436,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tmem_st_32x32b_x16(tO + 16 * q, o);
           }
         }
-        if (diag && valid < kTile) {
-          const int g = 2 * (J + j) + 1, sv = g % kSlots;
-          if (!uniform_wait(&kv_full[sv], (g / kSlots) & 1, abort_flag, status)) {
+        if (diag && valid < kTile && !CAREFUL) {
+          const int iv = 2 * (J + j) + 1, sv = iv % kSlots;
+          if (!uniform_wait(&kv_full[sv], (iv / kSlots) & 1, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -446,10 +498,68 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         store_rows_bf16(staging + warp * 4096, reinterpret_cast<uint32_t(&)[32]>(o[32 * b]),
                         out + 64 * b, p.o.token, valid - (row - lane), p.D - 64 * b);
       if (in) p.lse[static_cast<int64_t>(w.head) * p.T + tok] = (m + fast_log2(l)) * kLn2;
+      if (!CAREFUL) {
+        uint32_t any[4] = {};
+#pragma unroll
+        for (int i = 0; i < DP / 2; ++i) nonfinite_word(o[i], any[i & 3]);
+        if (in && nonfinite_found(any)) *sh.again = 1;
+      } else if (*reinterpret_cast<volatile int*>(sh.nonfinite_v) > round) {
+        // (a later round's mark is at worst a needless look; tile B also lacks what was
+        // cleared for tile A)
+        const int last = row - lane + 31 < valid ? row - lane + 31 : valid - 1;
+        add_nonfinite(static_cast<const uint16_t*>(p.v.p) + w.head / (p.Hq / p.Hkv) * p.v.head,
+                      p.v.token, static_cast<uint16_t*>(p.o.p) + tok * p.o.token +
+                      w.head * p.o.head, 0, p.D, w.t.start + 2 * w.t.tile * kTile,
+                      static_cast<int>(tok), w.t.start + q0 + last, 1.f);
+      }
     }
     tc_fence_before();
   }
+}
+
+template <int DP, bool PLAN>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const FwdShared<DP> sh(smem);
+  const int warp = uniform(threadIdx.x >> 5);
+  if (threadIdx.x == 0) {
+    *sh.abort_flag = 0;
+    *sh.again = *sh.nonfinite_v = 0;
+    sh.init_barriers();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(sh.tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(*sh.tmem_slot);  // S_A, S_B, O_A, O_B
+  int32_t* const status = PLAN || p.status ? p.status : &g_unasked;
+  int units;
+  if (PLAN) {
+    grid_dependency_wait();          // the tile list
+    units = *p.n_tiles;
+  } else {
+    units = own_unit(p, sh.own, reinterpret_cast<int32_t*>(sh.staging));
+  }
+  const int total = uniform(units) * p.Hq;
+  run_units<DP, PLAN, false>(tmQ, tmK, tmV, p, sh, tmem, total, status);
+  __syncthreads();
+  if (*sh.again && !*sh.abort_flag) {  // the same in every thread
+    // nothing is in flight: the barriers start afresh
+    if (threadIdx.x == 0) {
+      for (uint64_t* b = sh.kv_full; b <= sh.drain; ++b) mbar_inval(b);
+      sh.init_barriers();
+    }
+    __syncthreads();
+    tc_fence_after();
+    run_units<DP, PLAN, true>(tmQ, tmK, tmV, p, sh, tmem, total, status);
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

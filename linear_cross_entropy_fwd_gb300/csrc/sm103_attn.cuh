@@ -44,6 +44,10 @@ __device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, mbar_spin(bar, parity, abort_flag, status)) != 0;
 }
 
+__device__ __forceinline__ void mbar_inval(uint64_t* bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // An operand tile in shared memory, 128-byte swizzle (see smem_desc_sw128);
 // offsets within the tile are constants added to the descriptor's lower half.
 struct Operand16 {
@@ -247,6 +251,80 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// --------------------------------------- NaN and infinities in bf16 tiles
+// A product takes 0 times what a mask leaves out, and 0 times NaN or infinity is
+// NaN.  So what is not finite in the rows that a tile on the diagonal masks is
+// cleared in shared memory, and added again where it does belong.
+
+// `any` (0 at first) becomes NaN in a half when one of w's is not finite: w * 0.
+__device__ __forceinline__ void nonfinite_word(uint32_t w, uint32_t& any) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(any) : "r"(w), "r"(0u));
+}
+
+__device__ __forceinline__ bool nonfinite_found(const uint32_t (&any)[4]) {
+  return ((any[0] | any[1] | any[2] | any[3]) & 0x7fff7fffu) != 0;
+}
+
+// What of a pair of bf16 values is not finite (zeros in place of the rest).
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
+  const uint32_t lo = (w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+  const uint32_t hi = (w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+  return w & (lo | hi);
+}
+
+// Clears what is not finite in 16 bytes of shared memory; whether there was any.
+__device__ __forceinline__ bool clear_nonfinite_piece(uint8_t* piece) {
+  const uint4 q = *reinterpret_cast<const uint4*>(piece);
+  uint32_t w[4] = {q.x, q.y, q.z, q.w}, bad = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t b = nonfinite_halves(w[k]);
+    bad |= b;
+    w[k] ^= b;
+  }
+  if (bad) st_shared_v4(smem_addr(piece), w[0], w[1], w[2], w[3]);
+  return bad != 0;
+}
+
+// sum[e] += what is not finite in columns c + e of rows t0 .. t1 of a [T, D] bf16
+// matrix, for the rows within [from, to] of this lane; whether there was any in any
+// lane's.  The bounds t0 and t1 are the warp's.
+__device__ __forceinline__ bool sum_nonfinite(const uint16_t* m, int64_t pitch, int c, int t0,
+                                              int t1, int from, int to, float (&sum)[8]) {
+  uint32_t any = 0;
+  for (int t = t0; t <= t1; ++t) {
+    const uint4 q = *reinterpret_cast<const uint4*>(m + t * pitch + c);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t b = nonfinite_halves(w[k]);
+      any |= b;
+      if (b && t >= from && t <= to) {
+        sum[2 * k] += __uint_as_float(b << 16);
+        sum[2 * k + 1] += __uint_as_float(b & 0xffff0000u);
+      }
+    }
+  }
+  return any != 0;
+}
+
+// dst[c] += f times what is not finite in column c of rows t0 .. to of m, for the
+// columns [c0, c1) in eights.  Each lane has its own `to` and row `dst` (left out when
+// `to` is past t1, the warp's last row).
+__device__ __forceinline__ void add_nonfinite(const uint16_t* m, int64_t pitch, uint16_t* dst,
+                                              int c0, int c1, int t0, int to, int t1, float f) {
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 8) {
+    float sum[8] = {};
+    if (!sum_nonfinite(m, pitch, c, t0, t1, t0, to, sum) || to > t1) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (sum[e] != 0.f)
+        dst[c + e] = static_cast<uint16_t>(
+            pack_bf16x2(fmaf(sum[e], f, __uint_as_float(uint32_t{dst[c + e]} << 16)), 0.f));
+  }
 }
 
 // Fetch a 3D box into L2 ahead of its load.

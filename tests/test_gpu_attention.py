@@ -385,3 +385,37 @@ def test_attention_bits_do_not_depend_on_what_follows(cuda_lib, lens, Hq, Hkv, D
     for name in ("o", "dq"):
         assert torch.equal(got[name][:n - 5], ref[name][:n - 5]), name
     assert torch.equal(got["lse"][:, :n - 5], ref["lse"][:, :n - 5])
+
+
+POISON = [("nan", float("nan")), ("inf", float("inf")), ("-inf", -float("inf"))]
+POISONED_BATCHES = [
+    # lengths, heads, head size, the poisoned sequence and token
+    ([200, 300], 4, 2, 64, 1, 150),             # no plan; heads of a group shared out
+    ([200, 300], 4, 2, 128, 1, 270),            # in the partial last tile
+    ([300, 10], 2, 2, 80, 0, 100),              # first tile; its queries' pair reads it too
+    ([100] * 45 + [700], 8, 8, 128, 45, 129),   # a plan
+    ([60] * 30 + [513], 6, 3, 64, 30, 511),
+]
+
+
+def _poisoned(lens, Hq, Hkv, D, s, t, seed):
+    q, k, v, dO, cu = _inputs(lens, Hq, Hkv, D, seed, pad=2)
+    return q, k, v, dO, cu, int(cu[s]), int(cu[s]) + t, int(cu[s + 1])
+
+
+@pytest.mark.parametrize("what,x", POISON)
+@pytest.mark.parametrize("lens,Hq,Hkv,D,s,t", POISONED_BATCHES)
+def test_attention_nonfinite_v(cuda_lib, lens, Hq, Hkv, D, s, t, what, x):
+    """An element of one token's v reaches that column of o, from that token on."""
+    q, k, v, dO, cu, a, i, b = _poisoned(lens, Hq, Hkv, D, s, t, 31)
+    group, d, h = Hq // Hkv, D // 2 + 3, Hkv - 1
+    o, lse = cuda_lib.flce_attn_fwd(q, k, v, cu)
+    v2 = v.clone()
+    v2[i, h, d] = x
+    o2, lse2 = cuda_lib.flce_attn_fwd(q, k, v2, cu, sync=True)
+    assert torch.equal(lse2, lse)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[i:b, h * group:(h + 1) * group, d] = True
+    assert torch.equal(o2[~hit], o[~hit])
+    want = torch.full((), x, dtype=o.dtype, device=DEV).expand(int(hit.sum()))
+    assert torch.equal(o2[hit].nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
