@@ -352,9 +352,8 @@ FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t 
  * may be empty.  Tokens outside every sequence get zeros in o, dq, dk and dv
  * and -inf in lse; what their inputs hold is not used.
  * A NaN or infinity reaches what the formulas take it to: nothing of another
- * sequence, and in o and lse no token before it.  In the gradients one in k may also
- * reach dq of tokens before it, and one in q or dO dk and dv of tokens after it, in the
- * same block of 128 tokens.
+ * sequence, o, lse and dq of no token before the one whose k or v it is in, and dk and
+ * dv of no token after the one whose q or dO it is in.
  */
 typedef struct flce_attn {
   int64_t T;                 /* tokens, < 2^31 - 256 */

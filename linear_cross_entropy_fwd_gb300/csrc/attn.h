@@ -46,7 +46,7 @@ struct AttnParams {
   int32_t max_depth;    // units of the longest possible sequence
   float* lse;           // [Hq][T]
   float* delta;         // [Hq][T]
-  AttnOut v, o, dO, dq, dk, dv;
+  AttnOut k, v, o, dO, dq, dk, dv;
   int32_t* status;      // may be NULL without a plan
 };
 

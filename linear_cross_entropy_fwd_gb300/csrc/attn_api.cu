@@ -117,6 +117,7 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   }
   p.lse = a->lse;
   p.status = call.status;
+  p.k = AttnOut{const_cast<void*>(a->k), k.token, k.head};
   p.v = AttnOut{const_cast<void*>(a->v), v.token, v.head};
   p.o = AttnOut{a->o, oo.token, oo.head};
   p.dO = AttnOut{const_cast<void*>(a->dO), dO.token, dO.head};

@@ -22,6 +22,9 @@
 // Only tiles on the diagonal and at a sequence's end are masked, by selection,
 // and rows past the end of the sequence are cleared in shared memory where
 // they are summed over (they belong to another sequence and may hold anything).
+// So is what is not finite in the rows that a tile on the diagonal masks (0 times it
+// would be NaN); it is added again where it belongs.  Such rows are looked for only when
+// there is a sign of one: of Q or dO an lse or delta, of K a score, that is not finite.
 //
 // Roles (320 threads): warps 0-7 elementwise (warp w: TMEM lanes 32 (w % 4) ..,
 // columns 64 (w / 4) .. of a tile), warp 8 TMA, warp 9 MMA.
@@ -52,6 +55,20 @@ struct BwdShape {
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same; whether x holds in any of the threads.
+__device__ __forceinline__ bool named_barrier_or(int id, int threads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return any != 0;
 }
 
 template <int BOXES>
@@ -96,14 +113,21 @@ __device__ __forceinline__ void mma_over_rows_ss(uint32_t d_tmem, const Operand1
                (add || k > 0) ? 1u : 0u);
 }
 
-// Rows [valid, 128) of a tile become zeros (the elementwise threads).
+// Rows [valid, 128) of a tile become zeros, and if `look` is set so does what is not
+// finite in the rows before; whether this thread cleared any of the latter (the
+// elementwise threads, each its own pieces).
 template <int BOXES>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int valid) {
-  const int per = (kTile - valid) * 8;  // 16-byte pieces per box
-  for (int i = threadIdx.x; i < per * BOXES; i += kEwThreads)
-    st_shared_v4(smem_addr(tile) + (i / per) * kBoxBytes + valid * 128 + (i % per) * 16, 0, 0, 0,
-                 0);
+__device__ __forceinline__ bool clear_masked(uint8_t* tile, int valid, bool look) {
+  bool found = false;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < 8 * kTile * BOXES; i += kEwThreads) {
+    if (((i >> 3) & (kTile - 1)) >= valid)
+      st_shared_v4(smem_addr(tile) + i * 16, 0, 0, 0, 0);
+    else if (look)
+      found |= clear_nonfinite_piece(tile + i * 16);
+  }
   fence_proxy_async_smem();
+  return found;
 }
 
 // Accumulator columns [c0, c0 + 64) of this warp's rows, times f, to bf16.
@@ -138,6 +162,33 @@ __device__ __forceinline__ void put_partial(uint32_t taddr, uint8_t* mat, int ro
       st_shared_v4(smem_addr(mat) + row * (DP * 4) + ((piece ^ (row & 7)) << 4), r[4 * i],
                    r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
     }
+  }
+}
+
+// Accumulator columns [c0, c0 + 64) of this thread's row of dV, plus what is not finite
+// in dO of its key's own token, `from`, to the end of the tile (token t1), for each of
+// this CTA's heads; t0 is the tile's first token.
+__device__ __forceinline__ void add_nonfinite_dO(const AttnParams& p, uint32_t taddr, int c0,
+                                                 int head0, int heads, int t0, int from, int t1) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(taddr + c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const int col = c0 + c + 8 * part;
+      float sum[8] = {};
+      if (col < p.D)
+        for (int h = head0; h < head0 + heads; ++h)
+          sum_nonfinite(static_cast<const uint16_t*>(p.dO.p) + h * p.dO.head, p.dO.token, col, t0,
+                        t1, from, t1, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        r[8 * part + e] = __float_as_uint(__uint_as_float(r[8 * part + e]) + sum[e]);
+    }
+    tmem_st_32x32b_x16(taddr + c, r);
+    tmem_st_wait();
   }
 }
 
@@ -234,11 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = bars + 14;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* cleared_dO = abort_flag + 1;  // something in a tile on the diagonal
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 15; ++i) mbar_init(&bars[i], (i == 11 || i == 13) ? 8 : 1);
-    *abort_flag = 0;
+    *abort_flag = *cleared_dO = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -351,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = qt == kt || valid < kTile;
       float* lse2 = rows + s * 256;
       lse2[tid] = next;
-      named_barrier(1, kEwThreads);
+      const bool look = named_barrier_or(
+          1, kEwThreads, qt == kt && (__float_as_uint(next) & 0x7f800000u) == 0x7f800000u);
       next = fetch(it + 1);
       const float* dl = lse2 + kTile + 64 * half;
       const float* ls = lse2 + 64 * half;
@@ -386,11 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                      pack_bf16x2(P[8 * i + 2], P[8 * i + 3]),
                      pack_bf16x2(P[8 * i + 4], P[8 * i + 5]),
                      pack_bf16x2(P[8 * i + 6], P[8 * i + 7]));
-      if (valid < kTile) {
-        // S^T of this tile is complete, so Q is only read again by dK
+      if (valid < kTile || look) {
+        // S^T of this tile is complete, so Q is only read again by dK, and after dP^T
+        // (issued before this iteration's wait for P) dO only by dV
         ok = uniform_wait(&o_full[s], (it >> 1) & 1, abort_flag, p.status) && ok;
-        clear_rows<S::kBoxes>(smO + s * TB, valid);
-        clear_rows<S::kBoxes>(smQ + s * TB, valid);
+        ok = uniform_wait(dp_full, it & 1, abort_flag, p.status) && ok;
+        if (clear_masked<S::kBoxes>(smO + s * TB, valid, look)) *cleared_dO = 1;
+        clear_masked<S::kBoxes>(smQ + s * TB, valid, look);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -437,6 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // turn.
       const int key0 = kt * kTile + 32 * quarter;
       const int64_t tok = static_cast<int64_t>(t.start) + key0;
+      if (*cleared_dO && half < DP / 64) {
+        const int t0 = t.start + kt * kTile;
+        const int end = (kt + 1) * kTile < t.len ? (kt + 1) * kTile : t.len;
+        add_nonfinite_dO(p, tDV + lanes + 64 * half, 64 * half, head0, heads, t0, t0 + row,
+                         t.start + end - 1);
+      }
       uint16_t* dv = static_cast<uint16_t*>(p.dv.p) + tok * p.dv.token + kvh * p.dv.head;
       uint16_t* dk = static_cast<uint16_t*>(p.dk.p) + tok * p.dk.token + kvh * p.dk.head;
 #pragma unroll 1
@@ -509,11 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = bars + 14;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* cleared_k = abort_flag + 1;  // something in the tile on the diagonal
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 15; ++i) mbar_init(&bars[i], (i == 12 || i == 13) ? 8 : 1);
-    *abort_flag = 0;
+    *abort_flag = *cleared_k = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -609,7 +671,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dp_read);
-      named_barrier(2 + quarter, 64);  // the other half has read S too
+      bool look = false;
+      if (diag) {
+        // a row of K that is not finite has no finite score
+        float any[4] = {};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) any[i & 3] = fmaf(P[i], 0.f, any[i & 3]);
+        look = named_barrier_or(1, kEwThreads, !(any[0] + any[1] + (any[2] + any[3]) == 0.f));
+      } else {
+        named_barrier(2 + quarter, 64);  // the other half has read S too
+      }
       tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 64; ++i) d[i] = fast_exp2(fmaf(P[i], c, -lse2)) * (d[i] - delta);
@@ -623,7 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_32x32b_x32(tSj + lanes + 32 * half, w);
       tmem_st_wait();
       // S of this tile is complete, so K is only read again by dQ
-      if (diag && t.len - q0 < kTile) clear_rows<S::kBoxes>(smK + (j % 3) * TB, t.len - q0);
+      if (diag && (look || t.len - q0 < kTile) &&
+          clear_masked<S::kBoxes>(smK + (j % 3) * TB, t.len - q0, look))
+        *cleared_k = 1;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
@@ -633,9 +706,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every MMA is done: the key tiles' buffers stage the stores
       const int r0 = 32 * quarter;
       uint16_t* dq = static_cast<uint16_t*>(p.dq.p) + (tok - lane) * p.dq.token + h * p.dq.head;
-      if (half < DP / 64)
+      if (half < DP / 64) {
         store_cols(tDQ + lanes + 64 * half, p.scale, smK + warp * 4096, dq + 64 * half, p.dq.token,
                    t.len - q0 - r0, p.D - 64 * half);
+        if (*cleared_k) {  // K times a dS that is 0, if it is finite: NaN
+          const int end = q0 + r0 + 32 < t.len ? q0 + r0 + 32 : t.len;
+          add_nonfinite(static_cast<const uint16_t*>(p.k.p) + kvh * p.k.head, p.k.token,
+                        dq + lane * p.dq.token, 64 * half,
+                        p.D < 64 * half + 64 ? p.D : 64 * half + 64, t.start + q0,
+                        static_cast<int>(tok), t.start + end - 1, 0.f);
+        }
+      }
     }
     tc_fence_before();
   }

@@ -419,3 +419,80 @@ def test_attention_nonfinite_v(cuda_lib, lens, Hq, Hkv, D, s, t, what, x):
     assert torch.equal(o2[~hit], o[~hit])
     want = torch.full((), x, dtype=o.dtype, device=DEV).expand(int(hit.sum()))
     assert torch.equal(o2[hit].nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+
+
+@pytest.mark.parametrize("what,x", POISON)
+@pytest.mark.parametrize("lens,Hq,Hkv,D,s,t", POISONED_BATCHES)
+def test_attention_nonfinite_k(cuda_lib, lens, Hq, Hkv, D, s, t, what, x):
+    """A token's k reaches the outputs and dq of no token before it."""
+    q, k, v, dO, cu, a, i, b = _poisoned(lens, Hq, Hkv, D, s, t, 32)
+    group, h = Hq // Hkv, Hkv - 1
+    ref = _run(cuda_lib, q, k, v, dO, cu)
+    k2 = k.clone()
+    k2[i, h, 5] = x
+    got = _run(cuda_lib, q, k2, v, dO, cu)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[i:b, h * group:(h + 1) * group] = True
+    assert torch.equal(got["o"][~hit], ref["o"][~hit])
+    assert torch.equal(got["lse"].T[~hit], ref["lse"].T[~hit])
+    assert torch.equal(got["dq"][~hit], ref["dq"][~hit])
+    if what == "nan":
+        assert bool(got["o"][hit].isnan().all() and got["dq"][hit].isnan().all())
+    else:  # a score of -inf leaves o finite, and dq in that column 0 times infinity
+        assert not bool(got["dq"][hit][:, 5].isfinite().any())
+    hit = torch.zeros(k.shape[:2], dtype=torch.bool, device=DEV)
+    hit[a:b, h] = True
+    for n in ("dk", "dv"):
+        assert torch.equal(got[n][~hit], ref[n][~hit]), n
+        if what == "nan":
+            assert bool(got[n][hit].isnan().all()), n
+
+
+@pytest.mark.parametrize("what,x", POISON)
+@pytest.mark.parametrize("lens,Hq,Hkv,D,s,t", POISONED_BATCHES)
+def test_attention_nonfinite_q(cuda_lib, lens, Hq, Hkv, D, s, t, what, x):
+    """One head's q of one token reaches its own o and dq, and dk and dv of the tokens
+    that it sees: none after it."""
+    q, k, v, dO, cu, a, i, b = _poisoned(lens, Hq, Hkv, D, s, t, 33)
+    h = Hq - 1
+    kvh = h // (Hq // Hkv)
+    ref = _run(cuda_lib, q, k, v, dO, cu)
+    q2 = q.clone()
+    q2[i, h, 5] = x
+    got = _run(cuda_lib, q2, k, v, dO, cu)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[i, h] = True
+    for n in ("o", "dq"):
+        assert torch.equal(got[n][~hit], ref[n][~hit]), n
+        assert bool(got[n][hit].isnan().all()), n
+    assert torch.equal(got["lse"].T[~hit], ref["lse"].T[~hit])
+    hit = torch.zeros(k.shape[:2], dtype=torch.bool, device=DEV)
+    hit[a:i + 1, kvh] = True
+    for n in ("dk", "dv"):
+        assert torch.equal(got[n][~hit], ref[n][~hit]), n
+        assert bool(got[n][hit].isnan().all()), n
+
+
+@pytest.mark.parametrize("what,x", POISON)
+@pytest.mark.parametrize("lens,Hq,Hkv,D,s,t", POISONED_BATCHES)
+def test_attention_nonfinite_dO(cuda_lib, lens, Hq, Hkv, D, s, t, what, x):
+    """An element of one head's dO of one token reaches its own dq, dk of the tokens it
+    sees, and that column of their dv: none after it."""
+    q, k, v, dO, cu, a, i, b = _poisoned(lens, Hq, Hkv, D, s, t, 34)
+    h, d = 0, D // 2 + 1
+    ref = _run(cuda_lib, q, k, v, dO, cu)
+    dO2 = dO.clone()
+    dO2[i, h, d] = x
+    got = _run(cuda_lib, q, k, v, dO2, cu)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[i, h] = True
+    assert torch.equal(got["dq"][~hit], ref["dq"][~hit])
+    assert not bool(got["dq"][hit].isfinite().any())
+    hit = torch.zeros(k.shape[:2], dtype=torch.bool, device=DEV)
+    hit[a:i + 1, 0] = True
+    assert torch.equal(got["dk"][~hit], ref["dk"][~hit])
+    assert not bool(got["dk"][hit].isfinite().any())
+    hit = torch.zeros_like(k, dtype=torch.bool)
+    hit[a:i + 1, 0, d] = True
+    assert torch.equal(got["dv"][~hit], ref["dv"][~hit])
+    assert not bool(got["dv"][hit].isfinite().any())
