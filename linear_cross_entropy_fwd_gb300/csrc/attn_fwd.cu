@@ -40,6 +40,8 @@
 //
 // Roles (320 threads): warps 0-3 softmax and output of tile A, 4-7 of tile B
 // (warp w: TMEM lanes 32 (w % 4) ..), warp 8 TMA, warp 9 MMA.
+#include <cfloat>
+
 #include "attn.h"
 #include "host_util.h"
 #include "sm103_attn.cuh"
@@ -417,7 +419,7 @@ __device__ __forceinline__ void run_units(const CUtensorMap& tmQ, const CUtensor
         const float mx = c * fmaxf(max3(mxs[0], mxs[1], mxs[2]),
                                    max3(max3(mxs[3], mxs[4], mxs[5]), mxs[6], mxs[7]));
         if (j == 0) {
-          m = mx;
+          m = fmaxf(mx, -FLT_MAX);  // a tile may score nothing but -inf (k of infinities)
         } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
           // S_j complete means every MMA issued before it is: O is at rest.  Rows that
           // need no rescaling keep m (f = 1), so that no row's bits depend on the

@@ -496,3 +496,20 @@ def test_attention_nonfinite_dO(cuda_lib, lens, Hq, Hkv, D, s, t, what, x):
     hit[a:i + 1, 0, d] = True
     assert torch.equal(got["dv"][~hit], ref["dv"][~hit])
     assert not bool(got["dv"][hit].isfinite().any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_scores_of_minus_infinity(cuda_lib, D):
+    """Keys that score -inf count for nothing, also where they fill the first key tile;
+    a row that sees no others has an lse of -inf and no o."""
+    lens, cut = [300, 40], 140
+    q, k, v, dO, cu = _inputs(lens, 2, 1, D, 35)
+    q, k = q.clone(), k.clone()
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k[:cut, :, 0] = -math.inf
+    o, lse = cuda_lib.flce_attn_fwd(q, k, v, cu, sync=True)
+    val, tol = _reference(q, k, v, dO, lens, D ** -0.5)
+    seen = slice(cut, sum(lens))
+    _close("o", o[seen], val["o"][seen], tol["o"][seen])
+    _close("lse", lse[:, seen], val["lse"][:, seen], tol["lse"][:, seen])
+    assert bool((lse[:, :cut] == -math.inf).all() and o[:cut].isnan().all())
