@@ -398,9 +398,10 @@ FLCE_API size_t flce_attn_sizeof(void);
  *   polynomial s (a + b s^2 + c s^4) that takes singular values of [0, 1] out
  *   of the range of the products (|s| < 3.8, |b s^2 + c s^4| < 15) within
  *   `steps` steps (1 .. 64) is refused with FLCE_ERR_ARG.
- *   eps >= 0; a matrix of zeros gives zeros when eps > 0.
+ *   eps >= 0; a matrix of zeros gives zeros when eps > 0, and NaN when eps == 0.
  * Products take fp16 operands with fp32 sums, beside an fp32 X; the result is
- * rounded to bf16 once.  |G|_F is summed in fp32 (finite for |G_ij| < 1e19).
+ * rounded to bf16 once.  |G|_F is summed in fp32, with G scaled by a power of two
+ * where fp32 would not hold the squares: any finite entries will do.
  * Scratch: about 8 bytes per element of G and 4 per element of A.
  */
 FLCE_API int flce_orthogonalize(const void* G, int64_t batch, int64_t rows, int64_t cols,

@@ -803,13 +803,34 @@ __device__ float cta_sum(float s) {
   return all;
 }
 
-// parts[b][x] = sum of squares of the x-th share of matrix b.
-template <int ELT>
-__global__ void __launch_bounds__(kNormThreads)
-    ortho_norm(const void* g, int64_t elems, int vec, float* parts) {
-  grid_launch_dependents();
+// The largest |x| over the CTA, in every thread.
+__device__ float cta_max(float x) {
+  __shared__ float part[kNormThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float all = 0.f;
+#pragma unroll
+  for (int w = 0; w < kNormThreads / 32; ++w) all = fmaxf(all, part[w]);
+  __syncthreads();
+  return all;
+}
+
+// A sum of squares: 4^exponent times sum.
+struct Part {
+  float sum;
+  int32_t exponent;
+};
+
+// Squares below 2^-126 lose bits, and those of 2^40 elements lose less than 2^-109 in
+// all; a sum of this and more, and finite, is as good as fp32 makes it.
+constexpr float kSumLow = 0x1p-80f;
+
+// f(element) for the elements of this thread's share of a matrix, in order.
+template <int ELT, class F>
+__device__ __forceinline__ void for_share(const void* g, int64_t elems, int vec, F f) {
   const int64_t base = static_cast<int64_t>(blockIdx.y) * elems;
-  float s = 0.f;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kNormThreads;
   if (vec) {
@@ -823,30 +844,53 @@ __global__ void __launch_bounds__(kNormThreads)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (ELT == 4) {
-          const float f = __uint_as_float(w[k]);
-          s = fmaf(f, f, s);
+          f(__uint_as_float(w[k]));
         } else {
-          const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
-          s = fmaf(lo, lo, s);
-          s = fmaf(hi, hi, s);
+          f(__uint_as_float(w[k] << 16));
+          f(__uint_as_float(w[k] & 0xffff0000u));
         }
       }
     }
   } else {
 #pragma unroll 4
-    for (int64_t i = me; i < elems; i += step) {
-      const float f = load1<ELT>(g, base + i);
-      s = fmaf(f, f, s);
-    }
+    for (int64_t i = me; i < elems; i += step) f(load1<ELT>(g, base + i));
   }
-  s = cta_sum(s);
-  if (threadIdx.x == 0) parts[static_cast<int64_t>(blockIdx.y) * kMaxParts + blockIdx.x] = s;
+}
+
+// The sum of squares of a share whose plain sum was not: each element scaled by a power
+// of two that takes the largest to about 1, and added in the same order, so that a power
+// of two in G changes nothing else.
+template <int ELT>
+__device__ __noinline__ Part scaled_sum(const void* g, int64_t elems, int vec) {
+  float top = 0.f;
+  for_share<ELT>(g, elems, vec, [&](float x) { top = fmaxf(top, fabsf(x)); });
+  top = cta_max(top);
+  if (!(top > 0.f) || isinf(top)) return Part{top, 0};
+  int e = ilogbf(top);
+  e = e < -126 ? -126 : e > 126 ? 126 : e;  // 2^-e is exact
+  const float f = ldexpf(1.f, -e);
+  float s = 0.f;
+  for_share<ELT>(g, elems, vec, [&](float x) { s = fmaf(x * f, x * f, s); });
+  return Part{cta_sum(s), e};
+}
+
+// parts[b][x] = sum of squares of the x-th share of matrix b.
+template <int ELT>
+__global__ void __launch_bounds__(kNormThreads)
+    ortho_norm(const void* g, int64_t elems, int vec, Part* parts) {
+  grid_launch_dependents();
+  float s = 0.f;
+  for_share<ELT>(g, elems, vec, [&](float x) { s = fmaf(x, x, s); });
+  Part part{cta_sum(s), 0};
+  if (part.sum < kSumLow || isinf(part.sum))  // the same in every thread
+    part = scaled_sum<ELT>(g, elems, vec);
+  if (threadIdx.x == 0) parts[static_cast<int64_t>(blockIdx.y) * kMaxParts + blockIdx.x] = part;
 }
 
 struct SplitParams {
   const void* g;
   int64_t rows, cols;      // of G
-  const float* parts;
+  const Part* parts;
   int32_t n_parts;
   float eps;
   float* x;                // [k][ldx]
@@ -854,13 +898,33 @@ struct SplitParams {
   int64_t ldx, ldh, x_stride, h_stride;
 };
 
-// 1 / (|G_b| + eps), from the partial sums of the launch before.
-__device__ float inverse_norm(const SplitParams& p, int b) {
+// X = G * scale * inverse, from the partial sums of the launch before.
+struct Normal {
+  float scale;    // a power of two: 1 unless |G_b| is far from it
+  float inverse;  // 1 / ((|G_b| + eps) * scale)
+  __device__ __forceinline__ float operator()(float g) const { return g * scale * inverse; }
+};
+
+__device__ Normal normal_of(const SplitParams& p, int b) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const float part =
-      threadIdx.x < p.n_parts ? p.parts[static_cast<int64_t>(b) * kMaxParts + threadIdx.x] : 0.f;
-  return 1.f / (sqrtf(cta_sum(part)) + p.eps);
+  constexpr int kNone = -1000;
+  Part part{0.f, kNone};
+  if (threadIdx.x < p.n_parts) {
+    part = p.parts[static_cast<int64_t>(b) * kMaxParts + threadIdx.x];
+    if (part.sum == 0.f) part.exponent = kNone;  // zeros are of any scale
+  }
+  __shared__ int exponent;
+  if (threadIdx.x == 0) exponent = kNone;
+  __syncthreads();
+  const int e = __reduce_max_sync(0xffffffffu, part.exponent);
+  if ((threadIdx.x & 31) == 0) atomicMax(&exponent, e);
+  __syncthreads();
+  const int top = exponent == kNone ? 0 : exponent;
+  if (part.exponent != kNone && part.exponent != top)
+    part.sum = ldexpf(part.sum, 2 * (part.exponent - top));
+  const float scale = ldexpf(1.f, -top);
+  return Normal{scale, 1.f / (sqrtf(cta_sum(part.sum)) + p.eps * scale)};
 }
 
 // X = G / (|G| + eps) in fp32 and, times 4096, in fp16, for G with rows of
@@ -868,7 +932,7 @@ __device__ float inverse_norm(const SplitParams& p, int b) {
 template <int ELT>
 __global__ void __launch_bounds__(kNormThreads) ortho_split_rows(const SplitParams p) {
   const int b = static_cast<int>(blockIdx.y);
-  const float inv = inverse_norm(p, b);
+  const Normal normal = normal_of(p, b);
   const uint8_t* g = static_cast<const uint8_t*>(p.g) + static_cast<int64_t>(b) * p.rows * p.cols * ELT;
   const int64_t per_row = p.ldx / 8, n = p.rows * per_row;
 #pragma unroll 2
@@ -894,7 +958,7 @@ __global__ void __launch_bounds__(kNormThreads) ortho_split_rows(const SplitPara
       }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= inv;
+    for (int k = 0; k < 8; ++k) v[k] = normal(v[k]);
     float4* x = reinterpret_cast<float4*>(p.x + b * p.x_stride + r * p.ldx + c);
     x[0] = make_float4(v[0], v[1], v[2], v[3]);
     x[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -912,7 +976,7 @@ template <int ELT, bool TRANSPOSED>
 __global__ void __launch_bounds__(kNormThreads) ortho_split(const SplitParams p) {
   __shared__ float tile[TRANSPOSED ? 64 : 1][65];
   const int b = static_cast<int>(blockIdx.z);
-  const float inv = inverse_norm(p, b);
+  const Normal normal = normal_of(p, b);
   const int64_t base = static_cast<int64_t>(b) * p.rows * p.cols;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
   float* x = p.x + b * p.x_stride;
@@ -933,7 +997,7 @@ __global__ void __launch_bounds__(kNormThreads) ortho_split(const SplitParams p)
     const int64_t k = TRANSPOSED ? p.cols : p.rows, n = TRANSPOSED ? p.rows : p.cols;
     if (r >= k) continue;
     float v = 0.f;
-    if (c < n) v = (TRANSPOSED ? tile[tx][ty + i] : load1<ELT>(p.g, base + r * p.cols + c)) * inv;
+    if (c < n) v = normal(TRANSPOSED ? tile[tx][ty + i] : load1<ELT>(p.g, base + r * p.cols + c));
     if (c < p.ldx) x[r * p.ldx + c] = v;
     if (c < p.ldh) xh[r * p.ldh + c] = __float2half_rn(v * kHold);
   }
@@ -995,7 +1059,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
   size_t o = 0;
   const size_t B = static_cast<size_t>(batch);
   l.off_parts = o;
-  o += round256(B * kMaxParts * 4);
+  o += round256(B * kMaxParts * sizeof(Part));
   l.off_x = o;
   o += round256(B * static_cast<size_t>(l.k * l.ldx) * 4);
   for (int i = 0; i < 2; ++i) {
@@ -1128,7 +1192,7 @@ cudaError_t launch_small_update(const CUtensorMap& A, const CUtensorMap& X, Orth
 int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps,
         const float* coeffs, float eps, void* out, const Layout& l, uint8_t* w, int32_t* status,
         int sms, cudaStream_t s) {
-  float* parts = reinterpret_cast<float*>(w + l.off_parts);
+  Part* parts = reinterpret_cast<Part*>(w + l.off_parts);
   float* x = reinterpret_cast<float*>(w + l.off_x);
   __half* h[2] = {reinterpret_cast<__half*>(w + l.off_h[0]),
                   reinterpret_cast<__half*>(w + l.off_h[1])};

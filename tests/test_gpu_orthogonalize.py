@@ -180,3 +180,31 @@ def test_orthogonalize_small_side(cuda_lib, shape, dtype):
     got = cuda_lib.flce_orthogonalize(G, sync=True)
     _check(got, _reference(G))
     assert torch.equal(got, cuda_lib.flce_orthogonalize(G))
+
+
+@pytest.mark.parametrize("shape", [(150, 260), (2, 90, 33), (700, 640)])
+@pytest.mark.parametrize("power", [-126, -110, -75, 50, 64, 100, 123])
+def test_orthogonalize_far_scales(cuda_lib, shape, power):
+    """Powers of two whose squares fp32 does not hold: the same bits."""
+    G = _matrix("noise", shape, 11, "fp32") * 1024
+    G = torch.where(G.abs() < 2.0 ** -14, G.sign() * 2.0 ** -14, G)  # no entry becomes subnormal
+    s = 2.0 ** power if power > -112 else 2.0 ** (power + 14)
+    ref = cuda_lib.flce_orthogonalize(G, eps=0.0)
+    assert torch.equal(cuda_lib.flce_orthogonalize(G * s, eps=0.0, sync=True), ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_orthogonalize_extreme_entries(cuda_lib, dtype):
+    """The largest entries, subnormal ones, and both in one matrix."""
+    G = _matrix("noise", (120, 333), 12, "fp32") * 1000
+    top = torch.finfo(DT[dtype]).max
+    big = (G / G.abs().max() * top).to(DT[dtype])
+    assert bool(big.isfinite().all())
+    small = (G * 2.0 ** -132).to(DT[dtype])
+    spread = G.to(DT[dtype])
+    spread[5, 7], spread[50, 300] = top, -top / 2
+    both = torch.stack([big, small, spread])
+    got = cuda_lib.flce_orthogonalize(both, eps=0.0, sync=True)
+    _check(got, _reference(both, eps=0.0))
+    # the eps counts beside a norm of its own size only
+    _check(cuda_lib.flce_orthogonalize(big, eps=1.0), _reference(big, eps=1.0))
