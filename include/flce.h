@@ -309,7 +309,7 @@ FLCE_API int flce_fwd_noalloc(const void* X, const void* W, const int64_t* targe
  * to opts->dtype.
  *   W [V, H] and Y [N, H] of type opts->dtype, row-major, contiguous, 16-byte
  *   aligned, H * sizeof(element) a multiple of 16, H <= 2^20; ids [N] int64
- *   (int32 with opts->target_is_int32).
+ *   (int32 with opts->target_is_int32); scale finite.
  * A token whose id is ignore_index gets a row of zeros.  So does a token whose
  * id is outside [0, V), which also reports FLCE_ERR_TARGET.
  */

@@ -27,6 +27,8 @@
 //               goes on a list.  Further CTAs clear what the sort had no time
 //               for, except the rows that have tokens.
 //   3  join     adds the partial rows of each run on the list, in order.
+#include <cmath>
+
 #include "host_util.h"
 #include "sm103.cuh"
 
@@ -605,7 +607,8 @@ int check_embed(const char* who, const void* table, const void* rows, const void
                       "%s: sizes must satisfy 0 <= N < 2^31, 0 < H <= 2^20, 0 < V < 2^31", who);
   if (!table || (N > 0 && (!rows || !ids)))
     return host_error(FLCE_ERR_ARG, "%s: null pointer", who);
-  if (scale != scale) return host_error(FLCE_ERR_ARG, "%s: scale is NaN", who);
+  // (an infinite scale would make NaN of the zeros that ignored tokens get)
+  if (!std::isfinite(scale)) return host_error(FLCE_ERR_ARG, "%s: scale must be finite", who);
   const int elt = dtype == FLCE_FP32 ? 4 : 2;
   if ((H * elt) % 16 != 0)
     return host_error(FLCE_ERR_ALIGN, "%s: H * sizeof(element) = %lld is not a multiple of 16",

@@ -146,3 +146,14 @@ def test_orthogonalize_refusals(lib, kw, status):
     assert lib.flce_orthogonalize(a["G"], a["batch"], a["rows"], a["cols"], a["steps"], c,
                                   a["eps"], a["out"], ctypes.byref(o)) == status
     assert lib.flce_last_error()
+
+
+@pytest.mark.parametrize("scale", [float("inf"), -float("inf")])
+def test_embed_refuses_an_infinite_scale(lib, scale):
+    """0 times it is NaN: ignored tokens would not get their zeros."""
+    o = flce.make_opts(sync=0)
+    assert lib.flce_embed_fwd(A, A, 4, 16, 10, scale, -100, A, ctypes.byref(o)) == flce.FLCE_ERR_ARG
+    assert b"scale" in lib.flce_last_error()
+    assert lib.flce_embed_bwd(A, A, 4, 16, 10, scale, -100, A, 0,
+                              ctypes.byref(o)) == flce.FLCE_ERR_ARG
+    assert b"scale" in lib.flce_last_error()
