@@ -351,6 +351,11 @@ FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t 
  * are reported as FLCE_ERR_ARG and count as no sequence at all.  A sequence
  * may be empty.  Tokens outside every sequence get zeros in o, dq, dk and dv
  * and -inf in lse; what their inputs hold is not used.
+ * Outputs share no element with the inputs or with one another, except that a gradient
+ * may take o's place; slices of one buffer that interleave share none.  Overlaps of o
+ * with q, k, v, and of the gradients with q, k, v, dO and one another, are refused with
+ * FLCE_ERR_ARG where address, strides and sizes tell (same first element; equal token
+ * strides).
  * A NaN or infinity reaches what the formulas take it to: nothing of another
  * sequence, o, lse and dq of no token before the one whose k or v it is in, and dk and
  * dv of no token after the one whose q or dO it is in.

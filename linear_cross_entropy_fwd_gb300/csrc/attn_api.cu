@@ -31,6 +31,29 @@ int operand(Operand* out, const char* name, const void* p, int64_t token, int64_
   return FLCE_OK;
 }
 
+// Whether operands of `na` and `nb` heads share an element, as far as can be told: by
+// their address ranges, first elements and, for equal token strides, every pair of
+// heads (interleaved slices of one buffer share none).
+bool shared(const Operand& a, int na, const Operand& b, int nb, int64_t T, int D) {
+  using wide = __int128;  // strides below 2^38, T below 2^31
+  const wide a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const wide row = 2 * D, s = 2 * wide{a.token};
+  const wide wa = 2 * wide{na - 1} * a.head + row, wb = 2 * wide{nb - 1} * b.head + row;
+  if (a0 + (T - 1) * s + wa <= b0 || b0 + 2 * (T - 1) * wide{b.token} + wb <= a0) return false;
+  if (a0 == b0) return true;
+  if (a.token != b.token || wide{na} * nb > (1 << 16)) return false;  // not told
+  auto mod = [&](wide x) { return (x % s + s) % s; };
+  const wide off = mod(b0 - a0);
+  if (off >= wa && off + wb <= s) return false;  // beside each other in every token
+  for (int i = 0; i < na; ++i)
+    for (int j = 0; j < nb; ++j) {
+      const wide d = b0 + 2 * wide{j} * b.head - (a0 + 2 * wide{i} * a.head);
+      const wide r = mod(d), t = (d - r) / s;  // t tokens and r bytes apart
+      if ((r < row && t < T && -t < T) || (s - r < row && t + 1 < T && -t - 1 < T)) return true;
+    }
+  return false;
+}
+
 int tensor_map(CUtensorMap* m, const Operand& t, int64_t T, int heads, int D, const char* name) {
   const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(heads),
                             static_cast<uint64_t>(T)};
@@ -74,6 +97,29 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
       if ((rc = operand(&dq, "dq", a->dq, a->dq_token, a->dq_head, T, a->heads_q, D))) return rc;
       if ((rc = operand(&dk, "dk", a->dk, a->dk_token, a->dk_head, T, a->heads_kv, D))) return rc;
       if ((rc = operand(&dv, "dv", a->dv, a->dv_token, a->dv_head, T, a->heads_kv, D))) return rc;
+    }
+    // An output over what other CTAs, or the same one, still read; o over q too (a
+    // second pass over a unit, see attn_fwd.cu).  The gradients may take o's place:
+    // only delta is formed from it, before the first of them is written.
+    const struct { const char* name; Operand t; int heads; } in[] = {
+        {"q", q, a->heads_q}, {"k", k, a->heads_kv}, {"v", v, a->heads_kv}, {"dO", dO, a->heads_q}},
+        out[] = {{"dq", dq, a->heads_q}, {"dk", dk, a->heads_kv}, {"dv", dv, a->heads_kv}};
+    auto apart = [&](const auto& x, const auto& y) {
+      return shared(x.t, x.heads, y.t, y.heads, T, D)
+                 ? host_error(FLCE_ERR_ARG, "%s overlaps %s", x.name, y.name)
+                 : FLCE_OK;
+    };
+    if (backward) {
+      for (int i = 0; i < 3; ++i) {
+        for (const auto& x : in)
+          if ((rc = apart(out[i], x))) return rc;
+        for (int j = 0; j < i; ++j)
+          if ((rc = apart(out[i], out[j]))) return rc;
+      }
+    } else {
+      for (int j = 0; j < 3; ++j)
+        if (shared(oo, a->heads_q, in[j].t, in[j].heads, T, D))
+          return host_error(FLCE_ERR_ARG, "o overlaps %s", in[j].name);
     }
   }
   int sms = 0;

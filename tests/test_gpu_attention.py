@@ -513,3 +513,33 @@ def test_attention_scores_of_minus_infinity(cuda_lib, D):
     _close("o", o[seen], val["o"][seen], tol["o"][seen])
     _close("lse", lse[:, seen], val["lse"][:, seen], tol["lse"][:, seen])
     assert bool((lse[:, :cut] == -math.inf).all() and o[:cut].isnan().all())
+
+
+def test_attention_interleaved_and_in_place(cuda_lib):
+    """q, k and v by turns within each head, gradients likewise, or over o; outputs over
+    what is still read are refused."""
+    T, H, D = 330, 3, 64
+    lens = [200, 130]
+    q, k, v, dO, cu = _inputs(lens, H, H, D, 36)
+    ref = _run(cuda_lib, q, k, v, dO, cu)
+    buf = torch.stack([q, k, v], 2).contiguous()          # [T, H, 3, D]
+    a, b, c = buf.unbind(2)
+    o, lse = cuda_lib.flce_attn_fwd(a, b, c, cu)
+    grads = torch.empty_like(buf)
+    cuda_lib.flce_attn_bwd(dO, a, b, c, o, lse, cu, dq=grads[:, :, 0], dk=grads[:, :, 1],
+                           dv=grads[:, :, 2])
+    assert torch.equal(o, ref["o"]) and torch.equal(lse, ref["lse"])
+    for i, n in enumerate(("dq", "dk", "dv")):
+        assert torch.equal(grads[:, :, i], ref[n]), n
+    for n in ("dq", "dk", "dv"):
+        over = o.clone()
+        got = dict(zip(("dq", "dk", "dv"),
+                       cuda_lib.flce_attn_bwd(dO, q, k, v, over, lse, cu, **{n: over})))
+        for m in got:
+            assert torch.equal(got[m], ref[m]), (n, m)
+    for kw in (dict(out=a), dict(out=b)):
+        with pytest.raises(cuda_lib.FlceError, match="overlaps"):
+            cuda_lib.flce_attn_fwd(a, b, c, cu, **kw)
+    for kw in (dict(dq=a), dict(dk=b), dict(dv=c), dict(dq=dO), dict(dk=grads[:, :, 0], dq=grads[:, :, 0])):
+        with pytest.raises(cuda_lib.FlceError, match="overlaps"):
+            cuda_lib.flce_attn_bwd(dO, a, b, c, o, lse, cu, **kw)

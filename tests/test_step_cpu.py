@@ -157,3 +157,54 @@ def test_embed_refuses_an_infinite_scale(lib, scale):
     assert lib.flce_embed_bwd(A, A, 4, 16, 10, scale, -100, A, 0,
                               ctypes.byref(o)) == flce.FLCE_ERR_ARG
     assert b"scale" in lib.flce_last_error()
+
+
+# Token stride of the operands below: q, k and v as slices of one projection's output,
+# and their gradients as slices of another.
+QKV = dict(q=A, k=A + 2 * 256, v=A + 2 * 384, o=A + (1 << 30), dO=A + (2 << 30),
+           dq=A + (3 << 30), dk=A + (3 << 30) + 2 * 256, dv=A + (3 << 30) + 2 * 384,
+           **{n + "_token": 512 for n in ("q", "k", "v", "dq", "dk", "dv")})
+HEAD_BY_HEAD = {f: x for i, n in enumerate(("dq", "dk", "dv")) for f, x in (
+    (n, A + (3 << 30) + 2 * 64 * i), (n + "_token", 4 * 192), (n + "_head", 192))}
+
+
+def _attn_statuses(lib, kw):
+    """Statuses of both entries; a workspace of 0 bytes keeps an accepted call off the GPU."""
+    a = _attn(T=50000, batch=300, **{**QKV, **kw})
+    o = flce.make_opts(sync=0)
+    o.workspace, o.workspace_bytes = A, 0
+    return [fn(ctypes.byref(a), ctypes.byref(o)) for fn in (lib.flce_attn_fwd, lib.flce_attn_bwd)]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(),                                                       # beside each other per token
+    {**HEAD_BY_HEAD, "heads_kv": 4, "k_token": 512, "v": A + (4 << 30)},  # per head
+    dict(dq=A + (1 << 30)),                                       # a gradient over o
+    dict(o=A + 2 * 50000 * 512),                                  # right behind the projection
+    dict(dO=A + (3 << 30) - 2 * 50000 * 256),                     # right before the gradients
+])
+def test_attention_accepts_disjoint_layouts(lib, kw):
+    accepted = (flce.FLCE_ERR_ARCH, flce.FLCE_ERR_CUDA, flce.FLCE_ERR_WORKSPACE)
+    for status in _attn_statuses(lib, kw):
+        assert status in accepted, lib.flce_last_error()
+
+
+@pytest.mark.parametrize("kw,forward", [
+    (dict(o=A, o_token=512), True),                               # o over q
+    (dict(o=A + 2 * 256, o_token=512), True),                     # o over k and v
+    (dict(o=A + 2 * 48, o_token=512), True),                      # a part of a row
+    (dict(o=A + 2 * (512 * 49999 + 256), o_token=512), True),     # the last token of k
+    (dict(o=A + 2 * (512 * 50000 - 64), o_token=512), True),      # the end of v
+    (dict(dq=A, dq_token=512), False),                            # in place
+    (dict(dk=A + 2 * 256, dk_token=512), False),
+    (dict(dv=A + 2 * 384, dv_token=512), False),
+    (dict(dq=A + (2 << 30)), False),                              # dq over dO
+    (dict(dv=A + (3 << 30) + 2 * 256), False),                    # dv over dk
+    (dict(dk=A + (3 << 30) + 2 * 200), False),                    # dk into dq's last head
+    (dict(dv=A + (3 << 30) + 2 * 512 * 7 + 2 * 128), False),      # dq's heads, tokens later
+])
+def test_attention_refuses_overlaps(lib, kw, forward):
+    fwd, bwd = _attn_statuses(lib, kw)
+    assert (fwd if forward else bwd) == flce.FLCE_ERR_ARG
+    if not forward:
+        assert b"overlaps" in lib.flce_last_error()
