@@ -85,7 +85,7 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   if ((T / kTile + a->batch) * a->heads_q >= (int64_t{1} << 31))
     return host_error(FLCE_ERR_ARG, "(T / 128 + batch) * heads_q must be below 2^31");
   int rc = FLCE_OK;
-  Operand q, k, v, oo, dO{}, dq{}, dk{}, dv{};
+  Operand q{}, k{}, v{}, oo{}, dO{}, dq{}, dk{}, dv{};
   if (T > 0) {
     if ((rc = operand(&q, "q", a->q, a->q_token, a->q_head, T, a->heads_q, D))) return rc;
     if ((rc = operand(&k, "k", a->k, a->k_token, a->k_head, T, a->heads_kv, D))) return rc;
@@ -142,18 +142,18 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   p.max_tiles = static_cast<int32_t>(max_tiles);
   p.unit = unit;
   p.max_depth = static_cast<int32_t>((T + kTile * unit - 1) / (kTile * unit));
-  const size_t b_tiles = round256(static_cast<size_t>(max_tiles) * sizeof(AttnTile));
+  const size_t b_tiles = T > 0 ? round256(static_cast<size_t>(max_tiles) * sizeof(AttnTile)) : 0;
   const size_t b_bucket = round256((static_cast<size_t>(p.max_depth) + 2) * 4);
   const size_t b_delta =
       backward ? round256(static_cast<size_t>(a->heads_q) * static_cast<size_t>(T) * 4) : 0;
   const bool direct = !backward && a->batch >= 1 && a->batch <= kDirectSeqs &&
                       max_tiles * a->heads_q <= sms;
-  const bool planned = T > 0 && !direct;
+  // without tokens the plan only checks the offsets, for a caller who looks at the status
+  const bool planned = T > 0 ? !direct : o.sync || o.status_dev;
   StepCall call;
   if ((rc = call.begin(o, planned ? 256 + b_tiles + b_bucket + b_delta : 0,
                        planned ? StepCall::kKernelClears : StepCall::kIfAsked)))
     return rc;
-  if (T == 0) return call.end(FLCE_OK);
   if (planned) {
     uint8_t* w = call.scratch;
     p.n_tiles = reinterpret_cast<int32_t*>(w);
@@ -171,7 +171,7 @@ int attention(const flce_attn* a, const flce_opts* opts, bool backward) {
   p.dk = AttnOut{a->dk, dk.token, dk.head};
   p.dv = AttnOut{a->dv, dv.token, dv.head};
   cudaError_t e = planned ? launch_attn_plan(p, backward, sms, call.stream) : cudaSuccess;
-  if (max_tiles > 0) {
+  if (T > 0 && max_tiles > 0) {
     if (backward) {
       if (e == cudaSuccess) e = launch_attn_dkdv(mq, mk, mv, mO, p, sms, call.stream);
       if (e == cudaSuccess) e = launch_attn_dq(mq, mk, mv, mO, p, call.stream);

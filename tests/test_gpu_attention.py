@@ -543,3 +543,22 @@ def test_attention_interleaved_and_in_place(cuda_lib):
     for kw in (dict(dq=a), dict(dk=b), dict(dv=c), dict(dq=dO), dict(dk=grads[:, :, 0], dq=grads[:, :, 0])):
         with pytest.raises(cuda_lib.FlceError, match="overlaps"):
             cuda_lib.flce_attn_bwd(dO, a, b, c, o, lse, cu, **kw)
+
+
+@pytest.mark.parametrize("cu,good", [([0], True), ([0, 0, 0], True), ([0, 5], False), ([-1, 0], False),
+                                     ([2], False)])
+def test_attention_offsets_without_tokens(cuda_lib, cu, good):
+    """No token, but offsets: they are checked all the same."""
+    e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(2, 0, device=DEV)
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    info = {}
+    want = cuda_lib.FLCE_OK if good else cuda_lib.FLCE_ERR_ARG
+    cuda_lib.flce_attn_fwd(e, e, e, cu, info=info)
+    assert int(info["status"].item()) == want
+    cuda_lib.flce_attn_bwd(e, e, e, e, e, lse, cu, info=info)
+    assert int(info["status"].item()) == want
+    cuda_lib.flce_attn_fwd(e, e, e, cu)          # nobody looks: nothing to do
+    if not good:
+        with pytest.raises(cuda_lib.FlceError):
+            cuda_lib.flce_attn_bwd(e, e, e, e, e, lse, cu, sync=True)
