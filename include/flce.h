@@ -325,7 +325,8 @@ FLCE_API int flce_embed_fwd(const void* W, const void* ids, int64_t N, int64_t H
  *   dY [N, H] of type opts->dtype; dW [V, H] fp32; alignment as above.
  * Ignored and out-of-range ids take no part (the latter report
  * FLCE_ERR_TARGET).  N == 0 clears dW, or leaves it when accumulate is set.
- * Scratch: 16 bytes per token and two fp32 rows per 4 to 64 tokens;
+ * Scratch: two fp32 rows per 4 to 64 tokens and 8 bytes per token, 24 from 2049 tokens
+ * on (from 4097 beside 64 MiB or more of dW that are cleared while the ids are sorted);
  * opts->workspace_used reports it.
  */
 FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_t V,

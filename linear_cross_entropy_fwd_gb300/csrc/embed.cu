@@ -629,7 +629,7 @@ struct BwdPlan {
 
 // Entries per CTA of the sum: enough CTAs for twelve on each of 152 SMs,
 // within 4 .. kMaxChunk.
-BwdPlan plan_bwd(int64_t N, int64_t H, int64_t V, int elt) {
+BwdPlan plan_bwd(int64_t N, int64_t H, int64_t V, int elt, bool one_cta) {
   BwdPlan b{};
   int bits = 1;
   while ((int64_t{1} << bits) <= V) ++bits;  // keys 0 .. V
@@ -650,7 +650,7 @@ BwdPlan plan_bwd(int64_t N, int64_t H, int64_t V, int elt) {
   o += list;
   for (int i = 0; i < 2; ++i) {
     b.pair[i] = o;
-    if (N > kOneCtaFaster) o += round256(static_cast<size_t>(N) * 8);
+    if (!one_cta) o += round256(static_cast<size_t>(N) * 8);
   }
   b.counts = o;
   o += 256;
@@ -700,9 +700,9 @@ cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, embed_sort_kernel<CTAS>, p);
 }
 
-int run_bwd(const SortParams& sort, const SumParams& sum, int elt, int sms, cudaStream_t s) {
-  FLCE_TRY(one_cta_sorts(sort.N, sort.clear_vecs * 16) ? launch_sort<1>(sort, sms, s)
-                                                       : launch_sort<kSortCtas>(sort, sms, s));
+int run_bwd(const SortParams& sort, const SumParams& sum, int elt, bool one_cta, int sms,
+            cudaStream_t s) {
+  FLCE_TRY(one_cta ? launch_sort<1>(sort, sms, s) : launch_sort<kSortCtas>(sort, sms, s));
   const unsigned slices = (sum.nv + kSumThreads - 1) / kSumThreads;
   const int threads = static_cast<int>(((sum.nv + slices - 1) / slices + 31) / 32 * 32);
   int64_t x = sum.chunks;
@@ -766,7 +766,11 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   int sms = 0;
   if ((rc = host_device(&sms))) return rc;
   const int elt = o.dtype == FLCE_FP32 ? 4 : 2;
-  const BwdPlan b = plan_bwd(N, H, V, elt);
+  const int64_t beside_sort = (kClearBase + N * kClearPerToken) / (H * 4);
+  const int64_t clear_first =
+      accumulate ? 0 : V * H * 4 < kClearSplit || V < beside_sort ? V : beside_sort;
+  const bool one_cta = one_cta_sorts(N, clear_first * H * 4);
+  const BwdPlan b = plan_bwd(N, H, V, elt, one_cta);
   StepCall call;
   if ((rc = call.begin(o, N > 0 ? b.total : 0, StepCall::kIfAsked))) return rc;
   if (N == 0) {
@@ -788,9 +792,6 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   for (int i = 0; i < 2; ++i) sp.pair[i] = reinterpret_cast<uint2*>(w + b.pair[i]);
   sp.counts = reinterpret_cast<uint32_t*>(w + b.counts);
   sp.clear = accumulate ? nullptr : reinterpret_cast<float4*>(dW);
-  const int64_t beside_sort = (kClearBase + N * kClearPerToken) / (H * 4);
-  const int64_t clear_first =
-      accumulate ? 0 : V * H * 4 < kClearSplit || V < beside_sort ? V : beside_sort;
   sp.clear_vecs = clear_first * H / 4;
   sp.fetch = reinterpret_cast<const uint8_t*>(dW);
   sp.fetch_row = H * 4;
@@ -818,7 +819,7 @@ int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t H, int64_
   sm.clear_from = accumulate ? V : clear_first;
   const int64_t rows = kClearUnit / (H * 4);
   sm.clear_rows = static_cast<int32_t>(rows < 1 ? 1 : rows > kMaxClearRows ? kMaxClearRows : rows);
-  return call.end(run_bwd(sp, sm, elt, sms, call.stream));
+  return call.end(run_bwd(sp, sm, elt, one_cta, sms, call.stream));
 }
 
 }  // extern "C"

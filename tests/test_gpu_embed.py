@@ -233,3 +233,40 @@ def test_embed_bwd_large_tables(cuda_lib, N, H, V, dtype, kind):
     assert bool((err <= (n[:, None] + 2) * 2.0 ** -24 * 0.5 * mag).all())
     dW[rows] = 0.0
     assert bool((dW == 0).all())
+
+
+def _check_rows(dW, dY, ids, scale):
+    """As _check_bwd, on the GPU and for the rows that have tokens; the others are zero."""
+    keep = ids != IGN
+    rows, where, n = torch.unique(ids[keep], return_inverse=True, return_counts=True)
+    ref = torch.zeros(rows.numel(), dY.shape[1], dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(ref)
+    ref.index_add_(0, where, dY[keep].double())
+    mag.index_add_(0, where, dY[keep].double().abs())
+    err = (dW[rows].double() - scale * ref).abs()
+    assert bool((err <= (n[:, None] + 2) * 2.0 ** -24 * abs(scale) * mag).all())
+    assert int(dW.any(1).sum()) <= rows.numel() and not dW.isnan().any()
+
+
+@pytest.mark.parametrize("kind", ["uniform", "skewed", "one"])
+@pytest.mark.parametrize("N", [2048, 2049, 4096, 4097])
+def test_embed_bwd_sort_limits(cuda_lib, N, kind):
+    """Around the token counts that one CTA sorts, with a dW that makes it the choice up
+    to 4096 tokens (64 to 192 MiB to clear), and the scratch of either form."""
+    H, V = 1024, 17000
+    assert 64 << 20 <= V * H * 4 < 192 << 20
+    ids = _ids(kind, N, V, N).to(DEV)
+    dY = torch.randn(N, H, generator=torch.Generator().manual_seed(N)).bfloat16().to(DEV)
+    dense, tied = {}, {}
+    dW = torch.full((V, H), float("nan"), device=DEV)
+    cuda_lib.flce_embed_bwd(dY, ids, V, dW=dW, scale=0.5, info=dense)
+    assert int(dense["status"].item()) == 0
+    _check_rows(dW, dY, ids, 0.5)
+    acc = torch.zeros(V, H, device=DEV)
+    cuda_lib.flce_embed_bwd(dY, ids, dW=acc, accumulate=True, scale=0.5, info=tied)
+    assert torch.equal(acc, dW)  # the other sort, the same order
+    lists = 2 * -(-8 * N // 256) * 256
+    assert tied["workspace_bytes"] - dense["workspace_bytes"] == (lists if 2048 < N <= 4096 else 0)
+    ws = torch.empty(dense["workspace_bytes"], dtype=torch.uint8, device=DEV)
+    again = cuda_lib.flce_embed_bwd(dY, ids, V, scale=0.5, workspace=ws)
+    assert torch.equal(again, dW)
