@@ -414,6 +414,15 @@ FLCE_API int flce_orthogonalize(const void* G, int64_t batch, int64_t rows, int6
                                 int32_t steps, const float* coeffs, float eps, void* out,
                                 const flce_opts* opts);
 
+/*
+ * The tile shapes that flce_orthogonalize takes for a step's three products (X X^T,
+ * A^2, B X) on a device of `sms` SMs, so that a test can tell what it reaches:
+ * 0 CTA pairs, 1 single CTAs, 2 K shared out over a cluster, 3 A^2 and B X in one
+ * launch.  Host only.
+ */
+FLCE_API int flce_selftest_ortho_shapes(int64_t batch, int64_t rows, int64_t cols, int32_t sms,
+                                        int32_t shapes[3]);
+
 #ifdef __cplusplus
 }
 #endif

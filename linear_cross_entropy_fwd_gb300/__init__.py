@@ -39,7 +39,7 @@ EXPORTED = ["flce_opts_init", "flce_fwd_bwd", "flce_fwd_bwd_ex", "flce_fwd",
             "flce_last_error", "flce_version", "flce_opts_sizeof", "flce_fwd_noalloc",
             "flce_ce_fwd_bwd", "flce_selftest_wait_expiry", "flce_scale_convert",
             "flce_embed_fwd", "flce_embed_bwd", "flce_attn_fwd", "flce_attn_bwd",
-            "flce_attn_sizeof", "flce_orthogonalize"]
+            "flce_attn_sizeof", "flce_orthogonalize", "flce_selftest_ortho_shapes"]
 
 
 class FlceOpts(ctypes.Structure):
@@ -146,6 +146,8 @@ def load_library(path: str | None = None):
         lib.flce_embed_bwd.restype = i32
         lib.flce_orthogonalize.argtypes = [vp, i64, i64, i64, ctypes.c_int32, vp, f32, vp, po]
         lib.flce_orthogonalize.restype = i32
+        lib.flce_selftest_ortho_shapes.argtypes = [i64, i64, i64, ctypes.c_int32, vp]
+        lib.flce_selftest_ortho_shapes.restype = i32
         pa = ctypes.POINTER(FlceAttn)
         for fn in (lib.flce_attn_fwd, lib.flce_attn_bwd):
             fn.argtypes = [pa, po]

@@ -1134,22 +1134,28 @@ int64_t round_time(int64_t tiles, int64_t at_once, int64_t products, int64_t epi
 // 3000 x 3000 479 us against 576 (78 pairs of tiles on 76 pairs of SMs), 1024 x 16000
 // 414 against 435, 1500 x 4000 260 against 281, 16 of 384 x 2000 261 against 309; but
 // 2304 x 2304 363 against 348, 4096 x 4096 1154 against 1034.
+Shape gemm_shape(int mode, int64_t rows, int64_t cols, int64_t k, int64_t batch, int sms) {
+  auto tiles = [&](int64_t edge) {
+    const int64_t mb = (rows + edge - 1) / edge, nb = (cols + edge - 1) / edge;
+    return (mode != kUpdate ? mb * (mb + 1) / 2 : mb * nb) * batch;
+  };
+  if (mode == kGram && tiles(128) * kSplitCtas <= sms && k >= 2048) return kSplit;
+  const int64_t k_blk = (k + 63) / 64;
+  return round_time(tiles(128), sms, 7 * k_blk, 83) <=
+                 round_time(tiles(256), sms / 2, 10 * k_blk, mode == kUpdate ? 217 : 150)
+             ? kSingle
+             : kPair;
+}
+
 template <int MODE>
 cudaError_t launch_gemm(const CUtensorMap& A, const CUtensorMap& B, const OrthoParams& p, int64_t k,
                         int sms, cudaStream_t s) {
-  auto tiles = [&](int64_t edge) {
-    const int64_t mb = (p.rows + edge - 1) / edge, nb = (p.cols + edge - 1) / edge;
-    return (MODE != kUpdate ? mb * (mb + 1) / 2 : mb * nb) * p.batch;
-  };
+  const Shape shape = gemm_shape(MODE, p.rows, p.cols, k, p.batch, sms);
   if constexpr (MODE == kGram) {
-    if (tiles(128) * kSplitCtas <= sms && k >= 2048)
-      return launch_shape<MODE, kSplit>(A, B, p, k, sms, s);
+    if (shape == kSplit) return launch_shape<MODE, kSplit>(A, B, p, k, sms, s);
   }
-  const int64_t k_blk = (k + 63) / 64;
-  if (round_time(tiles(128), sms, 7 * k_blk, 83) <=
-      round_time(tiles(256), sms / 2, 10 * k_blk, MODE == kUpdate ? 217 : 150))
-    return launch_shape<MODE, kSingle>(A, B, p, k, sms, s);
-  return launch_shape<MODE, kPair>(A, B, p, k, sms, s);
+  return shape == kSingle ? launch_shape<MODE, kSingle>(A, B, p, k, sms, s)
+                          : launch_shape<MODE, kPair>(A, B, p, k, sms, s);
 }
 
 // A launch that may start while the one before finishes; the kernel waits for it.
@@ -1171,9 +1177,8 @@ cudaError_t launch_after(void (*kernel)(ARGS...), dim3 grid, int threads, uint32
 
 // Up to two rounds of CTAs (300 of 64 x 64 170 -> 92 us, 256 x 16000 182 -> 179; but
 // 256 x 65536 545 -> 611: there the tiles' loads, products and stores should overlap).
-bool small_update(const OrthoParams& p, int sms) {
-  const int64_t tiles = static_cast<int64_t>((p.rows + 127) / 128) * ((p.cols + 127) / 128);
-  return p.rows <= kSmallK && tiles * p.batch <= 2 * sms;
+bool small_update(int64_t rows, int64_t cols, int64_t batch, int sms) {
+  return rows <= kSmallK && (rows + 127) / 128 * ((cols + 127) / 128) * batch <= 2 * sms;
 }
 
 cudaError_t launch_small_update(const CUtensorMap& A, const CUtensorMap& X, OrthoParams p,
@@ -1259,7 +1264,7 @@ int run(const void* g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
       p.transposed = tr;
       p.result_vec = aligned16(out) && cols % 8 == 0;
     }
-    if (small_update(p, sms)) {
+    if (small_update(p.rows, p.cols, p.batch, sms)) {
       FLCE_TRY(launch_small_update(ma, mxn[i & 1], p, s));
       continue;
     }
@@ -1313,4 +1318,18 @@ extern "C" int flce_orthogonalize(const void* G, int64_t batch, int64_t rows, in
     rc = run(G, o.dtype, batch, rows, cols, steps, c, eps, out, l, call.scratch, call.status, sms,
              call.stream);
   return call.end(rc);
+}
+
+extern "C" int flce_selftest_ortho_shapes(int64_t batch, int64_t rows, int64_t cols, int32_t sms,
+                                          int32_t shapes[3]) {
+  host_clear_error();
+  if (batch < 1 || rows < 1 || cols < 1 || batch > 65535 || rows > (1 << 20) ||
+      cols > (1 << 20) || sms < 2 || !shapes)
+    return host_error(FLCE_ERR_ARG, "flce_selftest_ortho_shapes: sizes out of range");
+  const Layout l = layout(batch, rows, cols);
+  const bool merged = small_update(l.k, l.n, batch, sms);
+  shapes[0] = gemm_shape(kGram, l.k, l.k, l.n, batch, sms);
+  shapes[1] = merged ? 3 : gemm_shape(kPoly, l.k, l.k, l.k, batch, sms);
+  shapes[2] = merged ? 3 : gemm_shape(kUpdate, l.k, l.n, l.k, batch, sms);
+  return FLCE_OK;
 }

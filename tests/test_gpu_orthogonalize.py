@@ -6,6 +6,8 @@ mantissa); the fp16 operands of the products (half a step of 2^-11 each, three
 roundings per step that the next steps neither damp nor amplify much, since X
 itself stays in fp32) give 2e-3 in a simulation with those roundings.  5e-3
 covers the sum with room for small matrices, where single entries count."""
+import ctypes
+
 import pytest
 import torch
 
@@ -208,3 +210,38 @@ def test_orthogonalize_extreme_entries(cuda_lib, dtype):
     _check(got, _reference(both, eps=0.0))
     # the eps counts beside a norm of its own size only
     _check(cuda_lib.flce_orthogonalize(big, eps=1.0), _reference(big, eps=1.0))
+
+
+def shapes_of(lib, shape, sms):
+    """The tile shapes of a step's three products."""
+    batch = 1
+    for n in shape[:-2]:
+        batch *= n
+    out = (ctypes.c_int32 * 3)()
+    assert lib.flce_selftest_ortho_shapes(batch, *shape[-2:], sms, out) == 0
+    return tuple(out)
+
+
+PAIR, SINGLE, SPLIT, MERGED = range(4)
+FORMS = [
+    # last tile of 256 with one row; update tiles in one round of single CTAs
+    ((2361, 2305), "fp32", (PAIR, PAIR, SINGLE)),
+    # tall, every product on pairs, more than two tiles per pair; 76 rows in the last tile
+    ((4100, 2380), "bf16", (PAIR, PAIR, PAIR)),
+    # 216 rows there: some of the odd CTA's; no whole vectors
+    ((2520, 4133), "fp32", (PAIR, PAIR, PAIR)),
+    ((3, 1300, 1500), "bf16", (PAIR, PAIR, SINGLE)),
+    ((900, 2100), "fp32", (SPLIT, SINGLE, SINGLE)),
+    ((640, 640), "bf16", (SINGLE, SINGLE, SINGLE)),
+    ((8, 250, 1030), "bf16", (SINGLE, MERGED, MERGED)),
+]
+
+
+@pytest.mark.parametrize("shape,dtype,forms", FORMS)
+def test_orthogonalize_forms(cuda_lib, shape, dtype, forms):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert shapes_of(cuda_lib.load_library(), shape, sms) == forms
+    G = _matrix("signal", shape, sum(shape) + 2, dtype)
+    got = cuda_lib.flce_orthogonalize(G, sync=True)
+    _check(got, _reference(G))
+    assert torch.equal(got, cuda_lib.flce_orthogonalize(G))

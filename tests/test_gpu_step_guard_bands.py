@@ -125,3 +125,9 @@ def test_attention_far_tokens(cuda_lib):
     dq2, dk2, dv2 = cuda_lib.flce_attn_bwd(near[3], *near[:3], o2, lse2, cu)
     for a, b in ((o, o2), (lse, lse2), (dq, dq2), (dk, dk2), (dv, dv2)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("shape", [(2361, 2305), (2520, 4133), (4100, 2380), (2, 1300, 1405)])
+def test_orthogonalize_bounds_of_pairs(cuda_lib, shape):
+    """The same where the products run on CTA pairs."""
+    test_orthogonalize_bounds(cuda_lib, shape)

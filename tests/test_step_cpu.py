@@ -208,3 +208,20 @@ def test_attention_refuses_overlaps(lib, kw, forward):
     assert (fwd if forward else bwd) == flce.FLCE_ERR_ARG
     if not forward:
         assert b"overlaps" in lib.flce_last_error()
+
+
+def test_orthogonalize_tests_reach_every_tile_shape(lib):
+    """The cases of test_orthogonalize_forms take the tile shapes they are there for."""
+    from test_gpu_orthogonalize import FORMS, MERGED, PAIR, SINGLE, SPLIT, shapes_of
+    for shape, _, forms in FORMS:
+        assert shapes_of(lib, shape, 152) == forms, shape
+    reached = [set(x) for x in zip(*(forms for _, _, forms in FORMS))]
+    assert reached == [{PAIR, SINGLE, SPLIT}, {PAIR, SINGLE, MERGED}, {PAIR, SINGLE, MERGED}]
+
+
+@pytest.mark.parametrize("a", [(0, 8, 8, 152), (1, 0, 8, 152), (1, 8, (1 << 20) + 1, 152),
+                               (65536, 8, 8, 152), (1, 8, 8, 1)])
+def test_orthogonalize_shapes_refusals(lib, a):
+    out = (ctypes.c_int32 * 3)()
+    assert lib.flce_selftest_ortho_shapes(*a, out) == flce.FLCE_ERR_ARG
+    assert lib.flce_selftest_ortho_shapes(1, 8, 8, 152, None) == flce.FLCE_ERR_ARG
