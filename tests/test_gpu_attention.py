@@ -562,3 +562,15 @@ def test_attention_offsets_without_tokens(cuda_lib, cu, good):
     if not good:
         with pytest.raises(cuda_lib.FlceError):
             cuda_lib.flce_attn_bwd(e, e, e, e, e, lse, cu, sync=True)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([4500], 2, 1, 128), ([3001, 1700], 2, 1, 64),
+                                           ([2600, 77], 3, 1, 80)])
+def test_attention_long_sequences(cuda_lib, lens, Hq, Hkv, D):
+    """Dozens of key tiles per row.  fp32 sums of n terms in chains of 32 per tile, then
+    over the tiles: (32 + n / 128) 2^-24 of the terms' sizes, within e up to 28,000."""
+    q, k, v, dO, cu = _inputs(lens, Hq, Hkv, D, D + 1, pad=5)
+    got = _run(cuda_lib, q, k, v, dO, cu)
+    val, tol = _reference(q, k, v, dO, lens, D ** -0.5)
+    for n in val:
+        _close(n, got[n], val[n], tol[n])

@@ -270,3 +270,17 @@ def test_embed_bwd_sort_limits(cuda_lib, N, kind):
     ws = torch.empty(dense["workspace_bytes"], dtype=torch.uint8, device=DEV)
     again = cuda_lib.flce_embed_bwd(dY, ids, V, scale=0.5, workspace=ws)
     assert torch.equal(again, dW)
+
+
+@pytest.mark.parametrize("kind", ["uniform", "skewed", "one"])
+@pytest.mark.parametrize("N,H,V,dtype", [(65536, 256, 5003, "bf16"), (130001, 72, 128256, "fp32")])
+def test_embed_bwd_many_tokens(cuda_lib, N, H, V, dtype, kind):
+    """The long-context batch: runs of up to N equal ids, many passes of each CTA's sort."""
+    ids = _ids(kind, N, V, N, torch.int32 if N % 2 else torch.int64).to(DEV)
+    dY = torch.randn(N, H, generator=torch.Generator().manual_seed(N)).to(DT[dtype]).to(DEV)
+    dW = torch.full((V, H), float("nan"), device=DEV)
+    cuda_lib.flce_embed_bwd(dY, ids, V, dW=dW, scale=2.0, sync=True)
+    _check_rows(dW, dY, ids.long(), 2.0)
+    acc = torch.zeros(V, H, device=DEV)
+    cuda_lib.flce_embed_bwd(dY, ids, dW=acc, accumulate=True, scale=2.0)
+    assert torch.equal(acc, dW)
