@@ -320,8 +320,11 @@ FLCE_API int flce_embed_fwd(const void* W, const void* ids, int64_t N, int64_t H
  * Its gradient: dW[v] = scale * sum of dY[i] over the tokens i with ids[i] == v,
  * or dW[v] += that sum when accumulate is not 0 (a weight tied to the head's:
  * dW then holds what flce_fwd_bwd() left there; rows that no token has are not
- * touched).  Equal ids are added in ascending token order in fp32, so the
- * result does not change from run to run.
+ * touched).  Equal ids are added in fp32 in a fixed order, so the result does not
+ * change from run to run: in ascending token order within pieces of 32 to 64 of them,
+ * then the pieces' sums, in ascending order within eighths of them.  The length of a
+ * piece depends on N and H, so other tokens in the batch may change the last bits.
+ * What is added to an old value is added at L2, where numbers below 2^-126 are zero.
  *   dY [N, H] of type opts->dtype; dW [V, H] fp32; alignment as above.
  * Ignored and out-of-range ids take no part (the latter report
  * FLCE_ERR_TARGET).  N == 0 clears dW, or leaves it when accumulate is set.

@@ -6,8 +6,9 @@
 // The forward pass and the sums are bound by memory traffic: one multiply or
 // add per element.
 //
-// The gradient sums equal ids in ascending token order, in fp32, and gives
-// the same bits on every run: no element of dW is added to twice.  Three launches:
+// The gradient sums equal ids in fp32 in a fixed order (ascending tokens in a piece of
+// a run, then the pieces), and gives the same bits on every run: no element of dW is
+// added to twice.  Three launches:
 //   1  sort     tokens by id, stable (radix digits of at most 9 bits), in one
 //               launch: one CTA with everything in shared memory for up to
 //               2048 tokens (7 to 13 us; at 4096 21 us against the cluster's
@@ -441,7 +442,8 @@ struct Acc {  // the elements of one 16-byte vector in fp32
 };
 
 // dW row piece: (dW +) scale * sum.  The addition is done at L2, so that no
-// thread waits for the old value; every element gets one addend.
+// thread waits for the old value; every element gets one addend.  (L2 takes subnormal
+// numbers for zeros.)
 __device__ __forceinline__ void finish4(float* dst, float4 v, float scale, bool accumulate) {
   v.x *= scale;
   v.y *= scale;

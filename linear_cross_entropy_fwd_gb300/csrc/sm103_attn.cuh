@@ -135,14 +135,6 @@ __device__ __forceinline__ void commit_pair_elected(uint64_t* bar, uint16_t cta_
       : "memory");
 }
 
-__device__ __forceinline__ void arrive_elected(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ void expect_tx_elected(uint64_t* bar, uint32_t bytes) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
@@ -234,14 +226,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return reinterpret_cast<const float2&>(d);
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
       : "=l"(d)
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
   return reinterpret_cast<const float2&>(d);

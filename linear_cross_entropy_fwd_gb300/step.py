@@ -100,8 +100,8 @@ def flce_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, V: int | None = None, *,
                    sync: bool = False, workspace: torch.Tensor | None = None,
                    info: dict | None = None) -> torch.Tensor:
     """The gradient of ``flce_embed_fwd`` in fp32 [V, H]: row v is ``scale``
-    times the sum of ``dY[i]`` over the tokens with ``ids[i] == v``, added in
-    ascending i.  ``accumulate=True`` adds it to ``dW`` (a weight tied to the
+    times the sum of ``dY[i]`` over the tokens with ``ids[i] == v``, added in a
+    fixed order.  ``accumulate=True`` adds it to ``dW`` (a weight tied to the
     head's) and touches no other row; otherwise dW is overwritten."""
     lib = _library()
     if dY.dim() != 2 or not dY.is_cuda or not dY.is_contiguous():
