@@ -671,6 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dp_read);
+      named_barrier(2 + quarter, 64);  // the other half has read S too
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) d[i] = fast_exp2(fmaf(P[i], c, -lse2)) * (d[i] - delta);
       bool look = false;
       if (diag) {
         // a row of K that is not finite has no finite score
@@ -678,13 +682,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) any[i & 3] = fmaf(P[i], 0.f, any[i & 3]);
         look = named_barrier_or(1, kEwThreads, !(any[0] + any[1] + (any[2] + any[3]) == 0.f));
-      } else {
-        named_barrier(2 + quarter, 64);  // the other half has read S too
-      }
-      tc_fence_after();
-#pragma unroll
-      for (int i = 0; i < 64; ++i) d[i] = fast_exp2(fmaf(P[i], c, -lse2)) * (d[i] - delta);
-      if (diag) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) d[i] = i + 64 * half > row ? 0.f : d[i];
       }
