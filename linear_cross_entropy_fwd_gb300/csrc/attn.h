@@ -88,7 +88,7 @@ __device__ void blank_outside(const AttnParams& p, bool ok, int64_t me, int64_t 
 
 // A forward pass whose units all run at once has no plan: every CTA finds its own,
 // with a thread per sequence (57, 1 and 130 tokens, 8 heads: 28 us with a plan, 19
-// without, most of it on the host).
+// without on the same machine, most of it on the host; 18 to 27 us on others).
 constexpr int kDirectSeqs = 256;
 
 // Launchers.  Tensor maps: box 64 x 1 x 128 of [T, heads, D], 128-byte swizzle.

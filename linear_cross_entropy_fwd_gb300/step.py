@@ -196,8 +196,8 @@ def flce_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     """Causal attention over packed sequences; returns (o, lse).
 
     q [T, heads_q, D], k and v [T, heads_kv, D] in bf16 with a contiguous last
-    axis (slices of one projection's output will do); ``cu_seqlens`` int32
-    [sequences + 1] on the device.  ``scale`` defaults to D ** -0.5.  o is
+    axis (slices of one projection's output will do), none of it over ``out``;
+    ``cu_seqlens`` int32 [sequences + 1] on the device.  ``scale`` defaults to D ** -0.5.  o is
     [T, heads_q, D], lse fp32 [heads_q, T]."""
     lib = _library()
     if q.dim() != 3:
@@ -221,7 +221,8 @@ def flce_attn_bwd(dO: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
                   sync: bool = False, workspace: torch.Tensor | None = None,
                   info: dict | None = None):
     """Gradients of ``flce_attn_fwd`` at its inputs and outputs; returns
-    (dq, dk, dv) in bf16, dk and dv summed over the query heads they serve."""
+    (dq, dk, dv) in bf16, dk and dv summed over the query heads they serve.  They may
+    share memory with ``o``, but not with the other inputs or one another."""
     lib = _library()
     a = _attn_args(q, k, v, cu_seqlens, scale, o, lse)
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
