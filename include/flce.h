@@ -345,7 +345,8 @@ FLCE_API int flce_embed_bwd(const void* dY, const void* ids, int64_t N, int64_t 
  * and for the gradients, with delta_i = sum_d dO_id O_id:
  *   dS = P o (dO V^T - delta),  dQ = scale dS K,
  *   dK = scale dS^T Q and dV = P^T dO, summed over the query heads of the group.
- * Products are bf16 with fp32 sums; P and dS are rounded to bf16 for theirs.
+ * Products are bf16 with fp32 sums; P and dS are rounded to bf16 for theirs, and
+ * delta takes o as it is stored.
  *
  * Every tensor is bf16 [T, heads, head_dim] with a contiguous last axis and
  * its own token and head strides in elements (multiples of 8, not 0, so q, k
