@@ -166,10 +166,10 @@ __device__ __forceinline__ void put_partial(uint32_t taddr, uint8_t* mat, int ro
 }
 
 // Accumulator columns [c0, c0 + 64) of this thread's row of dV, plus what is not finite
-// in dO of its key's own token, `from`, to the end of the tile (token t1), for each of
-// this CTA's heads; t0 is the tile's first token.
+// in dO of n tokens down from t1 (the tile's last, to its key's own), for each of this
+// CTA's heads.
 __device__ __forceinline__ void add_nonfinite_dO(const AttnParams& p, uint32_t taddr, int c0,
-                                                 int head0, int heads, int t0, int from, int t1) {
+                                                 int head0, int heads, int t1, int n) {
 #pragma unroll 1
   for (int c = 0; c < 64; c += 16) {
     uint32_t r[16];
@@ -181,12 +181,13 @@ __device__ __forceinline__ void add_nonfinite_dO(const AttnParams& p, uint32_t t
       float sum[8] = {};
       if (col < p.D)
         for (int h = head0; h < head0 + heads; ++h)
-          sum_nonfinite(static_cast<const uint16_t*>(p.dO.p) + h * p.dO.head, p.dO.token, col, t0,
-                        t1, from, t1, sum);
+          sum_nonfinite(static_cast<const uint16_t*>(p.dO.p) + t1 * p.dO.token + h * p.dO.head,
+                        -p.dO.token, n, col, sum);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         r[8 * part + e] = __float_as_uint(__uint_as_float(r[8 * part + e]) + sum[e]);
     }
+    __syncwarp();
     tmem_st_32x32b_x16(taddr + c, r);
     tmem_st_wait();
   }
@@ -493,10 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key0 = kt * kTile + 32 * quarter;
       const int64_t tok = static_cast<int64_t>(t.start) + key0;
       if (*cleared_dO && half < DP / 64) {
-        const int t0 = t.start + kt * kTile;
         const int end = (kt + 1) * kTile < t.len ? (kt + 1) * kTile : t.len;
-        add_nonfinite_dO(p, tDV + lanes + 64 * half, 64 * half, head0, heads, t0, t0 + row,
-                         t.start + end - 1);
+        add_nonfinite_dO(p, tDV + lanes + 64 * half, 64 * half, head0, heads, t.start + end - 1,
+                         end - (kt * kTile + row));
       }
       uint16_t* dv = static_cast<uint16_t*>(p.dv.p) + tok * p.dv.token + kvh * p.dv.head;
       uint16_t* dk = static_cast<uint16_t*>(p.dk.p) + tok * p.dk.token + kvh * p.dk.head;
@@ -706,13 +706,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (half < DP / 64) {
         store_cols(tDQ + lanes + 64 * half, p.scale, smK + warp * 4096, dq + 64 * half, p.dq.token,
                    t.len - q0 - r0, p.D - 64 * half);
-        if (*cleared_k) {  // K times a dS that is 0, if it is finite: NaN
-          const int end = q0 + r0 + 32 < t.len ? q0 + r0 + 32 : t.len;
-          add_nonfinite(static_cast<const uint16_t*>(p.k.p) + kvh * p.k.head, p.k.token,
-                        dq + lane * p.dq.token, 64 * half,
-                        p.D < 64 * half + 64 ? p.D : 64 * half + 64, t.start + q0,
-                        static_cast<int>(tok), t.start + end - 1, 0.f);
-        }
+        if (*cleared_k && in)  // K times a dS that is 0, if it is finite: NaN
+          add_nonfinite(static_cast<const uint16_t*>(p.k.p) +
+                            (static_cast<int64_t>(t.start) + q0) * p.k.token + kvh * p.k.head,
+                        p.k.token, row + 1, dq + lane * p.dq.token, 64 * half,
+                        p.D < 64 * half + 64 ? p.D : 64 * half + 64, 0.f);
+        __syncwarp();
       }
     }
     tc_fence_before();

@@ -508,11 +508,14 @@ __device__ __forceinline__ void run_units(const CUtensorMap& tmQ, const CUtensor
       } else if (*reinterpret_cast<volatile int*>(sh.nonfinite_v) > round) {
         // (a later round's mark is at worst a needless look; tile B also lacks what was
         // cleared for tile A)
-        const int last = row - lane + 31 < valid ? row - lane + 31 : valid - 1;
-        add_nonfinite(static_cast<const uint16_t*>(p.v.p) + w.head / (p.Hq / p.Hkv) * p.v.head,
-                      p.v.token, static_cast<uint16_t*>(p.o.p) + tok * p.o.token +
-                      w.head * p.o.head, 0, p.D, w.t.start + 2 * w.t.tile * kTile,
-                      static_cast<int>(tok), w.t.start + q0 + last, 1.f);
+        const int64_t t0 = static_cast<int64_t>(w.t.start) + 2 * w.t.tile * kTile;
+        if (in)
+          add_nonfinite(static_cast<const uint16_t*>(p.v.p) + t0 * p.v.token +
+                            w.head / (p.Hq / p.Hkv) * p.v.head,
+                        p.v.token, static_cast<int>(tok - t0) + 1,
+                        static_cast<uint16_t*>(p.o.p) + tok * p.o.token + w.head * p.o.head, 0,
+                        p.D, 1.f);
+        __syncwarp();
       }
     }
     tc_fence_before();

@@ -272,37 +272,35 @@ __device__ __forceinline__ bool clear_nonfinite_piece(uint8_t* piece) {
   return bad != 0;
 }
 
-// sum[e] += what is not finite in columns c + e of rows t0 .. t1 of a [T, D] bf16
-// matrix, for the rows within [from, to] of this lane; whether there was any in any
-// lane's.  The bounds t0 and t1 are the warp's.
-__device__ __forceinline__ bool sum_nonfinite(const uint16_t* m, int64_t pitch, int c, int t0,
-                                              int t1, int from, int to, float (&sum)[8]) {
-  uint32_t any = 0;
-  for (int t = t0; t <= t1; ++t) {
-    const uint4 q = *reinterpret_cast<const uint4*>(m + t * pitch + c);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// sum[e] += what is not finite in columns c + e of n rows of a [T, D] bf16 matrix, from
+// `row` on in steps of `pitch`, until all sums are NaN.
+__device__ __forceinline__ void sum_nonfinite(const uint16_t* row, int64_t pitch, int n, int c,
+                                              float (&sum)[8]) {
+#pragma unroll 1
+  for (int i = 0; i < n; ++i, row += pitch) {
+    const uint4 q = *reinterpret_cast<const uint4*>(row + c);
+    const uint32_t w[4] = {nonfinite_halves(q.x), nonfinite_halves(q.y), nonfinite_halves(q.z),
+                           nonfinite_halves(q.w)};
+    if (!(w[0] | w[1] | w[2] | w[3])) continue;
+    bool settled = true;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t b = nonfinite_halves(w[k]);
-      any |= b;
-      if (b && t >= from && t <= to) {
-        sum[2 * k] += __uint_as_float(b << 16);
-        sum[2 * k + 1] += __uint_as_float(b & 0xffff0000u);
-      }
+      sum[2 * k] += __uint_as_float(w[k] << 16);
+      sum[2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+      settled = settled && isnan(sum[2 * k]) && isnan(sum[2 * k + 1]);
     }
+    if (settled) break;
   }
-  return any != 0;
 }
 
-// dst[c] += f times what is not finite in column c of rows t0 .. to of m, for the
-// columns [c0, c1) in eights.  Each lane has its own `to` and row `dst` (left out when
-// `to` is past t1, the warp's last row).
-__device__ __forceinline__ void add_nonfinite(const uint16_t* m, int64_t pitch, uint16_t* dst,
-                                              int c0, int c1, int t0, int to, int t1, float f) {
+// dst[c] += f times what is not finite in column c of n rows from `row` on, for the
+// columns [c0, c1) in eights; each lane has its own n and dst.
+__device__ __forceinline__ void add_nonfinite(const uint16_t* row, int64_t pitch, int n,
+                                              uint16_t* dst, int c0, int c1, float f) {
 #pragma unroll 1
   for (int c = c0; c < c1; c += 8) {
     float sum[8] = {};
-    if (!sum_nonfinite(m, pitch, c, t0, t1, t0, to, sum) || to > t1) continue;
+    sum_nonfinite(row, pitch, n, c, sum);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (sum[e] != 0.f)
