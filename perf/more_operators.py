@@ -105,7 +105,7 @@ def _dt(name):
 
 
 def _randn(g, *shape, dtype=torch.float32, std=1.0):
-    return torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32).mul_(std).to(dtype)
+    return torch.randn(shape, generator=g, device="cuda", dtype=torch.float32).mul_(std).to(dtype)
 
 
 def _activations(g, N, H, dtype):
@@ -137,10 +137,11 @@ def prepare(case, seed):
         s["w_" + n] = (1.0 + _randn(g, H, std=0.2)).to(pt)
         if case["bias"]:
             s["b_" + n] = _randn(g, H, dtype=pt, std=0.1)
-    shape = {"none": None, "channel": (1, H), "token": (N, 1), "full": (N, H),
-             "scalar": (1, 1)}[case["gate"]]
-    if shape:
-        s["gate"] = (0.5 + _randn(g, *shape, std=0.5)).to(pt if shape[0] == 1 else dt)
+    shape = {"channel": (H,), "token": (N, 1), "full": (N, H), "scalar": ()}
+    if case["gate"] != "none":
+        # a learned gate is a parameter, one computed for each token an activation
+        s["gate"] = ((0.5 + _randn(g, *shape[case["gate"]], std=0.5))
+                     .to(pt if case["gate"] in ("channel", "scalar") else dt))
     if op == "resnorm_bwd":
         h, z, stats = _plain_fwd(s)
         s.update(h_out=h, stats=stats)
@@ -221,11 +222,11 @@ def _plain_bwd(s):
     yh = (y - mean_y) * r_y if c["post"] else y
     if a is not None:
         u = _affine(yh, s.get("w_post"), s.get("b_post")) if c["post"] else yh
-        axes = [i for i in (0, 1) if s["gate"].shape[i] == 1]
         dg = c["beta"] * slope * u * dt
-        dg = dg.sum(axes, keepdim=True) if axes and c["gate"] != "full" else dg
-        # per-token gates are activations; gates with one row are parameters, their gradient fp32
-        out["dgate"] = dg if c["gate"] in ("channel", "scalar") else dg.to(s["gate"].dtype)
+        # gradients of parameters are fp32, those of activations have their type
+        out["dgate"] = {"channel": lambda: dg.sum(0), "scalar": lambda: dg.sum(),
+                        "token": lambda: dg.sum(1, keepdim=True).to(s["gate"].dtype),
+                        "full": lambda: dg.to(s["gate"].dtype)}[c["gate"]]()
     if c["post"]:
         out["dw_post"] = (du * yh).sum(0)
         if c["bias"]:
