@@ -427,6 +427,155 @@ FLCE_API int flce_orthogonalize(const void* G, int64_t batch, int64_t rows, int6
 FLCE_API int flce_selftest_ortho_shapes(int64_t batch, int64_t rows, int64_t cols, int32_t sms,
                                         int32_t shapes[3]);
 
+/* ------------------------------------------------------------------------
+ * Between a model's blocks: the residual join with its norms, and checkpoints
+ * of activations in 8 bits.  Options, status, scratch, streams and capture as
+ * for the operators around the head.
+ * ------------------------------------------------------------------------ */
+
+typedef enum flce_norm {
+  FLCE_NORM_RMS = 0,  /* n(x) = x / sqrt(mean(x^2) + eps) */
+  FLCE_NORM_LAYER = 1 /* n(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) */
+} flce_norm;
+
+typedef enum flce_gate {
+  FLCE_GATE_NONE = 0,
+  FLCE_GATE_SCALAR = 1,  /* one value, a parameter */
+  FLCE_GATE_CHANNEL = 2, /* [H], a parameter */
+  FLCE_GATE_TOKEN = 3,   /* one value per token, gate_row elements apart */
+  FLCE_GATE_FULL = 4     /* [N, H], rows gate_row elements apart */
+} flce_gate;
+
+typedef enum flce_act {
+  FLCE_ACT_NONE = 0,
+  FLCE_ACT_SIGMOID = 1,
+  FLCE_ACT_TANH = 2
+} flce_act;
+
+/*
+ * Residual join: what stands between a block's output y and the next block's input z.
+ *   u     = n(y) * w_post + b_post      (post_norm; else u = y)
+ *   h_out = alpha h + beta act(gate) u  (without h: the second term; without gate: 1)
+ *   z     = n(h_out) * w_pre + b_pre    (pre_norm; else no z)
+ * with n the RMS or layer norm over the H elements of a token.  All of it is computed in
+ * fp32.  h_out is rounded to the stream's type, and z is the norm of h_out as it is
+ * stored, so that the gradients, which read the stored h_out, are those of what was
+ * computed; z is rounded once.
+ *
+ * y and z (dy, dz and gates per token) have type opts->dtype; the stream (h, h_out, dh,
+ * dh_out) has it too, or is fp32 with stream_fp32.  Parameters (weights, biases, gates of
+ * kind SCALAR and CHANNEL) have type opts->dtype, or are fp32 with params_fp32.  A weight
+ * or bias may be NULL.  H is a multiple of 8, 8 .. 16384; N < 2^31.  Row tensors have a
+ * contiguous last axis and a row stride in elements of their own (a multiple of 8, at least
+ * H; gate_row of kind TOKEN: at least 1); tensors are 16-byte aligned (gates of kind SCALAR
+ * and TOKEN to their element).
+ * h_out may be h itself and z may be y; dh may be dh_out itself, and dy may be dz (same
+ * address, same stride).  Any other overlap of an output with an input or another output
+ * is refused with FLCE_ERR_ARG where addresses, strides and sizes tell; row tensors that
+ * interleave in one buffer at equal strides share nothing.
+ * A token's NaN or infinity stays in its own row of h_out, z, dh, dy and per-token gates'
+ * gradients; gradients of parameters are sums over the tokens.
+ *
+ * Forward.  stats, fp32 [4, N], optional: mean and 1 / sqrt(variance + eps) of y, then of
+ * h_out; zeros where there is no such norm, means of 0 for RMS.  h_out is optional.
+ * z_ckpt, optional: flce_ckpt_bytes(N, H) bytes that receive what flce_ckpt_save() makes
+ * of the stored z.
+ *
+ * Backward, at y, h_out (read with pre_norm) and stats as the forward pass left them, and
+ * the gradients dz (pre_norm) and dh_out (optional: what arrives on the stream besides):
+ *   dy; dh, optional; dgate of the gate's shape (per token: opts->dtype, dgate_row apart;
+ *   SCALAR and CHANNEL: fp32); dw_post, db_post, dw_pre, db_pre, fp32 [H], each optional.
+ * dgate is required with a gate.  Sums over tokens are fp32, in an order that N, H, the
+ * options and the device's number of SMs fix: the same call gives the same bits.
+ * N == 0 makes the parameters' gradients 0.
+ * Scratch: forward none, backward at most 608 fp32 rows of H per gradient of a parameter.
+ */
+typedef struct flce_resnorm {
+  int64_t N, H;
+  int32_t norm;               /* flce_norm */
+  int32_t post_norm, pre_norm;
+  int32_t stream_fp32, params_fp32;
+  int32_t gate_kind;          /* flce_gate */
+  int32_t gate_act;           /* flce_act */
+  float alpha, beta;          /* finite */
+  float eps;                  /* >= 0, finite */
+  const void* y;              /* each row tensor followed by its row stride */
+  int64_t y_row;
+  const void* h;              /* forward; NULL: none */
+  int64_t h_row;
+  const void* gate;
+  int64_t gate_row;
+  const void* w_post;
+  const void* b_post;
+  const void* w_pre;
+  const void* b_pre;
+  void* h_out;                /* written by flce_resnorm_fwd, read by flce_resnorm_bwd */
+  int64_t h_out_row;
+  float* stats;               /* likewise */
+  void* z;                    /* forward */
+  int64_t z_row;
+  void* z_ckpt;
+  const void* dz;             /* the rest: backward */
+  int64_t dz_row;
+  const void* dh_out;
+  int64_t dh_out_row;
+  void* dy;
+  int64_t dy_row;
+  void* dh;
+  int64_t dh_row;
+  void* dgate;
+  int64_t dgate_row;
+  float* dw_post;
+  float* db_post;
+  float* dw_pre;
+  float* db_pre;
+} flce_resnorm;
+
+FLCE_API int flce_resnorm_fwd(const flce_resnorm* a, const flce_opts* opts);
+FLCE_API int flce_resnorm_bwd(const flce_resnorm* a, const flce_opts* opts);
+
+/* sizeof(flce_resnorm) as compiled into the library. */
+FLCE_API size_t flce_resnorm_sizeof(void);
+
+/*
+ * Activation checkpoints in 8 bits.  32 consecutive values of a row share a scale 2^e:
+ * e is the smallest with |value| <= 448 2^e for all of them, but within -117 .. 119, and
+ * a value is stored as the e4m3 number next to value * 2^-e (ties to even).  So a value
+ * is off by at most 2^-4 of itself or 2^(e-10), whichever is more (values above
+ * 1.75 2^127 come back as that).  What is stored is exact in bf16.  A group that holds a
+ * NaN or an infinity comes back as NaN, all of it.
+ *
+ * A checkpoint of [N, H] is one buffer of flce_ckpt_bytes(N, H) bytes, 16-byte aligned:
+ * codes [N, P] with P = 32 ceil(H / 32), zeros from column H on, then scale bytes
+ * [N, 4 ceil(P / 128)], e + 127 each, or 255 for a group of NaN, zeros behind the last.
+ * Calls that read one take only what flce_ckpt_save() or flce_resnorm_fwd() can write.
+ */
+
+/* N (P + 4 ceil(P / 128)); 0 where N or H is out of range (0 .. 2^31 - 1, 1 .. 2^20). */
+FLCE_API size_t flce_ckpt_bytes(int64_t N, int64_t H);
+
+/*
+ * ckpt = x, for x [N, H] of type opts->dtype, rows x_row elements apart; and x = ckpt.
+ * H a multiple of 8, up to 2^20; x_row a multiple of 8, at least H; x 16-byte aligned.
+ */
+FLCE_API int flce_ckpt_save(const void* x, int64_t x_row, int64_t N, int64_t H, void* ckpt,
+                            const flce_opts* opts);
+FLCE_API int flce_ckpt_load(const void* ckpt, int64_t N, int64_t H, void* x, int64_t x_row,
+                            const flce_opts* opts);
+
+/*
+ * Weight gradient of a projection Y = X W^T (W [O, I]) from X's checkpoint:
+ *   dW = dY^T X, or dW += dY^T X when accumulate is not 0
+ *   dY [N, O] bf16, rows dY_row elements apart (a multiple of 8, at least O), 16-byte
+ *   aligned; ckpt of [N, I]; dW [O, I] fp32, contiguous, 16-byte aligned.  O and I are
+ *   multiples of 8, up to 2^20; N < 2^31.  opts->dtype must be FLCE_BF16.
+ * Products are bf16, exact for the stored X, with fp32 sums in a fixed order.  N == 0 makes
+ * dW 0, or leaves it when accumulate is set.
+ */
+FLCE_API int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt, int64_t N,
+                             int64_t O, int64_t I, float* dW, int32_t accumulate,
+                             const flce_opts* opts);
+
 #ifdef __cplusplus
 }
 #endif

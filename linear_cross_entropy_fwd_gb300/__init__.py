@@ -39,7 +39,9 @@ EXPORTED = ["flce_opts_init", "flce_fwd_bwd", "flce_fwd_bwd_ex", "flce_fwd",
             "flce_last_error", "flce_version", "flce_opts_sizeof", "flce_fwd_noalloc",
             "flce_ce_fwd_bwd", "flce_selftest_wait_expiry", "flce_scale_convert",
             "flce_embed_fwd", "flce_embed_bwd", "flce_attn_fwd", "flce_attn_bwd",
-            "flce_attn_sizeof", "flce_orthogonalize", "flce_selftest_ortho_shapes"]
+            "flce_attn_sizeof", "flce_orthogonalize", "flce_selftest_ortho_shapes",
+            "flce_resnorm_fwd", "flce_resnorm_bwd", "flce_resnorm_sizeof", "flce_ckpt_bytes",
+            "flce_ckpt_save", "flce_ckpt_load", "flce_ckpt_wgrad"]
 
 
 class FlceOpts(ctypes.Structure):
@@ -85,6 +87,22 @@ class FlceAttn(ctypes.Structure):
         f for name in ("dO", "dq", "dk", "dv") for f in (
             (name, ctypes.c_void_p), (name + "_token", ctypes.c_int64),
             (name + "_head", ctypes.c_int64))]
+
+
+class FlceResnorm(ctypes.Structure):
+    """Mirror of ``struct flce_resnorm`` (include/flce.h)."""
+    _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64)] + [
+        (name, ctypes.c_int32) for name in ("norm", "post_norm", "pre_norm", "stream_fp32",
+                                            "params_fp32", "gate_kind", "gate_act")] + [
+        (name, ctypes.c_float) for name in ("alpha", "beta", "eps")] + [
+        f for name in ("y", "h", "gate") for f in (
+            (name, ctypes.c_void_p), (name + "_row", ctypes.c_int64))] + [
+        (name, ctypes.c_void_p) for name in ("w_post", "b_post", "w_pre", "b_pre")] + [
+        ("h_out", ctypes.c_void_p), ("h_out_row", ctypes.c_int64), ("stats", ctypes.c_void_p),
+        ("z", ctypes.c_void_p), ("z_row", ctypes.c_int64), ("z_ckpt", ctypes.c_void_p)] + [
+        f for name in ("dz", "dh_out", "dy", "dh", "dgate") for f in (
+            (name, ctypes.c_void_p), (name + "_row", ctypes.c_int64))] + [
+        (name, ctypes.c_void_p) for name in ("dw_post", "db_post", "dw_pre", "db_pre")]
 
 
 class FlceError(RuntimeError):
@@ -154,6 +172,21 @@ def load_library(path: str | None = None):
             fn.restype = i32
         lib.flce_attn_sizeof.argtypes = []
         lib.flce_attn_sizeof.restype = ctypes.c_size_t
+        pr = ctypes.POINTER(FlceResnorm)
+        for fn in (lib.flce_resnorm_fwd, lib.flce_resnorm_bwd):
+            fn.argtypes = [pr, po]
+            fn.restype = i32
+        lib.flce_resnorm_sizeof.argtypes = []
+        lib.flce_resnorm_sizeof.restype = ctypes.c_size_t
+        lib.flce_ckpt_bytes.argtypes = [i64, i64]
+        lib.flce_ckpt_bytes.restype = ctypes.c_size_t
+        lib.flce_ckpt_save.argtypes = [vp, i64, i64, i64, vp, po]
+        lib.flce_ckpt_load.argtypes = [vp, i64, i64, vp, i64, po]
+        lib.flce_ckpt_wgrad.argtypes = [vp, i64, vp, i64, i64, i64, vp, ctypes.c_int32, po]
+        for fn in (lib.flce_ckpt_save, lib.flce_ckpt_load, lib.flce_ckpt_wgrad):
+            fn.restype = i32
+        if lib.flce_resnorm_sizeof() != ctypes.sizeof(FlceResnorm):
+            raise RuntimeError("flce_resnorm layout mismatch between libflce and the binding")
         if lib.flce_attn_sizeof() != ctypes.sizeof(FlceAttn):
             raise RuntimeError("flce_attn layout mismatch between libflce and the binding")
         if lib.flce_opts_sizeof() != ctypes.sizeof(FlceOpts):
@@ -603,3 +636,6 @@ class LinearCrossEntropyLoss(torch.nn.Module):
 
 from .step import (Embedding, PackedAttention, flce_attn_bwd, flce_attn_fwd,  # noqa: E402,F401
                    flce_embed_bwd, flce_embed_fwd, flce_orthogonalize)
+from .block import (Checkpoint, CheckpointedLinear, ResidualNorm,  # noqa: E402,F401
+                    ResnormGrads, checkpoint_bytes, flce_ckpt_load, flce_ckpt_save,
+                    flce_ckpt_wgrad, flce_resnorm_bwd, flce_resnorm_fwd)

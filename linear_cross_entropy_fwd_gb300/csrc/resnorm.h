@@ -1,0 +1,78 @@
+// resnorm.h -- what the residual join's kernels and their host side share (internal).
+//
+// For a token, with n(x) = (x - mean) r, r = 1 / sqrt(mean((x - mean)^2) + eps) and mean = 0
+// for the RMS norm:
+//   yh = n(y), u = yh w_post + b_post   (without a post-norm: yh = u = y)
+//   h' = alpha h + beta a u, a = act(gate), rounded to the stream's type
+//   xh = n(h'), z = xh w_pre + b_pre
+// and for the gradients, with g = dz w_pre:
+//   dt = dh' + r (g - [layer] mean(g) - xh mean(g xh)),  dh = alpha dt
+//   du = beta a dt,  dgate = beta act'(gate) u dt
+//   dy = r_y (gy - [layer] mean(gy) - yh mean(gy yh)), gy = du w_post   (else dy = du)
+//   dw_pre = sum dz xh, db_pre = sum dz, dw_post = sum du yh, db_post = sum du over tokens.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/flce.h"
+#include "ckpt.cuh"
+
+namespace flce {
+
+struct RowTensor {
+  void* p;
+  int64_t row;  // stride in elements
+};
+
+struct NormParams {
+  int64_t N;
+  int32_t H;
+  int32_t layer, post, pre, params_fp32;
+  int32_t gate_kind, act;
+  float alpha, beta, eps, inv_h;
+  RowTensor y, h, gate, h_out, z, dz, dh_out, dy, dh, dgate;
+  const void *w_post, *b_post, *w_pre, *b_pre;
+  float* stats;        // [4][N]
+  Ckpt ckpt;           // forward; codes null: none
+  // launch shape
+  int32_t warps;       // that share a row (of each CTA of a cluster)
+  int32_t groups;      // rows of a CTA at a time
+  // backward
+  int32_t cluster;     // CTAs that share a row
+  int32_t octets;      // of a row in each CTA of a cluster
+  float* part[5];      // sums over tokens of dw_pre, db_pre, dw_post, db_post, dgate:
+                       // [parts][H], or [parts] for a scalar gate; null: not wanted
+};
+
+constexpr int kMaxH = 16384;
+
+cudaError_t launch_resnorm_fwd(const NormParams& p, int y_bytes, int h_bytes, int sms,
+                               cudaStream_t s);
+
+// Sets the launch shape; returns the rows of each of part[].
+int64_t plan_resnorm_bwd(NormParams& p, int sms);
+cudaError_t launch_resnorm_bwd_bf16(const NormParams& p, int64_t parts, cudaStream_t s);
+cudaError_t launch_resnorm_bwd_mixed(const NormParams& p, int64_t parts, cudaStream_t s);
+cudaError_t launch_resnorm_bwd_fp32(const NormParams& p, int64_t parts, cudaStream_t s);
+
+// out[k][col] = sum over `parts` rows of part[k], fp32, in a fixed order.
+struct NormSums {
+  const float* part[5];
+  float* out[5];
+  int32_t width[5];  // columns; 0: not wanted
+  int64_t parts;
+};
+cudaError_t launch_resnorm_sums(const NormSums& p, cudaStream_t s);
+
+// act(g) and its derivative
+__device__ __forceinline__ float gate_act(int act, float g) {
+  if (act == FLCE_ACT_SIGMOID) return 1.f / (1.f + expf(-g));
+  return act == FLCE_ACT_TANH ? tanhf(g) : g;
+}
+__device__ __forceinline__ float gate_slope(int act, float a) {
+  if (act == FLCE_ACT_SIGMOID) return a * (1.f - a);
+  return act == FLCE_ACT_TANH ? 1.f - a * a : 1.f;
+}
+
+}  // namespace flce
