@@ -38,6 +38,7 @@ struct NormParams {
   // launch shape
   int32_t warps;       // that share a row (of each CTA of a cluster)
   int32_t groups;      // rows of a CTA at a time
+  int32_t stages;      // of the ring of rows
   // backward
   int32_t cluster;     // CTAs that share a row
   int32_t octets;      // of a row in each CTA of a cluster
@@ -46,6 +47,7 @@ struct NormParams {
 };
 
 constexpr int kMaxH = 16384;
+constexpr int kSmemPerSm = 200 << 10;  // for rings, beside the slots of the sums
 
 cudaError_t launch_resnorm_fwd(const NormParams& p, int y_bytes, int h_bytes, int sms,
                                cudaStream_t s);

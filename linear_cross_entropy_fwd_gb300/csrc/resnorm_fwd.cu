@@ -74,6 +74,7 @@ __device__ __forceinline__ void normalise(float (&x)[NV][8], const bool (&in)[NV
   r *= scale;
 }
 
+// x[j] = x[j] * w + b; either may be missing.
 template <class T, int NV>
 __device__ __forceinline__ void affine(float (&x)[NV][8], const bool (&in)[NV],
                                        const int (&oct)[NV], const void* w, const void* b,
@@ -96,9 +97,10 @@ __device__ __forceinline__ void affine(float (&x)[NV][8], const bool (&in)[NV],
 }
 
 template <class TY, class TH, int NV>
-__global__ void __launch_bounds__(kFwdThreads, NV == 4 ? 1 : 2)
+__global__ void __launch_bounds__(kFwdThreads, NV == 1 ? 2 : 1)
     resnorm_fwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float slots[kMaxRowWarps][2][kMaxSums][kMaxRowWarps];
+  extern __shared__ __align__(16) uint8_t ring_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = warp / p.warps;
   RowSums sums{slots[group], p.warps, warp - group * p.warps, group, 0};
@@ -113,60 +115,128 @@ __global__ void __launch_bounds__(kFwdThreads, NV == 4 ? 1 : 2)
     oct[j] = (j * p.warps + sums.warp) * 32 + lane;
     in[j] = oct[j] < octets;
   }
-  const bool pfp = p.params_fp32;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * p.groups + group; row < p.N;
-       row += static_cast<int64_t>(gridDim.x) * p.groups) {
-    float x[NV][8], hv[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = hv[j][i] = 0.f;
-      if (in[j]) {
-        octet_floats(load_octet<TY>(row_at<TY>(p.y.p, row, p.y.row), oct[j]), x[j]);
-        if (p.h.p) octet_floats(load_octet<TH>(row_at<TH>(p.h.p, row, p.h.row), oct[j]), hv[j]);
-      }
-    }
-    float mean_y = 0.f, r_y = 0.f, mean_h = 0.f, r_h = 0.f;
-    if (p.post) {
-      normalise<NV>(x, in, p.layer, p.eps, p.inv_h, sums, mean_y, r_y);
-      affine<TY, NV>(x, in, oct, p.w_post, p.b_post, pfp);
-    }
-    if (p.gate_kind != FLCE_GATE_NONE) {
-      float a = 0.f;
-      if (p.gate_kind == FLCE_GATE_SCALAR)
-        a = gate_act(p.act, one_element<TY>(p.gate.p, pfp, 0));
-      else if (p.gate_kind == FLCE_GATE_TOKEN)
-        a = gate_act(p.act, one_element<TY>(p.gate.p, false, row * p.gate.row));
+  const bool pfp = p.params_fp32, full = p.gate_kind == FLCE_GATE_FULL;
+  const bool channel = p.gate_kind == FLCE_GATE_CHANNEL;
+
+  // The ring: of each octet y, then h, then a gate per element.
+  const uint32_t step = blockDim.x * 16;
+  const uint32_t ring = smem_addr(ring_raw) + threadIdx.x * 16;
+  constexpr int kPer = 2 * kPieces<TY> + kPieces<TH>;
+  const uint32_t stage = step * NV * kPer;
+  auto fetch = [&](int64_t row, int s) {
+    if (row < p.N) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (!in[j]) continue;
-        float t[8];
-        if (p.gate_kind == FLCE_GATE_CHANNEL)
-          param_octet<TY>(p.gate.p, pfp, oct[j], 1.f, t);
-        else if (p.gate_kind == FLCE_GATE_FULL)
-          octet_floats(load_octet<TY>(row_at<TY>(p.gate.p, row, p.gate.row), oct[j]), t);
-        const bool each = p.gate_kind == FLCE_GATE_CHANNEL || p.gate_kind == FLCE_GATE_FULL;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[j][i] *= each ? gate_act(p.act, t[i]) : a;
+        const uint32_t at = ring + s * stage + j * kPer * step;
+        copy_octet<TY>(at, step, row_at<TY>(p.y.p, row, p.y.row), oct[j]);
+        if (p.h.p)
+          copy_octet<TH>(at + kPieces<TY> * step, step, row_at<TH>(p.h.p, row, p.h.row), oct[j]);
+        if (full)
+          copy_octet<TY>(at + (kPieces<TY> + kPieces<TH>) * step, step,
+                         row_at<TY>(p.gate.p, row, p.gate.row), oct[j]);
       }
     }
+    copies_commit();
+  };
+
+  // What multiplies n(y) whatever the row: beta, the weight and a gate per channel; with
+  // `b`, what is added (0 without a bias).  And a gate per element.
+  auto factor = [&](const void* w, float missing, int o, float (&f)[8]) {
+    param_octet<TY>(w, pfp, o, missing, f);
+    if (channel) {
+      float t[8];
+      param_octet<TY>(p.gate.p, pfp, o, 1.f, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= gate_act(p.act, t[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= p.beta;
+  };
+  // A thread with one octet keeps its factors.
+  float c[8], w_pre[8];
+  if (NV == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = w_pre[i] = 0.f;
+    if (in[0]) {
+      factor(p.w_post, 1.f, oct[0], c);
+      param_octet<TY>(p.w_pre, pfp, oct[0], 1.f, w_pre);
+    }
+  }
+  const bool token = p.gate_kind == FLCE_GATE_TOKEN;
+  float one = 1.f;  // a gate with one value
+  if (p.gate_kind == FLCE_GATE_SCALAR) one = gate_act(p.act, one_element<TY>(p.gate.p, pfp, 0));
+
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.groups + group;
+  const int64_t rows = static_cast<int64_t>(gridDim.x) * p.groups;
+  int s_in = 0, s_out = 0;
+  for (; s_in < p.stages - 1; ++s_in) fetch(first + s_in * rows, s_in);
+  for (int64_t row = first; row < p.N; row += rows) {
+    fetch(row + (p.stages - 1) * rows, s_in);
+    s_in = s_in + 1 == p.stages ? 0 : s_in + 1;
+    if (token) one = gate_act(p.act, one_element<TY>(p.gate.p, false, row * p.gate.row));
+    copies_wait(p.stages - 1);
+    const uint32_t at = ring + s_out * stage;
+    s_out = s_out + 1 == p.stages ? 0 : s_out + 1;
+    float x[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = fmaf(p.alpha, hv[j][i], p.beta * x[j][i]);
+      for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+      if (in[j]) shared_octet(TY{}, at + j * kPer * step, step, x[j]);
+    }
+    float mean_y = 0.f, r_y = 0.f, mean_h = 0.f, r_h = 0.f;
+    if (p.post) normalise<NV>(x, in, p.layer, p.eps, p.inv_h, sums, mean_y, r_y);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!in[j]) continue;
+      const uint32_t mine = at + j * kPer * step;
+      float t[8];
+      if (NV == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] *= c[i];
+      } else {
+        factor(p.w_post, 1.f, oct[j], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] *= t[i];
+      }
+      if (p.b_post) {
+        factor(p.b_post, 0.f, oct[j], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] += t[i];
+      }
+      if (full) {
+        shared_octet(TY{}, mine + (kPieces<TY> + kPieces<TH>) * step, step, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] *= gate_act(p.act, t[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] *= one;
+      if (p.h.p) {
+        shared_octet(TH{}, mine + kPieces<TY> * step, step, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] = fmaf(p.alpha, t[i], x[j][i]);
+      }
       // the stream is what is stored of it; see flce_resnorm
       const auto o = to_octet(TH{}, x[j]);
       octet_floats(o, x[j]);
-      if (in[j] && p.h_out.p)
+      if (p.h_out.p)
         static_cast<typename Elem<TH>::Octet*>(row_at<TH>(p.h_out.p, row, p.h_out.row))[oct[j]] = o;
     }
     if (p.pre) {
       normalise<NV>(x, in, p.layer, p.eps, p.inv_h, sums, mean_h, r_h);
-      affine<TY, NV>(x, in, oct, p.w_pre, p.b_pre, pfp);
+      if (NV == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[0][i] *= w_pre[i];
+        affine<TY, NV>(x, in, oct, nullptr, p.b_pre, pfp);
+      } else {
+        affine<TY, NV>(x, in, oct, p.w_pre, p.b_pre, pfp);
+      }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const auto o = to_octet(TY{}, x[j]);
-        if (in[j]) static_cast<typename Elem<TY>::Octet*>(row_at<TY>(p.z.p, row, p.z.row))[oct[j]] = o;
+        if (in[j])
+          static_cast<typename Elem<TY>::Octet*>(row_at<TY>(p.z.p, row, p.z.row))[oct[j]] = o;
         if (p.ckpt.codes) {
           octet_floats(o, x[j]);
           ckpt_store_octet(p.ckpt, row, oct[j], x[j]);
@@ -184,13 +254,23 @@ __global__ void __launch_bounds__(kFwdThreads, NV == 4 ? 1 : 2)
 
 template <class TY, class TH, int NV>
 cudaError_t launch(NormParams p, int sms, cudaStream_t s) {
+  static SmemLimit limit;
   const int octets = p.H / 8;
   p.warps = (octets + 32 * NV - 1) / (32 * NV);
   p.groups = kFwdThreads / 32 / p.warps;
+  const int threads = 32 * p.warps * p.groups;
+  const int stage = threads * 16 * NV * (2 * kPieces<TY> + kPieces<TH>);
+  // two CTAs on an SM where the registers let them, or one
+  int ctas = NV == 1 ? 2 : 1;
+  if (ctas == 2 && kSmemPerSm / 2 / stage < 3) ctas = 1;
+  p.stages = kSmemPerSm / ctas / stage;
+  if (p.stages > 4) p.stages = 4;
+  const cudaError_t e = limit.raise(resnorm_fwd_kernel<TY, TH, NV>, kSmemPerSm);
+  if (e != cudaSuccess) return e;
   const int64_t want = (p.N + p.groups - 1) / p.groups;
-  const int64_t most = static_cast<int64_t>(sms) * (NV == 4 ? 1 : 2);
-  resnorm_fwd_kernel<TY, TH, NV>
-      <<<static_cast<unsigned>(want < most ? want : most), 32 * p.warps * p.groups, 0, s>>>(p);
+  const int64_t most = static_cast<int64_t>(sms) * ctas;
+  resnorm_fwd_kernel<TY, TH, NV><<<static_cast<unsigned>(want < most ? want : most), threads,
+                                   static_cast<size_t>(p.stages) * stage, s>>>(p);
   return cudaGetLastError();
 }
 

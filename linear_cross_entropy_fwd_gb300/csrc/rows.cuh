@@ -102,6 +102,63 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 constexpr int kMaxRowWarps = 16;  // warps that share a row
 constexpr int kMaxSums = 8;
 
+// ---------------------------------------------------------------------------
+// A ring of rows in shared memory.  Every thread copies its own octets of the next rows with
+// 16-byte asynchronous copies and reads only those, so that no thread waits for another's;
+// the rows in flight hide memory's latency whatever the registers hold.  Stage `s` keeps
+// piece k of a thread at (s * pieces + k) * threads + thread.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Until at most `n` (0 .. 5) of this thread's groups are in flight.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (n == 4)
+    asm volatile("cp.async.wait_group 4;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 5;" ::: "memory");
+}
+constexpr int kMaxStages = 6;
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Octet `o` of a row of T to shared memory, its 16-byte pieces `step` apart; and back.
+template <class T>
+__device__ __forceinline__ void copy_octet(uint32_t dst, uint32_t step, const void* row, int o) {
+  const uint8_t* src = static_cast<const uint8_t*>(row) + o * (8 * Elem<T>::kBytes);
+  copy16(dst, src);
+  if (Elem<T>::kBytes == 4) copy16(dst + step, src + 16);
+}
+__device__ __forceinline__ void shared_octet(bf16_t, uint32_t a, uint32_t, float (&f)[8]) {
+  octet_floats(ld_shared16(a), f);
+}
+__device__ __forceinline__ void shared_octet(float, uint32_t a, uint32_t step, float (&f)[8]) {
+  Elem<float>::Octet o;
+  o.a = ld_shared16(a);
+  o.b = ld_shared16(a + step);
+  octet_floats(o, f);
+}
+template <class T>
+constexpr int kPieces = Elem<T>::kBytes / 2;  // 16-byte pieces of an octet
+
+// ---------------------------------------------------------------------------
 // Sums over a row that `warps` warps of the CTA share.  Every thread gets them, added in
 // an order that does not depend on timing.  Two sets of slots in turn: a warp that writes
 // one has passed the barrier that everybody reached after reading it.
@@ -123,29 +180,51 @@ struct RowSums {
     return v;
   }
 
+  // K sums (1, 2, 4 or 8) at once.  In a warp, each of the first log2 K exchanges also
+  // halves the number of sums that a lane goes on with, so that K sums take K + 4 - log2 K
+  // exchanges and lane l ends with sum l / (32 / K); the warps' sums are read back in the
+  // same arrangement.
   template <int K>
   __device__ __forceinline__ void add(float (&v)[K]) {
-    static_assert(K <= kMaxSums, "slots");
+    static_assert(K == 1 || K == 2 || K == 4 || K == 8, "a power of two");
+    constexpr int kLanes = 32 / K;  // that hold the same sum
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
+    for (int n = K / 2, d = 16; n > 0; n >>= 1, d >>= 1) {
+      const bool up = lane & d;
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
-    if (warps == 1) return;
-    float(*s)[kMaxRowWarps] = slots[turn & 1];
-    ++turn;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) s[k][warp] = v[k];
-    }
-    named_barrier(1 + id, warps * 32);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float4 t = *reinterpret_cast<const float4*>(&s[k][0]);
-      v[k] = (t.x + t.y) + (t.z + t.w);
-      for (int w = 4; w < warps; w += 4) {
-        t = *reinterpret_cast<const float4*>(&s[k][w]);
-        v[k] += (t.x + t.y) + (t.z + t.w);
+      for (int k = 0; k < n; ++k) {
+        const float give = up ? v[k] : v[k + n];
+        v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, give, d);
       }
+    }
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+    float t = v[0];
+    if (warps > 1) {
+      float(*s)[kMaxRowWarps] = slots[turn & 1];
+      ++turn;
+      const int k = lane / kLanes;
+      if (lane % kLanes == 0) s[k][warp] = t;
+      named_barrier(1 + id, warps * 32);
+      if (K == 8) {
+        const float4 q = *reinterpret_cast<const float4*>(&s[k][4 * (lane & 3)]);
+        t = (q.x + q.y) + (q.z + q.w);
+      } else if (K == 4) {
+        const float2 q = *reinterpret_cast<const float2*>(&s[k][2 * (lane & 7)]);
+        t = q.x + q.y;
+      } else {
+        t = s[k][lane & 15];
+      }
+      constexpr int kHold = K == 1 ? 16 : kLanes;  // lanes that share a sum's parts
+#pragma unroll
+      for (int d = kHold / 2; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    }
+    if (K == 1) {
+      v[0] = t;
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, t, k * kLanes);
     }
   }
 };
