@@ -21,7 +21,7 @@ struct CkptParams {
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p) {
   const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets) + threadIdx.x;
-  float v[kOctets][8];
+  Oct v[kOctets];
   int64_t row[kOctets];
   int o[kOctets];
 #pragma unroll
@@ -29,12 +29,11 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
     const int64_t i = base + k * kThreads;
     row[k] = i / p.padded;
     o[k] = static_cast<int>(i - row[k] * p.padded);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+    v[k] = zero_oct();
     if (i >= p.total)
       o[k] = p.padded;  // stores nothing
     else if (o[k] < p.octets)
-      octet_floats(load_octet<T>(row_at<T>(p.x, row[k], p.x_row), o[k]), v[k]);
+      v[k] = load_octet<T>(row_at<T>(p.x, row[k], p.x_row), o[k]);
   }
 #pragma unroll
   for (int k = 0; k < kOctets; ++k) ckpt_store_octet(p.c, row[k], o[k], v[k]);
@@ -49,9 +48,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p)
     if (i >= p.total) break;
     const int64_t row = i / p.padded;
     const int o = static_cast<int>(i - row * p.padded);
-    float v[8];
-    ckpt_load_octet(p.c, row, o, v);
-    store_octet<T>(row_at<T>(p.x, row, p.x_row), o, v);
+    store_octet<T>(row_at<T>(p.x, row, p.x_row), o, ckpt_load_octet(p.c, row, o));
   }
 }
 

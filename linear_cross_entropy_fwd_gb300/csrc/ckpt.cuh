@@ -49,23 +49,30 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
   return f;
 }
 
-// Stores octet `o` of a row: v holds its values (zeros behind the row's end, where `o` may
+// Stores octet `o` of a row: x holds its values (zeros behind the row's end, where `o` may
 // lie too).  Executed by whole warps whose lanes hold consecutive octets, lane 0 a multiple
 // of 4, so that four lanes hold a group.
 __device__ __forceinline__ void ckpt_store_octet(const Ckpt& c, int64_t row, int o,
-                                                 const float (&v)[8]) {
+                                                 const Oct& x) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 4; ++i) {
+    top = max(top, __float_as_uint(x.p[i].x) & 0x7fffffffu);
+    top = max(top, __float_as_uint(x.p[i].y) & 0x7fffffffu);
+  }
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   // ceil(log2(top / 448)) + 127: 448 = 1.75 * 2^8, and a mantissa above .75 carries
   int s = static_cast<int>((top + 0x1fffffu) >> 23) - 8;
   s = min(max(s, 127 - 117), 127 + 119);
   const float inv = __uint_as_float(static_cast<uint32_t>(254 - s) << 23);  // 2^-e
-  uint2 w;
-  w.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
-  w.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = mul2(x.p[i], pair(inv));
+    q[i] = e4m3x2(t.x, t.y);
+  }
+  uint2 w = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
   if (top >= 0x7f800000u) {
     s = 255;
     w = make_uint2(0, 0);
@@ -86,15 +93,14 @@ __device__ __forceinline__ float ckpt_scale(uint32_t byte) {
 }
 
 // Octet `o` of a row.
-__device__ __forceinline__ void ckpt_load_octet(const Ckpt& c, int64_t row, int o, float (&v)[8]) {
+__device__ __forceinline__ Oct ckpt_load_octet(const Ckpt& c, int64_t row, int o) {
   const uint2 w = *reinterpret_cast<const uint2*>(c.codes + row * c.pitch + o * 8);
   const float f = ckpt_scale(c.scales[row * c.spitch + (o >> 2)]);
+  Oct x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = from_e4m3x2((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
-    v[2 * i] = t.x * f;
-    v[2 * i + 1] = t.y * f;
-  }
+  for (int i = 0; i < 4; ++i)
+    x.p[i] = mul2(from_e4m3x2((i < 2 ? w.x : w.y) >> (16 * (i & 1))), pair(f));
+  return x;
 }
 
 // x [N, H] = the checkpoint; elements of 2 (bf16) or 4 bytes, rows x_row elements apart.

@@ -22,7 +22,8 @@ namespace flce {
 
 struct RowTensor {
   void* p;
-  int64_t row;  // stride in elements
+  int64_t row;   // stride in elements
+  int64_t step;  // bytes from a row to the next one of the same warps
 };
 
 struct NormParams {
@@ -38,7 +39,6 @@ struct NormParams {
   // launch shape
   int32_t warps;       // that share a row (of each CTA of a cluster)
   int32_t groups;      // rows of a CTA at a time
-  int32_t stages;      // of the ring of rows
   // backward
   int32_t cluster;     // CTAs that share a row
   int32_t octets;      // of a row in each CTA of a cluster
@@ -46,11 +46,18 @@ struct NormParams {
                        // [parts][H], or [parts] for a scalar gate; null: not wanted
 };
 
+// The steps of a launch whose warps take every `rows`-th row.
+inline void set_steps(NormParams& p, int64_t rows, int y_bytes, int h_bytes) {
+  for (RowTensor* t : {&p.y, &p.gate, &p.z, &p.dz, &p.dy, &p.dgate}) t->step = rows * t->row * y_bytes;
+  for (RowTensor* t : {&p.h, &p.h_out, &p.dh_out, &p.dh}) t->step = rows * t->row * h_bytes;
+}
+
 constexpr int kMaxH = 16384;
 constexpr int kSmemPerSm = 200 << 10;  // for rings, beside the slots of the sums
 
-cudaError_t launch_resnorm_fwd(const NormParams& p, int y_bytes, int h_bytes, int sms,
-                               cudaStream_t s);
+cudaError_t launch_resnorm_fwd_bf16(const NormParams& p, int sms, cudaStream_t s);
+cudaError_t launch_resnorm_fwd_mixed(const NormParams& p, int sms, cudaStream_t s);
+cudaError_t launch_resnorm_fwd_fp32(const NormParams& p, int sms, cudaStream_t s);
 
 // Sets the launch shape; returns the rows of each of part[].
 int64_t plan_resnorm_bwd(NormParams& p, int sms);
@@ -67,14 +74,22 @@ struct NormSums {
 };
 cudaError_t launch_resnorm_sums(const NormSums& p, cudaStream_t s);
 
-// act(g) and its derivative
+// act(g), and its derivative by act(g).  Quotients and exponentials within 2 units.
 __device__ __forceinline__ float gate_act(int act, float g) {
-  if (act == FLCE_ACT_SIGMOID) return 1.f / (1.f + expf(-g));
+  if (act == FLCE_ACT_SIGMOID) return __fdividef(1.f, 1.f + expf(-g));
   return act == FLCE_ACT_TANH ? tanhf(g) : g;
 }
 __device__ __forceinline__ float gate_slope(int act, float a) {
   if (act == FLCE_ACT_SIGMOID) return a * (1.f - a);
   return act == FLCE_ACT_TANH ? 1.f - a * a : 1.f;
 }
+__device__ __forceinline__ Oct gate_act_each(int act, Oct g) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    g.p[i] = make_float2(gate_act(act, g.p[i].x), gate_act(act, g.p[i].y));
+  return g;
+}
+// The same out of line, for what is done once: the code around it stays short.
+static __device__ __noinline__ Oct gate_act_oct(int act, Oct g) { return gate_act_each(act, g); }
 
 }  // namespace flce

@@ -8,18 +8,31 @@
 namespace flce {
 namespace {
 
-constexpr int kSumLanes = 32, kSumRows = 8;
+constexpr int kSumLanes = 32, kSumRows = 16, kSumAtOnce = 5;
 
-// One thread row takes every kSumRows-th part, then the thread rows are added in order.
+// One thread row takes every kSumRows-th part, kSumAtOnce loads in flight, then the thread
+// rows are added in order.
 __global__ void __launch_bounds__(kSumLanes * kSumRows)
     resnorm_sums_kernel(const __grid_constant__ NormSums p) {
   __shared__ float s[kSumRows][kSumLanes + 1];
   const int k = blockIdx.y, lane = threadIdx.x % kSumLanes, ty = threadIdx.x / kSumLanes;
   const int col = blockIdx.x * kSumLanes + lane;
+  grid_dependency_wait();
   if (blockIdx.x * kSumLanes >= static_cast<unsigned>(p.width[k])) return;
   float v = 0.f;
-  if (col < p.width[k])
-    for (int64_t i = ty; i < p.parts; i += kSumRows) v += p.part[k][i * p.width[k] + col];
+  if (col < p.width[k]) {
+    const float* at = p.part[k] + col;
+    for (int64_t i = ty; i < p.parts; i += kSumRows * kSumAtOnce) {
+      float t[kSumAtOnce];
+#pragma unroll
+      for (int j = 0; j < kSumAtOnce; ++j) {
+        const int64_t n = i + j * kSumRows;
+        t[j] = n < p.parts ? at[n * p.width[k]] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kSumAtOnce; ++j) v += t[j];
+    }
+  }
   s[ty][lane] = v;
   __syncthreads();
   if (ty != 0 || col >= p.width[k]) return;
@@ -33,9 +46,17 @@ cudaError_t launch_resnorm_sums(const NormSums& p, cudaStream_t s) {
   int most = 0;
   for (int k = 0; k < 5; ++k) most = p.width[k] > most ? p.width[k] : most;
   if (most == 0) return cudaSuccess;
-  resnorm_sums_kernel<<<dim3(static_cast<unsigned>((most + kSumLanes - 1) / kSumLanes), 5),
-                        kSumLanes * kSumRows, 0, s>>>(p);
-  return cudaGetLastError();
+  // its CTAs may start while the rows' kernel ends
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>((most + kSumLanes - 1) / kSumLanes), 5);
+  cfg.blockDim = dim3(kSumLanes * kSumRows);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.parts > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, resnorm_sums_kernel, p);
 }
 
 int64_t plan_resnorm_bwd(NormParams& p, int sms) {
@@ -256,7 +277,7 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
   p.beta = a.beta;
   p.eps = a.eps;
   p.inv_h = 1.f / static_cast<float>(H);
-  auto row = [](const void* q, int64_t stride) { return RowTensor{const_cast<void*>(q), stride}; };
+  auto row = [](const void* q, int64_t stride) { return RowTensor{const_cast<void*>(q), stride, 0}; };
   p.y = row(a.y, a.y_row);
   p.gate = row(a.gate, a.gate_row);
   p.w_post = a.w_post;
@@ -273,7 +294,9 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
     if ((rc = call.begin(o, 0, StepCall::kIfAsked))) return rc;
     if (N > 0) {
       const cudaError_t e =
-          launch_resnorm_fwd(p, static_cast<int>(ey), static_cast<int>(eh), sms, call.stream);
+          ey == 4   ? launch_resnorm_fwd_fp32(p, sms, call.stream)
+          : eh == 4 ? launch_resnorm_fwd_mixed(p, sms, call.stream)
+                    : launch_resnorm_fwd_bf16(p, sms, call.stream);
       if (e != cudaSuccess) rc = host_cuda_error(e, "resnorm_fwd");
     }
     return call.end(rc);

@@ -55,6 +55,9 @@ constexpr int kBwdPieces =
     kPieces<TY> + 2 * kPieces<TH> + (POST || GATE != kNoGate ? kPieces<TY> : 0) +
     (GATE == kFullGate ? kPieces<TY> : 0);
 
+template <class TY, class TH, bool POST, int GATE>
+constexpr int kBwdStages = ring_stages(kBwdPieces<TY, TH, POST, GATE>, kBwdThreads, kSmemPerSm, 6);
+
 // AFF: a mean or a bias is wanted.
 template <class TY, class TH, bool POST, bool AFF, int GATE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -71,6 +74,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     (&slots[0][0][0][0])[i] = 0.f;
   __syncthreads();
   if (p.cluster > 1) cluster_sync();  // every CTA runs before its slots are written
+  grid_launch_dependents();  // the sums' CTAs take the SMs that this launch's leave
   const int in_cta = sums.warp * 32 + lane;
   const int oct = rank * p.octets + in_cta;
   const bool in = in_cta < p.octets && oct < p.H / 8;
@@ -79,26 +83,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // a is the same in every row, so that it and the weight multiply the sums, not the rows
   constexpr bool kFixed = GATE == kNoGate || GATE == kChannelGate;
 
+  const int64_t unit = static_cast<int64_t>(blockIdx.x / p.cluster) * p.groups + group;
+  const int64_t units = static_cast<int64_t>(gridDim.x / p.cluster) * p.groups;
   const uint32_t step = blockDim.x * 16;
   const uint32_t ring = smem_addr(ring_raw) + threadIdx.x * 16;
-  const uint32_t stage = step * kBwdPieces<TY, TH, POST, GATE>;
+  constexpr int kStages = kBwdStages<TY, TH, POST, GATE>;
+  const uint32_t stage = step * kBwdPieces<TY, TH, POST, GATE>, end = kStages * stage;
   const uint32_t at_h = kPieces<TY> * step, at_dh = at_h + kPieces<TH> * step;
   const uint32_t at_y = at_dh + kPieces<TH> * step, at_gate = at_y + kPieces<TY> * step;
-  auto fetch = [&](int64_t row, int s) {
-    if (in && row < p.N) {
-      const uint32_t at = ring + s * stage;
+  int64_t ahead = unit;
+  Walk<TY> dz_in(p.dz.p, p.dz.row, unit, oct), y_in(p.y.p, p.y.row, unit, oct);
+  Walk<TH> h_in(p.h_out.p, p.h_out.row, unit, oct);
+  Walk<TH> dh_in(p.dh_out.p, p.dh_out.row, unit, oct);
+  Walk<TY> gate_in(p.gate.p, p.gate.row, unit, oct);
+  auto fetch = [&](uint32_t s) {
+    if (in && ahead < p.N) {
+      const uint32_t at = ring + s;
       if (p.pre) {
-        copy_octet<TY>(at, step, row_at<TY>(p.dz.p, row, p.dz.row), oct);
-        copy_octet<TH>(at + at_h, step, row_at<TH>(p.h_out.p, row, p.h_out.row), oct);
+        copy_octet<TY>(at, step, dz_in.at);
+        copy_octet<TH>(at + at_h, step, h_in.at);
       }
-      if (p.dh_out.p)
-        copy_octet<TH>(at + at_dh, step, row_at<TH>(p.dh_out.p, row, p.dh_out.row), oct);
-      if (kReadsY) copy_octet<TY>(at + at_y, step, row_at<TY>(p.y.p, row, p.y.row), oct);
-      if (GATE == kFullGate)
-        copy_octet<TY>(at + at_gate, step, row_at<TY>(p.gate.p, row, p.gate.row), oct);
+      if (p.dh_out.p) copy_octet<TH>(at + at_dh, step, dh_in.at);
+      if (kReadsY) copy_octet<TY>(at + at_y, step, y_in.at);
+      if (GATE == kFullGate) copy_octet<TY>(at + at_gate, step, gate_in.at);
+      ahead += units;
+      dz_in.at += p.dz.step;
+      h_in.at += p.h_out.step;
+      dh_in.at += p.dh_out.step;
+      if (kReadsY) y_in.at += p.y.step;
+      if (GATE == kFullGate) gate_in.at += p.gate.step;
     }
     copies_commit();
   };
+  uint32_t s_in = 0, s_out = 0;
+  for (; s_in < end - stage; s_in += stage) fetch(s_in);
   // a row's statistics, and its gate of one value, one row ahead
   struct Row {
     float mean_y, r_y, mean_h, r_h, gate;
@@ -118,197 +136,201 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       t.gate = one_element<TY>(p.gate.p, false, row * p.gate.row);
     return t;
   };
+  Row next = read_row(unit);
 
-  float w_pre[8], w_post[8], b_post[8];  // w_post: times beta a where that is fixed
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w_pre[i] = w_post[i] = b_post[i] = 0.f;
-  auto gate_of_channel = [&](float (&a)[8]) {  // act(gate), 1 without one
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = 1.f;
-    if (GATE == kChannelGate) {
-      param_octet<TY>(p.gate.p, pfp, oct, 1.f, a);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = gate_act(p.act, a[i]);
-    }
+  auto gate_of_channel = [&]() {  // act(gate), 1 without one
+    if (GATE != kChannelGate) return same_oct(1.f);
+    return gate_act_oct(p.act, param_octet<TY>(p.gate.p, pfp, oct, 1.f));
   };
+  // w_post: times beta a where that is fixed
+  Oct w_pre = zero_oct(), w_post = zero_oct(), b_post = zero_oct();
   if (in) {
-    param_octet<TY>(p.w_pre, pfp, oct, 1.f, w_pre);
-    param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f, w_post);
+    w_pre = param_octet<TY>(p.w_pre, pfp, oct, 1.f);
+    w_post = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f);
     if (kFixed) {
-      float a[8];
-      gate_of_channel(a);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w_post[i] *= p.beta * a[i];
+      scale_oct(w_post, gate_of_channel());
+      scale_oct(w_post, p.beta);
     } else if (POST && AFF) {
-      param_octet<TY>(p.b_post, pfp, oct, 0.f, b_post);
+      b_post = param_octet<TY>(p.b_post, pfp, oct, 0.f);
     }
   }
   float scalar = 0.f;
   if (GATE == kOneGate && p.gate_kind == FLCE_GATE_SCALAR) scalar = one_element<TY>(p.gate.p, pfp, 0);
 
   // Sums over tokens: dz xh, dz, and with a fixed gate yh dt, dt; else yh du, du.
-  float s_pre[8], s_bpre[8], s_post[8], s_bpost[8], s_one = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s_pre[i] = s_bpre[i] = s_post[i] = s_bpost[i] = 0.f;
-
-  const int64_t unit = static_cast<int64_t>(blockIdx.x / p.cluster) * p.groups + group;
-  const int64_t units = static_cast<int64_t>(gridDim.x / p.cluster) * p.groups;
-  int s_in = 0, s_out = 0;
-  for (; s_in < p.stages - 1; ++s_in) fetch(unit + s_in * units, s_in);
-  Row next = read_row(unit);
+  Oct s_pre = zero_oct(), s_bpre = zero_oct(), s_post = zero_oct(), s_bpost = zero_oct();
+  float s_one = 0.f;
+  Walk<TY> dy(p.dy.p, p.dy.row, unit, oct), dgate(p.dgate.p, p.dgate.row, unit, oct);
+  Walk<TH> dh(p.dh.p, p.dh.row, unit, oct);
   for (int64_t row = unit; row < p.N; row += units) {
-    fetch(row + (p.stages - 1) * units, s_in);
-    s_in = s_in + 1 == p.stages ? 0 : s_in + 1;
+    fetch(s_in);
+    s_in = s_in + stage == end ? 0 : s_in + stage;
     const Row t = next;
     next = read_row(row + units);
-    copies_wait(p.stages - 1);
-    const uint32_t at = ring + s_out * stage;
-    s_out = s_out + 1 == p.stages ? 0 : s_out + 1;
+    copies_wait<kStages - 1>();
+    const uint32_t at = ring + s_out;
+    s_out = s_out + stage == end ? 0 : s_out + stage;
 
-    float dz[8], xh[8], e[8], yh[8], a[8], slope[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dz[i] = xh[i] = e[i] = yh[i] = a[i] = slope[i] = 0.f;
+    Oct dz = zero_oct(), xh = zero_oct(), e = zero_oct(), yh = zero_oct(), a = zero_oct(), slope;
     if (in) {
       if (p.pre) {
-        shared_octet(TY{}, at, step, dz);
-        shared_octet(TH{}, at + at_h, step, xh);
+        dz = shared_octet(TY{}, at, step);
+        xh = shared_octet(TH{}, at + at_h, step);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xh[i] = AFF ? (xh[i] - t.mean_h) * t.r_h : xh[i] * t.r_h;
+        for (int i = 0; i < 4; ++i)
+          xh.p[i] = mul2(AFF ? plus2(xh.p[i], pair(-t.mean_h)) : xh.p[i], pair(t.r_h));
       }
-      if (p.dh_out.p) shared_octet(TH{}, at + at_dh, step, e);
-      if (kReadsY) shared_octet(TY{}, at + at_y, step, yh);
+      if (p.dh_out.p) e = shared_octet(TH{}, at + at_dh, step);
+      if (kReadsY) yh = shared_octet(TY{}, at + at_y, step);
       if (POST) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) yh[i] = AFF ? (yh[i] - t.mean_y) * t.r_y : yh[i] * t.r_y;
+        for (int i = 0; i < 4; ++i)
+          yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-t.mean_y)) : yh.p[i], pair(t.r_y));
       }
-      if (GATE == kFullGate) shared_octet(TY{}, at + at_gate, step, a);
+      if (GATE == kFullGate) a = shared_octet(TY{}, at + at_gate, step);
     }
     // beta act(gate) and its slope
-    if (GATE == kFullGate || GATE == kOneGate) {
+    auto act_of = [&](float g, float& value, float& gradient) {
+      g = gate_act(p.act, g);
+      gradient = p.beta * gate_slope(p.act, g);
+      value = p.beta * g;
+    };
+    if (GATE == kFullGate) {
 #pragma unroll
-      for (int i = 0; i < (GATE == kOneGate ? 1 : 8); ++i) {
-        if (GATE == kOneGate) a[i] = p.gate_kind == FLCE_GATE_TOKEN ? t.gate : scalar;
-        a[i] = gate_act(p.act, a[i]);
-        slope[i] = p.beta * gate_slope(p.act, a[i]);
-        a[i] *= p.beta;
+      for (int i = 0; i < 4; ++i) {
+        act_of(a.p[i].x, a.p[i].x, slope.p[i].x);
+        act_of(a.p[i].y, a.p[i].y, slope.p[i].y);
       }
     }
-    // beta a w_post of element i
-    auto weight = [&](int i) {
-      return kFixed ? w_post[i] : (GATE == kOneGate ? a[0] : a[i]) * w_post[i];
-    };
+    float one_a = 0.f, one_slope = 0.f;
+    if (GATE == kOneGate)
+      act_of(p.gate_kind == FLCE_GATE_TOKEN ? t.gate : scalar, one_a, one_slope);
+    // beta a, and beta a w_post
+    auto gate_at = [&](int i) { return GATE == kOneGate ? pair(one_a) : a.p[i]; };
+    auto weight = [&](int i) { return kFixed ? w_post.p[i] : mul2(gate_at(i), w_post.p[i]); };
 
     // sums: g xh, [g], and with a post-norm q yh e, q yh xh, [q yh, q e, q, q xh]
     constexpr int K = POST ? (AFF ? 8 : 4) : (AFF ? 2 : 1);
-    float v[K];
+    float2 v[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.f;
+    for (int k = 0; k < K; ++k) v[k] = pair(0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float g = dz[i] * w_pre[i];
-      v[0] = fmaf(g, xh[i], v[0]);
-      e[i] = fmaf(t.r_h, g, e[i]);
-      if (AFF) v[K - 1] += g;
+    for (int i = 0; i < 4; ++i) {
+      const float2 g = mul2(dz.p[i], w_pre.p[i]);
+      v[0] = mad2(g, xh.p[i], v[0]);
+      e.p[i] = mad2(pair(t.r_h), g, e.p[i]);
+      if (AFF) v[K - 1] = plus2(v[K - 1], g);
       if (POST) {
-        const float q = weight(i), qy = q * yh[i];
-        v[1] = fmaf(qy, e[i], v[1]);
-        v[2] = fmaf(qy, xh[i], v[2]);
+        const float2 q = weight(i), qy = mul2(q, yh.p[i]);
+        v[1] = mad2(qy, e.p[i], v[1]);
+        v[2] = mad2(qy, xh.p[i], v[2]);
         if (AFF) {
-          v[3] += qy;
-          v[4] = fmaf(q, e[i], v[4]);
-          v[5] += q;
-          v[6] = fmaf(q, xh[i], v[6]);
+          v[3] = plus2(v[3], qy);
+          v[4] = mad2(q, e.p[i], v[4]);
+          v[5] = plus2(v[5], q);
+          v[6] = mad2(q, xh.p[i], v[6]);
         }
       }
     }
+    float s[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = v[k].x + v[k].y;
     if (p.pre || POST) {
-      sums.add(v);
-      more.add(v);
+      sums.add(s);
+      more.add(s);
     }
-    const float m2 = t.r_h * v[0] * p.inv_h;
-    const float m1 = AFF && layer ? t.r_h * v[K - 1] * p.inv_h : 0.f;
+    const float m2 = t.r_h * s[0] * p.inv_h;
+    const float m1 = AFF && layer ? t.r_h * s[K - 1] * p.inv_h : 0.f;
     float c1 = 0.f, c2 = 0.f;
     if (POST) {
-      c2 = (v[1] - m2 * v[2] - (AFF ? m1 * v[3] : 0.f)) * p.inv_h;
-      if (AFF && layer) c1 = (v[4] - m2 * v[6] - m1 * v[5]) * p.inv_h;
+      c2 = t.r_y * p.inv_h * (s[1] - m2 * s[2] - (AFF ? m1 * s[3] : 0.f));
+      if (AFF && layer) c1 = t.r_y * p.inv_h * (s[4] - m2 * s[6] - m1 * s[5]);
     }
-    float one = 0.f, dg[8];
+    float2 one = pair(0.f);
+    Oct dg;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float dt = fmaf(-m2, xh[i], e[i]);
-      if (AFF) dt -= m1;
-      s_pre[i] = fmaf(dz[i], xh[i], s_pre[i]);
-      if (AFF) s_bpre[i] += dz[i];
-      const float gy = weight(i) * dt;
+    for (int i = 0; i < 4; ++i) {
+      float2 dt = mad2(pair(-m2), xh.p[i], e.p[i]);
+      if (AFF) dt = plus2(dt, pair(-m1));
+      s_pre.p[i] = mad2(dz.p[i], xh.p[i], s_pre.p[i]);
+      if (AFF) s_bpre.p[i] = plus2(s_bpre.p[i], dz.p[i]);
+      float2 gy = mul2(weight(i), dt);
       if (kFixed) {
-        if (kReadsY) s_post[i] = fmaf(yh[i], dt, s_post[i]);
-        if (POST && AFF) s_bpost[i] += dt;
+        if (kReadsY) s_post.p[i] = mad2(yh.p[i], dt, s_post.p[i]);
+        if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], dt);
       } else {
-        const float du = (GATE == kOneGate ? a[0] : a[i]) * dt;
-        const float u = POST ? fmaf(yh[i], w_post[i], AFF ? b_post[i] : 0.f) : yh[i];
+        const float2 du = mul2(gate_at(i), dt);
+        const float2 u = POST ? (AFF ? mad2(yh.p[i], w_post.p[i], b_post.p[i])
+                                     : mul2(yh.p[i], w_post.p[i]))
+                              : yh.p[i];
         if (GATE == kOneGate)
-          one = fmaf(u, in ? dt : 0.f, one);
+          one = mad2(u, in ? dt : pair(0.f), one);
         else
-          dg[i] = slope[i] * u * dt;
-        if (POST) s_post[i] = fmaf(yh[i], du, s_post[i]);
-        if (POST && AFF) s_bpost[i] += du;
+          dg.p[i] = mul2(mul2(slope.p[i], u), dt);
+        if (POST) s_post.p[i] = mad2(yh.p[i], du, s_post.p[i]);
+        if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], du);
       }
-      xh[i] = p.alpha * dt;                                           // dh
-      e[i] = POST ? t.r_y * (fmaf(-c2, yh[i], gy) - (AFF ? c1 : 0.f)) : gy;  // dy
+      if (POST) {
+        gy = mad2(pair(-c2), yh.p[i], mul2(pair(t.r_y), gy));
+        if (AFF) gy = plus2(gy, pair(-c1));
+      }
+      e.p[i] = gy;                         // dy
+      xh.p[i] = mul2(pair(p.alpha), dt);   // dh
     }
     if (in) {
-      store_octet<TY>(row_at<TY>(p.dy.p, row, p.dy.row), oct, e);
-      if (p.dh.p) store_octet<TH>(row_at<TH>(p.dh.p, row, p.dh.row), oct, xh);
-      if (GATE == kFullGate) store_octet<TY>(row_at<TY>(p.dgate.p, row, p.dgate.row), oct, dg);
+      dy.put(to_octet(TY{}, e));
+      if (p.dh.p) dh.put(to_octet(TH{}, xh));
+      if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg));
     }
+    dy.at += p.dy.step;
+    dh.at += p.dh.step;
+    if (GATE == kFullGate) dgate.at += p.dgate.step;
     if (GATE == kOneGate) {
       if (p.gate_kind == FLCE_GATE_TOKEN) {
-        float s[1] = {one};
-        sums.add(s);
-        more.add(s);
+        float d[1] = {one.x + one.y};
+        sums.add(d);
+        more.add(d);
         if (in_cta == 0 && rank == 0)
-          store_element(TY{}, p.dgate.p, row * p.dgate.row, slope[0] * s[0]);
+          store_element(TY{}, p.dgate.p, row * p.dgate.row, one_slope * d[0]);
       } else {
-        s_one = fmaf(slope[0], one, s_one);
+        s_one = fmaf(one_slope, one.x + one.y, s_one);
       }
     }
   }
 
-  auto put = [&](float* part, const float (&s)[8]) {
-    if (part && in) store_octet<float>(part + unit * p.H, oct, s);
+  auto put = [&](float* part, const Oct& o) {
+    if (part && in) store_octet<float>(part + unit * p.H, oct, o);
   };
   put(p.part[0], s_pre);
   if (AFF) put(p.part[1], s_bpre);
   if (kFixed && kReadsY && in) {
-    float a[8], f[8];
-    gate_of_channel(a);
+    Oct a = gate_of_channel();
     if (GATE == kChannelGate) {
       // dgate = slope (w_post sum yh dt + b_post sum dt)
-      param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= s_post[i];
+      Oct f = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f);
+      scale_oct(f, s_post);
       if (POST && AFF) {
-        param_octet<TY>(p.b_post, pfp, oct, 0.f, b_post);
+        b_post = param_octet<TY>(p.b_post, pfp, oct, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = fmaf(b_post[i], s_bpost[i], f[i]);
+        for (int i = 0; i < 4; ++i) f.p[i] = mad2(b_post.p[i], s_bpost.p[i], f.p[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= p.beta * gate_slope(p.act, a[i]);
+      for (int i = 0; i < 4; ++i)
+        f.p[i] = mul2(f.p[i], make_float2(p.beta * gate_slope(p.act, a.p[i].x),
+                                          p.beta * gate_slope(p.act, a.p[i].y)));
       put(p.part[4], f);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s_post[i] *= p.beta * a[i];
-      s_bpost[i] *= p.beta * a[i];
-    }
+    scale_oct(a, p.beta);
+    scale_oct(s_post, a);
+    scale_oct(s_bpost, a);
   }
   if (POST) put(p.part[2], s_post);
   if (POST && AFF) put(p.part[3], s_bpost);
   if (GATE == kOneGate && p.part[4]) {
-    float s[1] = {s_one};
-    sums.add(s);
-    more.add(s);
-    if (in_cta == 0 && rank == 0) p.part[4][unit] = s[0];
+    float d[1] = {s_one};
+    sums.add(d);
+    more.add(d);
+    if (in_cta == 0 && rank == 0) p.part[4][unit] = d[0];
   }
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while another writes to its slots
 }
@@ -317,16 +339,16 @@ template <class TY, class TH, bool POST, bool AFF, int GATE>
 cudaError_t launch_bwd(NormParams p, int64_t parts, cudaStream_t s) {
   static SmemLimit limit;
   const int threads = 32 * p.warps * p.groups;
-  const int stage = threads * 16 * kBwdPieces<TY, TH, POST, GATE>;
-  p.stages = kSmemPerSm / stage < kMaxStages ? kSmemPerSm / stage : kMaxStages;
+  const int ring = threads * 16 * kBwdPieces<TY, TH, POST, GATE> * kBwdStages<TY, TH, POST, GATE>;
   const auto kernel = resnorm_bwd_kernel<TY, TH, POST, AFF, GATE>;
   const cudaError_t e = limit.raise(kernel, kSmemPerSm);
   if (e != cudaSuccess) return e;
+  set_steps(p, parts, Elem<TY>::kBytes, Elem<TH>::kBytes);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(parts / p.groups * p.cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages) * stage;
+  cfg.dynamicSmemBytes = static_cast<size_t>(ring);
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);

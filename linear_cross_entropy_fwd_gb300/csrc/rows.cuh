@@ -22,40 +22,97 @@ struct Elem<float> {
   };
 };
 
-__device__ __forceinline__ void octet_floats(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// An octet in fp32, as four pairs: the arithmetic on it is two elements an instruction.
+struct Oct {
+  float2 p[4];
+};
+
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float2 pair_op(uint64_t d) { return reinterpret_cast<const float2&>(d); }
+__device__ __forceinline__ uint64_t pair_bits(const float2& a) {
+  return reinterpret_cast<const uint64_t&>(a);
 }
-__device__ __forceinline__ void octet_floats(const Elem<float>::Octet& v, float (&f)[8]) {
-  const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_op(d);
+}
+__device__ __forceinline__ float2 plus2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_op(d);
+}
+__device__ __forceinline__ float2 mad2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_op(d);
 }
 
-__device__ __forceinline__ uint4 to_octet(bf16_t, const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ Oct zero_oct() {
+  Oct o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = pair(0.f);
+  return o;
 }
-__device__ __forceinline__ Elem<float>::Octet to_octet(float, const float (&f)[8]) {
+__device__ __forceinline__ Oct same_oct(float x) {
+  Oct o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = pair(x);
+  return o;
+}
+__device__ __forceinline__ void scale_oct(Oct& x, const Oct& f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.p[i] = mul2(x.p[i], f.p[i]);
+}
+__device__ __forceinline__ void scale_oct(Oct& x, float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.p[i] = mul2(x.p[i], pair(f));
+}
+__device__ __forceinline__ float sum_oct(const Oct& x) {
+  const float2 t = plus2(plus2(x.p[0], x.p[1]), plus2(x.p[2], x.p[3]));
+  return t.x + t.y;
+}
+
+__device__ __forceinline__ Oct from_octet(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Oct o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return o;
+}
+__device__ __forceinline__ Oct from_octet(const Elem<float>::Octet& v) {
+  Oct o;
+  o.p[0] = make_float2(__uint_as_float(v.a.x), __uint_as_float(v.a.y));
+  o.p[1] = make_float2(__uint_as_float(v.a.z), __uint_as_float(v.a.w));
+  o.p[2] = make_float2(__uint_as_float(v.b.x), __uint_as_float(v.b.y));
+  o.p[3] = make_float2(__uint_as_float(v.b.z), __uint_as_float(v.b.w));
+  return o;
+}
+
+__device__ __forceinline__ uint4 to_octet(bf16_t, const Oct& f) {
+  return make_uint4(pack_bf16x2(f.p[0].x, f.p[0].y), pack_bf16x2(f.p[1].x, f.p[1].y),
+                    pack_bf16x2(f.p[2].x, f.p[2].y), pack_bf16x2(f.p[3].x, f.p[3].y));
+}
+__device__ __forceinline__ Elem<float>::Octet to_octet(float, const Oct& f) {
   Elem<float>::Octet o;
-  o.a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                   __float_as_uint(f[3]));
-  o.b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                   __float_as_uint(f[7]));
+  o.a = make_uint4(__float_as_uint(f.p[0].x), __float_as_uint(f.p[0].y),
+                   __float_as_uint(f.p[1].x), __float_as_uint(f.p[1].y));
+  o.b = make_uint4(__float_as_uint(f.p[2].x), __float_as_uint(f.p[2].y),
+                   __float_as_uint(f.p[3].x), __float_as_uint(f.p[3].y));
   return o;
 }
 
 // Octet `o` of a row of T at `row`.
 template <class T>
-__device__ __forceinline__ typename Elem<T>::Octet load_octet(const void* row, int o) {
-  return static_cast<const typename Elem<T>::Octet*>(row)[o];
+__device__ __forceinline__ Oct load_octet(const void* row, int o) {
+  return from_octet(static_cast<const typename Elem<T>::Octet*>(row)[o]);
 }
 template <class T>
-__device__ __forceinline__ void store_octet(void* row, int o, const float (&f)[8]) {
+__device__ __forceinline__ void store_octet(void* row, int o, const Oct& f) {
   static_cast<typename Elem<T>::Octet*>(row)[o] = to_octet(T{}, f);
 }
 
@@ -70,16 +127,9 @@ __device__ __forceinline__ void* row_at(void* base, int64_t row, int64_t stride)
 
 // Octet `o` of a parameter vector, fp32 or T; `missing` for each element without a vector.
 template <class T>
-__device__ __forceinline__ void param_octet(const void* p, bool fp32, int o, float missing,
-                                            float (&f)[8]) {
-  if (!p) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = missing;
-  } else if (fp32) {
-    octet_floats(load_octet<float>(p, o), f);
-  } else {
-    octet_floats(load_octet<T>(p, o), f);
-  }
+__device__ __forceinline__ Oct param_octet(const void* p, bool fp32, int o, float missing) {
+  if (!p) return same_oct(missing);
+  return fp32 ? load_octet<float>(p, o) : load_octet<T>(p, o);
 }
 
 // One element of type T, or fp32.
@@ -113,22 +163,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// Until at most `n` (0 .. 5) of this thread's groups are in flight.
-__device__ __forceinline__ void copies_wait(int n) {
-  if (n == 0)
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (n == 2)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (n == 3)
-    asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (n == 4)
-    asm volatile("cp.async.wait_group 4;" ::: "memory");
-  else
-    asm volatile("cp.async.wait_group 5;" ::: "memory");
+// Until at most N of this thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr int kMaxStages = 6;
+// Stages of a ring whose threads keep `pieces` pieces in each.
+constexpr int ring_stages(int pieces, int threads, int bytes, int most) {
+  return bytes / (pieces * threads * 16) < most ? bytes / (pieces * threads * 16) : most;
+}
 
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   uint4 v;
@@ -139,22 +182,34 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   return v;
 }
 
-// Octet `o` of a row of T to shared memory, its 16-byte pieces `step` apart; and back.
+// One octet of T at `src` to shared memory, its 16-byte pieces `step` apart; and back.
 template <class T>
-__device__ __forceinline__ void copy_octet(uint32_t dst, uint32_t step, const void* row, int o) {
-  const uint8_t* src = static_cast<const uint8_t*>(row) + o * (8 * Elem<T>::kBytes);
+__device__ __forceinline__ void copy_octet(uint32_t dst, uint32_t step, const uint8_t* src) {
   copy16(dst, src);
   if (Elem<T>::kBytes == 4) copy16(dst + step, src + 16);
 }
-__device__ __forceinline__ void shared_octet(bf16_t, uint32_t a, uint32_t, float (&f)[8]) {
-  octet_floats(ld_shared16(a), f);
+__device__ __forceinline__ Oct shared_octet(bf16_t, uint32_t a, uint32_t) {
+  return from_octet(ld_shared16(a));
 }
-__device__ __forceinline__ void shared_octet(float, uint32_t a, uint32_t step, float (&f)[8]) {
+__device__ __forceinline__ Oct shared_octet(float, uint32_t a, uint32_t step) {
   Elem<float>::Octet o;
   o.a = ld_shared16(a);
   o.b = ld_shared16(a + step);
-  octet_floats(o, f);
+  return from_octet(o);
 }
+
+// A thread's octet of one row after the other.  The step to the next one is a launch
+// parameter, so that it takes no registers.
+template <class T>
+struct Walk {
+  uint8_t* at;
+  __device__ __forceinline__ Walk(const void* base, int64_t row_stride, int64_t row, int octet)
+      : at(static_cast<uint8_t*>(const_cast<void*>(base)) +
+           (row * row_stride + 8 * octet) * Elem<T>::kBytes) {}
+  __device__ __forceinline__ void put(const typename Elem<T>::Octet& o) const {
+    *reinterpret_cast<typename Elem<T>::Octet*>(at) = o;
+  }
+};
 template <class T>
 constexpr int kPieces = Elem<T>::kBytes / 2;  // 16-byte pieces of an octet
 
@@ -207,6 +262,16 @@ struct RowSums {
       const int k = lane / kLanes;
       if (lane % kLanes == 0) s[k][warp] = t;
       named_barrier(1 + id, warps * 32);
+      if (K == 1) {  // fewer steps one after the other than exchanges would take
+        const float4 q = *reinterpret_cast<const float4*>(&s[0][0]);
+        t = (q.x + q.y) + (q.z + q.w);
+        for (int w = 4; w < warps; w += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(&s[0][w]);
+          t += (r.x + r.y) + (r.z + r.w);
+        }
+        v[0] = t;
+        return;
+      }
       if (K == 8) {
         const float4 q = *reinterpret_cast<const float4*>(&s[k][4 * (lane & 3)]);
         t = (q.x + q.y) + (q.z + q.w);
@@ -216,9 +281,8 @@ struct RowSums {
       } else {
         t = s[k][lane & 15];
       }
-      constexpr int kHold = K == 1 ? 16 : kLanes;  // lanes that share a sum's parts
 #pragma unroll
-      for (int d = kHold / 2; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+      for (int d = kLanes / 2; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
     }
     if (K == 1) {
       v[0] = t;
