@@ -14,42 +14,80 @@ struct CkptParams {
   Ckpt c;
   void* x;
   int64_t x_row, total;  // total: octets of all rows, the checkpoint's padding included
-  int32_t octets;        // of a row of x
-  int32_t padded;        // of a row of codes (save) or of x (load)
+  uint32_t octets;       // of a row of x
+  uint32_t padded;       // of a row of codes (save) or of x (load)
+};
+
+// A thread's octets, kThreads apart: row and octet of each.  One 64-bit division for a CTA,
+// one of 32 bits for a thread, and for rows longer than a step none after it.
+struct Place {
+  int64_t row;
+  uint32_t o;
+  __device__ __forceinline__ Place(int64_t cta, uint32_t padded) {
+    row = cta / padded;
+    o = static_cast<uint32_t>(cta - row * padded) + threadIdx.x;
+    wrap(padded);
+  }
+  __device__ __forceinline__ void wrap(uint32_t padded) {
+    const uint32_t q = o / padded;
+    row += q;
+    o -= q * padded;
+  }
+  __device__ __forceinline__ void next(uint32_t padded) {
+    o += kThreads;
+    if (padded < kThreads) {
+      wrap(padded);
+    } else if (o >= padded) {
+      o -= padded;
+      ++row;
+    }
+  }
 };
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p) {
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets) + threadIdx.x;
-  Oct v[kOctets];
-  int64_t row[kOctets];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets);
+  Place at(first, p.padded);
+  typename Elem<T>::Octet v[kOctets];
+  uint8_t* scales[kOctets];
   int o[kOctets];
 #pragma unroll
   for (int k = 0; k < kOctets; ++k) {
-    const int64_t i = base + k * kThreads;
-    row[k] = i / p.padded;
-    o[k] = static_cast<int>(i - row[k] * p.padded);
-    v[k] = zero_oct();
-    if (i >= p.total)
-      o[k] = p.padded;  // stores nothing
-    else if (o[k] < p.octets)
-      v[k] = load_octet<T>(row_at<T>(p.x, row[k], p.x_row), o[k]);
+    const bool there = first + threadIdx.x + k * kThreads < p.total;
+    o[k] = there ? at.o : p.padded;  // `padded` stores nothing
+    scales[k] = p.c.scales + at.row * p.c.spitch;
+    v[k] = {};
+    if (there && at.o < p.octets)
+      v[k] = *(static_cast<const typename Elem<T>::Octet*>(row_at<T>(p.x, at.row, p.x_row)) + at.o);
+    at.next(p.padded);
   }
+  // the codes of all rows follow one another
+  uint8_t* codes = p.c.codes + (first + threadIdx.x) * 8;
 #pragma unroll
-  for (int k = 0; k < kOctets; ++k) ckpt_store_octet(p.c, row[k], o[k], v[k]);
+  for (int k = 0; k < kOctets; ++k)
+    ckpt_store_octet(p.c, codes + k * kThreads * 8, scales[k], o[k], v[k]);
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p) {
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets) + threadIdx.x;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets);
+  Place at(first, p.padded);
+  uint2 codes[kOctets];
+  uint32_t scale[kOctets];
+  typename Elem<T>::Octet* to[kOctets];
 #pragma unroll
   for (int k = 0; k < kOctets; ++k) {
-    const int64_t i = base + k * kThreads;
-    if (i >= p.total) break;
-    const int64_t row = i / p.padded;
-    const int o = static_cast<int>(i - row * p.padded);
-    store_octet<T>(row_at<T>(p.x, row, p.x_row), o, ckpt_load_octet(p.c, row, o));
+    to[k] = nullptr;
+    if (first + threadIdx.x + k * kThreads < p.total) {
+      to[k] = static_cast<typename Elem<T>::Octet*>(row_at<T>(p.x, at.row, p.x_row)) + at.o;
+      codes[k] = *reinterpret_cast<const uint2*>(p.c.codes + at.row * p.c.pitch + at.o * 8);
+      scale[k] = p.c.scales[at.row * p.c.spitch + (at.o >> 2)];
+    }
+    at.next(p.padded);
   }
+#pragma unroll
+  for (int k = 0; k < kOctets; ++k)
+    if (to[k]) *to[k] = to_octet(T{}, ckpt_octet(codes[k], scale[k]));
 }
 
 CkptParams params(const Ckpt& c, void* x, int64_t x_row, int64_t N, int64_t H, bool save) {
@@ -57,8 +95,8 @@ CkptParams params(const Ckpt& c, void* x, int64_t x_row, int64_t N, int64_t H, b
   p.c = c;
   p.x = x;
   p.x_row = N > 1 ? x_row : H;
-  p.octets = static_cast<int32_t>(H / 8);
-  p.padded = save ? p.c.pitch / 8 : p.octets;
+  p.octets = static_cast<uint32_t>(H / 8);
+  p.padded = save ? static_cast<uint32_t>(p.c.pitch) / 8 : p.octets;
   p.total = N * p.padded;
   return p;
 }

@@ -49,27 +49,41 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
   return f;
 }
 
-// Stores octet `o` of a row: x holds its values (zeros behind the row's end, where `o` may
-// lie too).  Executed by whole warps whose lanes hold consecutive octets, lane 0 a multiple
-// of 4, so that four lanes hold a group.
-__device__ __forceinline__ void ckpt_store_octet(const Ckpt& c, int64_t row, int o,
-                                                 const Oct& x) {
-  uint32_t top = 0;
+// The bits of the largest magnitude of an octet, as fp32; NaN above infinity's.
+__device__ __forceinline__ uint32_t octet_top(const uint4& v) {
+  uint32_t m = v.x & 0x7fff7fffu;
+  const uint32_t w[3] = {v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    top = max(top, __float_as_uint(x.p[i].x) & 0x7fffffffu);
-    top = max(top, __float_as_uint(x.p[i].y) & 0x7fffffffu);
-  }
+  for (int i = 0; i < 3; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+  return max(m << 16, m & 0x7fff0000u);
+}
+__device__ __forceinline__ uint32_t octet_top(const Elem<float>::Octet& v) {
+  const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+  return m;
+}
+
+// Stores octet `o` of a row whose octet goes to `codes` and whose scales begin at `scales`:
+// v holds its values (zeros behind the row's end, where `o` may lie too).  Executed by whole
+// warps whose lanes hold consecutive octets, lane 0 a multiple of 4, so that four lanes hold
+// a group.
+template <class OctetT>
+__device__ __forceinline__ void ckpt_store_octet(const Ckpt& c, uint8_t* codes, uint8_t* scales,
+                                                 int o, const OctetT& v) {
+  uint32_t top = octet_top(v);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   // ceil(log2(top / 448)) + 127: 448 = 1.75 * 2^8, and a mantissa above .75 carries
   int s = static_cast<int>((top + 0x1fffffu) >> 23) - 8;
   s = min(max(s, 127 - 117), 127 + 119);
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - s) << 23);  // 2^-e
+  const float2 inv = pair(__uint_as_float(static_cast<uint32_t>(254 - s) << 23));  // 2^-e
+  const Oct x = from_octet(v);
   uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 t = mul2(x.p[i], pair(inv));
+    const float2 t = mul2(x.p[i], inv);
     q[i] = e4m3x2(t.x, t.y);
   }
   uint2 w = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
@@ -77,13 +91,13 @@ __device__ __forceinline__ void ckpt_store_octet(const Ckpt& c, int64_t row, int
     s = 255;
     w = make_uint2(0, 0);
   }
-  if (o * 8 < c.pitch) *reinterpret_cast<uint2*>(c.codes + row * c.pitch + o * 8) = w;
-  if ((o & 3) == 0 && o * 8 < c.pitch) {
-    uint8_t* to = c.scales + row * c.spitch;
+  if (o * 8 >= c.pitch) return;
+  *reinterpret_cast<uint2*>(codes) = w;
+  if ((o & 3) == 0) {
     int g = o >> 2;
-    to[g] = static_cast<uint8_t>(s);
+    scales[g] = static_cast<uint8_t>(s);
     if (o * 8 + 32 == c.pitch)
-      while (++g < c.spitch) to[g] = 0;
+      while (++g < c.spitch) scales[g] = 0;
   }
 }
 
@@ -92,14 +106,13 @@ __device__ __forceinline__ float ckpt_scale(uint32_t byte) {
   return __uint_as_float(byte == 255 ? 0x7fffffffu : byte << 23);
 }
 
-// Octet `o` of a row.
-__device__ __forceinline__ Oct ckpt_load_octet(const Ckpt& c, int64_t row, int o) {
-  const uint2 w = *reinterpret_cast<const uint2*>(c.codes + row * c.pitch + o * 8);
-  const float f = ckpt_scale(c.scales[row * c.spitch + (o >> 2)]);
+// The octet of these codes and this scale byte.
+__device__ __forceinline__ Oct ckpt_octet(const uint2& codes, uint32_t scale) {
+  const float f = ckpt_scale(scale);
   Oct x;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    x.p[i] = mul2(from_e4m3x2((i < 2 ? w.x : w.y) >> (16 * (i & 1))), pair(f));
+    x.p[i] = mul2(from_e4m3x2((i < 2 ? codes.x : codes.y) >> (16 * (i & 1))), pair(f));
   return x;
 }
 

@@ -276,7 +276,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const auto o = to_octet(TY{}, v);
           if (in[j])
             reinterpret_cast<typename Elem<TY>::Octet*>(z.at + q * p.z.step)[j * jump] = o;
-          if (p.ckpt.codes) ckpt_store_octet(p.ckpt, row + q * rows, oct[j], from_octet(o));
+          if (p.ckpt.codes) {
+            const int64_t at_row = row + q * rows;
+            ckpt_store_octet(p.ckpt, p.ckpt.codes + at_row * p.ckpt.pitch + oct[j] * 8,
+                             p.ckpt.scales + at_row * p.ckpt.spitch, oct[j], o);
+          }
         }
     }
     h_out.at += R * p.h_out.step;
