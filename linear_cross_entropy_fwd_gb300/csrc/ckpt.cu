@@ -13,9 +13,11 @@ constexpr int kThreads = 256, kOctets = 4;  // octets of a thread, loaded togeth
 struct CkptParams {
   Ckpt c;
   void* x;
-  int64_t x_row, total;  // total: octets of all rows, the checkpoint's padding included
-  uint32_t octets;       // of a row of x
-  uint32_t padded;       // of a row of codes (save) or of x (load)
+  int64_t x_row;
+  uint32_t octets;  // of a row of x
+  uint32_t padded;  // of a row of codes, its padding included (save), or of x (load)
+  int64_t total;    // of all rows, `padded` each
+  int32_t* clear;
 };
 
 // A thread's octets, kThreads apart: row and octet of each.  One 64-bit division for a CTA,
@@ -68,8 +70,11 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
     ckpt_store_octet(p.c, codes + k * kThreads * 8, scales[k], o[k], v[k]);
 }
 
+// `clear`, optional, becomes 0.
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p) {
+  grid_launch_dependents();
+  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets);
   Place at(first, p.padded);
   uint2 codes[kOctets];
@@ -150,7 +155,8 @@ int save_or_load(const char* fn, void* x, int64_t x_row, int64_t N, int64_t H, v
         ckpt_save_kernel<float><<<grid_of(p), kThreads, 0, call.stream>>>(p);
       e = cudaGetLastError();
     } else {
-      e = launch_ckpt_load(c, x, x_row, N, H, o.dtype == FLCE_FP32 ? 4 : 2, call.stream);
+      e = launch_ckpt_load(c, x, x_row, N, H, o.dtype == FLCE_FP32 ? 4 : 2, nullptr,
+                           call.stream);
     }
     if (e != cudaSuccess) rc = host_cuda_error(e, fn);
   }
@@ -160,8 +166,9 @@ int save_or_load(const char* fn, void* x, int64_t x_row, int64_t N, int64_t H, v
 }  // namespace
 
 cudaError_t launch_ckpt_load(const Ckpt& c, void* x, int64_t x_row, int64_t N, int64_t H, int elt,
-                             cudaStream_t s) {
-  const CkptParams p = params(c, x, x_row, N, H, false);
+                             int32_t* clear, cudaStream_t s) {
+  CkptParams p = params(c, x, x_row, N, H, false);
+  p.clear = clear;
   if (elt == 2)
     ckpt_load_kernel<bf16_t><<<grid_of(p), kThreads, 0, s>>>(p);
   else

@@ -1,11 +1,368 @@
 // ckpt_wgrad.cu -- a projection's weight gradient from its input's 8-bit checkpoint:
 // dW [O, I] (+)= dY^T X, dY [N, O] bf16, X [N, I] as ckpt.cuh stores it.
+//
+// X is read back into bf16 scratch, exactly, and multiplied on CTA pairs (tcgen05,
+// cta_group::2, 256 x 256 tiles, both operands MN-major), as the head's dW is.  What differs:
+//
+// Sums.  The tensor core cuts off what falls behind an accumulator's last bit instead of
+// rounding it, always towards zero, once for every 16 tokens: 1e-5 of the result after 16384
+// of them.  So an accumulator in TMEM takes kPiece k-blocks at most, and the pieces are added
+// in registers, rounded, in ascending order: eight warps hold a CTA's half of a tile, 128
+// sums a thread, and the tensor core goes on with the other accumulator meanwhile.  (Adding
+// the pieces to dW at L2 took a quarter of the time of the products.)
+//
+// The last tiles.  Tiles that do not fill a round of all pairs are shared out over all pairs
+// along the tokens, evenly; each pair's share of a tile goes to scratch and a second kernel
+// adds a tile's shares in order (8192 x 6144 x 4096: 4 of 384 tiles are left, which would be
+// a sixth round).  Where that gains less than it costs the last round stays as it is.
 #include "ckpt.cuh"
+#include "epilogues.cuh"
 #include "host_util.h"
-#include "launch.h"
+#include "sm103_attn.cuh"
 
 namespace flce {
 namespace {
+
+constexpr int kStages = 6;                    // of 32 KB in each CTA of a pair
+constexpr int kTileM = 2 * BM;                // a pair's tile; BN wide
+constexpr int kPiece = 32;                    // k-blocks of 64 tokens in an accumulator
+constexpr uint32_t kOperandBytes = BM * 128;  // of A, and of B, in a stage of one CTA
+constexpr int kSumWarps = 8;                  // 32 rows of a tile by kSumCols columns each
+constexpr int kSumCols = 4 * BN / kSumWarps;
+constexpr int kWgradThreads = 64 + 32 * kSumWarps;
+constexpr uint32_t kStaging = kSumWarps * STAGING_BUF_BYTES;
+constexpr size_t kWgradSmem = 1024 + kStages * 2 * kOperandBytes + kStaging + SMEM_BARRIER_BYTES;
+
+// How the tiles are dealt out (GemmGrid for the order of the tiles and k-blocks).
+struct WgradPlan {
+  GemmGrid g;
+  int32_t units;       // pairs
+  int32_t whole;       // tiles that one pair does from end to end; the rest is shared out
+  int32_t accumulate;
+  int64_t O, I;
+  float* dW;           // of the join
+  float* shares;       // [2 units][kTileM][BN]
+};
+
+// A pair's next work: k-blocks k0 .. k1 of a tile, into dW or into its share `slot`.
+struct Item {
+  int32_t tile, k0, k1, slot;  // slot < 0: dW
+};
+
+// First k-block (of those of all shared tiles, one after the other) of unit u's share.
+__host__ __device__ inline int64_t share_start(const WgradPlan& p, int u) {
+  const int64_t all = static_cast<int64_t>(p.g.num_m_blk * p.g.num_n_blk - p.whole) * p.g.num_k_blk;
+  return all * u / p.units;
+}
+
+struct Items {
+  const WgradPlan& p;
+  int unit, tile, segment = 0;
+  int64_t at, end;
+  __device__ Items(const WgradPlan& plan, int u)
+      : p(plan), unit(u), tile(u), at(share_start(plan, u)), end(share_start(plan, u + 1)) {}
+  __device__ bool next(Item& it) {
+    if (tile < p.whole) {
+      it = Item{tile, 0, p.g.num_k_blk, -1};
+      tile += p.units;
+      return true;
+    }
+    if (at >= end) return false;
+    const int64_t t = at / p.g.num_k_blk;
+    it.tile = p.whole + static_cast<int32_t>(t);
+    it.k0 = static_cast<int32_t>(at - t * p.g.num_k_blk);
+    const int64_t left = end - at;
+    it.k1 = it.k0 + left < p.g.num_k_blk ? it.k0 + static_cast<int32_t>(left) : p.g.num_k_blk;
+    at += it.k1 - it.k0;
+    it.slot = it.k0 == 0 && it.k1 == p.g.num_k_blk ? -1 : 2 * unit + segment;
+    ++segment;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int piece_count(const Item& it) {
+  return (it.k1 - it.k0 + kPiece - 1) / kPiece;
+}
+__device__ __forceinline__ int piece_length(const Item& it, int n) {
+  return (it.k1 - it.k0 + n - 1) / n;
+}
+
+__global__ void __launch_bounds__(kWgradThreads, 1)
+    ckpt_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmOut,
+                      const __grid_constant__ CUtensorMap tmShares,
+                      const __grid_constant__ WgradPlan p) {
+  constexpr uint32_t kBox = 128u * 64;  // 64 elements of MN by 64 tokens
+  constexpr uint32_t kAdvance = 16u * 128u;
+  constexpr uint32_t kIdesc = make_idesc(1, true, true, kTileM, BN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* smA = smem;
+  uint8_t* smB = smem + kStages * kOperandBytes;
+  uint8_t* staging = smB + kStages * kOperandBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
+  uint64_t* full = bars;                    // [kStages]  (the even CTA's are used)
+  uint64_t* empty = bars + kStages;         // [kStages]
+  uint64_t* acc_full = bars + 2 * kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;       // [2]  (the even CTA's are used)
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = static_cast<int>(blockIdx.x >> 1);
+  int* const status = p.g.status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kSumWarps * 2);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmOut);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_base_slot, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before any remote signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_base_slot;
+  // The previous launch writes X and starts only when all before it is done: nothing but the
+  // loads of X waits for it.
+  grid_launch_dependents();
+
+  Items items(p, unit);
+  Item it;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t s = 0, round = 0, loads = 0;
+    const uint32_t a_base = smem_addr(smA), b_base = smem_addr(smB);
+    const uint32_t full_even = mapa_shared(smem_addr(&full[0]), 0);
+    bool ok = true, first = true;
+    uint32_t early = 0;  // stages whose dY is on its way before X is there
+    while (ok && items.next(it)) {
+      int mu, n_blk;
+      tile_coords(p.g, it.tile, mu, n_blk);
+      const int a_mn = uniform(mu * kTileM + static_cast<int>(rank) * BM);
+      const int b_mn = uniform(n_blk * BN + static_cast<int>(rank) * BM);
+      auto load_a = [&](uint32_t stage, int kb) {
+        if (rank == 0) expect_tx_elected(&full[stage], 4 * kOperandBytes);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          tma_load_2d_pair_elected(&tmA, full_even + 8 * stage,
+                                   a_base + stage * kOperandBytes + j * kBox, a_mn + 64 * j,
+                                   kb * 64);
+      };
+      if (first) {
+        first = false;
+        for (; early < kStages && it.k0 + static_cast<int>(early) < it.k1; ++early)
+          load_a(early, it.k0 + early);
+        grid_dependency_wait();
+      }
+      for (int kb = it.k0; kb < it.k1; ++kb, ++loads) {
+        if (loads >= early) {
+          if (!uniform_wait(&empty[s], (round & 1) ^ 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          load_a(s, kb);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          tma_load_2d_pair_elected(&tmB, full_even + 8 * s, b_base + s * kOperandBytes + j * kBox,
+                                   b_mn + 64 * j, kb * 64);
+        if (++s == kStages) {
+          s = 0;
+          ++round;
+        }
+      }
+    }
+    // Every load has landed before this CTA leaves: the even CTA's on its barriers, the
+    // odd one's when the MMAs have released them.
+    if (lane == 0) {
+      const uint32_t n = loads < kStages ? loads : kStages;
+      for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t q = loads - 1 - i;
+        mbar_wait_drain(rank == 0 ? &full[q % kStages] : &empty[q % kStages], (q / kStages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    if (rank == 0) {
+      uint32_t s = 0, round = 0, acc = 0;
+      bool ok = true;
+      const Operand16 a0(smem_addr(smA), kBox), b0(smem_addr(smB), kBox);
+      while (ok && items.next(it)) {
+        const int pieces = piece_count(it), length = piece_length(it, pieces);
+        for (int k0 = it.k0; ok && k0 < it.k1; k0 += length, ++acc) {
+          const uint32_t buf = acc & 1;
+          if (!uniform_wait(&acc_empty[buf], ((acc >> 1) & 1) ^ 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + buf * BN;
+          const int k1 = k0 + length < it.k1 ? k0 + length : it.k1;
+          uint32_t add = 0;
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!uniform_wait(&full[s], round & 1, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const Operand16 a = moved(a0, s * kOperandBytes), b = moved(b0, s * kOperandBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              mma_f16_pair_at(d_tmem, a, k * kAdvance, b, k * kAdvance, kIdesc, add);
+              add = 1;
+            }
+            commit_pair_elected(&empty[s], 0x3);
+            if (++s == kStages) {
+              s = 0;
+              ++round;
+            }
+          }
+          if (ok) commit_pair_elected(&acc_full[buf], 0x3);
+        }
+      }
+      commit_pair_elected(drain, 0x1);
+      if (lane == 0) mbar_wait_drain(drain, 0);
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- sums
+    const int q = warp & 3;                        // TMEM lanes 32 q .. 32 q + 31
+    const int col = ((warp - 2) >> 2) * kSumCols;  // and kSumCols columns from here
+    uint8_t* buffer = staging + (warp - 2) * STAGING_BUF_BYTES;
+    const uint32_t free_bar = mapa_shared(smem_addr(&acc_empty[0]), 0);
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + col;
+    uint32_t acc = 0;
+    bool ok = true;
+    while (ok && items.next(it)) {
+      float2 sum[kSumCols / 2];
+#pragma unroll
+      for (int c = 0; c < kSumCols / 2; ++c) sum[c] = pair(0.f);
+      const int length = piece_length(it, piece_count(it));
+      for (int k0 = it.k0; k0 < it.k1; k0 += length, ++acc) {
+        const uint32_t buf = acc & 1;
+        if (!mbar_wait(&acc_full[buf], (acc >> 1) & 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int u = 0; u < kSumCols / 16; ++u) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(lanes + buf * BN + 16 * u, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            sum[8 * u + c] = plus2(sum[8 * u + c], make_float2(__uint_as_float(r[2 * c]),
+                                                               __uint_as_float(r[2 * c + 1])));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
+      }
+      if (!ok) break;
+      int mu, n_blk;
+      tile_coords(p.g, it.tile, mu, n_blk);
+      const bool share = it.slot >= 0;
+      const int x = (share ? 0 : n_blk * BN) + col;
+      const int y = (share ? it.slot : mu) * kTileM + static_cast<int>(rank) * BM + 32 * q;
+#pragma unroll
+      for (int u = 0; u < kSumCols / 32; ++u) {
+        if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const float2 v = sum[16 * u + 2 * ch], w = sum[16 * u + 2 * ch + 1];
+          staging_put16(buffer, lane, ch, __float_as_uint(v.x), __float_as_uint(v.y),
+                        __float_as_uint(w.x), __float_as_uint(w.y));
+        }
+        if (!share && p.accumulate)
+          staging_release<true>(&tmOut, buffer, lane, x + 32 * u, y);
+        else
+          staging_release<false>(share ? &tmShares : &tmOut, buffer, lane, x + 32 * u, y);
+      }
+    }
+    if (lane == 0) bulk_wait<0>();  // stores done before shared memory goes away
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the pair still uses it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// dW of the shared tiles: each the sum of its shares, in ascending order of their tokens.
+constexpr int kJoinThreads = 256, kJoinRows = 4, kJoinAtOnce = 8;
+
+__global__ void __launch_bounds__(kJoinThreads)
+    ckpt_wgrad_join_kernel(const __grid_constant__ WgradPlan p) {
+  // of the shared tiles' k-blocks, this tile's; u: the first unit with some of them
+  const int64_t t = blockIdx.x, k0 = t * p.g.num_k_blk, k1 = k0 + p.g.num_k_blk;
+  int u = static_cast<int>(t * p.units / (p.g.num_m_blk * p.g.num_n_blk - p.whole));
+  while (u > 0 && share_start(p, u) > k0) --u;
+  while (share_start(p, u + 1) <= k0) ++u;
+  int end = u + 1;
+  while (share_start(p, end) < k1) ++end;
+  const bool behind = share_start(p, u) < k0;  // unit u ends another tile first
+  grid_dependency_wait();
+  if (end == u + 1 && !behind && share_start(p, end) >= k1) return;  // it did the whole tile
+  int mu, n_blk;
+  tile_coords(p.g, p.whole + static_cast<int>(t), mu, n_blk);
+  const int col = (threadIdx.x & 63) * 4, row = blockIdx.y * kJoinRows + (threadIdx.x >> 6);
+  const int64_t at = mu * static_cast<int64_t>(kTileM) + row;
+  if (n_blk * BN + col >= p.I || at >= p.O) return;
+  float4* to = reinterpret_cast<float4*>(p.dW + at * p.I + n_blk * BN + col);
+  const float4* from = reinterpret_cast<const float4*>(p.shares + row * BN + col);
+  constexpr int64_t kSlot = kTileM * BN / 4;
+  float4 s = from[(2 * u + (behind ? 1 : 0)) * kSlot];
+  for (int w = u + 1; w < end; w += kJoinAtOnce) {
+    float4 a[kJoinAtOnce];
+#pragma unroll
+    for (int i = 0; i < kJoinAtOnce; ++i)
+      a[i] = w + i < end ? from[2 * (w + i) * kSlot] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinAtOnce; ++i) {
+      s.x += a[i].x;
+      s.y += a[i].y;
+      s.z += a[i].z;
+      s.w += a[i].w;
+    }
+  }
+  if (p.accumulate) {
+    const float4 v = *to;
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  *to = s;
+}
 
 int check(const void* dY, int64_t dY_row, const void* ckpt, int64_t N, int64_t O, int64_t I,
           const float* dW, int32_t dtype) {
@@ -33,12 +390,64 @@ int check(const void* dY, int64_t dY_row, const void* ckpt, int64_t N, int64_t O
   return FLCE_OK;
 }
 
+// Boxes of `box` rows by `box` columns of a matrix.
 int map_of(CUtensorMap* m, const void* p, CUtensorMapDataType t, int64_t cols, int64_t rows,
-           int64_t pitch, uint32_t box_cols, uint32_t box_rows, const char* what) {
+           int64_t pitch, uint32_t box, const char* what) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
   const uint64_t pitches[1] = {static_cast<uint64_t>(pitch)};
-  const uint32_t box[2] = {box_cols, box_rows};
-  return host_tensor_map(m, p, t, 2, dims, pitches, box, what);
+  const uint32_t boxes[2] = {box, box};
+  return host_tensor_map(m, p, t, 2, dims, pitches, boxes, what);
+}
+
+// Whether the last tiles are shared out (they never make more shares than k-blocks): what idle pairs would lose (0.29 us for a k-block),
+// against writing and reading the shares (a launch of 4 us, and 3 bytes a picosecond).
+WgradPlan plan(int64_t N, int64_t O, int64_t I, int units, bool accumulate) {
+  WgradPlan p{};
+  p.g.num_m_blk = static_cast<int32_t>((O + kTileM - 1) / kTileM);
+  p.g.num_n_blk = static_cast<int32_t>((I + BN - 1) / BN);
+  p.g.num_k_blk = static_cast<int32_t>((N + 63) / 64);
+  p.g.raster_n = 1;
+  p.g.n_band = 8;  // pairs that run together take about 8 x 9 tiles
+  p.accumulate = accumulate;
+  p.units = units;
+  const int tiles = p.g.num_m_blk * p.g.num_n_blk, left = tiles % units;
+  const double gain = 0.29 * p.g.num_k_blk * (1.0 - static_cast<double>(left) / units);
+  const double cost = 4.0 + 2.0 * (units + left) * kTileM * BN * 4 / 3e6;
+  const bool enough = static_cast<int64_t>(left) * p.g.num_k_blk >= units;
+  p.whole = left && enough && gain > cost ? tiles - left : tiles;
+  if (p.whole == tiles && tiles < units) p.units = tiles;
+  return p;
+}
+
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int units, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * units));
+  cfg.blockDim = dim3(kWgradThreads);
+  cfg.dynamicSmemBytes = kWgradSmem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+cudaError_t launch_join(const WgradPlan& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(p.g.num_m_blk * p.g.num_n_blk - p.whole),
+                     kTileM / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ckpt_wgrad_join_kernel, p);
 }
 
 }  // namespace
@@ -55,8 +464,13 @@ extern "C" int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt,
   if (rc) return rc;
   int sms = 0;
   if ((rc = host_device(&sms))) return rc;
+  const WgradPlan all = plan(N, O, I, sms / 2, accumulate != 0);
+  const bool shared = N > 0 && all.whole < all.g.num_m_blk * all.g.num_n_blk;
+  const size_t x_bytes = round256(static_cast<size_t>(N) * static_cast<size_t>(I) * 2);
+  const int64_t share_rows = shared ? 2 * static_cast<int64_t>(all.units) * kTileM : 0;
   StepCall call;
-  if ((rc = call.begin(o, N > 0 ? round256(static_cast<size_t>(N) * I * 2) : 0, StepCall::kCleared)))
+  if ((rc = call.begin(o, x_bytes + static_cast<size_t>(share_rows) * BN * 4,
+                       N > 0 ? StepCall::kKernelClears : StepCall::kCleared)))
     return rc;
   if (N == 0) {
     if (!accumulate) {
@@ -66,31 +480,33 @@ extern "C" int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt,
     }
     return call.end(rc);
   }
-  CUtensorMap ma, mb, mw;
-  int units = 0;
-  cudaError_t e = gemm_prepare_bf16(sms, &units);
-  if (e != cudaSuccess) return call.end(host_cuda_error(e, "gemm_prepare"));
-  if ((rc = map_of(&ma, dY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, O, N, (N > 1 ? dY_row : O) * 2, 64,
-                   64, "dY")) ||
-      (rc = map_of(&mb, call.scratch, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, I, N, I * 2, 64, 64,
-                   "X")) ||
-      (rc = map_of(&mw, dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, I, O, I * 4, 32, 32, "dW")))
+  WgradPlan p = all;
+  p.g.status = call.status;
+  p.O = O;
+  p.I = I;
+  p.dW = dW;
+  p.shares = reinterpret_cast<float*>(call.scratch + x_bytes);
+  CUtensorMap ma, mb, mw, ms;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto fp32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  if ((rc = map_of(&ma, dY, bf16, O, N, (N > 1 ? dY_row : O) * 2, 64, "dY")) ||
+      (rc = map_of(&mb, call.scratch, bf16, I, N, I * 2, 64, "X")) ||
+      (rc = map_of(&mw, dW, fp32, I, O, I * 4, 32, "dW")))
     return call.end(rc);
-  e = launch_ckpt_load(ckpt_view(const_cast<void*>(ckpt), N, I), call.scratch, I, N, I, 2,
-                       call.stream);
+  ms = mw;
+  if (shared && (rc = map_of(&ms, p.shares, fp32, BN, share_rows, BN * 4, 32, "shares")))
+    return call.end(rc);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(ckpt_wgrad_kernel, kWgradSmem);
+  if (e == cudaSuccess)
+    e = launch_ckpt_load(ckpt_view(const_cast<void*>(ckpt), N, I), call.scratch, I, N, I, 2,
+                         call.status, call.stream);
   if (e == cudaSuccess) {
-    GemmGrid g{};
-    g.num_m_blk = static_cast<int32_t>((O + 2 * BM - 1) / (2 * BM));
-    g.num_n_blk = static_cast<int32_t>((I + BN - 1) / BN);
-    g.num_k_blk = static_cast<int32_t>((N + 63) / 64);
-    g.raster_n = 1;
-    g.wait_operands = 1;
-    g.status = call.status;
-    const int64_t tiles = static_cast<int64_t>(g.num_m_blk) * g.num_n_blk;
-    const StoreParams sp{0, 0, accumulate ? 1 : 0};
-    e = launch_dw_bf16(ma, mb, mw, g, sp, static_cast<int>(tiles < units ? tiles : units),
-                       call.stream);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = pair_config(attr, p.units, call.stream);
+    e = cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel, ma, mb, mw, ms, p);
   }
+  if (e == cudaSuccess && shared) e = launch_join(p, call.stream);
   if (e != cudaSuccess) rc = host_cuda_error(e, "ckpt_wgrad");
   return call.end(rc);
 }

@@ -1,5 +1,5 @@
-// sm103_attn.cuh -- further inline-PTX wrappers, used by the attention and
-// orthogonalisation kernels: 3-D TMA loads, MMAs whose A operand lies in
+// sm103_attn.cuh -- further inline-PTX wrappers, used by the attention, orthogonalisation
+// and checkpoint kernels: 3-D TMA loads, MMAs whose A operand lies in
 // TMEM, stores to TMEM, and pairs of fp32 operations.
 #pragma once
 #include "sm103.cuh"
@@ -142,6 +142,19 @@ __device__ __forceinline__ void expect_tx_elected(uint64_t* bar, uint32_t bytes)
       "@e mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(
           smem_addr(bar)),
       "r"(bytes)
+      : "memory");
+}
+
+// 2D tiled load within a CTA pair (see tma_load_2d_pair).
+__device__ __forceinline__ void tma_load_2d_pair_elected(const CUtensorMap* map,
+                                                         uint32_t bar_cluster, uint32_t dst,
+                                                         int32_t x, int32_t y) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
       : "memory");
 }
 

@@ -101,11 +101,11 @@ def test_strides(cuda_lib):
 
 
 def _check_wgrad(got, dY, x, old):
-    dY, x = dY.cpu().double(), x.cpu().double()
+    dY, x = dY.double(), x.double()
     want, A = dY.t() @ x, dY.t().abs() @ x.abs()
     if old is not None:
-        want, A = want + old.cpu().double(), A + old.cpu().double().abs()
-    err = (got.cpu().double() - want)
+        want, A = want + old.double(), A + old.double().abs()
+    err = got.double() - want
     assert bool((err.abs() <= (dY.shape[0] + 17) * 2.0 ** -23 * A).all())
     assert err.norm() <= 1e-5 * want.norm()
 
@@ -132,6 +132,33 @@ def test_wgrad(cuda_lib, N, O, I):
     wide = torch.full((N, O + 16), float("nan"), dtype=BF, device=DEV)
     wide[:, 8:8 + O] = dY
     assert torch.equal(cuda_lib.flce_ckpt_wgrad(wide[:, 8:8 + O], ck), dW)
+
+
+@pytest.mark.parametrize("N,O,I", [
+    (20001, 264, 264),    # fewer tiles than CTA pairs, each shared by many
+    (8200, 520, 2056),    # 27 tiles, shared by two or three
+    (9000, 2568, 2056),   # 99 tiles: a whole round and 23
+    (30000, 8, 8),        # one tile
+    (2500, 3400, 3000)])  # 168 tiles, two whole rounds and 16 that are not shared out
+def test_wgrad_shared_tiles(cuda_lib, N, O, I):
+    """Tiles that several CTA pairs share along the tokens."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    dY = torch.randn(N, O, generator=g, device=DEV).to(BF)
+    x = torch.randn(N, I, generator=g, device=DEV).to(BF)
+    ck = cuda_lib.flce_ckpt_save(x)
+    x = cuda_lib.flce_ckpt_load(ck)
+    dW = torch.full((O, I), float("nan"), device=DEV)
+    cuda_lib.flce_ckpt_wgrad(dY, ck, dW=dW, sync=True)
+    _check_wgrad(dW, dY, x, None)
+    assert torch.equal(cuda_lib.flce_ckpt_wgrad(dY, ck), dW)
+    old = torch.randn(O, I, generator=g, device=DEV)
+    acc = old.clone()
+    info = {}
+    cuda_lib.flce_ckpt_wgrad(dY, ck, dW=acc, accumulate=True, info=info)
+    _check_wgrad(acc, dY, x, old)
+    assert int(info["status"].item()) == 0
+    ws = torch.full((info["workspace_bytes"],), 0xFF, dtype=torch.uint8, device=DEV)  # NaN
+    assert torch.equal(cuda_lib.flce_ckpt_wgrad(dY, ck, workspace=ws), dW)
 
 
 def test_wgrad_every_scale(cuda_lib):
