@@ -172,9 +172,8 @@ def load_library(path: str | None = None):
             fn.restype = i32
         lib.flce_attn_sizeof.argtypes = []
         lib.flce_attn_sizeof.restype = ctypes.c_size_t
-        pr = ctypes.POINTER(FlceResnorm)
-        for fn in (lib.flce_resnorm_fwd, lib.flce_resnorm_bwd):
-            fn.argtypes = [pr, po]
+        for fn in (lib.flce_resnorm_fwd, lib.flce_resnorm_bwd):  # FlceResnorm, or its bytes
+            fn.argtypes = [vp, po]
             fn.restype = i32
         lib.flce_resnorm_sizeof.argtypes = []
         lib.flce_resnorm_sizeof.restype = ctypes.c_size_t

@@ -6,13 +6,13 @@ through ``sync=True`` or ``info['status']``.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import NamedTuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import FlceResnorm, _check_out, _dtype_code, scale_convert
+from . import _check_out, _dtype_code, scale_convert
 from .step import _call, _library
 
 NORMS = {"rms": 0, "layer": 1}
@@ -21,32 +21,41 @@ GATE_NONE, GATE_SCALAR, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = range(5)
 _HALF = (torch.bfloat16, torch.float32)
 
 
-def _rows(name, t, N, H, dtype, device):
+# struct flce_resnorm, for _pack: at the size of these calls, filling a ctypes structure
+# field by field takes longer than the library's side of the call.
+_pack = struct.Struct("@qq7i3f" + "Pq" * 3 + "4P" + "Pq" + "P" + "Pq" + "P" + "Pq" * 5 + "4P").pack
+assert struct.calcsize("@qq7i3f") % 8 == 0
+_NONE = (0, 0)
+
+
+def _rows(name, t, shape, dtype, device):
     """A [N, H] tensor of ``dtype`` with a contiguous last axis; its address and row stride."""
+    if t is None:
+        return _NONE
+    row, last = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype is dtype and t.shape == shape and t.device == device and last == 1:
+        return t.data_ptr(), row
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (N, H):
-        raise ValueError(f"{name} must have shape {(N, H)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    row, last = t.stride()
-    if last != 1 and H > 1:
+    if last != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
     return t.data_ptr(), row
 
 
-def _vector(name, t, H, dtype, device):
+def _vector(name, t, shape, dtype, device):
     if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != (H,) or t.device != device or not t.is_contiguous():
-        _check_out(t, (H,), dtype, device, name)
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _check_out(t, shape, dtype, device, name)
     return t.data_ptr()
 
 
 def _gate_kind(gate, N, H):
     """A scalar or [H] is a learned gate; [N, 1] and [N, H] are gates computed per token."""
-    if gate is None:
-        return GATE_NONE
     if gate.dim() < 2:
         if gate.dim() == 1 and gate.shape[0] != H:
             raise ValueError(f"gate must have {H} elements, got {gate.shape[0]}")
@@ -58,53 +67,59 @@ def _gate_kind(gate, N, H):
     return GATE_FULL if gate.shape[1] == H else GATE_TOKEN
 
 
-def _gate_address(name, gate, kind, N, H, dtype, device):
-    if kind == GATE_NONE:
-        return None, 0
+def _gate_address(gate, kind, shape, dtype, device):
     if kind == GATE_FULL:
-        return _rows(name, gate, N, H, dtype, device)
+        return _rows("gate", gate, shape, dtype, device)
     if gate.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {gate.dtype}")
+        raise TypeError(f"gate must be {dtype}, got {gate.dtype}")
     if gate.device != device or (kind == GATE_CHANNEL and not gate.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+        raise ValueError(f"gate must be a contiguous CUDA tensor on {device}")
     return gate.data_ptr(), gate.stride(0) if kind == GATE_TOKEN else 0
 
 
-def _params_dtype(y, *params):
-    """The one type of all parameters: y's, or fp32."""
-    given = {t.dtype for t in params if t is not None}
-    if not given:
-        return y.dtype
-    if len(given) > 1 or not given <= {y.dtype, torch.float32}:
-        raise TypeError(f"weights, biases and learned gates must all be {y.dtype} or all fp32")
-    return given.pop()
-
-
-def _common(y, N, H, stream_dtype, w_post, b_post, w_pre, b_pre, gate, gate_act, kind, alpha,
-            beta, eps, post_norm, pre_norm):
-    """The fields that both passes share, in the structure's order up to ``eps``; the gate's
-    and parameters' addresses; the gate's kind and the type of learned parameters."""
-    dev = y.device
+def _common(y, shape, dev, stream_dtype, w_post, b_post, w_pre, b_pre, gate, gate_act, kind,
+            alpha, beta, eps, post_norm, pre_norm):
+    """The fields that both passes share: the structure's up to ``eps``, the gate's, the
+    parameters'; and the gate's kind."""
+    dt = y.dtype
     if kind not in NORMS:
         raise ValueError(f"kind must be one of {sorted(NORMS)}")
     if gate_act not in ACTS:
         raise ValueError(f"gate_act must be one of {[k for k in ACTS if k]}")
-    if stream_dtype is not y.dtype and (stream_dtype is not torch.float32):
-        raise TypeError(f"the stream must be {y.dtype} or fp32")
-    post = (w_post is not None or b_post is not None) if post_norm is None else bool(post_norm)
-    if not post and (w_post is not None or b_post is not None):
+    if stream_dtype is not dt and stream_dtype is not torch.float32:
+        raise TypeError(f"the stream must be {dt} or fp32")
+    given = w_post is not None or b_post is not None
+    post = given if post_norm is None else bool(post_norm)
+    if given and not post:
         raise ValueError("w_post and b_post need post_norm")
     if not pre_norm and (w_pre is not None or b_pre is not None):
         raise ValueError("w_pre and b_pre need pre_norm")
-    gk = _gate_kind(gate, N, H)
-    learned = gate if gk in (GATE_SCALAR, GATE_CHANNEL) else None
-    pt = _params_dtype(y, w_post, b_post, w_pre, b_pre, learned)
+    N, H = shape
+    gk = GATE_NONE if gate is None else _gate_kind(gate, N, H)
+    learned = gate if gk == GATE_SCALAR or gk == GATE_CHANNEL else None
+    # the one type of all parameters: y's, or fp32
+    pt = None
+    for t in (w_post, b_post, w_pre, b_pre, learned):
+        if t is not None:
+            if pt is None:
+                pt = t.dtype
+            if t.dtype is not pt or (pt is not dt and pt is not torch.float32):
+                raise TypeError(f"weights, biases and learned gates must all be {dt} or all fp32")
     head = (N, H, NORMS[kind], post, bool(pre_norm), stream_dtype is torch.float32,
-            pt is torch.float32, gk, ACTS[gate_act], float(alpha), float(beta), float(eps))
-    ga = _gate_address("gate", gate, gk, N, H, pt if learned is not None else y.dtype, dev)
-    vecs = (_vector("w_post", w_post, H, pt, dev), _vector("b_post", b_post, H, pt, dev),
-            _vector("w_pre", w_pre, H, pt, dev), _vector("b_pre", b_pre, H, pt, dev))
-    return head, ga, vecs, gk, post
+            pt is torch.float32, gk, ACTS[gate_act], alpha, beta, eps)
+    ga = _NONE if gate is None else _gate_address(gate, gk, shape, dt if learned is None else pt,
+                                                  dev)
+    one = (H,)
+    vecs = (_vector("w_post", w_post, one, pt, dev), _vector("b_post", b_post, one, pt, dev),
+            _vector("w_pre", w_pre, one, pt, dev), _vector("b_pre", b_pre, one, pt, dev))
+    return head, ga, vecs, gk
+
+
+def _check_stats(stats, N, dev):
+    if stats.shape != (4, N) or stats.dtype is not torch.float32 or stats.device != dev \
+            or not stats.is_contiguous():
+        _check_out(stats, (4, N), torch.float32, dev, "stats")
+    return stats.data_ptr()
 
 
 def _check_y(y, name="y"):
@@ -163,35 +178,34 @@ def flce_resnorm_fwd(y: torch.Tensor, h: torch.Tensor | None = None, *,
     y.  ``checkpoint``, of [N, H], receives z in 8 bits."""
     lib = _library()
     _check_y(y)
-    N, H = y.shape
-    dev = y.device
-    st = h.dtype if h is not None else stream_dtype or y.dtype
-    head, ga, vecs, _, _ = _common(y, N, H, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
-                                   kind, alpha, beta, eps, post_norm, pre_norm)
+    shape = y.shape
+    N, H = shape
+    dev, dt = y.device, y.dtype
+    st = h.dtype if h is not None else stream_dtype or dt
+    head, ga, vecs, _ = _common(y, shape, dev, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
+                                kind, alpha, beta, eps, post_norm, pre_norm)
     if out is None:
-        out = torch.empty((N, H), dtype=st, device=dev)
-    if stats is None:
-        stats = torch.empty((4, N), dtype=torch.float32, device=dev)
-    elif stats.shape != (4, N) or stats.dtype is not torch.float32 or stats.device != dev \
-            or not stats.is_contiguous():
-        _check_out(stats, (4, N), torch.float32, dev, "stats")
+        out = torch.empty(shape, dtype=st, device=dev)
     if not pre_norm:
         z = None
     elif z is None:
-        z = torch.empty((N, H), dtype=y.dtype, device=dev)
-    ck = None
+        z = torch.empty(shape, dtype=dt, device=dev)
+    if stats is None:
+        stats = torch.empty((4, N), dtype=torch.float32, device=dev)
+    ck = 0
     if checkpoint is not None:
         if not pre_norm or (checkpoint.N, checkpoint.H) != (N, H) \
                 or checkpoint.data.device != dev:
             raise ValueError(f"checkpoint must be of z, {(N, H)} on {dev}")
         ck = checkpoint.data.data_ptr()
-    a = FlceResnorm(*head, *_rows("y", y, N, H, y.dtype, dev),
-                    *((None, 0) if h is None else _rows("h", h, N, H, st, dev)), *ga, *vecs,
-                    *_rows("out", out, N, H, st, dev), stats.data_ptr(),
-                    *((None, 0) if z is None else _rows("z", z, N, H, y.dtype, dev)), ck)
-    _call(lib.flce_resnorm_fwd, dev, y.dtype, (ctypes.byref(a),), sync=sync, workspace=None,
-          info=info)
+    a = _pack(*head, *_rows("y", y, shape, dt, dev), *_rows("h", h, shape, st, dev), *ga, *vecs,
+              *_rows("out", out, shape, st, dev), _check_stats(stats, N, dev),
+              *_rows("z", z, shape, dt, dev), ck, *_NO_BACKWARD)
+    _call(lib.flce_resnorm_fwd, dev, dt, (a,), sync=sync, workspace=None, info=info)
     return out, z, stats
+
+
+_NO_BACKWARD = (0,) * 14
 
 
 class ResnormGrads(NamedTuple):
@@ -223,47 +237,49 @@ def flce_resnorm_bwd(dz: torch.Tensor | None, dh_out: torch.Tensor | None, y: to
     (``need_dh=False`` for a join without h)."""
     lib = _library()
     _check_y(y)
-    N, H = y.shape
-    dev = y.device
+    shape = y.shape
+    N, H = shape
+    dev, dt = y.device, y.dtype
     st = (h_out.dtype if h_out is not None else dh_out.dtype if dh_out is not None
-          else stream_dtype or y.dtype)
-    head, ga, vecs, gk, _ = _common(y, N, H, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
-                                    kind, alpha, beta, eps, post_norm, pre_norm)
+          else stream_dtype or dt)
+    head, ga, vecs, gk = _common(y, shape, dev, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
+                                 kind, alpha, beta, eps, post_norm, pre_norm)
     if (dz is not None) != bool(pre_norm):
         raise ValueError("dz goes with a pre-norm")
     if pre_norm and h_out is None:
         raise ValueError("a pre-norm's gradient needs h_out")
-    if stats.shape != (4, N) or stats.dtype is not torch.float32 or stats.device != dev \
-            or not stats.is_contiguous():
-        _check_out(stats, (4, N), torch.float32, dev, "stats")
     if dy is None:
-        dy = torch.empty((N, H), dtype=y.dtype, device=dev)
+        dy = torch.empty(shape, dtype=dt, device=dev)
     if dh is None and need_dh:
-        dh = torch.empty((N, H), dtype=st, device=dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    if gk in (GATE_SCALAR, GATE_CHANNEL):
-        dgate = torch.empty(gate.shape, **f32)
+        dh = torch.empty(shape, dtype=st, device=dev)
+    dga = _NONE
+    dgate = None
+    if gk == GATE_SCALAR:
+        dgate = torch.empty((), dtype=torch.float32, device=dev)
+    elif gk > GATE_CHANNEL:
+        dgate = torch.empty(gate.shape, dtype=dt, device=dev)
+        dga = dgate.data_ptr(), H if gk == GATE_FULL else 1
+    # gradients of the parameters, in one buffer
+    d = [w_post, b_post, w_pre, b_pre, gate if gk == GATE_CHANNEL else None]
+    n = sum(t is not None for t in d)
+    at = [0] * 5
+    if n:
+        sums = torch.empty((n, H), dtype=torch.float32, device=dev)
+        p, parts = sums.data_ptr(), iter(sums.unbind())
+        for i in range(5):
+            if d[i] is not None:
+                d[i], at[i] = next(parts), p
+                p += 4 * H
+    if gk == GATE_CHANNEL:
+        dgate, dga = d[4], (at[4], 0)
+    elif gk == GATE_SCALAR:
         dga = dgate.data_ptr(), 0
-    elif gk:
-        dgate = torch.empty(gate.shape, dtype=y.dtype, device=dev)
-        dga = dgate.data_ptr(), dgate.stride(0)
-    else:
-        dgate, dga = None, (None, 0)
-    n = sum(t is not None for t in (w_post, b_post, w_pre, b_pre))
-    sums = iter(torch.empty((n, H), **f32) if n else ())
-    d = [None if t is None else next(sums) for t in (w_post, b_post, w_pre, b_pre)]
-
-    def rows(name, t, dtype):
-        return (None, 0) if t is None else _rows(name, t, N, H, dtype, dev)
-
-    a = FlceResnorm(*head, *rows("y", y, y.dtype), None, 0, *ga, *vecs,
-                    *rows("h_out", h_out, st), stats.data_ptr(), None, 0, None,
-                    *rows("dz", dz, y.dtype), *rows("dh_out", dh_out, st),
-                    *rows("dy", dy, y.dtype), *rows("dh", dh, st), *dga,
-                    *(None if t is None else t.data_ptr() for t in d))
-    _call(lib.flce_resnorm_bwd, dev, y.dtype, (ctypes.byref(a),), sync=sync,
-          workspace=workspace, info=info)
-    return ResnormGrads(dy, dh, dgate, *d)
+    a = _pack(*head, *_rows("y", y, shape, dt, dev), 0, 0, *ga, *vecs,
+              *_rows("h_out", h_out, shape, st, dev), _check_stats(stats, N, dev), 0, 0, 0,
+              *_rows("dz", dz, shape, dt, dev), *_rows("dh_out", dh_out, shape, st, dev),
+              *_rows("dy", dy, shape, dt, dev), *_rows("dh", dh, shape, st, dev), *dga, *at[:4])
+    _call(lib.flce_resnorm_bwd, dev, dt, (a,), sync=sync, workspace=workspace, info=info)
+    return ResnormGrads(dy, dh, dgate, *d[:4])
 
 
 def flce_ckpt_save(x: torch.Tensor, *, out: Checkpoint | None = None, sync: bool = False,
@@ -277,7 +293,7 @@ def flce_ckpt_save(x: torch.Tensor, *, out: Checkpoint | None = None, sync: bool
     elif (out.N, out.H) != (N, H) or out.data.device != x.device:
         raise ValueError(f"out must be a checkpoint of {(N, H)} on {x.device}")
     _call(lib.flce_ckpt_save, x.device, x.dtype,
-          (*_rows("x", x, N, H, x.dtype, x.device), N, H, out.data.data_ptr()), sync=sync,
+          (*_rows("x", x, x.shape, x.dtype, x.device), N, H, out.data.data_ptr()), sync=sync,
           workspace=None, info=info)
     return out
 
@@ -293,7 +309,7 @@ def flce_ckpt_load(ckpt: Checkpoint, *, dtype: torch.dtype = torch.bfloat16,
             raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
         out = torch.empty((N, H), dtype=dtype, device=dev)
     _dtype_code(out)
-    p, row = _rows("out", out, N, H, out.dtype, dev)
+    p, row = _rows("out", out, (N, H), out.dtype, dev)
     _call(lib.flce_ckpt_load, dev, out.dtype, (ckpt.data.data_ptr(), N, H, p, row), sync=sync,
           workspace=None, info=info)
     return out
@@ -321,7 +337,7 @@ def flce_ckpt_wgrad(dY: torch.Tensor, ckpt: Checkpoint, *, dW: torch.Tensor | No
     else:
         _check_out(dW, (O, I), torch.float32, dev, "dW")
     _call(lib.flce_ckpt_wgrad, dev, dY.dtype,
-          (*_rows("dY", dY, N, O, dY.dtype, dev), ckpt.data.data_ptr(), N, O, I,
+          (*_rows("dY", dY, dY.shape, dY.dtype, dev), ckpt.data.data_ptr(), N, O, I,
            dW.data_ptr(), 1 if accumulate else 0), sync=sync, workspace=workspace, info=info)
     return dW
 

@@ -55,8 +55,18 @@ constexpr int kBwdPieces =
     kPieces<TY> + 2 * kPieces<TH> + (POST || GATE != kNoGate ? kPieces<TY> : 0) +
     (GATE == kFullGate ? kPieces<TY> : 0);
 
+// Rows that a group takes at a time: two share the exchange of their sums, where the
+// registers hold two (8192 x 4096 in bf16 with both norms: 75 us with one).
 template <class TY, class TH, bool POST, int GATE>
-constexpr int kBwdStages = ring_stages(kBwdPieces<TY, TH, POST, GATE>, kBwdThreads, kSmemPerSm, 6);
+constexpr int kBwdFit = ring_stages(kBwdPieces<TY, TH, POST, GATE>, kBwdThreads, kSmemPerSm, 6);
+template <class TY, class TH, bool POST, bool AFF, int GATE>
+constexpr int kBwdRows = POST && !AFF && (GATE == kNoGate || GATE == kChannelGate) &&
+                                 kBwdFit<TY, TH, POST, GATE> >= 4
+                             ? 2
+                             : 1;
+template <class TY, class TH, bool POST, bool AFF, int GATE>
+constexpr int kBwdStages = kBwdFit<TY, TH, POST, GATE> / kBwdRows<TY, TH, POST, AFF, GATE> *
+                           kBwdRows<TY, TH, POST, AFF, GATE>;
 
 // AFF: a mean or a bias is wanted.
 template <class TY, class TH, bool POST, bool AFF, int GATE>
@@ -87,7 +97,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int64_t units = static_cast<int64_t>(gridDim.x / p.cluster) * p.groups;
   const uint32_t step = blockDim.x * 16;
   const uint32_t ring = smem_addr(ring_raw) + threadIdx.x * 16;
-  constexpr int kStages = kBwdStages<TY, TH, POST, GATE>;
+  constexpr int R = kBwdRows<TY, TH, POST, AFF, GATE>;
+  constexpr int kStages = kBwdStages<TY, TH, POST, AFF, GATE>;
   const uint32_t stage = step * kBwdPieces<TY, TH, POST, GATE>, end = kStages * stage;
   const uint32_t at_h = kPieces<TY> * step, at_dh = at_h + kPieces<TH> * step;
   const uint32_t at_y = at_dh + kPieces<TH> * step, at_gate = at_y + kPieces<TY> * step;
@@ -116,7 +127,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     copies_commit();
   };
   uint32_t s_in = 0, s_out = 0;
-  for (; s_in < end - stage; s_in += stage) fetch(s_in);
+  for (; s_in < end - R * stage; s_in += stage) fetch(s_in);
   // a row's statistics, and its gate of one value, one row ahead
   struct Row {
     float mean_y, r_y, mean_h, r_h, gate;
@@ -136,7 +147,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       t.gate = one_element<TY>(p.gate.p, false, row * p.gate.row);
     return t;
   };
-  Row next = read_row(unit);
+  Row next[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) next[q] = read_row(unit + q * units);
 
   auto gate_of_channel = [&]() {  // act(gate), 1 without one
     if (GATE != kChannelGate) return same_oct(1.f);
@@ -162,140 +175,163 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float s_one = 0.f;
   Walk<TY> dy(p.dy.p, p.dy.row, unit, oct), dgate(p.dgate.p, p.dgate.row, unit, oct);
   Walk<TH> dh(p.dh.p, p.dh.row, unit, oct);
-  for (int64_t row = unit; row < p.N; row += units) {
-    fetch(s_in);
-    s_in = s_in + stage == end ? 0 : s_in + stage;
-    const Row t = next;
-    next = read_row(row + units);
-    copies_wait<kStages - 1>();
-    const uint32_t at = ring + s_out;
-    s_out = s_out + stage == end ? 0 : s_out + stage;
-
-    Oct dz = zero_oct(), xh = zero_oct(), e = zero_oct(), yh = zero_oct(), a = zero_oct(), slope;
-    if (in) {
-      if (p.pre) {
-        dz = shared_octet(TY{}, at, step);
-        xh = shared_octet(TH{}, at + at_h, step);
+  for (int64_t row = unit; row < p.N; row += R * units) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          xh.p[i] = mul2(AFF ? plus2(xh.p[i], pair(-t.mean_h)) : xh.p[i], pair(t.r_h));
-      }
-      if (p.dh_out.p) e = shared_octet(TH{}, at + at_dh, step);
-      if (kReadsY) yh = shared_octet(TY{}, at + at_y, step);
-      if (POST) {
+    for (int q = 0; q < R; ++q) fetch(s_in + q * stage);
+    s_in = s_in + R * stage == end ? 0 : s_in + R * stage;
+    Row t[R];
+    bool there[R];  // this thread has an octet of the row
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-t.mean_y)) : yh.p[i], pair(t.r_y));
-      }
-      if (GATE == kFullGate) a = shared_octet(TY{}, at + at_gate, step);
+    for (int q = 0; q < R; ++q) {
+      t[q] = next[q];
+      next[q] = read_row(row + (R + q) * units);
+      there[q] = in && (q == 0 || row + q * units < p.N);
     }
+    copies_wait<kStages - R>();
+
+    Oct dz, xh, e, yh, a = zero_oct(), slope = zero_oct();
+    float one_a = 0.f, one_slope = 0.f;
     // beta act(gate) and its slope
     auto act_of = [&](float g, float& value, float& gradient) {
       g = gate_act(p.act, g);
       gradient = p.beta * gate_slope(p.act, g);
       value = p.beta * g;
     };
-    if (GATE == kFullGate) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        act_of(a.p[i].x, a.p[i].x, slope.p[i].x);
-        act_of(a.p[i].y, a.p[i].y, slope.p[i].y);
-      }
-    }
-    float one_a = 0.f, one_slope = 0.f;
-    if (GATE == kOneGate)
-      act_of(p.gate_kind == FLCE_GATE_TOKEN ? t.gate : scalar, one_a, one_slope);
     // beta a, and beta a w_post
     auto gate_at = [&](int i) { return GATE == kOneGate ? pair(one_a) : a.p[i]; };
     auto weight = [&](int i) { return kFixed ? w_post.p[i] : mul2(gate_at(i), w_post.p[i]); };
-
-    // sums: g xh, [g], and with a post-norm q yh e, q yh xh, [q yh, q e, q, q xh]
-    constexpr int K = POST ? (AFF ? 8 : 4) : (AFF ? 2 : 1);
-    float2 v[K];
+    // row q's dz, xh, e = dh' + r g and yh; a second time where two rows are in hand, which
+    // takes fewer registers than keeping them
+    auto read = [&](int q) {
+      const uint32_t at = ring + s_out + q * stage;
+      dz = xh = e = yh = a = zero_oct();
+      if (there[q]) {
+        if (p.pre) {
+          dz = shared_octet(TY{}, at, step);
+          xh = shared_octet(TH{}, at + at_h, step);
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = pair(0.f);
+          for (int i = 0; i < 4; ++i)
+            xh.p[i] = mul2(AFF ? plus2(xh.p[i], pair(-t[q].mean_h)) : xh.p[i], pair(t[q].r_h));
+        }
+        if (p.dh_out.p) e = shared_octet(TH{}, at + at_dh, step);
+        if (kReadsY) yh = shared_octet(TY{}, at + at_y, step);
+        if (POST) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 g = mul2(dz.p[i], w_pre.p[i]);
-      v[0] = mad2(g, xh.p[i], v[0]);
-      e.p[i] = mad2(pair(t.r_h), g, e.p[i]);
-      if (AFF) v[K - 1] = plus2(v[K - 1], g);
-      if (POST) {
-        const float2 q = weight(i), qy = mul2(q, yh.p[i]);
-        v[1] = mad2(qy, e.p[i], v[1]);
-        v[2] = mad2(qy, xh.p[i], v[2]);
-        if (AFF) {
-          v[3] = plus2(v[3], qy);
-          v[4] = mad2(q, e.p[i], v[4]);
-          v[5] = plus2(v[5], q);
-          v[6] = mad2(q, xh.p[i], v[6]);
+          for (int i = 0; i < 4; ++i)
+            yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-t[q].mean_y)) : yh.p[i], pair(t[q].r_y));
+        }
+        if (GATE == kFullGate) a = shared_octet(TY{}, at + at_gate, step);
+      }
+      if (GATE == kFullGate) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          act_of(a.p[i].x, a.p[i].x, slope.p[i].x);
+          act_of(a.p[i].y, a.p[i].y, slope.p[i].y);
         }
       }
-    }
-    float s[K];
+      if (GATE == kOneGate)
+        act_of(p.gate_kind == FLCE_GATE_TOKEN ? t[q].gate : scalar, one_a, one_slope);
+    };
+    // sums of a row: g xh, [g], and with a post-norm q yh e, q yh xh, [q yh, q e, q, q xh]
+    constexpr int K = POST ? (AFF ? 8 : 4) : (AFF ? 2 : 1);
+    float s[R * K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = v[k].x + v[k].y;
+    for (int q = 0; q < R; ++q) {
+      read(q);
+      float2 v[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = pair(0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 g = mul2(dz.p[i], w_pre.p[i]);
+        v[0] = mad2(g, xh.p[i], v[0]);
+        e.p[i] = mad2(pair(t[q].r_h), g, e.p[i]);
+        if (AFF) v[K - 1] = plus2(v[K - 1], g);
+        if (POST) {
+          const float2 w = weight(i), wy = mul2(w, yh.p[i]);
+          v[1] = mad2(wy, e.p[i], v[1]);
+          v[2] = mad2(wy, xh.p[i], v[2]);
+          if (AFF) {
+            v[3] = plus2(v[3], wy);
+            v[4] = mad2(w, e.p[i], v[4]);
+            v[5] = plus2(v[5], w);
+            v[6] = mad2(w, xh.p[i], v[6]);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) s[q * K + k] = v[k].x + v[k].y;
+    }
     if (p.pre || POST) {
       sums.add(s);
       more.add(s);
     }
-    const float m2 = t.r_h * s[0] * p.inv_h;
-    const float m1 = AFF && layer ? t.r_h * s[K - 1] * p.inv_h : 0.f;
-    float c1 = 0.f, c2 = 0.f;
-    if (POST) {
-      c2 = t.r_y * p.inv_h * (s[1] - m2 * s[2] - (AFF ? m1 * s[3] : 0.f));
-      if (AFF && layer) c1 = t.r_y * p.inv_h * (s[4] - m2 * s[6] - m1 * s[5]);
-    }
-    float2 one = pair(0.f);
-    Oct dg;
+
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 dt = mad2(pair(-m2), xh.p[i], e.p[i]);
-      if (AFF) dt = plus2(dt, pair(-m1));
-      s_pre.p[i] = mad2(dz.p[i], xh.p[i], s_pre.p[i]);
-      if (AFF) s_bpre.p[i] = plus2(s_bpre.p[i], dz.p[i]);
-      float2 gy = mul2(weight(i), dt);
-      if (kFixed) {
-        if (kReadsY) s_post.p[i] = mad2(yh.p[i], dt, s_post.p[i]);
-        if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], dt);
-      } else {
-        const float2 du = mul2(gate_at(i), dt);
-        const float2 u = POST ? (AFF ? mad2(yh.p[i], w_post.p[i], b_post.p[i])
-                                     : mul2(yh.p[i], w_post.p[i]))
-                              : yh.p[i];
-        if (GATE == kOneGate)
-          one = mad2(u, in ? dt : pair(0.f), one);
-        else
-          dg.p[i] = mul2(mul2(slope.p[i], u), dt);
-        if (POST) s_post.p[i] = mad2(yh.p[i], du, s_post.p[i]);
-        if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], du);
-      }
+    for (int q = 0; q < R; ++q) {
+      const float r_h = t[q].r_h, r_y = t[q].r_y;
+      const float m2 = r_h * s[q * K] * p.inv_h;
+      const float m1 = AFF && layer ? r_h * s[q * K + K - 1] * p.inv_h : 0.f;
+      float c1 = 0.f, c2 = 0.f;
       if (POST) {
-        gy = mad2(pair(-c2), yh.p[i], mul2(pair(t.r_y), gy));
-        if (AFF) gy = plus2(gy, pair(-c1));
+        const float* v = &s[q * K];
+        c2 = r_y * p.inv_h * (v[1] - m2 * v[2] - (AFF ? m1 * v[3] : 0.f));
+        if (AFF && layer) c1 = r_y * p.inv_h * (v[4] - m2 * v[6] - m1 * v[5]);
       }
-      e.p[i] = gy;                         // dy
-      xh.p[i] = mul2(pair(p.alpha), dt);   // dh
-    }
-    if (in) {
-      dy.put(to_octet(TY{}, e));
-      if (p.dh.p) dh.put(to_octet(TH{}, xh));
-      if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg));
-    }
-    dy.at += p.dy.step;
-    dh.at += p.dh.step;
-    if (GATE == kFullGate) dgate.at += p.dgate.step;
-    if (GATE == kOneGate) {
-      if (p.gate_kind == FLCE_GATE_TOKEN) {
-        float d[1] = {one.x + one.y};
-        sums.add(d);
-        more.add(d);
-        if (in_cta == 0 && rank == 0)
-          store_element(TY{}, p.dgate.p, row * p.dgate.row, one_slope * d[0]);
-      } else {
-        s_one = fmaf(one_slope, one.x + one.y, s_one);
+      if (R > 1) read(q);
+      float2 one = pair(0.f);
+      Oct dg;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (R > 1) e.p[i] = mad2(pair(r_h), mul2(dz.p[i], w_pre.p[i]), e.p[i]);
+        float2 dt = mad2(pair(-m2), xh.p[i], e.p[i]);
+        if (AFF) dt = plus2(dt, pair(-m1));
+        s_pre.p[i] = mad2(dz.p[i], xh.p[i], s_pre.p[i]);
+        if (AFF) s_bpre.p[i] = plus2(s_bpre.p[i], dz.p[i]);
+        float2 gy = mul2(weight(i), dt);
+        if (kFixed) {
+          if (kReadsY) s_post.p[i] = mad2(yh.p[i], dt, s_post.p[i]);
+          if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], dt);
+        } else {
+          const float2 du = mul2(gate_at(i), dt);
+          const float2 u = POST ? (AFF ? mad2(yh.p[i], w_post.p[i], b_post.p[i])
+                                       : mul2(yh.p[i], w_post.p[i]))
+                                : yh.p[i];
+          if (GATE == kOneGate)
+            one = mad2(u, in ? dt : pair(0.f), one);
+          else
+            dg.p[i] = mul2(mul2(slope.p[i], u), dt);
+          if (POST) s_post.p[i] = mad2(yh.p[i], du, s_post.p[i]);
+          if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], du);
+        }
+        if (POST) {
+          gy = mad2(pair(-c2), yh.p[i], mul2(pair(r_y), gy));
+          if (AFF) gy = plus2(gy, pair(-c1));
+        }
+        e.p[i] = gy;                        // dy
+        xh.p[i] = mul2(pair(p.alpha), dt);  // dh
+      }
+      if (there[q]) {
+        dy.put(to_octet(TY{}, e));
+        if (p.dh.p) dh.put(to_octet(TH{}, xh));
+        if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg));
+      }
+      dy.at += p.dy.step;
+      dh.at += p.dh.step;
+      if (GATE == kFullGate) dgate.at += p.dgate.step;
+      if (GATE == kOneGate) {
+        if (p.gate_kind == FLCE_GATE_TOKEN) {
+          float d[1] = {one.x + one.y};
+          sums.add(d);
+          more.add(d);
+          if (in_cta == 0 && rank == 0)
+            store_element(TY{}, p.dgate.p, row * p.dgate.row, one_slope * d[0]);
+        } else {
+          s_one = fmaf(one_slope, one.x + one.y, s_one);
+        }
       }
     }
+    s_out = s_out + R * stage == end ? 0 : s_out + R * stage;
   }
 
   auto put = [&](float* part, const Oct& o) {
@@ -339,7 +375,8 @@ template <class TY, class TH, bool POST, bool AFF, int GATE>
 cudaError_t launch_bwd(NormParams p, int64_t parts, cudaStream_t s) {
   static SmemLimit limit;
   const int threads = 32 * p.warps * p.groups;
-  const int ring = threads * 16 * kBwdPieces<TY, TH, POST, GATE> * kBwdStages<TY, TH, POST, GATE>;
+  const int ring = threads * 16 * kBwdPieces<TY, TH, POST, GATE> *
+                   kBwdStages<TY, TH, POST, AFF, GATE>;
   const auto kernel = resnorm_bwd_kernel<TY, TH, POST, AFF, GATE>;
   const cudaError_t e = limit.raise(kernel, kSmemPerSm);
   if (e != cudaSuccess) return e;
