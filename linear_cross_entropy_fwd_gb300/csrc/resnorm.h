@@ -53,7 +53,7 @@ inline void set_steps(NormParams& p, int64_t rows, int y_bytes, int h_bytes) {
 }
 
 constexpr int kMaxH = 16384;
-constexpr int kSmemPerSm = 200 << 10;  // for rings, beside the slots of the sums
+constexpr int kSmemPerSm = 208 << 10;  // for rings, beside the slots of the sums
 
 cudaError_t launch_resnorm_fwd_bf16(const NormParams& p, int sms, cudaStream_t s);
 cudaError_t launch_resnorm_fwd_mixed(const NormParams& p, int sms, cudaStream_t s);
@@ -74,21 +74,48 @@ struct NormSums {
 };
 cudaError_t launch_resnorm_sums(const NormSums& p, cudaStream_t s);
 
-// act(g), and its derivative by act(g).  Quotients and exponentials within 2 units.
+// act(g), and its derivative by act(g).  The sigmoid's exponential is off by about |g| units
+// in the last place; tanh is its Taylor series below 0.2, where 1 - 2 / (1 + e^2g) would lose
+// digits (the next term is 62/2835 g^9, 1e-8 of it), and above off by 10 units at most.
 __device__ __forceinline__ float gate_act(int act, float g) {
-  if (act == FLCE_ACT_SIGMOID) return __fdividef(1.f, 1.f + expf(-g));
-  return act == FLCE_ACT_TANH ? tanhf(g) : g;
+  if (act == FLCE_ACT_NONE) return g;
+  if (act == FLCE_ACT_SIGMOID) return __fdividef(1.f, 1.f + __expf(-g));
+  const float x = g * g;
+  const float series =
+      g * fmaf(x, fmaf(x, fmaf(x, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float far = 1.f - __fdividef(2.f, 1.f + __expf(2.f * g));
+  return fabsf(g) < 0.2f ? series : far;
 }
 __device__ __forceinline__ float gate_slope(int act, float a) {
   if (act == FLCE_ACT_SIGMOID) return a * (1.f - a);
   return act == FLCE_ACT_TANH ? 1.f - a * a : 1.f;
 }
 __device__ __forceinline__ Oct gate_act_each(int act, Oct g) {
+  if (act == FLCE_ACT_SIGMOID) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    g.p[i] = make_float2(gate_act(act, g.p[i].x), gate_act(act, g.p[i].y));
+    for (int i = 0; i < 4; ++i)
+      g.p[i] = make_float2(gate_act(FLCE_ACT_SIGMOID, g.p[i].x), gate_act(FLCE_ACT_SIGMOID, g.p[i].y));
+  } else if (act == FLCE_ACT_TANH) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      g.p[i] = make_float2(gate_act(FLCE_ACT_TANH, g.p[i].x), gate_act(FLCE_ACT_TANH, g.p[i].y));
+  }
   return g;
 }
+// Slopes of a pair without a branch, which would wait for loads in flight: a - a^2 and
+// 1 - a^2 by their coefficients, or 1.
+struct GateSlope {
+  float c0, c1;
+  bool one;
+  __device__ __forceinline__ explicit GateSlope(int act)
+      : c0(act == FLCE_ACT_TANH ? 1.f : 0.f),
+        c1(act == FLCE_ACT_SIGMOID ? 1.f : 0.f),
+        one(act == FLCE_ACT_NONE) {}
+  __device__ __forceinline__ float2 operator()(float2 a) const {
+    const float2 s = mad2(a, plus2(pair(c1), mul2(a, pair(-1.f))), pair(c0));
+    return make_float2(one ? 1.f : s.x, one ? 1.f : s.y);
+  }
+};
 // The same out of line, for what is done once: the code around it stays short.
 static __device__ __noinline__ Oct gate_act_oct(int act, Oct g) { return gate_act_each(act, g); }
 

@@ -57,15 +57,28 @@ constexpr int kBwdPieces =
 
 // Rows that a group takes at a time: two share the exchange of their sums, where the
 // registers hold two (8192 x 4096 in bf16 with both norms: 75 us with one).
-template <class TY, class TH, bool POST, int GATE>
-constexpr int kBwdFit = ring_stages(kBwdPieces<TY, TH, POST, GATE>, kBwdThreads, kSmemPerSm, 6);
+// And behind the pieces, for each warp, the row's four statistics and its gate of one value:
+// a load a row ahead would have to keep registers through the row, or is moved to where it is
+// waited for (8192 x 4096 with gates per element 131 us, 54 of them waiting).
+constexpr uint32_t kRowBytes = 32, kTailBytes = kRowBytes * kMaxRowWarps;
+
+// Weights that wait in shared memory behind the ring instead of in registers: where a norm
+// after the block and its means or biases need those for sums.
+template <bool POST, bool AFF, int GATE>
+constexpr int kBwdVectors = POST && AFF ? (GATE == kFullGate ? 3 : 2) : 0;
+template <class TY, class TH, bool POST, bool AFF, int GATE>
+constexpr int kBwdFit =
+    ring_stages(kBwdPieces<TY, TH, POST, GATE>, kBwdThreads,
+                kSmemPerSm - 4 * static_cast<int>(kTailBytes) -
+                    kBwdVectors<POST, AFF, GATE> * kBwdThreads * 32,
+                4);
 template <class TY, class TH, bool POST, bool AFF, int GATE>
 constexpr int kBwdRows = POST && !AFF && (GATE == kNoGate || GATE == kChannelGate) &&
-                                 kBwdFit<TY, TH, POST, GATE> >= 4
+                                 kBwdFit<TY, TH, POST, AFF, GATE> >= 4
                              ? 2
                              : 1;
 template <class TY, class TH, bool POST, bool AFF, int GATE>
-constexpr int kBwdStages = kBwdFit<TY, TH, POST, GATE> / kBwdRows<TY, TH, POST, AFF, GATE> *
+constexpr int kBwdStages = kBwdFit<TY, TH, POST, AFF, GATE> / kBwdRows<TY, TH, POST, AFF, GATE> *
                            kBwdRows<TY, TH, POST, AFF, GATE>;
 
 // AFF: a mean or a bias is wanted.
@@ -99,7 +112,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t ring = smem_addr(ring_raw) + threadIdx.x * 16;
   constexpr int R = kBwdRows<TY, TH, POST, AFF, GATE>;
   constexpr int kStages = kBwdStages<TY, TH, POST, AFF, GATE>;
-  const uint32_t stage = step * kBwdPieces<TY, TH, POST, GATE>, end = kStages * stage;
+  const uint32_t tail = step * kBwdPieces<TY, TH, POST, GATE>, stage = tail + kTailBytes;
+  const uint32_t end = kStages * stage;
+  const uint32_t my_tail = smem_addr(ring_raw) + tail + warp * kRowBytes;
   const uint32_t at_h = kPieces<TY> * step, at_dh = at_h + kPieces<TH> * step;
   const uint32_t at_y = at_dh + kPieces<TH> * step, at_gate = at_y + kPieces<TY> * step;
   int64_t ahead = unit;
@@ -107,16 +122,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   Walk<TH> h_in(p.h_out.p, p.h_out.row, unit, oct);
   Walk<TH> dh_in(p.dh_out.p, p.dh_out.row, unit, oct);
   Walk<TY> gate_in(p.gate.p, p.gate.row, unit, oct);
+  const bool token = GATE == kOneGate && p.gate_kind == FLCE_GATE_TOKEN;
+  // address of a token's gate; its word, if all of that belongs to some token
+  auto gate_of = [&](int64_t row) {
+    return static_cast<const uint8_t*>(p.gate.p) + row * p.gate.row * Elem<TY>::kBytes;
+  };
   auto fetch = [&](uint32_t s) {
-    if (in && ahead < p.N) {
-      const uint32_t at = ring + s;
-      if (p.pre) {
-        copy_octet<TY>(at, step, dz_in.at);
-        copy_octet<TH>(at + at_h, step, h_in.at);
+    if (ahead < p.N) {
+      if (in) {
+        const uint32_t at = ring + s;
+        if (p.pre) {
+          copy_octet<TY>(at, step, dz_in.at);
+          copy_octet<TH>(at + at_h, step, h_in.at);
+        }
+        if (p.dh_out.p) copy_octet<TH>(at + at_dh, step, dh_in.at);
+        if (kReadsY) copy_octet<TY>(at + at_y, step, y_in.at);
+        if (GATE == kFullGate) copy_octet<TY>(at + at_gate, step, gate_in.at);
       }
-      if (p.dh_out.p) copy_octet<TH>(at + at_dh, step, dh_in.at);
-      if (kReadsY) copy_octet<TY>(at + at_y, step, y_in.at);
-      if (GATE == kFullGate) copy_octet<TY>(at + at_gate, step, gate_in.at);
+      if (lane < 4) {
+        if (lane < 2 ? POST : p.pre != 0)
+          copy4(my_tail + s + 4 * lane, p.stats + lane * p.N + ahead);
+      } else if (lane == 4 && token) {
+        const uint8_t* g = gate_of(ahead);
+        const uint8_t* word = g - (reinterpret_cast<uintptr_t>(g) & 3);
+        if (Elem<TY>::kBytes == 4 || (word >= gate_of(0) && word + 2 <= gate_of(p.N - 1)))
+          copy4(my_tail + s + 16, word);
+        else  // the first or the last of a tensor that ends within a word
+          st_shared4(my_tail + s + 16, static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(g))
+                                           << (8 * (g - word)));
+      }
       ahead += units;
       dz_in.at += p.dz.step;
       h_in.at += p.h_out.step;
@@ -128,82 +162,67 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   uint32_t s_in = 0, s_out = 0;
   for (; s_in < end - R * stage; s_in += stage) fetch(s_in);
-  // a row's statistics, and its gate of one value, one row ahead
-  struct Row {
-    float mean_y, r_y, mean_h, r_h, gate;
-  };
-  auto read_row = [&](int64_t row) {
-    Row t{0.f, 1.f, 0.f, 0.f, 0.f};
-    if (row >= p.N) return t;
-    if (POST) {
-      if (AFF) t.mean_y = p.stats[row];
-      t.r_y = p.stats[p.N + row];
-    }
-    if (p.pre) {
-      if (AFF) t.mean_h = p.stats[2 * p.N + row];
-      t.r_h = p.stats[3 * p.N + row];
-    }
-    if (GATE == kOneGate && p.gate_kind == FLCE_GATE_TOKEN)
-      t.gate = one_element<TY>(p.gate.p, false, row * p.gate.row);
-    return t;
-  };
-  Row next[R];
-#pragma unroll
-  for (int q = 0; q < R; ++q) next[q] = read_row(unit + q * units);
-
   auto gate_of_channel = [&]() {  // act(gate), 1 without one
     if (GATE != kChannelGate) return same_oct(1.f);
     return gate_act_oct(p.act, param_octet<TY>(p.gate.p, pfp, oct, 1.f));
   };
-  // w_post: times beta a where that is fixed
+  // w_post and b_post: times beta, and a where that is fixed
+  constexpr bool kShared = kBwdVectors<POST, AFF, GATE> > 0;
+  const uint32_t vectors = smem_addr(ring_raw) + end + in_cta * 16, plane = 32 * p.warps * 16;
   Oct w_pre = zero_oct(), w_post = zero_oct(), b_post = zero_oct();
   if (in) {
     w_pre = param_octet<TY>(p.w_pre, pfp, oct, 1.f);
     w_post = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f);
-    if (kFixed) {
-      scale_oct(w_post, gate_of_channel());
-      scale_oct(w_post, p.beta);
-    } else if (POST && AFF) {
+    if (kFixed) scale_oct(w_post, gate_of_channel());
+    scale_oct(w_post, p.beta);
+    if (GATE == kFullGate && POST && AFF) {
       b_post = param_octet<TY>(p.b_post, pfp, oct, 0.f);
+      scale_oct(b_post, p.beta);
     }
   }
+  if (kShared) {
+    if (group == 0) {
+      put_shared(vectors, plane, w_pre);
+      put_shared(vectors + 2 * plane, plane, w_post);
+      if (GATE == kFullGate) put_shared(vectors + 4 * plane, plane, b_post);
+    }
+    __syncthreads();
+  }
+  auto pre_weight = [&]() { return kShared ? shared_octet(float{}, vectors, plane) : w_pre; };
+  auto post_weight = [&]() {
+    return kShared ? shared_octet(float{}, vectors + 2 * plane, plane) : w_post;
+  };
   float scalar = 0.f;
   if (GATE == kOneGate && p.gate_kind == FLCE_GATE_SCALAR) scalar = one_element<TY>(p.gate.p, pfp, 0);
 
-  // Sums over tokens: dz xh, dz, and with a fixed gate yh dt, dt; else yh du, du.
+  // Sums over tokens: dz xh, dz, and yh du, du without the factor beta and a fixed gate's.
   Oct s_pre = zero_oct(), s_bpre = zero_oct(), s_post = zero_oct(), s_bpost = zero_oct();
   float s_one = 0.f;
   Walk<TY> dy(p.dy.p, p.dy.row, unit, oct), dgate(p.dgate.p, p.dgate.row, unit, oct);
   Walk<TH> dh(p.dh.p, p.dh.row, unit, oct);
+  const GateSlope slope(p.act);
   for (int64_t row = unit; row < p.N; row += R * units) {
 #pragma unroll
     for (int q = 0; q < R; ++q) fetch(s_in + q * stage);
     s_in = s_in + R * stage == end ? 0 : s_in + R * stage;
-    Row t[R];
     bool there[R];  // this thread has an octet of the row
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      t[q] = next[q];
-      next[q] = read_row(row + (R + q) * units);
-      there[q] = in && (q == 0 || row + q * units < p.N);
-    }
+    for (int q = 0; q < R; ++q) there[q] = in && (q == 0 || row + q * units < p.N);
     copies_wait<kStages - R>();
+    __syncwarp();  // the tails are read by all lanes
 
-    Oct dz, xh, e, yh, a = zero_oct(), slope = zero_oct();
-    float one_a = 0.f, one_slope = 0.f;
-    // beta act(gate) and its slope
-    auto act_of = [&](float g, float& value, float& gradient) {
-      g = gate_act(p.act, g);
-      gradient = p.beta * gate_slope(p.act, g);
-      value = p.beta * g;
-    };
-    // beta a, and beta a w_post
-    auto gate_at = [&](int i) { return GATE == kOneGate ? pair(one_a) : a.p[i]; };
-    auto weight = [&](int i) { return kFixed ? w_post.p[i] : mul2(gate_at(i), w_post.p[i]); };
-    // row q's dz, xh, e = dh' + r g and yh; a second time where two rows are in hand, which
-    // takes fewer registers than keeping them
+    Oct dz, xh, e, yh, a = zero_oct();
+    float one = 0.f;  // act(gate) of gates with one value; `a` of those per element
+    float mean_y, r_y, mean_h, r_h;
+    // row q's dz, xh, dh' and yh; a second time where two rows are in hand, which takes
+    // fewer registers than keeping them
     auto read = [&](int q) {
-      const uint32_t at = ring + s_out + q * stage;
+      const uint32_t at = ring + s_out + q * stage, row_at = my_tail + s_out + q * stage;
+      const uint4 t = ld_shared16(row_at);
+      mean_y = __uint_as_float(t.x);
+      r_y = __uint_as_float(t.y);
+      mean_h = __uint_as_float(t.z);
+      r_h = p.pre && (q == 0 || row + q * units < p.N) ? __uint_as_float(t.w) : 0.f;
       dz = xh = e = yh = a = zero_oct();
       if (there[q]) {
         if (p.pre) {
@@ -211,48 +230,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           xh = shared_octet(TH{}, at + at_h, step);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            xh.p[i] = mul2(AFF ? plus2(xh.p[i], pair(-t[q].mean_h)) : xh.p[i], pair(t[q].r_h));
+            xh.p[i] = mul2(AFF ? plus2(xh.p[i], pair(-mean_h)) : xh.p[i], pair(r_h));
         }
         if (p.dh_out.p) e = shared_octet(TH{}, at + at_dh, step);
         if (kReadsY) yh = shared_octet(TY{}, at + at_y, step);
         if (POST) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-t[q].mean_y)) : yh.p[i], pair(t[q].r_y));
+            yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-mean_y)) : yh.p[i], pair(r_y));
         }
-        if (GATE == kFullGate) a = shared_octet(TY{}, at + at_gate, step);
+        if (GATE == kFullGate)
+          a = gate_act_each(p.act, shared_octet(TY{}, at + at_gate, step));
       }
-      if (GATE == kFullGate) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          act_of(a.p[i].x, a.p[i].x, slope.p[i].x);
-          act_of(a.p[i].y, a.p[i].y, slope.p[i].y);
+      if (GATE == kOneGate) {
+        float g = scalar;
+        if (token) {
+          const uint32_t w = ld_shared4(row_at + 16);
+          const bool upper = Elem<TY>::kBytes == 2 &&
+                             (reinterpret_cast<uintptr_t>(gate_of(row + q * units)) & 2);
+          g = element_value<TY>(upper ? w >> 16 : w, false);
         }
+        one = gate_act(p.act, g);
       }
-      if (GATE == kOneGate)
-        act_of(p.gate_kind == FLCE_GATE_TOKEN ? t[q].gate : scalar, one_a, one_slope);
     };
-    // sums of a row: g xh, [g], and with a post-norm q yh e, q yh xh, [q yh, q e, q, q xh]
-    constexpr int K = POST ? (AFF ? 8 : 4) : (AFF ? 2 : 1);
+    // Sums of a row: g xh, [g]; and with a post-norm or a gate of one value, with w for
+    // beta [a] w_post: w yh e, w yh xh, [w yh], and for layer norms [w e, w, w xh].
+    constexpr bool kSumsY = POST || GATE == kOneGate;
+    constexpr int K = kSumsY ? (AFF ? 8 : 4) : (AFF ? 2 : 1);
     float s[R * K];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       read(q);
+      const Oct wp = pre_weight(), wq = post_weight();
       float2 v[K];
 #pragma unroll
       for (int k = 0; k < K; ++k) v[k] = pair(0.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 g = mul2(dz.p[i], w_pre.p[i]);
+        const float2 g = mul2(dz.p[i], wp.p[i]);
         v[0] = mad2(g, xh.p[i], v[0]);
-        e.p[i] = mad2(pair(t[q].r_h), g, e.p[i]);
+        e.p[i] = mad2(pair(r_h), g, e.p[i]);
         if (AFF) v[K - 1] = plus2(v[K - 1], g);
-        if (POST) {
-          const float2 w = weight(i), wy = mul2(w, yh.p[i]);
+        if (kSumsY) {
+          const float2 w = GATE == kFullGate ? mul2(a.p[i], wq.p[i]) : wq.p[i];
+          const float2 wy = mul2(w, yh.p[i]);
           v[1] = mad2(wy, e.p[i], v[1]);
           v[2] = mad2(wy, xh.p[i], v[2]);
-          if (AFF) {
-            v[3] = plus2(v[3], wy);
+          if (AFF) v[3] = plus2(v[3], wy);
+          if (AFF && POST) {
             v[4] = mad2(w, e.p[i], v[4]);
             v[5] = plus2(v[5], w);
             v[6] = mad2(w, xh.p[i], v[6]);
@@ -262,53 +287,59 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
       for (int k = 0; k < K; ++k) s[q * K + k] = v[k].x + v[k].y;
     }
-    if (p.pre || POST) {
+    if (p.pre || kSumsY) {
       sums.add(s);
       more.add(s);
     }
 
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      const float r_h = t[q].r_h, r_y = t[q].r_y;
+      if (R > 1) read(q);
       const float m2 = r_h * s[q * K] * p.inv_h;
       const float m1 = AFF && layer ? r_h * s[q * K + K - 1] * p.inv_h : 0.f;
-      float c1 = 0.f, c2 = 0.f;
+      // sum w yh dt: with a gate of one value its gradient, and dy's second mean
+      float wyd = 0.f, c1 = 0.f, c2 = 0.f;
+      if (kSumsY) wyd = s[q * K + 1] - m2 * s[q * K + 2] - (AFF ? m1 * s[q * K + 3] : 0.f);
       if (POST) {
-        const float* v = &s[q * K];
-        c2 = r_y * p.inv_h * (v[1] - m2 * v[2] - (AFF ? m1 * v[3] : 0.f));
-        if (AFF && layer) c1 = r_y * p.inv_h * (v[4] - m2 * v[6] - m1 * v[5]);
+        c2 = r_y * p.inv_h * wyd;
+        if (AFF && layer)
+          c1 = r_y * p.inv_h * (s[q * K + 4] - m2 * s[q * K + 6] - m1 * s[q * K + 5]);
       }
-      if (R > 1) read(q);
-      float2 one = pair(0.f);
-      Oct dg;
+      if (GATE == kOneGate) {
+        c1 *= one;
+        c2 *= one;
+      }
+      const Oct wp = R > 1 ? pre_weight() : zero_oct(), wq = post_weight();
+      const Oct bq = GATE == kFullGate && kShared
+                         ? shared_octet(float{}, vectors + 4 * plane, plane)
+                         : zero_oct();
+      Oct dg = zero_oct();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (R > 1) e.p[i] = mad2(pair(r_h), mul2(dz.p[i], w_pre.p[i]), e.p[i]);
+        if (R > 1) e.p[i] = mad2(pair(r_h), mul2(dz.p[i], wp.p[i]), e.p[i]);
         float2 dt = mad2(pair(-m2), xh.p[i], e.p[i]);
         if (AFF) dt = plus2(dt, pair(-m1));
         s_pre.p[i] = mad2(dz.p[i], xh.p[i], s_pre.p[i]);
         if (AFF) s_bpre.p[i] = plus2(s_bpre.p[i], dz.p[i]);
-        float2 gy = mul2(weight(i), dt);
-        if (kFixed) {
-          if (kReadsY) s_post.p[i] = mad2(yh.p[i], dt, s_post.p[i]);
-          if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], dt);
-        } else {
-          const float2 du = mul2(gate_at(i), dt);
-          const float2 u = POST ? (AFF ? mad2(yh.p[i], w_post.p[i], b_post.p[i])
-                                       : mul2(yh.p[i], w_post.p[i]))
-                                : yh.p[i];
-          if (GATE == kOneGate)
-            one = mad2(u, in ? dt : pair(0.f), one);
-          else
-            dg.p[i] = mul2(mul2(slope.p[i], u), dt);
-          if (POST) s_post.p[i] = mad2(yh.p[i], du, s_post.p[i]);
-          if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], du);
+        // du over beta, or beta a where that is fixed
+        float2 du = dt;
+        if (GATE == kOneGate) du = mul2(pair(one), dt);
+        if (GATE == kFullGate) {
+          du = mul2(a.p[i], dt);
+          // beta u: w_post is times beta, and beta itself without a post-norm
+          const float2 u = POST && AFF ? mad2(yh.p[i], wq.p[i], bq.p[i])
+                                       : mul2(yh.p[i], wq.p[i]);
+          dg.p[i] = mul2(mul2(slope(a.p[i]), u), dt);
         }
+        if (POST || GATE == kChannelGate) s_post.p[i] = mad2(yh.p[i], du, s_post.p[i]);
+        if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], du);
+        float2 gy = mul2(wq.p[i], du);
         if (POST) {
           gy = mad2(pair(-c2), yh.p[i], mul2(pair(r_y), gy));
           if (AFF) gy = plus2(gy, pair(-c1));
         }
         e.p[i] = gy;                        // dy
+        a.p[i] = dt;
         xh.p[i] = mul2(pair(p.alpha), dt);  // dh
       }
       if (there[q]) {
@@ -320,15 +351,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       dh.at += p.dh.step;
       if (GATE == kFullGate) dgate.at += p.dgate.step;
       if (GATE == kOneGate) {
-        if (p.gate_kind == FLCE_GATE_TOKEN) {
-          float d[1] = {one.x + one.y};
+        if (POST && p.b_post) {  // u has a part beside w yh
+          float d[1] = {0.f};
+          if (there[q]) {
+            Oct b = param_octet<TY>(p.b_post, pfp, oct, 0.f);
+            scale_oct(b, a);
+            d[0] = p.beta * sum_oct(b);
+          }
           sums.add(d);
           more.add(d);
-          if (in_cta == 0 && rank == 0)
-            store_element(TY{}, p.dgate.p, row * p.dgate.row, one_slope * d[0]);
-        } else {
-          s_one = fmaf(one_slope, one.x + one.y, s_one);
+          wyd += d[0];
         }
+        wyd *= gate_slope(p.act, one);
+        if (p.gate_kind == FLCE_GATE_SCALAR)
+          s_one += wyd;
+        else if (in_cta == 0 && rank == 0)
+          store_element(TY{}, p.dgate.p, (row + q * units) * p.dgate.row, wyd);
       }
     }
     s_out = s_out + R * stage == end ? 0 : s_out + R * stage;
@@ -356,18 +394,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                           p.beta * gate_slope(p.act, a.p[i].y)));
       put(p.part[4], f);
     }
-    scale_oct(a, p.beta);
     scale_oct(s_post, a);
     scale_oct(s_bpost, a);
   }
+  scale_oct(s_post, p.beta);
+  scale_oct(s_bpost, p.beta);
   if (POST) put(p.part[2], s_post);
   if (POST && AFF) put(p.part[3], s_bpost);
-  if (GATE == kOneGate && p.part[4]) {
-    float d[1] = {s_one};
-    sums.add(d);
-    more.add(d);
-    if (in_cta == 0 && rank == 0) p.part[4][unit] = d[0];
-  }
+  if (GATE == kOneGate && p.part[4] && in_cta == 0 && rank == 0) p.part[4][unit] = s_one;
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while another writes to its slots
 }
 
@@ -375,7 +409,8 @@ template <class TY, class TH, bool POST, bool AFF, int GATE>
 cudaError_t launch_bwd(NormParams p, int64_t parts, cudaStream_t s) {
   static SmemLimit limit;
   const int threads = 32 * p.warps * p.groups;
-  const int ring = threads * 16 * kBwdPieces<TY, TH, POST, GATE> *
+  const int vectors = kBwdVectors<POST, AFF, GATE> * 32 * p.warps * 32;
+  const int ring = (threads * 16 * kBwdPieces<TY, TH, POST, GATE> + static_cast<int>(kTailBytes)) *
                    kBwdStages<TY, TH, POST, AFF, GATE>;
   const auto kernel = resnorm_bwd_kernel<TY, TH, POST, AFF, GATE>;
   const cudaError_t e = limit.raise(kernel, kSmemPerSm);
@@ -385,7 +420,7 @@ cudaError_t launch_bwd(NormParams p, int64_t parts, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(parts / p.groups * p.cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(ring);
+  cfg.dynamicSmemBytes = static_cast<size_t>(ring + vectors);
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);

@@ -132,11 +132,19 @@ __device__ __forceinline__ Oct param_octet(const void* p, bool fp32, int o, floa
   return fp32 ? load_octet<float>(p, o) : load_octet<T>(p, o);
 }
 
-// One element of type T, or fp32.
+// One element of type T, or fp32: its bits, for a load that nothing waits for yet, and its value.
+template <class T>
+__device__ __forceinline__ uint32_t element_bits(const void* p, bool fp32, int64_t i) {
+  if (fp32 || Elem<T>::kBytes == 4) return static_cast<const uint32_t*>(p)[i];
+  return static_cast<const uint16_t*>(p)[i];
+}
+template <class T>
+__device__ __forceinline__ float element_value(uint32_t bits, bool fp32) {
+  return __uint_as_float(fp32 || Elem<T>::kBytes == 4 ? bits : bits << 16);
+}
 template <class T>
 __device__ __forceinline__ float one_element(const void* p, bool fp32, int64_t i) {
-  if (fp32 || Elem<T>::kBytes == 4) return static_cast<const float*>(p)[i];
-  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+  return element_value<T>(element_bits<T>(p, fp32, i), fp32);
 }
 __device__ __forceinline__ void store_element(bf16_t, void* p, int64_t i, float v) {
   static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
@@ -160,6 +168,9 @@ constexpr int kMaxSums = 8;
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -173,6 +184,14 @@ constexpr int ring_stages(int pieces, int threads, int bytes, int most) {
   return bytes / (pieces * threads * 16) < most ? bytes / (pieces * threads * 16) : most;
 }
 
+__device__ __forceinline__ void st_shared4(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -210,6 +229,12 @@ struct Walk {
     *reinterpret_cast<typename Elem<T>::Octet*>(at) = o;
   }
 };
+__device__ __forceinline__ void put_shared(uint32_t a, uint32_t step, const Oct& o) {
+  const Elem<float>::Octet v = to_octet(float{}, o);
+  st_shared_v4(a, v.a.x, v.a.y, v.a.z, v.a.w);
+  st_shared_v4(a + step, v.b.x, v.b.y, v.b.z, v.b.w);
+}
+
 template <class T>
 constexpr int kPieces = Elem<T>::kBytes / 2;  // 16-byte pieces of an octet
 
