@@ -31,6 +31,7 @@ struct NormParams {
   int32_t H;
   int32_t layer, post, pre, params_fp32;
   int32_t gate_kind, act;
+  int32_t wide;        // fp32 rows that are written are 32-byte aligned
   float alpha, beta, eps, inv_h;
   RowTensor y, h, gate, h_out, z, dz, dh_out, dy, dh, dgate;
   const void *w_post, *b_post, *w_pre, *b_pre;

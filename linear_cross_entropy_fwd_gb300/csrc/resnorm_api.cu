@@ -286,6 +286,11 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
   p.b_pre = a.b_pre;
   p.h_out = row(a.h_out, a.h_out_row);
   p.stats = a.stats;
+  p.wide = 1;
+  for (const void* q : {static_cast<const void*>(backward ? a.dy : a.h_out),
+                        static_cast<const void*>(backward ? a.dh : a.z),
+                        static_cast<const void*>(full ? a.dgate : nullptr)})
+    if (reinterpret_cast<uintptr_t>(q) & 31) p.wide = 0;
   StepCall call;
   if (!backward) {
     p.h = row(a.h, a.h_row);

@@ -109,7 +109,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int64_t unit = static_cast<int64_t>(blockIdx.x / p.cluster) * p.groups + group;
   const int64_t units = static_cast<int64_t>(gridDim.x / p.cluster) * p.groups;
   const uint32_t step = blockDim.x * 16;
-  const uint32_t ring = smem_addr(ring_raw) + threadIdx.x * 16;
+  const uint32_t ring = smem_addr(ring_raw);
+  const int mine = (p.octets < p.H / 8 - rank * p.octets ? p.octets : p.H / 8 - rank * p.octets);
+  const Slot<TY> slot_y(threadIdx.x, lane, in_cta, mine);
+  const Slot<TH> slot_h(threadIdx.x, lane, in_cta, mine);
   constexpr int R = kBwdRows<TY, TH, POST, AFF, GATE>;
   constexpr int kStages = kBwdStages<TY, TH, POST, AFF, GATE>;
   const uint32_t tail = step * kBwdPieces<TY, TH, POST, GATE>, stage = tail + kTailBytes;
@@ -117,6 +120,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t my_tail = smem_addr(ring_raw) + tail + warp * kRowBytes;
   const uint32_t at_h = kPieces<TY> * step, at_dh = at_h + kPieces<TH> * step;
   const uint32_t at_y = at_dh + kPieces<TH> * step, at_gate = at_y + kPieces<TY> * step;
+  constexpr bool kOwn = Slot<TY>::kOwn && Slot<TH>::kOwn;
   int64_t ahead = unit;
   Walk<TY> dz_in(p.dz.p, p.dz.row, unit, oct), y_in(p.y.p, p.y.row, unit, oct);
   Walk<TH> h_in(p.h_out.p, p.h_out.row, unit, oct);
@@ -129,15 +133,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   auto fetch = [&](uint32_t s) {
     if (ahead < p.N) {
-      if (in) {
-        const uint32_t at = ring + s;
+      const uint32_t at = ring + s;
+      // one branch for all copies where a lane makes all of its own or none
+      if (!kOwn || in) {
         if (p.pre) {
-          copy_octet<TY>(at, step, dz_in.at);
-          copy_octet<TH>(at + at_h, step, h_in.at);
+          slot_y.copy(at, dz_in.at, kOwn);
+          slot_h.copy(at + at_h, h_in.at, kOwn);
         }
-        if (p.dh_out.p) copy_octet<TH>(at + at_dh, step, dh_in.at);
-        if (kReadsY) copy_octet<TY>(at + at_y, step, y_in.at);
-        if (GATE == kFullGate) copy_octet<TY>(at + at_gate, step, gate_in.at);
+        if (p.dh_out.p) slot_h.copy(at + at_dh, dh_in.at, kOwn);
+        if (kReadsY) slot_y.copy(at + at_y, y_in.at, kOwn);
+        if (GATE == kFullGate) slot_y.copy(at + at_gate, gate_in.at, kOwn);
       }
       if (lane < 4) {
         if (lane < 2 ? POST : p.pre != 0)
@@ -188,9 +193,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     __syncthreads();
   }
-  auto pre_weight = [&]() { return kShared ? shared_octet(float{}, vectors, plane) : w_pre; };
+  auto pre_weight = [&]() { return kShared ? shared_oct(vectors, plane) : w_pre; };
   auto post_weight = [&]() {
-    return kShared ? shared_octet(float{}, vectors + 2 * plane, plane) : w_post;
+    return kShared ? shared_oct(vectors + 2 * plane, plane) : w_post;
   };
   float scalar = 0.f;
   if (GATE == kOneGate && p.gate_kind == FLCE_GATE_SCALAR) scalar = one_element<TY>(p.gate.p, pfp, 0);
@@ -209,38 +214,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
     for (int q = 0; q < R; ++q) there[q] = in && (q == 0 || row + q * units < p.N);
     copies_wait<kStages - R>();
-    __syncwarp();  // the tails are read by all lanes
+    __syncwarp();  // lanes read what others copied
 
     Oct dz, xh, e, yh, a = zero_oct();
     float one = 0.f;  // act(gate) of gates with one value; `a` of those per element
-    float mean_y, r_y, mean_h, r_h;
+    float mean_y, r_y, mean_h, r_h, rs_y[R], rs_h[R];
     // row q's dz, xh, dh' and yh; a second time where two rows are in hand, which takes
     // fewer registers than keeping them
-    auto read = [&](int q) {
+    auto read = [&](int q, bool again) {
       const uint32_t at = ring + s_out + q * stage, row_at = my_tail + s_out + q * stage;
-      const uint4 t = ld_shared16(row_at);
-      mean_y = __uint_as_float(t.x);
-      r_y = __uint_as_float(t.y);
-      mean_h = __uint_as_float(t.z);
-      r_h = p.pre && (q == 0 || row + q * units < p.N) ? __uint_as_float(t.w) : 0.f;
+      if (again) {  // two rows are taken of RMS norms only
+        mean_y = mean_h = 0.f;
+        r_y = rs_y[q];
+        r_h = rs_h[q];
+      } else {
+        const uint4 t = ld_shared16(row_at);
+        mean_y = __uint_as_float(t.x);
+        rs_y[q] = r_y = __uint_as_float(t.y);
+        mean_h = __uint_as_float(t.z);
+        rs_h[q] = r_h =
+            p.pre && (q == 0 || row + q * units < p.N) ? __uint_as_float(t.w) : 0.f;
+      }
       dz = xh = e = yh = a = zero_oct();
       if (there[q]) {
         if (p.pre) {
-          dz = shared_octet(TY{}, at, step);
-          xh = shared_octet(TH{}, at + at_h, step);
+          dz = slot_y.read(at);
+          xh = slot_h.read(at + at_h);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             xh.p[i] = mul2(AFF ? plus2(xh.p[i], pair(-mean_h)) : xh.p[i], pair(r_h));
         }
-        if (p.dh_out.p) e = shared_octet(TH{}, at + at_dh, step);
-        if (kReadsY) yh = shared_octet(TY{}, at + at_y, step);
+        if (p.dh_out.p) e = slot_h.read(at + at_dh);
+        if (kReadsY) yh = slot_y.read(at + at_y);
         if (POST) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-mean_y)) : yh.p[i], pair(r_y));
         }
         if (GATE == kFullGate)
-          a = gate_act_each(p.act, shared_octet(TY{}, at + at_gate, step));
+          a = gate_act_each(p.act, slot_y.read(at + at_gate));
       }
       if (GATE == kOneGate) {
         float g = scalar;
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     float s[R * K];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      read(q);
+      read(q, false);
       const Oct wp = pre_weight(), wq = post_weight();
       float2 v[K];
 #pragma unroll
@@ -287,14 +299,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
       for (int k = 0; k < K; ++k) s[q * K + k] = v[k].x + v[k].y;
     }
+    // (the exchanges also see to it that all lanes have read what later copies overwrite)
     if (p.pre || kSumsY) {
       sums.add(s);
       more.add(s);
+    } else {
+      __syncwarp();
     }
 
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      if (R > 1) read(q);
+      if (R > 1) {
+        read(q, true);
+        if (!kOwn && q == R - 1) __syncwarp();  // as above
+      }
       const float m2 = r_h * s[q * K] * p.inv_h;
       const float m1 = AFF && layer ? r_h * s[q * K + K - 1] * p.inv_h : 0.f;
       // sum w yh dt: with a gate of one value its gradient, and dy's second mean
@@ -311,7 +329,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       const Oct wp = R > 1 ? pre_weight() : zero_oct(), wq = post_weight();
       const Oct bq = GATE == kFullGate && kShared
-                         ? shared_octet(float{}, vectors + 4 * plane, plane)
+                         ? shared_oct(vectors + 4 * plane, plane)
                          : zero_oct();
       Oct dg = zero_oct();
 #pragma unroll
@@ -343,9 +361,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         xh.p[i] = mul2(pair(p.alpha), dt);  // dh
       }
       if (there[q]) {
-        dy.put(to_octet(TY{}, e));
-        if (p.dh.p) dh.put(to_octet(TH{}, xh));
-        if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg));
+        dy.put(to_octet(TY{}, e), p.wide);
+        if (p.dh.p) dh.put(to_octet(TH{}, xh), p.wide);
+        if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg), p.wide);
       }
       dy.at += p.dy.step;
       dh.at += p.dh.step;

@@ -126,10 +126,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.groups + group;
   const int64_t rows = static_cast<int64_t>(gridDim.x) * p.groups;
 
-  // The ring: of each octet y, then h, then a gate per element.
+  // The ring: of each of a thread's octets y, then h, then a gate per element.
   const uint32_t step = blockDim.x * 16;
-  const uint32_t ring = smem_addr(ring_raw) + threadIdx.x * 16;
+  const uint32_t ring = smem_addr(ring_raw);
   constexpr int kPer = kPieces<TY> + kPieces<TH> + (FULL ? kPieces<TY> : 0);
+  const uint32_t at_h = kPieces<TY> * step, at_gate = at_h + kPieces<TH> * step;
   constexpr int R = kFwdRows<TY, TH, NV, FULL>;
   constexpr int kStages = kFwdStages<TY, TH, NV, FULL> / R * R;
   static_assert(kStages >= 1, "a stage of the longest row");
@@ -141,14 +142,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (ahead < p.N) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (!in[j]) continue;
         const uint32_t to = ring + s + j * kPer * step;
-        copy_octet<TY>(to, step, y.at + j * jump * 8 * Elem<TY>::kBytes);
-        if (p.h.p)
-          copy_octet<TH>(to + kPieces<TY> * step, step, h.at + j * jump * 8 * Elem<TH>::kBytes);
-        if (FULL)
-          copy_octet<TY>(to + (kPieces<TY> + kPieces<TH>) * step, step,
-                         gate.at + j * jump * 8 * Elem<TY>::kBytes);
+        const Slot<TY> slot_y(threadIdx.x, lane, oct[j], octets);
+        const Slot<TH> slot_h(threadIdx.x, lane, oct[j], octets);
+        constexpr bool kOwn = Slot<TY>::kOwn && Slot<TH>::kOwn;
+        if (kOwn && !in[j]) continue;
+        slot_y.copy(to, y.at + j * jump * 8 * Elem<TY>::kBytes, kOwn);
+        if (p.h.p) slot_h.copy(to + at_h, h.at + j * jump * 8 * Elem<TH>::kBytes, kOwn);
+        if (FULL) slot_y.copy(to + at_gate, gate.at + j * jump * 8 * Elem<TY>::kBytes, kOwn);
       }
       ahead += rows;
       y.at += p.y.step;
@@ -209,14 +210,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mean_y[q] = r_y[q] = mean_h[q] = r_h[q] = 0.f;
     }
     copies_wait<kStages - R>();
+    __syncwarp();  // lanes read what others copied
+    const Slot<TY> slot_y(threadIdx.x, lane, 0, 0);
+    const Slot<TH> slot_h(threadIdx.x, lane, 0, 0);
     const uint32_t at = ring + s_out;
     s_out = s_out + R * stage == end ? 0 : s_out + R * stage;
 #pragma unroll
     for (int q = 0; q < R; ++q)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        x[q][j] = in[j] && there[q] ? shared_octet(TY{}, at + q * stage + j * kPer * step, step)
-                                    : zero_oct();
+        x[q][j] = in[j] && there[q] ? slot_y.read(at + q * stage + j * kPer * step) : zero_oct();
     if (p.post) normalise<R, NV, LAYER>(x, in, p.eps, p.inv_h, sums, mean_y, r_y, f);
 #pragma unroll
     for (int q = 0; q < R; ++q)
@@ -237,22 +240,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         scale_oct(v, kKeep  ? c[kKeep ? j : 0]
                      : FULL ? factor(oct[j])
-                            : shared_octet(float{}, factors + oct[j] * 32, 16));
+                            : shared_oct(factors + oct[j] * 32, 16));
         if (FULL)
-          scale_oct(v, gate_act_each(p.act, shared_octet(
-                           TY{}, mine + (kPieces<TY> + kPieces<TH>) * step, step)));
+          scale_oct(v, gate_act_each(p.act, slot_y.read(mine + at_gate)));
         if (one_gate) scale_oct(v, gate_act(p.act, gate1[q]));
         if (p.h.p) {
-          const Oct t = shared_octet(TH{}, mine + kPieces<TY> * step, step);
+          const Oct t = slot_h.read(mine + at_h);
 #pragma unroll
           for (int i = 0; i < 4; ++i) v.p[i] = mad2(pair(p.alpha), t.p[i], v.p[i]);
         }
         // the stream is what is stored of it; see flce_resnorm
         const auto o = to_octet(TH{}, v);
         if (p.h_out.p)
-          reinterpret_cast<typename Elem<TH>::Octet*>(h_out.at + q * p.h_out.step)[j * jump] = o;
+          h_out.put(o, p.wide, q * p.h_out.step + j * jump * 8 * Elem<TH>::kBytes);
         v = from_octet(o);
       }
+    // all lanes have read what later copies overwrite: here, or by the exchanges of sums
+    if (!p.pre) __syncwarp();
     if (p.pre) {
       normalise<R, NV, LAYER>(x, in, p.eps, p.inv_h, sums, mean_h, r_h, f);
 #pragma unroll
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (!there[q]) continue;
           const auto o = to_octet(TY{}, v);
           if (in[j])
-            reinterpret_cast<typename Elem<TY>::Octet*>(z.at + q * p.z.step)[j * jump] = o;
+            z.put(o, p.wide, q * p.z.step + j * jump * 8 * Elem<TY>::kBytes);
           if (p.ckpt.codes) {
             const int64_t at_row = row + q * rows;
             ckpt_store_octet(p.ckpt, p.ckpt.codes + at_row * p.ckpt.pitch + oct[j] * 8,

@@ -161,10 +161,9 @@ constexpr int kMaxRowWarps = 16;  // warps that share a row
 constexpr int kMaxSums = 8;
 
 // ---------------------------------------------------------------------------
-// A ring of rows in shared memory.  Every thread copies its own octets of the next rows with
-// 16-byte asynchronous copies and reads only those, so that no thread waits for another's;
-// the rows in flight hide memory's latency whatever the registers hold.  Stage `s` keeps
-// piece k of a thread at (s * pieces + k) * threads + thread.
+// A ring of rows in shared memory.  Every warp copies its own octets of the next rows with
+// 16-byte asynchronous copies and reads only those, so that no warp waits for another's;
+// the rows in flight hide memory's latency whatever the registers hold.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -201,20 +200,74 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   return v;
 }
 
-// One octet of T at `src` to shared memory, its 16-byte pieces `step` apart; and back.
+// A thread's place for one octet of T in each stage.  A bf16 octet is one 16-byte piece.  An
+// fp32 octet is two: a warp's 32 octets are copied as 64 pieces side by side (each lane's
+// two pieces next to one another would ask for every 32-byte sector twice), so lanes read
+// what others copied, after a __syncwarp.  Piece c lies at c ^ (c >> 3 & 1), which spreads a
+// quarter warp's reads of every other piece over all banks.
 template <class T>
-__device__ __forceinline__ void copy_octet(uint32_t dst, uint32_t step, const uint8_t* src) {
-  copy16(dst, src);
-  if (Elem<T>::kBytes == 4) copy16(dst + step, src + 16);
-}
-__device__ __forceinline__ Oct shared_octet(bf16_t, uint32_t a, uint32_t) {
-  return from_octet(ld_shared16(a));
-}
-__device__ __forceinline__ Oct shared_octet(float, uint32_t a, uint32_t step) {
+struct Slot;
+template <>
+struct Slot<bf16_t> {
+  uint32_t at;
+  bool there;
+  __device__ __forceinline__ Slot(int thread, int, int octet, int octets)
+      : at(thread * 16), there(octet < octets) {}
+  static constexpr bool kOwn = true;  // a lane copies what it reads
+  __device__ __forceinline__ void copy(uint32_t region, const uint8_t* octet, bool known) const {
+    if (known || there) copy16(region + at, octet);
+  }
+  __device__ __forceinline__ Oct read(uint32_t region) const {
+    return from_octet(ld_shared16(region + at));
+  }
+};
+template <>
+struct Slot<float> {
+  uint32_t to, first, second;
+  int back;
+  bool a, b;
+  __device__ __forceinline__ Slot(int thread, int lane, int octet, int octets)
+      : back(16 * lane),
+        a(octet - lane + lane / 2 < octets),
+        b(octet - lane + 16 + lane / 2 < octets) {
+    const uint32_t warp = (thread - lane) * 32, flip = lane >> 2 & 1;
+    to = warp + (lane ^ (lane >> 3 & 1)) * 16;
+    first = warp + ((2 * lane) ^ flip) * 16;
+    second = warp + ((2 * lane + 1) ^ flip) * 16;
+  }
+  static constexpr bool kOwn = false;
+  __device__ __forceinline__ void copy(uint32_t region, const uint8_t* octet, bool) const {
+    if (a) copy16(region + to, octet - back);
+    if (b) copy16(region + to + 512, octet - back + 512);
+  }
+  __device__ __forceinline__ Oct read(uint32_t region) const {
+    Elem<float>::Octet o;
+    o.a = ld_shared16(region + first);
+    o.b = ld_shared16(region + second);
+    return from_octet(o);
+  }
+};
+
+// An fp32 octet kept as two planes `step` bytes apart.
+__device__ __forceinline__ Oct shared_oct(uint32_t a, uint32_t step) {
   Elem<float>::Octet o;
   o.a = ld_shared16(a);
   o.b = ld_shared16(a + step);
   return from_octet(o);
+}
+
+__device__ __forceinline__ void put_octet(void* at, const uint4& o, bool) {
+  *static_cast<uint4*>(at) = o;
+}
+// `wide`: 32-byte aligned, so that a store covers whole sectors.
+__device__ __forceinline__ void put_octet(void* at, const Elem<float>::Octet& o, bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(o.a.x),
+                 "r"(o.a.y), "r"(o.a.z), "r"(o.a.w), "r"(o.b.x), "r"(o.b.y), "r"(o.b.z),
+                 "r"(o.b.w)
+                 : "memory");
+  else
+    *static_cast<Elem<float>::Octet*>(at) = o;
 }
 
 // A thread's octet of one row after the other.  The step to the next one is a launch
@@ -225,8 +278,9 @@ struct Walk {
   __device__ __forceinline__ Walk(const void* base, int64_t row_stride, int64_t row, int octet)
       : at(static_cast<uint8_t*>(const_cast<void*>(base)) +
            (row * row_stride + 8 * octet) * Elem<T>::kBytes) {}
-  __device__ __forceinline__ void put(const typename Elem<T>::Octet& o) const {
-    *reinterpret_cast<typename Elem<T>::Octet*>(at) = o;
+  __device__ __forceinline__ void put(const typename Elem<T>::Octet& o, bool wide,
+                                      int64_t bytes = 0) const {
+    put_octet(at + bytes, o, wide);
   }
 };
 __device__ __forceinline__ void put_shared(uint32_t a, uint32_t step, const Oct& o) {

@@ -156,6 +156,34 @@ def test_strides_and_in_place(cuda_lib, H):
     assert torch.equal(y, z) and z3 is y
 
 
+@pytest.mark.parametrize("N,H", [(3, 8), (21, 264), (9, 4104)])
+@pytest.mark.parametrize("types", [TYPES[2], TYPES[4]])
+def test_addresses_of_16_bytes(cuda_lib, N, H, types):
+    """Rows that begin 16 bytes past a multiple of 32, and per-token gates that begin and end
+    within a word, in tensors that end where the last of them does."""
+    flce = cuda_lib
+    t, p, opts = _make(N, H, *types, post=True, gate="token", act="tanh")
+    out, z, stats = _forward(flce, t, p, opts)
+    got = flce.flce_resnorm_bwd(t["dz"], t["dh_out"], t["y"], out, stats, **p, **opts)
+
+    def off(x, like=None):
+        n = 16 // x.element_size()
+        raw = torch.empty(x.numel() + n, dtype=x.dtype, device=DEV)
+        raw[n:] = x.reshape(-1)
+        return raw[n:].view(x.shape)
+
+    s = {k: off(v) for k, v in t.items()}
+    raw = torch.empty(N + 1, dtype=p["gate"].dtype, device=DEV)
+    raw[1:] = p["gate"][:, 0]
+    q = {**p, "gate": raw[1:].view(N, 1)}
+    o2, z2, st2 = flce.flce_resnorm_fwd(s["y"], s["h"], **q, **opts, out=off(out), z=off(z))
+    assert torch.equal(o2, out) and torch.equal(z2, z) and torch.equal(st2, stats)
+    g2 = flce.flce_resnorm_bwd(s["dz"], s["dh_out"], s["y"], o2, st2, **q, **opts,
+                               dy=off(t["y"]), dh=off(t["h"]))
+    for a, b in zip(got, g2):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
 def test_nan_and_infinity_stay_in_their_rows(cuda_lib):
     for kind, H in (("rms", 200), ("layer", 200), ("rms", 5000)):
         t, p, opts = _make(40, H, BF, BF, BF, kind=kind, post=True, gate="full", act="sigmoid")
