@@ -31,6 +31,7 @@ struct NormParams {
   int32_t H;
   int32_t layer, post, pre, params_fp32;
   int32_t gate_kind, act;
+  int32_t biased;      // backward: a mean or a bias is wanted
   int32_t wide;        // fp32 rows that are written are 32-byte aligned
   float alpha, beta, eps, inv_h;
   RowTensor y, h, gate, h_out, z, dz, dh_out, dy, dh, dgate;
@@ -43,6 +44,8 @@ struct NormParams {
   // backward
   int32_t cluster;     // CTAs that share a row
   int32_t octets;      // of a row in each CTA of a cluster
+  int32_t nv;          // octets of a thread
+  int32_t sms, fit;    // of the device; CTAs or clusters that run at once
   float* part[5];      // sums over tokens of dw_pre, db_pre, dw_post, db_post, dgate:
                        // [parts][H], or [parts] for a scalar gate; null: not wanted
 };
@@ -60,11 +63,11 @@ cudaError_t launch_resnorm_fwd_bf16(const NormParams& p, int sms, cudaStream_t s
 cudaError_t launch_resnorm_fwd_mixed(const NormParams& p, int sms, cudaStream_t s);
 cudaError_t launch_resnorm_fwd_fp32(const NormParams& p, int sms, cudaStream_t s);
 
-// Sets the launch shape; returns the rows of each of part[].
-int64_t plan_resnorm_bwd(NormParams& p, int sms);
-cudaError_t launch_resnorm_bwd_bf16(const NormParams& p, int64_t parts, cudaStream_t s);
-cudaError_t launch_resnorm_bwd_mixed(const NormParams& p, int64_t parts, cudaStream_t s);
-cudaError_t launch_resnorm_bwd_fp32(const NormParams& p, int64_t parts, cudaStream_t s);
+// With parts == 0, the launch's shape is set and nothing is run; else `parts` is the number of
+// rows of each of part[]: the grid's groups of warps.
+cudaError_t launch_resnorm_bwd_bf16(NormParams& p, int64_t parts, cudaStream_t s);
+cudaError_t launch_resnorm_bwd_mixed(NormParams& p, int64_t parts, cudaStream_t s);
+cudaError_t launch_resnorm_bwd_fp32(NormParams& p, int64_t parts, cudaStream_t s);
 
 // out[k][col] = sum over `parts` rows of part[k], fp32, in a fixed order.
 struct NormSums {

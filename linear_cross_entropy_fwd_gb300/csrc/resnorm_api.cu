@@ -59,19 +59,6 @@ cudaError_t launch_resnorm_sums(const NormSums& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, resnorm_sums_kernel, p);
 }
 
-int64_t plan_resnorm_bwd(NormParams& p, int sms) {
-  const int octets = p.H / 8;
-  constexpr int most = 32 * kMaxRowWarps;
-  p.cluster = octets <= most ? 1 : octets <= 2 * most ? 2 : 4;
-  p.octets = (octets + p.cluster - 1) / p.cluster;
-  p.warps = (p.octets + 31) / 32;
-  p.groups = kMaxRowWarps / p.warps;
-  int64_t grid = (p.N + p.groups - 1) / p.groups;
-  const int64_t fit = sms / p.cluster > 0 ? sms / p.cluster : 1;
-  if (grid > fit) grid = fit;
-  return grid * p.groups;
-}
-
 namespace {
 
 using wide = __int128;
@@ -311,7 +298,22 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
   p.dy = row(a.dy, a.dy_row);
   p.dh = row(a.dh, a.dh_row);
   p.dgate = row(a.dgate, a.dgate_row);
-  const int64_t parts = N > 0 ? plan_resnorm_bwd(p, sms) : 0;
+  // what of it a row's kernel is to make decides between its variants, hence its shape
+  auto rows_kernel = [&](int64_t parts) {
+    return ey == 4   ? launch_resnorm_bwd_fp32(p, parts, call.stream)
+           : eh == 4 ? launch_resnorm_bwd_mixed(p, parts, call.stream)
+                     : launch_resnorm_bwd_bf16(p, parts, call.stream);
+  };
+  p.biased = a.norm == FLCE_NORM_LAYER || (a.post_norm && (a.b_post || a.db_post)) ||
+             (a.pre_norm && a.db_pre);
+  int64_t parts = 0;
+  if (N > 0) {
+    p.sms = sms;
+    const cudaError_t e = rows_kernel(0);
+    if (e != cudaSuccess) return host_cuda_error(e, "resnorm_bwd");
+    const int64_t want = (N + p.groups - 1) / p.groups;
+    parts = (want < p.fit ? want : p.fit) * p.groups;
+  }
   size_t at[5], bytes = 0;
   for (int k = 0; k < 5; ++k) {
     at[k] = bytes;
@@ -328,10 +330,7 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
     t.width[k] = sums[k].width;
   }
   cudaError_t e = cudaSuccess;
-  if (N > 0)
-    e = ey == 4   ? launch_resnorm_bwd_fp32(p, parts, call.stream)
-        : eh == 4 ? launch_resnorm_bwd_mixed(p, parts, call.stream)
-                  : launch_resnorm_bwd_bf16(p, parts, call.stream);
+  if (N > 0) e = rows_kernel(parts);
   if (e == cudaSuccess) e = launch_resnorm_sums(t, call.stream);
   if (e != cudaSuccess) rc = host_cuda_error(e, "resnorm_bwd");
   return call.end(rc);

@@ -6,7 +6,7 @@ namespace flce {
 cudaError_t launch_resnorm_fwd_bf16(const NormParams& p, int sms, cudaStream_t s) {
   return launch_fwd_types<bf16_t, bf16_t>(p, sms, s);
 }
-cudaError_t launch_resnorm_bwd_bf16(const NormParams& p, int64_t parts, cudaStream_t s) {
+cudaError_t launch_resnorm_bwd_bf16(NormParams& p, int64_t parts, cudaStream_t s) {
   return launch_bwd_types<bf16_t, bf16_t>(p, parts, s);
 }
 }  // namespace flce

@@ -11,6 +11,8 @@
 //   dt = e - r m1 - r m2 xh,   sum gy yh = sum q yh e - r m1 sum q yh - r m2 sum q yh xh
 // (and the same without yh), so all sums of a row are taken together, one exchange per row.
 #pragma once
+#include <atomic>
+
 #include "host_util.h"
 #include "resnorm.h"
 
@@ -55,34 +57,36 @@ constexpr int kBwdPieces =
     kPieces<TY> + 2 * kPieces<TH> + (POST || GATE != kNoGate ? kPieces<TY> : 0) +
     (GATE == kFullGate ? kPieces<TY> : 0);
 
-// Rows that a group takes at a time: two share the exchange of their sums, where the
-// registers hold two (8192 x 4096 in bf16 with both norms: 75 us with one).
 // And behind the pieces, for each warp, the row's four statistics and its gate of one value:
 // a load a row ahead would have to keep registers through the row, or is moved to where it is
 // waited for (8192 x 4096 with gates per element 131 us, 54 of them waiting).
 constexpr uint32_t kRowBytes = 32, kTailBytes = kRowBytes * kMaxRowWarps;
 
-// Weights that wait in shared memory behind the ring instead of in registers: where a norm
-// after the block and its means or biases need those for sums.
-template <bool POST, bool AFF, int GATE>
-constexpr int kBwdVectors = POST && AFF ? (GATE == kFullGate ? 3 : 2) : 0;
-template <class TY, class TH, bool POST, bool AFF, int GATE>
-constexpr int kBwdFit =
-    ring_stages(kBwdPieces<TY, TH, POST, GATE>, kBwdThreads,
-                kSmemPerSm - 4 * static_cast<int>(kTailBytes) -
-                    kBwdVectors<POST, AFF, GATE> * kBwdThreads * 32,
-                4);
-template <class TY, class TH, bool POST, bool AFF, int GATE>
-constexpr int kBwdRows = POST && !AFF && (GATE == kNoGate || GATE == kChannelGate) &&
-                                 kBwdFit<TY, TH, POST, AFF, GATE> >= 4
-                             ? 2
-                             : 1;
-template <class TY, class TH, bool POST, bool AFF, int GATE>
-constexpr int kBwdStages = kBwdFit<TY, TH, POST, AFF, GATE> / kBwdRows<TY, TH, POST, AFF, GATE> *
-                           kBwdRows<TY, TH, POST, AFF, GATE>;
+// What the launch and the kernel agree on, for NV octets a thread.
+template <class TY, class TH, bool POST, bool AFF, int GATE, int NV>
+struct BwdShape {
+  static constexpr int kPiecesRow = NV * kBwdPieces<TY, TH, POST, GATE>;
+  // Rows that a group takes at a time: two share the exchange of their sums, where the
+  // registers hold two (8192 x 4096 in bf16 with both norms: 79 us with one, 70 with two).
+  static constexpr bool kTwoRows = NV == 1 && Elem<TH>::kBytes + Elem<TY>::kBytes <= 6 && POST &&
+                                   !AFF && (GATE == kNoGate || GATE == kChannelGate);
+  // Weights that wait in shared memory behind the ring instead of in registers: where a norm
+  // after the block and its means or biases, a second row or a second octet need those.
+  static constexpr int kVectors = POST && AFF && GATE == kFullGate           ? 3
+                                  : NV > 1 || (POST && AFF) || kTwoRows ? 2
+                                                                             : 0;
+  static constexpr int kFit =
+      ring_stages(kPiecesRow, kBwdThreads,
+                  kSmemPerSm - 4 * static_cast<int>(kTailBytes) - kVectors * NV * kBwdThreads * 32,
+                  4);
+  static constexpr int kRows = kTwoRows && kFit >= 4 ? 2 : 1;
+  static constexpr int kStages = kFit / kRows * kRows;
+  // Two octets a thread: twice the sums over tokens in registers, and two stages.
+  static constexpr bool kPossible = NV == 1 || (!(POST && AFF) && kStages >= 2);
+};
 
 // AFF: a mean or a bias is wanted.
-template <class TY, class TH, bool POST, bool AFF, int GATE>
+template <class TY, class TH, bool POST, bool AFF, int GATE, int NV>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     resnorm_bwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float slots[kMaxRowWarps][2][kMaxSums][kMaxRowWarps];
@@ -98,9 +102,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   if (p.cluster > 1) cluster_sync();  // every CTA runs before its slots are written
   grid_launch_dependents();  // the sums' CTAs take the SMs that this launch's leave
-  const int in_cta = sums.warp * 32 + lane;
-  const int oct = rank * p.octets + in_cta;
-  const bool in = in_cta < p.octets && oct < p.H / 8;
+  using Shape = BwdShape<TY, TH, POST, AFF, GATE, NV>;
+  // this thread's octets: of those of its CTA, and of the row
+  const int jump = 32 * p.warps;
+  const int mine = p.octets < p.H / 8 - rank * p.octets ? p.octets : p.H / 8 - rank * p.octets;
+  int in_cta[NV], oct[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    in_cta[j] = j * jump + sums.warp * 32 + lane;
+    oct[j] = rank * p.octets + in_cta[j];
+    in[j] = in_cta[j] < mine;
+  }
   const bool pfp = p.params_fp32, layer = p.layer;
   constexpr bool kReadsY = POST || GATE != kNoGate;
   // a is the same in every row, so that it and the weight multiply the sums, not the rows
@@ -110,22 +123,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int64_t units = static_cast<int64_t>(gridDim.x / p.cluster) * p.groups;
   const uint32_t step = blockDim.x * 16;
   const uint32_t ring = smem_addr(ring_raw);
-  const int mine = (p.octets < p.H / 8 - rank * p.octets ? p.octets : p.H / 8 - rank * p.octets);
-  const Slot<TY> slot_y(threadIdx.x, lane, in_cta, mine);
-  const Slot<TH> slot_h(threadIdx.x, lane, in_cta, mine);
-  constexpr int R = kBwdRows<TY, TH, POST, AFF, GATE>;
-  constexpr int kStages = kBwdStages<TY, TH, POST, AFF, GATE>;
-  const uint32_t tail = step * kBwdPieces<TY, TH, POST, GATE>, stage = tail + kTailBytes;
+  constexpr int R = Shape::kRows;
+  constexpr int kStages = Shape::kStages;
+  const uint32_t per_octet = step * (Shape::kPiecesRow / NV);
+  const uint32_t tail = per_octet * NV, stage = tail + kTailBytes;
   const uint32_t end = kStages * stage;
   const uint32_t my_tail = smem_addr(ring_raw) + tail + warp * kRowBytes;
   const uint32_t at_h = kPieces<TY> * step, at_dh = at_h + kPieces<TH> * step;
   const uint32_t at_y = at_dh + kPieces<TH> * step, at_gate = at_y + kPieces<TY> * step;
   constexpr bool kOwn = Slot<TY>::kOwn && Slot<TH>::kOwn;
   int64_t ahead = unit;
-  Walk<TY> dz_in(p.dz.p, p.dz.row, unit, oct), y_in(p.y.p, p.y.row, unit, oct);
-  Walk<TH> h_in(p.h_out.p, p.h_out.row, unit, oct);
-  Walk<TH> dh_in(p.dh_out.p, p.dh_out.row, unit, oct);
-  Walk<TY> gate_in(p.gate.p, p.gate.row, unit, oct);
+  Walk<TY> dz_in(p.dz.p, p.dz.row, unit, oct[0]), y_in(p.y.p, p.y.row, unit, oct[0]);
+  Walk<TH> h_in(p.h_out.p, p.h_out.row, unit, oct[0]);
+  Walk<TH> dh_in(p.dh_out.p, p.dh_out.row, unit, oct[0]);
+  Walk<TY> gate_in(p.gate.p, p.gate.row, unit, oct[0]);
   const bool token = GATE == kOneGate && p.gate_kind == FLCE_GATE_TOKEN;
   // address of a token's gate; its word, if all of that belongs to some token
   auto gate_of = [&](int64_t row) {
@@ -133,16 +144,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   auto fetch = [&](uint32_t s) {
     if (ahead < p.N) {
-      const uint32_t at = ring + s;
-      // one branch for all copies where a lane makes all of its own or none
-      if (!kOwn || in) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t at = ring + s + j * per_octet;
+        const Slot<TY> slot_y(threadIdx.x, lane, in_cta[j], mine);
+        const Slot<TH> slot_h(threadIdx.x, lane, in_cta[j], mine);
+        const int y_on = j * jump * 8 * Elem<TY>::kBytes, h_on = j * jump * 8 * Elem<TH>::kBytes;
+        // one branch for all copies where a lane makes all of its own or none
+        if (kOwn && !in[j]) continue;
         if (p.pre) {
-          slot_y.copy(at, dz_in.at, kOwn);
-          slot_h.copy(at + at_h, h_in.at, kOwn);
+          slot_y.copy(at, dz_in.at + y_on, kOwn);
+          slot_h.copy(at + at_h, h_in.at + h_on, kOwn);
         }
-        if (p.dh_out.p) slot_h.copy(at + at_dh, dh_in.at, kOwn);
-        if (kReadsY) slot_y.copy(at + at_y, y_in.at, kOwn);
-        if (GATE == kFullGate) slot_y.copy(at + at_gate, gate_in.at, kOwn);
+        if (p.dh_out.p) slot_h.copy(at + at_dh, dh_in.at + h_on, kOwn);
+        if (kReadsY) slot_y.copy(at + at_y, y_in.at + y_on, kOwn);
+        if (GATE == kFullGate) slot_y.copy(at + at_gate, gate_in.at + y_on, kOwn);
       }
       if (lane < 4) {
         if (lane < 2 ? POST : p.pre != 0)
@@ -167,76 +183,96 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   uint32_t s_in = 0, s_out = 0;
   for (; s_in < end - R * stage; s_in += stage) fetch(s_in);
-  auto gate_of_channel = [&]() {  // act(gate), 1 without one
+  auto gate_of_channel = [&](int j) {  // act(gate), 1 without one
     if (GATE != kChannelGate) return same_oct(1.f);
-    return gate_act_oct(p.act, param_octet<TY>(p.gate.p, pfp, oct, 1.f));
+    return gate_act_oct(p.act, param_octet<TY>(p.gate.p, pfp, oct[j], 1.f));
   };
   // w_post and b_post: times beta, and a where that is fixed
-  constexpr bool kShared = kBwdVectors<POST, AFF, GATE> > 0;
-  const uint32_t vectors = smem_addr(ring_raw) + end + in_cta * 16, plane = 32 * p.warps * 16;
-  Oct w_pre = zero_oct(), w_post = zero_oct(), b_post = zero_oct();
-  if (in) {
-    w_pre = param_octet<TY>(p.w_pre, pfp, oct, 1.f);
-    w_post = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f);
-    if (kFixed) scale_oct(w_post, gate_of_channel());
-    scale_oct(w_post, p.beta);
-    if (GATE == kFullGate && POST && AFF) {
-      b_post = param_octet<TY>(p.b_post, pfp, oct, 0.f);
-      scale_oct(b_post, p.beta);
+  constexpr bool kShared = Shape::kVectors > 0;
+  const uint32_t plane = NV * jump * 16;
+  const uint32_t vectors = smem_addr(ring_raw) + end + in_cta[0] * 16;
+  Oct w_pre = zero_oct(), w_post = zero_oct();
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    Oct b_post = zero_oct();
+    w_pre = w_post = zero_oct();
+    if (in[j]) {
+      w_pre = param_octet<TY>(p.w_pre, pfp, oct[j], 1.f);
+      w_post = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct[j], 1.f);
+      if (kFixed) scale_oct(w_post, gate_of_channel(j));
+      scale_oct(w_post, p.beta);
+      if (Shape::kVectors == 3) {
+        b_post = param_octet<TY>(p.b_post, pfp, oct[j], 0.f);
+        scale_oct(b_post, p.beta);
+      }
+    }
+    if (kShared && group == 0) {
+      const uint32_t to = vectors + j * jump * 16;
+      put_shared(to, plane, w_pre);
+      put_shared(to + 2 * plane, plane, w_post);
+      if (Shape::kVectors == 3) put_shared(to + 4 * plane, plane, b_post);
     }
   }
-  if (kShared) {
-    if (group == 0) {
-      put_shared(vectors, plane, w_pre);
-      put_shared(vectors + 2 * plane, plane, w_post);
-      if (GATE == kFullGate) put_shared(vectors + 4 * plane, plane, b_post);
-    }
-    __syncthreads();
-  }
-  auto pre_weight = [&]() { return kShared ? shared_oct(vectors, plane) : w_pre; };
-  auto post_weight = [&]() {
-    return kShared ? shared_oct(vectors + 2 * plane, plane) : w_post;
+  if (kShared) __syncthreads();
+  auto vector = [&](int k, int j) {
+    return shared_oct(vectors + 2 * k * plane + j * jump * 16, plane);
   };
+  auto pre_weight = [&](int j) { return kShared ? vector(0, j) : w_pre; };
+  auto post_weight = [&](int j) { return kShared ? vector(1, j) : w_post; };
   float scalar = 0.f;
   if (GATE == kOneGate && p.gate_kind == FLCE_GATE_SCALAR) scalar = one_element<TY>(p.gate.p, pfp, 0);
 
   // Sums over tokens: dz xh, dz, and yh du, du without the factor beta and a fixed gate's.
-  Oct s_pre = zero_oct(), s_bpre = zero_oct(), s_post = zero_oct(), s_bpost = zero_oct();
+  Oct s_pre[NV], s_bpre[NV], s_post[NV], s_bpost[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) s_pre[j] = s_bpre[j] = s_post[j] = s_bpost[j] = zero_oct();
   float s_one = 0.f;
-  Walk<TY> dy(p.dy.p, p.dy.row, unit, oct), dgate(p.dgate.p, p.dgate.row, unit, oct);
-  Walk<TH> dh(p.dh.p, p.dh.row, unit, oct);
+  Walk<TY> dy(p.dy.p, p.dy.row, unit, oct[0]), dgate(p.dgate.p, p.dgate.row, unit, oct[0]);
+  Walk<TH> dh(p.dh.p, p.dh.row, unit, oct[0]);
   const GateSlope slope(p.act);
   for (int64_t row = unit; row < p.N; row += R * units) {
 #pragma unroll
     for (int q = 0; q < R; ++q) fetch(s_in + q * stage);
     s_in = s_in + R * stage == end ? 0 : s_in + R * stage;
-    bool there[R];  // this thread has an octet of the row
-#pragma unroll
-    for (int q = 0; q < R; ++q) there[q] = in && (q == 0 || row + q * units < p.N);
+    auto there = [&](int q, int j) { return in[j] && (q == 0 || row + q * units < p.N); };
     copies_wait<kStages - R>();
     __syncwarp();  // lanes read what others copied
 
     Oct dz, xh, e, yh, a = zero_oct();
     float one = 0.f;  // act(gate) of gates with one value; `a` of those per element
-    float mean_y, r_y, mean_h, r_h, rs_y[R], rs_h[R];
-    // row q's dz, xh, dh' and yh; a second time where two rows are in hand, which takes
-    // fewer registers than keeping them
-    auto read = [&](int q, bool again) {
-      const uint32_t at = ring + s_out + q * stage, row_at = my_tail + s_out + q * stage;
-      if (again) {  // two rows are taken of RMS norms only
-        mean_y = mean_h = 0.f;
-        r_y = rs_y[q];
-        r_h = rs_h[q];
-      } else {
+    float mean_y = 0.f, r_y = 1.f, mean_h = 0.f, r_h = 0.f, rs_y[R] = {}, rs_h[R] = {};
+    // dz, xh, dh' and yh of row q's octet j; a second time where two are in hand, which
+    // takes fewer registers than keeping them
+    const Slot<TY> slot_y(threadIdx.x, lane, 0, 0);
+    const Slot<TH> slot_h(threadIdx.x, lane, 0, 0);
+    auto read = [&](int q, int j, bool again) {
+      const uint32_t at = ring + s_out + q * stage + j * per_octet;
+      const uint32_t row_at = my_tail + s_out + q * stage;
+      if (again) {
+        if (R > 1) {  // of RMS norms
+          r_y = rs_y[q];
+          r_h = rs_h[q];
+        }
+      } else if (j == 0) {
         const uint4 t = ld_shared16(row_at);
-        mean_y = __uint_as_float(t.x);
+        mean_y = AFF ? __uint_as_float(t.x) : 0.f;
         rs_y[q] = r_y = __uint_as_float(t.y);
-        mean_h = __uint_as_float(t.z);
+        mean_h = AFF ? __uint_as_float(t.z) : 0.f;
         rs_h[q] = r_h =
             p.pre && (q == 0 || row + q * units < p.N) ? __uint_as_float(t.w) : 0.f;
+        if (GATE == kOneGate) {
+          float g = scalar;
+          if (token) {
+            const uint32_t w = ld_shared4(row_at + 16);
+            const bool upper = Elem<TY>::kBytes == 2 &&
+                               (reinterpret_cast<uintptr_t>(gate_of(row + q * units)) & 2);
+            g = element_value<TY>(upper ? w >> 16 : w, false);
+          }
+          one = gate_act(p.act, g);
+        }
       }
       dz = xh = e = yh = a = zero_oct();
-      if (there[q]) {
+      if (there(q, j)) {
         if (p.pre) {
           dz = slot_y.read(at);
           xh = slot_h.read(at + at_h);
@@ -251,18 +287,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int i = 0; i < 4; ++i)
             yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-mean_y)) : yh.p[i], pair(r_y));
         }
-        if (GATE == kFullGate)
-          a = gate_act_each(p.act, slot_y.read(at + at_gate));
-      }
-      if (GATE == kOneGate) {
-        float g = scalar;
-        if (token) {
-          const uint32_t w = ld_shared4(row_at + 16);
-          const bool upper = Elem<TY>::kBytes == 2 &&
-                             (reinterpret_cast<uintptr_t>(gate_of(row + q * units)) & 2);
-          g = element_value<TY>(upper ? w >> 16 : w, false);
-        }
-        one = gate_act(p.act, g);
+        if (GATE == kFullGate) a = gate_act_each(p.act, slot_y.read(at + at_gate));
       }
     };
     // Sums of a row: g xh, [g]; and with a post-norm or a gate of one value, with w for
@@ -272,27 +297,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     float s[R * K];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      read(q, false);
-      const Oct wp = pre_weight(), wq = post_weight();
       float2 v[K];
 #pragma unroll
       for (int k = 0; k < K; ++k) v[k] = pair(0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 g = mul2(dz.p[i], wp.p[i]);
-        v[0] = mad2(g, xh.p[i], v[0]);
-        e.p[i] = mad2(pair(r_h), g, e.p[i]);
-        if (AFF) v[K - 1] = plus2(v[K - 1], g);
-        if (kSumsY) {
-          const float2 w = GATE == kFullGate ? mul2(a.p[i], wq.p[i]) : wq.p[i];
-          const float2 wy = mul2(w, yh.p[i]);
-          v[1] = mad2(wy, e.p[i], v[1]);
-          v[2] = mad2(wy, xh.p[i], v[2]);
-          if (AFF) v[3] = plus2(v[3], wy);
-          if (AFF && POST) {
-            v[4] = mad2(w, e.p[i], v[4]);
-            v[5] = plus2(v[5], w);
-            v[6] = mad2(w, xh.p[i], v[6]);
+      for (int j = 0; j < NV; ++j) {
+        read(q, j, false);
+        const Oct wp = pre_weight(j), wq = post_weight(j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 g = mul2(dz.p[i], wp.p[i]);
+          v[0] = mad2(g, xh.p[i], v[0]);
+          e.p[i] = mad2(pair(r_h), g, e.p[i]);
+          if (AFF) v[K - 1] = plus2(v[K - 1], g);
+          if (kSumsY) {
+            const float2 w = GATE == kFullGate ? mul2(a.p[i], wq.p[i]) : wq.p[i];
+            const float2 wy = mul2(w, yh.p[i]);
+            v[1] = mad2(wy, e.p[i], v[1]);
+            v[2] = mad2(wy, xh.p[i], v[2]);
+            if (AFF) v[3] = plus2(v[3], wy);
+            if (AFF && POST) {
+              v[4] = mad2(w, e.p[i], v[4]);
+              v[5] = plus2(v[5], w);
+              v[6] = mad2(w, xh.p[i], v[6]);
+            }
           }
         }
       }
@@ -307,75 +335,80 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       __syncwarp();
     }
 
+    constexpr bool kAgain = R > 1 || NV > 1;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      if (R > 1) {
-        read(q, true);
-        if (!kOwn && q == R - 1) __syncwarp();  // as above
-      }
-      const float m2 = r_h * s[q * K] * p.inv_h;
-      const float m1 = AFF && layer ? r_h * s[q * K + K - 1] * p.inv_h : 0.f;
-      // sum w yh dt: with a gate of one value its gradient, and dy's second mean
-      float wyd = 0.f, c1 = 0.f, c2 = 0.f;
-      if (kSumsY) wyd = s[q * K + 1] - m2 * s[q * K + 2] - (AFF ? m1 * s[q * K + 3] : 0.f);
-      if (POST) {
-        c2 = r_y * p.inv_h * wyd;
-        if (AFF && layer)
-          c1 = r_y * p.inv_h * (s[q * K + 4] - m2 * s[q * K + 6] - m1 * s[q * K + 5]);
-      }
-      if (GATE == kOneGate) {
-        c1 *= one;
-        c2 *= one;
-      }
-      const Oct wp = R > 1 ? pre_weight() : zero_oct(), wq = post_weight();
-      const Oct bq = GATE == kFullGate && kShared
-                         ? shared_oct(vectors + 4 * plane, plane)
-                         : zero_oct();
-      Oct dg = zero_oct();
+      float c1 = 0.f, c2 = 0.f, m1 = 0.f, m2 = 0.f, wyd = 0.f;
+      Oct dt_b = zero_oct();  // sum b_post dt of this thread
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (R > 1) e.p[i] = mad2(pair(r_h), mul2(dz.p[i], wp.p[i]), e.p[i]);
-        float2 dt = mad2(pair(-m2), xh.p[i], e.p[i]);
-        if (AFF) dt = plus2(dt, pair(-m1));
-        s_pre.p[i] = mad2(dz.p[i], xh.p[i], s_pre.p[i]);
-        if (AFF) s_bpre.p[i] = plus2(s_bpre.p[i], dz.p[i]);
-        // du over beta, or beta a where that is fixed
-        float2 du = dt;
-        if (GATE == kOneGate) du = mul2(pair(one), dt);
-        if (GATE == kFullGate) {
-          du = mul2(a.p[i], dt);
-          // beta u: w_post is times beta, and beta itself without a post-norm
-          const float2 u = POST && AFF ? mad2(yh.p[i], wq.p[i], bq.p[i])
-                                       : mul2(yh.p[i], wq.p[i]);
-          dg.p[i] = mul2(mul2(slope(a.p[i]), u), dt);
+      for (int j = 0; j < NV; ++j) {
+        if (kAgain) {
+          read(q, j, true);
+          if (!kOwn && q == R - 1 && j == NV - 1) __syncwarp();  // as above
         }
-        if (POST || GATE == kChannelGate) s_post.p[i] = mad2(yh.p[i], du, s_post.p[i]);
-        if (POST && AFF) s_bpost.p[i] = plus2(s_bpost.p[i], du);
-        float2 gy = mul2(wq.p[i], du);
-        if (POST) {
-          gy = mad2(pair(-c2), yh.p[i], mul2(pair(r_y), gy));
-          if (AFF) gy = plus2(gy, pair(-c1));
+        if (j == 0) {
+          m2 = r_h * s[q * K] * p.inv_h;
+          m1 = AFF && layer ? r_h * s[q * K + K - 1] * p.inv_h : 0.f;
+          // sum w yh dt: with a gate of one value its gradient, and dy's second mean
+          if (kSumsY) wyd = s[q * K + 1] - m2 * s[q * K + 2] - (AFF ? m1 * s[q * K + 3] : 0.f);
+          if (POST) {
+            c2 = r_y * p.inv_h * wyd;
+            if (AFF && layer)
+              c1 = r_y * p.inv_h * (s[q * K + 4] - m2 * s[q * K + 6] - m1 * s[q * K + 5]);
+          }
+          if (GATE == kOneGate) {
+            c1 *= one;
+            c2 *= one;
+          }
         }
-        e.p[i] = gy;                        // dy
-        a.p[i] = dt;
-        xh.p[i] = mul2(pair(p.alpha), dt);  // dh
-      }
-      if (there[q]) {
-        dy.put(to_octet(TY{}, e), p.wide);
-        if (p.dh.p) dh.put(to_octet(TH{}, xh), p.wide);
-        if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg), p.wide);
+        const Oct wp = kAgain ? pre_weight(j) : zero_oct(), wq = post_weight(j);
+        const Oct bq = Shape::kVectors == 3 ? vector(2, j) : zero_oct();
+        Oct dg = zero_oct();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (kAgain) e.p[i] = mad2(pair(r_h), mul2(dz.p[i], wp.p[i]), e.p[i]);
+          float2 dt = mad2(pair(-m2), xh.p[i], e.p[i]);
+          if (AFF) dt = plus2(dt, pair(-m1));
+          s_pre[j].p[i] = mad2(dz.p[i], xh.p[i], s_pre[j].p[i]);
+          if (AFF) s_bpre[j].p[i] = plus2(s_bpre[j].p[i], dz.p[i]);
+          // du over beta, or beta a where that is fixed
+          float2 du = dt;
+          if (GATE == kOneGate) du = mul2(pair(one), dt);
+          if (GATE == kFullGate) {
+            du = mul2(a.p[i], dt);
+            // beta u: w_post is times beta, and beta itself without a post-norm
+            const float2 u = Shape::kVectors == 3 ? mad2(yh.p[i], wq.p[i], bq.p[i])
+                                                  : mul2(yh.p[i], wq.p[i]);
+            dg.p[i] = mul2(mul2(slope(a.p[i]), u), dt);
+          }
+          if (POST || GATE == kChannelGate) s_post[j].p[i] = mad2(yh.p[i], du, s_post[j].p[i]);
+          if (POST && AFF) s_bpost[j].p[i] = plus2(s_bpost[j].p[i], du);
+          float2 gy = mul2(wq.p[i], du);
+          if (POST) {
+            gy = mad2(pair(-c2), yh.p[i], mul2(pair(r_y), gy));
+            if (AFF) gy = plus2(gy, pair(-c1));
+          }
+          e.p[i] = gy;                        // dy
+          if (GATE == kOneGate) a.p[i] = dt;
+          xh.p[i] = mul2(pair(p.alpha), dt);  // dh
+        }
+        const int y_on = j * jump * 8 * Elem<TY>::kBytes, h_on = j * jump * 8 * Elem<TH>::kBytes;
+        if (there(q, j)) {
+          dy.put(to_octet(TY{}, e), p.wide, y_on);
+          if (p.dh.p) dh.put(to_octet(TH{}, xh), p.wide, h_on);
+          if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg), p.wide, y_on);
+          if (GATE == kOneGate && POST && AFF && p.b_post) {
+            dt_b = param_octet<TY>(p.b_post, pfp, oct[j], 0.f);
+            scale_oct(dt_b, a);
+          }
+        }
       }
       dy.at += p.dy.step;
       dh.at += p.dh.step;
       if (GATE == kFullGate) dgate.at += p.dgate.step;
       if (GATE == kOneGate) {
-        if (POST && p.b_post) {  // u has a part beside w yh
-          float d[1] = {0.f};
-          if (there[q]) {
-            Oct b = param_octet<TY>(p.b_post, pfp, oct, 0.f);
-            scale_oct(b, a);
-            d[0] = p.beta * sum_oct(b);
-          }
+        if (POST && AFF && p.b_post) {  // u has a part beside w yh
+          float d[1] = {p.beta * sum_oct(dt_b)};
           sums.add(d);
           more.add(d);
           wyd += d[0];
@@ -383,60 +416,64 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         wyd *= gate_slope(p.act, one);
         if (p.gate_kind == FLCE_GATE_SCALAR)
           s_one += wyd;
-        else if (in_cta == 0 && rank == 0)
+        else if (in_cta[0] == 0 && rank == 0)
           store_element(TY{}, p.dgate.p, (row + q * units) * p.dgate.row, wyd);
       }
     }
     s_out = s_out + R * stage == end ? 0 : s_out + R * stage;
   }
 
-  auto put = [&](float* part, const Oct& o) {
-    if (part && in) store_octet<float>(part + unit * p.H, oct, o);
-  };
-  put(p.part[0], s_pre);
-  if (AFF) put(p.part[1], s_bpre);
-  if (kFixed && kReadsY && in) {
-    Oct a = gate_of_channel();
-    if (GATE == kChannelGate) {
-      // dgate = slope (w_post sum yh dt + b_post sum dt)
-      Oct f = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct, 1.f);
-      scale_oct(f, s_post);
-      if (POST && AFF) {
-        b_post = param_octet<TY>(p.b_post, pfp, oct, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f.p[i] = mad2(b_post.p[i], s_bpost.p[i], f.p[i]);
+  for (int j = 0; j < NV; ++j) {
+    auto put = [&](float* part, const Oct& o) {
+      if (part && in[j]) store_octet<float>(part + unit * p.H, oct[j], o);
+    };
+    put(p.part[0], s_pre[j]);
+    if (AFF) put(p.part[1], s_bpre[j]);
+    if (kFixed && kReadsY && in[j]) {
+      const Oct a = gate_of_channel(j);
+      if (GATE == kChannelGate) {
+        // dgate = slope (w_post sum yh dt + b_post sum dt)
+        Oct f = param_octet<TY>(POST ? p.w_post : nullptr, pfp, oct[j], 1.f);
+        scale_oct(f, s_post[j]);
+        if (POST && AFF) {
+          const Oct b = param_octet<TY>(p.b_post, pfp, oct[j], 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f.p[i] = mad2(b.p[i], s_bpost[j].p[i], f.p[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f.p[i] = mul2(f.p[i], make_float2(p.beta * gate_slope(p.act, a.p[i].x),
+                                            p.beta * gate_slope(p.act, a.p[i].y)));
+        put(p.part[4], f);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        f.p[i] = mul2(f.p[i], make_float2(p.beta * gate_slope(p.act, a.p[i].x),
-                                          p.beta * gate_slope(p.act, a.p[i].y)));
-      put(p.part[4], f);
+      scale_oct(s_post[j], a);
+      scale_oct(s_bpost[j], a);
     }
-    scale_oct(s_post, a);
-    scale_oct(s_bpost, a);
+    scale_oct(s_post[j], p.beta);
+    scale_oct(s_bpost[j], p.beta);
+    if (POST) put(p.part[2], s_post[j]);
+    if (POST && AFF) put(p.part[3], s_bpost[j]);
   }
-  scale_oct(s_post, p.beta);
-  scale_oct(s_bpost, p.beta);
-  if (POST) put(p.part[2], s_post);
-  if (POST && AFF) put(p.part[3], s_bpost);
-  if (GATE == kOneGate && p.part[4] && in_cta == 0 && rank == 0) p.part[4][unit] = s_one;
+  if (GATE == kOneGate && p.part[4] && in_cta[0] == 0 && rank == 0) p.part[4][unit] = s_one;
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while another writes to its slots
 }
 
-template <class TY, class TH, bool POST, bool AFF, int GATE>
-cudaError_t launch_bwd(NormParams p, int64_t parts, cudaStream_t s) {
+// With parts == 0, sets p.fit, the clusters that run at once: of four CTAs fewer than the SMs
+// would make, as a cluster stays within one of the device's processor clusters.
+template <class TY, class TH, bool POST, bool AFF, int GATE, int NV>
+cudaError_t launch_bwd_nv(NormParams& p, int64_t parts, cudaStream_t s) {
+  using Shape = BwdShape<TY, TH, POST, AFF, GATE, NV>;
   static SmemLimit limit;
   const int threads = 32 * p.warps * p.groups;
-  const int vectors = kBwdVectors<POST, AFF, GATE> * 32 * p.warps * 32;
-  const int ring = (threads * 16 * kBwdPieces<TY, TH, POST, GATE> + static_cast<int>(kTailBytes)) *
-                   kBwdStages<TY, TH, POST, AFF, GATE>;
-  const auto kernel = resnorm_bwd_kernel<TY, TH, POST, AFF, GATE>;
-  const cudaError_t e = limit.raise(kernel, kSmemPerSm);
+  const int vectors = Shape::kVectors * NV * 32 * p.warps * 32;
+  const int ring = (threads * 16 * Shape::kPiecesRow + static_cast<int>(kTailBytes)) * Shape::kStages;
+  const auto kernel = resnorm_bwd_kernel<TY, TH, POST, AFF, GATE, NV>;
+  cudaError_t e = limit.raise(kernel, kSmemPerSm);
   if (e != cudaSuccess) return e;
-  set_steps(p, parts, Elem<TY>::kBytes, Elem<TH>::kBytes);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(parts / p.groups * p.cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>((parts ? parts / p.groups : 1) * p.cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(ring + vectors);
   cfg.stream = s;
@@ -446,11 +483,64 @@ cudaError_t launch_bwd(NormParams p, int64_t parts, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (parts == 0) {
+    p.fit = p.sms;
+    if (p.cluster == 1) return cudaSuccess;
+    // of a CTA at its largest, so that the order of the sums does not go by earlier calls
+    cfg.blockDim = dim3(kBwdThreads);
+    cfg.dynamicSmemBytes = kSmemPerSm;
+    static std::atomic<int> known[64][2];  // by device and size
+    int dev = 0, n = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    std::atomic<int>& at = known[dev & 63][p.cluster == 4];
+    n = at.load(std::memory_order_relaxed);
+    if (n == 0) {
+      if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+      if (n < 1) n = 1;
+      at.store(n, std::memory_order_relaxed);
+    }
+    p.fit = n;
+    return cudaSuccess;
+  }
+  set_steps(p, parts, Elem<TY>::kBytes, Elem<TH>::kBytes);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Warps of 16 that are busy with rows of `octets` octets, NV of them a thread.
+inline int busy_warps(int octets, int nv) {
+  const int warps = (octets + 32 * nv - 1) / (32 * nv);
+  return kMaxRowWarps / warps * warps;
+}
+
+// The launch's shape: two octets a thread where that spares a cluster (4096 x 8192: 75 us, 104
+// with a cluster of two) or keeps half as many warps again busy (16000 x 2056: 9 of 16 with
+// one, 118 us; 15 with two, 96).
+inline void plan_bwd(NormParams& p, bool two) {
+  const int octets = p.H / 8;
+  const int nv = two && (octets > 32 * kMaxRowWarps ||
+                         2 * busy_warps(octets, 2) >= 3 * busy_warps(octets, 1))
+                     ? 2
+                     : 1;
+  const int most = 32 * kMaxRowWarps * nv;
+  p.nv = nv;
+  p.cluster = octets <= most ? 1 : octets <= 2 * most ? 2 : 4;
+  p.octets = (octets + p.cluster - 1) / p.cluster;
+  p.warps = (p.octets + 32 * nv - 1) / (32 * nv);
+  p.groups = kMaxRowWarps / p.warps;
+}
+
+// parts == 0: sets the launch's shape only.
+template <class TY, class TH, bool POST, bool AFF, int GATE>
+cudaError_t launch_bwd(NormParams& p, int64_t parts, cudaStream_t s) {
+  constexpr bool kTwo = BwdShape<TY, TH, POST, AFF, GATE, 2>::kPossible;
+  if (parts == 0) plan_bwd(p, kTwo);
+  if constexpr (kTwo)
+    if (p.nv == 2) return launch_bwd_nv<TY, TH, POST, AFF, GATE, 2>(p, parts, s);
+  return launch_bwd_nv<TY, TH, POST, AFF, GATE, 1>(p, parts, s);
+}
+
 template <class TY, class TH, bool POST, bool AFF>
-cudaError_t launch_bwd_gate(const NormParams& p, int64_t parts, cudaStream_t s) {
+cudaError_t launch_bwd_gate(NormParams& p, int64_t parts, cudaStream_t s) {
   switch (p.gate_kind) {
     case FLCE_GATE_NONE:
       return launch_bwd<TY, TH, POST, AFF, kNoGate>(p, parts, s);
@@ -464,13 +554,12 @@ cudaError_t launch_bwd_gate(const NormParams& p, int64_t parts, cudaStream_t s) 
 }
 
 template <class TY, class TH>
-cudaError_t launch_bwd_types(const NormParams& p, int64_t parts, cudaStream_t s) {
-  const bool aff = p.layer || p.b_post || p.part[1] || p.part[3];
+cudaError_t launch_bwd_types(NormParams& p, int64_t parts, cudaStream_t s) {
   if (p.post)
-    return aff ? launch_bwd_gate<TY, TH, true, true>(p, parts, s)
-               : launch_bwd_gate<TY, TH, true, false>(p, parts, s);
-  return aff ? launch_bwd_gate<TY, TH, false, true>(p, parts, s)
-             : launch_bwd_gate<TY, TH, false, false>(p, parts, s);
+    return p.biased ? launch_bwd_gate<TY, TH, true, true>(p, parts, s)
+                    : launch_bwd_gate<TY, TH, true, false>(p, parts, s);
+  return p.biased ? launch_bwd_gate<TY, TH, false, true>(p, parts, s)
+                  : launch_bwd_gate<TY, TH, false, false>(p, parts, s);
 }
 
 }  // namespace flce

@@ -6,7 +6,7 @@ namespace flce {
 cudaError_t launch_resnorm_fwd_fp32(const NormParams& p, int sms, cudaStream_t s) {
   return launch_fwd_types<float, float>(p, sms, s);
 }
-cudaError_t launch_resnorm_bwd_fp32(const NormParams& p, int64_t parts, cudaStream_t s) {
+cudaError_t launch_resnorm_bwd_fp32(NormParams& p, int64_t parts, cudaStream_t s) {
   return launch_bwd_types<float, float>(p, parts, s);
 }
 }  // namespace flce

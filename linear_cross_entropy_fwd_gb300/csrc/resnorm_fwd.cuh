@@ -95,11 +95,16 @@ __device__ __forceinline__ void normalise(Oct (&x)[R][NV], const bool (&in)[NV],
   }
 }
 
+// Biases wait in shared memory behind the ring: read again from where they are, they took
+// twice the time of all the rest (8192 x 4096, layer norms on both sides: 97 us).
+template <int NV, bool FULL>
+constexpr bool kBiasShared = NV <= 2 && !FULL;
 // Stages of the ring: a row's y, h and, FULL, a gate per element.
 template <class TY, class TH, int NV, bool FULL>
-constexpr int kFwdStages = ring_stages(NV * (kPieces<TY> * (FULL ? 2 : 1) + kPieces<TH>),
-                                       kFwdThreads,
-                                       kSmemPerSm - (NV == 4 && !FULL ? kMaxH * 4 : 0), 6);
+constexpr int kFwdStages = ring_stages(
+    NV * (kPieces<TY> * (FULL ? 2 : 1) + kPieces<TH>), kFwdThreads,
+    kSmemPerSm - (kBiasShared<NV, FULL> ? 2 * NV * kFwdThreads * 32 : NV == 4 && !FULL ? kMaxH * 4 : 0),
+    6);
 // Rows that a group takes at a time: two share the instructions around them and the
 // exchanges of their sums (8192 x 4096 in bf16 with both norms: 55 us with one).
 template <class TY, class TH, int NV, bool FULL>
@@ -163,33 +168,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   for (int i = threadIdx.x; i < kMaxRowWarps * 2 * kMaxSums * kMaxRowWarps; i += blockDim.x)
     (&slots[0][0][0][0])[i] = 0.f;
-  // What multiplies n(y) whatever the row: beta and a gate per channel, and the weight
-  // where no bias is added before them.  A thread keeps its octets', and the other norm's
-  // weight; of the longest rows it waits in shared memory behind the ring or, where gates
-  // per element need that room, is read again.
-  auto factor = [&](int o) {
-    Oct f = param_octet<TY>(p.b_post ? nullptr : p.w_post, pfp, o, 1.f);
-    if (p.gate_kind == FLCE_GATE_CHANNEL)
+  // What multiplies n(y) whatever the row: the weight, beta and a gate per channel; and what
+  // is added, likewise (0 without a bias).  A thread keeps its octets' factors, and the other
+  // norm's weights; of the longest rows they wait in shared memory behind the ring or, where
+  // gates per element need that room, are read again.
+  auto factor = [&](const void* w, float missing, int o) {
+    Oct f = param_octet<TY>(w, pfp, o, missing);
+    if (!FULL && p.gate_kind == FLCE_GATE_CHANNEL)
       scale_oct(f, gate_act_oct(p.act, param_octet<TY>(p.gate.p, pfp, o, 1.f)));
     scale_oct(f, p.beta);
     return f;
   };
-  constexpr bool kKeep = NV <= 2;
+  constexpr bool kKeep = NV <= 2, kBias = kBiasShared<NV, FULL>;
   const uint32_t factors = smem_addr(ring_raw) + end;
+  const uint32_t plane = NV * jump * 16;
+  const uint32_t biases = factors + oct[0] * 16;  // two planes each: b_post, b_pre
   Oct c[kKeep ? NV : 1], w_pre[kKeep ? NV : 1];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     if (kKeep) {
-      c[j] = in[j] ? factor(oct[j]) : zero_oct();
+      c[j] = in[j] ? factor(p.w_post, 1.f, oct[j]) : zero_oct();
       w_pre[j] = in[j] ? param_octet<TY>(p.w_pre, pfp, oct[j], 1.f) : zero_oct();
     } else if (!FULL && in[j]) {
-      store_octet<float>(ring_raw + end, oct[j], factor(oct[j]));  // read by this thread only
+      store_octet<float>(ring_raw + end, oct[j], factor(p.w_post, 1.f, oct[j]));  // its own
+    }
+    if (kBias && group == 0 && in[j]) {
+      if (p.b_post) put_shared(biases + j * jump * 16, plane, factor(p.b_post, 0.f, oct[j]));
+      if (p.b_pre)
+        put_shared(biases + 2 * plane + j * jump * 16, plane,
+                   param_octet<TY>(p.b_pre, pfp, oct[j], 0.f));
     }
   }
   const bool token = p.gate_kind == FLCE_GATE_TOKEN;
   const bool one_gate = token || p.gate_kind == FLCE_GATE_SCALAR;
-  float one = 0.f;  // a gate with one value
-  if (p.gate_kind == FLCE_GATE_SCALAR) one = one_element<TY>(p.gate.p, pfp, 0);
+  // a gate with one value: its bits, a token's an iteration ahead (of the last row again
+  // behind it, as a branch would wait for what it loads)
+  uint32_t one[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) one[q] = 0;
+  auto read_gates = [&](int64_t row) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t at = row + q * rows < p.N ? row + q * rows : p.N - 1;
+      one[q] = element_bits<TY>(p.gate.p, false, at * p.gate.row);
+    }
+  };
+  if (token) read_gates(first);
+  float scalar = 0.f;
+  if (one_gate && !token) scalar = one_element<TY>(p.gate.p, pfp, 0);
   Walk<TH> h_out(p.h_out.p, p.h_out.row, first, oct[0]);
   Walk<TY> z(p.z.p, p.z.row, first, oct[0]);
   __syncthreads();
@@ -204,11 +230,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       there[q] = q == 0 || row + q * rows < p.N;
-      gate1[q] = one;
-      if (token && there[q])
-        gate1[q] = one_element<TY>(p.gate.p, false, (row + q * rows) * p.gate.row);
+      gate1[q] = token ? element_value<TY>(one[q], false) : scalar;
       mean_y[q] = r_y[q] = mean_h[q] = r_h[q] = 0.f;
     }
+    if (token) read_gates(row + R * rows);
     copies_wait<kStages - R>();
     __syncwarp();  // lanes read what others copied
     const Slot<TY> slot_y(threadIdx.x, lane, 0, 0);
@@ -232,15 +257,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         const uint32_t mine = at + q * stage + j * kPer * step;
         if (p.post) scale_oct(v, f[q]);
-        if (p.b_post) {
-          const Oct w = param_octet<TY>(p.w_post, pfp, oct[j], 1.f);
-          const Oct t = param_octet<TY>(p.b_post, pfp, oct[j], 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v.p[i] = mad2(v.p[i], w.p[i], t.p[i]);
-        }
         scale_oct(v, kKeep  ? c[kKeep ? j : 0]
-                     : FULL ? factor(oct[j])
+                     : FULL ? factor(p.w_post, 1.f, oct[j])
                             : shared_oct(factors + oct[j] * 32, 16));
+        if (p.b_post)
+          add_oct(v, kBias ? shared_oct(biases + j * jump * 16, plane)
+                           : factor(p.b_post, 0.f, oct[j]));
         if (FULL)
           scale_oct(v, gate_act_each(p.act, slot_y.read(mine + at_gate)));
         if (one_gate) scale_oct(v, gate_act(p.act, gate1[q]));
@@ -268,11 +290,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             scale_oct(v, f[q]);
             scale_oct(v, kKeep ? w_pre[kKeep ? j : 0]
                                : param_octet<TY>(p.w_pre, pfp, oct[j], 1.f));
-            if (p.b_pre) {
-              const Oct t = param_octet<TY>(p.b_pre, pfp, oct[j], 0.f);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v.p[i] = plus2(v.p[i], t.p[i]);
-            }
+            if (p.b_pre)
+              add_oct(v, kBias ? shared_oct(biases + 2 * plane + j * jump * 16, plane)
+                               : param_octet<TY>(p.b_pre, pfp, oct[j], 0.f));
           } else {
             v = zero_oct();
           }
@@ -313,7 +333,9 @@ cudaError_t launch(NormParams p, int sms, cudaStream_t s) {
   constexpr int kStages =
       kFwdStages<TY, TH, NV, FULL> / kFwdRows<TY, TH, NV, FULL> * kFwdRows<TY, TH, NV, FULL>;
   const int stage = threads * 16 * NV * (kPieces<TY> * (FULL ? 2 : 1) + kPieces<TH>);
-  const int factors = NV <= 2 || FULL ? 0 : p.H * 4;
+  const int factors = kBiasShared<NV, FULL> ? (p.b_post || p.b_pre ? 4 * NV * 32 * p.warps * 16 : 0)
+                      : NV == 4 && !FULL    ? p.H * 4
+                                            : 0;
   const auto kernel = resnorm_fwd_kernel<TY, TH, NV, LAYER, FULL>;
   const cudaError_t e = limit.raise(kernel, kSmemPerSm);
   if (e != cudaSuccess) return e;

@@ -71,6 +71,10 @@ __device__ __forceinline__ void scale_oct(Oct& x, float f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) x.p[i] = mul2(x.p[i], pair(f));
 }
+__device__ __forceinline__ void add_oct(Oct& x, const Oct& y) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.p[i] = plus2(x.p[i], y.p[i]);
+}
 __device__ __forceinline__ float sum_oct(const Oct& x) {
   const float2 t = plus2(plus2(x.p[0], x.p[1]), plus2(x.p[2], x.p[3]));
   return t.x + t.y;
