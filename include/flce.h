@@ -488,7 +488,7 @@ typedef enum flce_act {
  * dgate is required with a gate.  Sums over tokens are fp32, in an order that N, H, the
  * options and the device's number of SMs fix: the same call gives the same bits.
  * N == 0 makes the parameters' gradients 0.
- * Scratch: forward none, backward at most 608 fp32 rows of H per gradient of a parameter.
+ * Scratch: forward none; backward up to 32 KB per SM and gradient of a parameter.
  */
 typedef struct flce_resnorm {
   int64_t N, H;
@@ -569,8 +569,12 @@ FLCE_API int flce_ckpt_load(const void* ckpt, int64_t N, int64_t H, void* x, int
  *   dY [N, O] bf16, rows dY_row elements apart (a multiple of 8, at least O), 16-byte
  *   aligned; ckpt of [N, I]; dW [O, I] fp32, contiguous, 16-byte aligned.  O and I are
  *   multiples of 8, up to 2^20; N < 2^31.  opts->dtype must be FLCE_BF16.
- * Products are bf16, exact for the stored X, with fp32 sums in a fixed order.  N == 0 makes
- * dW 0, or leaves it when accumulate is set.
+ * Products are bf16, exact for the stored X.  Sums are fp32, in an order that N, O, I and the
+ * device's number of SMs fix; where they pass through the tensor core's accumulators, 2048
+ * tokens at most, each 16 tokens' sum is cut off, not rounded.  N == 0 makes dW 0, or leaves
+ * it when accumulate is set.
+ * Scratch: X in bf16, 2 N I bytes; and 256 KB per SM where the last tiles are shared out
+ * along the tokens (opts->workspace_used tells).
  */
 FLCE_API int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt, int64_t N,
                              int64_t O, int64_t I, float* dW, int32_t accumulate,

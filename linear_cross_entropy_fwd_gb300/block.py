@@ -254,32 +254,20 @@ def flce_resnorm_bwd(dz: torch.Tensor | None, dh_out: torch.Tensor | None, y: to
         dh = torch.empty(shape, dtype=st, device=dev)
     dga = _NONE
     dgate = None
-    if gk == GATE_SCALAR:
-        dgate = torch.empty((), dtype=torch.float32, device=dev)
-    elif gk > GATE_CHANNEL:
-        dgate = torch.empty(gate.shape, dtype=dt, device=dev)
+    if gk != GATE_NONE:
+        dgate = torch.empty(gate.shape, dtype=dt if gk > GATE_CHANNEL else torch.float32,
+                            device=dev)
         dga = dgate.data_ptr(), H if gk == GATE_FULL else 1
-    # gradients of the parameters, in one buffer
-    d = [w_post, b_post, w_pre, b_pre, gate if gk == GATE_CHANNEL else None]
-    n = sum(t is not None for t in d)
-    at = [0] * 5
-    if n:
-        sums = torch.empty((n, H), dtype=torch.float32, device=dev)
-        p, parts = sums.data_ptr(), iter(sums.unbind())
-        for i in range(5):
-            if d[i] is not None:
-                d[i], at[i] = next(parts), p
-                p += 4 * H
-    if gk == GATE_CHANNEL:
-        dgate, dga = d[4], (at[4], 0)
-    elif gk == GATE_SCALAR:
-        dga = dgate.data_ptr(), 0
+    one = (H,)  # (a tensor each: the views of a common one would take longer to make)
+    d = [None if t is None else torch.empty(one, dtype=torch.float32, device=dev)
+         for t in (w_post, b_post, w_pre, b_pre)]
+    at = [0 if t is None else t.data_ptr() for t in d]
     a = _pack(*head, *_rows("y", y, shape, dt, dev), 0, 0, *ga, *vecs,
               *_rows("h_out", h_out, shape, st, dev), _check_stats(stats, N, dev), 0, 0, 0,
               *_rows("dz", dz, shape, dt, dev), *_rows("dh_out", dh_out, shape, st, dev),
-              *_rows("dy", dy, shape, dt, dev), *_rows("dh", dh, shape, st, dev), *dga, *at[:4])
+              *_rows("dy", dy, shape, dt, dev), *_rows("dh", dh, shape, st, dev), *dga, *at)
     _call(lib.flce_resnorm_bwd, dev, dt, (a,), sync=sync, workspace=workspace, info=info)
-    return ResnormGrads(dy, dh, dgate, *d[:4])
+    return ResnormGrads(dy, dh, dgate, *d)
 
 
 def flce_ckpt_save(x: torch.Tensor, *, out: Checkpoint | None = None, sync: bool = False,

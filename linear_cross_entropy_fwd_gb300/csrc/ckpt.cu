@@ -70,11 +70,14 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
     ckpt_store_octet(p.c, codes + k * kThreads * 8, scales[k], o[k], v[k]);
 }
 
-// `clear`, optional, becomes 0.
+// With `clear`, which becomes 0, the next launch knows that it may start meanwhile; other
+// callers' may be anything.
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p) {
-  grid_launch_dependents();
-  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0;
+  if (p.clear) {
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0;
+  }
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * kOctets);
   Place at(first, p.padded);
   uint2 codes[kOctets];

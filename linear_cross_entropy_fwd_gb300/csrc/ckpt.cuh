@@ -117,7 +117,7 @@ __device__ __forceinline__ Oct ckpt_octet(const uint2& codes, uint32_t scale) {
 }
 
 // x [N, H] = the checkpoint; elements of 2 (bf16) or 4 bytes, rows x_row elements apart.
-// The next launch may start meanwhile.  `clear`, if not null, becomes 0.
+// `clear`, if not null, becomes 0, and the next launch may start meanwhile.
 cudaError_t launch_ckpt_load(const Ckpt& c, void* x, int64_t x_row, int64_t N, int64_t H, int elt,
                              int32_t* clear, cudaStream_t s);
 

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
   const uint32_t tmem_base = *tmem_base_slot;
   // The previous launch writes X and starts only when all before it is done: nothing but the
   // loads of X waits for it.
-  grid_launch_dependents();
+  if (p.whole < p.g.num_m_blk * p.g.num_n_blk) grid_launch_dependents();  // the join is next
 
   Items items(p, unit);
   Item it;

@@ -46,6 +46,7 @@ struct NormParams {
   int32_t octets;      // of a row in each CTA of a cluster
   int32_t nv;          // octets of a thread
   int32_t sms, fit;    // of the device; CTAs or clusters that run at once
+  int32_t sums_follow; // the next launch is launch_resnorm_sums
   float* part[5];      // sums over tokens of dw_pre, db_pre, dw_post, db_post, dgate:
                        // [parts][H], or [parts] for a scalar gate; null: not wanted
 };

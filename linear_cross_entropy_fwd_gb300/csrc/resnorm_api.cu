@@ -328,6 +328,7 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
     t.part[k] = p.part[k];
     t.out[k] = sums[k].p;
     t.width[k] = sums[k].width;
+    p.sums_follow = 1;
   }
   cudaError_t e = cudaSuccess;
   if (N > 0) e = rows_kernel(parts);

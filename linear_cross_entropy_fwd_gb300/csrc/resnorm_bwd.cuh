@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     (&slots[0][0][0][0])[i] = 0.f;
   __syncthreads();
   if (p.cluster > 1) cluster_sync();  // every CTA runs before its slots are written
-  grid_launch_dependents();  // the sums' CTAs take the SMs that this launch's leave
+  if (p.sums_follow) grid_launch_dependents();  // their CTAs take the SMs that this launch's leave
   using Shape = BwdShape<TY, TH, POST, AFF, GATE, NV>;
   // this thread's octets: of those of its CTA, and of the row
   const int jump = 32 * p.warps;
