@@ -11,10 +11,12 @@
 // sums a thread, and the tensor core goes on with the other accumulator meanwhile.  (Adding
 // the pieces to dW at L2 took a quarter of the time of the products.)
 //
-// The last tiles.  Tiles that do not fill a round of all pairs are shared out over all pairs
-// along the tokens, evenly; each pair's share of a tile goes to scratch and a second kernel
-// adds a tile's shares in order (8192 x 6144 x 4096: 4 of 384 tiles are left, which would be
-// a sixth round).  Where that gains less than it costs the last round stays as it is.
+// The last tiles.  Tiles that do not fill a round of all pairs are shared out along the
+// tokens, evenly; each pair's share of a tile goes to scratch and a second kernel adds a
+// tile's shares in order (8192 x 6144 x 4096: 4 of 384 tiles are left, a sixth round: 260 us
+// with it, 235 us shared).  Where that gains less than it costs the last round stays.
+#include <cmath>
+
 #include "ckpt.cuh"
 #include "epilogues.cuh"
 #include "host_util.h"
@@ -37,11 +39,12 @@ constexpr size_t kWgradSmem = 1024 + kStages * 2 * kOperandBytes + kStaging + SM
 struct WgradPlan {
   GemmGrid g;
   int32_t units;       // pairs
-  int32_t whole;       // tiles that one pair does from end to end; the rest is shared out
+  int32_t whole;       // tiles that one pair does from end to end
+  int32_t sharers;     // pairs that share the rest
   int32_t accumulate;
   int64_t O, I;
   float* dW;           // of the join
-  float* shares;       // [2 units][kTileM][BN]
+  float* shares;       // [2 sharers][kTileM][BN]
 };
 
 // A pair's next work: k-blocks k0 .. k1 of a tile, into dW or into its share `slot`.
@@ -52,7 +55,7 @@ struct Item {
 // First k-block (of those of all shared tiles, one after the other) of unit u's share.
 __host__ __device__ inline int64_t share_start(const WgradPlan& p, int u) {
   const int64_t all = static_cast<int64_t>(p.g.num_m_blk * p.g.num_n_blk - p.whole) * p.g.num_k_blk;
-  return all * u / p.units;
+  return u >= p.sharers ? all : all * u / p.sharers;
 }
 
 struct Items {
@@ -317,49 +320,52 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
   }
 }
 
-// dW of the shared tiles: each the sum of its shares, in ascending order of their tokens.
-constexpr int kJoinThreads = 256, kJoinRows = 4, kJoinAtOnce = 8;
+// dW of the shared tiles: each the sum of its shares, in ascending order of their tokens.  A
+// CTA has kJoinRows rows of a tile, a thread four columns of one, kJoinAtOnce loads in flight.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 64, kJoinAtOnce = 8;
+
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
 
 __global__ void __launch_bounds__(kJoinThreads)
     ckpt_wgrad_join_kernel(const __grid_constant__ WgradPlan p) {
-  // of the shared tiles' k-blocks, this tile's; u: the first unit with some of them
-  const int64_t t = blockIdx.x, k0 = t * p.g.num_k_blk, k1 = k0 + p.g.num_k_blk;
-  int u = static_cast<int>(t * p.units / (p.g.num_m_blk * p.g.num_n_blk - p.whole));
-  while (u > 0 && share_start(p, u) > k0) --u;
-  while (share_start(p, u + 1) <= k0) ++u;
-  int end = u + 1;
-  while (share_start(p, end) < k1) ++end;
-  const bool behind = share_start(p, u) < k0;  // unit u ends another tile first
+  // The units u .. end with some of this tile's k-blocks, and whether unit u ends another tile
+  // first: a few long divisions, by one thread.
+  __shared__ int found[3];
+  const int64_t t = blockIdx.y;  // of the shared tiles
+  if (threadIdx.x == 0) {
+    const int64_t shared = p.g.num_m_blk * p.g.num_n_blk - p.whole;
+    const int64_t k0 = t * p.g.num_k_blk, k1 = k0 + p.g.num_k_blk;
+    const int u = static_cast<int>(((k0 + 1) * p.sharers - 1) / (shared * p.g.num_k_blk));
+    const int end = static_cast<int>(((t + 1) * p.sharers + shared - 1) / shared);
+    const int64_t at = share_start(p, u);
+    found[0] = u;
+    found[1] = at == k0 && share_start(p, u + 1) >= k1 ? u : end;  // unit u did the whole tile
+    found[2] = at < k0;
+  }
+  __syncthreads();
+  const int u = found[0], end = found[1];
+  const bool behind = found[2];
   grid_dependency_wait();
-  if (end == u + 1 && !behind && share_start(p, end) >= k1) return;  // it did the whole tile
+  if (end == u) return;
   int mu, n_blk;
   tile_coords(p.g, p.whole + static_cast<int>(t), mu, n_blk);
-  const int col = (threadIdx.x & 63) * 4, row = blockIdx.y * kJoinRows + (threadIdx.x >> 6);
+  const int row = blockIdx.x * kJoinRows + (threadIdx.x >> 6), quad = threadIdx.x & 63;
   const int64_t at = mu * static_cast<int64_t>(kTileM) + row;
-  if (n_blk * BN + col >= p.I || at >= p.O) return;
-  float4* to = reinterpret_cast<float4*>(p.dW + at * p.I + n_blk * BN + col);
-  const float4* from = reinterpret_cast<const float4*>(p.shares + row * BN + col);
+  if (at >= p.O || n_blk * BN + 4 * quad >= p.I) return;
+  const float4* from = reinterpret_cast<const float4*>(p.shares) + row * (BN / 4) + quad;
   constexpr int64_t kSlot = kTileM * BN / 4;
-  float4 s = from[(2 * u + (behind ? 1 : 0)) * kSlot];
-  for (int w = u + 1; w < end; w += kJoinAtOnce) {
+  float4* to = reinterpret_cast<float4*>(p.dW + at * p.I + n_blk * BN + 4 * quad);
+  float4 s = p.accumulate ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = u; w < end; w += kJoinAtOnce) {
     float4 a[kJoinAtOnce];
 #pragma unroll
     for (int i = 0; i < kJoinAtOnce; ++i)
-      a[i] = w + i < end ? from[2 * (w + i) * kSlot] : make_float4(0.f, 0.f, 0.f, 0.f);
+      a[i] = w + i < end ? from[(2 * (w + i) + (w + i == u && behind ? 1 : 0)) * kSlot]
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kJoinAtOnce; ++i) {
-      s.x += a[i].x;
-      s.y += a[i].y;
-      s.z += a[i].z;
-      s.w += a[i].w;
-    }
-  }
-  if (p.accumulate) {
-    const float4 v = *to;
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+    for (int i = 0; i < kJoinAtOnce; ++i) add4(s, a[i]);
   }
   *to = s;
 }
@@ -399,8 +405,12 @@ int map_of(CUtensorMap* m, const void* p, CUtensorMapDataType t, int64_t cols, i
   return host_tensor_map(m, p, t, 2, dims, pitches, boxes, what);
 }
 
-// Whether the last tiles are shared out (they never make more shares than k-blocks): what idle pairs would lose (0.29 us for a k-block),
-// against writing and reading the shares (a launch of 4 us, and 3 bytes a picosecond).
+// Whether the last tiles are shared out, and among how many pairs: a k-block takes 0.29 us, a
+// share 0.18 us to be written and read (256 KB each way), the join a launch of 4 us.  So n
+// pairs take 0.29 K / n + 0.18 n for the K k-blocks of these tiles, least at
+// n = sqrt(0.29 K / 0.18).  One round, shared: 20000 x 1000 x 1000 (16 tiles) 168 -> 64 us,
+// 9768 x 184 x 424 (2 tiles) 68 -> 20; the last round only, 8192 x 4096 x 4096 (28 of 256
+// tiles) 178 -> 170.  With 0.06 in place of 0.18 65536 x 256 x 256 takes 41 us, not 34.
 WgradPlan plan(int64_t N, int64_t O, int64_t I, int units, bool accumulate) {
   WgradPlan p{};
   p.g.num_m_blk = static_cast<int32_t>((O + kTileM - 1) / kTileM);
@@ -411,11 +421,18 @@ WgradPlan plan(int64_t N, int64_t O, int64_t I, int units, bool accumulate) {
   p.accumulate = accumulate;
   p.units = units;
   const int tiles = p.g.num_m_blk * p.g.num_n_blk, left = tiles % units;
-  const double gain = 0.29 * p.g.num_k_blk * (1.0 - static_cast<double>(left) / units);
-  const double cost = 4.0 + 2.0 * (units + left) * kTileM * BN * 4 / 3e6;
-  const bool enough = static_cast<int64_t>(left) * p.g.num_k_blk >= units;
-  p.whole = left && enough && gain > cost ? tiles - left : tiles;
-  if (p.whole == tiles && tiles < units) p.units = tiles;
+  p.whole = tiles;
+  p.sharers = 1;
+  if (left) {
+    const double blocks = static_cast<double>(left) * p.g.num_k_blk;
+    int n = static_cast<int>(std::sqrt(0.29 * blocks / 0.18));
+    n = n < units ? n : units;
+    if (n > left && 0.29 * blocks / n + 0.18 * n + 4.0 < 0.29 * p.g.num_k_blk) {
+      p.whole = tiles - left;
+      p.sharers = n;
+    }
+  }
+  if (tiles < units) p.units = p.whole ? tiles : p.sharers;
   return p;
 }
 
@@ -439,8 +456,8 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int units, cudaStream_
 cudaError_t launch_join(const WgradPlan& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(p.g.num_m_blk * p.g.num_n_blk - p.whole),
-                     kTileM / kJoinRows);
+  cfg.gridDim =
+      dim3(kTileM / kJoinRows, static_cast<unsigned>(p.g.num_m_blk * p.g.num_n_blk - p.whole));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -467,7 +484,7 @@ extern "C" int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt,
   const WgradPlan all = plan(N, O, I, sms / 2, accumulate != 0);
   const bool shared = N > 0 && all.whole < all.g.num_m_blk * all.g.num_n_blk;
   const size_t x_bytes = round256(static_cast<size_t>(N) * static_cast<size_t>(I) * 2);
-  const int64_t share_rows = shared ? 2 * static_cast<int64_t>(all.units) * kTileM : 0;
+  const int64_t share_rows = shared ? 2 * static_cast<int64_t>(all.sharers) * kTileM : 0;
   StepCall call;
   if ((rc = call.begin(o, x_bytes + static_cast<size_t>(share_rows) * BN * 4,
                        N > 0 ? StepCall::kKernelClears : StepCall::kCleared)))
