@@ -65,7 +65,7 @@ cudaError_t launch_resnorm_fwd_mixed(const NormParams& p, int sms, cudaStream_t 
 cudaError_t launch_resnorm_fwd_fp32(const NormParams& p, int sms, cudaStream_t s);
 
 // With parts == 0, the launch's shape is set and nothing is run; else `parts` is the number of
-// rows of each of part[]: the grid's groups of warps.
+// rows of each of part[]: the grid's CTAs or clusters.
 cudaError_t launch_resnorm_bwd_bf16(NormParams& p, int64_t parts, cudaStream_t s);
 cudaError_t launch_resnorm_bwd_mixed(NormParams& p, int64_t parts, cudaStream_t s);
 cudaError_t launch_resnorm_bwd_fp32(NormParams& p, int64_t parts, cudaStream_t s);

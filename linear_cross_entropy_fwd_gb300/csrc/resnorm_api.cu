@@ -8,7 +8,7 @@
 namespace flce {
 namespace {
 
-constexpr int kSumLanes = 32, kSumRows = 16, kSumAtOnce = 5;
+constexpr int kSumLanes = 32, kSumRows = 16, kSumAtOnce = 10;
 
 // One thread row takes every kSumRows-th part, kSumAtOnce loads in flight, then the thread
 // rows are added in order.
@@ -312,7 +312,7 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
     const cudaError_t e = rows_kernel(0);
     if (e != cudaSuccess) return host_cuda_error(e, "resnorm_bwd");
     const int64_t want = (N + p.groups - 1) / p.groups;
-    parts = (want < p.fit ? want : p.fit) * p.groups;
+    parts = want < p.fit ? want : p.fit;
   }
   size_t at[5], bytes = 0;
   for (int k = 0; k < 5; ++k) {

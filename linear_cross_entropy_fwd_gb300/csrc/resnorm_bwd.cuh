@@ -2,8 +2,8 @@
 // translation unit per pair of types includes it.
 //
 // A thread has the same 8 columns of every row that its warps take, so that the sums over
-// tokens stay in its registers until the end, one fp32 row for each group of warps; a second
-// kernel adds those in a fixed order.  Rows of more than 4096 elements are shared by the
+// tokens stay in its registers until the end, one fp32 row for each CTA; a second kernel adds
+// those in a fixed order.  Rows of more than 4096 elements are shared by the
 // CTAs of a cluster for the same reason: 8 columns a thread is what 5 such sums leave room for.
 //
 // The two norms' sums would follow one another (the post-norm's need dt, dt needs the
@@ -72,7 +72,7 @@ struct BwdShape {
                                    !AFF && (GATE == kNoGate || GATE == kChannelGate);
   // Weights that wait in shared memory behind the ring instead of in registers: where a norm
   // after the block and its means or biases, a second row or a second octet need those.
-  static constexpr int kVectors = POST && AFF && GATE == kFullGate           ? 3
+  static constexpr int kVectors = POST && AFF && (GATE == kFullGate || GATE == kOneGate) ? 3
                                   : NV > 1 || (POST && AFF) || kTwoRows ? 2
                                                                              : 0;
   static constexpr int kFit =
@@ -83,6 +83,10 @@ struct BwdShape {
   static constexpr int kStages = kFit / kRows * kRows;
   // Two octets a thread: twice the sums over tokens in registers, and two stages.
   static constexpr bool kPossible = NV == 1 || (!(POST && AFF) && kStages >= 2);
+  // Sums over tokens that a thread has; the groups' are added where the ring was.
+  static constexpr int kTokenSums =
+      1 + AFF + POST + (POST && AFF) + (GATE == kChannelGate ? 1 : 0);
+  static_assert(!kPossible || kStages * kPiecesRow * 16 >= kTokenSums * NV * 32, "they fit");
 };
 
 // AFF: a mean or a bias is wanted.
@@ -91,6 +95,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     resnorm_bwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float slots[kMaxRowWarps][2][kMaxSums][kMaxRowWarps];
   __shared__ float cluster_slots[2][4][kMaxSums];
+  __shared__ float ones[kMaxRowWarps];
   extern __shared__ __align__(16) uint8_t ring_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = warp / p.warps;
@@ -220,13 +225,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   auto pre_weight = [&](int j) { return kShared ? vector(0, j) : w_pre; };
   auto post_weight = [&](int j) { return kShared ? vector(1, j) : w_post; };
   float scalar = 0.f;
-  if (GATE == kOneGate && p.gate_kind == FLCE_GATE_SCALAR) scalar = one_element<TY>(p.gate.p, pfp, 0);
+  if (GATE == kOneGate && !token) scalar = gate_act(p.act, one_element<TY>(p.gate.p, pfp, 0));
 
   // Sums over tokens: dz xh, dz, and yh du, du without the factor beta and a fixed gate's.
   Oct s_pre[NV], s_bpre[NV], s_post[NV], s_bpost[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) s_pre[j] = s_bpre[j] = s_post[j] = s_bpost[j] = zero_oct();
   float s_one = 0.f;
+  // Sum of w over a row, where w is the same in every row.
+  constexpr bool kSumW = POST && AFF && GATE != kFullGate;
+  float sum_w = 0.f;
+  if (kSumW) {
+    float t[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) t[0] += sum_oct(post_weight(j));
+    sums.add(t);
+    more.add(t);
+    sum_w = t[0];
+  }
+  // The gradient of a gate of one value has sum b_post dt in it, which needs the sums of its
+  // row: it is taken with the next row's.
+  constexpr bool kCarry = kSumW && GATE == kOneGate;
+  float carry = 0.f, wyd_before = 0.f, one_before = 0.f;
+  auto put_one = [&](int64_t row, float wyd, float act) {
+    if (!token)
+      s_one += wyd;
+    else if (in_cta[0] == 0 && rank == 0)
+      store_element(TY{}, p.dgate.p, row * p.dgate.row, wyd * gate_slope(p.act, act));
+  };
   Walk<TY> dy(p.dy.p, p.dy.row, unit, oct[0]), dgate(p.dgate.p, p.dgate.row, unit, oct[0]);
   Walk<TH> dh(p.dh.p, p.dh.row, unit, oct[0]);
   const GateSlope slope(p.act);
@@ -261,14 +287,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         rs_h[q] = r_h =
             p.pre && (q == 0 || row + q * units < p.N) ? __uint_as_float(t.w) : 0.f;
         if (GATE == kOneGate) {
-          float g = scalar;
+          one = scalar;
           if (token) {
             const uint32_t w = ld_shared4(row_at + 16);
             const bool upper = Elem<TY>::kBytes == 2 &&
                                (reinterpret_cast<uintptr_t>(gate_of(row + q * units)) & 2);
-            g = element_value<TY>(upper ? w >> 16 : w, false);
+            one = gate_act(p.act, element_value<TY>(upper ? w >> 16 : w, false));
           }
-          one = gate_act(p.act, g);
         }
       }
       dz = xh = e = yh = a = zero_oct();
@@ -291,7 +316,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     };
     // Sums of a row: g xh, [g]; and with a post-norm or a gate of one value, with w for
-    // beta [a] w_post: w yh e, w yh xh, [w yh], and for layer norms [w e, w, w xh].
+    // beta [a] w_post: w yh e, w yh xh, [w yh], and for layer norms [w e, w, w xh].  Where
+    // sum w is known, the row before's b_post dt takes its place.
     constexpr bool kSumsY = POST || GATE == kOneGate;
     constexpr int K = kSumsY ? (AFF ? 8 : 4) : (AFF ? 2 : 1);
     float s[R * K];
@@ -318,7 +344,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (AFF) v[3] = plus2(v[3], wy);
             if (AFF && POST) {
               v[4] = mad2(w, e.p[i], v[4]);
-              v[5] = plus2(v[5], w);
+              if (!kSumW) v[5] = plus2(v[5], w);
               v[6] = mad2(w, xh.p[i], v[6]);
             }
           }
@@ -327,6 +353,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
       for (int k = 0; k < K; ++k) s[q * K + k] = v[k].x + v[k].y;
     }
+    if (kCarry) s[5] = carry;
     // (the exchanges also see to it that all lanes have read what later copies overwrite)
     if (p.pre || kSumsY) {
       sums.add(s);
@@ -334,12 +361,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     } else {
       __syncwarp();
     }
+    if (kCarry && row != unit) put_one(row - units, wyd_before + s[5], one_before);
 
     constexpr bool kAgain = R > 1 || NV > 1;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float c1 = 0.f, c2 = 0.f, m1 = 0.f, m2 = 0.f, wyd = 0.f;
-      Oct dt_b = zero_oct();  // sum b_post dt of this thread
+      carry = kCarry ? 0.f : carry;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (kAgain) {
@@ -354,7 +382,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (POST) {
             c2 = r_y * p.inv_h * wyd;
             if (AFF && layer)
-              c1 = r_y * p.inv_h * (s[q * K + 4] - m2 * s[q * K + 6] - m1 * s[q * K + 5]);
+              c1 = r_y * p.inv_h * (s[q * K + 4] - m2 * s[q * K + 6] -
+                                      m1 * (kSumW ? sum_w : s[q * K + 5]));
           }
           if (GATE == kOneGate) {
             c1 *= one;
@@ -389,47 +418,64 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (AFF) gy = plus2(gy, pair(-c1));
           }
           e.p[i] = gy;                        // dy
-          if (GATE == kOneGate) a.p[i] = dt;
+          if (kCarry) a.p[i] = mul2(bq.p[i], dt);
           xh.p[i] = mul2(pair(p.alpha), dt);  // dh
         }
+        if (kCarry) carry += sum_oct(a);
         const int y_on = j * jump * 8 * Elem<TY>::kBytes, h_on = j * jump * 8 * Elem<TH>::kBytes;
         if (there(q, j)) {
           dy.put(to_octet(TY{}, e), p.wide, y_on);
           if (p.dh.p) dh.put(to_octet(TH{}, xh), p.wide, h_on);
           if (GATE == kFullGate) dgate.put(to_octet(TY{}, dg), p.wide, y_on);
-          if (GATE == kOneGate && POST && AFF && p.b_post) {
-            dt_b = param_octet<TY>(p.b_post, pfp, oct[j], 0.f);
-            scale_oct(dt_b, a);
-          }
         }
       }
       dy.at += p.dy.step;
       dh.at += p.dh.step;
       if (GATE == kFullGate) dgate.at += p.dgate.step;
-      if (GATE == kOneGate) {
-        if (POST && AFF && p.b_post) {  // u has a part beside w yh
-          float d[1] = {p.beta * sum_oct(dt_b)};
-          sums.add(d);
-          more.add(d);
-          wyd += d[0];
-        }
-        wyd *= gate_slope(p.act, one);
-        if (p.gate_kind == FLCE_GATE_SCALAR)
-          s_one += wyd;
-        else if (in_cta[0] == 0 && rank == 0)
-          store_element(TY{}, p.dgate.p, (row + q * units) * p.dgate.row, wyd);
+      if (kCarry) {
+        wyd_before = wyd;
+        one_before = one;
+      } else if (GATE == kOneGate) {
+        put_one(row + q * units, wyd, one);
       }
     }
     s_out = s_out + R * stage == end ? 0 : s_out + R * stage;
   }
 
+  if (kCarry && unit < p.N) {
+    float t[1] = {carry};
+    sums.add(t);
+    more.add(t);
+    // of the last row, which is the units before the first that there is not
+    put_one(unit + (p.N - 1 - unit) / units * units, wyd_before + t[0], one_before);
+  }
+
+  // The groups' sums over tokens, then the CTA's, in order of the groups.
+  const int64_t part_row = blockIdx.x / p.cluster;
+  const bool alone = p.groups == 1;
+  const uint32_t planes = ring + in_cta[0] * 16;
+  auto place = [&](int k, int g, int j) {
+    return planes + 2 * plane * (k * p.groups + g) + j * jump * 16;
+  };
+  if (!alone) {
+    copies_wait<0>();
+    __syncthreads();  // all have left the ring
+  }
+  constexpr int kBpre = 1, kGate = 1 + AFF, kPost = kGate + (GATE == kChannelGate ? 1 : 0);
+  float* to[5] = {p.part[0]};  // by plane
+  if (AFF) to[kBpre] = p.part[1];
+  if (GATE == kChannelGate) to[kGate] = p.part[4];
+  if (POST) to[kPost] = p.part[2];
+  if (POST && AFF) to[kPost + 1] = p.part[3];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    auto put = [&](float* part, const Oct& o) {
-      if (part && in[j]) store_octet<float>(part + unit * p.H, oct[j], o);
+    auto put = [&](int k, const Oct& o) {
+      if (!to[k] || !in[j]) return;
+      if (alone) store_octet<float>(to[k] + part_row * p.H, oct[j], o);
+      else put_shared(place(k, group, j), plane, o);
     };
-    put(p.part[0], s_pre[j]);
-    if (AFF) put(p.part[1], s_bpre[j]);
+    put(0, s_pre[j]);
+    if (AFF) put(kBpre, s_bpre[j]);
     if (kFixed && kReadsY && in[j]) {
       const Oct a = gate_of_channel(j);
       if (GATE == kChannelGate) {
@@ -445,17 +491,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < 4; ++i)
           f.p[i] = mul2(f.p[i], make_float2(p.beta * gate_slope(p.act, a.p[i].x),
                                             p.beta * gate_slope(p.act, a.p[i].y)));
-        put(p.part[4], f);
+        put(kGate, f);
       }
       scale_oct(s_post[j], a);
       scale_oct(s_bpost[j], a);
     }
     scale_oct(s_post[j], p.beta);
     scale_oct(s_bpost[j], p.beta);
-    if (POST) put(p.part[2], s_post[j]);
-    if (POST && AFF) put(p.part[3], s_bpost[j]);
+    if (POST) put(kPost, s_post[j]);
+    if (POST && AFF) put(kPost + 1, s_bpost[j]);
   }
-  if (GATE == kOneGate && p.part[4] && in_cta[0] == 0 && rank == 0) p.part[4][unit] = s_one;
+  if (GATE == kOneGate && in_cta[0] == 0) ones[group] = s_one * gate_slope(p.act, scalar);
+  if (!alone || GATE == kOneGate) __syncthreads();
+  if (!alone) {
+#pragma unroll
+    for (int k = 0; k < Shape::kTokenSums; ++k) {
+      if (k % p.groups != group || !to[k]) continue;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!in[j]) continue;
+        Oct o = shared_oct(place(k, 0, j), plane);
+        for (int g = 1; g < p.groups; ++g) {
+          const Oct t = shared_oct(place(k, g, j), plane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o.p[i] = plus2(o.p[i], t.p[i]);
+        }
+        store_octet<float>(to[k] + part_row * p.H, oct[j], o);
+      }
+    }
+  }
+  if (GATE == kOneGate && p.part[4] && threadIdx.x == 0 && rank == 0) {
+    float v = ones[0];
+    for (int g = 1; g < p.groups; ++g) v += ones[g];
+    p.part[4][part_row] = v;
+  }
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while another writes to its slots
 }
 
@@ -473,7 +542,7 @@ cudaError_t launch_bwd_nv(NormParams& p, int64_t parts, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>((parts ? parts / p.groups : 1) * p.cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>((parts ? parts : 1) * p.cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(ring + vectors);
   cfg.stream = s;
@@ -502,7 +571,7 @@ cudaError_t launch_bwd_nv(NormParams& p, int64_t parts, cudaStream_t s) {
     p.fit = n;
     return cudaSuccess;
   }
-  set_steps(p, parts, Elem<TY>::kBytes, Elem<TH>::kBytes);
+  set_steps(p, parts * p.groups, Elem<TY>::kBytes, Elem<TH>::kBytes);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
