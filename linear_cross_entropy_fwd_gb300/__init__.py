@@ -11,7 +11,9 @@ with the exact gradients ("Cálculo Preciso").
 
 C names are kept: ``flce_fwd_bwd``, ``flce_fwd_bwd_ex``, ``flce_fwd``,
 ``flce_fwd_bwd_host``, ``flce_fwd_noalloc``, ``flce_ce_fwd_bwd``,
-``flce_workspace_bytes``; ``scale_convert`` wraps ``flce_scale_convert``.
+``flce_workspace_bytes``; ``scale_convert`` wraps ``flce_scale_convert``.  The other operators of
+a training step are bound in ``step.py`` (embedding, attention, orthogonalisation) and
+``block.py`` (residual joins with their norms, checkpoints in 8 bits).
 ``LinearCrossEntropyLoss`` is the autograd front with the overview's
 (weight, input, target) order.  Every output buffer handed to the library
 is checked for shape, dtype, device and contiguity first, and each call runs

@@ -15,6 +15,11 @@
 // tokens, evenly; each pair's share of a tile goes to scratch and a second kernel adds a
 // tile's shares in order (8192 x 6144 x 4096: 4 of 384 tiles are left, a sixth round: 260 us
 // with it, 235 us shared).  Where that gains less than it costs the last round stays.
+//
+// Bound by the tensor cores under the board's power limit: 16384 x 14336 x 4096 in 1,006 us
+// when the board is cool (1,913 TFLOP/s), 1,127 back to back (1,707; the measured sustained rate
+// of a plain product is 1,715); tensor pipe 95% active.  Small products have about 11 us
+// before and behind their tiles, the reading back of X included (2048 x 2048 x 2048: 22 us).
 #include <cmath>
 
 #include "ckpt.cuh"

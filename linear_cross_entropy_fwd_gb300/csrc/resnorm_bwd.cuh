@@ -1,10 +1,17 @@
 // resnorm_bwd.cuh -- the residual join's backward pass (resnorm.h has the formulas); one
 // translation unit per pair of types includes it.
 //
-// A thread has the same 8 columns of every row that its warps take, so that the sums over
-// tokens stay in its registers until the end, one fp32 row for each CTA; a second kernel adds
-// those in a fixed order.  Rows of more than 4096 elements are shared by the
-// CTAs of a cluster for the same reason: 8 columns a thread is what 5 such sums leave room for.
+// Bound by memory where rows share what goes on around them: dz, dh', h' (and y) are read
+// once, dh and dy written once.  8192 x 4096 in bf16: 59 us with a norm before the block (5
+// streams, 5.7 TB/s), 71 us with one after it too (6, 5.7 TB/s); 65536 x 4096 with the norm before the block 414 us
+// (6.5 TB/s).  Means and biases on both sides make the instructions the bound: 89 us.
+//
+// A thread has the same NV octets of every row that its warps take, so that the sums over
+// tokens stay in its registers until the end; the CTA's groups of warps add theirs in shared
+// memory, one fp32 row for each CTA is left, and a second kernel adds those in a fixed order
+// (without the step between, 65536 x 256: 63 us, 18 of them in the second kernel; 37 with it).
+// One octet a thread, 4096 elements a CTA, is what 5 such sums leave room for, two what 2 or 3
+// do; longer rows are shared by the CTAs of a cluster, at an exchange of 1 us more per row.
 //
 // The two norms' sums would follow one another (the post-norm's need dt, dt needs the
 // pre-norm's).  But dt is linear in them: with e = dh' + r g and q = beta a w_post,
@@ -59,7 +66,7 @@ constexpr int kBwdPieces =
 
 // And behind the pieces, for each warp, the row's four statistics and its gate of one value:
 // a load a row ahead would have to keep registers through the row, or is moved to where it is
-// waited for (8192 x 4096 with gates per element 131 us, 54 of them waiting).
+// waited for (8192 x 4096 with gates per element: 131 us, 54 of them waiting; 93 now).
 constexpr uint32_t kRowBytes = 32, kTailBytes = kRowBytes * kMaxRowWarps;
 
 // What the launch and the kernel agree on, for NV octets a thread.
@@ -67,7 +74,8 @@ template <class TY, class TH, bool POST, bool AFF, int GATE, int NV>
 struct BwdShape {
   static constexpr int kPiecesRow = NV * kBwdPieces<TY, TH, POST, GATE>;
   // Rows that a group takes at a time: two share the exchange of their sums, where the
-  // registers hold two (8192 x 4096 in bf16 with both norms: 79 us with one, 70 with two).
+  // registers hold two (8192 x 4096 in bf16 with both norms: 79 us with one, 71 with two).
+  // With means or biases a second row takes longer to read again than it saves: 99 us, 89.
   static constexpr bool kTwoRows = NV == 1 && Elem<TH>::kBytes + Elem<TY>::kBytes <= 6 && POST &&
                                    !AFF && (GATE == kNoGate || GATE == kChannelGate);
   // Weights that wait in shared memory behind the ring instead of in registers: where a norm
@@ -581,9 +589,9 @@ inline int busy_warps(int octets, int nv) {
   return kMaxRowWarps / warps * warps;
 }
 
-// The launch's shape: two octets a thread where that spares a cluster (4096 x 8192: 75 us, 104
+// The launch's shape: two octets a thread where that spares a cluster (4096 x 8192: 74 us, 104
 // with a cluster of two) or keeps half as many warps again busy (16000 x 2056: 9 of 16 with
-// one, 118 us; 15 with two, 96).
+// one, 118 us; 15 with two, 92).
 inline void plan_bwd(NormParams& p, bool two) {
   const int octets = p.H / 8;
   const int nv = two && (octets > 32 * kMaxRowWarps ||
