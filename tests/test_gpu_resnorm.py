@@ -110,6 +110,43 @@ def test_many_rows(cuda_lib):
         _both(cuda_lib, N, H, BF, BF, BF, post=True, gate="channel")
 
 
+@pytest.mark.parametrize("gate", ["none", "scalar", "channel", "token", "full"])
+@pytest.mark.parametrize("kind,post,bias", [("layer", True, True), ("rms", False, False)])
+def test_many_rows_of_every_gate(cuda_lib, gate, kind, post, bias):
+    """As above; what a row leaves for the next one's sums, and the sums of the groups."""
+    act = "none" if gate == "none" else "sigmoid"
+    for N, H in ((20011, 64), (3001, 1000), (1003, 4096), (333, 8192), (157, 12296)):
+        _both(cuda_lib, N, H, BF, FP if H == 1000 else BF, FP, kind=kind, post=post, bias=bias,
+              gate=gate, act=act)
+
+
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+@pytest.mark.parametrize("kind,bias", [("rms", False), ("layer", True)])
+def test_nan_among_many_rows(cuda_lib, gate, kind, bias):
+    """Rows that come before and after one with NaN or infinities in the same warps."""
+    for N, H in ((5000, 64), (2500, 1000), (500, 4096), (300, 8192)):
+        t, p, opts = _make(N, H, BF, BF, BF, kind=kind, post=True, bias=bias, gate=gate,
+                           act="tanh")
+        out, z, stats = _forward(cuda_lib, t, p, opts)
+        got = cuda_lib.flce_resnorm_bwd(t["dz"], t["dh_out"], t["y"], out, stats, **p, **opts)
+        bad = torch.zeros(N, dtype=torch.bool, device=DEV)
+        bad[::7] = True
+        t["y"][::14, 11], t["h"][7::14, H - 1] = float("nan"), float("inf")
+        if gate != "channel":
+            p["gate"][::21, -1] = float("inf")  # of a bad row too; a tanh of 1
+            bad[::21] = True
+        out2, z2, stats2 = _forward(cuda_lib, t, p, opts)
+        for a, b in ((out, out2), (z, z2)):
+            assert torch.equal(a[~bad], b[~bad])
+        t["dz"][3::91, 5], t["dh_out"][5::91, 7] = float("nan"), float("-inf")
+        bad[3::91] = bad[5::91] = True
+        got2 = cuda_lib.flce_resnorm_bwd(t["dz"], t["dh_out"], t["y"], out2, stats2, **p, **opts)
+        names = ["dy", "dh"] + (["dgate"] if gate != "channel" else [])
+        for n in names:
+            a, b = getattr(got, n), getattr(got2, n)
+            assert torch.equal(a[~bad], b[~bad]), (n, N, H)
+
+
 def test_no_gradient_on_the_stream(cuda_lib):
     t, p, opts = _make(33, 128, BF, BF, BF, post=True, gate="scalar", act="tanh")
     out, _, stats = _forward(cuda_lib, t, p, opts)
