@@ -41,7 +41,7 @@ def _rows(name, t, shape, dtype, device):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if last != 1 and shape[1] > 1:
+    if last != 1 and t.numel():  # (without rows its strides are anything)
         raise ValueError(f"{name} must have a contiguous last axis")
     return t.data_ptr(), row
 
@@ -433,11 +433,14 @@ class _CheckpointedLinearFunction(torch.autograd.Function):
 
 class CheckpointedLinear(torch.nn.Module):
     """``linear(x, weight, saved=None)`` -> ``x @ weight.T`` in bf16, whose backward pass takes
-    the weight's gradient from x in 8 bits instead of x itself.  x [..., I], weight [O, I];
-    ``saved`` is a checkpoint of x that another call made (``ResidualNorm``, or a linear
-    that shares the input)."""
+    the weight's gradient from x in 8 bits instead of x itself.  x [..., I], weight [O, I], O
+    and I multiples of 8; ``saved`` is a checkpoint of x that another call made
+    (``ResidualNorm``, or a linear that shares the input)."""
 
     def forward(self, x, weight, saved: Checkpoint | None = None):
         if x.dtype is not torch.bfloat16 or weight.dtype is not torch.bfloat16:
             raise TypeError("CheckpointedLinear takes bf16 x and weight")
+        if weight.dim() != 2 or x.shape[-1:] != weight.shape[1:] \
+                or weight.shape[0] % 8 or weight.shape[1] % 8:
+            raise ValueError("x must be [..., I] and weight [O, I], O and I multiples of 8")
         return _CheckpointedLinearFunction.apply(x, weight, saved)

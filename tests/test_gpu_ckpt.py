@@ -221,3 +221,21 @@ def test_binding_refusals(cuda_lib):
             (TypeError, lambda: cuda_lib.CheckpointedLinear()(x.float(), x))]:
         with pytest.raises(err):
             call()
+
+
+def test_linear_refuses_what_its_backward_pass_could_not_take(cuda_lib):
+    """In the forward pass, not when the gradients are due."""
+    x = torch.zeros(4, 64, dtype=BF, device=DEV)
+    linear = cuda_lib.CheckpointedLinear()
+    for w in (torch.zeros(12, 64, dtype=BF, device=DEV), torch.zeros(64, dtype=BF, device=DEV),
+              torch.zeros(16, 72, dtype=BF, device=DEV)):
+        with pytest.raises(ValueError):
+            linear(x, w)
+    with pytest.raises(ValueError):
+        linear(x[:, :20], torch.zeros(16, 20, dtype=BF, device=DEV))
+    with pytest.raises(ValueError):
+        linear(x[0, 0], torch.zeros(16, 64, dtype=BF, device=DEV))
+    w = torch.zeros(16, 64, dtype=BF, device=DEV, requires_grad=True)
+    out = linear(x[:0], w)
+    out.sum().backward()
+    assert out.shape == (0, 16) and not w.grad.any()

@@ -275,6 +275,11 @@ def test_empty(cuda_lib):
                                     sync=True)
     for n in ("dgate", "dw_post", "db_post", "dw_pre", "db_pre"):
         assert getattr(got, n).shape == (64,) and not getattr(got, n).any()
+    y = torch.zeros(0, 64, dtype=BF, device=DEV, requires_grad=True)
+    w = torch.ones(64, device=DEV, requires_grad=True)
+    h, z = cuda_lib.ResidualNorm()(y, y, w_pre=w)
+    (h.sum() + z.sum()).backward()  # gradients that are one number, spread over no rows
+    assert y.grad.shape == (0, 64) and not w.grad.any()
 
 
 def test_checkpoint_of_z(cuda_lib):
