@@ -2,13 +2,14 @@
 // dW [O, I] (+)= dY^T X, dY [N, O] bf16, X [N, I] as ckpt.cuh stores it.
 //
 // X is read back into bf16 scratch, exactly, and multiplied on CTA pairs (tcgen05,
-// cta_group::2, 256 x 256 tiles, both operands MN-major), as the head's dW is.  What differs:
+// cta_group::2, tiles of 256 x 256 or 256 x 128, both operands MN-major), as the head's dW is.
+// What differs:
 //
 // Sums.  The tensor core cuts off what falls behind an accumulator's last bit instead of
 // rounding it, always towards zero, once for every 16 tokens: 1e-5 of the result after 16384
 // of them.  So an accumulator in TMEM takes kPiece k-blocks at most, and the pieces are added
-// in registers, rounded, in ascending order: eight warps hold a CTA's half of a tile, 128
-// sums a thread, and the tensor core goes on with the other accumulator meanwhile.  (Adding
+// in registers, rounded, in ascending order: eight warps hold a CTA's half of a tile, up to
+// 128 sums a thread, and the tensor core goes on with the other accumulator meanwhile.  (Adding
 // the pieces to dW at L2 took a quarter of the time of the products.)
 //
 // The last tiles.  Tiles that do not fill a round of all pairs are shared out along the
@@ -18,8 +19,9 @@
 //
 // Bound by the tensor cores under the board's power limit: 16384 x 14336 x 4096 in 1,006 us
 // when the board is cool (1,913 TFLOP/s), 1,127 back to back (1,707; the measured sustained rate
-// of a plain product is 1,715); tensor pipe 95% active.  Small products have about 11 us
-// before and behind their tiles, the reading back of X included (2048 x 2048 x 2048: 22 us).
+// of a plain product is 1,715); tensor pipe 95% active.  Small products have 9 to 11 us
+// before and behind their tiles, the reading back of X included (2048 x 2048 x 2048: 22 us,
+// 1994 x 1000 x 2056: 19).
 #include <cmath>
 
 #include "ckpt.cuh"
@@ -30,15 +32,20 @@
 namespace flce {
 namespace {
 
-constexpr int kStages = 6;                    // of 32 KB in each CTA of a pair
-constexpr int kTileM = 2 * BM;                // a pair's tile; BN wide
-constexpr int kPiece = 32;                    // k-blocks of 64 tokens in an accumulator
-constexpr uint32_t kOperandBytes = BM * 128;  // of A, and of B, in a stage of one CTA
-constexpr int kSumWarps = 8;                  // 32 rows of a tile by kSumCols columns each
-constexpr int kSumCols = 4 * BN / kSumWarps;
+constexpr int kTileM = 2 * BM;          // a pair's tile, TN wide: 256 or 128
+constexpr int kPiece = 32;              // k-blocks of 64 tokens in an accumulator
+constexpr uint32_t kABytes = BM * 128;  // of A in a stage of one CTA
+constexpr int kSumWarps = 8;            // 32 rows of a tile by kSumCols columns each
 constexpr int kWgradThreads = 64 + 32 * kSumWarps;
-constexpr uint32_t kStaging = kSumWarps * STAGING_BUF_BYTES;
-constexpr size_t kWgradSmem = 1024 + kStages * 2 * kOperandBytes + kStaging + SMEM_BARRIER_BYTES;
+
+template <int TN>
+struct WgradShape {
+  static constexpr uint32_t kBBytes = TN / 2 * 128;
+  static constexpr int kStages = TN == 256 ? 6 : 8;  // of 32 or 24 KB in each CTA of a pair
+  static constexpr int kSumCols = 4 * TN / kSumWarps;
+  static constexpr size_t kSmem = 1024 + kStages * (kABytes + kBBytes) +
+                                  kSumWarps * STAGING_BUF_BYTES + SMEM_BARRIER_BYTES;
+};
 
 // How the tiles are dealt out (GemmGrid for the order of the tiles and k-blocks).
 struct WgradPlan {
@@ -47,9 +54,10 @@ struct WgradPlan {
   int32_t whole;       // tiles that one pair does from end to end
   int32_t sharers;     // pairs that share the rest
   int32_t accumulate;
+  int32_t tn;          // columns of a tile
   int64_t O, I;
   float* dW;           // of the join
-  float* shares;       // [2 sharers][kTileM][BN]
+  float* shares;       // [2 sharers][kTileM][tn]
 };
 
 // A pair's next work: k-blocks k0 .. k1 of a tile, into dW or into its share `slot`.
@@ -95,6 +103,7 @@ __device__ __forceinline__ int piece_length(const Item& it, int n) {
   return (it.k1 - it.k0 + n - 1) / n;
 }
 
+template <int TN>
 __global__ void __launch_bounds__(kWgradThreads, 1)
     ckpt_wgrad_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -103,14 +112,17 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
                       const __grid_constant__ WgradPlan p) {
   constexpr uint32_t kBox = 128u * 64;  // 64 elements of MN by 64 tokens
   constexpr uint32_t kAdvance = 16u * 128u;
-  constexpr uint32_t kIdesc = make_idesc(1, true, true, kTileM, BN);
+  constexpr uint32_t kIdesc = make_idesc(1, true, true, kTileM, TN);
+  using Shape = WgradShape<TN>;
+  constexpr int kStages = Shape::kStages, kSumCols = Shape::kSumCols;
+  constexpr uint32_t kBBytes = Shape::kBBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* smA = smem;
-  uint8_t* smB = smem + kStages * kOperandBytes;
-  uint8_t* staging = smB + kStages * kOperandBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
+  uint8_t* smB = smem + kStages * kABytes;
+  uint8_t* staging = smB + kStages * kBBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kSumWarps * STAGING_BUF_BYTES);
   uint64_t* full = bars;                    // [kStages]  (the even CTA's are used)
   uint64_t* empty = bars + kStages;         // [kStages]
   uint64_t* acc_full = bars + 2 * kStages;  // [2]
@@ -168,13 +180,13 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       int mu, n_blk;
       tile_coords(p.g, it.tile, mu, n_blk);
       const int a_mn = uniform(mu * kTileM + static_cast<int>(rank) * BM);
-      const int b_mn = uniform(n_blk * BN + static_cast<int>(rank) * BM);
+      const int b_mn = uniform(n_blk * TN + static_cast<int>(rank) * (TN / 2));
       auto load_a = [&](uint32_t stage, int kb) {
-        if (rank == 0) expect_tx_elected(&full[stage], 4 * kOperandBytes);
+        if (rank == 0) expect_tx_elected(&full[stage], 2 * (kABytes + kBBytes));
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           tma_load_2d_pair_elected(&tmA, full_even + 8 * stage,
-                                   a_base + stage * kOperandBytes + j * kBox, a_mn + 64 * j,
+                                   a_base + stage * kABytes + j * kBox, a_mn + 64 * j,
                                    kb * 64);
       };
       if (first) {
@@ -192,8 +204,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
           load_a(s, kb);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          tma_load_2d_pair_elected(&tmB, full_even + 8 * s, b_base + s * kOperandBytes + j * kBox,
+        for (int j = 0; j < TN / 128; ++j)
+          tma_load_2d_pair_elected(&tmB, full_even + 8 * s, b_base + s * kBBytes + j * kBox,
                                    b_mn + 64 * j, kb * 64);
         if (++s == kStages) {
           s = 0;
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + buf * BN;
+          const uint32_t d_tmem = tmem_base + buf * TN;
           const int k1 = k0 + length < it.k1 ? k0 + length : it.k1;
           uint32_t add = 0;
           for (int kb = k0; kb < k1; ++kb) {
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
               break;
             }
             tc_fence_after();
-            const Operand16 a = moved(a0, s * kOperandBytes), b = moved(b0, s * kOperandBytes);
+            const Operand16 a = moved(a0, s * kABytes), b = moved(b0, s * kBBytes);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               mma_f16_pair_at(d_tmem, a, k * kAdvance, b, k * kAdvance, kIdesc, add);
@@ -278,7 +290,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
 #pragma unroll
         for (int u = 0; u < kSumCols / 16; ++u) {
           uint32_t r[16];
-          tmem_ld_32x32b_x16(lanes + buf * BN + 16 * u, r);
+          tmem_ld_32x32b_x16(lanes + buf * TN + 16 * u, r);
           tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < 8; ++c)
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       int mu, n_blk;
       tile_coords(p.g, it.tile, mu, n_blk);
       const bool share = it.slot >= 0;
-      const int x = (share ? 0 : n_blk * BN) + col;
+      const int x = (share ? 0 : n_blk * TN) + col;
       const int y = (share ? it.slot : mu) * kTileM + static_cast<int>(rank) * BM + 32 * q;
 #pragma unroll
       for (int u = 0; u < kSumCols / 32; ++u) {
@@ -327,12 +339,15 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
 
 // dW of the shared tiles: each the sum of its shares, in ascending order of their tokens.  A
 // CTA has kJoinRows rows of a tile, a thread four columns of one, kJoinAtOnce loads in flight.
-constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 64, kJoinAtOnce = 8;
+constexpr int kJoinThreads = 256, kJoinAtOnce = 8;
+template <int TN>
+constexpr int kJoinRows = kJoinThreads / (TN / 4);
 
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
   a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
+template <int TN>
 __global__ void __launch_bounds__(kJoinThreads)
     ckpt_wgrad_join_kernel(const __grid_constant__ WgradPlan p) {
   // The units u .. end with some of this tile's k-blocks, and whether unit u ends another tile
@@ -356,12 +371,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (end == u) return;
   int mu, n_blk;
   tile_coords(p.g, p.whole + static_cast<int>(t), mu, n_blk);
-  const int row = blockIdx.x * kJoinRows + (threadIdx.x >> 6), quad = threadIdx.x & 63;
+  const int row = blockIdx.x * kJoinRows<TN> + threadIdx.x / (TN / 4);
+  const int quad = threadIdx.x % (TN / 4);
   const int64_t at = mu * static_cast<int64_t>(kTileM) + row;
-  if (at >= p.O || n_blk * BN + 4 * quad >= p.I) return;
-  const float4* from = reinterpret_cast<const float4*>(p.shares) + row * (BN / 4) + quad;
-  constexpr int64_t kSlot = kTileM * BN / 4;
-  float4* to = reinterpret_cast<float4*>(p.dW + at * p.I + n_blk * BN + 4 * quad);
+  if (at >= p.O || n_blk * TN + 4 * quad >= p.I) return;
+  const float4* from = reinterpret_cast<const float4*>(p.shares) + row * (TN / 4) + quad;
+  constexpr int64_t kSlot = kTileM * TN / 4;
+  float4* to = reinterpret_cast<float4*>(p.dW + at * p.I + n_blk * TN + 4 * quad);
   float4 s = p.accumulate ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int w = u; w < end; w += kJoinAtOnce) {
     float4 a[kJoinAtOnce];
@@ -410,42 +426,73 @@ int map_of(CUtensorMap* m, const void* p, CUtensorMapDataType t, int64_t cols, i
   return host_tensor_map(m, p, t, 2, dims, pitches, boxes, what);
 }
 
-// Whether the last tiles are shared out, and among how many pairs: a k-block takes 0.29 us, a
-// share 0.18 us to be written and read (256 KB each way), the join a launch of 4 us.  So n
-// pairs take 0.29 K / n + 0.18 n for the K k-blocks of these tiles, least at
-// n = sqrt(0.29 K / 0.18).  One round, shared: 20000 x 1000 x 1000 (16 tiles) 168 -> 64 us,
-// 9768 x 184 x 424 (2 tiles) 68 -> 20; the last round only, 8192 x 4096 x 4096 (28 of 256
-// tiles) 178 -> 170.  With 0.06 in place of 0.18 65536 x 256 x 256 takes 41 us, not 34.
-WgradPlan plan(int64_t N, int64_t O, int64_t I, int units, bool accumulate) {
+// The tiles of one width dealt out, and an estimate of the time.  A k-block takes a pair 0.34 us
+// (0.22 in tiles of 128), a tile's results 5.4 us (2.2) to be written while the next one's
+// products run, and there are 11 us (9.5) around the rounds.
+//
+// The last round's tiles, K k-blocks in all, may be shared by n pairs along the tokens: a share
+// takes 0.18 us (0.09) to be written and read, 256 KB (128) each way, the join a launch of
+// 4 us.  So they take 0.34 K / n + 0.18 n, least at n = sqrt(0.34 K / 0.18).  One round,
+// shared: 20000 x 1000 x 1000 (16 tiles) 168 -> 64 us, 9768 x 184 x 424 (2 tiles) 68 -> 20; the
+// last round only, 8192 x 4096 x 4096 (28 of 256 tiles) 178 -> 170.  With 0.06 in place of
+// 0.18 65536 x 256 x 256 takes 41 us, not 34.  Where little is expected the pairs keep whole
+// tiles, which they read side by side (16384 x 14336 x 4096, 60 of 896 tiles left, back to
+// back: 1,148 us, 1,180 with those shared).
+WgradPlan deal(int64_t N, int64_t O, int64_t I, int units, int tn, double* us) {
+  const double block = tn == 256 ? 0.34 : 0.22, results = tn == 256 ? 5.4 : 2.2;
+  const double share = tn == 256 ? 0.18 : 0.09, around = tn == 256 ? 11.0 : 9.5;
   WgradPlan p{};
+  p.tn = tn;
   p.g.num_m_blk = static_cast<int32_t>((O + kTileM - 1) / kTileM);
-  p.g.num_n_blk = static_cast<int32_t>((I + BN - 1) / BN);
+  p.g.num_n_blk = static_cast<int32_t>((I + tn - 1) / tn);
   p.g.num_k_blk = static_cast<int32_t>((N + 63) / 64);
   p.g.raster_n = 1;
-  p.g.n_band = 8;  // pairs that run together take about 8 x 9 tiles
-  p.accumulate = accumulate;
+  p.g.n_band = 8 * (256 / tn);  // pairs that run together take about 8 x 9 tiles of 256
   p.units = units;
   const int tiles = p.g.num_m_blk * p.g.num_n_blk, left = tiles % units;
+  const int rounds = (tiles + units - 1) / units;
+  const double tile = block * p.g.num_k_blk, round = tile > results ? tile : results;
+  *us = around + (rounds - 1) * round + tile;
   p.whole = tiles;
   p.sharers = 1;
   if (left) {
-    const double blocks = static_cast<double>(left) * p.g.num_k_blk;
-    int n = static_cast<int>(std::sqrt(0.29 * blocks / 0.18));
+    int n = static_cast<int>(std::sqrt(left * tile / share));
     n = n < units ? n : units;
-    if (n > left && 0.29 * blocks / n + 0.18 * n + 4.0 < 0.29 * p.g.num_k_blk) {
+    const double shared = n > left ? left * tile / n + share * n + 4.0 : tile;
+    if (shared < 0.9 * tile) {
       p.whole = tiles - left;
       p.sharers = n;
+      *us += shared - tile;
     }
   }
   if (tiles < units) p.units = p.whole ? tiles : p.sharers;
   return p;
 }
 
-cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int units, cudaStream_t s) {
+// Tiles of 128 columns where they are expected to take less time: where few of 256 leave pairs
+// idle (1994 x 1000 x 2056 24.6 -> 18.9 us, 4096 x 2048 x 1024 29.7 -> 23.2), or where there are few
+// tokens (52 x 5376 x 992 16.1 -> 11.5).  Where tiles abound those of 256 take
+// half as much of L2 (8192 x 4096 x 4096 171 us against 222).
+WgradPlan plan(int64_t N, int64_t O, int64_t I, int units, bool accumulate) {
+  double wide_us, narrow_us;
+  const WgradPlan wide = deal(N, O, I, units, 256, &wide_us);
+  const WgradPlan narrow = deal(N, O, I, units, 128, &narrow_us);
+  WgradPlan p = narrow_us < 0.95 * wide_us ? narrow : wide;
+  p.accumulate = accumulate;
+  return p;
+}
+
+template <int TN>
+cudaError_t launch_products(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mw,
+                            const CUtensorMap& ms, const WgradPlan& p, cudaStream_t s) {
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(ckpt_wgrad_kernel<TN>, WgradShape<TN>::kSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * units));
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.units));
   cfg.blockDim = dim3(kWgradThreads);
-  cfg.dynamicSmemBytes = kWgradSmem;
+  cfg.dynamicSmemBytes = WgradShape<TN>::kSmem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -455,21 +502,22 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int units, cudaStream_
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cfg;
+  return cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel<TN>, ma, mb, mw, ms, p);
 }
 
+template <int TN>
 cudaError_t launch_join(const WgradPlan& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim =
-      dim3(kTileM / kJoinRows, static_cast<unsigned>(p.g.num_m_blk * p.g.num_n_blk - p.whole));
+      dim3(kTileM / kJoinRows<TN>, static_cast<unsigned>(p.g.num_m_blk * p.g.num_n_blk - p.whole));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ckpt_wgrad_join_kernel, p);
+  return cudaLaunchKernelEx(&cfg, ckpt_wgrad_join_kernel<TN>, p);
 }
 
 }  // namespace
@@ -491,7 +539,7 @@ extern "C" int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt,
   const size_t x_bytes = round256(static_cast<size_t>(N) * static_cast<size_t>(I) * 2);
   const int64_t share_rows = shared ? 2 * static_cast<int64_t>(all.sharers) * kTileM : 0;
   StepCall call;
-  if ((rc = call.begin(o, x_bytes + static_cast<size_t>(share_rows) * BN * 4,
+  if ((rc = call.begin(o, x_bytes + static_cast<size_t>(share_rows) * all.tn * 4,
                        N > 0 ? StepCall::kKernelClears : StepCall::kCleared)))
     return rc;
   if (N == 0) {
@@ -516,19 +564,15 @@ extern "C" int flce_ckpt_wgrad(const void* dY, int64_t dY_row, const void* ckpt,
       (rc = map_of(&mw, dW, fp32, I, O, I * 4, 32, "dW")))
     return call.end(rc);
   ms = mw;
-  if (shared && (rc = map_of(&ms, p.shares, fp32, BN, share_rows, BN * 4, 32, "shares")))
+  if (shared && (rc = map_of(&ms, p.shares, fp32, p.tn, share_rows, p.tn * 4, 32, "shares")))
     return call.end(rc);
-  static SmemLimit limit;
-  cudaError_t e = limit.raise(ckpt_wgrad_kernel, kWgradSmem);
+  cudaError_t e = launch_ckpt_load(ckpt_view(const_cast<void*>(ckpt), N, I), call.scratch, I, N,
+                                   I, 2, call.status, call.stream);
   if (e == cudaSuccess)
-    e = launch_ckpt_load(ckpt_view(const_cast<void*>(ckpt), N, I), call.scratch, I, N, I, 2,
-                         call.status, call.stream);
-  if (e == cudaSuccess) {
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_config(attr, p.units, call.stream);
-    e = cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel, ma, mb, mw, ms, p);
-  }
-  if (e == cudaSuccess && shared) e = launch_join(p, call.stream);
+    e = p.tn == 256 ? launch_products<256>(ma, mb, mw, ms, p, call.stream)
+                    : launch_products<128>(ma, mb, mw, ms, p, call.stream);
+  if (e == cudaSuccess && shared)
+    e = p.tn == 256 ? launch_join<256>(p, call.stream) : launch_join<128>(p, call.stream);
   if (e != cudaSuccess) rc = host_cuda_error(e, "ckpt_wgrad");
   return call.end(rc);
 }

@@ -135,13 +135,16 @@ def test_wgrad(cuda_lib, N, O, I):
 
 
 @pytest.mark.parametrize("N,O,I", [
-    (20001, 264, 264),    # fewer tiles than CTA pairs, each shared by many
-    (8200, 520, 2056),    # 27 tiles, shared by two or three
-    (9000, 2568, 2056),   # 99 tiles: a whole round and 23
+    (20001, 264, 264),    # 6 tiles of 128 columns, each shared by many CTA pairs
+    (8200, 520, 2056),    # 51 tiles of 128, not shared
+    (9000, 2568, 2056),   # 99 tiles of 256: a whole round and 23 that are shared
     (30000, 8, 8),        # one tile
-    (2500, 3400, 3000)])  # 168 tiles, two whole rounds and 16 that are not shared out
+    (2500, 3400, 3000),   # 168 tiles of 256, two whole rounds and 16 that are not shared out
+    (8192, 2600, 1000),   # 44 tiles of 256, all shared
+    (3040, 2976, 1624),   # 156 tiles of 128, of which 4 are shared
+    (14, 5656, 2056)])    # 391 tiles of 128, five rounds
 def test_wgrad_shared_tiles(cuda_lib, N, O, I):
-    """Tiles that several CTA pairs share along the tokens."""
+    """Either width of tiles, and tiles that several CTA pairs share along the tokens."""
     g = torch.Generator(device=DEV).manual_seed(N)
     dY = torch.randn(N, O, generator=g, device=DEV).to(BF)
     x = torch.randn(N, I, generator=g, device=DEV).to(BF)
