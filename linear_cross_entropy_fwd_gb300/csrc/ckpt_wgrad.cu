@@ -305,22 +305,31 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       int mu, n_blk;
       tile_coords(p.g, it.tile, mu, n_blk);
       const bool share = it.slot >= 0;
+      // The last tile's results go out through the ring, which is done with: all at once.
+      Items behind = items;
+      Item none;
+      const bool last = !behind.next(none);
+      uint8_t* to = last ? smem + (warp - 2) * (kSumCols / 32) * STAGING_BUF_BYTES : buffer;
+      const uint32_t next = last ? STAGING_BUF_BYTES : 0;
       const int x = (share ? 0 : n_blk * TN) + col;
       const int y = (share ? it.slot : mu) * kTileM + static_cast<int>(rank) * BM + 32 * q;
 #pragma unroll
       for (int u = 0; u < kSumCols / 32; ++u) {
-        if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
-        __syncwarp();
+        if (!last) {
+          if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+          __syncwarp();
+        }
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const float2 v = sum[16 * u + 2 * ch], w = sum[16 * u + 2 * ch + 1];
-          staging_put16(buffer, lane, ch, __float_as_uint(v.x), __float_as_uint(v.y),
+          staging_put16(to + u * next, lane, ch, __float_as_uint(v.x), __float_as_uint(v.y),
                         __float_as_uint(w.x), __float_as_uint(w.y));
         }
         if (!share && p.accumulate)
-          staging_release<true>(&tmOut, buffer, lane, x + 32 * u, y);
+          staging_release<true>(&tmOut, to + u * next, lane, x + 32 * u, y);
         else
-          staging_release<false>(share ? &tmShares : &tmOut, buffer, lane, x + 32 * u, y);
+          staging_release<false>(share ? &tmShares : &tmOut, to + u * next, lane, x + 32 * u,
+                                 y);
       }
     }
     if (lane == 0) bulk_wait<0>();  // stores done before shared memory goes away
