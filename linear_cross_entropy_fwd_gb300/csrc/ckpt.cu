@@ -2,7 +2,8 @@
 //
 // Bound by memory: 2 or 4 bytes a value on one side, 8.25 bits on the other.  A thread holds
 // an octet, four neighbouring lanes a group that shares a scale.  65536 x 4096 in bf16: saved in
-// 126 us (6.5 TB/s), loaded in 117 (7.0 TB/s).
+// 126 us (6.5 TB/s), loaded in 117 (7.0 TB/s); 32768 x 4096 in fp32 95 and 100 us (an octet
+// stored in halves: 126).
 #include "ckpt.cuh"
 #include "host_util.h"
 
@@ -19,6 +20,7 @@ struct CkptParams {
   uint32_t padded;  // of a row of codes, its padding included (save), or of x (load)
   int64_t total;    // of all rows, `padded` each
   int32_t* clear;
+  bool wide;        // x is 32-byte aligned
 };
 
 // A thread's octets, kThreads apart: row and octet of each.  One 64-bit division for a CTA,
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p)
   }
 #pragma unroll
   for (int k = 0; k < kOctets; ++k)
-    if (to[k]) *to[k] = to_octet(T{}, ckpt_octet(codes[k], scale[k]));
+    if (to[k]) put_octet(to[k], to_octet(T{}, ckpt_octet(codes[k], scale[k])), p.wide);
 }
 
 CkptParams params(const Ckpt& c, void* x, int64_t x_row, int64_t N, int64_t H, bool save) {
@@ -107,6 +109,7 @@ CkptParams params(const Ckpt& c, void* x, int64_t x_row, int64_t N, int64_t H, b
   p.octets = static_cast<uint32_t>(H / 8);
   p.padded = save ? static_cast<uint32_t>(p.c.pitch) / 8 : p.octets;
   p.total = N * p.padded;
+  p.wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
   return p;
 }
 

@@ -17,9 +17,9 @@
 // tile's shares in order (8192 x 6144 x 4096: 4 of 384 tiles are left, a sixth round: 260 us
 // with it, 235 us shared).  Where that gains less than it costs the last round stays.
 //
-// Bound by the tensor cores under the board's power limit: 16384 x 14336 x 4096 in 1,006 us
-// when the board is cool (1,913 TFLOP/s), 1,127 back to back (1,707; the measured sustained rate
-// of a plain product is 1,715); tensor pipe 95% active.  Small products have 9 to 11 us
+// Bound by the tensor cores under the board's power limit: 16384 x 14336 x 4096 in 982 us
+// when the board is cool (1,960 TFLOP/s), 1,094 to 1,160 back to back (1,660 to 1,760; the measured
+// sustained rate of a plain product is 1,715); tensor pipe 96% active.  Small products have 9 to 11 us
 // before and behind their tiles, the reading back of X included (2048 x 2048 x 2048: 22 us,
 // 1994 x 1000 x 2056: 19).
 #include <cmath>

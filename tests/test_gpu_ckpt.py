@@ -100,6 +100,17 @@ def test_strides(cuda_lib):
     assert bool((wide[:, 216:] == 3).all())
 
 
+def test_fp32_rows_at_any_16_bytes(cuda_lib):
+    """Rows that begin on a multiple of 32 bytes, and those that do not."""
+    ck = cuda_lib.flce_ckpt_save(_x(70, 136, FP).to(DEV))
+    want = cuda_lib.flce_ckpt_load(ck, dtype=FP)
+    for at in (0, 4, 8, 12):
+        buf = torch.full((70, 160), 3.0, device=DEV)
+        cuda_lib.flce_ckpt_load(ck, out=buf[:, at:at + 136])
+        assert torch.equal(buf[:, at:at + 136], want)
+        assert bool((buf[:, :at] == 3).all()) and bool((buf[:, at + 136:] == 3).all())
+
+
 def _check_wgrad(got, dY, x, old):
     dY, x = dY.double(), x.double()
     want, A = dY.t() @ x, dY.t().abs() @ x.abs()
