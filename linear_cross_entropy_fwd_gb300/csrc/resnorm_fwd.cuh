@@ -7,8 +7,8 @@
 // rows.cuh).  A mean and a variance are two sums one after the other, so that nothing
 // cancels; RMS norms need one.  A row may hold anything finite.
 //
-// 8192 x 4096 in bf16: 46 us with RMS norms on either or both sides (5.8 TB/s), 51 with a
-// layer norm, 68 with two and their biases, whose four exchanges per pair of rows are then
+// 8192 x 4096 in bf16: 46 us with an RMS norm before the next block (5.8 TB/s), 48 with one on
+// both sides (32768 x 4096: 161 and 165, 6.6 TB/s), 51 with a layer norm, 68 with two and their biases, whose four exchanges per pair of rows are then
 // the bound; fp32 throughout 95 us (5.7 TB/s).  One token takes 4.6 us, a launch's latency.
 #pragma once
 #include "host_util.h"
@@ -114,7 +114,18 @@ constexpr int kFwdStages = ring_stages(
 template <class TY, class TH, int NV, bool FULL>
 constexpr int kFwdRows = NV <= 2 && kFwdStages<TY, TH, NV, FULL> >= 4 ? 2 : 1;
 
+// Without a norm after the block h' follows its loads at once, and many rows in bf16 take less
+// time when the next ones are asked for behind it (LATE), not before: 32768 x 4096 161 us
+// against 187, 12288 x 4096 65 against 71, with a gate per element 81 either way, 6144 x 4096 36
+// against 35.  (With that norm, which keeps loads and stores apart, 182 against 165 at 32768;
+// with layer norms or an fp32 stream no gain.)
 template <class TY, class TH, int NV, bool LAYER, bool FULL>
+constexpr bool kMayBeLate = NV == 2 && !LAYER && Elem<TH>::kBytes == 2 &&
+                            kFwdRows<TY, TH, NV, FULL> == 2;
+constexpr int kLateRows = 40;  // of a group of warps, at least
+
+// LATE: without a norm after the block.
+template <class TY, class TH, int NV, bool LAYER, bool FULL, bool LATE>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     resnorm_fwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float slots[kMaxRowWarps][2][kMaxSums][kMaxRowWarps];
@@ -224,10 +235,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   Walk<TY> z(p.z.p, p.z.row, first, oct[0]);
   __syncthreads();
 
-  for (int64_t row = first; row < p.N; row += R * rows) {
+  auto fetch_rows = [&] {
 #pragma unroll
     for (int q = 0; q < R; ++q) fetch(s_in + q * stage);
     s_in = s_in + R * stage == end ? 0 : s_in + R * stage;
+  };
+  static_assert(!LATE || kStages >= 2 * R, "rows in hand and rows on their way");
+  const bool post = !LATE && p.post;
+  for (int64_t row = first; row < p.N; row += R * rows) {
+    if (!LATE) fetch_rows();
     bool there[R];
     Oct x[R][NV];
     float gate1[R], mean_y[R], r_y[R], mean_h[R], r_h[R], f[R];
@@ -238,7 +254,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mean_y[q] = r_y[q] = mean_h[q] = r_h[q] = 0.f;
     }
     if (token) read_gates(row + R * rows);
-    copies_wait<kStages - R>();
+    copies_wait<kStages - R - (LATE ? R : 0)>();
     __syncwarp();  // lanes read what others copied
     const Slot<TY> slot_y(threadIdx.x, lane, 0, 0);
     const Slot<TH> slot_h(threadIdx.x, lane, 0, 0);
@@ -249,7 +265,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         x[q][j] = in[j] && there[q] ? slot_y.read(at + q * stage + j * kPer * step) : zero_oct();
-    if (p.post) normalise<R, NV, LAYER>(x, in, p.eps, p.inv_h, sums, mean_y, r_y, f);
+    if (post) normalise<R, NV, LAYER>(x, in, p.eps, p.inv_h, sums, mean_y, r_y, f);
 #pragma unroll
     for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           continue;
         }
         const uint32_t mine = at + q * stage + j * kPer * step;
-        if (p.post) scale_oct(v, f[q]);
+        if (post) scale_oct(v, f[q]);
         scale_oct(v, kKeep  ? c[kKeep ? j : 0]
                      : FULL ? factor(p.w_post, 1.f, oct[j])
                             : shared_oct(factors + oct[j] * 32, 16));
@@ -281,6 +297,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           h_out.put(o, p.wide, q * p.h_out.step + j * jump * 8 * Elem<TH>::kBytes);
         v = from_octet(o);
       }
+    if (LATE) fetch_rows();
     // all lanes have read what later copies overwrite: here, or by the exchanges of sums
     if (!p.pre) __syncwarp();
     if (p.pre) {
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-template <class TY, class TH, int NV, bool LAYER, bool FULL>
+template <class TY, class TH, int NV, bool LAYER, bool FULL, bool LATE = false>
 cudaError_t launch(NormParams p, int sms, cudaStream_t s) {
   static SmemLimit limit;
   const int octets = p.H / 8;
@@ -340,11 +357,14 @@ cudaError_t launch(NormParams p, int sms, cudaStream_t s) {
   const int factors = kBiasShared<NV, FULL> ? (p.b_post || p.b_pre ? 4 * NV * 32 * p.warps * 16 : 0)
                       : NV == 4 && !FULL    ? p.H * 4
                                             : 0;
-  const auto kernel = resnorm_fwd_kernel<TY, TH, NV, LAYER, FULL>;
-  const cudaError_t e = limit.raise(kernel, kSmemPerSm);
-  if (e != cudaSuccess) return e;
   const int64_t want = (p.N + p.groups - 1) / p.groups;
   const int64_t grid = want < sms ? want : sms;
+  if constexpr (!LATE && kMayBeLate<TY, TH, NV, LAYER, FULL>)
+    if (!p.post && p.N >= kLateRows * grid * p.groups)
+      return launch<TY, TH, NV, LAYER, FULL, true>(p, sms, s);
+  const auto kernel = resnorm_fwd_kernel<TY, TH, NV, LAYER, FULL, LATE>;
+  const cudaError_t e = limit.raise(kernel, kSmemPerSm);
+  if (e != cudaSuccess) return e;
   set_steps(p, grid * p.groups, Elem<TY>::kBytes, Elem<TH>::kBytes);
   kernel<<<static_cast<unsigned>(grid), threads,
            static_cast<size_t>(kStages) * stage + factors, s>>>(p);

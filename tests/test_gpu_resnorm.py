@@ -147,6 +147,25 @@ def test_nan_among_many_rows(cuda_lib, gate, kind, bias):
             assert torch.equal(a[~bad], b[~bad]), (n, N, H)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(gate="full", act="sigmoid"), dict(h=False),
+                                dict(gate="token", bias=True, alpha=0.5)])
+def test_rows_that_are_asked_for_late(cuda_lib, kw):
+    """bf16 rows of RMS norms without one after the block, 40 or more to a group of warps."""
+    for N, H in ((97301, 264), (6101, 8192)):
+        t, p, opts = _make(N, H, BF, BF, BF, **kw)
+        out, z, stats = _forward(cuda_lib, t, p, opts, sync=True)
+        _check_forward(t, p, opts, out, z)
+        few, zf, sf = cuda_lib.flce_resnorm_fwd(
+            t["y"][:99], None if t["h"] is None else t["h"][:99],
+            **{**p, "gate": None if p["gate"] is None else p["gate"][:99]}, **opts)
+        assert torch.equal(few, out[:99]) and torch.equal(zf, z[:99])
+        assert torch.equal(sf, stats[:, :99])
+        z2 = t["y"].clone()
+        h2 = None if t["h"] is None else t["h"].clone()
+        cuda_lib.flce_resnorm_fwd(z2, h2, **p, **opts, out=h2, z=z2)
+        assert torch.equal(z2, z) and (h2 is None or torch.equal(h2, out))
+
+
 def test_no_gradient_on_the_stream(cuda_lib):
     t, p, opts = _make(33, 128, BF, BF, BF, post=True, gate="scalar", act="tanh")
     out, _, stats = _forward(cuda_lib, t, p, opts)
