@@ -2,6 +2,10 @@
 on both sides, a gate, checkpointed projections, packed attention and the head, its gradients
 against autograd in 64 bits and against differences; captured into a graph; second
 derivatives, which are refused."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -242,3 +246,47 @@ def test_other_streams(cuda_lib):
     torch.cuda.synchronize()
     for a in got:
         assert all(torch.equal(u, v) for u, v in zip(a, want))
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import linear_cross_entropy_fwd_gb300 as flce
+g = torch.Generator(device="cuda").manual_seed(1)
+BF = torch.bfloat16
+def r(*s):
+    return torch.randn(*s, generator=g, device="cuda").to(BF)
+N, H = 300, int(sys.argv[2])
+y, h, dz, dh, w, b, gate = r(N, H), r(N, H), r(N, H), r(N, H), r(H), r(H), r(N, 1)
+kw = dict(w_pre=w, w_post=w, b_post=b, gate=gate, gate_act="tanh", kind="layer")
+def run():
+    out, z, stats = flce.flce_resnorm_fwd(y, h, **kw)
+    grads = flce.flce_resnorm_bwd(dz, dh, y, out, stats, **kw)
+    ck = flce.flce_ckpt_save(z)
+    dW = flce.flce_ckpt_wgrad(dz, ck)
+    return [out, z, stats, *grads, ck.data, dW, flce.flce_ckpt_load(ck)]
+# one call that takes scratch, for the device's state; none of the kernels below
+flce.flce_embed_bwd(y[:8], torch.zeros(8, dtype=torch.int64, device="cuda"), 16)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+for _ in range(2):
+    graph.replay()
+torch.cuda.synchronize()
+want = run()
+torch.cuda.synchronize()
+assert len(got) == len(want)
+for i, (a, e) in enumerate(zip(got, want)):
+    assert (a is None) == (e is None) and (a is None or torch.equal(a, e)), i
+print("same")
+"""
+
+
+@pytest.mark.parametrize("H", [1000, 5000])
+def test_first_calls_inside_a_capture(cuda_lib, H):
+    """Kernels that nothing has warmed up: attributes and launch shapes are found in the capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST, root, str(H)], capture_output=True,
+                       text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip() == "same", p.stdout + p.stderr
