@@ -2,9 +2,9 @@
 // translation unit per pair of types includes it.
 //
 // Bound by memory where rows share what goes on around them: dz, dh', h' (and y) are read
-// once, dh and dy written once.  8192 x 4096 in bf16: 59 us with a norm before the block (5
-// streams, 5.7 TB/s), 71 us with one after it too (6, 5.7 TB/s); 65536 x 4096 with the norm before the block 414 us
-// (6.5 TB/s).  Means and biases on both sides make the instructions the bound: 89 us.
+// once, dh and dy written once.  8192 x 4096 in bf16: 57 us with a norm before the next block
+// (5 streams, 5.9 TB/s), 73 us with one on both sides (6, 5.5 TB/s); 65536 x 4096 390 us (6.9
+// TB/s) and 515 (6.3).  Means and biases on both sides make the instructions the bound: 89 us.
 //
 // A thread has the same NV octets of every row that its warps take, so that the sums over
 // tokens stay in its registers until the end; the CTA's groups of warps add theirs in shared
@@ -66,7 +66,7 @@ constexpr int kBwdPieces =
 
 // And behind the pieces, for each warp, the row's four statistics and its gate of one value:
 // a load a row ahead would have to keep registers through the row, or is moved to where it is
-// waited for (8192 x 4096 with gates per element: 131 us, 54 of them waiting; 93 now).
+// waited for (8192 x 4096 with gates per element: 131 us, 54 of them waiting; 88 now).
 constexpr uint32_t kRowBytes = 32, kTailBytes = kRowBytes * kMaxRowWarps;
 
 // What the launch and the kernel agree on, for NV octets a thread.
@@ -194,8 +194,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     copies_commit();
   };
+  // Single bf16 rows that are not read again ask for the next ones behind the exchange of their
+  // sums, between their own loads and stores, when their own stage is free too: 65536 x 4096
+  // 390 us, 415 with the copies first; with gates per element 632 and 683; 30000 x 1000 55
+  // either way.  (Pairs of rows 79 and 74 at 8192 x 4096, two octets a thread 67 and 58 at
+  // 4096 x 8192; with an fp32 stream, or means on both sides, up to 4% more.)
+  constexpr bool kAgain = R > 1 || NV > 1;
+  constexpr bool kLate = !kAgain && Elem<TH>::kBytes == 2 && !(POST && AFF);
+  constexpr int kAhead = kLate ? kStages : kStages - R;
   uint32_t s_in = 0, s_out = 0;
-  for (; s_in < end - R * stage; s_in += stage) fetch(s_in);
+  for (; s_in < kAhead * stage; s_in += stage) fetch(s_in);
+  if (s_in == end) s_in = 0;
   auto gate_of_channel = [&](int j) {  // act(gate), 1 without one
     if (GATE != kChannelGate) return same_oct(1.f);
     return gate_act_oct(p.act, param_octet<TY>(p.gate.p, pfp, oct[j], 1.f));
@@ -265,9 +274,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   Walk<TH> dh(p.dh.p, p.dh.row, unit, oct[0]);
   const GateSlope slope(p.act);
   for (int64_t row = unit; row < p.N; row += R * units) {
+    auto fetch_rows = [&] {
 #pragma unroll
-    for (int q = 0; q < R; ++q) fetch(s_in + q * stage);
-    s_in = s_in + R * stage == end ? 0 : s_in + R * stage;
+      for (int q = 0; q < R; ++q) fetch(s_in + q * stage);
+      s_in = s_in + R * stage == end ? 0 : s_in + R * stage;
+    };
+    if (!kLate) fetch_rows();
     auto there = [&](int q, int j) { return in[j] && (q == 0 || row + q * units < p.N); };
     copies_wait<kStages - R>();
     __syncwarp();  // lanes read what others copied
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (kCarry && row != unit) put_one(row - units, wyd_before + s[5], one_before);
 
-    constexpr bool kAgain = R > 1 || NV > 1;
+    if (kLate) fetch_rows();
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float c1 = 0.f, c2 = 0.f, m1 = 0.f, m2 = 0.f, wyd = 0.f;
