@@ -8,8 +8,9 @@
 // cancels; RMS norms need one.  A row may hold anything finite.
 //
 // 8192 x 4096 in bf16: 46 us with an RMS norm before the next block (5.8 TB/s), 48 with one on
-// both sides (32768 x 4096: 161 and 165, 6.6 TB/s), 51 with a layer norm, 68 with two and their biases, whose four exchanges per pair of rows are then
-// the bound; fp32 throughout 95 us (5.7 TB/s).  One token takes 4.6 us, a launch's latency.
+// both sides (32768 x 4096: 161 and 165, 6.6 TB/s), 51 with a layer norm, 68 with two and their
+// biases, whose four exchanges per pair of rows are then the bound; fp32 throughout 95 us (5.7
+// TB/s).  One token takes 4.5 us, a launch's latency.
 #pragma once
 #include "host_util.h"
 #include "resnorm.h"
