@@ -465,7 +465,8 @@ typedef enum flce_act {
  * y and z (dy, dz and gates per token) have type opts->dtype; the stream (h, h_out, dh,
  * dh_out) has it too, or is fp32 with stream_fp32.  Parameters (weights, biases, gates of
  * kind SCALAR and CHANNEL) have type opts->dtype, or are fp32 with params_fp32.  A weight
- * or bias may be NULL.  H is a multiple of 8, 8 .. 16384; N < 2^31.  Row tensors have a
+ * or bias may be NULL; those of a norm that there is not, and their gradients, are neither
+ * read nor written, whatever they point to.  H is a multiple of 8, 8 .. 16384; N < 2^31.  Row tensors have a
  * contiguous last axis and a row stride in elements of their own (a multiple of 8, at least
  * H; gate_row of kind TOKEN: at least 1); tensors are 16-byte aligned (gates of kind SCALAR
  * and TOKEN to their element).

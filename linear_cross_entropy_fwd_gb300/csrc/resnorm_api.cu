@@ -112,6 +112,9 @@ int resnorm(const flce_resnorm* in, const flce_opts* opts, bool backward) {
     a.dz = a.dh_out = nullptr;
     a.dy = a.dh = nullptr;
   }
+  // a norm that there is not has no parameters: the forward kernel takes what is given
+  if (!a.post_norm) a.w_post = a.b_post = nullptr;
+  if (!a.pre_norm) a.w_pre = a.b_pre = nullptr;
   if (o.dtype != FLCE_BF16 && o.dtype != FLCE_FP32)
     return host_error(FLCE_ERR_ARG, "unknown dtype %d", o.dtype);
   if (a.N < 0 || a.N >= (int64_t{1} << 31))
