@@ -458,18 +458,20 @@ typedef enum flce_act {
  *   h_out = alpha h + beta act(gate) u  (without h: the second term; without gate: 1)
  *   z     = n(h_out) * w_pre + b_pre    (pre_norm; else no z)
  * with n the RMS or layer norm over the H elements of a token.  All of it is computed in
- * fp32.  h_out is rounded to the stream's type, and z is the norm of h_out as it is
- * stored, so that the gradients, which read the stored h_out, are those of what was
- * computed; z is rounded once.
+ * fp32.  A sigmoid is off by 3.5 units in its last place at most, a tanh by 2; of gates per
+ * element beside a bf16 stream a sigmoid may be off by 2^-16 of itself.  Their slopes are
+ * a (1 - a) and 1 - a^2 in fp32, off by up to 2^-21 of 1 where a gate is saturated.  h_out
+ * is rounded to the stream's type, and z is the norm of h_out as it is stored, so that the
+ * gradients, which read the stored h_out, are those of what was computed; z is rounded once.
  *
  * y and z (dy, dz and gates per token) have type opts->dtype; the stream (h, h_out, dh,
  * dh_out) has it too, or is fp32 with stream_fp32.  Parameters (weights, biases, gates of
  * kind SCALAR and CHANNEL) have type opts->dtype, or are fp32 with params_fp32.  A weight
  * or bias may be NULL; those of a norm that there is not, and their gradients, are neither
- * read nor written, whatever they point to.  H is a multiple of 8, 8 .. 16384; N < 2^31.  Row tensors have a
- * contiguous last axis and a row stride in elements of their own (a multiple of 8, at least
- * H; gate_row of kind TOKEN: at least 1); tensors are 16-byte aligned (gates of kind SCALAR
- * and TOKEN to their element).
+ * read nor written, whatever they point to.  H is a multiple of 8, 8 .. 16384; N < 2^31.
+ * Row tensors have a contiguous last axis and a row stride in elements of their own (a
+ * multiple of 8, at least H; gate_row of kind TOKEN: at least 1); tensors are 16-byte
+ * aligned (gates of kind SCALAR and TOKEN to their element).
  * h_out may be h itself and z may be y; dh may be dh_out itself, and dy may be dz (same
  * address, same stride).  Any other overlap of an output with an input or another output
  * is refused with FLCE_ERR_ARG where addresses, strides and sizes tell; row tensors that

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   const bool pfp = p.params_fp32, layer = p.layer;
   constexpr bool kReadsY = POST || GATE != kNoGate;
+  constexpr bool kBf16 = Elem<TH>::kBytes == 2;
   // a is the same in every row, so that it and the weight multiply the sums, not the rows
   constexpr bool kFixed = GATE == kNoGate || GATE == kChannelGate;
 
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int i = 0; i < 4; ++i)
             yh.p[i] = mul2(AFF ? plus2(yh.p[i], pair(-mean_y)) : yh.p[i], pair(r_y));
         }
-        if (GATE == kFullGate) a = gate_act_each(p.act, slot_y.read(at + at_gate));
+        if (GATE == kFullGate) a = gate_act_each<kBf16>(p.act, slot_y.read(at + at_gate));
       }
     };
     // Sums of a row: g xh, [g]; and with a post-norm or a gate of one value, with w for

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   const int jump = p.warps * 32;  // octets from one of a thread's to the next
   const bool pfp = p.params_fp32;
+  constexpr bool kBf16 = Elem<TH>::kBytes == 2;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.groups + group;
   const int64_t rows = static_cast<int64_t>(gridDim.x) * p.groups;
 
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           add_oct(v, kBias ? shared_oct(biases + j * jump * 16, plane)
                            : factor(p.b_post, 0.f, oct[j]));
         if (FULL)
-          scale_oct(v, gate_act_each(p.act, slot_y.read(mine + at_gate)));
+          scale_oct(v, gate_act_each<kBf16>(p.act, slot_y.read(mine + at_gate)));
         if (one_gate) scale_oct(v, gate_act(p.act, gate1[q]));
         if (p.h.p) {
           const Oct t = slot_h.read(mine + at_h);

@@ -1,9 +1,11 @@
 """Edges of the operators between blocks: arguments that a form does not use, sums
-over tokens that are exact."""
+over tokens that are exact, gates far from zero."""
 import ctypes
 
 import pytest
 import torch
+
+import block_util as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -123,3 +125,85 @@ def test_sums_over_tokens_are_exact(cuda_lib, gate, kind, bias, post):
         assert torch.equal(got.dw_pre.double(), (dz.double() * xh).sum(0)), (N, H)
         if bias:
             assert torch.equal(got.db_pre.double(), dz.double().sum(0)), (N, H)
+
+
+# ------------------------------------------------------------------------- gates
+UNITS = {"sigmoid": 3.5, "tanh": 2}
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "tanh"])
+@pytest.mark.parametrize("kind", ["full", "token", "channel", "scalar"])
+def test_gates_far_from_zero(cuda_lib, act, kind):
+    """act(gate) alone, as the join of ones: no h, beta 1, no norms.  The sigmoid is e or 1 over
+    1 + e with e = exp(-|g|): the exponential is within 1 unit in the last place, 2^-23, the sum
+    rounds once, the quotient is within 2 units: 3.5 2^-23 of the result, and 2 2^-149 where that is
+    subnormal.  tanhf is within 2 units."""
+    N, H = 16, 512
+    far = torch.cat([torch.linspace(-110, 110, N * H // 2),
+                     torch.logspace(-30, 0.5, N * H // 4), -torch.logspace(-30, 0.5, N * H // 4)])
+    far[:3] = torch.tensor([float("inf"), float("-inf"), float("nan")])
+    far = far.to(DEV)
+    if kind == "full":
+        gates = [far.view(N, H)]
+    elif kind == "token":
+        gates = [far[i::8].reshape(-1, 1) for i in range(8)]
+    elif kind == "channel":
+        gates = [far[i:i + H] for i in range(0, N * H, H)]
+    else:
+        gates = [far[i] for i in range(0, N * H, 301)]
+    for g in gates:
+        rows = g.shape[0] if kind in ("full", "token") else 2
+        y = torch.ones(rows, H, device=DEV)
+        got, _, _ = cuda_lib.flce_resnorm_fwd(y, gate=g, gate_act=act, pre_norm=False, sync=True)
+        want = ref.ACT[act](g.double()).expand(rows, H)
+        nan = want.isnan()
+        assert torch.equal(got.isnan(), nan)
+        err = (got.double() - want).abs()[~nan]
+        tol = UNITS[act] * 2.0 ** -23 * want[~nan].abs() + 2.0 ** -148
+        assert bool((err <= tol).all()), (float((err / tol).max()),
+                                          float(g.expand(rows, H)[~nan][(err / tol).argmax()]))
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "tanh"])
+@pytest.mark.parametrize("kind", ["full", "token", "channel", "scalar"])
+def test_gradients_of_gates_far_from_zero(cuda_lib, act, kind):
+    """dy = act(gate) dt likewise; dgate's slope is a (1 - a) or 1 - a^2 of the activation in
+    fp32, off by that activation's error, 4 2^-23 of 1 (a sigmoid's times 1 - 2 a, a tanh's 2
+    units times 2 a), and three roundings of numbers up to 1; sums of up to 128 of them round about
+    ten times more, 2^-24 of the sum each.  8 + 3 + 10 times 2^-24, below 2^-19."""
+    N, H = 16, 64
+    far = torch.linspace(-60, 60, N * H, device=DEV)
+    shape = {"full": (N, H), "token": (N * H, 1), "channel": (16, H), "scalar": (1024,)}[kind]
+    gates = [far.view(shape)] if kind in ("full", "token") else \
+        list(far.view(shape)) if kind == "channel" else list(far[::37])
+    for g in gates:
+        rows = g.shape[0] if kind in ("full", "token") else 2
+        y = torch.ones(rows, H, device=DEV)
+        got = cuda_lib.flce_resnorm_bwd(None, y, y, None, torch.zeros(4, rows, device=DEV), gate=g,
+                                        gate_act=act, pre_norm=False, sync=True)
+        leaf = g.double().requires_grad_()
+        a = ref.ACT[act](leaf)
+        want = a.detach().expand(rows, H)
+        tol = UNITS[act] * 2.0 ** -23 * want.abs() + 2.0 ** -148
+        assert bool(((got.dy.double() - want).abs() <= tol).all())
+        slope, = torch.autograd.grad(a.expand(rows, H).sum(), leaf)
+        times = rows * H / g.numel()
+        assert bool(((got.dgate.double() - slope).abs() <= 2.0 ** -19 * times).all())
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "tanh"])
+def test_bf16_gates_far_from_zero(cuda_lib, act):
+    """Every bf16 gate, forward and backward: the faster exponential that bf16 rows may take is off
+    by at most 2 + 1.2 |g| units, with the rest 2^-16 of a normal result; half a step of bf16 is
+    2^-8 of it, or 2^-134."""
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF).to(DEV).view(128, 512)
+    y = torch.ones(128, 512, dtype=BF, device=DEV)
+    want = ref.ACT[act](every.double())
+    nan = want.isnan()
+    kw = dict(gate=every, gate_act=act, pre_norm=False, sync=True)
+    got, _, stats = cuda_lib.flce_resnorm_fwd(y, **kw)
+    g = cuda_lib.flce_resnorm_bwd(None, y, y, None, stats, **kw)
+    for v in (got, g.dy):
+        assert torch.equal(v.isnan(), nan)
+        err = (v.double() - want).abs()[~nan]
+        assert bool((err <= (2.0 ** -8 + 2.0 ** -16) * want[~nan].abs() + 2.0 ** -134).all())
