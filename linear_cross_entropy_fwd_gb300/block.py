@@ -330,11 +330,17 @@ def flce_ckpt_wgrad(dY: torch.Tensor, ckpt: Checkpoint, *, dW: torch.Tensor | No
     return dW
 
 
+def _aligned(t):
+    """t, or a copy of it that is contiguous and begins on 16 bytes."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _row_strided(t):
-    """t itself if the library takes its strides, else a contiguous copy."""
+    """t itself if the library takes its strides and address, else a copy that it takes."""
     ok = (t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0
           and t.data_ptr() % 16 == 0)
-    return t if ok else t.contiguous()
+    return t if ok else _aligned(t)
 
 
 def _as(grad, like):
@@ -349,11 +355,11 @@ class _ResidualNormFunction(torch.autograd.Function):
     def forward(ctx, y, h, w_pre, b_pre, w_post, b_post, gate, opts):
         y = _row_strided(y)
         h = None if h is None else _row_strided(h)
-        params = [None if t is None else t.contiguous() for t in (w_pre, b_pre, w_post, b_post)]
+        params = [None if t is None else _aligned(t) for t in (w_pre, b_pre, w_post, b_post)]
         if gate is not None and gate.dim() == 2 and gate.shape[1] > 1:
             gate = _row_strided(gate)
         elif gate is not None:
-            gate = gate.contiguous()
+            gate = _aligned(gate) if gate.dim() == 1 else gate.contiguous()
         kw = dict(zip(("w_pre", "b_pre", "w_post", "b_post"), params), gate=gate,
                   **{k: v for k, v in opts.items() if k != "checkpoint"})
         ck = Checkpoint.empty(*y.shape, y.device) if opts["checkpoint"] else None

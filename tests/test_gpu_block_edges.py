@@ -1,5 +1,5 @@
 """Edges of the operators between blocks: arguments that a form does not use, sums
-over tokens that are exact, gates far from zero."""
+over tokens that are exact, gates far from zero, and what the modules take and keep."""
 import ctypes
 
 import pytest
@@ -207,3 +207,52 @@ def test_bf16_gates_far_from_zero(cuda_lib, act):
         assert torch.equal(v.isnan(), nan)
         err = (v.double() - want).abs()[~nan]
         assert bool((err <= (2.0 ** -8 + 2.0 ** -16) * want[~nan].abs() + 2.0 ** -134).all())
+
+
+# ----------------------------------------------------------------------- modules
+def _off(t, n=1):
+    """t's values `n` elements behind a 16-byte boundary."""
+    raw = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)
+    v = raw[n:n + t.numel()].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("gate", [(), (64,), (24, 1), (24, 64)])
+def test_modules_take_views_at_any_element(cuda_lib, dtype, gate):
+    """Inputs, parameters, incoming gradients that begin anywhere in a flat buffer: the bits of the
+    same call on tensors of their own."""
+    flce, N, H = cuda_lib, 24, 64
+    t = dict(y=_randn(N, H, dtype=dtype, seed=1), h=_randn(N, H, dtype=dtype, seed=2),
+             gate=_randn(*gate, dtype=dtype),
+             **{k: _randn(H, dtype=dtype, seed=i) for i, k in
+                enumerate(("w_pre", "b_pre", "w_post", "b_post"))})
+    grads = [_randn(N, H, dtype=dtype, seed=3), _randn(N, H, dtype=dtype, seed=4)]
+    join = flce.ResidualNorm("layer", gate_act="tanh")
+
+    def run(place):
+        leaves = {k: place(v).requires_grad_() for k, v in t.items()}
+        kw = dict(leaves)
+        out = join(kw.pop("y"), kw.pop("h"), **kw)
+        g = torch.autograd.grad(out, list(leaves.values()), [place(x) for x in grads])
+        return [*out, *g]
+
+    for a, b in zip(run(_off), run(torch.clone)):
+        assert torch.equal(a, b)
+
+
+def test_linear_takes_views_at_any_element(cuda_lib):
+    """Small whole numbers, which every product here holds exactly."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, W, dy = (torch.randint(-2, 3, s, generator=g, device=DEV).to(BF)
+                for s in ((24, 64), (48, 64), (24, 48)))
+
+    def run(place):
+        leaves = [place(v).requires_grad_() for v in (x, W)]
+        out = cuda_lib.CheckpointedLinear()(*leaves)
+        return [out, *torch.autograd.grad(out, leaves, place(dy))]
+
+    for a, b in zip(run(_off), run(torch.clone)):
+        assert torch.equal(a, b)
