@@ -77,11 +77,10 @@ def _gate_address(gate, kind, shape, dtype, device):
     return gate.data_ptr(), gate.stride(0) if kind == GATE_TOKEN else 0
 
 
-def _common(y, shape, dev, stream_dtype, w_post, b_post, w_pre, b_pre, gate, gate_act, kind,
+def _common(dt, shape, dev, stream_dtype, w_post, b_post, w_pre, b_pre, gate, gate_act, kind,
             alpha, beta, eps, post_norm, pre_norm):
     """The fields that both passes share: the structure's up to ``eps``, the gate's, the
     parameters'; and the gate's kind."""
-    dt = y.dtype
     if kind not in NORMS:
         raise ValueError(f"kind must be one of {sorted(NORMS)}")
     if gate_act not in ACTS:
@@ -182,7 +181,7 @@ def flce_resnorm_fwd(y: torch.Tensor, h: torch.Tensor | None = None, *,
     N, H = shape
     dev, dt = y.device, y.dtype
     st = h.dtype if h is not None else stream_dtype or dt
-    head, ga, vecs, _ = _common(y, shape, dev, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
+    head, ga, vecs, _ = _common(dt, shape, dev, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
                                 kind, alpha, beta, eps, post_norm, pre_norm)
     if out is None:
         out = torch.empty(shape, dtype=st, device=dev)
@@ -219,14 +218,15 @@ class ResnormGrads(NamedTuple):
     db_pre: torch.Tensor | None
 
 
-def flce_resnorm_bwd(dz: torch.Tensor | None, dh_out: torch.Tensor | None, y: torch.Tensor,
-                     h_out: torch.Tensor | None, stats: torch.Tensor, *,
+def flce_resnorm_bwd(dz: torch.Tensor | None, dh_out: torch.Tensor | None,
+                     y: torch.Tensor | None, h_out: torch.Tensor | None, stats: torch.Tensor, *,
                      w_pre: torch.Tensor | None = None, b_pre: torch.Tensor | None = None,
                      w_post: torch.Tensor | None = None, b_post: torch.Tensor | None = None,
                      gate: torch.Tensor | None = None, gate_act: str | None = None,
                      kind: str = "rms", alpha: float = 1.0, beta: float = 1.0,
                      eps: float = 1e-6, pre_norm: bool = True, post_norm: bool | None = None,
                      need_dh: bool = True, stream_dtype: torch.dtype | None = None,
+                     dtype: torch.dtype | None = None,
                      dy: torch.Tensor | None = None, dh: torch.Tensor | None = None,
                      sync: bool = False, workspace: torch.Tensor | None = None,
                      info: dict | None = None) -> ResnormGrads:
@@ -234,20 +234,30 @@ def flce_resnorm_bwd(dz: torch.Tensor | None, dh_out: torch.Tensor | None, y: to
     gradient of z (None without a pre-norm), dh_out what reaches h_out besides (None:
     nothing).  dy may be dz itself and dh may be dh_out.  Gradients of weights, biases and
     learned gates are fp32; dy and per-token gates' have y's type, dh the stream's
-    (``need_dh=False`` for a join without h)."""
+    (``need_dh=False`` for a join without h).  y is read for a post-norm or a gate and may be
+    None without them, h_out without a pre-norm; ``dtype`` is y's type then, where it is
+    neither dz's nor dh_out's."""
     lib = _library()
-    _check_y(y)
-    shape = y.shape
+    name, like = (("y", y) if y is not None else ("dz", dz) if dz is not None
+                  else ("dh_out", dh_out))
+    if like is None:
+        raise ValueError("neither dz nor dh_out is given")
+    _check_y(like, name)
+    shape = like.shape
     N, H = shape
-    dev, dt = y.device, y.dtype
+    dev, dt = like.device, dtype if dtype is not None and like is dh_out else like.dtype
+    if dt not in _HALF:
+        raise TypeError(f"unsupported dtype {dt} (bf16 or fp32)")
     st = (h_out.dtype if h_out is not None else dh_out.dtype if dh_out is not None
           else stream_dtype or dt)
-    head, ga, vecs, gk = _common(y, shape, dev, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
+    head, ga, vecs, gk = _common(dt, shape, dev, st, w_post, b_post, w_pre, b_pre, gate, gate_act,
                                  kind, alpha, beta, eps, post_norm, pre_norm)
     if (dz is not None) != bool(pre_norm):
         raise ValueError("dz goes with a pre-norm")
     if pre_norm and h_out is None:
         raise ValueError("a pre-norm's gradient needs h_out")
+    if y is None and (gate is not None or head[3]):
+        raise ValueError("gradients of a post-norm or a gate need y")
     if dy is None:
         dy = torch.empty(shape, dtype=dt, device=dev)
     if dh is None and need_dh:
@@ -364,8 +374,12 @@ class _ResidualNormFunction(torch.autograd.Function):
                   **{k: v for k, v in opts.items() if k != "checkpoint"})
         ck = Checkpoint.empty(*y.shape, y.device) if opts["checkpoint"] else None
         h_out, z, stats = flce_resnorm_fwd(y, h, checkpoint=ck, **kw)
-        ctx.save_for_backward(y, h_out, stats, *params, gate)
-        ctx.opts, ctx.has_h = opts, h is not None
+        # what the gradients read: a plain pre-norm join keeps its stream and not y
+        reads_y = gate is not None or params[2] is not None or params[3] is not None \
+            or opts["post_norm"]
+        ctx.save_for_backward(y if reads_y else None, h_out if opts["pre_norm"] else None, stats,
+                              *params, gate)
+        ctx.opts, ctx.has_h, ctx.dtype = opts, h is not None, y.dtype
         ctx.set_materialize_grads(False)
         if ck is None:
             return h_out, z, None
@@ -377,13 +391,14 @@ class _ResidualNormFunction(torch.autograd.Function):
     def backward(ctx, dh_out, dz, _):
         y, h_out, stats, w_pre, b_pre, w_post, b_post, gate = ctx.saved_tensors
         if dz is None and ctx.opts["pre_norm"]:  # z was not used
-            dz = torch.zeros_like(y)
+            dz = torch.zeros(h_out.shape, dtype=ctx.dtype, device=h_out.device)
         if dh_out is None and dz is None:
             return (None,) * 8
         g = flce_resnorm_bwd(
             None if dz is None else _row_strided(dz),
             None if dh_out is None else _row_strided(dh_out), y, h_out, stats, w_pre=w_pre,
             b_pre=b_pre, w_post=w_post, b_post=b_post, gate=gate, need_dh=ctx.has_h,
+            dtype=ctx.dtype,
             **{k: v for k, v in ctx.opts.items() if k != "checkpoint"})
         return (g.dy, g.dh, _as(g.dw_pre, w_pre), _as(g.db_pre, b_pre), _as(g.dw_post, w_post),
                 _as(g.db_post, b_post), _as(g.dgate, gate), None)

@@ -256,3 +256,72 @@ def test_linear_takes_views_at_any_element(cuda_lib):
 
     for a, b in zip(run(_off), run(torch.clone)):
         assert torch.equal(a, b)
+
+
+class _Saved:
+    """The tensors that autograd keeps between the passes."""
+
+    def __enter__(self):
+        self.kept = []
+
+        def pack(t):
+            self.kept.append(t)
+            return t
+
+        self.hooks = torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t)
+        self.hooks.__enter__()
+        return self
+
+    def __exit__(self, *a):
+        self.hooks.__exit__(*a)
+
+    def holds(self, t):
+        return any(k.data_ptr() == t.data_ptr() for k in self.kept)
+
+
+@pytest.mark.parametrize("kw,y_needed,h_needed", [
+    (dict(), False, True), (dict(w_post=True), True, True), (dict(gate=True), True, True),
+    (dict(pre_norm=False), False, False), (dict(pre_norm=False, w_post=True), True, False)])
+def test_join_keeps_what_its_gradients_read(cuda_lib, kw, y_needed, h_needed):
+    N, H = 40, 264
+    kw = dict(kw)
+    y, h = _randn(N, H, seed=1).requires_grad_(), _randn(N, H, seed=2).requires_grad_()
+    p = {k: _randn(H, seed=3).requires_grad_() for k in ("w_post", "gate") if kw.pop(k, False)}
+    opts = dict(kind="rms", gate_act=None, alpha=1.0, beta=1.0, eps=1e-6,
+                pre_norm=kw.get("pre_norm", True), post_norm="w_post" in p)
+    with _Saved() as saved:
+        ho, z = cuda_lib.ResidualNorm(**kw)(y, h, **p)
+    assert saved.holds(y) == y_needed and saved.holds(ho) == h_needed
+    dz = _randn(N, H, seed=4) if opts["pre_norm"] else None
+    dh_out = _randn(N, H, seed=5)
+    leaves = dict(dy=y, dh=h, **{"d" + k: v for k, v in p.items()})
+    outs = [(ho, dh_out)] + ([(z, dz)] if dz is not None else [])
+    got = torch.autograd.grad([o for o, _ in outs], list(leaves.values()), [g for _, g in outs])
+    want = ref.join_grads(dz, dh_out, y.detach(), ho.detach(),
+                          {k: p[k].detach() if k in p else None
+                           for k in ("w_pre", "b_pre", "w_post", "b_post", "gate")}, opts)
+    for (k, leaf), g in zip(leaves.items(), got):
+        ref.check(g, *want[k], k)
+
+
+def test_gradients_without_y(cuda_lib):
+    """The entry point itself takes no y where nothing reads it, and says so where something does."""
+    N, H = 40, 264
+    y, h, dz, dh = (_randn(N, H, seed=i) for i in range(4))
+    out, _, stats = cuda_lib.flce_resnorm_fwd(y, h)
+    full = cuda_lib.flce_resnorm_bwd(dz, dh, y, out, stats)
+    for args in ((dz, dh), (dz, None)):
+        a = cuda_lib.flce_resnorm_bwd(*args, None, out, stats, sync=True)
+        b = cuda_lib.flce_resnorm_bwd(*args, y, out, stats)
+        assert torch.equal(a.dy, b.dy) and torch.equal(a.dh, b.dh)
+    assert torch.equal(full.dy, cuda_lib.flce_resnorm_bwd(dz, dh, None, out, stats).dy)
+    only = cuda_lib.flce_resnorm_bwd(None, dh, None, None, stats, pre_norm=False, sync=True)
+    assert torch.equal(only.dy, dh) and torch.equal(only.dh, dh)
+    mixed = cuda_lib.flce_resnorm_bwd(None, dh.float(), None, None, stats, pre_norm=False,
+                                      dtype=BF, sync=True)
+    assert torch.equal(mixed.dy, dh) and torch.equal(mixed.dh, dh.float())
+    for kw in (dict(post_norm=True), dict(gate=_randn(H))):
+        with pytest.raises(ValueError):
+            cuda_lib.flce_resnorm_bwd(dz, dh, None, out, stats, **kw)
+    with pytest.raises(ValueError):
+        cuda_lib.flce_resnorm_bwd(None, None, None, None, stats, pre_norm=False)
