@@ -429,12 +429,13 @@ class ResidualNorm(torch.nn.Module):
 
 class _CheckpointedLinearFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, saved):
+    def forward(ctx, x, weight, saved, keep):
         flat = _row_strided(x.reshape(-1, x.shape[-1]))
-        ck = flce_ckpt_save(flat) if saved is None else saved
-        if (ck.N, ck.H) != tuple(flat.shape):
+        if saved is not None and (saved.N, saved.H) != tuple(flat.shape):
             raise ValueError(f"saved must be a checkpoint of {tuple(flat.shape)}")
-        ctx.save_for_backward(weight, ck.data)
+        if keep and saved is None:
+            saved = flce_ckpt_save(flat)
+        ctx.save_for_backward(weight, saved.data if keep else None)
         ctx.shape = x.shape
         return (flat @ weight.t()).view(*x.shape[:-1], weight.shape[0])
 
@@ -449,14 +450,15 @@ class _CheckpointedLinearFunction(torch.autograd.Function):
         if ctx.needs_input_grad[1]:
             ck = Checkpoint(data, flat.shape[0], weight.shape[1])
             dW = _as(flce_ckpt_wgrad(flat, ck), weight)
-        return dx, dW, None
+        return dx, dW, None, None
 
 
 class CheckpointedLinear(torch.nn.Module):
     """``linear(x, weight, saved=None)`` -> ``x @ weight.T`` in bf16, whose backward pass takes
     the weight's gradient from x in 8 bits instead of x itself.  x [..., I], weight [O, I], O
     and I multiples of 8; ``saved`` is a checkpoint of x that another call made
-    (``ResidualNorm``, or a linear that shares the input)."""
+    (``ResidualNorm``, or a linear that shares the input).  Where weight has no gradient to come
+    (frozen, or under ``no_grad``) no checkpoint is made or kept."""
 
     def forward(self, x, weight, saved: Checkpoint | None = None):
         if x.dtype is not torch.bfloat16 or weight.dtype is not torch.bfloat16:
@@ -464,4 +466,5 @@ class CheckpointedLinear(torch.nn.Module):
         if weight.dim() != 2 or x.shape[-1:] != weight.shape[1:] \
                 or weight.shape[0] % 8 or weight.shape[1] % 8:
             raise ValueError("x must be [..., I] and weight [O, I], O and I multiples of 8")
-        return _CheckpointedLinearFunction.apply(x, weight, saved)
+        return _CheckpointedLinearFunction.apply(x, weight, saved,
+                                                 weight.requires_grad and torch.is_grad_enabled())

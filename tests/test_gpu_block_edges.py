@@ -325,3 +325,27 @@ def test_gradients_without_y(cuda_lib):
             cuda_lib.flce_resnorm_bwd(dz, dh, None, out, stats, **kw)
     with pytest.raises(ValueError):
         cuda_lib.flce_resnorm_bwd(None, None, None, None, stats, pre_norm=False)
+
+
+def test_linear_keeps_no_checkpoint_without_a_use(cuda_lib, monkeypatch):
+    """A weight that is frozen, and a call under no_grad."""
+    import linear_cross_entropy_fwd_gb300.block as block
+    calls, save = [], block.flce_ckpt_save
+    monkeypatch.setattr(block, "flce_ckpt_save", lambda *a, **k: calls.append(1) or save(*a, **k))
+    x, W = _randn(24, 64).requires_grad_(), _randn(48, 64)
+    linear = cuda_lib.CheckpointedLinear()
+    with _Saved() as saved:
+        out = linear(x, W)
+    assert not calls and all(t.dtype is not torch.uint8 for t in saved.kept)
+    dy = _randn(24, 48)
+    dx, = torch.autograd.grad(out, x, dy)
+    assert torch.equal(dx, dy @ W)
+    with torch.no_grad():
+        assert torch.equal(linear(x, W.clone().requires_grad_()), x @ W.t())
+    assert not calls
+    ck = cuda_lib.flce_ckpt_save(x.detach())
+    with _Saved() as saved:
+        linear(x, W, ck)
+    assert not saved.holds(ck.data)
+    linear(x, W.clone().requires_grad_())
+    assert len(calls) == 1
