@@ -390,18 +390,21 @@ class _ResidualNormFunction(torch.autograd.Function):
     @once_differentiable  # the kernels' results carry no graph of their own
     def backward(ctx, dh_out, dz, _):
         y, h_out, stats, w_pre, b_pre, w_post, b_post, gate = ctx.saved_tensors
-        if dz is None and ctx.opts["pre_norm"]:  # z was not used
-            dz = torch.zeros(h_out.shape, dtype=ctx.dtype, device=h_out.device)
         if dh_out is None and dz is None:
             return (None,) * 8
+        # without a use of z its norm has no part in the gradients, whatever the stream holds
+        opts = {k: v for k, v in ctx.opts.items() if k != "checkpoint"}
+        unused = dz is None and opts["pre_norm"]
         g = flce_resnorm_bwd(
             None if dz is None else _row_strided(dz),
-            None if dh_out is None else _row_strided(dh_out), y, h_out, stats, w_pre=w_pre,
-            b_pre=b_pre, w_post=w_post, b_post=b_post, gate=gate, need_dh=ctx.has_h,
-            dtype=ctx.dtype,
-            **{k: v for k, v in ctx.opts.items() if k != "checkpoint"})
-        return (g.dy, g.dh, _as(g.dw_pre, w_pre), _as(g.db_pre, b_pre), _as(g.dw_post, w_post),
-                _as(g.db_post, b_post), _as(g.dgate, gate), None)
+            None if dh_out is None else _row_strided(dh_out), y, None if unused else h_out, stats,
+            w_pre=None if unused else w_pre, b_pre=None if unused else b_pre, w_post=w_post,
+            b_post=b_post, gate=gate, need_dh=ctx.has_h, dtype=ctx.dtype,
+            **{**opts, "pre_norm": dz is not None})
+        dw_pre, db_pre = (_as(d, t) if d is not None or t is None else torch.zeros_like(t)
+                          for d, t in ((g.dw_pre, w_pre), (g.db_pre, b_pre)))
+        return (g.dy, g.dh, dw_pre, db_pre, _as(g.dw_post, w_post), _as(g.db_post, b_post),
+                _as(g.dgate, gate), None)
 
 
 class ResidualNorm(torch.nn.Module):

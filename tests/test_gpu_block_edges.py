@@ -349,3 +349,19 @@ def test_linear_keeps_no_checkpoint_without_a_use(cuda_lib, monkeypatch):
     assert not saved.holds(ck.data)
     linear(x, W.clone().requires_grad_())
     assert len(calls) == 1
+
+
+def test_unused_z_brings_nothing(cuda_lib):
+    """Rows of the stream that are not finite, and a loss that does not go through z: dh is
+    alpha dh_out and dy act(gate) dh_out, in those rows too; the pre-norm's parameters get zeros."""
+    N, H = 24, 64
+    y, h = _randn(N, H, dtype=FP, seed=1), _randn(N, H, dtype=FP, seed=2)
+    h[3, 5], h[7, 0] = float("inf"), float("nan")
+    y.requires_grad_(), h.requires_grad_()
+    gate = _randn(H, dtype=FP, seed=3)
+    w, b = _randn(H, dtype=FP).requires_grad_(), _randn(H, dtype=FP).requires_grad_()
+    ho, _ = cuda_lib.ResidualNorm(alpha=0.5)(y, h, w_pre=w, b_pre=b, gate=gate)
+    dh = _randn(N, H, dtype=FP, seed=4)
+    ho.backward(dh)
+    assert torch.equal(h.grad, 0.5 * dh) and torch.equal(y.grad, gate * dh)
+    assert not w.grad.any() and not b.grad.any()
