@@ -6,6 +6,7 @@ through ``sync=True`` or ``info['status']``.
 """
 from __future__ import annotations
 
+import math
 import struct
 from typing import NamedTuple
 
@@ -353,6 +354,11 @@ def _row_strided(t):
     return t if ok else _aligned(t)
 
 
+def _flat(t):
+    """[..., n] as rows of n."""
+    return t.reshape(math.prod(t.shape[:-1]), t.shape[-1])
+
+
 def _as(grad, like):
     """A parameter's fp32 gradient in the parameter's type."""
     if grad is None or grad.dtype is like.dtype:
@@ -433,7 +439,7 @@ class ResidualNorm(torch.nn.Module):
 class _CheckpointedLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, saved, keep):
-        flat = _row_strided(x.reshape(-1, x.shape[-1]))
+        flat = _row_strided(_flat(x))
         if saved is not None and (saved.N, saved.H) != tuple(flat.shape):
             raise ValueError(f"saved must be a checkpoint of {tuple(flat.shape)}")
         if keep and saved is None:
@@ -446,7 +452,7 @@ class _CheckpointedLinearFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_out):
         weight, data = ctx.saved_tensors
-        flat = _row_strided(grad_out.reshape(-1, grad_out.shape[-1]))
+        flat = _row_strided(_flat(grad_out))
         dx = dW = None
         if ctx.needs_input_grad[0]:
             dx = (flat @ weight).view(ctx.shape)
@@ -469,5 +475,10 @@ class CheckpointedLinear(torch.nn.Module):
         if weight.dim() != 2 or x.shape[-1:] != weight.shape[1:] \
                 or weight.shape[0] % 8 or weight.shape[1] % 8:
             raise ValueError("x must be [..., I] and weight [O, I], O and I multiples of 8")
-        return _CheckpointedLinearFunction.apply(x, weight, saved,
-                                                 weight.requires_grad and torch.is_grad_enabled())
+        if not x.is_cuda or weight.device != x.device \
+                or (saved is not None and saved.data.device != x.device):
+            raise ValueError("x, weight and saved must be on one CUDA device")
+        keep = weight.requires_grad and torch.is_grad_enabled()
+        if keep and not all(8 <= n <= 1 << 20 for n in weight.shape):
+            raise ValueError("O and I of a weight with a gradient must be 8 .. 2^20")
+        return _CheckpointedLinearFunction.apply(x, weight, saved, keep)

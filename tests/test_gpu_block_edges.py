@@ -1,6 +1,7 @@
 """Edges of the operators between blocks: arguments that a form does not use, sums
 over tokens that are exact, gates far from zero, and what the modules take and keep."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -365,3 +366,21 @@ def test_unused_z_brings_nothing(cuda_lib):
     ho.backward(dh)
     assert torch.equal(h.grad, 0.5 * dh) and torch.equal(y.grad, gate * dh)
     assert not w.grad.any() and not b.grad.any()
+
+
+def test_linear_refuses_in_the_forward_pass(cuda_lib):
+    """A weight larger than the gradient's entry point takes, or without rows or columns, and a
+    checkpoint or a weight elsewhere than x.  A frozen weight needs no such gradient."""
+    linear = cuda_lib.CheckpointedLinear()
+    x = _randn(2, 8)
+    for shape, y in (((1 << 20) + 8, 8), x), ((0, 8), x), ((8, 0), x[:, :0]):
+        W = torch.zeros(shape, dtype=BF, device=DEV)
+        assert linear(y, W).shape == (2, shape[0])
+        with pytest.raises(ValueError):
+            linear(y, W.requires_grad_())
+    W = _randn(8, 8).requires_grad_()
+    with pytest.raises(ValueError):
+        linear(x, W, SimpleNamespace(N=2, H=8, data=torch.zeros(72, dtype=torch.uint8)))
+    for a, b in ((x, W.detach().cpu()), (x.cpu(), W), (x.cpu(), W.detach().cpu())):
+        with pytest.raises(ValueError):
+            linear(a, b)
