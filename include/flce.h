@@ -488,8 +488,10 @@ typedef enum flce_act {
  * the gradients dz (pre_norm) and dh_out (optional: what arrives on the stream besides):
  *   dy; dh, optional; dgate of the gate's shape (per token: opts->dtype, dgate_row apart;
  *   SCALAR and CHANNEL: fp32); dw_post, db_post, dw_pre, db_pre, fp32 [H], each optional.
- * dgate is required with a gate.  Sums over tokens are fp32, in an order that N, H, the
- * options and the device's number of SMs fix: the same call gives the same bits.
+ * dgate is required with a gate.  Sums over tokens are fp32: the same call gives the same
+ * bits.  Their order goes by N, H, the types, the form of the join (norms, the gate's kind,
+ * whether a bias is given or its gradient wanted) and the device: its number of SMs and, for
+ * rows that several of them share, how many clusters of them run at once.
  * N == 0 makes the parameters' gradients 0.
  * Scratch: forward none; backward up to 32 KB per SM and gradient of a parameter.
  */
