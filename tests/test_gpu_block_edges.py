@@ -1,6 +1,7 @@
 """Edges of the operators between blocks: arguments that a form does not use, sums
 over tokens that are exact, gates far from zero, and what the modules take and keep."""
 import ctypes
+import math
 from types import SimpleNamespace
 
 import pytest
@@ -384,3 +385,32 @@ def test_linear_refuses_in_the_forward_pass(cuda_lib):
     for a, b in ((x, W.detach().cpu()), (x.cpu(), W), (x.cpu(), W.detach().cpu())):
         with pytest.raises(ValueError):
             linear(a, b)
+
+
+# ------------------------------------------------------------- checkpoints
+@pytest.mark.parametrize("dt,st", [(BF, BF), (BF, FP), (FP, FP)])
+@pytest.mark.parametrize("post,gate,kind", [(False, None, "rms"), (True, "channel", "rms"),
+                                            (True, "full", "layer")])
+def test_checkpoint_of_many_rows(cuda_lib, dt, st, post, gate, kind):
+    """Where each group of warps has many rows, pairs of rows among them, and where rows are
+    asked for late (the sizes with most rows): the bytes of the definition for z's first and last
+    rows, and those that a checkpoint of the stored z has for all."""
+    for N, H in ((20011, 64), (9001, 200), (97301, 264), (3001, 1000), (1001, 5000), (6101, 8192),
+                 (333, 8200)):
+        p = dict(w_pre=_randn(H, dtype=dt, seed=1), kind=kind)
+        if post:
+            p["w_post"] = _randn(H, dtype=dt, seed=2)
+        if gate is not None:
+            p["gate"] = _randn(*((H,) if gate == "channel" else (N, H)), dtype=dt, seed=3)
+        y, h = _randn(N, H, dtype=dt, seed=4), _randn(N, H, dtype=st, seed=5)
+        ck = cuda_lib.Checkpoint.empty(N, H, DEV)
+        ck.data.fill_(0xA5)
+        out, z, stats = cuda_lib.flce_resnorm_fwd(y, h, **p, checkpoint=ck, sync=True)
+        plain = cuda_lib.flce_resnorm_fwd(y, h, **p)
+        assert all(torch.equal(a, b) for a, b in zip(plain, (out, z, stats)))
+        assert torch.equal(ck.data, cuda_lib.flce_ckpt_save(z).data)
+        P = 32 * math.ceil(H / 32)
+        rows = torch.cat([torch.arange(5), torch.arange(N - 5, N)])
+        codes, scales = ref.quantise(z[rows.to(DEV)])
+        assert torch.equal(ck.data[:N * P].view(N, P)[rows.to(DEV)].cpu(), codes)
+        assert torch.equal(ck.data[N * P:].view(N, -1)[rows.to(DEV)].cpu(), scales)
