@@ -414,3 +414,19 @@ def test_checkpoint_of_many_rows(cuda_lib, dt, st, post, gate, kind):
         codes, scales = ref.quantise(z[rows.to(DEV)])
         assert torch.equal(ck.data[:N * P].view(N, P)[rows.to(DEV)].cpu(), codes)
         assert torch.equal(ck.data[N * P:].view(N, -1)[rows.to(DEV)].cpu(), scales)
+
+
+@pytest.mark.parametrize("N,O,I", [(16384, 1024, 4864), (16384, 1024, 2432)])
+def test_wgrad_adds_pieces(cuda_lib, N, O, I):
+    """A sum of one sign over many tokens, in 76 tiles of 256 or 128 columns that a CTA pair each
+    does from end to end.  An accumulator takes 2048 tokens, 16 at a time; what a step cuts off is
+    less than 2^-23 of the sum so far, k / 128 of the piece's after k steps: 64.5 2^-23 of a piece.
+    Eight pieces are added with a rounding of 2^-24 each.  In one accumulator 1024 steps would cut
+    off up to 512.5 2^-23, and half a unit on average: four times what is allowed."""
+    g = torch.Generator(device=DEV).manual_seed(I)
+    dY = torch.rand(N, O, generator=g, device=DEV).to(BF)
+    ck = cuda_lib.flce_ckpt_save(torch.rand(N, I, generator=g, device=DEV).to(BF))
+    dW = cuda_lib.flce_ckpt_wgrad(dY, ck, sync=True)
+    want = dY.double().t() @ cuda_lib.flce_ckpt_load(ck).double()
+    err = (dW.double() - want).norm() / want.norm()
+    assert err <= 64.5 * 2.0 ** -23 + 8 * 2.0 ** -24
