@@ -66,7 +66,7 @@ constexpr int kBwdPieces =
 
 // And behind the pieces, for each warp, the row's four statistics and its gate of one value:
 // a load a row ahead would have to keep registers through the row, or is moved to where it is
-// waited for (8192 x 4096 with gates per element: 131 us, 54 of them waiting; 88 now).
+// waited for (8192 x 4096 with gates per element: 131 us, 54 of them waiting; 90 now).
 constexpr uint32_t kRowBytes = 32, kTailBytes = kRowBytes * kMaxRowWarps;
 
 // What the launch and the kernel agree on, for NV octets a thread.
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   // Single bf16 rows that are not read again ask for the next ones behind the exchange of their
   // sums, between their own loads and stores, when their own stage is free too: 65536 x 4096
-  // 390 us, 415 with the copies first; with gates per element 632 and 683; 30000 x 1000 55
+  // 390 us, 415 with the copies first; with gates per element, sigmoids, 641 and 705; 30000 x 1000 55
   // either way.  (Pairs of rows 79 and 74 at 8192 x 4096, two octets a thread 67 and 58 at
   // 4096 x 8192; with an fp32 stream, or means on both sides, up to 4% more.)
   constexpr bool kAgain = R > 1 || NV > 1;
