@@ -576,9 +576,9 @@ FLCE_API int flce_ckpt_load(const void* ckpt, int64_t N, int64_t H, void* x, int
  *   multiples of 8, up to 2^20; N < 2^31.  opts->dtype must be FLCE_BF16.
  * Products are bf16, exact for the stored X.  Sums are fp32, in an order that N, O, I and the
  * device's number of SMs fix; where they pass through the tensor core's accumulators, 2048
- * tokens at most, each 16 tokens' sum is cut off, not rounded: 6e-7 of dW by norm for inputs
- * of random sign, 2.4e-6 for those of one sign, whatever N.  N == 0 makes dW 0, or leaves it
- * when accumulate is set.
+ * tokens at most, each 16 tokens' sum is cut off, not rounded: 6e-7 to 8e-7 of dW by norm for
+ * inputs of random sign, 2.4e-6 for those of one sign, whatever N.  N == 0 makes dW 0, or
+ * leaves it when accumulate is set.
  * Scratch: X in bf16, 2 N I bytes; and 256 KB per SM where the last tiles are shared out
  * along the tokens (opts->workspace_used tells).
  */

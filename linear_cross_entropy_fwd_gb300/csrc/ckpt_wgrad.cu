@@ -12,10 +12,11 @@
 // up to 128 sums a thread, and the tensor core goes on with the other accumulator meanwhile.
 // (Adding the pieces to dW at L2 took a quarter of the time of the products.)
 //   That is a choice of time over digits.  Off from 64-bit sums, by norm, inputs of random sign:
-// 6.2e-7 whatever N; a plain fp32 product 1.4e-7 with 2048 tokens, 3.6e-7 with 8192, 5.7e-7 with
-// 16384.  Inputs of one sign: 2.4e-6, all downwards; plain 0.3e-6, 1.0e-6, 1.7e-6.  Pieces of 1024
-// tokens: 2.8e-7 and 0.9e-6, but 8192 x 6144 x 4096 takes 249 us for 242 and 16384 x 512 x 512 32
-// for 26; of 512: 1.4e-7 and 0.4e-6, 293 us.
+// 6.2e-7 whatever N (7.7e-7 with tokens and channels of different sizes); a plain fp32 product
+// 1.4e-7 with 2048 tokens, 3.6e-7 with 8192, 5.7e-7 with 16384.  Inputs of one sign: 2.4e-6, all
+// downwards; plain 0.3e-6, 1.0e-6, 1.7e-6.  Pieces of 1024 tokens: 2.8e-7 and 0.9e-6, but 8192 x
+// 6144 x 4096 takes 249 us for 242 and 16384 x 512 x 512 32 for 26; of 512: 1.4e-7 and 0.4e-6,
+// 293 us.
 //
 // The last tiles.  Tiles that do not fill a round of all pairs are shared out along the
 // tokens, evenly; each pair's share of a tile goes to scratch and a second kernel adds a
